@@ -95,7 +95,7 @@ def _segments(n, segs, g):
     else:
         cuts = torch.randint(0, n + 1, (segs - 1,), generator=g, device=DEV).sort().values
     ends = torch.tensor([0, n], device=DEV)
-    return torch.cat([ends[:1], cuts, ends[1:]]).to(torch.int32)
+    return torch.cat([ends[:1], cuts, ends[1:]])
 
 
 def _sizes(case):
@@ -209,7 +209,7 @@ def _act_grad(z, act):
 
 
 def _segment_of(n, seg):
-    return torch.searchsorted(seg[1:].contiguous(), torch.arange(n, dtype=torch.int32, device=seg.device), right=True)
+    return torch.searchsorted(seg[1:].contiguous(), torch.arange(n, device=seg.device), right=True)
 
 
 def _by_segment(rows, row_seg, segs):
@@ -363,7 +363,7 @@ def work(case):
     op = case["op"]
     if op.startswith("norm"):
         n, C, x, y = case["n"], case["C"], SIZE[case["xt"]], SIZE[case["yt"]]
-        stats = 8 * case["segs"] * case["groups"] + 4 * (case["segs"] + 1)
+        stats = 8 * case["segs"] * case["groups"] + 8 * (case["segs"] + 1)
         if op == "norm_fwd":
             return {"bytes": n * C * (x + y) + 8 * C + stats, "flops": 8 * n * C}
         return {"bytes": n * C * (2 * x + y) + 16 * C + stats, "flops": 20 * n * C}
