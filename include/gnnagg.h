@@ -622,6 +622,132 @@ gnn_status gnn_spmm_bwd_blocked(const gnn_csr* csr, const gnn_boundary* bnd,
                                 gnn_stream_t stream);
 
 /* ------------------------------------------------------------------------ */
+/* Node-wise block: group norm, gated feed-forward projections, AdamW.       */
+/* ------------------------------------------------------------------------ */
+/* The second half of a graph-transformer or deep-GCN layer, which works on
+ * every node by itself, and the optimiser step.  No counterpart on the pages
+ * (they train with a framework's own layers and optimiser). */
+#define GNN_F32 0
+#define GNN_BF16 1
+#define GNN_F16 2
+
+#define GNN_ACT_NONE 0
+#define GNN_ACT_RELU 1
+#define GNN_ACT_SILU 2    /* z / (1 + exp(-z))                     */
+#define GNN_ACT_GELU 3    /* z (1 + erf(z / sqrt 2)) / 2           */
+#define GNN_ACT_SIGMOID 4 /* 1 / (1 + exp(-z))                     */
+
+/* Matrices of this section: row-major, 16-byte aligned rows.  A 4-byte type
+ * has a row stride that is a multiple of 4 and its output columns
+ * F..round_up(F,4)-1 are written as zero; a 2-byte type has a row stride that
+ * is a multiple of 8 and, as an output, at least round_up(F,16), with columns
+ * F..round_up(F,16)-1 written as zero (the operand layout of
+ * gnn_dense_fwd).  Padding columns of inputs are not used. */
+
+/* Group norm with an activation, channels last.  Segment s holds the rows
+ * [seg_start[s], seg_start[s+1]) -- a graph of a batch, or a partition:
+ * gnn_boundary.part_start fits -- with seg_start[0] = 0, ascending,
+ * seg_start[n_seg] = n (device int64; NULL: one segment of n rows; empty
+ * segments are allowed and get mean 0, rstd 1/sqrt(eps)).  Group g holds the
+ * channels [g C/groups, (g+1) C/groups).  With mean and (biased) variance
+ * over a segment's rows and a group's channels:
+ *   xh = (x - mean) rstd,  rstd = 1/sqrt(var + eps),
+ *   Y = act(gamma xh + beta)           (gamma, beta fp32 [C]; NULL: 1, 0).
+ * mean, rstd: fp32 [n_seg][groups], kept for the backward.  Statistics are
+ * held in fp32 about a value of the group, so a large mean does not cancel.
+ * Types (x_type -> y_type): GNN_F32 -> any, GNN_BF16 -> GNN_BF16,
+ * GNN_F16 -> GNN_F16.  C <= 1024, a multiple of groups.  Rows of a seg_start
+ * that is not ascending raise the device-check flag. */
+gnn_status gnn_group_norm_workspace(int64_t n, int32_t C, int32_t groups, int32_t n_seg,
+                                    size_t* ws_bytes);
+gnn_status gnn_group_norm_fwd(const void* X, int64_t ldx, int32_t x_type, int64_t n, int32_t C,
+                              int32_t groups, const int64_t* seg_start, int32_t n_seg,
+                              const float* gamma, const float* beta, double eps, int32_t act,
+                              void* Y, int64_t ldy, int32_t y_type, float* mean, float* rstd,
+                              void* ws, size_t ws_bytes, gnn_stream_t stream);
+/* Backward from X and the kept mean, rstd (dY has y_type, dX x_type): with
+ * dz = dY act'(gamma xh + beta) and m the values of a segment's group,
+ *   dX = rstd (gamma dz - (sum gamma dz + xh sum gamma dz xh) / m),
+ *   dgamma = sum dz xh, dbeta = sum dz over all rows (fp32 [C]; either may be
+ * NULL).  Sums are added in a fixed order (deterministic). */
+gnn_status gnn_group_norm_bwd(const void* dY, int64_t ldy, int32_t y_type, const void* X,
+                              int64_t ldx, int32_t x_type, int64_t n, int32_t C, int32_t groups,
+                              const int64_t* seg_start, int32_t n_seg, const float* gamma,
+                              const float* beta, int32_t act, const float* mean,
+                              const float* rstd, void* dX, int64_t lddx, float* dgamma,
+                              float* dbeta, void* ws, size_t ws_bytes, gnn_stream_t stream);
+
+/* Gated feed-forward projections on tcgen05: H = act(X Wg) * (X Wu) in one
+ * kernel.  X [n][F_in], Wg and Wu [F_in][F_mid], H [n][F_mid], all of one
+ * 2-byte type (GNN_BF16 or GNN_F16); products accumulate in fp32 and H is
+ * rounded once.  Row strides are multiples of 8. */
+gnn_status gnn_gated_workspace(int64_t n, int32_t F_in, int32_t F_mid, size_t* fwd_bytes,
+                               size_t* bwd_bytes);
+gnn_status gnn_gated_fwd(const void* X, int64_t ldx, int32_t type, int64_t n, int32_t F_in,
+                         const void* Wg, int64_t ldwg, const void* Wu, int64_t ldwu,
+                         int32_t F_mid, int32_t act, void* H, int64_t ldh, void* ws,
+                         size_t ws_bytes, gnn_stream_t stream);
+/* Backward, which recomputes G = X Wg and U = X Wu (nothing is kept from the
+ * forward): dG = dH U act'(G), dU = dH act(G), rounded to `type` as tensor-core
+ * operands; dX = dG Wg^T + dU Wu^T, dWg = X^T dG, dWu = X^T dU, each
+ * accumulated in fp32, in a fixed order, and rounded to `type`.  dH is `type`
+ * or GNN_F32 (dh_type).  dX may be NULL; dWg and dWu may both be NULL. */
+gnn_status gnn_gated_bwd(const void* dH, int64_t lddh, int32_t dh_type, const void* X,
+                         int64_t ldx, int32_t type, int64_t n, int32_t F_in, const void* Wg,
+                         int64_t ldwg, const void* Wu, int64_t ldwu, int32_t F_mid, int32_t act,
+                         void* dX, int64_t lddx, void* dWg, int64_t lddwg, void* dWu,
+                         int64_t lddwu, void* ws, size_t ws_bytes, gnn_stream_t stream);
+
+/* One AdamW step over many tensors.  The descriptors are a host array (they
+ * go to the kernels as launch parameters, so they may change from call to
+ * call and a call can be captured into a graph); what they point at is device
+ * memory.  Per element, in fp32 with every product, sum, division and root
+ * rounded (no contraction), g' = g s:
+ *   m = beta1 m + (1 - beta1) g',  v = beta2 v + ((1 - beta2) g') g',
+ *   param = param (1 - lr weight_decay)
+ *           - lr/(1 - beta1^t) (m / (sqrt(v) / sqrt(1 - beta2^t) + eps)).
+ * state_bits 32: m, v fp32 [n].  state_bits 8: m, v hold e4m3 codes [n] and
+ * m_scale, v_scale one fp32 per 256 elements [ceil(n/256)]: m = code m_scale,
+ * sqrt(v) = code v_scale, scale = largest magnitude of the block / 448 (zero,
+ * with zero codes, when that is below the smallest normal fp32), codes rounded
+ * to nearest even from value (1/scale), except that a positive sqrt(v) never
+ * becomes zero (its smallest code is 2^-9), which would leave eps alone in the
+ * division.  The parameter update uses m and v before they are rounded to
+ * codes.  copy (NULL or bf16 [n]) receives the updated parameters rounded. */
+typedef struct gnn_adamw_tensor {
+  void* param;      /* fp32 or bf16 [n], updated in place */
+  const void* grad; /* fp32, bf16 or fp16 [n]             */
+  void* m;
+  void* v;
+  float* m_scale; /* state_bits 8 only */
+  float* v_scale;
+  uint16_t* copy;
+  int64_t n;
+} gnn_adamw_tensor;
+
+/* Step count and bias-correction powers, in device memory so that a captured
+ * step advances them; start from {0, 1, 1, 0}. */
+typedef struct gnn_adamw_state {
+  double steps;     /* steps taken, t - 1 of the next one          */
+  double beta1_pow; /* beta1^steps                                 */
+  double beta2_pow;
+  double skipped;   /* steps left out for a gradient not finite    */
+} gnn_adamw_state;
+
+/* s = grad_scale (1 over a loss scale; 1 without one), and with max_norm > 0
+ * also the clipping factor: norm = grad_scale sqrt(sum of all g^2), written to
+ * grad_norm (fp32, may be NULL), s = grad_scale max_norm / max(norm + 1e-6,
+ * max_norm).  A norm that is not finite leaves every tensor and the step count
+ * as they are and counts in `skipped`; max_norm = HUGE_VAL checks without
+ * clipping.  max_norm 0: no norm is formed. */
+gnn_status gnn_adamw_workspace(size_t* ws_bytes);
+gnn_status gnn_adamw_step(const gnn_adamw_tensor* tensors, int32_t n_tensors, int32_t param_type,
+                          int32_t grad_type, int32_t state_bits, gnn_adamw_state* state, double lr,
+                          double beta1, double beta2, double eps, double weight_decay,
+                          double grad_scale, double max_norm, float* grad_norm, void* ws,
+                          size_t ws_bytes, gnn_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
 /* Epoch control (SYLVIE guide, sections 8 and 11).  Host code.              */
 /* ------------------------------------------------------------------------ */
 #define GNN_LDR_MAX_DELTA 64

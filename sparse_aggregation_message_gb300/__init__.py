@@ -11,7 +11,7 @@ from typing import Optional, Sequence
 
 from . import _abi
 from ._abi import (CSR_DEDUP, CSR_GCN, CSR_MEAN, CSR_SELF_LOOPS, CSR_SYMMETRIZE,  # noqa: F401
-                   GnnBitRule, GnnBlocked,
+                   GnnAdamwTensor, GnnBitRule, GnnBlocked,
                    GnnBoundary, GnnCsr, GnnError, GnnLdrState, call, load)
 
 LdrState = GnnLdrState
@@ -27,6 +27,9 @@ __all__ = [
     "gnn_layer_tf_workspace", "gnn_layer_fwd_tf", "gnn_layer_bwd_tf",
     "gnn_gat_index", "gnn_gat_workspace", "gnn_gat_layer_fwd", "gnn_gat_layer_bwd",
     "gnn_spmm_bwd_masked", "gnn_spmm_bwd_local_masked", "gnn_dense_bwd_z", "ldz_for",
+    "gnn_group_norm_workspace", "gnn_group_norm_fwd", "gnn_group_norm_bwd",
+    "gnn_gated_workspace", "gnn_gated_fwd", "gnn_gated_bwd",
+    "AdamwTensors", "adamw_state", "gnn_adamw_workspace", "gnn_adamw_step",
     "Blocked", "gnn_blocked_build", "gnn_spmm_fwd_blocked", "gnn_spmm_bwd_blocked",
 ]
 
@@ -149,6 +152,16 @@ class Boundary:
 def _workspace(nbytes: int, device):
     torch = _torch()
     return torch.empty(max(int(nbytes), 1), dtype=torch.uint8, device=device)
+
+
+def _workspace_on(nbytes: int, device, stream):
+    """Scratch for a call on `stream`: allocated there, so that the allocator
+    hands it out again only behind the call's work."""
+    torch = _torch()
+    if stream is None:
+        return _workspace(nbytes, device)
+    with torch.cuda.stream(stream):
+        return _workspace(nbytes, device)
 
 
 def gnn_csr_build(n: int, src, dst, flags: int = CSR_GCN, stream=None) -> Csr:
@@ -721,6 +734,198 @@ def gnn_gat_layer_bwd(csr: Csr, bnd: Optional[Boundary], tpos, spos, dH_out, H_o
          F_in, F_out, seed & 0xFFFFFFFF, _ptr(packed_ws), _ptr(meta_ws), _ptr(dW), _ptr(da_l),
          _ptr(da_r), _ptr(dH_in), dH_in.stride(0) if dH_in is not None else 0, _ptr(g_out),
          _ptr(ws), ws.numel(), _stream(stream))
+
+
+# ---------------------------------------------------------------- node-wise block
+ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "sigmoid": 4}
+
+
+def _type(t) -> int:
+    """GNN_F32, GNN_BF16 or GNN_F16 (-1, which the library refuses, for any other)."""
+    import torch
+    return {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}.get(t.dtype, -1)
+
+
+def _rows(t, n: int, F: int, what: str) -> int:
+    """Row stride of a matrix that holds n rows of F columns, each contiguous."""
+    if t.dim() != 2 or t.shape[0] < n or t.shape[1] < F or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{what}: needs a [>={n}, >={F}] matrix with contiguous rows, got "
+                         f"{tuple(t.shape)} with strides {t.stride()}")
+    if t.device.type != "cuda":
+        raise ValueError(f"{what}: needs a CUDA tensor")
+    return max(t.stride(0), F) if t.shape[0] <= 1 and t.stride(0) < F else t.stride(0)
+
+
+def _f32(t, count: int, what: str):
+    import torch
+    if t is None:
+        return None
+    if t.dtype != torch.float32 or t.numel() < count or not t.is_contiguous() or t.device.type != "cuda":
+        raise ValueError(f"{what}: needs a contiguous fp32 CUDA tensor of {count} elements")
+    return t.data_ptr()
+
+
+def _act(act: str) -> int:
+    if act not in ACTS:
+        raise ValueError(f"act: one of {sorted(ACTS)}, got {act!r}")
+    return ACTS[act]
+
+
+def _seg(seg_start):
+    import torch
+    if seg_start is None:
+        return None, 1
+    if seg_start.dtype != torch.int64 or seg_start.dim() != 1 or seg_start.numel() < 2 or \
+            not seg_start.is_contiguous() or seg_start.device.type != "cuda":
+        raise ValueError("seg_start: needs a contiguous int64 CUDA tensor of n_seg + 1 elements")
+    return seg_start.data_ptr(), seg_start.numel() - 1
+
+
+def gnn_group_norm_workspace(n: int, C: int, groups: int, n_seg: int = 1) -> int:
+    nb = ctypes.c_size_t()
+    call("gnn_group_norm_workspace", n, C, groups, n_seg, ctypes.byref(nb))
+    return nb.value
+
+
+def gnn_group_norm_fwd(X, n: int, C: int, groups: int, Y, mean, rstd, seg_start=None, gamma=None, beta=None,
+                       eps: float = 1e-5, act: str = "none", ws=None, stream=None) -> None:
+    """Y = act(gamma (x - mean) rstd + beta) over the segments of rows that
+    seg_start cuts (``Boundary.part_start`` fits; None: all rows are one);
+    mean and rstd [n_seg, groups] are kept for the backward."""
+    seg, n_seg = _seg(seg_start)
+    ldx, ldy = _rows(X, n, C, "X"), _rows(Y, n, C, "Y")
+    if ws is None:
+        ws = _workspace_on(gnn_group_norm_workspace(n, C, groups, n_seg), X.device, stream)
+    call("gnn_group_norm_fwd", _ptr(X), ldx, _type(X), n, C, groups, seg, n_seg, _f32(gamma, C, "gamma"),
+         _f32(beta, C, "beta"), float(eps), _act(act), _ptr(Y), ldy, _type(Y),
+         _f32(mean, n_seg * groups, "mean"), _f32(rstd, n_seg * groups, "rstd"), _ptr(ws), ws.numel(),
+         _stream(stream))
+
+
+def gnn_group_norm_bwd(dY, X, n: int, C: int, groups: int, mean, rstd, dX, dgamma=None, dbeta=None,
+                       seg_start=None, gamma=None, beta=None, act: str = "none", ws=None,
+                       stream=None) -> None:
+    """dX, dgamma and dbeta of gnn_group_norm_fwd from dY, X and the kept
+    mean and rstd (dY has Y's type, dX has X's)."""
+    seg, n_seg = _seg(seg_start)
+    ldx, ldy, lddx = _rows(X, n, C, "X"), _rows(dY, n, C, "dY"), _rows(dX, n, C, "dX")
+    if dX.dtype != X.dtype:
+        raise ValueError("dX: needs X's type")
+    if ws is None:
+        ws = _workspace_on(gnn_group_norm_workspace(n, C, groups, n_seg), X.device, stream)
+    call("gnn_group_norm_bwd", _ptr(dY), ldy, _type(dY), _ptr(X), ldx, _type(X), n, C, groups, seg, n_seg,
+         _f32(gamma, C, "gamma"), _f32(beta, C, "beta"), _act(act), _f32(mean, n_seg * groups, "mean"),
+         _f32(rstd, n_seg * groups, "rstd"), _ptr(dX), lddx, _f32(dgamma, C, "dgamma"),
+         _f32(dbeta, C, "dbeta"), _ptr(ws), ws.numel(), _stream(stream))
+
+
+def gnn_gated_workspace(n: int, F_in: int, F_mid: int):
+    """Workspace bytes of gnn_gated_fwd and gnn_gated_bwd."""
+    f, b = ctypes.c_size_t(), ctypes.c_size_t()
+    call("gnn_gated_workspace", n, F_in, F_mid, ctypes.byref(f), ctypes.byref(b))
+    return f.value, b.value
+
+
+def _one_type(X, **others) -> int:
+    for name, t in others.items():
+        if t is not None and t.dtype != X.dtype:
+            raise ValueError(f"{name}: needs X's type {X.dtype}, got {t.dtype}")
+    return _type(X)
+
+
+def gnn_gated_fwd(X, n: int, F_in: int, Wg, Wu, F_mid: int, H, act: str = "silu", ws=None,
+                  stream=None) -> None:
+    """H = act(X Wg) * (X Wu) on tcgen05 (X, Wg, Wu, H of one type, bf16 or
+    fp16; Wg, Wu [F_in, F_mid])."""
+    t = _one_type(X, Wg=Wg, Wu=Wu, H=H)
+    need = gnn_gated_workspace(n, F_in, F_mid)[0]
+    if ws is None and need:
+        ws = _workspace_on(need, X.device, stream)
+    call("gnn_gated_fwd", _ptr(X), _rows(X, n, F_in, "X"), t, n, F_in, _ptr(Wg), _rows(Wg, F_in, F_mid, "Wg"),
+         _ptr(Wu), _rows(Wu, F_in, F_mid, "Wu"), F_mid, _act(act), _ptr(H), _rows(H, n, F_mid, "H"),
+         _ptr(ws), ws.numel() if ws is not None else 0, _stream(stream))
+
+
+def gnn_gated_bwd(dH, X, n: int, F_in: int, Wg, Wu, F_mid: int, dX=None, dWg=None, dWu=None,
+                  act: str = "silu", ws=None, stream=None) -> None:
+    """dX, dWg and dWu of gnn_gated_fwd (X's type; the projections are
+    recomputed).  dH has X's type or fp32."""
+    t = _one_type(X, Wg=Wg, Wu=Wu, dX=dX, dWg=dWg, dWu=dWu)
+    if ws is None:
+        ws = _workspace_on(gnn_gated_workspace(n, F_in, F_mid)[1], X.device, stream)
+    call("gnn_gated_bwd", _ptr(dH), _rows(dH, n, F_mid, "dH"), _type(dH), _ptr(X), _rows(X, n, F_in, "X"), t, n,
+         F_in, _ptr(Wg), _rows(Wg, F_in, F_mid, "Wg"), _ptr(Wu), _rows(Wu, F_in, F_mid, "Wu"), F_mid, _act(act),
+         _ptr(dX), _rows(dX, n, F_in, "dX") if dX is not None else 0,
+         _ptr(dWg), _rows(dWg, F_in, F_mid, "dWg") if dWg is not None else 0,
+         _ptr(dWu), _rows(dWu, F_in, F_mid, "dWu") if dWu is not None else 0,
+         _ptr(ws), ws.numel(), _stream(stream))
+
+
+class AdamwTensors:
+    """The tensors of an optimiser, checked once: lists of parameters (fp32 or
+    bf16, updated in place), their gradients, m, v and, with 8-bit states
+    (torch.float8_e4m3fn m and v), the scales m_scale and v_scale (fp32, one
+    per 256 elements of a tensor); copies (bf16, optional) receive the updated
+    parameters.  All are contiguous CUDA tensors and stay the caller's."""
+
+    def __init__(self, params, grads, m, v, m_scale=None, v_scale=None, copies=None):
+        import torch
+        k = len(params)
+        self.count = k
+        lists = dict(params=params, grads=grads, m=m, v=v, m_scale=m_scale, v_scale=v_scale, copies=copies)
+        for name, ts in lists.items():
+            if ts is not None and len(ts) != k:
+                raise ValueError(f"{name}: {len(ts)} tensors for {k} parameters")
+        self.state_bits = 8 if k and m[0].dtype == torch.float8_e4m3fn else 32
+        if self.state_bits == 8 and (m_scale is None or v_scale is None):
+            raise ValueError("8-bit states need m_scale and v_scale")
+        state = torch.float8_e4m3fn if self.state_bits == 8 else torch.float32
+        want = dict(params=params[0].dtype if k else torch.float32, grads=grads[0].dtype if k else torch.float32,
+                    m=state, v=state, m_scale=torch.float32, v_scale=torch.float32, copies=torch.bfloat16)
+        for name, ts in lists.items():
+            for i, t in enumerate(ts or ()):
+                n = params[i].numel()
+                size = -(-n // 256) if name.endswith("scale") else n
+                if t.dtype != want[name] or t.numel() != size or not t.is_contiguous() or t.device.type != "cuda":
+                    raise ValueError(f"{name}[{i}]: needs a contiguous {want[name]} CUDA tensor of {size} elements")
+        self.param_type = _type(params[0]) if k else 0
+        self.grad_type = _type(grads[0]) if k else 0
+        self._keep = {name: list(ts) for name, ts in lists.items() if ts is not None}
+        at = lambda ts, i: None if ts is None else ts[i].data_ptr()  # noqa: E731
+        self.c = (GnnAdamwTensor * max(k, 1))(*[
+            GnnAdamwTensor(at(params, i), at(grads, i), at(m, i), at(v, i),
+                           at(m_scale, i) if self.state_bits == 8 else None,
+                           at(v_scale, i) if self.state_bits == 8 else None, at(copies, i), params[i].numel())
+            for i in range(k)])
+
+
+def adamw_state(device="cuda"):
+    """A new optimiser's step state: {steps, beta1^steps, beta2^steps, steps
+    skipped} as a device fp64 tensor (save and load it with the weights)."""
+    import torch
+    return torch.tensor([0.0, 1.0, 1.0, 0.0], dtype=torch.float64, device=device)
+
+
+def gnn_adamw_workspace() -> int:
+    nb = ctypes.c_size_t()
+    call("gnn_adamw_workspace", ctypes.byref(nb))
+    return nb.value
+
+
+def gnn_adamw_step(tensors: AdamwTensors, state, lr: float, beta1: float = 0.9, beta2: float = 0.999,
+                   eps: float = 1e-8, weight_decay: float = 0.01, grad_scale: float = 1.0,
+                   max_norm: float = 0.0, grad_norm=None, ws=None, stream=None) -> None:
+    """One AdamW step over every tensor; with max_norm > 0 the gradients are
+    clipped by their global norm (written to grad_norm, fp32 [1]) and a step
+    whose norm is not finite is skipped."""
+    import torch
+    if state.dtype != torch.float64 or state.numel() != 4 or not state.is_contiguous() or state.device.type != "cuda":
+        raise ValueError("state: needs the fp64 CUDA tensor that adamw_state makes")
+    if ws is None:
+        ws = _workspace_on(gnn_adamw_workspace(), state.device, stream)
+    call("gnn_adamw_step", tensors.c, tensors.count, tensors.param_type, tensors.grad_type, tensors.state_bits,
+         _ptr(state), float(lr), float(beta1), float(beta2), float(eps), float(weight_decay), float(grad_scale),
+         float(max_norm), _f32(grad_norm, 1, "grad_norm"), _ptr(ws), ws.numel(), _stream(stream))
 
 
 # ---------------------------------------------------------------- epoch control (host only)

@@ -56,6 +56,11 @@ class GnnLdrState(ctypes.Structure):
                 ("ldr", ctypes.c_double * (GNN_LDR_MAX_DELTA + 1))]
 
 
+class GnnAdamwTensor(ctypes.Structure):
+    _fields_ = [("param", c_vp), ("grad", c_vp), ("m", c_vp), ("v", c_vp), ("m_scale", c_vp),
+                ("v_scale", c_vp), ("copy", c_vp), ("n", c_i64)]
+
+
 P_csr = ctypes.POINTER(GnnCsr)
 P_bnd = ctypes.POINTER(GnnBoundary)
 P_rule = ctypes.POINTER(GnnBitRule)
@@ -147,6 +152,24 @@ PROTOTYPES = {
     "gnn_ldr_update": (ctypes.c_int, [ctypes.c_void_p, ctypes.POINTER(ctypes.c_double), c_i32,
                                       ctypes.c_double]),
     "gnn_quant_divide": (ctypes.c_int, [c_vp, c_vp, c_vp, c_i64, c_vp]),
+    "gnn_group_norm_workspace": (ctypes.c_int, [c_i64, c_i32, c_i32, c_i32, P_size]),
+    "gnn_group_norm_fwd": (ctypes.c_int, [c_vp, c_i64, c_i32, c_i64, c_i32, c_i32, c_vp, c_i32, c_vp, c_vp,
+                                          ctypes.c_double, c_i32, c_vp, c_i64, c_i32, c_vp, c_vp, c_vp,
+                                          c_size, c_vp]),
+    "gnn_group_norm_bwd": (ctypes.c_int, [c_vp, c_i64, c_i32, c_vp, c_i64, c_i32, c_i64, c_i32, c_i32, c_vp,
+                                          c_i32, c_vp, c_vp, c_i32, c_vp, c_vp, c_vp, c_i64, c_vp, c_vp,
+                                          c_vp, c_size, c_vp]),
+    "gnn_gated_workspace": (ctypes.c_int, [c_i64, c_i32, c_i32, P_size, P_size]),
+    "gnn_gated_fwd": (ctypes.c_int, [c_vp, c_i64, c_i32, c_i64, c_i32, c_vp, c_i64, c_vp, c_i64, c_i32, c_i32,
+                                     c_vp, c_i64, c_vp, c_size, c_vp]),
+    "gnn_gated_bwd": (ctypes.c_int, [c_vp, c_i64, c_i32, c_vp, c_i64, c_i32, c_i64, c_i32, c_vp, c_i64, c_vp,
+                                     c_i64, c_i32, c_i32, c_vp, c_i64, c_vp, c_i64, c_vp, c_i64, c_vp,
+                                     c_size, c_vp]),
+    "gnn_adamw_workspace": (ctypes.c_int, [P_size]),
+    "gnn_adamw_step": (ctypes.c_int, [ctypes.POINTER(GnnAdamwTensor), c_i32, c_i32, c_i32, c_i32, c_vp,
+                                      ctypes.c_double, ctypes.c_double, ctypes.c_double, ctypes.c_double,
+                                      ctypes.c_double, ctypes.c_double, ctypes.c_double, c_vp, c_vp, c_size,
+                                      c_vp]),
     "gnn_sync_check": (ctypes.c_int, [c_vp]),
 }
 

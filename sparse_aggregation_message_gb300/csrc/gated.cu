@@ -1,0 +1,670 @@
+// Gated feed-forward projections H = act(X Wg) * (X Wu) and their backward
+// pass on tcgen05 tensor cores.
+//
+// One persistent, warp-specialised kernel shape serves the four products:
+//   FWD  G|U = X [Wg|Wu], epilogue H = act(G) * U
+//   ACT  the same product again in the backward, epilogue dG|dU from dH
+//   DX   dX = [dG|dU] [Wg|Wu]^T (one accumulation over both halves)
+//   DW   dWg|dWu = X^T [dG|dU], split over the rows
+// A 128 x 256 accumulator tile of FWD and ACT holds 128 gate and the same 128
+// up columns, so both factors of an output element meet in one thread and G, U
+// never reach memory.  Weights are read as they lie ([F_in][F_mid], columns
+// contiguous): MN-major operands in FWD/ACT, K-major in DX.
+//
+// Roles: warp 0 issues TMA loads into a ring of 128-byte-swizzled tiles, warp 1
+// issues the MMAs from one thread, warps 2-9 drain one of two TMEM accumulators
+// while the next tile is multiplied (eight of them: exponentials of 128 x 128
+// outputs would take longer than the product on four).  Every wait is bounded.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "gemm.h"
+#include "internal.h"
+#include "nodewise.cuh"
+#include "tc.cuh"
+
+namespace gnn {
+
+namespace {
+
+enum Mode { FWD, ACT, DX, DW };
+
+constexpr int BM = 128, BN = 256, BK = 64;
+constexpr int A_STAGE = BM * BK * 2;  // 16 KB
+constexpr int B_STAGE = BN * BK * 2;  // 32 KB
+constexpr int BOX = 64 * BK * 2;      // one 64-wide block of an MN-major operand: 8 KB
+constexpr int SUB = 32 * 128;         // a warp's 32 rows x 128 bytes of staged output
+constexpr int EPI_WARPS = 8;
+constexpr int THREADS = 64 + 32 * EPI_WARPS;
+
+constexpr int stages(Mode m) { return m == ACT ? 3 : 4; }
+constexpr int subs(Mode m) { return m == ACT ? 2 : m == DW ? 0 : 1; }  // staging tiles of an epilogue warp
+constexpr int smem_bytes(Mode m) {
+  return stages(m) * (A_STAGE + B_STAGE) + EPI_WARPS * subs(m) * SUB + 1024 /*barriers*/ + 1024 /*align*/;
+}
+
+struct Args {
+  CUtensorMap a[2], b[2];  // the operands (of the gate and the up half where they differ)
+  CUtensorMap out[2];      // H, or dG and dU, or dX
+  CUtensorMap dh;
+  int M, N, K;             // rows of the output, columns of one half, length of one half's sum
+  int bn;                  // DX: tile columns
+  int num_m, num_n, num_kb;  // tiles; k blocks of one half
+  int act, dh_f32;
+  int splits, kb_per_split;  // DW
+  float* part;
+  unsigned* flags;
+};
+
+struct Smem {
+  uint8_t *a, *b, *out;
+  uint64_t *full, *empty, *tfull, *tempty, *dh;
+  uint32_t* tmem;
+  volatile int* abort_flag;
+};
+
+template <Mode M>
+__device__ __forceinline__ Smem carve(uint8_t* raw) {
+  Smem s;
+  uint8_t* p = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+  s.a = p;
+  s.b = p + stages(M) * A_STAGE;
+  s.out = s.b + stages(M) * B_STAGE;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(s.out + EPI_WARPS * subs(M) * SUB);
+  s.full = bars;
+  s.empty = bars + 4;
+  s.tfull = bars + 8;
+  s.tempty = bars + 10;
+  s.dh = bars + 12;
+  s.tmem = reinterpret_cast<uint32_t*>(bars + 12 + EPI_WARPS);
+  s.abort_flag = reinterpret_cast<volatile int*>(s.tmem + 1);
+  return s;
+}
+
+// A tile's place: row block, column block, half (DW: gate or up), k blocks.
+struct Tile {
+  int m0, n0, half, split, kb0, kb1;
+};
+template <Mode M>
+__device__ __forceinline__ Tile tile_at(const Args& g, int t) {
+  Tile r;
+  if (M == DW) {
+    r.m0 = (t % g.num_m) * BM;
+    t /= g.num_m;
+    r.n0 = (t % g.num_n) * BN;
+    t /= g.num_n;
+    r.half = t & 1;
+    r.split = t >> 1;
+    r.kb0 = r.split * g.kb_per_split;
+    r.kb1 = min(g.num_kb, r.kb0 + g.kb_per_split);
+  } else {
+    // the column blocks of one row block run side by side, so its rows are
+    // read from memory once and from L2 after that
+    r.n0 = (t % g.num_n) * (M == DX ? g.bn : BN / 2);
+    r.m0 = (t / g.num_n) * BM;
+    r.half = r.split = 0;
+    r.kb0 = 0;
+    r.kb1 = M == DX ? 2 * g.num_kb : g.num_kb;
+  }
+  return r;
+}
+template <Mode M>
+__device__ __forceinline__ int num_tiles(const Args& g) {
+  return g.num_m * g.num_n * (M == DW ? 2 * g.splits : 1);
+}
+
+template <Mode M>
+__device__ __forceinline__ void load_stage(const Args& g, const Smem& s, const Tile& t, int kb, int st) {
+  uint8_t* a = s.a + st * A_STAGE;
+  uint8_t* b = s.b + st * B_STAGE;
+  uint64_t* bar = &s.full[st];
+  if (M == FWD || M == ACT) {
+    tc::mbar_expect_tx(bar, A_STAGE + B_STAGE);
+    tc::tma_load_2d(a, &g.a[0], bar, kb * BK, t.m0);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) tc::tma_load_2d(b + j * BOX, &g.b[j >> 1], bar, t.n0 + 64 * (j & 1), kb * BK);
+  } else if (M == DX) {
+    const int half = kb >= g.num_kb;
+    const int k = (half ? kb - g.num_kb : kb) * BK;
+    tc::mbar_expect_tx(bar, A_STAGE + g.bn * BK * 2);
+    tc::tma_load_2d(a, &g.a[half], bar, k, t.m0);
+    tc::tma_load_2d(b, &g.b[half], bar, k, t.n0);
+  } else {
+    tc::mbar_expect_tx(bar, A_STAGE + B_STAGE);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) tc::tma_load_2d(a + j * BOX, &g.a[0], bar, t.m0 + 64 * j, kb * BK);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) tc::tma_load_2d(b + j * BOX, &g.b[t.half], bar, t.n0 + 64 * j, kb * BK);
+  }
+}
+
+// Eight 2-byte columns of a staged row: chunk k of row r of a swizzled tile.
+__device__ __forceinline__ uint4* staged(uint8_t* tile, int r, int k) {
+  return reinterpret_cast<uint4*>(tile + r * 128 + ((k ^ (r & 7)) << 4));
+}
+
+// Runs f with the activation as a compile-time value.
+template <class Fn>
+__device__ __forceinline__ void with_act(int act, Fn f) {
+  switch (act) {
+    case GNN_ACT_RELU: f(std::integral_constant<int, GNN_ACT_RELU>()); break;
+    case GNN_ACT_SILU: f(std::integral_constant<int, GNN_ACT_SILU>()); break;
+    case GNN_ACT_GELU: f(std::integral_constant<int, GNN_ACT_GELU>()); break;
+    case GNN_ACT_SIGMOID: f(std::integral_constant<int, GNN_ACT_SIGMOID>()); break;
+    default: f(std::integral_constant<int, GNN_ACT_NONE>());
+  }
+}
+
+template <Mode M, class T>
+__global__ void __launch_bounds__(THREADS, 1) gated_kernel(const __grid_constant__ Args g) {
+  extern __shared__ uint8_t smem_raw[];
+  const Smem s = carve<M>(smem_raw);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+  constexpr int ST = stages(M);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < ST; ++i) {
+      tc::mbar_init(&s.full[i], 1);
+      tc::mbar_init(&s.empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(&s.tfull[i], 1);
+      tc::mbar_init(&s.tempty[i], 32 * EPI_WARPS);
+    }
+    for (int i = 0; i < EPI_WARPS; ++i) tc::mbar_init(&s.dh[i], 1);
+    *s.abort_flag = 0;
+    tc::fence_barrier_init();
+  }
+  if (warp == 1) {
+    tc::tmem_alloc(s.tmem, 2 * BN);
+    tc::tmem_relinquish();
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = *s.tmem;
+  const int tiles = num_tiles<M>(g);
+
+  if (warp == 0 && lane == 0) {
+    int st = 0;
+    uint32_t ph = 0;
+    for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
+      const Tile w = tile_at<M>(g, t);
+      for (int kb = w.kb0; kb < w.kb1; ++kb) {
+        if (!tc::mbar_wait(&s.empty[st], ph ^ 1, g.flags, s.abort_flag)) goto done;
+        load_stage<M>(g, s, w, kb, st);
+        if (++st == ST) { st = 0; ph ^= 1; }
+      }
+    }
+  } else if (warp == 1 && lane == 0) {
+    constexpr bool a_mn = M == DW, b_mn = M != DX;
+    const uint32_t idesc = tc::idesc_16(kBf16, BM, M == DX ? g.bn : BN, a_mn, b_mn);
+    int st = 0, it = 0;
+    uint32_t ph = 0;
+    for (int t = blockIdx.x; t < tiles; t += gridDim.x, ++it) {
+      const Tile w = tile_at<M>(g, t);
+      const int acc = it & 1;
+      if (!tc::mbar_wait(&s.tempty[acc], ((it >> 1) & 1) ^ 1, g.flags, s.abort_flag)) goto done;
+      tc::fence_after_sync();
+      const uint32_t d = tmem + acc * BN;
+      for (int kb = w.kb0; kb < w.kb1; ++kb) {
+        if (!tc::mbar_wait(&s.full[st], ph, g.flags, s.abort_flag)) goto done;
+        tc::fence_after_sync();
+        const uint32_t a0 = tc::smem_u32(s.a + st * A_STAGE), b0 = tc::smem_u32(s.b + st * B_STAGE);
+#pragma unroll
+        for (int k = 0; k < BK / 16; ++k)  // 16 elements of K: 32 bytes K-major, 16 rows of 128 bytes MN-major
+          tc::mma_bf16(d, tc::sw128_desc(a0 + k * (a_mn ? 2048 : 32), a_mn ? BOX : 16),
+                       tc::sw128_desc(b0 + k * (b_mn ? 2048 : 32), b_mn ? BOX : 16), idesc,
+                       kb > w.kb0 || k ? 1u : 0u);
+        tc::mma_commit(&s.empty[st]);
+        if (++st == ST) { st = 0; ph ^= 1; }
+      }
+      tc::mma_commit(&s.tfull[acc]);
+    }
+  } else if (warp >= 2) {
+    const int e = warp - 2, q = warp & 3, h = e >> 2;  // TMEM lane quarter, column half
+    uint8_t* stage = s.out + e * subs(M) * SUB;
+    const uint32_t lane0 = tmem + ((uint32_t)(q * 32) << 16);
+    int it = 0;
+    for (int t = blockIdx.x; t < tiles; t += gridDim.x, ++it) {
+      const Tile w = tile_at<M>(g, t);
+      const int acc = it & 1;
+      const uint32_t base = lane0 + acc * BN;
+      const int row = w.m0 + q * 32;  // of the warp
+      if (M == ACT) {
+        // this warp's dH into its staging tiles, once the stores of the last
+        // tile have read them
+        if (lane == 0) {
+          tc::bulk_wait_read<0>();
+          tc::mbar_expect_tx(&s.dh[e], g.dh_f32 ? 2 * SUB : SUB);
+          tc::tma_load_2d(stage, &g.dh, &s.dh[e], w.n0 + h * 64, row);
+          if (g.dh_f32) tc::tma_load_2d(stage + SUB, &g.dh, &s.dh[e], w.n0 + h * 64 + 32, row);
+        }
+      }
+      if (!tc::mbar_wait(&s.tfull[acc], (it >> 1) & 1, g.flags, s.abort_flag)) goto done;
+      tc::fence_after_sync();
+      if (M == FWD) {
+        if (lane == 0) tc::bulk_wait_read<0>();
+        __syncwarp();
+#pragma unroll 1
+        for (int c = 0; c < 64; c += 32) {
+          uint32_t gate[32], up[32];
+          tc::tmem_ld32(base + h * 64 + c, gate);
+          tc::tmem_ld32(base + BN / 2 + h * 64 + c, up);
+          tc::tmem_wait_ld();
+          if (c == 32) {
+            tc::fence_before_sync();
+            tc::mbar_arrive(&s.tempty[acc]);
+          }
+          with_act(g.act, [&](auto A) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              uint32_t o[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const int i = 8 * k + 2 * j;
+                o[j] = Pack2<T>::to(act_f(__uint_as_float(gate[i]), A) * __uint_as_float(up[i]),
+                                    act_f(__uint_as_float(gate[i + 1]), A) * __uint_as_float(up[i + 1]));
+              }
+              *staged(stage, lane, (c >> 3) + k) = make_uint4(o[0], o[1], o[2], o[3]);
+            }
+          });
+        }
+        tc::fence_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          tc::tma_store_2d(&g.out[0], stage, w.n0 + h * 64, row);
+          tc::bulk_commit();
+        }
+      } else if (M == ACT) {
+        if (!tc::mbar_wait(&s.dh[e], it & 1, g.flags, s.abort_flag)) goto done;
+        // columns 0-31 come first: with dH in fp32 they fill the first tile, and
+        // the bf16 outputs of all 64 columns take half of each
+        float dh[2][32];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          if (g.dh_f32) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const uint4 v = *staged(stage + c * SUB, lane, k);
+              dh[c][4 * k] = __uint_as_float(v.x), dh[c][4 * k + 1] = __uint_as_float(v.y);
+              dh[c][4 * k + 2] = __uint_as_float(v.z), dh[c][4 * k + 3] = __uint_as_float(v.w);
+            }
+          } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint4 v = *staged(stage, lane, c * 4 + k);
+              const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const float2 f = Pack2<T>::from(x[j]);
+                dh[c][8 * k + 2 * j] = f.x, dh[c][8 * k + 2 * j + 1] = f.y;
+              }
+            }
+          }
+        }
+        __syncwarp();
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t gate[32], up[32];
+          tc::tmem_ld32(base + h * 64 + c * 32, gate);
+          tc::tmem_ld32(base + BN / 2 + h * 64 + c * 32, up);
+          tc::tmem_wait_ld();
+          if (c == 1) {
+            tc::fence_before_sync();
+            tc::mbar_arrive(&s.tempty[acc]);
+          }
+          with_act(g.act, [&](auto A) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              uint32_t og[4], ou[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                float x[2], y[2];
+#pragma unroll
+                for (int z = 0; z < 2; ++z) {
+                  const int i = 8 * k + 2 * j + z;
+                  float a, d;
+                  act_grad_f(__uint_as_float(gate[i]), A, a, d);
+                  x[z] = dh[c][i] * __uint_as_float(up[i]) * d;
+                  y[z] = dh[c][i] * a;
+                }
+                og[j] = Pack2<T>::to(x[0], x[1]);
+                ou[j] = Pack2<T>::to(y[0], y[1]);
+              }
+              *staged(stage, lane, c * 4 + k) = make_uint4(og[0], og[1], og[2], og[3]);
+              *staged(stage + SUB, lane, c * 4 + k) = make_uint4(ou[0], ou[1], ou[2], ou[3]);
+            }
+          });
+        }
+        tc::fence_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          tc::tma_store_2d(&g.out[0], stage, w.n0 + h * 64, row);
+          tc::tma_store_2d(&g.out[1], stage + SUB, w.n0 + h * 64, row);
+          tc::bulk_commit();
+        }
+      } else if (M == DX) {
+        // 64-column pieces of the tile, dealt to the two column halves in turn
+        const int pieces = (g.bn + 63) / 64;
+        for (int c = h; c < pieces; c += 2) {
+          uint32_t v[64];
+          tc::tmem_ld32(base + c * 64, *reinterpret_cast<uint32_t(*)[32]>(v));
+          tc::tmem_ld32(base + c * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(v + 32));
+          tc::tmem_wait_ld();
+          if (lane == 0) tc::bulk_wait_read<0>();
+          __syncwarp();
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            uint32_t o[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              o[j] = Pack2<T>::to(__uint_as_float(v[8 * k + 2 * j]), __uint_as_float(v[8 * k + 2 * j + 1]));
+            *staged(stage, lane, k) = make_uint4(o[0], o[1], o[2], o[3]);
+          }
+          tc::fence_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tc::tma_store_2d(&g.out[0], stage, w.n0 + c * 64, row);
+            tc::bulk_commit();
+          }
+        }
+        tc::fence_before_sync();
+        tc::mbar_arrive(&s.tempty[acc]);
+      } else {
+        float* prow = g.part + (((int64_t)w.split * 2 + w.half) * g.num_m * BM + row + lane) * ((int64_t)g.num_n * BN) +
+                      w.n0 + h * (BN / 2);
+#pragma unroll 1
+        for (int c = 0; c < BN / 2; c += 32) {
+          uint32_t v[32];
+          tc::tmem_ld32(base + h * (BN / 2) + c, v);
+          tc::tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 32; j += 4)
+            *reinterpret_cast<uint4*>(prow + c + j) = make_uint4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+        }
+        tc::fence_before_sync();
+        tc::mbar_arrive(&s.tempty[acc]);
+      }
+    }
+  }
+done:
+  if (warp >= 2 && lane == 0) tc::bulk_wait_all();  // stores finish before the block exits
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == 1) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, 2 * BN);
+  }
+}
+
+// dWg and dWu from the split partials, added in split order; padding columns
+// up to a multiple of 16 come out zero (their partials are).
+template <class T>
+__global__ void __launch_bounds__(256) gated_dw_kernel(const float* part, int splits, int D, int F, int64_t ldp,
+                                                       int64_t half_stride, T* dWg, int64_t ldg, T* dWu,
+                                                       int64_t ldu) {
+  const int per = (F + 15) / 16 * 2;  // chunks of 8 columns
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= (int64_t)2 * D * per) return;
+  const int c = (int)(i % per) * 8;
+  const int64_t r = i / per;
+  const int half = r >= D;
+  const int64_t d = half ? r - D : r;
+  const float* p = part + half * half_stride + d * ldp + c;
+  float acc[8] = {};
+  for (int s = 0; s < splits; ++s) {
+    float v[8];
+    load_vec<8>(p + s * 2 * half_stride, v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc[j] += v[j];
+  }
+  store_vec<8>((half ? dWu + d * ldu : dWg + d * ldg) + c, acc);
+}
+
+// ---------------------------------------------------------------- host side
+int sm_count() {
+  static int n = 0;
+  if (n == 0) {
+    int dev = 0;
+    cudaGetDevice(&dev);
+    cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+    if (n <= 0) n = 152;
+  }
+  return n;
+}
+
+int64_t up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
+
+// The split of the weight gradients over the rows: the number of parts whose
+// rounds of tiles over the SMs take the fewest k blocks, each part at least
+// eight of them and its tile's drain counted as four.
+struct DwPlan {
+  int num_m, num_n, splits, kb_per_split;
+  size_t part_floats;
+};
+DwPlan dw_plan(int64_t n, int D, int F) {
+  DwPlan p;
+  p.num_m = (D + BM - 1) / BM;
+  p.num_n = (F + BN - 1) / BN;
+  const int64_t kb = (n + BK - 1) / BK, tiles = 2ll * p.num_m * p.num_n;
+  int64_t best = -1;
+  p.splits = 1;
+  p.kb_per_split = (int)(kb > 0 ? kb : 1);
+  for (int64_t s = 1; s <= 152 && s * 8 <= (kb > 8 ? kb : 8); ++s) {
+    if (s > 1 && s * tiles > 4 * 152) break;  // bounds the partials
+    const int64_t per = (kb + s - 1) / s, used = (kb + per - 1) / (per > 0 ? per : 1);
+    const int64_t rounds = (used * tiles + 151) / 152, cost = rounds * (per + 4);
+    if (used > 0 && (best < 0 || cost < best)) {
+      best = cost;
+      p.splits = (int)used;
+      p.kb_per_split = (int)per;
+    }
+  }
+  p.part_floats = (size_t)p.splits * 2 * p.num_m * BM * p.num_n * BN;
+  return p;
+}
+
+struct GatedWs {
+  void* dg;
+  void* du;
+  float* part;
+  int64_t ldf;
+  size_t bytes;
+};
+GatedWs gated_ws(void* base, size_t cap, int64_t n, int D, int F, bool* ok) {
+  Arena ar(base, cap);
+  GatedWs w{};
+  w.ldf = up(F, 8);
+  w.dg = ar.take<uint16_t>((size_t)n * w.ldf);
+  w.du = ar.take<uint16_t>((size_t)n * w.ldf);
+  w.part = ar.take<float>(dw_plan(n, D, F).part_floats);
+  w.bytes = ar.used;
+  *ok = ar.ok();
+  return w;
+}
+
+template <Mode M, class T>
+gnn_status launch_gated(const Args& g, cudaStream_t st) {
+  static bool ready = false;
+  if (!ready) {
+    GNN_CUDA(cudaFuncSetAttribute(gated_kernel<M, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(M)));
+    ready = true;
+  }
+  const int64_t tiles = (int64_t)g.num_m * g.num_n * (M == DW ? 2 * g.splits : 1);
+  const int grid = (int)(tiles < sm_count() ? tiles : sm_count());
+  gated_kernel<M, T><<<grid, THREADS, smem_bytes(M), st>>>(g);
+  GNN_CHECK_LAUNCH();
+  return GNN_OK;
+}
+
+// A map of a 2-byte matrix of `cols` used columns.
+template <class T>
+gnn_status map16(CUtensorMap* m, const void* p, int64_t rows, int64_t cols, int64_t ld, int box_c, int box_r) {
+  return encode_tmap_2d(m, std::is_same<T, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                          : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                        p, (uint64_t)cols, (uint64_t)rows, (uint64_t)ld * 2, (uint32_t)box_c, (uint32_t)box_r);
+}
+
+#define GNN_TRY(expr)                 \
+  do {                                \
+    const gnn_status s_ = (expr);     \
+    if (s_ != GNN_OK) return s_;      \
+  } while (0)
+
+struct Mat {
+  void* p;
+  int64_t ld;
+};
+
+template <class T>
+gnn_status product_args(Args& g, int64_t n, int D, int F, int act, Mat X, Mat Wg, Mat Wu) {
+  g.flags = device_flags();
+  if (!g.flags) return fail(GNN_ERR_CUDA, "device flag word unavailable");
+  g.M = (int)n, g.N = F, g.K = D, g.act = act;
+  g.num_m = (int)((n + BM - 1) / BM), g.num_n = (F + BN / 2 - 1) / (BN / 2), g.num_kb = (D + BK - 1) / BK;
+  GNN_TRY(map16<T>(&g.a[0], X.p, n, D, X.ld, BK, BM));
+  GNN_TRY(map16<T>(&g.b[0], Wg.p, D, F, Wg.ld, 64, BK));
+  GNN_TRY(map16<T>(&g.b[1], Wu.p, D, F, Wu.ld, 64, BK));
+  return GNN_OK;
+}
+
+template <class T>
+gnn_status gated_fwd(int64_t n, int D, int F, int act, Mat X, Mat Wg, Mat Wu, Mat H, cudaStream_t st) {
+  Args g{};
+  GNN_TRY(product_args<T>(g, n, D, F, act, X, Wg, Wu));
+  GNN_TRY(map16<T>(&g.out[0], H.p, n, up(F, 16), H.ld, 64, 32));
+  return launch_gated<FWD, T>(g, st);
+}
+
+template <class T>
+gnn_status gated_bwd(int64_t n, int D, int F, int act, int dh_f32, Mat dH, Mat X, Mat Wg, Mat Wu, Mat dX,
+                     Mat dWg, Mat dWu, const GatedWs& w, cudaStream_t st) {
+  if (n > 0) {
+    Args g{};
+    GNN_TRY(product_args<T>(g, n, D, F, act, X, Wg, Wu));
+    g.dh_f32 = dh_f32;
+    if (dh_f32)
+      GNN_TRY(encode_tmap_2d(&g.dh, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, dH.p, F, n, dH.ld * 4, 32, 32));
+    else
+      GNN_TRY(map16<T>(&g.dh, dH.p, n, F, dH.ld, 64, 32));
+    GNN_TRY(map16<T>(&g.out[0], w.dg, n, F, w.ldf, 64, 32));
+    GNN_TRY(map16<T>(&g.out[1], w.du, n, F, w.ldf, 64, 32));
+    GNN_TRY((launch_gated<ACT, T>(g, st)));
+    if (dX.p) {
+      Args d{};
+      d.flags = g.flags;
+      const int num_n = (D + BN - 1) / BN;
+      d.bn = num_n == 1 ? (int)up(D, 16) : (int)up((D + num_n - 1) / num_n, 64);
+      d.num_m = g.num_m, d.num_n = (D + d.bn - 1) / d.bn, d.num_kb = (F + BK - 1) / BK;
+      GNN_TRY(map16<T>(&d.a[0], w.dg, n, F, w.ldf, BK, BM));
+      GNN_TRY(map16<T>(&d.a[1], w.du, n, F, w.ldf, BK, BM));
+      GNN_TRY(map16<T>(&d.b[0], Wg.p, D, F, Wg.ld, BK, d.bn));
+      GNN_TRY(map16<T>(&d.b[1], Wu.p, D, F, Wu.ld, BK, d.bn));
+      GNN_TRY(map16<T>(&d.out[0], dX.p, n, up(D, 16), dX.ld, 64, 32));
+      GNN_TRY((launch_gated<DX, T>(d, st)));
+    }
+  }
+  if (dWg.p) {
+    const DwPlan p = dw_plan(n, D, F);
+    int splits = 0;
+    if (n > 0) {
+      Args d{};
+      d.flags = device_flags();
+      d.num_m = p.num_m, d.num_n = p.num_n, d.num_kb = (int)((n + BK - 1) / BK);
+      d.splits = splits = p.splits, d.kb_per_split = p.kb_per_split, d.part = w.part;
+      GNN_TRY(map16<T>(&d.a[0], X.p, n, D, X.ld, 64, BK));
+      GNN_TRY(map16<T>(&d.b[0], w.dg, n, F, w.ldf, 64, BK));
+      GNN_TRY(map16<T>(&d.b[1], w.du, n, F, w.ldf, 64, BK));
+      GNN_TRY((launch_gated<DW, T>(d, st)));
+    }
+    const int64_t work = 2ll * D * (up(F, 16) / 8), ldp = (int64_t)p.num_n * BN;
+    gated_dw_kernel<T><<<(unsigned)((work + 255) / 256), 256, 0, st>>>(
+        w.part, splits, D, F, ldp, (int64_t)p.num_m * BM * ldp, static_cast<T*>(dWg.p), dWg.ld,
+        static_cast<T*>(dWu.p), dWu.ld);
+    GNN_CHECK_LAUNCH();
+  }
+  return GNN_OK;
+}
+
+gnn_status check_gated(const char* who, int64_t n, int D, int F) {
+  if (n < 0 || n > (int64_t)0x7fffffff - 256) return fail(GNN_ERR_INVALID_ARG, "%s: bad row count", who);
+  if (D < 1 || F < 1) return fail(GNN_ERR_INVALID_ARG, "%s: F_in/F_mid must be >= 1", who);
+  if (D > 65536 || F > 65536) return fail(GNN_ERR_UNSUPPORTED, "%s: F_in or F_mid > 65536", who);
+  // tile counts are 32-bit
+  if ((n / BM + 1) * (int64_t)(F / (BN / 2) + 1) > 0x3fffffff || (n / BM + 1) * (int64_t)(D / 64 + 1) > 0x3fffffff)
+    return fail(GNN_ERR_UNSUPPORTED, "%s: too many tiles (n=%lld)", who, (long long)n);
+  return GNN_OK;
+}
+
+bool bad_mat(const void* p, int64_t ld, int64_t cols, int elem) {
+  return !p || ((uintptr_t)p & 15) || (ld * elem) % 16 || ld < cols || ld > ((int64_t)1 << 36);
+}
+
+}  // namespace
+
+}  // namespace gnn
+
+using namespace gnn;
+
+extern "C" gnn_status gnn_gated_workspace(int64_t n, int32_t F_in, int32_t F_mid, size_t* fwd_bytes,
+                                          size_t* bwd_bytes) {
+  gnn_status s = check_gated("gnn_gated_workspace", n, F_in, F_mid);
+  if (s != GNN_OK) return s;
+  GNN_REQUIRE(fwd_bytes || bwd_bytes, "gnn_gated_workspace: NULL result");
+  bool ok;
+  if (fwd_bytes) *fwd_bytes = 0;
+  if (bwd_bytes) *bwd_bytes = gated_ws(nullptr, 0, n, F_in, F_mid, &ok).bytes;
+  return GNN_OK;
+}
+
+extern "C" gnn_status gnn_gated_fwd(const void* X, int64_t ldx, int32_t type, int64_t n, int32_t F_in,
+                                    const void* Wg, int64_t ldwg, const void* Wu, int64_t ldwu,
+                                    int32_t F_mid, int32_t act, void* H, int64_t ldh, void* ws,
+                                    size_t ws_bytes, gnn_stream_t stream) {
+  (void)ws, (void)ws_bytes;
+  gnn_status s = check_gated("gnn_gated_fwd", n, F_in, F_mid);
+  if (s != GNN_OK) return s;
+  GNN_REQUIRE((type == GNN_BF16 || type == GNN_F16) && is_act(act), "gnn_gated_fwd: type is bf16 or fp16, act GNN_ACT_*");
+  if (n == 0) return GNN_OK;
+  GNN_REQUIRE(!bad_mat(X, ldx, F_in, 2), "gnn_gated_fwd: X needs 16-byte aligned rows and ldx >= F_in");
+  GNN_REQUIRE(!bad_mat(Wg, ldwg, F_mid, 2) && !bad_mat(Wu, ldwu, F_mid, 2),
+              "gnn_gated_fwd: Wg and Wu need 16-byte aligned rows and strides >= F_mid");
+  GNN_REQUIRE(!bad_mat(H, ldh, up(F_mid, 16), 2),
+              "gnn_gated_fwd: H needs 16-byte aligned rows and ldh >= round_up(F_mid, 16)");
+  const Mat x{const_cast<void*>(X), ldx}, g{const_cast<void*>(Wg), ldwg}, u{const_cast<void*>(Wu), ldwu}, h{H, ldh};
+  cudaStream_t st = as_stream(stream);
+  return type == GNN_BF16 ? gated_fwd<__nv_bfloat16>(n, F_in, F_mid, act, x, g, u, h, st)
+                          : gated_fwd<__half>(n, F_in, F_mid, act, x, g, u, h, st);
+}
+
+extern "C" gnn_status gnn_gated_bwd(const void* dH, int64_t lddh, int32_t dh_type, const void* X,
+                                    int64_t ldx, int32_t type, int64_t n, int32_t F_in, const void* Wg,
+                                    int64_t ldwg, const void* Wu, int64_t ldwu, int32_t F_mid,
+                                    int32_t act, void* dX, int64_t lddx, void* dWg, int64_t lddwg,
+                                    void* dWu, int64_t lddwu, void* ws, size_t ws_bytes,
+                                    gnn_stream_t stream) {
+  gnn_status s = check_gated("gnn_gated_bwd", n, F_in, F_mid);
+  if (s != GNN_OK) return s;
+  GNN_REQUIRE((type == GNN_BF16 || type == GNN_F16) && is_act(act), "gnn_gated_bwd: type is bf16 or fp16, act GNN_ACT_*");
+  GNN_REQUIRE(dh_type == type || dh_type == GNN_F32, "gnn_gated_bwd: dh_type is type or GNN_F32");
+  GNN_REQUIRE((dWg == nullptr) == (dWu == nullptr), "gnn_gated_bwd: dWg and dWu come together");
+  GNN_REQUIRE(n == 0 || (!bad_mat(X, ldx, F_in, 2) && !bad_mat(dH, lddh, F_mid, dh_type == GNN_F32 ? 4 : 2)),
+              "gnn_gated_bwd: X and dH need 16-byte aligned rows and strides >= their columns");
+  GNN_REQUIRE(n == 0 || (!bad_mat(Wg, ldwg, F_mid, 2) && !bad_mat(Wu, ldwu, F_mid, 2)),
+              "gnn_gated_bwd: Wg and Wu need 16-byte aligned rows and strides >= F_mid");
+  GNN_REQUIRE(n == 0 || !dX || !bad_mat(dX, lddx, up(F_in, 16), 2),
+              "gnn_gated_bwd: dX needs 16-byte aligned rows and lddx >= round_up(F_in, 16)");
+  GNN_REQUIRE(!dWg || (!bad_mat(dWg, lddwg, up(F_mid, 16), 2) && !bad_mat(dWu, lddwu, up(F_mid, 16), 2)),
+              "gnn_gated_bwd: dWg and dWu need 16-byte aligned rows and strides >= round_up(F_mid, 16)");
+  bool ok;
+  const GatedWs w = gated_ws(ws, ws_bytes, n, F_in, F_mid, &ok);
+  GNN_REQUIRE(ws && ok && ((uintptr_t)ws & 15) == 0, "gnn_gated_bwd: workspace too small (%zu < %zu) or misaligned",
+              ws_bytes, w.bytes);
+  const Mat dh{const_cast<void*>(dH), lddh}, x{const_cast<void*>(X), ldx}, g{const_cast<void*>(Wg), ldwg},
+      u{const_cast<void*>(Wu), ldwu}, dx{dX, lddx}, dg{dWg, lddwg}, du{dWu, lddwu};
+  cudaStream_t st = as_stream(stream);
+  const int f32 = dh_type == GNN_F32;
+  return type == GNN_BF16 ? gated_bwd<__nv_bfloat16>(n, F_in, F_mid, act, f32, dh, x, g, u, dx, dg, du, w, st)
+                          : gated_bwd<__half>(n, F_in, F_mid, act, f32, dh, x, g, u, dx, dg, du, w, st);
+}

@@ -1,6 +1,7 @@
 // Launch wrappers of the tcgen05 dense transform and its elementwise helpers.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stddef.h>
 #include <stdint.h>
@@ -34,6 +35,11 @@ gnn_status launch_cast_bf16(int64_t n, int F, const float* X, int64_t ldx, uint1
 // dZ = dH' * 1[H' > 0] in fp32 with row stride ldz (a multiple of 4).
 gnn_status launch_relu_mask_f32(int64_t n, int F, const float* dH, int64_t ldg, const float* Hout,
                                 int64_t ldh, float* dZ, int64_t ldz, cudaStream_t st);
+
+// A 128-byte-swizzled map of a row-major matrix: outer rows of `inner` elements,
+// row_bytes apart (a multiple of 16, as is base), cut into box_outer x box_inner.
+gnn_status encode_tmap_2d(CUtensorMap* map, CUtensorMapDataType type, const void* base, uint64_t inner,
+                          uint64_t outer, uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer);
 
 gnn_status launch_transpose_w(const uint16_t* W, int F_in, int F_out, int K, uint16_t* Wt,
                               cudaStream_t st);

@@ -1,0 +1,731 @@
+// Group norm with an activation, channels last, over contiguous row ranges
+// ("segments": graphs of a batch, or partitions), forward and backward.
+//
+// The rows are cut into tiles of R.  A segment of at most 2R rows is "short":
+// the block of the tile it starts in takes it whole, statistics and output in
+// one launch (the second read of its rows comes from L1/L2).  A longer segment
+// is cut at the tile borders: the first launch leaves per (piece, group)
+// partials, the second joins them in piece order, the third forms the output.
+// The piece of segment s in tile t has index t + s, which is unique because
+// both only grow along the rows; so no plan has to be built from seg_start.
+#include <cuda_runtime.h>
+
+#include "internal.h"
+#include "nodewise.cuh"
+
+namespace gnn {
+
+namespace {
+
+constexpr int THREADS = 256;
+constexpr int FIN_THREADS = 512;
+
+struct NormArgs {
+  const void* X;
+  const void* dY;
+  void* out;  // Y or dX
+  int64_t ldx, ldy, ldo;
+  int64_t n;
+  int C, groups, cg, n_seg, act;
+  int CH;  // chunks of V channels a row has, padding columns of the output included
+  int64_t R;
+  int tiles;
+  const int64_t* seg;  // may be NULL: one segment
+  const float* gamma;
+  const float* beta;
+  float eps;
+  float* mean;
+  float* rstd;
+  float2* part;  // forward: (mean, M2) of a piece's group; backward: the two sums
+  float2* joined;  // backward: the two sums over a long segment's group, / m
+  float* dpart;    // backward: [tiles][2][C] sums of dz and dz xh
+  float* dgamma;
+  float* dbeta;
+  unsigned* flags;
+};
+
+__device__ __forceinline__ int64_t seg_at(const NormArgs& a, int s) {
+  return a.seg ? a.seg[s] : (s ? a.n : 0);
+}
+// The segment that holds row r: the last one that starts at or before it.
+__device__ __forceinline__ int seg_of(const NormArgs& a, int64_t r) {
+  if (!a.seg) return 0;
+  int lo = 0, hi = a.n_seg;  // seg[lo] <= r < seg[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (a.seg[mid] <= r)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  return lo;
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// The pieces of tile t in row order: calls f(s, first row, end row, whole),
+// `whole` true for a short segment taken from its first row to its last.
+template <class Fn>
+__device__ __forceinline__ void for_pieces(const NormArgs& a, int t, Fn f) {
+  const int64_t r0 = (int64_t)t * a.R, r1 = min(a.n, r0 + a.R);
+  int s = seg_of(a, r0);
+  int64_t row = r0;
+  while (row < r1 && s < a.n_seg) {
+    const int64_t sb = seg_at(a, s), se = min(seg_at(a, s + 1), a.n);
+    if (se <= row) {  // empty (or not ascending, which the join launch flags)
+      ++s;
+      continue;
+    }
+    if (sb < 0 || sb > row) break;
+    if (se - sb <= 2 * a.R) {
+      if (sb >= r0) f(s, sb, se, true);
+    } else {
+      f(s, row, min(se, r1), false);
+    }
+    row = se;
+    ++s;
+  }
+}
+
+// A thread's place: V channels of every RP-th row.
+template <int V>
+struct Place {
+  int RP, ro, ch, c0;
+  bool on, in;  // takes part; has channels below C
+  int g[V];
+  __device__ __forceinline__ Place(const NormArgs& a) {
+    RP = THREADS / a.CH;
+    ro = threadIdx.x / a.CH;
+    ch = threadIdx.x % a.CH;
+    c0 = ch * V;
+    on = ro < RP;
+    in = on && c0 < a.C;
+#pragma unroll
+    for (int k = 0; k < V; ++k) g[k] = min(c0 + k, a.C - 1) / a.cg;
+  }
+};
+
+// One fp32 value per channel of the thread (the fill where src is NULL).
+template <int V>
+__device__ __forceinline__ void load_channels(const float* src, const Place<V>& p, int C, float fill,
+                                              float (&v)[V]) {
+#pragma unroll
+  for (int k = 0; k < V; ++k) v[k] = src && p.c0 + k < C ? src[p.c0 + k] : fill;
+}
+
+// Sums over the row places, then over each group's channels: red1/red2 hold
+// [RP][CH * V] partials; ch1/ch2 [C] get the channel sums and f(g, s1, s2) runs
+// in one lane per group with the group's sums, each channel times w[c] (NULL:
+// 1).  L lanes (a power of two) share a group, so narrow groups do not leave
+// most of a warp idle.  Ends with a barrier.
+template <class Fn>
+__device__ __forceinline__ void block_sums(const NormArgs& a, int RP, int width, const float* red1,
+                                           const float* red2, float* ch1, float* ch2, const float* w,
+                                           int L, Fn f) {
+  __syncthreads();
+  for (int c = threadIdx.x; c < a.C; c += THREADS) {
+    float s1 = 0.f, s2 = 0.f;
+    for (int r = 0; r < RP; ++r) {
+      s1 += red1[r * width + c];
+      s2 += red2[r * width + c];
+    }
+    ch1[c] = s1;
+    ch2[c] = s2;
+  }
+  __syncthreads();
+  const int per = THREADS / L, l = threadIdx.x & (L - 1);
+  for (int g0 = 0; g0 < a.groups; g0 += per) {
+    const int g = g0 + threadIdx.x / L;
+    float s1 = 0.f, s2 = 0.f;
+    if (g < a.groups) {
+      for (int j = l; j < a.cg; j += L) {
+        const int c = g * a.cg + j;
+        const float wc = w ? w[c] : 1.f;
+        s1 += wc * ch1[c];
+        s2 += wc * ch2[c];
+      }
+    }
+    for (int o = L >> 1; o; o >>= 1) {
+      s1 += __shfl_xor_sync(0xffffffffu, s1, o);
+      s2 += __shfl_xor_sync(0xffffffffu, s2, o);
+    }
+    if (g < a.groups && l == 0) f(g, s1, s2);
+  }
+  __syncthreads();
+}
+
+// Y of the rows [ra, rb) from per-group (mean, rstd), last rows first: those
+// are the ones the statistics pass read last and the caches still hold.
+template <class TX, class TY, int V>
+__device__ __forceinline__ void fwd_rows(const NormArgs& a, const Place<V>& p, int64_t ra, int64_t rb,
+                                         const float* gmean, const float* grstd) {
+  if (!p.on) return;
+  constexpr int U = 16 / V;
+  float mu[V], sc[V], bt[V];
+  load_channels<V>(a.gamma, p, a.C, 1.f, sc);
+  load_channels<V>(a.beta, p, a.C, 0.f, bt);
+#pragma unroll
+  for (int k = 0; k < V; ++k) {
+    mu[k] = gmean[p.g[k]];
+    sc[k] *= grstd[p.g[k]];
+  }
+  const TX* X = static_cast<const TX*>(a.X) + p.c0;
+  TY* Y = static_cast<TY*>(a.out) + p.c0;
+  for (int64_t r = rb - 1 - p.ro; r >= ra; r -= (int64_t)U * p.RP) {
+    float x[U][V];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (p.in && r - u * p.RP >= ra) load_vec<V>(X + (r - u * p.RP) * a.ldx, x[u]);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (r - u * p.RP < ra) break;
+      float y[V];
+#pragma unroll
+      for (int k = 0; k < V; ++k)
+        y[k] = p.c0 + k < a.C ? act_f((x[u][k] - mu[k]) * sc[k] + bt[k], a.act) : 0.f;
+      store_vec<V>(Y + (r - u * p.RP) * a.ldo, y);
+    }
+  }
+}
+
+// Statistics of every piece of a tile; short segments end here with their
+// output.  A group's sums are formed about its value in the piece's first row,
+// so a mean far from zero does not cancel in E[x^2] - mean^2.
+template <class TX, class TY, int V>
+__global__ void __launch_bounds__(THREADS, 3) norm_fwd_stats_kernel(NormArgs a, int L) {
+  extern __shared__ float sm[];
+  cudaTriggerProgrammaticLaunchCompletion();
+  const Place<V> p(a);
+  const int width = a.CH * V;
+  float* red1 = sm;
+  float* red2 = red1 + p.RP * width;
+  float* ch1 = red2 + p.RP * width;
+  float* ch2 = ch1 + a.C;
+  float* gm = ch2 + a.C;
+  float* gr = gm + a.groups;
+  const TX* X = static_cast<const TX*>(a.X);
+  const int t = blockIdx.x;
+  for_pieces(a, t, [&](int s, int64_t ra, int64_t rb, bool whole) {
+    if (p.on) {
+      constexpr int U = 16 / V;
+      float piv[V], S[V], Q[V];
+#pragma unroll
+      for (int k = 0; k < V; ++k) {
+        piv[k] = to_f32(X[ra * a.ldx + (int64_t)p.g[k] * a.cg]);
+        S[k] = 0.f;
+        Q[k] = 0.f;
+      }
+      if (p.in) {
+        for (int64_t r = ra + p.ro; r < rb; r += (int64_t)U * p.RP) {
+          float x[U][V];
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+            if (r + u * p.RP < rb) load_vec<V>(X + p.c0 + (r + u * p.RP) * a.ldx, x[u]);
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            if (r + u * p.RP >= rb) break;
+#pragma unroll
+            for (int k = 0; k < V; ++k) {
+              const float d = x[u][k] - piv[k];
+              S[k] += d;
+              Q[k] += d * d;
+            }
+          }
+        }
+      }
+      store_vec<V>(red1 + p.ro * width + p.c0, S);
+      store_vec<V>(red2 + p.ro * width + p.c0, Q);
+    }
+    const float m = (float)(rb - ra) * (float)a.cg;
+    block_sums(a, p.RP, width, red1, red2, ch1, ch2, nullptr, L, [&](int g, float S, float Q) {
+      const float d = S / m;
+      const float mean = to_f32(X[ra * a.ldx + (int64_t)g * a.cg]) + d;
+      const float m2 = fmaxf(Q - S * d, 0.f) + 0.f * Q;  // the product keeps a NaN
+      if (whole) {
+        const float rstd = rsqrtf(m2 / m + a.eps);
+        gm[g] = mean;
+        gr[g] = rstd;
+        a.mean[(int64_t)s * a.groups + g] = mean;
+        a.rstd[(int64_t)s * a.groups + g] = rstd;
+      } else {
+        a.part[((int64_t)t + s) * a.groups + g] = make_float2(mean, m2);
+      }
+    });
+    if (whole) {
+      fwd_rows<TX, TY, V>(a, p, ra, rb, gm, gr);
+      __syncthreads();  // gm, gr and the partials are written again
+    }
+  });
+}
+
+// The long segment that starts in tile t, or -1.
+__device__ __forceinline__ int long_start(const NormArgs& a, int t) {
+  if (t >= a.tiles) return -1;
+  const int64_t r0 = (int64_t)t * a.R, r1 = min(a.n, r0 + a.R);
+  const int s = seg_of(a, r1 - 1);
+  const int64_t sb = seg_at(a, s), se = min(seg_at(a, s + 1), a.n);
+  return sb >= r0 && sb < r1 && se - sb > 2 * a.R ? s : -1;
+}
+
+// Segments without rows, and what seg_start has to be.
+__device__ __forceinline__ void check_segments(const NormArgs& a, bool fill) {
+  const int64_t stride = (int64_t)gridDim.x * blockDim.x;
+  for (int64_t s = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; s < a.n_seg; s += stride) {
+    const int64_t sb = seg_at(a, (int)s), se = seg_at(a, (int)s + 1);
+    if (sb > se || (s == 0 && sb != 0) || (s == a.n_seg - 1 && se != a.n)) atomicOr(a.flags, 1u);
+    if (fill && se <= sb) {
+      for (int g = 0; g < a.groups; ++g) {
+        a.mean[s * a.groups + g] = 0.f;
+        a.rstd[s * a.groups + g] = rsqrtf(a.eps);
+      }
+    }
+  }
+}
+
+// Joins the pieces of long segments: with d_i = mean_i - mean_0 and
+// D = sum m_i d_i / M, mean = mean_0 + D, M2 = sum (M2_i + m_i d_i^2) - M D^2.
+__global__ void __launch_bounds__(FIN_THREADS) norm_fwd_join_kernel(NormArgs a) {
+  cudaTriggerProgrammaticLaunchCompletion();
+  cudaGridDependencySynchronize();
+  check_segments(a, true);
+  const int t = blockIdx.x, s = long_start(a, t);
+  if (s < 0) return;
+  const int lane = threadIdx.x & 31;
+  const int64_t sb = seg_at(a, s), se = min(seg_at(a, s + 1), a.n);
+  const int t1 = (int)((se - 1) / a.R);
+  for (int g = threadIdx.x >> 5; g < a.groups; g += FIN_THREADS / 32) {
+    const float2* part = a.part + (int64_t)s * a.groups + g;
+    const float first = part[(int64_t)t * a.groups].x;
+    float M = 0.f, S = 0.f, Q = 0.f;
+#pragma unroll 4
+    for (int i = t + lane; i <= t1; i += 32) {
+      const float2 v = part[(int64_t)i * a.groups];
+      const float m = (float)(min(se, (i + 1) * a.R) - max(sb, i * a.R)) * (float)a.cg;
+      const float d = v.x - first;
+      M += m;
+      S += m * d;
+      Q += v.y + m * d * d;
+    }
+    M = warp_sum(M), S = warp_sum(S), Q = warp_sum(Q);
+    if (lane == 0) {
+      const float D = S / M;
+      a.mean[(int64_t)s * a.groups + g] = first + D;
+      a.rstd[(int64_t)s * a.groups + g] = rsqrtf(fmaxf(Q - S * D, 0.f) / M + 0.f * Q + a.eps);
+    }
+  }
+}
+
+template <class TX, class TY, int V>
+__global__ void __launch_bounds__(THREADS, 3) norm_fwd_apply_kernel(NormArgs a) {
+  cudaGridDependencySynchronize();
+  const Place<V> p(a);
+  for_pieces(a, blockIdx.x, [&](int s, int64_t ra, int64_t rb, bool whole) {
+    if (!whole)
+      fwd_rows<TX, TY, V>(a, p, ra, rb, a.mean + (int64_t)s * a.groups, a.rstd + (int64_t)s * a.groups);
+  });
+}
+
+// ------------------------------------------------------------------ backward
+// The values a thread needs of its channels in one segment.
+template <int V>
+struct BwdChannels {
+  float mu[V], rs[V], ga[V], be[V];
+  __device__ __forceinline__ BwdChannels(const NormArgs& a, const Place<V>& p, int s) {
+    load_channels<V>(a.gamma, p, a.C, 1.f, ga);
+    load_channels<V>(a.beta, p, a.C, 0.f, be);
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      mu[k] = a.mean[(int64_t)s * a.groups + p.g[k]];
+      rs[k] = a.rstd[(int64_t)s * a.groups + p.g[k]];
+    }
+  }
+  // dz of channel k, and its xh
+  __device__ __forceinline__ float dz(int k, float x, float dy, int act, float& xh) const {
+    xh = (x - mu[k]) * rs[k];
+    float av, d;
+    act_grad_f(ga[k] * xh + be[k], act, av, d);
+    return dy * d;
+  }
+};
+
+// dX of the rows [ra, rb); gA, gB: the segment's two sums over each group, / m.
+template <class TX, class TY, int V>
+__device__ __forceinline__ void bwd_rows(const NormArgs& a, const Place<V>& p, int s, int64_t ra,
+                                         int64_t rb, const float* gA, const float* gB, int gstride) {
+  if (!p.on) return;
+  constexpr int U = 8 / V;
+  const BwdChannels<V> b(a, p, s);
+  float A[V], B[V];
+#pragma unroll
+  for (int k = 0; k < V; ++k) {
+    A[k] = gA[p.g[k] * gstride];
+    B[k] = gB[p.g[k] * gstride];
+  }
+  const TX* X = static_cast<const TX*>(a.X) + p.c0;
+  const TY* dY = static_cast<const TY*>(a.dY) + p.c0;
+  TX* dX = static_cast<TX*>(a.out) + p.c0;
+  for (int64_t r = rb - 1 - p.ro; r >= ra; r -= (int64_t)U * p.RP) {
+    float x[U][V], dy[U][V];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (p.in && r - u * p.RP >= ra) {
+        load_vec<V>(X + (r - u * p.RP) * a.ldx, x[u]);
+        load_vec<V>(dY + (r - u * p.RP) * a.ldy, dy[u]);
+      }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (r - u * p.RP < ra) break;
+      float o[V];
+#pragma unroll
+      for (int k = 0; k < V; ++k) {
+        float xh;
+        const float dz = b.dz(k, x[u][k], dy[u][k], a.act, xh);
+        o[k] = p.c0 + k < a.C ? b.rs[k] * (b.ga[k] * dz - A[k] - xh * B[k]) : 0.f;
+      }
+      store_vec<V>(dX + (r - u * p.RP) * a.ldo, o);
+    }
+  }
+}
+
+template <class TX, class TY, int V>
+__global__ void __launch_bounds__(THREADS, 2) norm_bwd_sums_kernel(NormArgs a, int L) {
+  extern __shared__ float sm[];
+  cudaTriggerProgrammaticLaunchCompletion();
+  const Place<V> p(a);
+  const int width = a.CH * V;
+  float* red1 = sm;
+  float* red2 = red1 + p.RP * width;
+  float* ch1 = red2 + p.RP * width;
+  float* ch2 = ch1 + a.C;
+  float* acc1 = ch2 + a.C;  // this tile's share of dbeta, dgamma
+  float* acc2 = acc1 + a.C;
+  float* gA = acc2 + a.C;
+  float* gB = gA + a.groups;
+  const TX* X = static_cast<const TX*>(a.X);
+  const TY* dY = static_cast<const TY*>(a.dY);
+  const int t = blockIdx.x;
+  for (int c = threadIdx.x; c < a.C; c += THREADS) acc1[c] = acc2[c] = 0.f;
+  for_pieces(a, t, [&](int s, int64_t ra, int64_t rb, bool whole) {
+    if (p.on) {
+      constexpr int U = 8 / V;
+      const BwdChannels<V> b(a, p, s);
+      float P1[V], P2[V];
+#pragma unroll
+      for (int k = 0; k < V; ++k) P1[k] = P2[k] = 0.f;
+      if (p.in) {
+        for (int64_t r = ra + p.ro; r < rb; r += (int64_t)U * p.RP) {
+          float x[U][V], dy[U][V];
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+            if (r + u * p.RP < rb) {
+              load_vec<V>(X + p.c0 + (r + u * p.RP) * a.ldx, x[u]);
+              load_vec<V>(dY + p.c0 + (r + u * p.RP) * a.ldy, dy[u]);
+            }
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            if (r + u * p.RP >= rb) break;
+#pragma unroll
+            for (int k = 0; k < V; ++k) {
+              float xh;
+              const float dz = b.dz(k, x[u][k], dy[u][k], a.act, xh);
+              P1[k] += dz;
+              P2[k] += dz * xh;
+            }
+          }
+        }
+      }
+      store_vec<V>(red1 + p.ro * width + p.c0, P1);
+      store_vec<V>(red2 + p.ro * width + p.c0, P2);
+    }
+    const float m = (float)(rb - ra) * (float)a.cg;
+    block_sums(a, p.RP, width, red1, red2, ch1, ch2, a.gamma, L, [&](int g, float A, float B) {
+      if (whole) {
+        gA[g] = A / m;
+        gB[g] = B / m;
+      } else {
+        a.part[((int64_t)t + s) * a.groups + g] = make_float2(A, B);
+      }
+    });
+    for (int c = threadIdx.x; c < a.C; c += THREADS) {
+      acc1[c] += ch1[c];
+      acc2[c] += ch2[c];
+    }
+    if (whole) bwd_rows<TX, TY, V>(a, p, s, ra, rb, gA, gB, 1);
+    __syncthreads();
+  });
+  if (a.dpart) {
+    float* d = a.dpart + (int64_t)t * 2 * a.C;
+    for (int c = threadIdx.x; c < a.C; c += THREADS) {
+      d[c] = acc1[c];
+      d[a.C + c] = acc2[c];
+    }
+  }
+}
+
+// The first max(tiles, 1) blocks join long segments; the others add the tiles'
+// shares of dbeta and dgamma, 32 columns each, in tile order.
+__global__ void __launch_bounds__(FIN_THREADS) norm_bwd_join_kernel(NormArgs a) {
+  cudaTriggerProgrammaticLaunchCompletion();
+  cudaGridDependencySynchronize();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  constexpr int NW = FIN_THREADS / 32;
+  const int joiners = max(a.tiles, 1);
+  if ((int)blockIdx.x >= joiners) {
+    __shared__ float red[NW][32];
+    const int col = ((int)blockIdx.x - joiners) * 32 + lane;
+    float sum = 0.f;
+    if (col < 2 * a.C) {
+#pragma unroll 8
+      for (int i = warp; i < a.tiles; i += NW) sum += a.dpart[(int64_t)i * 2 * a.C + col];
+    }
+    red[warp][lane] = sum;
+    __syncthreads();
+    if (warp == 0 && col < 2 * a.C) {
+      float v = 0.f;
+      for (int w = 0; w < NW; ++w) v += red[w][lane];
+      if (col < a.C) {
+        if (a.dbeta) a.dbeta[col] = v;
+      } else if (a.dgamma) {
+        a.dgamma[col - a.C] = v;
+      }
+    }
+    return;
+  }
+  check_segments(a, false);
+  const int t = blockIdx.x, s = long_start(a, t);
+  if (s < 0) return;
+  const int64_t sb = seg_at(a, s), se = min(seg_at(a, s + 1), a.n);
+  const int t1 = (int)((se - 1) / a.R);
+  const float m = (float)(se - sb) * (float)a.cg;
+  for (int g = warp; g < a.groups; g += NW) {
+    const float2* part = a.part + (int64_t)s * a.groups + g;
+    float A = 0.f, B = 0.f;
+#pragma unroll 4
+    for (int i = t + lane; i <= t1; i += 32) {
+      const float2 v = part[(int64_t)i * a.groups];
+      A += v.x;
+      B += v.y;
+    }
+    A = warp_sum(A), B = warp_sum(B);
+    if (lane == 0) a.joined[(int64_t)s * a.groups + g] = make_float2(A / m, B / m);
+  }
+}
+
+template <class TX, class TY, int V>
+__global__ void __launch_bounds__(THREADS, 2) norm_bwd_apply_kernel(NormArgs a) {
+  cudaGridDependencySynchronize();
+  const Place<V> p(a);
+  for_pieces(a, blockIdx.x, [&](int s, int64_t ra, int64_t rb, bool whole) {
+    if (!whole) {
+      const float* j = &a.joined[(int64_t)s * a.groups].x;
+      bwd_rows<TX, TY, V>(a, p, s, ra, rb, j, j + 1, 2);
+    }
+  });
+}
+
+// ---------------------------------------------------------------- host side
+// About eight tiles per SM, so that the whole grid is resident in two or three
+// turns and a long segment has few pieces to join; at least 16 rows each.
+constexpr int64_t kTiles = 152 * 8, kTileRows = 16;
+
+int64_t tile_rows(int64_t n, int RP) {
+  const int64_t r = (n + kTiles - 1) / kTiles, least = RP > kTileRows ? RP : kTileRows;
+  return r > least ? r : least;
+}
+int64_t most_tiles(int64_t n) {
+  const int64_t R = tile_rows(n, 1);
+  return (n + R - 1) / R;
+}
+
+struct NormWs {
+  float2* part;
+  float2* joined;
+  float* dpart;
+  size_t bytes;
+};
+NormWs norm_ws(void* base, size_t cap, int64_t n, int C, int groups, int n_seg, bool* ok) {
+  Arena ar(base, cap);
+  NormWs w{};
+  w.part = ar.take<float2>((size_t)(most_tiles(n) + n_seg) * groups);
+  w.joined = ar.take<float2>((size_t)n_seg * groups);
+  w.dpart = ar.take<float>((size_t)most_tiles(n) * 2 * C);
+  w.bytes = ar.used;
+  *ok = ar.ok();
+  return w;
+}
+
+gnn_status check_norm(const char* who, int64_t n, int C, int groups, int n_seg) {
+  if (n < 0 || n > (int64_t)0x7fffffff) return fail(GNN_ERR_INVALID_ARG, "%s: bad row count", who);
+  if (C < 1 || groups < 1 || C % groups || n_seg < 1)
+    return fail(GNN_ERR_INVALID_ARG, "%s: needs groups >= 1 that divide C >= 1, and n_seg >= 1", who);
+  if (C > kMaxF) return fail(GNN_ERR_UNSUPPORTED, "%s: C=%d > %d", who, C, kMaxF);
+  return GNN_OK;
+}
+
+// One matrix operand: type size, row stride, alignment.
+bool bad_rows(const void* p, int64_t ld, int type, int C, bool output) {
+  const int64_t unit = type == GNN_F32 ? 4 : 8, pad = type == GNN_F32 ? 4 : output ? 16 : 8;
+  return !p || ((uintptr_t)p & 15) || ld % unit || ld < (C + pad - 1) / pad * pad;
+}
+
+struct Launch {
+  cudaStream_t st;
+  template <class... P, class... A>
+  gnn_status run(bool after, int64_t grid, int block, size_t smem, void (*k)(P...), A... args) const {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = after ? 1 : 0;  // may start while the launch before it ends
+    count_launch();
+    GNN_CUDA(cudaLaunchKernelEx(&cfg, k, args...));
+    return GNN_OK;
+  }
+};
+
+int lanes_for(int cg) {
+  int l = 1;
+  while (l < cg && l < 32) l <<= 1;
+  return l;
+}
+
+template <class TX, class TY, int V>
+gnn_status norm_fwd(NormArgs a, cudaStream_t st) {
+  const int pad = sizeof(TY) == 4 ? 4 : 16;
+  a.CH = (a.C + pad - 1) / pad * pad / V;
+  const int RP = THREADS / a.CH;
+  a.R = tile_rows(a.n, RP);
+  a.tiles = (int)((a.n + a.R - 1) / a.R);
+  const size_t smem = sizeof(float) * (size_t)(2 * RP * a.CH * V + 2 * a.C + 2 * a.groups);
+  const Launch l{st};
+  gnn_status s = GNN_OK;
+  if (a.tiles) s = l.run(false, a.tiles, THREADS, smem, norm_fwd_stats_kernel<TX, TY, V>, a, lanes_for(a.cg));
+  if (s == GNN_OK) s = l.run(a.tiles > 0, a.tiles ? a.tiles : 1, FIN_THREADS, 0, norm_fwd_join_kernel, a);
+  if (s == GNN_OK && a.tiles) s = l.run(true, a.tiles, THREADS, 0, norm_fwd_apply_kernel<TX, TY, V>, a);
+  return s;
+}
+
+template <class TX, class TY, int V>
+gnn_status norm_bwd(NormArgs a, cudaStream_t st) {
+  const int pad = sizeof(TX) == 4 ? 4 : 16;
+  a.CH = (a.C + pad - 1) / pad * pad / V;
+  const int RP = THREADS / a.CH;
+  a.R = tile_rows(a.n, RP);
+  a.tiles = (int)((a.n + a.R - 1) / a.R);
+  const size_t smem = sizeof(float) * (size_t)(2 * RP * a.CH * V + 4 * a.C + 2 * a.groups);
+  const Launch l{st};
+  gnn_status s = GNN_OK;
+  if (a.tiles) s = l.run(false, a.tiles, THREADS, smem, norm_bwd_sums_kernel<TX, TY, V>, a, lanes_for(a.cg));
+  const int cols = a.dpart ? (2 * a.C + 31) / 32 : 0;
+  if (s == GNN_OK)
+    s = l.run(a.tiles > 0, (a.tiles ? a.tiles : 1) + cols, FIN_THREADS, 0, norm_bwd_join_kernel, a);
+  if (s == GNN_OK && a.tiles) s = l.run(true, a.tiles, THREADS, 0, norm_bwd_apply_kernel<TX, TY, V>, a);
+  return s;
+}
+
+}  // namespace
+
+}  // namespace gnn
+
+using namespace gnn;
+
+extern "C" gnn_status gnn_group_norm_workspace(int64_t n, int32_t C, int32_t groups, int32_t n_seg,
+                                               size_t* ws_bytes) {
+  gnn_status s = check_norm("gnn_group_norm_workspace", n, C, groups, n_seg);
+  if (s != GNN_OK) return s;
+  GNN_REQUIRE(ws_bytes, "gnn_group_norm_workspace: NULL ws_bytes");
+  bool ok;
+  *ws_bytes = norm_ws(nullptr, 0, n, C, groups, n_seg, &ok).bytes;
+  return GNN_OK;
+}
+
+static gnn_status check_norm_args(const char* who, int x_type, int y_type, int act, const int64_t* seg,
+                                  int n_seg, const float* gamma, const float* beta) {
+  if (!is_type(x_type) || !is_type(y_type) || !is_act(act))
+    return fail(GNN_ERR_INVALID_ARG, "%s: unknown type or activation", who);
+  if (x_type != GNN_F32 && x_type != y_type)
+    return fail(GNN_ERR_UNSUPPORTED, "%s: a 2-byte x_type needs the same y_type", who);
+  if (!seg && n_seg != 1) return fail(GNN_ERR_INVALID_ARG, "%s: seg_start NULL needs n_seg = 1", who);
+  if (((uintptr_t)seg & 7) || ((uintptr_t)gamma & 3) || ((uintptr_t)beta & 3))
+    return fail(GNN_ERR_INVALID_ARG, "%s: misaligned seg_start, gamma or beta", who);
+  return GNN_OK;
+}
+
+extern "C" gnn_status gnn_group_norm_fwd(const void* X, int64_t ldx, int32_t x_type, int64_t n,
+                                         int32_t C, int32_t groups, const int64_t* seg_start,
+                                         int32_t n_seg, const float* gamma, const float* beta,
+                                         double eps, int32_t act, void* Y, int64_t ldy,
+                                         int32_t y_type, float* mean, float* rstd, void* ws,
+                                         size_t ws_bytes, gnn_stream_t stream) {
+  const char* who = "gnn_group_norm_fwd";
+  gnn_status s = check_norm(who, n, C, groups, n_seg);
+  if (s != GNN_OK) return s;
+  if ((s = check_norm_args(who, x_type, y_type, act, seg_start, n_seg, gamma, beta)) != GNN_OK) return s;
+  GNN_REQUIRE(eps > 0 && eps < 1e30, "gnn_group_norm_fwd: eps must be positive");
+  GNN_REQUIRE(mean && rstd, "gnn_group_norm_fwd: NULL mean or rstd");
+  GNN_REQUIRE(n == 0 || !bad_rows(X, ldx, x_type, C, false), "gnn_group_norm_fwd: X needs 16-byte aligned rows "
+              "and ldx >= C");
+  GNN_REQUIRE(n == 0 || !bad_rows(Y, ldy, y_type, C, true), "gnn_group_norm_fwd: Y needs 16-byte aligned rows and "
+              "ldy >= C rounded up to 4 (fp32) or 16");
+  bool ok;
+  const NormWs w = norm_ws(ws, ws_bytes, n, C, groups, n_seg, &ok);
+  GNN_REQUIRE(ws && ok, "gnn_group_norm_fwd: workspace too small (%zu < %zu)", ws_bytes, w.bytes);
+  NormArgs a{};
+  a.X = X, a.ldx = ldx, a.out = Y, a.ldo = ldy, a.n = n, a.C = C, a.groups = groups, a.cg = C / groups;
+  a.n_seg = n_seg, a.act = act, a.seg = seg_start, a.gamma = gamma, a.beta = beta, a.eps = (float)eps;
+  a.mean = mean, a.rstd = rstd, a.part = w.part;
+  a.flags = device_flags();
+  if (!a.flags) return fail(GNN_ERR_CUDA, "device flag word unavailable");
+  cudaStream_t st = as_stream(stream);
+  if (x_type == GNN_BF16) return norm_fwd<__nv_bfloat16, __nv_bfloat16, 8>(a, st);
+  if (x_type == GNN_F16) return norm_fwd<__half, __half, 8>(a, st);
+  if (y_type == GNN_BF16) return norm_fwd<float, __nv_bfloat16, 4>(a, st);
+  if (y_type == GNN_F16) return norm_fwd<float, __half, 4>(a, st);
+  return norm_fwd<float, float, 4>(a, st);
+}
+
+extern "C" gnn_status gnn_group_norm_bwd(const void* dY, int64_t ldy, int32_t y_type, const void* X,
+                                         int64_t ldx, int32_t x_type, int64_t n, int32_t C,
+                                         int32_t groups, const int64_t* seg_start, int32_t n_seg,
+                                         const float* gamma, const float* beta, int32_t act,
+                                         const float* mean, const float* rstd, void* dX, int64_t lddx,
+                                         float* dgamma, float* dbeta, void* ws, size_t ws_bytes,
+                                         gnn_stream_t stream) {
+  const char* who = "gnn_group_norm_bwd";
+  gnn_status s = check_norm(who, n, C, groups, n_seg);
+  if (s != GNN_OK) return s;
+  if ((s = check_norm_args(who, x_type, y_type, act, seg_start, n_seg, gamma, beta)) != GNN_OK) return s;
+  GNN_REQUIRE(mean && rstd, "gnn_group_norm_bwd: NULL mean or rstd");
+  GNN_REQUIRE(n == 0 || !bad_rows(X, ldx, x_type, C, false), "gnn_group_norm_bwd: X needs 16-byte aligned rows "
+              "and ldx >= C");
+  GNN_REQUIRE(n == 0 || !bad_rows(dY, ldy, y_type, C, false), "gnn_group_norm_bwd: dY needs 16-byte aligned rows "
+              "and ldy >= C");
+  GNN_REQUIRE(n == 0 || !bad_rows(dX, lddx, x_type, C, true), "gnn_group_norm_bwd: dX needs 16-byte aligned rows "
+              "and lddx >= C rounded up to 4 (fp32) or 16");
+  bool ok;
+  const NormWs w = norm_ws(ws, ws_bytes, n, C, groups, n_seg, &ok);
+  GNN_REQUIRE(ws && ok, "gnn_group_norm_bwd: workspace too small (%zu < %zu)", ws_bytes, w.bytes);
+  NormArgs a{};
+  a.X = X, a.ldx = ldx, a.dY = dY, a.ldy = ldy, a.out = dX, a.ldo = lddx, a.n = n, a.C = C, a.groups = groups;
+  a.cg = C / groups, a.n_seg = n_seg, a.act = act, a.seg = seg_start, a.gamma = gamma, a.beta = beta;
+  a.mean = const_cast<float*>(mean), a.rstd = const_cast<float*>(rstd);
+  a.part = w.part, a.joined = w.joined, a.dpart = dgamma || dbeta ? w.dpart : nullptr;
+  a.dgamma = dgamma, a.dbeta = dbeta;
+  a.flags = device_flags();
+  if (!a.flags) return fail(GNN_ERR_CUDA, "device flag word unavailable");
+  cudaStream_t st = as_stream(stream);
+  if (x_type == GNN_BF16) return norm_bwd<__nv_bfloat16, __nv_bfloat16, 8>(a, st);
+  if (x_type == GNN_F16) return norm_bwd<__half, __half, 8>(a, st);
+  if (y_type == GNN_BF16) return norm_bwd<float, __nv_bfloat16, 4>(a, st);
+  if (y_type == GNN_F16) return norm_bwd<float, __half, 4>(a, st);
+  return norm_bwd<float, float, 4>(a, st);
+}
