@@ -708,8 +708,9 @@ gnn_status gnn_gated_bwd(const void* dH, int64_t lddh, int32_t dh_type, const vo
  *           - lr/(1 - beta1^t) (m / (sqrt(v) / sqrt(1 - beta2^t) + eps)).
  * state_bits 32: m, v fp32 [n].  state_bits 8: m, v hold e4m3 codes [n] and
  * m_scale, v_scale one fp32 per 256 elements [ceil(n/256)]: m = code m_scale,
- * sqrt(v) = code v_scale, scale = largest magnitude of the block / 448 (zero,
- * with zero codes, when that is below the smallest normal fp32), codes rounded
+ * sqrt(v) = code v_scale, scale = largest magnitude of the block times the
+ * fp32 value of 1/448 (zero, with zero codes, when that is below the smallest
+ * normal fp32), codes rounded
  * to nearest even from value (1/scale), except that a positive sqrt(v) never
  * becomes zero (its smallest code is 2^-9), which would leave eps alone in the
  * division.  The parameter update uses m and v before they are rounded to

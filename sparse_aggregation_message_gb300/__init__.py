@@ -157,11 +157,11 @@ def _workspace(nbytes: int, device):
 def _workspace_on(nbytes: int, device, stream):
     """Scratch for a call on `stream`: allocated there, so that the allocator
     hands it out again only behind the call's work."""
-    torch = _torch()
+    import torch
     if stream is None:
-        return _workspace(nbytes, device)
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
     with torch.cuda.stream(stream):
-        return _workspace(nbytes, device)
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
 
 
 def gnn_csr_build(n: int, src, dst, flags: int = CSR_GCN, stream=None) -> Csr:
@@ -740,29 +740,42 @@ def gnn_gat_layer_bwd(csr: Csr, bnd: Optional[Boundary], tpos, spos, dH_out, H_o
 ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "sigmoid": 4}
 
 
+_TYPES = {}  # torch dtype -> GNN_F32, GNN_BF16, GNN_F16
+
+
 def _type(t) -> int:
-    """GNN_F32, GNN_BF16 or GNN_F16 (-1, which the library refuses, for any other)."""
-    import torch
-    return {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}.get(t.dtype, -1)
+    """The library's number of a tensor's type (-1, which it refuses, for one it does not have)."""
+    if not _TYPES:
+        import torch
+        _TYPES.update({torch.float32: 0, torch.bfloat16: 1, torch.float16: 2})
+    return _TYPES.get(t.dtype, -1)
 
 
 def _rows(t, n: int, F: int, what: str) -> int:
     """Row stride of a matrix that holds n rows of F columns, each contiguous."""
-    if t.dim() != 2 or t.shape[0] < n or t.shape[1] < F or (t.shape[1] > 1 and t.stride(1) != 1):
+    shape = t.shape
+    if len(shape) != 2 or shape[0] < n or shape[1] < F or (shape[1] > 1 and t.stride(1) != 1):
         raise ValueError(f"{what}: needs a [>={n}, >={F}] matrix with contiguous rows, got "
-                         f"{tuple(t.shape)} with strides {t.stride()}")
-    if t.device.type != "cuda":
+                         f"{tuple(shape)} with strides {t.stride()}")
+    if not t.is_cuda:
         raise ValueError(f"{what}: needs a CUDA tensor")
-    return max(t.stride(0), F) if t.shape[0] <= 1 and t.stride(0) < F else t.stride(0)
+    return t.stride(0)
 
 
 def _f32(t, count: int, what: str):
-    import torch
     if t is None:
         return None
-    if t.dtype != torch.float32 or t.numel() < count or not t.is_contiguous() or t.device.type != "cuda":
+    if _type(t) != 0 or t.numel() < count or not t.is_contiguous() or not t.is_cuda:
         raise ValueError(f"{what}: needs a contiguous fp32 CUDA tensor of {count} elements")
     return t.data_ptr()
+
+
+def _current(t, stream) -> int:
+    """The raw stream of a call on t: `stream`, or t's device's current one."""
+    if stream is not None:
+        return stream.cuda_stream
+    import torch
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
 def _act(act: str) -> int:
@@ -799,7 +812,7 @@ def gnn_group_norm_fwd(X, n: int, C: int, groups: int, Y, mean, rstd, seg_start=
     call("gnn_group_norm_fwd", _ptr(X), ldx, _type(X), n, C, groups, seg, n_seg, _f32(gamma, C, "gamma"),
          _f32(beta, C, "beta"), float(eps), _act(act), _ptr(Y), ldy, _type(Y),
          _f32(mean, n_seg * groups, "mean"), _f32(rstd, n_seg * groups, "rstd"), _ptr(ws), ws.numel(),
-         _stream(stream))
+         _current(X, stream))
 
 
 def gnn_group_norm_bwd(dY, X, n: int, C: int, groups: int, mean, rstd, dX, dgamma=None, dbeta=None,
@@ -816,7 +829,7 @@ def gnn_group_norm_bwd(dY, X, n: int, C: int, groups: int, mean, rstd, dX, dgamm
     call("gnn_group_norm_bwd", _ptr(dY), ldy, _type(dY), _ptr(X), ldx, _type(X), n, C, groups, seg, n_seg,
          _f32(gamma, C, "gamma"), _f32(beta, C, "beta"), _act(act), _f32(mean, n_seg * groups, "mean"),
          _f32(rstd, n_seg * groups, "rstd"), _ptr(dX), lddx, _f32(dgamma, C, "dgamma"),
-         _f32(dbeta, C, "dbeta"), _ptr(ws), ws.numel(), _stream(stream))
+         _f32(dbeta, C, "dbeta"), _ptr(ws), ws.numel(), _current(X, stream))
 
 
 def gnn_gated_workspace(n: int, F_in: int, F_mid: int):
@@ -836,14 +849,11 @@ def _one_type(X, **others) -> int:
 def gnn_gated_fwd(X, n: int, F_in: int, Wg, Wu, F_mid: int, H, act: str = "silu", ws=None,
                   stream=None) -> None:
     """H = act(X Wg) * (X Wu) on tcgen05 (X, Wg, Wu, H of one type, bf16 or
-    fp16; Wg, Wu [F_in, F_mid])."""
+    fp16; Wg, Wu [F_in, F_mid]).  It needs no workspace."""
     t = _one_type(X, Wg=Wg, Wu=Wu, H=H)
-    need = gnn_gated_workspace(n, F_in, F_mid)[0]
-    if ws is None and need:
-        ws = _workspace_on(need, X.device, stream)
     call("gnn_gated_fwd", _ptr(X), _rows(X, n, F_in, "X"), t, n, F_in, _ptr(Wg), _rows(Wg, F_in, F_mid, "Wg"),
          _ptr(Wu), _rows(Wu, F_in, F_mid, "Wu"), F_mid, _act(act), _ptr(H), _rows(H, n, F_mid, "H"),
-         _ptr(ws), ws.numel() if ws is not None else 0, _stream(stream))
+         _ptr(ws), ws.numel() if ws is not None else 0, _current(X, stream))
 
 
 def gnn_gated_bwd(dH, X, n: int, F_in: int, Wg, Wu, F_mid: int, dX=None, dWg=None, dWu=None,
@@ -858,7 +868,7 @@ def gnn_gated_bwd(dH, X, n: int, F_in: int, Wg, Wu, F_mid: int, dX=None, dWg=Non
          _ptr(dX), _rows(dX, n, F_in, "dX") if dX is not None else 0,
          _ptr(dWg), _rows(dWg, F_in, F_mid, "dWg") if dWg is not None else 0,
          _ptr(dWu), _rows(dWu, F_in, F_mid, "dWu") if dWu is not None else 0,
-         _ptr(ws), ws.numel(), _stream(stream))
+         _ptr(ws), ws.numel(), _current(X, stream))
 
 
 class AdamwTensors:
@@ -925,7 +935,7 @@ def gnn_adamw_step(tensors: AdamwTensors, state, lr: float, beta1: float = 0.9, 
         ws = _workspace_on(gnn_adamw_workspace(), state.device, stream)
     call("gnn_adamw_step", tensors.c, tensors.count, tensors.param_type, tensors.grad_type, tensors.state_bits,
          _ptr(state), float(lr), float(beta1), float(beta2), float(eps), float(weight_decay), float(grad_scale),
-         float(max_norm), _f32(grad_norm, 1, "grad_norm"), _ptr(ws), ws.numel(), _stream(stream))
+         float(max_norm), _f32(grad_norm, 1, "grad_norm"), _ptr(ws), ws.numel(), _current(state, stream))
 
 
 # ---------------------------------------------------------------- epoch control (host only)

@@ -218,7 +218,7 @@ class GnnError(RuntimeError):
 
 
 def call(name, *args):
-    lib = load()
+    lib = _LIB or load()
     st = getattr(lib, name)(*args)
     if st != 0:
         raise GnnError(name, st, lib.gnn_last_error().decode(errors="replace"))

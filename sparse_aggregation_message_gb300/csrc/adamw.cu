@@ -12,6 +12,7 @@
 
 #include <cmath>
 
+#include "device.cuh"
 #include "internal.h"
 #include "nodewise.cuh"
 
@@ -24,7 +25,7 @@ constexpr int CHUNK = 4 * BLOCK;  // elements a warp takes at a time
 constexpr int THREADS = 256;
 constexpr int MAX_TENSORS = 56;  // of one launch: the descriptors stay below 4 KB
 constexpr int NORM_BLOCKS = 152 * 4;
-constexpr float F8_MAX = 448.f;
+constexpr float F8_INV = 1.f / 448.f;  // 448: the largest e4m3 value
 
 struct Table {
   int count;
@@ -35,6 +36,7 @@ struct Table {
 
 struct Hyper {
   float b1, c1, b2, c2, decay, eps;
+  bool paired;  // eps <= 2^60: denominators stay in the paired quotient's range
 };
 
 // The scalars of a step, formed by begin_kernel.
@@ -58,98 +60,251 @@ __device__ __forceinline__ int tensor_of(const Table& tab, int64_t c) {
   return lo;
 }
 
-// Eight elements of a 256-element step: consecutive ones where the tensor is
-// aligned and the step is full, else every 32nd, one by one (elements past the
-// end read as zero and are not written).
-struct Lane {
-  int64_t at;  // element of j = 0
-  int stride;  // to the next j
-  int live;    // how many of the eight exist
-  bool vec;
-  __device__ __forceinline__ Lane(int64_t base, int64_t n, bool aligned) {
-    const int lane = threadIdx.x & 31;
-    vec = aligned && base + BLOCK <= n;
-    at = base + (vec ? lane * 8 : lane);
-    stride = vec ? 1 : 32;
-    live = vec ? 8 : at < n ? (int)min((int64_t)8, (n - at + 31) / 32) : 0;
+// The eight elements of a lane in a 256-element step, as they lie in memory
+// (two words a byte of the type).  VEC: consecutive ones, in 16-byte accesses
+// where they fit; else every 32nd, one by one, of which `live` exist (the others
+// read as zero and are not written).  `p` points at the first.
+template <class T, bool VEC>
+struct Raw {
+  static constexpr int W = 2 * sizeof(T);
+  uint32_t w[W];
+  __device__ __forceinline__ void load(const T* p, int live) {
+    if constexpr (VEC) {
+      if constexpr (W == 2) {
+        const uint2 a = *reinterpret_cast<const uint2*>(p);
+        w[0] = a.x, w[1] = a.y;
+      } else {
+#pragma unroll
+        for (int i = 0; i < W; i += 4) {
+          const uint4 a = reinterpret_cast<const uint4*>(p)[i / 4];
+          w[i] = a.x, w[i + 1] = a.y, w[i + 2] = a.z, w[i + 3] = a.w;
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < W; ++i) w[i] = 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (j < live) {
+          if constexpr (sizeof(T) == 4)
+            w[j] = reinterpret_cast<const uint32_t*>(p)[j * 32];
+          else if constexpr (sizeof(T) == 2)
+            w[j >> 1] |= (uint32_t)reinterpret_cast<const uint16_t*>(p)[j * 32] << (16 * (j & 1));
+          else
+            w[j >> 2] |= (uint32_t)reinterpret_cast<const uint8_t*>(p)[j * 32] << (8 * (j & 3));
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ void to(float (&v)[8]) const {
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) {
+      if constexpr (sizeof(T) == 4) {
+        v[j] = __uint_as_float(w[j]), v[j + 1] = __uint_as_float(w[j + 1]);
+      } else if constexpr (sizeof(T) == 2) {
+        const float2 f = Pack2<T>::from(w[j >> 1]);
+        v[j] = f.x, v[j + 1] = f.y;
+      } else {  // e4m3 codes
+        const __half2_raw h =
+            __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[j >> 2] >> (8 * (j & 3))), __NV_E4M3);
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+        v[j] = f.x, v[j + 1] = f.y;
+      }
+    }
   }
 };
 
-template <class T>
-__device__ __forceinline__ void load8(const T* p, const Lane& l, float (&v)[8]) {
-  if (l.vec) {
-    load_vec<8>(p + l.at, v);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = j < l.live ? to_f32(p[l.at + j * 32]) : 0.f;
-  }
-}
-template <class T>
-__device__ __forceinline__ void store8(T* p, const Lane& l, const float (&v)[8]) {
-  if (l.vec) {
-    store_vec<8>(p + l.at, v);
+template <bool VEC, class T>
+__device__ __forceinline__ void store8(T* p, int live, const float (&v)[8]) {
+  if constexpr (VEC) {
+    store_vec<8>(p, v);
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      if (j < l.live) p[l.at + j * 32] = from_f32<T>(v[j]);
+      if (j < live) p[j * 32] = from_f32<T>(v[j]);
   }
 }
-// e4m3 codes
-__device__ __forceinline__ void load8(const uint8_t* p, const Lane& l, float (&v)[8]) {
-  uint32_t w[2] = {0, 0};
-  if (l.vec) {
-    const uint2 a = *reinterpret_cast<const uint2*>(p + l.at);
-    w[0] = a.x, w[1] = a.y;
+template <bool VEC>
+__device__ __forceinline__ void store8(uint8_t* p, int live, const uint32_t (&w)[2]) {
+  if constexpr (VEC) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      if (j < l.live) w[j >> 2] |= (uint32_t)p[l.at + j * 32] << (8 * (j & 3));
-  }
-#pragma unroll
-  for (int j = 0; j < 8; j += 2) {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[j >> 2] >> (8 * (j & 3))), __NV_E4M3);
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-    v[j] = f.x, v[j + 1] = f.y;
-  }
-}
-__device__ __forceinline__ void store8(uint8_t* p, const Lane& l, const uint32_t (&w)[2]) {
-  if (l.vec) {
-    *reinterpret_cast<uint2*>(p + l.at) = make_uint2(w[0], w[1]);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (j < l.live) p[l.at + j * 32] = (uint8_t)(w[j >> 2] >> (8 * (j & 3)));
+      if (j < live) p[j * 32] = (uint8_t)(w[j >> 2] >> (8 * (j & 3)));
   }
 }
 
-// Codes of a warp's 256 values and their scale, which lane 0 writes.  `low`:
-// values above zero keep at least the smallest code.
-template <bool LOW>
-__device__ __forceinline__ void quantise8(const float (&x)[8], const Lane& l, uint8_t* codes, float* scale_out) {
-  float top = 0.f;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const float m = fabsf(x[j]);
-    top = m > top || m != m ? m : top;
-  }
+// Codes of a warp's 256 values and their scale, which lane 0 writes; top: the
+// largest magnitude of this lane's.  LOW: values above zero keep at least the
+// smallest code; `usual`: all of them are above zero, and far from subnormal,
+// so what would round to zero is lifted just over half of that code first.
+template <bool VEC, bool LOW>
+__device__ __forceinline__ void quantise8(const float (&x)[8], float top, bool usual, int live, uint8_t* codes,
+                                          float* scale_out) {
   // magnitudes are ordered as their bit patterns are, NaN above all
   top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
-  float scale = __fdiv_rn(top, F8_MAX);
+  float scale = __fmul_rn(top, F8_INV);
   if (scale < 1.17549435e-38f) scale = 0.f;
   const float inv = scale > 0.f ? __fdiv_rn(1.f, scale) : 0.f;
   uint32_t w[2] = {0, 0};
 #pragma unroll
   for (int j = 0; j < 8; j += 2) {
-    uint32_t q = __nv_cvt_float2_to_fp8x2(make_float2(__fmul_rn(x[j], inv), __fmul_rn(x[j + 1], inv)),
-                                          __NV_SATFINITE, __NV_E4M3);
-    if (LOW && scale > 0.f) {
+    float2 y = mul2_rn(make_float2(x[j], x[j + 1]), dup2(inv));
+    if (LOW && usual) y = make_float2(fmaxf(y.x, 0x1.000002p-10f), fmaxf(y.y, 0x1.000002p-10f));
+    uint32_t q = __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
+    if (LOW && !usual && scale > 0.f) {
       if (x[j] > 0.f && (q & 0xffu) == 0) q |= 1u;
       if (x[j + 1] > 0.f && (q & 0xff00u) == 0) q |= 0x100u;
     }
     w[j >> 2] |= q << (8 * (j & 3));
   }
-  store8(codes, l, w);
+  store8<VEC>(codes, live, w);
   if ((threadIdx.x & 31) == 0) *scale_out = scale;
+}
+
+// Smallest and largest of three; a NaN is the largest of any.
+__device__ __forceinline__ float min3(float a, float b, float c) {
+  float d;
+  asm("min.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ float min8(const float (&v)[8]) {
+  return min3(min3(min3(fabsf(v[0]), fabsf(v[1]), fabsf(v[2])), fabsf(v[3]), fabsf(v[4])),
+              min3(fabsf(v[5]), fabsf(v[6]), fabsf(v[7])), __int_as_float(0x7f800000));
+}
+__device__ __forceinline__ float max8(const float (&v)[8]) {
+  return max3_nan(max3_nan(max3_nan(fabsf(v[0]), fabsf(v[1]), fabsf(v[2])), fabsf(v[3]), fabsf(v[4])),
+                  max3_nan(fabsf(v[5]), fabsf(v[6]), fabsf(v[7])), 0.f);
+}
+
+// Square roots and quotients of pairs, rounded to nearest, for operands whose
+// every step below stays normal (the caller checks).  The root is Goldschmidt's
+// iteration from an approximate reciprocal root, with h -> 1/(2 sqrt v), and a
+// final residual correction; the quotient is Markstein's method (IBM J. Res.
+// Dev. 34(1), 1990): the reciprocal to the last bit by one Newton step, a
+// quotient made faithful by one fused residual and rounded correctly by the
+// next.  Two operations to an instruction: the update had 70 instructions an
+// element with the scalar root and quotient and issue was as scarce as
+// bandwidth in the 8-bit form.
+__device__ __forceinline__ float2 sqrt2_rn(float2 v) {
+  float2 y;
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y.x) : "f"(v.x));
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y.y) : "f"(v.y));
+  float2 g = mul2_rn(v, y), h = mul2_rn(dup2(0.5f), y);
+  const float2 e = fma2_rn(make_float2(-h.x, -h.y), g, dup2(0.5f));
+  g = fma2_rn(g, e, g);
+  h = fma2_rn(h, e, h);
+  return fma2_rn(fma2_rn(make_float2(-g.x, -g.y), g, v), h, g);
+}
+__device__ __forceinline__ float2 quot2_rn(float2 a, float2 b) {
+  float2 y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y.x) : "f"(b.x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y.y) : "f"(b.y));
+  const float2 nb = make_float2(-b.x, -b.y);
+  y = fma2_rn(fma2_rn(nb, y, dup2(1.f)), y, y);
+  float2 q = mul2_rn(a, y);
+  q = fma2_rn(fma2_rn(nb, q, a), y, q);
+  return fma2_rn(fma2_rn(nb, q, a), y, q);
+}
+
+// One tensor's arrays at a lane's first element of a step, and what the step
+// reads of them.
+template <class TP, class TG, bool Q8, bool VEC>
+struct Step {
+  using TS = typename std::conditional<Q8, uint8_t, float>::type;
+  Raw<TP, VEC> p;
+  Raw<TG, VEC> g;
+  Raw<TS, VEC> m, v;
+  float ms, vs;
+};
+template <class TP, class TG, bool Q8>
+struct At {
+  using TS = typename std::conditional<Q8, uint8_t, float>::type;
+  TP* p;
+  const TG* g;
+  TS *m, *v;
+  float *ms, *vs;
+  __nv_bfloat16* copy;
+  __device__ __forceinline__ At(const gnn_adamw_tensor& t, int64_t base, int64_t at)
+      : p(static_cast<TP*>(t.param) + at), g(static_cast<const TG*>(t.grad) + at), m(static_cast<TS*>(t.m) + at),
+        v(static_cast<TS*>(t.v) + at), ms(Q8 ? t.m_scale + base / BLOCK : nullptr),
+        vs(Q8 ? t.v_scale + base / BLOCK : nullptr),
+        copy(t.copy ? reinterpret_cast<__nv_bfloat16*>(t.copy) + at : nullptr) {}
+  // step u of a chunk
+  template <bool VEC>
+  __device__ __forceinline__ void load(Step<TP, TG, Q8, VEC>& s, int u, int live) const {
+    s.p.load(p + u * BLOCK, live);
+    s.g.load(g + u * BLOCK, live);
+    s.m.load(m + u * BLOCK, live);
+    s.v.load(v + u * BLOCK, live);
+    if (Q8) s.ms = ms[u], s.vs = vs[u];
+  }
+};
+
+template <class TP, class TG, bool Q8, bool VEC>
+__device__ __forceinline__ void update(const Step<TP, TG, Q8, VEC>& now, const At<TP, TG, Q8>& at, int u, int live,
+                                       const Hyper& h, const Control& c) {
+  float p[8], g[8], m[8], v[8];
+  now.p.to(p), now.g.to(g), now.m.to(m), now.v.to(v);
+  // A product that feeds a sum stays scalar: in paired form the two may be
+  // contracted into one fused operation.
+#pragma unroll
+  for (int j = 0; j < 8; j += 2) {
+    if (Q8) {
+      const float2 a = mul2_rn(make_float2(m[j], m[j + 1]), dup2(now.ms));
+      float2 b = mul2_rn(make_float2(v[j], v[j + 1]), dup2(now.vs));
+      b = mul2_rn(b, b);
+      m[j] = a.x, m[j + 1] = a.y, v[j] = b.x, v[j + 1] = b.y;
+    }
+    const float2 gs = mul2_rn(make_float2(g[j], g[j + 1]), dup2(c.grad));
+    const float2 gc = mul2_rn(gs, dup2(h.c2));
+    m[j] = __fadd_rn(__fmul_rn(m[j], h.b1), __fmul_rn(gs.x, h.c1));
+    m[j + 1] = __fadd_rn(__fmul_rn(m[j + 1], h.b1), __fmul_rn(gs.y, h.c1));
+    v[j] = __fadd_rn(__fmul_rn(v[j], h.b2), __fmul_rn(gc.x, gs.x));
+    v[j + 1] = __fadd_rn(__fmul_rn(v[j + 1], h.b2), __fmul_rn(gc.y, gs.y));
+  }
+  // v in [2^-80, 2^80] and |m| in [2^-50, 2^50] leave every step of the paired
+  // root and quotient normal (sqrt(v)/sqrt(1 - beta2^t) + eps lies in
+  // [2^-40, 2^68]); where a lane has zeros, NaN or what is outside, its warp
+  // takes the scalar ones
+  const float mtop = max8(m), vtop = max8(v);
+  const bool usual = __all_sync(0xffffffffu, h.paired && mtop <= 0x1p50f && vtop <= 0x1p80f &&
+                                                 min8(m) >= 0x1p-50f && min8(v) >= 0x1p-80f);
+  if (usual) {
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) {
+      const float2 s = sqrt2_rn(make_float2(v[j], v[j + 1]));
+      const float2 q = quot2_rn(make_float2(m[j], m[j + 1]), make_float2(__fadd_rn(__fmul_rn(s.x, c.fix), h.eps),
+                                                                         __fadd_rn(__fmul_rn(s.y, c.fix), h.eps)));
+      const float2 d = mul2_rn(dup2(c.step), q);
+      p[j] = __fsub_rn(__fmul_rn(p[j], h.decay), d.x);
+      p[j + 1] = __fsub_rn(__fmul_rn(p[j + 1], h.decay), d.y);
+      if (Q8) v[j] = s.x, v[j + 1] = s.y;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float s = __fsqrt_rn(v[j]);
+      const float q = __fdiv_rn(m[j], __fadd_rn(__fmul_rn(s, c.fix), h.eps));
+      p[j] = __fsub_rn(__fmul_rn(p[j], h.decay), __fmul_rn(c.step, q));
+      if (Q8) v[j] = s;
+    }
+  }
+  store8<VEC>(at.p + u * BLOCK, live, p);
+  if (at.copy) store8<VEC>(at.copy + u * BLOCK, live, p);
+  if constexpr (Q8) {
+    quantise8<VEC, false>(m, mtop, usual, live, at.m + u * BLOCK, at.ms + u);
+    quantise8<VEC, true>(v, __fsqrt_rn(vtop), usual, live, at.v + u * BLOCK, at.vs + u);
+  } else {
+    store8<VEC>(at.m + u * BLOCK, live, m);
+    store8<VEC>(at.v + u * BLOCK, live, v);
+  }
 }
 
 template <class TP, class TG, bool Q8>
@@ -158,50 +313,39 @@ __global__ void __launch_bounds__(THREADS, 3)
   cudaGridDependencySynchronize();
   const Control c = *ctl;
   if (c.skip) return;
+  const int lane = threadIdx.x & 31;
   const int64_t chunks = tab.first[tab.count];
   const int64_t warps = (int64_t)gridDim.x * (THREADS / 32);
   for (int64_t k = (int64_t)blockIdx.x * (THREADS / 32) + (threadIdx.x >> 5); k < chunks; k += warps) {
     const int i = tensor_of(tab, k);
     const gnn_adamw_tensor& t = tab.t[i];
-    const bool aligned = tab.aligned >> i & 1;
-    const int64_t b0 = (k - tab.first[i]) * CHUNK;
-    for (int64_t base = b0; base < min(b0 + CHUNK, t.n); base += BLOCK) {
-      const Lane l(base, t.n, aligned);
-      float p[8], g[8], m[8], v[8];
-      load8(static_cast<const TP*>(t.param), l, p);
-      load8(static_cast<const TG*>(t.grad), l, g);
-      if constexpr (Q8) {
-        load8(static_cast<const uint8_t*>(t.m), l, m);
-        load8(static_cast<const uint8_t*>(t.v), l, v);
-        const float ms = t.m_scale[base / BLOCK], vs = t.v_scale[base / BLOCK];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          m[j] = __fmul_rn(m[j], ms);
-          v[j] = __fmul_rn(v[j], vs);
-          v[j] = __fmul_rn(v[j], v[j]);
-        }
-      } else {
-        load8(static_cast<const float*>(t.m), l, m);
-        load8(static_cast<const float*>(t.v), l, v);
+    const int64_t base = (k - tab.first[i]) * CHUNK, left = t.n - base;
+    // whole steps of an aligned tensor, then what remains
+    const int whole = (tab.aligned >> i & 1) ? (int)min(left / BLOCK, (int64_t)(CHUNK / BLOCK)) : 0;
+    if (whole) {
+      const At<TP, TG, Q8> at(t, base, base + lane * 8);
+      // With 8-bit states the next step's loads are requested before this one's
+      // arithmetic (1054 -> 959 us at 242M elements); with fp32 states their 32
+      // registers spill and bandwidth is reached without (772 against 827 us at 184M).
+      Step<TP, TG, Q8, true> next;
+      if (Q8) at.load(next, 0, 8);
+#pragma unroll 1
+      for (int u = 0; u < whole; ++u) {
+        if (!Q8) at.load(next, u, 8);
+        const Step<TP, TG, Q8, true> now = next;
+        if (Q8 && u + 1 < whole) at.load(next, u + 1, 8);
+        update(now, at, u, 8, h, c);
       }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float gs = __fmul_rn(g[j], c.grad);
-        m[j] = __fadd_rn(__fmul_rn(m[j], h.b1), __fmul_rn(gs, h.c1));
-        v[j] = __fadd_rn(__fmul_rn(v[j], h.b2), __fmul_rn(__fmul_rn(gs, h.c2), gs));
-        const float root = __fsqrt_rn(v[j]);
-        const float den = __fadd_rn(__fmul_rn(root, c.fix), h.eps);
-        p[j] = __fsub_rn(__fmul_rn(p[j], h.decay), __fmul_rn(c.step, __fdiv_rn(m[j], den)));
-        if (Q8) v[j] = root;
-      }
-      store8(static_cast<TP*>(t.param), l, p);
-      if (t.copy) store8(reinterpret_cast<__nv_bfloat16*>(t.copy), l, p);
-      if constexpr (Q8) {
-        quantise8<false>(m, l, static_cast<uint8_t*>(t.m), t.m_scale + base / BLOCK);
-        quantise8<true>(v, l, static_cast<uint8_t*>(t.v), t.v_scale + base / BLOCK);
-      } else {
-        store8(static_cast<float*>(t.m), l, m);
-        store8(static_cast<float*>(t.v), l, v);
+    }
+    if (whole < CHUNK / BLOCK && left > whole * BLOCK) {
+      const At<TP, TG, Q8> at(t, base, base + lane);
+#pragma unroll 1
+      for (int u = whole; u < CHUNK / BLOCK && left > u * BLOCK; ++u) {
+        const int64_t mine = left - u * BLOCK - lane;  // elements from this lane's first one on
+        const int live = mine <= 0 ? 0 : (int)min((mine + 31) / 32, (int64_t)8);
+        Step<TP, TG, Q8, false> now;
+        at.load(now, u, live);
+        update(now, at, u, live, h, c);
       }
     }
   }
@@ -218,35 +362,59 @@ __device__ __forceinline__ double block_sum(double v, double* sm) {
   return s;
 }
 
-// Partial sums of g^2, one per block.  Eight squares are added in fp32 and the
-// eights in fp64 (fp64 rates are low); where eight squares leave the range
-// that fp32 holds well, they are formed again in fp64.
+// A lane's 32 squares of a chunk are added in fp32, chunks in fp64 (with eight
+// squares to an fp64 addition the fp64 pipe was 73% busy); where the 32 leave
+// the range that fp32 holds well, they are formed again in fp64.
+template <class TG, bool VEC>
+__device__ __forceinline__ double squares(const Raw<TG, VEC> (&raw)[CHUNK / BLOCK]) {
+  float s = 0.f;
+#pragma unroll
+  for (int u = 0; u < CHUNK / BLOCK; ++u) {
+    float g[8];
+    raw[u].to(g);
+    s += ((g[0] * g[0] + g[1] * g[1]) + (g[2] * g[2] + g[3] * g[3])) +
+         ((g[4] * g[4] + g[5] * g[5]) + (g[6] * g[6] + g[7] * g[7]));
+  }
+  if (s > 1e-28f && s < 1e38f) return (double)s;
+  double d = 0;
+#pragma unroll
+  for (int u = 0; u < CHUNK / BLOCK; ++u) {
+    float g[8];
+    raw[u].to(g);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) d += (double)g[j] * (double)g[j];
+  }
+  return d;
+}
+
+// Partial sums of g^2, one per block.
 template <class TG>
 __global__ void __launch_bounds__(THREADS) norm_kernel(const __grid_constant__ Table tab, double* partial,
                                                        int add) {
   __shared__ double sm[THREADS / 32];
   cudaTriggerProgrammaticLaunchCompletion();
+  const int lane = threadIdx.x & 31;
   const int64_t chunks = tab.first[tab.count];
   const int64_t warps = (int64_t)gridDim.x * (THREADS / 32);
   double sum = 0;
   for (int64_t k = (int64_t)blockIdx.x * (THREADS / 32) + (threadIdx.x >> 5); k < chunks; k += warps) {
     const int i = tensor_of(tab, k);
     const gnn_adamw_tensor& t = tab.t[i];
-    const bool aligned = tab.aligned >> i & 1;
-    const int64_t b0 = (k - tab.first[i]) * CHUNK;
-    for (int64_t base = b0; base < min(b0 + CHUNK, t.n); base += BLOCK) {
-      const Lane l(base, t.n, aligned);
-      float g[8];
-      load8(static_cast<const TG*>(t.grad), l, g);
-      float s = 0.f;
+    const int64_t base = (k - tab.first[i]) * CHUNK, left = t.n - base;
+    const TG* g = static_cast<const TG*>(t.grad) + base;
+    if ((tab.aligned >> i & 1) && left >= CHUNK) {
+      Raw<TG, true> raw[CHUNK / BLOCK];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) s += g[j] * g[j];
-      if (s > 1e-30f && s < 1e38f) {
-        sum += (double)s;
-      } else {
+      for (int u = 0; u < CHUNK / BLOCK; ++u) raw[u].load(g + u * BLOCK + lane * 8, 8);
+      sum += squares(raw);
+    } else {
+      Raw<TG, false> raw[CHUNK / BLOCK];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) sum += (double)g[j] * (double)g[j];
+      for (int u = 0; u < CHUNK / BLOCK; ++u) {
+        const int64_t mine = left - u * BLOCK - lane;
+        raw[u].load(g + u * BLOCK + lane, mine <= 0 ? 0 : (int)min((mine + 31) / 32, (int64_t)8));
       }
+      sum += squares(raw);
     }
   }
   const double total = block_sum(sum, sm);
@@ -259,32 +427,44 @@ __global__ void __launch_bounds__(THREADS)
                  double beta2, double grad_scale, double max_norm, float* grad_norm, Control* ctl) {
   // max_norm 0: there are no partials, and no norm
   __shared__ double sm[THREADS / 32];
+  __shared__ float scalars[2];
   cudaTriggerProgrammaticLaunchCompletion();
+  // what the norm has no part in, one thread each, while its launch still runs
+  // (the state is nobody's but this kernel's)
+  double power = 0;
+  if (threadIdx.x == 32) {
+    power = state->beta1_pow * beta1;
+    scalars[0] = (float)(lr / (1.0 - power));
+  } else if (threadIdx.x == 64) {
+    power = state->beta2_pow * beta2;
+    scalars[1] = (float)(1.0 / sqrt(1.0 - power));
+  }
   cudaGridDependencySynchronize();
   double sum = 0;
   for (int i = threadIdx.x; i < n_partial; i += THREADS) sum += partial[i];
   sum = block_sum(sum, sm);
-  if (threadIdx.x != 0) return;
-  Control c{(float)grad_scale, 0.f, 0.f, 0};
-  if (max_norm > 0) {
-    const double norm = fabs(grad_scale) * sqrt(sum);
-    if (grad_norm) *grad_norm = (float)norm;
-    if (!isfinite(norm)) {
-      c.skip = 1;
-      state->skipped += 1.0;
-    } else if (isfinite(max_norm)) {
-      c.grad = (float)(grad_scale * (max_norm / fmax(norm + 1e-6, max_norm)));
+  __shared__ int skip;
+  if (threadIdx.x == 0) {
+    Control c{(float)grad_scale, scalars[0], scalars[1], 0};
+    if (max_norm > 0) {
+      const double norm = fabs(grad_scale) * sqrt(sum);
+      if (grad_norm) *grad_norm = (float)norm;
+      if (!isfinite(norm))
+        c.skip = 1;
+      else if (isfinite(max_norm))
+        c.grad = (float)(grad_scale * (max_norm / fmax(norm + 1e-6, max_norm)));
     }
+    *ctl = c;
+    if (c.skip)
+      state->skipped += 1.0;
+    else
+      state->steps += 1.0;
+    skip = c.skip;
   }
-  if (!c.skip) {
-    const double p1 = state->beta1_pow * beta1, p2 = state->beta2_pow * beta2;
-    c.step = (float)(lr / (1.0 - p1));
-    c.fix = (float)(1.0 / sqrt(1.0 - p2));
-    state->steps += 1.0;
-    state->beta1_pow = p1;
-    state->beta2_pow = p2;
-  }
-  *ctl = c;
+  __syncthreads();
+  if (skip) return;
+  if (threadIdx.x == 32) state->beta1_pow = power;
+  if (threadIdx.x == 64) state->beta2_pow = power;
 }
 
 bool aligned_to(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
@@ -369,7 +549,7 @@ extern "C" gnn_status gnn_adamw_step(const gnn_adamw_tensor* tensors, int32_t n_
   Control* ctl = static_cast<Control*>(ws);
   double* partial = reinterpret_cast<double*>(static_cast<char*>(ws) + 256);
   const Hyper h{(float)beta1, (float)(1.0 - beta1), (float)beta2, (float)(1.0 - beta2),
-                (float)(1.0 - lr * weight_decay), (float)eps};
+                (float)(1.0 - lr * weight_decay), (float)eps, eps <= 0x1p60};
   auto* update = param_type == GNN_F32 ? update_kernel<float>(grad_type, q8)
                                        : update_kernel<__nv_bfloat16>(grad_type, q8);
   auto* norm = grad_type == GNN_BF16 ? norm_kernel<__nv_bfloat16>

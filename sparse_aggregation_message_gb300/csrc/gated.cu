@@ -143,18 +143,6 @@ __device__ __forceinline__ uint4* staged(uint8_t* tile, int r, int k) {
   return reinterpret_cast<uint4*>(tile + r * 128 + ((k ^ (r & 7)) << 4));
 }
 
-// Runs f with the activation as a compile-time value.
-template <class Fn>
-__device__ __forceinline__ void with_act(int act, Fn f) {
-  switch (act) {
-    case GNN_ACT_RELU: f(std::integral_constant<int, GNN_ACT_RELU>()); break;
-    case GNN_ACT_SILU: f(std::integral_constant<int, GNN_ACT_SILU>()); break;
-    case GNN_ACT_GELU: f(std::integral_constant<int, GNN_ACT_GELU>()); break;
-    case GNN_ACT_SIGMOID: f(std::integral_constant<int, GNN_ACT_SIGMOID>()); break;
-    default: f(std::integral_constant<int, GNN_ACT_NONE>());
-  }
-}
-
 template <Mode M, class T>
 __global__ void __launch_bounds__(THREADS, 1) gated_kernel(const __grid_constant__ Args g) {
   extern __shared__ uint8_t smem_raw[];

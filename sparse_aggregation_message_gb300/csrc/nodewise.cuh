@@ -7,6 +7,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "gnnagg.h"
 
 namespace gnn {
@@ -134,6 +136,18 @@ __device__ __forceinline__ void act_grad_f(float z, int act, float& a, float& d)
     default:
       a = z;
       d = 1.f;
+  }
+}
+
+// Runs f with the activation as a compile-time value.
+template <class Fn>
+__device__ __forceinline__ void with_act(int act, Fn f) {
+  switch (act) {
+    case GNN_ACT_RELU: f(std::integral_constant<int, GNN_ACT_RELU>()); break;
+    case GNN_ACT_SILU: f(std::integral_constant<int, GNN_ACT_SILU>()); break;
+    case GNN_ACT_GELU: f(std::integral_constant<int, GNN_ACT_GELU>()); break;
+    case GNN_ACT_SIGMOID: f(std::integral_constant<int, GNN_ACT_SIGMOID>()); break;
+    default: f(std::integral_constant<int, GNN_ACT_NONE>());
   }
 }
 

@@ -17,7 +17,11 @@ namespace gnn {
 
 namespace {
 
-constexpr int THREADS = 256;
+// A block holds as many rows of CH chunks side by side as fit 192 threads, at
+// least one (at most 256 threads then).  Small blocks: segments of a batch
+// are small, a block takes one at a time, and more blocks have more of them
+// in flight.
+constexpr int MAX_THREADS = 256, AIM_THREADS = 192;
 constexpr int FIN_THREADS = 512;
 
 struct NormArgs {
@@ -28,6 +32,7 @@ struct NormArgs {
   int64_t n;
   int C, groups, cg, n_seg, act;
   int CH;  // chunks of V channels a row has, padding columns of the output included
+  int RP;  // rows a block holds side by side: RP * CH threads take part
   int64_t R;
   int tiles;
   const int64_t* seg;  // may be NULL: one segment
@@ -61,6 +66,10 @@ __device__ __forceinline__ int seg_of(const NormArgs& a, int64_t r) {
   return lo;
 }
 
+__device__ __forceinline__ float* align16(float* p) {
+  return reinterpret_cast<float*>((reinterpret_cast<uintptr_t>(p) + 15) & ~uintptr_t(15));
+}
+
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -91,23 +100,87 @@ __device__ __forceinline__ void for_pieces(const NormArgs& a, int t, Fn f) {
   }
 }
 
-// A thread's place: V channels of every RP-th row.
+// A thread's place: V channels of every RP-th row of a piece.
 template <int V>
 struct Place {
-  int RP, ro, ch, c0;
+  int ro, c0;
   bool on, in;  // takes part; has channels below C
   int g[V];
   __device__ __forceinline__ Place(const NormArgs& a) {
-    RP = THREADS / a.CH;
     ro = threadIdx.x / a.CH;
-    ch = threadIdx.x % a.CH;
-    c0 = ch * V;
-    on = ro < RP;
+    c0 = (threadIdx.x % a.CH) * V;
+    on = ro < a.RP;
     in = on && c0 < a.C;
 #pragma unroll
     for (int k = 0; k < V; ++k) g[k] = min(c0 + k, a.C - 1) / a.cg;
   }
+  // how many rows of [ra, rb) are this thread's
+  __device__ __forceinline__ int rows(const NormArgs& a, int64_t ra, int64_t rb) const {
+    return on ? (int)((rb - ra - ro + a.RP - 1) / a.RP) : 0;
+  }
 };
+
+// A thread's own ring of rows in shared memory: row i + DEPTH is requested with
+// an asynchronous copy as row i is used, so DEPTH rows a thread are in flight
+// at no cost in registers.  Every thread reads only what it copied itself, so
+// there is no barrier; the slot that is filled is the one that was used up an
+// iteration earlier.
+template <int BYTES>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// One or two matrices (TB = void: one) walked row by row in steps of da, db
+// elements from pa, pb, V elements a row and thread; f(row number, a, b).
+template <int V, int DEPTH, class TA, class TB, class Fn>
+__device__ __forceinline__ void stream_rows(char* ring, int rows, const TA* pa, int64_t da, const TB* pb,
+                                            int64_t db, Fn f) {
+  constexpr int SA = V * sizeof(TA), SB = V * sizeof(TB);
+  const int stride_a = blockDim.x * SA, stride_b = blockDim.x * SB;
+  char* ra = ring + threadIdx.x * SA;
+  char* rb = ring + (DEPTH + 1) * stride_a + threadIdx.x * SB;
+  const uint32_t sa = static_cast<uint32_t>(__cvta_generic_to_shared(ra));
+  const uint32_t sb = static_cast<uint32_t>(__cvta_generic_to_shared(rb));
+  int fill = 0;
+#pragma unroll
+  for (int i = 0; i < DEPTH; ++i) {
+    if (i < rows) {
+      copy_async<SA>(sa + fill * stride_a, pa);
+      if (pb) copy_async<SB>(sb + fill * stride_b, pb);
+      pa += da;
+      if (pb) pb += db;
+    }
+    ++fill;
+    copy_commit();
+  }
+  int use = 0;
+  for (int i = 0; i < rows; ++i) {
+    copy_wait<DEPTH - 1>();
+    float a[V], b[V];
+    load_vec<V>(reinterpret_cast<const TA*>(ra + use * stride_a), a);
+    if (pb) load_vec<V>(reinterpret_cast<const TB*>(rb + use * stride_b), b);
+    if (i + DEPTH < rows) {
+      copy_async<SA>(sa + fill * stride_a, pa);
+      if (pb) copy_async<SB>(sb + fill * stride_b, pb);
+      pa += da;
+      if (pb) pb += db;
+    }
+    copy_commit();
+    fill = fill == DEPTH ? 0 : fill + 1;
+    use = use == DEPTH ? 0 : use + 1;
+    f(i, a, b);
+  }
+  copy_wait<0>();
+}
+constexpr int FWD_DEPTH = 8, BWD_DEPTH = 6;
 
 // One fp32 value per channel of the thread (the fill where src is NULL).
 template <int V>
@@ -123,13 +196,13 @@ __device__ __forceinline__ void load_channels(const float* src, const Place<V>& 
 // 1).  L lanes (a power of two) share a group, so narrow groups do not leave
 // most of a warp idle.  Ends with a barrier.
 template <class Fn>
-__device__ __forceinline__ void block_sums(const NormArgs& a, int RP, int width, const float* red1,
+__device__ __forceinline__ void block_sums(const NormArgs& a, int width, const float* red1,
                                            const float* red2, float* ch1, float* ch2, const float* w,
                                            int L, Fn f) {
   __syncthreads();
-  for (int c = threadIdx.x; c < a.C; c += THREADS) {
+  for (int c = threadIdx.x; c < a.C; c += blockDim.x) {
     float s1 = 0.f, s2 = 0.f;
-    for (int r = 0; r < RP; ++r) {
+    for (int r = 0; r < a.RP; ++r) {
       s1 += red1[r * width + c];
       s2 += red2[r * width + c];
     }
@@ -137,7 +210,7 @@ __device__ __forceinline__ void block_sums(const NormArgs& a, int RP, int width,
     ch2[c] = s2;
   }
   __syncthreads();
-  const int per = THREADS / L, l = threadIdx.x & (L - 1);
+  const int per = blockDim.x / L, l = threadIdx.x & (L - 1);
   for (int g0 = 0; g0 < a.groups; g0 += per) {
     const int g = g0 + threadIdx.x / L;
     float s1 = 0.f, s2 = 0.f;
@@ -162,9 +235,8 @@ __device__ __forceinline__ void block_sums(const NormArgs& a, int RP, int width,
 // are the ones the statistics pass read last and the caches still hold.
 template <class TX, class TY, int V>
 __device__ __forceinline__ void fwd_rows(const NormArgs& a, const Place<V>& p, int64_t ra, int64_t rb,
-                                         const float* gmean, const float* grstd) {
-  if (!p.on) return;
-  constexpr int U = 16 / V;
+                                         const float* gmean, const float* grstd, char* ring) {
+  const int rows = p.rows(a, ra, rb);
   float mu[V], sc[V], bt[V];
   load_channels<V>(a.gamma, p, a.C, 1.f, sc);
   load_channels<V>(a.beta, p, a.C, 0.f, bt);
@@ -173,45 +245,47 @@ __device__ __forceinline__ void fwd_rows(const NormArgs& a, const Place<V>& p, i
     mu[k] = gmean[p.g[k]];
     sc[k] *= grstd[p.g[k]];
   }
-  const TX* X = static_cast<const TX*>(a.X) + p.c0;
-  TY* Y = static_cast<TY*>(a.out) + p.c0;
-  for (int64_t r = rb - 1 - p.ro; r >= ra; r -= (int64_t)U * p.RP) {
-    float x[U][V];
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (p.in && r - u * p.RP >= ra) load_vec<V>(X + (r - u * p.RP) * a.ldx, x[u]);
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (r - u * p.RP < ra) break;
+  const int64_t last = ra + p.ro + (int64_t)(rows - 1) * a.RP;
+  const TX* X = static_cast<const TX*>(a.X) + last * a.ldx + p.c0;
+  TY* Y = static_cast<TY*>(a.out) + last * a.ldo + p.c0;
+  const int64_t dx = (int64_t)a.RP * a.ldx, dy = (int64_t)a.RP * a.ldo;
+  if (!p.in) {  // padding columns only
+    const float zero[V] = {};
+    for (int i = 0; i < rows; ++i, Y -= dy) store_vec<V>(Y, zero);
+    return;
+  }
+  with_act(a.act, [&](auto act) {
+    stream_rows<V, FWD_DEPTH>(ring, rows, X, -dx, (const float*)nullptr, 0, [&](int, float (&x)[V], float (&)[V]) {
       float y[V];
 #pragma unroll
-      for (int k = 0; k < V; ++k)
-        y[k] = p.c0 + k < a.C ? act_f((x[u][k] - mu[k]) * sc[k] + bt[k], a.act) : 0.f;
-      store_vec<V>(Y + (r - u * p.RP) * a.ldo, y);
-    }
-  }
+      for (int k = 0; k < V; ++k) y[k] = p.c0 + k < a.C ? act_f((x[k] - mu[k]) * sc[k] + bt[k], act) : 0.f;
+      store_vec<V>(Y, y);
+      Y -= dy;
+    });
+  });
 }
 
 // Statistics of every piece of a tile; short segments end here with their
 // output.  A group's sums are formed about its value in the piece's first row,
 // so a mean far from zero does not cancel in E[x^2] - mean^2.
 template <class TX, class TY, int V>
-__global__ void __launch_bounds__(THREADS, 3) norm_fwd_stats_kernel(NormArgs a, int L) {
+__global__ void __launch_bounds__(MAX_THREADS, 3) norm_fwd_stats_kernel(NormArgs a, int L) {
   extern __shared__ float sm[];
   cudaTriggerProgrammaticLaunchCompletion();
   const Place<V> p(a);
   const int width = a.CH * V;
   float* red1 = sm;
-  float* red2 = red1 + p.RP * width;
-  float* ch1 = red2 + p.RP * width;
+  float* red2 = red1 + a.RP * width;
+  float* ch1 = red2 + a.RP * width;
   float* ch2 = ch1 + a.C;
   float* gm = ch2 + a.C;
   float* gr = gm + a.groups;
+  char* ring = reinterpret_cast<char*>(align16(gr + a.groups));
   const TX* X = static_cast<const TX*>(a.X);
   const int t = blockIdx.x;
   for_pieces(a, t, [&](int s, int64_t ra, int64_t rb, bool whole) {
     if (p.on) {
-      constexpr int U = 16 / V;
+      constexpr int U = 32 / V;
       float piv[V], S[V], Q[V];
 #pragma unroll
       for (int k = 0; k < V; ++k) {
@@ -219,29 +293,33 @@ __global__ void __launch_bounds__(THREADS, 3) norm_fwd_stats_kernel(NormArgs a, 
         S[k] = 0.f;
         Q[k] = 0.f;
       }
-      if (p.in) {
-        for (int64_t r = ra + p.ro; r < rb; r += (int64_t)U * p.RP) {
-          float x[U][V];
+      const TX* at = X + (ra + p.ro) * a.ldx + p.c0;
+      const int64_t dx = (int64_t)a.RP * a.ldx;
+      for (int i = p.in ? p.rows(a, ra, rb) : 0; i > 0; i -= U) {
+        float x[U][V];
 #pragma unroll
-          for (int u = 0; u < U; ++u)
-            if (r + u * p.RP < rb) load_vec<V>(X + p.c0 + (r + u * p.RP) * a.ldx, x[u]);
+        for (int u = 0; u < U; ++u, at += dx) {
+          if (u < i) {
+            load_vec<V>(at, x[u]);
+          } else {
 #pragma unroll
-          for (int u = 0; u < U; ++u) {
-            if (r + u * p.RP >= rb) break;
-#pragma unroll
-            for (int k = 0; k < V; ++k) {
-              const float d = x[u][k] - piv[k];
-              S[k] += d;
-              Q[k] += d * d;
-            }
+            for (int k = 0; k < V; ++k) x[u][k] = piv[k];
           }
         }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int k = 0; k < V; ++k) {
+            const float d = x[u][k] - piv[k];
+            S[k] += d;
+            Q[k] += d * d;
+          }
       }
       store_vec<V>(red1 + p.ro * width + p.c0, S);
       store_vec<V>(red2 + p.ro * width + p.c0, Q);
     }
     const float m = (float)(rb - ra) * (float)a.cg;
-    block_sums(a, p.RP, width, red1, red2, ch1, ch2, nullptr, L, [&](int g, float S, float Q) {
+    block_sums(a, width, red1, red2, ch1, ch2, nullptr, L, [&](int g, float S, float Q) {
       const float d = S / m;
       const float mean = to_f32(X[ra * a.ldx + (int64_t)g * a.cg]) + d;
       const float m2 = fmaxf(Q - S * d, 0.f) + 0.f * Q;  // the product keeps a NaN
@@ -256,24 +334,15 @@ __global__ void __launch_bounds__(THREADS, 3) norm_fwd_stats_kernel(NormArgs a, 
       }
     });
     if (whole) {
-      fwd_rows<TX, TY, V>(a, p, ra, rb, gm, gr);
+      fwd_rows<TX, TY, V>(a, p, ra, rb, gm, gr, ring);
       __syncthreads();  // gm, gr and the partials are written again
     }
   });
 }
 
-// The long segment that starts in tile t, or -1.
-__device__ __forceinline__ int long_start(const NormArgs& a, int t) {
-  if (t >= a.tiles) return -1;
-  const int64_t r0 = (int64_t)t * a.R, r1 = min(a.n, r0 + a.R);
-  const int s = seg_of(a, r1 - 1);
-  const int64_t sb = seg_at(a, s), se = min(seg_at(a, s + 1), a.n);
-  return sb >= r0 && sb < r1 && se - sb > 2 * a.R ? s : -1;
-}
-
 // Segments without rows, and what seg_start has to be.
-__device__ __forceinline__ void check_segments(const NormArgs& a, bool fill) {
-  const int64_t stride = (int64_t)gridDim.x * blockDim.x;
+__device__ __forceinline__ void check_segments(const NormArgs& a, int blocks, bool fill) {
+  const int64_t stride = (int64_t)blocks * blockDim.x;
   for (int64_t s = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; s < a.n_seg; s += stride) {
     const int64_t sb = seg_at(a, (int)s), se = seg_at(a, (int)s + 1);
     if (sb > se || (s == 0 && sb != 0) || (s == a.n_seg - 1 && se != a.n)) atomicOr(a.flags, 1u);
@@ -286,46 +355,57 @@ __device__ __forceinline__ void check_segments(const NormArgs& a, bool fill) {
   }
 }
 
+// Calls f(s, first row, end row, first piece's tile, last one's) for the long
+// segments of this block.
+template <class Fn>
+__device__ __forceinline__ void for_long(const NormArgs& a, int blocks, Fn f) {
+  for (int s = blockIdx.x; s < a.n_seg; s += blocks) {
+    const int64_t sb = seg_at(a, s), se = min(seg_at(a, s + 1), a.n);
+    if (sb >= 0 && se - sb > 2 * a.R) f(s, sb, se, (int)(sb / a.R), (int)((se - 1) / a.R));
+  }
+}
+
 // Joins the pieces of long segments: with d_i = mean_i - mean_0 and
 // D = sum m_i d_i / M, mean = mean_0 + D, M2 = sum (M2_i + m_i d_i^2) - M D^2.
 __global__ void __launch_bounds__(FIN_THREADS) norm_fwd_join_kernel(NormArgs a) {
   cudaTriggerProgrammaticLaunchCompletion();
   cudaGridDependencySynchronize();
-  check_segments(a, true);
-  const int t = blockIdx.x, s = long_start(a, t);
-  if (s < 0) return;
+  check_segments(a, gridDim.x, true);
   const int lane = threadIdx.x & 31;
-  const int64_t sb = seg_at(a, s), se = min(seg_at(a, s + 1), a.n);
-  const int t1 = (int)((se - 1) / a.R);
-  for (int g = threadIdx.x >> 5; g < a.groups; g += FIN_THREADS / 32) {
-    const float2* part = a.part + (int64_t)s * a.groups + g;
-    const float first = part[(int64_t)t * a.groups].x;
-    float M = 0.f, S = 0.f, Q = 0.f;
+  for_long(a, gridDim.x, [&](int s, int64_t sb, int64_t se, int t0, int t1) {
+    for (int g = threadIdx.x >> 5; g < a.groups; g += FIN_THREADS / 32) {
+      const float2* part = a.part + (int64_t)s * a.groups + g;
+      const float first = part[(int64_t)t0 * a.groups].x;
+      float M = 0.f, S = 0.f, Q = 0.f;
 #pragma unroll 4
-    for (int i = t + lane; i <= t1; i += 32) {
-      const float2 v = part[(int64_t)i * a.groups];
-      const float m = (float)(min(se, (i + 1) * a.R) - max(sb, i * a.R)) * (float)a.cg;
-      const float d = v.x - first;
-      M += m;
-      S += m * d;
-      Q += v.y + m * d * d;
+      for (int i = t0 + lane; i <= t1; i += 32) {
+        const float2 v = part[(int64_t)i * a.groups];
+        const float m = (float)(min(se, (i + 1) * a.R) - max(sb, i * a.R)) * (float)a.cg;
+        const float d = v.x - first;
+        M += m;
+        S += m * d;
+        Q += v.y + m * d * d;
+      }
+      M = warp_sum(M), S = warp_sum(S), Q = warp_sum(Q);
+      if (lane == 0) {
+        const float D = S / M;
+        a.mean[(int64_t)s * a.groups + g] = first + D;
+        a.rstd[(int64_t)s * a.groups + g] = rsqrtf(fmaxf(Q - S * D, 0.f) / M + 0.f * Q + a.eps);
+      }
     }
-    M = warp_sum(M), S = warp_sum(S), Q = warp_sum(Q);
-    if (lane == 0) {
-      const float D = S / M;
-      a.mean[(int64_t)s * a.groups + g] = first + D;
-      a.rstd[(int64_t)s * a.groups + g] = rsqrtf(fmaxf(Q - S * D, 0.f) / M + 0.f * Q + a.eps);
-    }
-  }
+  });
 }
 
 template <class TX, class TY, int V>
-__global__ void __launch_bounds__(THREADS, 3) norm_fwd_apply_kernel(NormArgs a) {
+__global__ void __launch_bounds__(MAX_THREADS, 3) norm_fwd_apply_kernel(NormArgs a) {
+  extern __shared__ float sm[];
   cudaGridDependencySynchronize();
   const Place<V> p(a);
-  for_pieces(a, blockIdx.x, [&](int s, int64_t ra, int64_t rb, bool whole) {
+  // last tiles first, as within a tile
+  for_pieces(a, gridDim.x - 1 - blockIdx.x, [&](int s, int64_t ra, int64_t rb, bool whole) {
     if (!whole)
-      fwd_rows<TX, TY, V>(a, p, ra, rb, a.mean + (int64_t)s * a.groups, a.rstd + (int64_t)s * a.groups);
+      fwd_rows<TX, TY, V>(a, p, ra, rb, a.mean + (int64_t)s * a.groups, a.rstd + (int64_t)s * a.groups,
+                             reinterpret_cast<char*>(sm));
   });
 }
 
@@ -344,7 +424,8 @@ struct BwdChannels {
     }
   }
   // dz of channel k, and its xh
-  __device__ __forceinline__ float dz(int k, float x, float dy, int act, float& xh) const {
+  template <class Act>
+  __device__ __forceinline__ float dz(int k, float x, float dy, Act act, float& xh) const {
     xh = (x - mu[k]) * rs[k];
     float av, d;
     act_grad_f(ga[k] * xh + be[k], act, av, d);
@@ -355,9 +436,9 @@ struct BwdChannels {
 // dX of the rows [ra, rb); gA, gB: the segment's two sums over each group, / m.
 template <class TX, class TY, int V>
 __device__ __forceinline__ void bwd_rows(const NormArgs& a, const Place<V>& p, int s, int64_t ra,
-                                         int64_t rb, const float* gA, const float* gB, int gstride) {
-  if (!p.on) return;
-  constexpr int U = 8 / V;
+                                         int64_t rb, const float* gA, const float* gB, int gstride,
+                                         char* ring) {
+  const int rows = p.rows(a, ra, rb);
   const BwdChannels<V> b(a, p, s);
   float A[V], B[V];
 #pragma unroll
@@ -365,84 +446,76 @@ __device__ __forceinline__ void bwd_rows(const NormArgs& a, const Place<V>& p, i
     A[k] = gA[p.g[k] * gstride];
     B[k] = gB[p.g[k] * gstride];
   }
-  const TX* X = static_cast<const TX*>(a.X) + p.c0;
-  const TY* dY = static_cast<const TY*>(a.dY) + p.c0;
-  TX* dX = static_cast<TX*>(a.out) + p.c0;
-  for (int64_t r = rb - 1 - p.ro; r >= ra; r -= (int64_t)U * p.RP) {
-    float x[U][V], dy[U][V];
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (p.in && r - u * p.RP >= ra) {
-        load_vec<V>(X + (r - u * p.RP) * a.ldx, x[u]);
-        load_vec<V>(dY + (r - u * p.RP) * a.ldy, dy[u]);
-      }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (r - u * p.RP < ra) break;
+  const int64_t last = ra + p.ro + (int64_t)(rows - 1) * a.RP;
+  const TX* X = static_cast<const TX*>(a.X) + last * a.ldx + p.c0;
+  const TY* dY = static_cast<const TY*>(a.dY) + last * a.ldy + p.c0;
+  TX* dX = static_cast<TX*>(a.out) + last * a.ldo + p.c0;
+  const int64_t sx = (int64_t)a.RP * a.ldx, sy = (int64_t)a.RP * a.ldy, so = (int64_t)a.RP * a.ldo;
+  if (!p.in) {
+    const float zero[V] = {};
+    for (int i = 0; i < rows; ++i, dX -= so) store_vec<V>(dX, zero);
+    return;
+  }
+  with_act(a.act, [&](auto act) {
+    stream_rows<V, BWD_DEPTH>(ring, rows, X, -sx, dY, -sy, [&](int, float (&x)[V], float (&dy)[V]) {
       float o[V];
 #pragma unroll
       for (int k = 0; k < V; ++k) {
         float xh;
-        const float dz = b.dz(k, x[u][k], dy[u][k], a.act, xh);
+        const float dz = b.dz(k, x[k], dy[k], act, xh);
         o[k] = p.c0 + k < a.C ? b.rs[k] * (b.ga[k] * dz - A[k] - xh * B[k]) : 0.f;
       }
-      store_vec<V>(dX + (r - u * p.RP) * a.ldo, o);
-    }
-  }
+      store_vec<V>(dX, o);
+      dX -= so;
+    });
+  });
 }
 
 template <class TX, class TY, int V>
-__global__ void __launch_bounds__(THREADS, 2) norm_bwd_sums_kernel(NormArgs a, int L) {
+__global__ void __launch_bounds__(MAX_THREADS, 2) norm_bwd_sums_kernel(NormArgs a, int L) {
   extern __shared__ float sm[];
   cudaTriggerProgrammaticLaunchCompletion();
   const Place<V> p(a);
   const int width = a.CH * V;
   float* red1 = sm;
-  float* red2 = red1 + p.RP * width;
-  float* ch1 = red2 + p.RP * width;
+  float* red2 = red1 + a.RP * width;
+  float* ch1 = red2 + a.RP * width;
   float* ch2 = ch1 + a.C;
   float* acc1 = ch2 + a.C;  // this tile's share of dbeta, dgamma
   float* acc2 = acc1 + a.C;
   float* gA = acc2 + a.C;
   float* gB = gA + a.groups;
+  char* ring = reinterpret_cast<char*>(align16(gB + a.groups));
   const TX* X = static_cast<const TX*>(a.X);
   const TY* dY = static_cast<const TY*>(a.dY);
   const int t = blockIdx.x;
-  for (int c = threadIdx.x; c < a.C; c += THREADS) acc1[c] = acc2[c] = 0.f;
+  for (int c = threadIdx.x; c < a.C; c += blockDim.x) acc1[c] = acc2[c] = 0.f;
   for_pieces(a, t, [&](int s, int64_t ra, int64_t rb, bool whole) {
     if (p.on) {
-      constexpr int U = 8 / V;
       const BwdChannels<V> b(a, p, s);
       float P1[V], P2[V];
 #pragma unroll
       for (int k = 0; k < V; ++k) P1[k] = P2[k] = 0.f;
-      if (p.in) {
-        for (int64_t r = ra + p.ro; r < rb; r += (int64_t)U * p.RP) {
-          float x[U][V], dy[U][V];
+      const TX* px = X + (ra + p.ro) * a.ldx + p.c0;
+      const TY* py = dY + (ra + p.ro) * a.ldy + p.c0;
+      const int64_t sx = (int64_t)a.RP * a.ldx, sy = (int64_t)a.RP * a.ldy;
+      with_act(a.act, [&](auto act) {
+        stream_rows<V, BWD_DEPTH>(ring, p.in ? p.rows(a, ra, rb) : 0, px, sx, py, sy,
+                                  [&](int, float (&x)[V], float (&dy)[V]) {
 #pragma unroll
-          for (int u = 0; u < U; ++u)
-            if (r + u * p.RP < rb) {
-              load_vec<V>(X + p.c0 + (r + u * p.RP) * a.ldx, x[u]);
-              load_vec<V>(dY + p.c0 + (r + u * p.RP) * a.ldy, dy[u]);
-            }
-#pragma unroll
-          for (int u = 0; u < U; ++u) {
-            if (r + u * p.RP >= rb) break;
-#pragma unroll
-            for (int k = 0; k < V; ++k) {
-              float xh;
-              const float dz = b.dz(k, x[u][k], dy[u][k], a.act, xh);
-              P1[k] += dz;
-              P2[k] += dz * xh;
-            }
-          }
-        }
-      }
+                                    for (int k = 0; k < V; ++k) {
+                                      float xh;
+                                      const float dz = b.dz(k, x[k], dy[k], act, xh);
+                                      P1[k] += dz;
+                                      P2[k] += dz * xh;
+                                    }
+                                  });
+      });
       store_vec<V>(red1 + p.ro * width + p.c0, P1);
       store_vec<V>(red2 + p.ro * width + p.c0, P2);
     }
     const float m = (float)(rb - ra) * (float)a.cg;
-    block_sums(a, p.RP, width, red1, red2, ch1, ch2, a.gamma, L, [&](int g, float A, float B) {
+    block_sums(a, width, red1, red2, ch1, ch2, a.gamma, L, [&](int g, float A, float B) {
       if (whole) {
         gA[g] = A / m;
         gB[g] = B / m;
@@ -450,30 +523,29 @@ __global__ void __launch_bounds__(THREADS, 2) norm_bwd_sums_kernel(NormArgs a, i
         a.part[((int64_t)t + s) * a.groups + g] = make_float2(A, B);
       }
     });
-    for (int c = threadIdx.x; c < a.C; c += THREADS) {
+    for (int c = threadIdx.x; c < a.C; c += blockDim.x) {
       acc1[c] += ch1[c];
       acc2[c] += ch2[c];
     }
-    if (whole) bwd_rows<TX, TY, V>(a, p, s, ra, rb, gA, gB, 1);
+    if (whole) bwd_rows<TX, TY, V>(a, p, s, ra, rb, gA, gB, 1, ring);
     __syncthreads();
   });
   if (a.dpart) {
     float* d = a.dpart + (int64_t)t * 2 * a.C;
-    for (int c = threadIdx.x; c < a.C; c += THREADS) {
+    for (int c = threadIdx.x; c < a.C; c += blockDim.x) {
       d[c] = acc1[c];
       d[a.C + c] = acc2[c];
     }
   }
 }
 
-// The first max(tiles, 1) blocks join long segments; the others add the tiles'
+// The first `joiners` blocks join long segments; the others add the tiles'
 // shares of dbeta and dgamma, 32 columns each, in tile order.
-__global__ void __launch_bounds__(FIN_THREADS) norm_bwd_join_kernel(NormArgs a) {
+__global__ void __launch_bounds__(FIN_THREADS) norm_bwd_join_kernel(NormArgs a, int joiners) {
   cudaTriggerProgrammaticLaunchCompletion();
   cudaGridDependencySynchronize();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   constexpr int NW = FIN_THREADS / 32;
-  const int joiners = max(a.tiles, 1);
   if ((int)blockIdx.x >= joiners) {
     __shared__ float red[NW][32];
     const int col = ((int)blockIdx.x - joiners) * 32 + lane;
@@ -495,34 +567,33 @@ __global__ void __launch_bounds__(FIN_THREADS) norm_bwd_join_kernel(NormArgs a) 
     }
     return;
   }
-  check_segments(a, false);
-  const int t = blockIdx.x, s = long_start(a, t);
-  if (s < 0) return;
-  const int64_t sb = seg_at(a, s), se = min(seg_at(a, s + 1), a.n);
-  const int t1 = (int)((se - 1) / a.R);
-  const float m = (float)(se - sb) * (float)a.cg;
-  for (int g = warp; g < a.groups; g += NW) {
-    const float2* part = a.part + (int64_t)s * a.groups + g;
-    float A = 0.f, B = 0.f;
+  check_segments(a, joiners, false);
+  for_long(a, joiners, [&](int s, int64_t sb, int64_t se, int t0, int t1) {
+    const float m = (float)(se - sb) * (float)a.cg;
+    for (int g = warp; g < a.groups; g += NW) {
+      const float2* part = a.part + (int64_t)s * a.groups + g;
+      float A = 0.f, B = 0.f;
 #pragma unroll 4
-    for (int i = t + lane; i <= t1; i += 32) {
-      const float2 v = part[(int64_t)i * a.groups];
-      A += v.x;
-      B += v.y;
+      for (int i = t0 + lane; i <= t1; i += 32) {
+        const float2 v = part[(int64_t)i * a.groups];
+        A += v.x;
+        B += v.y;
+      }
+      A = warp_sum(A), B = warp_sum(B);
+      if (lane == 0) a.joined[(int64_t)s * a.groups + g] = make_float2(A / m, B / m);
     }
-    A = warp_sum(A), B = warp_sum(B);
-    if (lane == 0) a.joined[(int64_t)s * a.groups + g] = make_float2(A / m, B / m);
-  }
+  });
 }
 
 template <class TX, class TY, int V>
-__global__ void __launch_bounds__(THREADS, 2) norm_bwd_apply_kernel(NormArgs a) {
+__global__ void __launch_bounds__(MAX_THREADS, 2) norm_bwd_apply_kernel(NormArgs a) {
+  extern __shared__ float sm[];
   cudaGridDependencySynchronize();
   const Place<V> p(a);
-  for_pieces(a, blockIdx.x, [&](int s, int64_t ra, int64_t rb, bool whole) {
+  for_pieces(a, gridDim.x - 1 - blockIdx.x, [&](int s, int64_t ra, int64_t rb, bool whole) {
     if (!whole) {
       const float* j = &a.joined[(int64_t)s * a.groups].x;
-      bwd_rows<TX, TY, V>(a, p, s, ra, rb, j, j + 1, 2);
+      bwd_rows<TX, TY, V>(a, p, s, ra, rb, j, j + 1, 2, reinterpret_cast<char*>(sm));
     }
   });
 }
@@ -598,37 +669,55 @@ int lanes_for(int cg) {
   return l;
 }
 
+// Threads, rows and tiles of a launch; returns the block size.
+int plan(NormArgs& a, int pad, int V) {
+  a.CH = (a.C + pad - 1) / pad * pad / V;
+  a.RP = a.CH < AIM_THREADS ? AIM_THREADS / a.CH : 1;
+  a.R = tile_rows(a.n, a.RP);
+  a.tiles = (int)((a.n + a.R - 1) / a.R);
+  return (a.RP * a.CH + 31) / 32 * 32;
+}
+int joiners(const NormArgs& a) { return a.n_seg < 4 * 152 ? a.n_seg : 4 * 152; }
+
+// Kernels whose ring may pass 48 KB of shared memory.
+template <class K>
+gnn_status allow_smem(K* k, bool& ready) {
+  if (!ready) GNN_CUDA(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024));
+  ready = true;
+  return GNN_OK;
+}
+
 template <class TX, class TY, int V>
 gnn_status norm_fwd(NormArgs a, cudaStream_t st) {
-  const int pad = sizeof(TY) == 4 ? 4 : 16;
-  a.CH = (a.C + pad - 1) / pad * pad / V;
-  const int RP = THREADS / a.CH;
-  a.R = tile_rows(a.n, RP);
-  a.tiles = (int)((a.n + a.R - 1) / a.R);
-  const size_t smem = sizeof(float) * (size_t)(2 * RP * a.CH * V + 2 * a.C + 2 * a.groups);
+  static bool ready1 = false, ready2 = false;
+  const int threads = plan(a, sizeof(TY) == 4 ? 4 : 16, V);
+  const size_t ring = (size_t)(FWD_DEPTH + 1) * threads * V * sizeof(TX);
+  const size_t smem = sizeof(float) * (size_t)(2 * a.RP * a.CH * V + 2 * a.C + 2 * a.groups) + 16 + ring;
   const Launch l{st};
-  gnn_status s = GNN_OK;
-  if (a.tiles) s = l.run(false, a.tiles, THREADS, smem, norm_fwd_stats_kernel<TX, TY, V>, a, lanes_for(a.cg));
-  if (s == GNN_OK) s = l.run(a.tiles > 0, a.tiles ? a.tiles : 1, FIN_THREADS, 0, norm_fwd_join_kernel, a);
-  if (s == GNN_OK && a.tiles) s = l.run(true, a.tiles, THREADS, 0, norm_fwd_apply_kernel<TX, TY, V>, a);
+  gnn_status s = allow_smem(norm_fwd_stats_kernel<TX, TY, V>, ready1);
+  if (s == GNN_OK) s = allow_smem(norm_fwd_apply_kernel<TX, TY, V>, ready2);
+  if (s == GNN_OK && a.tiles)
+    s = l.run(false, a.tiles, threads, smem, norm_fwd_stats_kernel<TX, TY, V>, a, lanes_for(a.cg));
+  if (s == GNN_OK) s = l.run(a.tiles > 0, joiners(a), FIN_THREADS, 0, norm_fwd_join_kernel, a);
+  if (s == GNN_OK && a.tiles) s = l.run(true, a.tiles, threads, ring, norm_fwd_apply_kernel<TX, TY, V>, a);
   return s;
 }
 
 template <class TX, class TY, int V>
 gnn_status norm_bwd(NormArgs a, cudaStream_t st) {
-  const int pad = sizeof(TX) == 4 ? 4 : 16;
-  a.CH = (a.C + pad - 1) / pad * pad / V;
-  const int RP = THREADS / a.CH;
-  a.R = tile_rows(a.n, RP);
-  a.tiles = (int)((a.n + a.R - 1) / a.R);
-  const size_t smem = sizeof(float) * (size_t)(2 * RP * a.CH * V + 4 * a.C + 2 * a.groups);
+  static bool ready1 = false, ready2 = false;
+  const int threads = plan(a, sizeof(TX) == 4 ? 4 : 16, V);
+  const size_t ring = (size_t)(BWD_DEPTH + 1) * threads * V * (sizeof(TX) + sizeof(TY));
+  const size_t smem = sizeof(float) * (size_t)(2 * a.RP * a.CH * V + 4 * a.C + 2 * a.groups) + 16 + ring;
   const Launch l{st};
-  gnn_status s = GNN_OK;
-  if (a.tiles) s = l.run(false, a.tiles, THREADS, smem, norm_bwd_sums_kernel<TX, TY, V>, a, lanes_for(a.cg));
+  gnn_status s = allow_smem(norm_bwd_sums_kernel<TX, TY, V>, ready1);
+  if (s == GNN_OK) s = allow_smem(norm_bwd_apply_kernel<TX, TY, V>, ready2);
+  if (s == GNN_OK && a.tiles)
+    s = l.run(false, a.tiles, threads, smem, norm_bwd_sums_kernel<TX, TY, V>, a, lanes_for(a.cg));
   const int cols = a.dpart ? (2 * a.C + 31) / 32 : 0;
   if (s == GNN_OK)
-    s = l.run(a.tiles > 0, (a.tiles ? a.tiles : 1) + cols, FIN_THREADS, 0, norm_bwd_join_kernel, a);
-  if (s == GNN_OK && a.tiles) s = l.run(true, a.tiles, THREADS, 0, norm_bwd_apply_kernel<TX, TY, V>, a);
+    s = l.run(a.tiles > 0, joiners(a) + cols, FIN_THREADS, 0, norm_bwd_join_kernel, a, joiners(a));
+  if (s == GNN_OK && a.tiles) s = l.run(true, a.tiles, threads, ring, norm_bwd_apply_kernel<TX, TY, V>, a);
   return s;
 }
 

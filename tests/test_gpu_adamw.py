@@ -36,7 +36,7 @@ def blocks(x):
 
 def quantise(x, low):
     b = blocks(x)
-    scale = b.abs().amax(1) / 448.0
+    scale = b.abs().amax(1) * torch.tensor(1 / 448, dtype=torch.float32)
     scale = torch.where(scale < 2.0 ** -126, torch.zeros_like(scale), scale)
     inv = torch.where(scale > 0, 1 / scale, torch.zeros_like(scale))
     q = (b * inv[:, None]).to(F8).float()
