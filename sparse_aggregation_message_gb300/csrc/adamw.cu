@@ -21,7 +21,8 @@ namespace gnn {
 namespace {
 
 constexpr int BLOCK = 256;      // elements that share a scale, and of one warp step
-constexpr int CHUNK = 4 * BLOCK;  // elements a warp takes at a time
+constexpr int MAX_UNITS = 16;   // blocks a warp takes in a row, at most
+constexpr int NORM_UNITS = 4;
 constexpr int THREADS = 256;
 constexpr int MAX_TENSORS = 56;  // of one launch: the descriptors stay below 4 KB
 constexpr int NORM_BLOCKS = 152 * 4;
@@ -29,6 +30,7 @@ constexpr float F8_INV = 1.f / 448.f;  // 448: the largest e4m3 value
 
 struct Table {
   int count;
+  int units;  // blocks of a chunk, which one warp takes
   int64_t first[MAX_TENSORS + 1];  // first chunk of tensor i
   gnn_adamw_tensor t[MAX_TENSORS];
   uint64_t aligned;  // bit i: every pointer of tensor i suits eight elements a lane
@@ -94,6 +96,31 @@ struct Raw {
             w[j >> 2] |= (uint32_t)reinterpret_cast<const uint8_t*>(p)[j * 32] << (8 * (j & 3));
         }
       }
+    }
+  }
+  // From a lane's slot of a ring: parts of 16 bytes (8 for a one-byte type), each
+  // for every thread of the block side by side.
+  __device__ __forceinline__ void from_ring(const char* part) {
+    if constexpr (W == 2) {
+      const uint2 a = reinterpret_cast<const uint2*>(part)[threadIdx.x];
+      w[0] = a.x, w[1] = a.y;
+    } else {
+#pragma unroll
+      for (int i = 0; i < W; i += 4) {
+        const uint4 a = reinterpret_cast<const uint4*>(part)[threadIdx.x + i / 4 * THREADS];
+        w[i] = a.x, w[i + 1] = a.y, w[i + 2] = a.z, w[i + 3] = a.w;
+      }
+    }
+  }
+  static __device__ __forceinline__ void to_ring(uint32_t part, const T* p) {
+    if constexpr (W == 2) {
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(part + threadIdx.x * 8), "l"(p) : "memory");
+    } else {
+#pragma unroll
+      for (int i = 0; i < W; i += 4)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(part + (threadIdx.x + i / 4 * THREADS) * 16),
+                     "l"(reinterpret_cast<const char*>(p) + 4 * i)
+                     : "memory");
     }
   }
   __device__ __forceinline__ void to(float (&v)[8]) const {
@@ -222,6 +249,12 @@ struct Step {
   Raw<TG, VEC> g;
   Raw<TS, VEC> m, v;
   float ms, vs;
+  // bytes of the parts of a ring slot
+  static constexpr int P = THREADS * 8 * sizeof(TP), G = THREADS * 8 * sizeof(TG), S = THREADS * 8 * sizeof(TS);
+  static constexpr int SLOT = P + G + 2 * S;
+  __device__ __forceinline__ void from_ring(const char* slot) {
+    p.from_ring(slot), g.from_ring(slot + P), m.from_ring(slot + P + G), v.from_ring(slot + P + G + S);
+  }
 };
 template <class TP, class TG, bool Q8>
 struct At {
@@ -244,6 +277,13 @@ struct At {
     s.m.load(m + u * BLOCK, live);
     s.v.load(v + u * BLOCK, live);
     if (Q8) s.ms = ms[u], s.vs = vs[u];
+  }
+  __device__ __forceinline__ void to_ring(uint32_t slot, int u) const {
+    using S = Step<TP, TG, Q8, true>;
+    Raw<TP, true>::to_ring(slot, p + u * BLOCK);
+    Raw<TG, true>::to_ring(slot + S::P, g + u * BLOCK);
+    Raw<TS, true>::to_ring(slot + S::P + S::G, m + u * BLOCK);
+    Raw<TS, true>::to_ring(slot + S::P + S::G + S::S, v + u * BLOCK);
   }
 };
 
@@ -307,9 +347,21 @@ __device__ __forceinline__ void update(const Step<TP, TG, Q8, VEC>& now, const A
   }
 }
 
+// With 8-bit states a lane's next steps are copied into its own slots of shared
+// memory AHEAD steps before their use (no barrier: each lane reads what it
+// copied); registers alone could hold one step ahead.  With fp32 states 24 warps
+// of plain loads reach the bandwidth (6.6 TB/s at 184M elements), and holding a
+// step ahead in registers spilt and lost 7%.
+constexpr int AHEAD = 2;
+template <class TP, class TG, bool Q8>
+constexpr int ring_bytes() {
+  return Q8 ? (AHEAD + 1) * Step<TP, TG, Q8, true>::SLOT : 0;
+}
+
 template <class TP, class TG, bool Q8>
 __global__ void __launch_bounds__(THREADS, 3)
     adamw_kernel(const __grid_constant__ Table tab, const Hyper h, const Control* ctl) {
+  extern __shared__ __align__(16) char slots[];
   cudaGridDependencySynchronize();
   const Control c = *ctl;
   if (c.skip) return;
@@ -319,28 +371,48 @@ __global__ void __launch_bounds__(THREADS, 3)
   for (int64_t k = (int64_t)blockIdx.x * (THREADS / 32) + (threadIdx.x >> 5); k < chunks; k += warps) {
     const int i = tensor_of(tab, k);
     const gnn_adamw_tensor& t = tab.t[i];
-    const int64_t base = (k - tab.first[i]) * CHUNK, left = t.n - base;
+    const int64_t base = (k - tab.first[i]) * (tab.units * BLOCK), left = t.n - base;
     // whole steps of an aligned tensor, then what remains
-    const int whole = (tab.aligned >> i & 1) ? (int)min(left / BLOCK, (int64_t)(CHUNK / BLOCK)) : 0;
+    const int whole = (tab.aligned >> i & 1) ? (int)min(left / BLOCK, (int64_t)tab.units) : 0;
     if (whole) {
       const At<TP, TG, Q8> at(t, base, base + lane * 8);
-      // With 8-bit states the next step's loads are requested before this one's
-      // arithmetic (1054 -> 959 us at 242M elements); with fp32 states their 32
-      // registers spill and bandwidth is reached without (772 against 827 us at 184M).
-      Step<TP, TG, Q8, true> next;
-      if (Q8) at.load(next, 0, 8);
+      Step<TP, TG, Q8, true> now;
+      if constexpr (Q8) {
+        // lanes 0-15 hold the chunk's scales of m, 16-31 those of v
+        float scale = 0.f;
+        if ((lane & 15) < whole) scale = lane < 16 ? at.ms[lane] : at.vs[lane - 16];
+        const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(slots));
+        constexpr int SLOT = Step<TP, TG, Q8, true>::SLOT;
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u) {
+          if (u < whole) at.to_ring(ring + u * SLOT, u);
+          asm volatile("cp.async.commit_group;" ::: "memory");
+        }
+        int use = 0, fill = AHEAD * SLOT;
 #pragma unroll 1
-      for (int u = 0; u < whole; ++u) {
-        if (!Q8) at.load(next, u, 8);
-        const Step<TP, TG, Q8, true> now = next;
-        if (Q8 && u + 1 < whole) at.load(next, u + 1, 8);
-        update(now, at, u, 8, h, c);
+        for (int u = 0; u < whole; ++u) {
+          asm volatile("cp.async.wait_group %0;" ::"n"(AHEAD - 1) : "memory");
+          now.from_ring(slots + use);
+          now.ms = __shfl_sync(0xffffffffu, scale, u);
+          now.vs = __shfl_sync(0xffffffffu, scale, 16 + u);
+          if (u + AHEAD < whole) at.to_ring(ring + fill, u + AHEAD);
+          asm volatile("cp.async.commit_group;" ::: "memory");
+          fill = use;  // used up before the next step's copies go there
+          use = use == AHEAD * SLOT ? 0 : use + SLOT;
+          update(now, at, u, 8, h, c);
+        }
+      } else {
+#pragma unroll 1
+        for (int u = 0; u < whole; ++u) {
+          at.load(now, u, 8);
+          update(now, at, u, 8, h, c);
+        }
       }
     }
-    if (whole < CHUNK / BLOCK && left > whole * BLOCK) {
+    if (whole < tab.units && left > whole * BLOCK) {
       const At<TP, TG, Q8> at(t, base, base + lane);
 #pragma unroll 1
-      for (int u = whole; u < CHUNK / BLOCK && left > u * BLOCK; ++u) {
+      for (int u = whole; u < tab.units && left > u * BLOCK; ++u) {
         const int64_t mine = left - u * BLOCK - lane;  // elements from this lane's first one on
         const int live = mine <= 0 ? 0 : (int)min((mine + 31) / 32, (int64_t)8);
         Step<TP, TG, Q8, false> now;
@@ -366,10 +438,10 @@ __device__ __forceinline__ double block_sum(double v, double* sm) {
 // squares to an fp64 addition the fp64 pipe was 73% busy); where the 32 leave
 // the range that fp32 holds well, they are formed again in fp64.
 template <class TG, bool VEC>
-__device__ __forceinline__ double squares(const Raw<TG, VEC> (&raw)[CHUNK / BLOCK]) {
+__device__ __forceinline__ double squares(const Raw<TG, VEC> (&raw)[NORM_UNITS]) {
   float s = 0.f;
 #pragma unroll
-  for (int u = 0; u < CHUNK / BLOCK; ++u) {
+  for (int u = 0; u < NORM_UNITS; ++u) {
     float g[8];
     raw[u].to(g);
     s += ((g[0] * g[0] + g[1] * g[1]) + (g[2] * g[2] + g[3] * g[3])) +
@@ -378,7 +450,7 @@ __device__ __forceinline__ double squares(const Raw<TG, VEC> (&raw)[CHUNK / BLOC
   if (s > 1e-28f && s < 1e38f) return (double)s;
   double d = 0;
 #pragma unroll
-  for (int u = 0; u < CHUNK / BLOCK; ++u) {
+  for (int u = 0; u < NORM_UNITS; ++u) {
     float g[8];
     raw[u].to(g);
 #pragma unroll
@@ -400,17 +472,17 @@ __global__ void __launch_bounds__(THREADS) norm_kernel(const __grid_constant__ T
   for (int64_t k = (int64_t)blockIdx.x * (THREADS / 32) + (threadIdx.x >> 5); k < chunks; k += warps) {
     const int i = tensor_of(tab, k);
     const gnn_adamw_tensor& t = tab.t[i];
-    const int64_t base = (k - tab.first[i]) * CHUNK, left = t.n - base;
+    const int64_t base = (k - tab.first[i]) * (NORM_UNITS * BLOCK), left = t.n - base;
     const TG* g = static_cast<const TG*>(t.grad) + base;
-    if ((tab.aligned >> i & 1) && left >= CHUNK) {
-      Raw<TG, true> raw[CHUNK / BLOCK];
+    if ((tab.aligned >> i & 1) && left >= NORM_UNITS * BLOCK) {
+      Raw<TG, true> raw[NORM_UNITS];
 #pragma unroll
-      for (int u = 0; u < CHUNK / BLOCK; ++u) raw[u].load(g + u * BLOCK + lane * 8, 8);
+      for (int u = 0; u < NORM_UNITS; ++u) raw[u].load(g + u * BLOCK + lane * 8, 8);
       sum += squares(raw);
     } else {
-      Raw<TG, false> raw[CHUNK / BLOCK];
+      Raw<TG, false> raw[NORM_UNITS];
 #pragma unroll
-      for (int u = 0; u < CHUNK / BLOCK; ++u) {
+      for (int u = 0; u < NORM_UNITS; ++u) {
         const int64_t mine = left - u * BLOCK - lane;
         raw[u].load(g + u * BLOCK + lane, mine <= 0 ? 0 : (int)min((mine + 31) / 32, (int64_t)8));
       }
@@ -469,26 +541,12 @@ __global__ void __launch_bounds__(THREADS)
 
 bool aligned_to(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 
-template <class TP, class TG, bool Q8>
-void (*update_kernel())(const Table, const Hyper, const Control*) {
-  return adamw_kernel<TP, TG, Q8>;
-}
-template <class TP, class TG>
-void (*update_kernel(bool q8))(const Table, const Hyper, const Control*) {
-  return q8 ? update_kernel<TP, TG, true>() : update_kernel<TP, TG, false>();
-}
-template <class TP>
-void (*update_kernel(int gt, bool q8))(const Table, const Hyper, const Control*) {
-  if (gt == GNN_BF16) return update_kernel<TP, __nv_bfloat16>(q8);
-  if (gt == GNN_F16) return update_kernel<TP, __half>(q8);
-  return update_kernel<TP, float>(q8);
-}
-
 template <class... P, class... A>
-gnn_status launch(cudaStream_t st, bool after, int64_t grid, void (*k)(P...), A... args) {
+gnn_status launch(cudaStream_t st, bool after, int64_t grid, size_t smem, void (*k)(P...), A... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -498,6 +556,30 @@ gnn_status launch(cudaStream_t st, bool after, int64_t grid, void (*k)(P...), A.
   count_launch();
   GNN_CUDA(cudaLaunchKernelEx(&cfg, k, args...));
   return GNN_OK;
+}
+
+using Update = gnn_status (*)(cudaStream_t, bool, int64_t, const Table&, const Hyper&, const Control*);
+
+template <class TP, class TG, bool Q8>
+gnn_status launch_update(cudaStream_t st, bool after, int64_t grid, const Table& tab, const Hyper& h,
+                         const Control* ctl) {
+  constexpr int smem = ring_bytes<TP, TG, Q8>();
+  static bool ready = false;
+  if (!ready) {
+    GNN_CUDA(cudaFuncSetAttribute(adamw_kernel<TP, TG, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+    ready = true;
+  }
+  return launch(st, after, grid, smem, adamw_kernel<TP, TG, Q8>, tab, h, ctl);
+}
+template <class TP, class TG>
+Update update_for(bool q8) {
+  return q8 ? launch_update<TP, TG, true> : launch_update<TP, TG, false>;
+}
+template <class TP>
+Update update_for(int gt, bool q8) {
+  if (gt == GNN_BF16) return update_for<TP, __nv_bfloat16>(q8);
+  if (gt == GNN_F16) return update_for<TP, __half>(q8);
+  return update_for<TP, float>(q8);
 }
 
 }  // namespace
@@ -550,13 +632,15 @@ extern "C" gnn_status gnn_adamw_step(const gnn_adamw_tensor* tensors, int32_t n_
   double* partial = reinterpret_cast<double*>(static_cast<char*>(ws) + 256);
   const Hyper h{(float)beta1, (float)(1.0 - beta1), (float)beta2, (float)(1.0 - beta2),
                 (float)(1.0 - lr * weight_decay), (float)eps, eps <= 0x1p60};
-  auto* update = param_type == GNN_F32 ? update_kernel<float>(grad_type, q8)
-                                       : update_kernel<__nv_bfloat16>(grad_type, q8);
+  const Update update = param_type == GNN_F32 ? update_for<float>(grad_type, q8)
+                                              : update_for<__nv_bfloat16>(grad_type, q8);
   auto* norm = grad_type == GNN_BF16 ? norm_kernel<__nv_bfloat16>
                : grad_type == GNN_F16 ? norm_kernel<__half> : norm_kernel<float>;
   // the launches a pass over all tensors takes: tables of up to MAX_TENSORS
-  auto each = [&](auto&& run) -> gnn_status {
+  auto each = [&](int units, auto&& run) -> gnn_status {
     Table tab;
+    tab.units = units;
+    const int64_t chunk = (int64_t)units * BLOCK;
     int i = 0;
     while (i < n_tensors) {
       tab.count = 0;
@@ -567,7 +651,7 @@ extern "C" gnn_status gnn_adamw_step(const gnn_adamw_tensor* tensors, int32_t n_
         if (t.n == 0) continue;
         const int k = tab.count++;
         tab.t[k] = t;
-        tab.first[k + 1] = tab.first[k] + (t.n + CHUNK - 1) / CHUNK;
+        tab.first[k + 1] = tab.first[k] + (t.n + chunk - 1) / chunk;
         if (aligned_to(t.param, 16) && aligned_to(t.grad, 16) && aligned_to(t.m, q8 ? 8 : 16) &&
             aligned_to(t.v, q8 ? 8 : 16) && aligned_to(t.copy, 16))
           tab.aligned |= 1ull << k;
@@ -584,21 +668,27 @@ extern "C" gnn_status gnn_adamw_step(const gnn_adamw_tensor* tensors, int32_t n_
   };
   int n_partial = 0;
   if (max_norm > 0) {
-    const gnn_status s = each([&](const Table& tab) -> gnn_status {
+    const gnn_status s = each(NORM_UNITS, [&](const Table& tab) -> gnn_status {
       // every launch writes or adds to all partials of the first's grid
       const int64_t grid = n_partial ? n_partial : grid_for(tab, NORM_BLOCKS);
-      const gnn_status r = launch(st, false, grid, norm, tab, partial, n_partial ? 1 : 0);
+      const gnn_status r = launch(st, false, grid, 0, norm, tab, partial, n_partial ? 1 : 0);
       n_partial = (int)grid;
       return r;
     });
     if (s != GNN_OK) return s;
   }
-  gnn_status s = launch(st, n_partial > 0, 1, begin_kernel, (const double*)partial, n_partial, state, lr,
+  gnn_status s = launch(st, n_partial > 0, 1, 0, begin_kernel, (const double*)partial, n_partial, state, lr,
                         beta1, beta2, grad_scale, max_norm, grad_norm, ctl);
   if (s != GNN_OK) return s;
+  // A chunk is what a warp takes in a row: long enough to fill its ring, short
+  // enough that every warp of the card has a few.
+  int64_t blocks = 0;
+  for (int i = 0; i < n_tensors; ++i) blocks += (tensors[i].n + BLOCK - 1) / BLOCK;
+  const int64_t share = blocks / (152 * 3 * (THREADS / 32) * 4);
+  const int units = share < 1 ? 1 : share > MAX_UNITS ? MAX_UNITS : (int)share;
   bool first = true;
-  return each([&](const Table& tab) -> gnn_status {
-    const gnn_status r = launch(st, first, grid_for(tab, 152 * 3 * 4), update, tab, h, (const Control*)ctl);
+  return each(units, [&](const Table& tab) -> gnn_status {
+    const gnn_status r = update(st, first, grid_for(tab, 152 * 3 * 4), tab, h, ctl);
     first = false;
     return r;
   });

@@ -96,15 +96,49 @@ __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) { retu
 template <>
 __device__ __forceinline__ __half from_f32<__half>(float x) { return __float2half_rn(x); }
 
+// 2^x and 1/x in one instruction each, subnormals taken as zero: all that is
+// formed from them below is compared with one.
+__device__ __forceinline__ float ex2_f(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp_f(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+
 // 1 / (1 + exp(-z)): exp(-z) may reach infinity, whose reciprocal is zero.
-__device__ __forceinline__ float sigmoid_f(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
+__device__ __forceinline__ float sigmoid_f(float z) { return rcp_f(1.f + ex2_f(-kLog2e * z)); }
+
+// The normal distribution's Phi(z) and exp(-z^2/2).  With x = |z|/sqrt 2,
+// erfc(x) = t P(t) exp(-x^2), t = 1/(1 + 0.3275911 x): Abramowitz and Stegun
+// 7.1.26, absolute error at most 1.5e-7, so at most 7.5e-8 in Phi.  It shares
+// its exponential with the derivative of gelu.
+__device__ __forceinline__ float phi_f(float z, float& e) {
+  const float x = fabsf(z);
+  e = ex2_f((-0.5f * kLog2e) * z * z);
+  const float t = rcp_f(fmaf(0.3275911f * 0.70710678118654752f, x, 1.f));
+  float q = fmaf(1.061405429f, t, -1.453152027f);
+  q = fmaf(q, t, 1.421413741f);
+  q = fmaf(q, t, -0.284496736f);
+  q = fmaf(q, t, 0.254829592f);
+  q = 0.5f * t * q * e;
+  return z >= 0.f ? 1.f - q : q;
+}
 
 // act(z); `act` is the same for a whole launch, so the branch is uniform.
 __device__ __forceinline__ float act_f(float z, int act) {
   switch (act) {
     case GNN_ACT_RELU: return z > 0.f ? z : (z != z ? z : 0.f);
     case GNN_ACT_SILU: return z * sigmoid_f(z);
-    case GNN_ACT_GELU: return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
+    case GNN_ACT_GELU: {
+      float e;
+      return z * phi_f(z, e);
+    }
     case GNN_ACT_SIGMOID: return sigmoid_f(z);
     default: return z;
   }
@@ -120,13 +154,14 @@ __device__ __forceinline__ void act_grad_f(float z, int act, float& a, float& d)
     case GNN_ACT_SILU: {
       const float s = sigmoid_f(z);
       a = z * s;
-      d = s * (1.f + z * (1.f - s));
+      d = fmaf(a, 1.f - s, s);
       break;
     }
     case GNN_ACT_GELU: {
-      const float c = 0.5f * (1.f + erff(z * 0.70710678118654752f));
+      float e;
+      const float c = phi_f(z, e);
       a = z * c;
-      d = c + z * 0.39894228040143268f * __expf(-0.5f * z * z);
+      d = fmaf(z * 0.39894228040143268f, e, c);
       break;
     }
     case GNN_ACT_SIGMOID:

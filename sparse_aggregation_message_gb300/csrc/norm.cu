@@ -120,11 +120,11 @@ struct Place {
   }
 };
 
-// A thread's own ring of rows in shared memory: row i + DEPTH is requested with
-// an asynchronous copy as row i is used, so DEPTH rows a thread are in flight
-// at no cost in registers.  Every thread reads only what it copied itself, so
-// there is no barrier; the slot that is filled is the one that was used up an
-// iteration earlier.
+// A thread's own ring in shared memory: pairs of rows are requested with
+// asynchronous copies DEPTH pairs ahead of their use, so 2 DEPTH rows a thread
+// are in flight at no cost in registers.  Every thread reads only what it
+// copied itself, so there is no barrier; the slot that is filled is the one
+// that was used up an iteration earlier.
 template <int BYTES>
 __device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
   if constexpr (BYTES == 16)
@@ -132,55 +132,81 @@ __device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
   else
     asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
 }
+// V elements from a shared-memory address, as fp32.
+template <int V, class T>
+__device__ __forceinline__ void load_shared(uint32_t at, float (&v)[V]) {
+  constexpr int W = V * sizeof(T) / 4;
+  uint32_t w[W];
+  if constexpr (W == 4)
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                 : "r"(at)
+                 : "memory");
+  else
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(at) : "memory");
+#pragma unroll
+  for (int i = 0; i < W; ++i) {
+    if constexpr (sizeof(T) == 4) {
+      v[i] = __uint_as_float(w[i]);
+    } else {
+      const float2 f = Pack2<T>::from(w[i]);
+      v[2 * i] = f.x, v[2 * i + 1] = f.y;
+    }
+  }
+}
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void copy_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// One or two matrices (TB = void: one) walked row by row in steps of da, db
-// elements from pa, pb, V elements a row and thread; f(row number, a, b).
-template <int V, int DEPTH, class TA, class TB, class Fn>
+// One or two matrices (pb NULL: one) walked row by row in steps of da, db
+// elements from pa, pb, V elements a row and thread; f(a, b) for every row.
+template <int V, int DEPTH, bool TWO, class TA, class TB, class Fn>
 __device__ __forceinline__ void stream_rows(char* ring, int rows, const TA* pa, int64_t da, const TB* pb,
                                             int64_t db, Fn f) {
   constexpr int SA = V * sizeof(TA), SB = V * sizeof(TB);
-  const int stride_a = blockDim.x * SA, stride_b = blockDim.x * SB;
-  char* ra = ring + threadIdx.x * SA;
-  char* rb = ring + (DEPTH + 1) * stride_a + threadIdx.x * SB;
-  const uint32_t sa = static_cast<uint32_t>(__cvta_generic_to_shared(ra));
-  const uint32_t sb = static_cast<uint32_t>(__cvta_generic_to_shared(rb));
-  int fill = 0;
+  const uint32_t row_a = blockDim.x * SA, row_b = blockDim.x * SB;  // bytes between a slot's two rows
+  const uint32_t end = 2 * row_a * (DEPTH + 1);
+  const uint32_t sa = static_cast<uint32_t>(__cvta_generic_to_shared(ring)) + threadIdx.x * SA;
+  const uint32_t sb = static_cast<uint32_t>(__cvta_generic_to_shared(ring)) + end + threadIdx.x * SB;
+  int ahead = rows;  // rows not yet requested
+  auto request = [&](uint32_t slot) {
+    if (ahead > 0) {
+      copy_async<SA>(sa + slot, pa);
+      if (TWO) copy_async<SB>(sb + slot * SB / SA, pb);
+    }
+    if (ahead > 1) {
+      copy_async<SA>(sa + slot + row_a, pa + da);
+      if (TWO) copy_async<SB>(sb + slot * SB / SA + row_b, pb + db);
+    }
+    ahead -= 2;
+    pa += 2 * da;
+    if (TWO) pb += 2 * db;
+    copy_commit();
+  };
+  auto read = [&](uint32_t slot, int second, float (&a)[V], float (&b)[V]) {
+    load_shared<V, TA>(sa + slot + second * row_a, a);
+    if (TWO) load_shared<V, TB>(sb + slot * SB / SA + second * row_b, b);
+  };
 #pragma unroll
-  for (int i = 0; i < DEPTH; ++i) {
-    if (i < rows) {
-      copy_async<SA>(sa + fill * stride_a, pa);
-      if (pb) copy_async<SB>(sb + fill * stride_b, pb);
-      pa += da;
-      if (pb) pb += db;
-    }
-    ++fill;
-    copy_commit();
-  }
-  int use = 0;
-  for (int i = 0; i < rows; ++i) {
+  for (int i = 0; i < DEPTH; ++i) request(i * 2 * row_a);
+  uint32_t use = 0, fill = DEPTH * 2 * row_a;
+  for (int i = rows; i > 0; i -= 2) {
     copy_wait<DEPTH - 1>();
-    float a[V], b[V];
-    load_vec<V>(reinterpret_cast<const TA*>(ra + use * stride_a), a);
-    if (pb) load_vec<V>(reinterpret_cast<const TB*>(rb + use * stride_b), b);
-    if (i + DEPTH < rows) {
-      copy_async<SA>(sa + fill * stride_a, pa);
-      if (pb) copy_async<SB>(sb + fill * stride_b, pb);
-      pa += da;
-      if (pb) pb += db;
-    }
-    copy_commit();
-    fill = fill == DEPTH ? 0 : fill + 1;
-    use = use == DEPTH ? 0 : use + 1;
-    f(i, a, b);
+    float a0[V], b0[V], a1[V], b1[V];
+    read(use, 0, a0, b0);
+    read(use, 1, a1, b1);  // without a second row: what the slot held, not used
+    request(fill);
+    fill = use;
+    use += 2 * row_a;
+    if (use == end) use = 0;
+    f(a0, b0);
+    if (i > 1) f(a1, b1);
   }
   copy_wait<0>();
 }
-constexpr int FWD_DEPTH = 8, BWD_DEPTH = 6;
+constexpr int FWD_DEPTH = 4, BWD_DEPTH = 3;
 
 // One fp32 value per channel of the thread (the fill where src is NULL).
 template <int V>
@@ -255,7 +281,7 @@ __device__ __forceinline__ void fwd_rows(const NormArgs& a, const Place<V>& p, i
     return;
   }
   with_act(a.act, [&](auto act) {
-    stream_rows<V, FWD_DEPTH>(ring, rows, X, -dx, (const float*)nullptr, 0, [&](int, float (&x)[V], float (&)[V]) {
+    stream_rows<V, FWD_DEPTH, false>(ring, rows, X, -dx, X, 0, [&](float (&x)[V], float (&)[V]) {
       float y[V];
 #pragma unroll
       for (int k = 0; k < V; ++k) y[k] = p.c0 + k < a.C ? act_f((x[k] - mu[k]) * sc[k] + bt[k], act) : 0.f;
@@ -457,7 +483,7 @@ __device__ __forceinline__ void bwd_rows(const NormArgs& a, const Place<V>& p, i
     return;
   }
   with_act(a.act, [&](auto act) {
-    stream_rows<V, BWD_DEPTH>(ring, rows, X, -sx, dY, -sy, [&](int, float (&x)[V], float (&dy)[V]) {
+    stream_rows<V, BWD_DEPTH, true>(ring, rows, X, -sx, dY, -sy, [&](float (&x)[V], float (&dy)[V]) {
       float o[V];
 #pragma unroll
       for (int k = 0; k < V; ++k) {
@@ -500,8 +526,8 @@ __global__ void __launch_bounds__(MAX_THREADS, 2) norm_bwd_sums_kernel(NormArgs 
       const TY* py = dY + (ra + p.ro) * a.ldy + p.c0;
       const int64_t sx = (int64_t)a.RP * a.ldx, sy = (int64_t)a.RP * a.ldy;
       with_act(a.act, [&](auto act) {
-        stream_rows<V, BWD_DEPTH>(ring, p.in ? p.rows(a, ra, rb) : 0, px, sx, py, sy,
-                                  [&](int, float (&x)[V], float (&dy)[V]) {
+        stream_rows<V, BWD_DEPTH, true>(ring, p.in ? p.rows(a, ra, rb) : 0, px, sx, py, sy,
+                                  [&](float (&x)[V], float (&dy)[V]) {
 #pragma unroll
                                     for (int k = 0; k < V; ++k) {
                                       float xh;
@@ -691,7 +717,7 @@ template <class TX, class TY, int V>
 gnn_status norm_fwd(NormArgs a, cudaStream_t st) {
   static bool ready1 = false, ready2 = false;
   const int threads = plan(a, sizeof(TY) == 4 ? 4 : 16, V);
-  const size_t ring = (size_t)(FWD_DEPTH + 1) * threads * V * sizeof(TX);
+  const size_t ring = (size_t)2 * (FWD_DEPTH + 1) * threads * V * sizeof(TX);
   const size_t smem = sizeof(float) * (size_t)(2 * a.RP * a.CH * V + 2 * a.C + 2 * a.groups) + 16 + ring;
   const Launch l{st};
   gnn_status s = allow_smem(norm_fwd_stats_kernel<TX, TY, V>, ready1);
@@ -707,7 +733,7 @@ template <class TX, class TY, int V>
 gnn_status norm_bwd(NormArgs a, cudaStream_t st) {
   static bool ready1 = false, ready2 = false;
   const int threads = plan(a, sizeof(TX) == 4 ? 4 : 16, V);
-  const size_t ring = (size_t)(BWD_DEPTH + 1) * threads * V * (sizeof(TX) + sizeof(TY));
+  const size_t ring = (size_t)2 * (BWD_DEPTH + 1) * threads * V * (sizeof(TX) + sizeof(TY));
   const size_t smem = sizeof(float) * (size_t)(2 * a.RP * a.CH * V + 4 * a.C + 2 * a.groups) + 16 + ring;
   const Launch l{st};
   gnn_status s = allow_smem(norm_bwd_sums_kernel<TX, TY, V>, ready1);
