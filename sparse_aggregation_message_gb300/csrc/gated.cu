@@ -6,15 +6,21 @@
 //   ACT  the same product again in the backward, epilogue dG|dU from dH
 //   DX   dX = [dG|dU] [Wg|Wu]^T (one accumulation over both halves)
 //   DW   dWg|dWu = X^T [dG|dU], split over the rows
-// A 128 x 256 accumulator tile of FWD and ACT holds 128 gate and the same 128
-// up columns, so both factors of an output element meet in one thread and G, U
-// never reach memory.  Weights are read as they lie ([F_in][F_mid], columns
-// contiguous): MN-major operands in FWD/ACT, K-major in DX.
+// A 256 x 256 tile belongs to a pair of CTAs (cta_group::2), each with 128 of
+// its rows and half of B in shared memory.  On single CTAs (128 x 256 tiles) all
+// four products ran at the rate their operands came from L2, 13.5-15 TB/s,
+// 57-65% of the tensor rate; the pair halves B's share of that traffic.
+// In FWD and ACT the first CTA's half of B is the gate's columns and the
+// second's the same columns of up, so both factors of an output element meet in
+// one thread and G, U never reach memory.  Weights are read as they lie
+// ([F_in][F_mid], columns contiguous): MN-major operands in FWD/ACT, K-major in
+// DX.
 //
 // Roles: warp 0 issues TMA loads into a ring of 128-byte-swizzled tiles, warp 1
-// issues the MMAs from one thread, warps 2-9 drain one of two TMEM accumulators
-// while the next tile is multiplied (eight of them: exponentials of 128 x 128
-// outputs would take longer than the product on four).  Every wait is bounded.
+// of the first CTA issues the MMAs from one thread, warps 2-9 drain one of two
+// TMEM accumulators while the next tile is multiplied (eight of them:
+// exponentials of 128 x 128 outputs would take longer than the product on
+// four).  Every wait is bounded.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -29,15 +35,16 @@ namespace {
 
 enum Mode { FWD, ACT, DX, DW };
 
-constexpr int BM = 128, BN = 256, BK = 64;
-constexpr int A_STAGE = BM * BK * 2;  // 16 KB
-constexpr int B_STAGE = BN * BK * 2;  // 32 KB
+constexpr int BM = 256, BN = 256, BK = 64;  // of a pair of CTAs
+constexpr int CM = BM / 2, CN = BN / 2;      // a CTA's rows of A and of B
+constexpr int A_STAGE = CM * BK * 2;  // 16 KB
+constexpr int B_STAGE = CN * BK * 2;  // 16 KB
 constexpr int BOX = 64 * BK * 2;      // one 64-wide block of an MN-major operand: 8 KB
 constexpr int SUB = 32 * 128;         // a warp's 32 rows x 128 bytes of staged output
 constexpr int EPI_WARPS = 8;
 constexpr int THREADS = 64 + 32 * EPI_WARPS;
 
-constexpr int stages(Mode m) { return m == ACT ? 3 : 4; }
+constexpr int stages(Mode m) { return m == ACT ? 5 : 6; }
 constexpr int subs(Mode m) { return m == ACT ? 2 : m == DW ? 0 : 1; }  // staging tiles of an epilogue warp
 constexpr int smem_bytes(Mode m) {
   return stages(m) * (A_STAGE + B_STAGE) + EPI_WARPS * subs(m) * SUB + 1024 /*barriers*/ + 1024 /*align*/;
@@ -72,16 +79,16 @@ __device__ __forceinline__ Smem carve(uint8_t* raw) {
   s.out = s.b + stages(M) * B_STAGE;
   uint64_t* bars = reinterpret_cast<uint64_t*>(s.out + EPI_WARPS * subs(M) * SUB);
   s.full = bars;
-  s.empty = bars + 4;
-  s.tfull = bars + 8;
-  s.tempty = bars + 10;
-  s.dh = bars + 12;
-  s.tmem = reinterpret_cast<uint32_t*>(bars + 12 + EPI_WARPS);
+  s.empty = bars + 6;
+  s.tfull = bars + 12;
+  s.tempty = bars + 14;
+  s.dh = bars + 16;
+  s.tmem = reinterpret_cast<uint32_t*>(bars + 16 + EPI_WARPS);
   s.abort_flag = reinterpret_cast<volatile int*>(s.tmem + 1);
   return s;
 }
 
-// A tile's place: row block, column block, half (DW: gate or up), k blocks.
+// A tile's place: first row and column of the pair's, half (DW: gate or up), k blocks.
 struct Tile {
   int m0, n0, half, split, kb0, kb1;
 };
@@ -113,28 +120,34 @@ __device__ __forceinline__ int num_tiles(const Args& g) {
   return g.num_m * g.num_n * (M == DW ? 2 * g.splits : 1);
 }
 
+// Bytes that both CTAs load in a stage.
 template <Mode M>
-__device__ __forceinline__ void load_stage(const Args& g, const Smem& s, const Tile& t, int kb, int st) {
+__device__ __forceinline__ uint32_t stage_bytes(const Args& g) {
+  return 2 * (A_STAGE + (M == DX ? g.bn / 2 * BK * 2 : B_STAGE));
+}
+
+// This CTA's share of a stage; `bar`: the first CTA's barrier.
+template <Mode M>
+__device__ __forceinline__ void load_stage(const Args& g, const Smem& s, const Tile& t, int kb, int st, int rank,
+                                           uint32_t bar) {
   uint8_t* a = s.a + st * A_STAGE;
   uint8_t* b = s.b + st * B_STAGE;
-  uint64_t* bar = &s.full[st];
+  const int m = t.m0 + rank * CM;
   if (M == FWD || M == ACT) {
-    tc::mbar_expect_tx(bar, A_STAGE + B_STAGE);
-    tc::tma_load_2d(a, &g.a[0], bar, kb * BK, t.m0);
+    tc::tma_load_2d_pair(a, &g.a[0], bar, kb * BK, m);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) tc::tma_load_2d(b + j * BOX, &g.b[j >> 1], bar, t.n0 + 64 * (j & 1), kb * BK);
+    for (int j = 0; j < 2; ++j) tc::tma_load_2d_pair(b + j * BOX, &g.b[rank], bar, t.n0 + 64 * j, kb * BK);
   } else if (M == DX) {
     const int half = kb >= g.num_kb;
     const int k = (half ? kb - g.num_kb : kb) * BK;
-    tc::mbar_expect_tx(bar, A_STAGE + g.bn * BK * 2);
-    tc::tma_load_2d(a, &g.a[half], bar, k, t.m0);
-    tc::tma_load_2d(b, &g.b[half], bar, k, t.n0);
+    tc::tma_load_2d_pair(a, &g.a[half], bar, k, m);
+    tc::tma_load_2d_pair(b, &g.b[half], bar, k, t.n0 + rank * (g.bn / 2));
   } else {
-    tc::mbar_expect_tx(bar, A_STAGE + B_STAGE);
 #pragma unroll
-    for (int j = 0; j < 2; ++j) tc::tma_load_2d(a + j * BOX, &g.a[0], bar, t.m0 + 64 * j, kb * BK);
+    for (int j = 0; j < 2; ++j) tc::tma_load_2d_pair(a + j * BOX, &g.a[0], bar, m + 64 * j, kb * BK);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) tc::tma_load_2d(b + j * BOX, &g.b[t.half], bar, t.n0 + 64 * j, kb * BK);
+    for (int j = 0; j < 2; ++j)
+      tc::tma_load_2d_pair(b + j * BOX, &g.b[t.half], bar, t.n0 + rank * CN + 64 * j, kb * BK);
   }
 }
 
@@ -144,12 +157,14 @@ __device__ __forceinline__ uint4* staged(uint8_t* tile, int r, int k) {
 }
 
 template <Mode M, class T>
-__global__ void __launch_bounds__(THREADS, 1) gated_kernel(const __grid_constant__ Args g) {
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) gated_kernel(const __grid_constant__ Args g) {
   extern __shared__ uint8_t smem_raw[];
   const Smem s = carve<M>(smem_raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
   constexpr int ST = stages(M);
+  const int rank = (int)tc::cluster_rank();
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   if (threadIdx.x == 0) {
     for (int i = 0; i < ST; ++i) {
       tc::mbar_init(&s.full[i], 1);
@@ -157,18 +172,19 @@ __global__ void __launch_bounds__(THREADS, 1) gated_kernel(const __grid_constant
     }
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(&s.tfull[i], 1);
-      tc::mbar_init(&s.tempty[i], 32 * EPI_WARPS);
+      tc::mbar_init(&s.tempty[i], 2 * EPI_WARPS);  // a lane of each warp, of both CTAs
     }
     for (int i = 0; i < EPI_WARPS; ++i) tc::mbar_init(&s.dh[i], 1);
     *s.abort_flag = 0;
     tc::fence_barrier_init();
   }
   if (warp == 1) {
-    tc::tmem_alloc(s.tmem, 2 * BN);
-    tc::tmem_relinquish();
+    tc::tmem_alloc_pair(s.tmem, 2 * BN);
+    tc::tmem_relinquish_pair();
   }
   tc::fence_before_sync();
   __syncthreads();
+  tc::cluster_sync();  // the partner's barriers are there
   tc::fence_after_sync();
   const uint32_t tmem = *s.tmem;
   const int tiles = num_tiles<M>(g);
@@ -176,23 +192,29 @@ __global__ void __launch_bounds__(THREADS, 1) gated_kernel(const __grid_constant
   if (warp == 0 && lane == 0) {
     int st = 0;
     uint32_t ph = 0;
-    for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
+    for (int t = pair; t < tiles; t += pairs) {
       const Tile w = tile_at<M>(g, t);
       for (int kb = w.kb0; kb < w.kb1; ++kb) {
         if (!tc::mbar_wait(&s.empty[st], ph ^ 1, g.flags, s.abort_flag)) goto done;
-        load_stage<M>(g, s, w, kb, st);
+        if (rank == 0) tc::mbar_expect_tx(&s.full[st], stage_bytes<M>(g));
+        load_stage<M>(g, s, w, kb, st, rank, tc::map_to_rank(&s.full[st], 0));
         if (++st == ST) { st = 0; ph ^= 1; }
       }
     }
-  } else if (warp == 1 && lane == 0) {
+    // every stage's release has arrived before this CTA may end
+    for (int i = 0; i < ST; ++i) {
+      if (!tc::mbar_wait(&s.empty[st], ph ^ 1, g.flags, s.abort_flag)) goto done;
+      if (++st == ST) { st = 0; ph ^= 1; }
+    }
+  } else if (warp == 1 && lane == 0 && rank == 0) {
     constexpr bool a_mn = M == DW, b_mn = M != DX;
     const uint32_t idesc = tc::idesc_16(kBf16, BM, M == DX ? g.bn : BN, a_mn, b_mn);
     int st = 0, it = 0;
     uint32_t ph = 0;
-    for (int t = blockIdx.x; t < tiles; t += gridDim.x, ++it) {
+    for (int t = pair; t < tiles; t += pairs, ++it) {
       const Tile w = tile_at<M>(g, t);
       const int acc = it & 1;
-      if (!tc::mbar_wait(&s.tempty[acc], ((it >> 1) & 1) ^ 1, g.flags, s.abort_flag)) goto done;
+      if (!tc::mbar_wait<true>(&s.tempty[acc], ((it >> 1) & 1) ^ 1, g.flags, s.abort_flag)) goto done;
       tc::fence_after_sync();
       const uint32_t d = tmem + acc * BN;
       for (int kb = w.kb0; kb < w.kb1; ++kb) {
@@ -201,24 +223,31 @@ __global__ void __launch_bounds__(THREADS, 1) gated_kernel(const __grid_constant
         const uint32_t a0 = tc::smem_u32(s.a + st * A_STAGE), b0 = tc::smem_u32(s.b + st * B_STAGE);
 #pragma unroll
         for (int k = 0; k < BK / 16; ++k)  // 16 elements of K: 32 bytes K-major, 16 rows of 128 bytes MN-major
-          tc::mma_bf16(d, tc::sw128_desc(a0 + k * (a_mn ? 2048 : 32), a_mn ? BOX : 16),
-                       tc::sw128_desc(b0 + k * (b_mn ? 2048 : 32), b_mn ? BOX : 16), idesc,
-                       kb > w.kb0 || k ? 1u : 0u);
-        tc::mma_commit(&s.empty[st]);
+          tc::mma_16_pair(d, tc::sw128_desc(a0 + k * (a_mn ? 2048 : 32), a_mn ? BOX : 16),
+                          tc::sw128_desc(b0 + k * (b_mn ? 2048 : 32), b_mn ? BOX : 16), idesc,
+                          kb > w.kb0 || k ? 1u : 0u);
+        tc::mma_commit_pair(&s.empty[st]);
         if (++st == ST) { st = 0; ph ^= 1; }
       }
-      tc::mma_commit(&s.tfull[acc]);
+      tc::mma_commit_pair(&s.tfull[acc]);
     }
   } else if (warp >= 2) {
     const int e = warp - 2, q = warp & 3, h = e >> 2;  // TMEM lane quarter, column half
     uint8_t* stage = s.out + e * subs(M) * SUB;
     const uint32_t lane0 = tmem + ((uint32_t)(q * 32) << 16);
+    const uint32_t freed0 = tc::map_to_rank(&s.tempty[0], 0), freed1 = tc::map_to_rank(&s.tempty[1], 0);
+    // hands the accumulator back to the first CTA's MMA warp
+    auto release = [&](int acc) {
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive_cluster(acc ? freed1 : freed0);
+    };
     int it = 0;
-    for (int t = blockIdx.x; t < tiles; t += gridDim.x, ++it) {
+    for (int t = pair; t < tiles; t += pairs, ++it) {
       const Tile w = tile_at<M>(g, t);
       const int acc = it & 1;
       const uint32_t base = lane0 + acc * BN;
-      const int row = w.m0 + q * 32;  // of the warp
+      const int row = w.m0 + rank * CM + q * 32;  // of the warp
       if (M == ACT) {
         // this warp's dH into its staging tiles, once the stores of the last
         // tile have read them
@@ -240,10 +269,7 @@ __global__ void __launch_bounds__(THREADS, 1) gated_kernel(const __grid_constant
           tc::tmem_ld32(base + h * 64 + c, gate);
           tc::tmem_ld32(base + BN / 2 + h * 64 + c, up);
           tc::tmem_wait_ld();
-          if (c == 32) {
-            tc::fence_before_sync();
-            tc::mbar_arrive(&s.tempty[acc]);
-          }
+          if (c == 32) release(acc);
           with_act(g.act, [&](auto A) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -298,10 +324,7 @@ __global__ void __launch_bounds__(THREADS, 1) gated_kernel(const __grid_constant
           tc::tmem_ld32(base + h * 64 + c * 32, gate);
           tc::tmem_ld32(base + BN / 2 + h * 64 + c * 32, up);
           tc::tmem_wait_ld();
-          if (c == 1) {
-            tc::fence_before_sync();
-            tc::mbar_arrive(&s.tempty[acc]);
-          }
+          if (c == 1) release(acc);
           with_act(g.act, [&](auto A) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -357,8 +380,7 @@ __global__ void __launch_bounds__(THREADS, 1) gated_kernel(const __grid_constant
             tc::bulk_commit();
           }
         }
-        tc::fence_before_sync();
-        tc::mbar_arrive(&s.tempty[acc]);
+        release(acc);
       } else {
         float* prow = g.part + (((int64_t)w.split * 2 + w.half) * g.num_m * BM + row + lane) * ((int64_t)g.num_n * BN) +
                       w.n0 + h * (BN / 2);
@@ -371,8 +393,7 @@ __global__ void __launch_bounds__(THREADS, 1) gated_kernel(const __grid_constant
           for (int j = 0; j < 32; j += 4)
             *reinterpret_cast<uint4*>(prow + c + j) = make_uint4(v[j], v[j + 1], v[j + 2], v[j + 3]);
         }
-        tc::fence_before_sync();
-        tc::mbar_arrive(&s.tempty[acc]);
+        release(acc);
       }
     }
   }
@@ -380,9 +401,10 @@ done:
   if (warp >= 2 && lane == 0) tc::bulk_wait_all();  // stores finish before the block exits
   tc::fence_before_sync();
   __syncthreads();
+  tc::cluster_sync();  // nothing of the partner's arrives here any more
   if (warp == 1) {
     tc::fence_after_sync();
-    tc::tmem_dealloc(tmem, 2 * BN);
+    tc::tmem_dealloc_pair(tmem, 2 * BN);
   }
 }
 
@@ -439,10 +461,10 @@ DwPlan dw_plan(int64_t n, int D, int F) {
   int64_t best = -1;
   p.splits = 1;
   p.kb_per_split = (int)(kb > 0 ? kb : 1);
-  for (int64_t s = 1; s <= 152 && s * 8 <= (kb > 8 ? kb : 8); ++s) {
-    if (s > 1 && s * tiles > 4 * 152) break;  // bounds the partials
+  for (int64_t s = 1; s <= 76 && s * 8 <= (kb > 8 ? kb : 8); ++s) {
+    if (s > 1 && s * tiles > 4 * 76) break;  // bounds the partials
     const int64_t per = (kb + s - 1) / s, used = (kb + per - 1) / (per > 0 ? per : 1);
-    const int64_t rounds = (used * tiles + 151) / 152, cost = rounds * (per + 4);
+    const int64_t rounds = (used * tiles + 75) / 76, cost = rounds * (per + 4);
     if (used > 0 && (best < 0 || cost < best)) {
       best = cost;
       p.splits = (int)used;
@@ -480,8 +502,8 @@ gnn_status launch_gated(const Args& g, cudaStream_t st) {
     ready = true;
   }
   const int64_t tiles = (int64_t)g.num_m * g.num_n * (M == DW ? 2 * g.splits : 1);
-  const int grid = (int)(tiles < sm_count() ? tiles : sm_count());
-  gated_kernel<M, T><<<grid, THREADS, smem_bytes(M), st>>>(g);
+  const int pairs = (int)(tiles < sm_count() / 2 ? tiles : sm_count() / 2);
+  gated_kernel<M, T><<<2 * pairs, THREADS, smem_bytes(M), st>>>(g);
   GNN_CHECK_LAUNCH();
   return GNN_OK;
 }
@@ -511,7 +533,7 @@ gnn_status product_args(Args& g, int64_t n, int D, int F, int act, Mat X, Mat Wg
   if (!g.flags) return fail(GNN_ERR_CUDA, "device flag word unavailable");
   g.M = (int)n, g.N = F, g.K = D, g.act = act;
   g.num_m = (int)((n + BM - 1) / BM), g.num_n = (F + BN / 2 - 1) / (BN / 2), g.num_kb = (D + BK - 1) / BK;
-  GNN_TRY(map16<T>(&g.a[0], X.p, n, D, X.ld, BK, BM));
+  GNN_TRY(map16<T>(&g.a[0], X.p, n, D, X.ld, BK, CM));
   GNN_TRY(map16<T>(&g.b[0], Wg.p, D, F, Wg.ld, 64, BK));
   GNN_TRY(map16<T>(&g.b[1], Wu.p, D, F, Wu.ld, 64, BK));
   return GNN_OK;
@@ -543,12 +565,12 @@ gnn_status gated_bwd(int64_t n, int D, int F, int act, int dh_f32, Mat dH, Mat X
       Args d{};
       d.flags = g.flags;
       const int num_n = (D + BN - 1) / BN;
-      d.bn = num_n == 1 ? (int)up(D, 16) : (int)up((D + num_n - 1) / num_n, 64);
+      d.bn = (int)up((D + num_n - 1) / num_n, 64);
       d.num_m = g.num_m, d.num_n = (D + d.bn - 1) / d.bn, d.num_kb = (F + BK - 1) / BK;
-      GNN_TRY(map16<T>(&d.a[0], w.dg, n, F, w.ldf, BK, BM));
-      GNN_TRY(map16<T>(&d.a[1], w.du, n, F, w.ldf, BK, BM));
-      GNN_TRY(map16<T>(&d.b[0], Wg.p, D, F, Wg.ld, BK, d.bn));
-      GNN_TRY(map16<T>(&d.b[1], Wu.p, D, F, Wu.ld, BK, d.bn));
+      GNN_TRY(map16<T>(&d.a[0], w.dg, n, F, w.ldf, BK, CM));
+      GNN_TRY(map16<T>(&d.a[1], w.du, n, F, w.ldf, BK, CM));
+      GNN_TRY(map16<T>(&d.b[0], Wg.p, D, F, Wg.ld, BK, d.bn / 2));
+      GNN_TRY(map16<T>(&d.b[1], Wu.p, D, F, Wu.ld, BK, d.bn / 2));
       GNN_TRY(map16<T>(&d.out[0], dX.p, n, up(D, 16), dX.ld, 64, 32));
       GNN_TRY((launch_gated<DX, T>(d, st)));
     }
