@@ -233,8 +233,11 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release;" ::: "memory");
   asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
 }
+// For a barrier that hands TMEM back: the tcgen05 fences order the accesses, so
+// the arrival needs no release at cluster scope (which waits for the thread's
+// other memory accesses: the first stall of the epilogue when it had one).
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
 // A tile load into this CTA's shared memory that completes on a barrier of
 // either CTA of the pair (a shared::cluster address).
