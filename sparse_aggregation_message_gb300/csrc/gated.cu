@@ -159,6 +159,7 @@ __device__ __forceinline__ uint4* staged(uint8_t* tile, int r, int k) {
 template <Mode M, class T>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) gated_kernel(const __grid_constant__ Args g) {
   extern __shared__ uint8_t smem_raw[];
+  cudaTriggerProgrammaticLaunchCompletion();
   const Smem s = carve<M>(smem_raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
@@ -186,6 +187,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) gated_ke
   __syncthreads();
   tc::cluster_sync();  // the partner's barriers are there
   tc::fence_after_sync();
+  cudaGridDependencySynchronize();  // DX and DW read what ACT writes
   const uint32_t tmem = *s.tmem;
   const int tiles = num_tiles<M>(g);
 
@@ -414,6 +416,7 @@ template <class T>
 __global__ void __launch_bounds__(256) gated_dw_kernel(const float* part, int splits, int D, int F, int64_t ldp,
                                                        int64_t half_stride, T* dWg, int64_t ldg, T* dWu,
                                                        int64_t ldu) {
+  cudaGridDependencySynchronize();
   const int per = (F + 15) / 16 * 2;  // chunks of 8 columns
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= (int64_t)2 * D * per) return;
@@ -430,6 +433,110 @@ __global__ void __launch_bounds__(256) gated_dw_kernel(const float* part, int sp
     for (int j = 0; j < 8; ++j) acc[j] += v[j];
   }
   store_vec<8>((half ? dWu + d * ldu : dWg + d * ldg) + c, acc);
+}
+
+// H of up to NR rows without tensor cores.  A few rows read the weights once and
+// do next to nothing with them, so what counts is that every SM reads, with
+// much in flight: a block takes `cols` columns of both matrices, eight to a lane
+// (16-byte loads), cols / 8 lanes side by side; its warps and their lane rows
+// share the inner length, and a lane requests its next four rows of each matrix
+// before it multiplies the last four.  On 128 columns to a pair of CTAs as above,
+// F_mid = 1024 keeps 16 SMs busy.
+constexpr int ROW_THREADS = 256, ROW_CHUNK = 2048;
+
+template <class T, int NR>
+__global__ void __launch_bounds__(ROW_THREADS)
+    gated_rows_kernel(const T* __restrict__ X, int64_t ldx, int n, int D, const T* __restrict__ Wg, int64_t ldg,
+                      const T* __restrict__ Wu, int64_t ldu, int F, int act, T* __restrict__ H, int64_t ldh,
+                      int cols) {
+  constexpr int W = ROW_THREADS / 32, U = 4;
+  __shared__ T xs[NR][ROW_CHUNK];
+  __shared__ float red[W][NR][2][64];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int across = cols / 8, down = 32 / across;  // lanes of a row of weights, rows of a warp
+  const int c = blockIdx.x * cols + 8 * (lane % across);
+  const int k0 = warp * down + lane / across, step = W * down;
+  const bool in = c < F;  // a row of weights has its stride, so its last eight columns are there
+  float ag[NR][8] = {}, au[NR][8] = {};
+  uint4 wg[U], wu[U];
+  const T* pg = Wg + (int64_t)k0 * ldg + c;
+  const T* pu = Wu + (int64_t)k0 * ldu + c;
+  int left = in ? (D - k0 + step - 1) / step : 0;  // rows of weights not yet requested
+  auto request = [&] {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      wg[u] = wu[u] = make_uint4(0, 0, 0, 0);
+      if (u < left) {
+        wg[u] = *reinterpret_cast<const uint4*>(pg);
+        wu[u] = *reinterpret_cast<const uint4*>(pu);
+      }
+      pg += step * ldg;
+      pu += step * ldu;
+    }
+    left -= U;
+  };
+  request();
+  for (int kb = 0; kb < D; kb += ROW_CHUNK) {
+    const int len = min(ROW_CHUNK, D - kb);
+    if (kb) __syncthreads();
+    for (int i = threadIdx.x; i < NR * len; i += ROW_THREADS) {
+      const int r = i / len, k = i - r * len;
+      xs[r][k] = r < n ? X[r * ldx + kb + k] : from_f32<T>(0.f);
+    }
+    __syncthreads();
+    // a chunk holds a whole number of batches of rows, so only the last ends early
+    for (int k = k0; k < len; k += U * step) {
+      uint4 g[U], p[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) g[u] = wg[u], p[u] = wu[u];
+      request();
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (k + u * step >= len) break;
+        const uint32_t gw[4] = {g[u].x, g[u].y, g[u].z, g[u].w}, pw[4] = {p[u].x, p[u].y, p[u].z, p[u].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 gv = Pack2<T>::from(gw[j]), uv = Pack2<T>::from(pw[j]);
+#pragma unroll
+          for (int r = 0; r < NR; ++r) {
+            const float x = to_f32(xs[r][k + u * step]);
+            ag[r][2 * j] = fmaf(x, gv.x, ag[r][2 * j]);
+            ag[r][2 * j + 1] = fmaf(x, gv.y, ag[r][2 * j + 1]);
+            au[r][2 * j] = fmaf(x, uv.x, au[r][2 * j]);
+            au[r][2 * j + 1] = fmaf(x, uv.y, au[r][2 * j + 1]);
+          }
+        }
+      }
+    }
+  }
+  // over a warp's lane rows, then over the warps, in order
+#pragma unroll
+  for (int r = 0; r < NR; ++r) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      for (int o = 16; o >= across; o >>= 1) {
+        ag[r][j] += __shfl_xor_sync(0xffffffffu, ag[r][j], o);
+        au[r][j] += __shfl_xor_sync(0xffffffffu, au[r][j], o);
+      }
+      if (lane < across) {
+        red[warp][r][0][8 * lane + j] = ag[r][j];
+        red[warp][r][1][8 * lane + j] = au[r][j];
+      }
+    }
+  }
+  __syncthreads();
+  const int end = (F + 15) / 16 * 16;  // padding columns come out zero
+  for (int i = threadIdx.x; i < NR * cols; i += ROW_THREADS) {
+    const int r = i / cols, j = i % cols, col = blockIdx.x * cols + j;
+    if (r >= n || col >= end) continue;
+    float g = 0.f, u = 0.f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      g += red[w][r][0][j];
+      u += red[w][r][1][j];
+    }
+    H[r * ldh + col] = from_f32<T>(col < F ? act_f(g, act) * u : 0.f);
+  }
 }
 
 // ---------------------------------------------------------------- host side
@@ -494,8 +601,26 @@ GatedWs gated_ws(void* base, size_t cap, int64_t n, int D, int F, bool* ok) {
   return w;
 }
 
+// `after`: may start while the launch before it, one of this call's, ends.
+template <class... P, class... A>
+gnn_status launch(bool after, int grid, int block, size_t smem, cudaStream_t st, void (*k)(P...), const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3((unsigned)block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = after ? 1 : 0;
+  count_launch();
+  GNN_CUDA(cudaLaunchKernelEx(&cfg, k, args...));
+  return GNN_OK;
+}
+
 template <Mode M, class T>
-gnn_status launch_gated(const Args& g, cudaStream_t st) {
+gnn_status launch_gated(bool after, const Args& g, cudaStream_t st) {
   static bool ready = false;
   if (!ready) {
     GNN_CUDA(cudaFuncSetAttribute(gated_kernel<M, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(M)));
@@ -503,9 +628,7 @@ gnn_status launch_gated(const Args& g, cudaStream_t st) {
   }
   const int64_t tiles = (int64_t)g.num_m * g.num_n * (M == DW ? 2 * g.splits : 1);
   const int pairs = (int)(tiles < sm_count() / 2 ? tiles : sm_count() / 2);
-  gated_kernel<M, T><<<2 * pairs, THREADS, smem_bytes(M), st>>>(g);
-  GNN_CHECK_LAUNCH();
-  return GNN_OK;
+  return launch(after, 2 * pairs, THREADS, smem_bytes(M), st, gated_kernel<M, T>, g);
 }
 
 // A map of a 2-byte matrix of `cols` used columns.
@@ -539,12 +662,30 @@ gnn_status product_args(Args& g, int64_t n, int D, int F, int act, Mat X, Mat Wg
   return GNN_OK;
 }
 
+template <class T, int NR>
+gnn_status launch_rows(int n, int D, int F, int act, Mat X, Mat Wg, Mat Wu, Mat H, cudaStream_t st) {
+  // as many columns to a block as leave every SM two: wide rows of weights are
+  // read in longer pieces
+  int cols = 64;
+  while (cols > 16 && (F + cols - 1) / cols < 2 * 152) cols /= 2;
+  const int grid = (int)((up(F, 16) + cols - 1) / cols);
+  gated_rows_kernel<T, NR><<<grid, ROW_THREADS, 0, st>>>(
+      static_cast<const T*>(X.p), X.ld, n, D, static_cast<const T*>(Wg.p), Wg.ld, static_cast<const T*>(Wu.p), Wu.ld, F,
+      act, static_cast<T*>(H.p), H.ld, cols);
+  GNN_CHECK_LAUNCH();
+  return GNN_OK;
+}
+
 template <class T>
 gnn_status gated_fwd(int64_t n, int D, int F, int act, Mat X, Mat Wg, Mat Wu, Mat H, cudaStream_t st) {
+  // One or two rows (measured in us at 1024 x 4096, rows against tensor cores:
+  // 1 row 6.8 / 10.4, 2 rows 8.0 / 10.5, 4 rows 18.4 / 10.7).
+  if (n == 1) return launch_rows<T, 1>((int)n, D, F, act, X, Wg, Wu, H, st);
+  if (n == 2) return launch_rows<T, 2>((int)n, D, F, act, X, Wg, Wu, H, st);
   Args g{};
   GNN_TRY(product_args<T>(g, n, D, F, act, X, Wg, Wu));
   GNN_TRY(map16<T>(&g.out[0], H.p, n, up(F, 16), H.ld, 64, 32));
-  return launch_gated<FWD, T>(g, st);
+  return launch_gated<FWD, T>(false, g, st);
 }
 
 template <class T>
@@ -560,7 +701,7 @@ gnn_status gated_bwd(int64_t n, int D, int F, int act, int dh_f32, Mat dH, Mat X
       GNN_TRY(map16<T>(&g.dh, dH.p, n, F, dH.ld, 64, 32));
     GNN_TRY(map16<T>(&g.out[0], w.dg, n, F, w.ldf, 64, 32));
     GNN_TRY(map16<T>(&g.out[1], w.du, n, F, w.ldf, 64, 32));
-    GNN_TRY((launch_gated<ACT, T>(g, st)));
+    GNN_TRY((launch_gated<ACT, T>(false, g, st)));
     if (dX.p) {
       Args d{};
       d.flags = g.flags;
@@ -572,7 +713,7 @@ gnn_status gated_bwd(int64_t n, int D, int F, int act, int dh_f32, Mat dH, Mat X
       GNN_TRY(map16<T>(&d.b[0], Wg.p, D, F, Wg.ld, BK, d.bn / 2));
       GNN_TRY(map16<T>(&d.b[1], Wu.p, D, F, Wu.ld, BK, d.bn / 2));
       GNN_TRY(map16<T>(&d.out[0], dX.p, n, up(D, 16), dX.ld, 64, 32));
-      GNN_TRY((launch_gated<DX, T>(d, st)));
+      GNN_TRY((launch_gated<DX, T>(true, d, st)));
     }
   }
   if (dWg.p) {
@@ -586,13 +727,11 @@ gnn_status gated_bwd(int64_t n, int D, int F, int act, int dh_f32, Mat dH, Mat X
       GNN_TRY(map16<T>(&d.a[0], X.p, n, D, X.ld, 64, BK));
       GNN_TRY(map16<T>(&d.b[0], w.dg, n, F, w.ldf, 64, BK));
       GNN_TRY(map16<T>(&d.b[1], w.du, n, F, w.ldf, 64, BK));
-      GNN_TRY((launch_gated<DW, T>(d, st)));
+      GNN_TRY((launch_gated<DW, T>(true, d, st)));
     }
     const int64_t work = 2ll * D * (up(F, 16) / 8), ldp = (int64_t)p.num_n * BN;
-    gated_dw_kernel<T><<<(unsigned)((work + 255) / 256), 256, 0, st>>>(
-        w.part, splits, D, F, ldp, (int64_t)p.num_m * BM * ldp, static_cast<T*>(dWg.p), dWg.ld,
-        static_cast<T*>(dWu.p), dWu.ld);
-    GNN_CHECK_LAUNCH();
+    GNN_TRY(launch(n > 0, (int)((work + 255) / 256), 256, 0, st, gated_dw_kernel<T>, (const float*)w.part, splits, D, F,
+                   ldp, (int64_t)p.num_m * BM * ldp, static_cast<T*>(dWg.p), dWg.ld, static_cast<T*>(dWu.p), dWu.ld));
   }
   return GNN_OK;
 }

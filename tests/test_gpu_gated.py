@@ -80,6 +80,13 @@ def test_forward(n, D, F, act, t):
     assert torch.all(buf[:, F:pad] == 0) and torch.all(torch.isnan(buf[:, pad:]))
 
 
+@pytest.mark.parametrize("n,D,F", [(1, 2048, 40), (2, 2049, 33), (1, 5000, 700), (2, 4100, 10016), (3, 2049, 33), (1, 7, 1)])
+@pytest.mark.parametrize("t", ["bf16", "f16"])
+def test_few_rows(n, D, F, t):
+    """One and two rows take their own kernel: long inner lengths, every width of its blocks."""
+    test_forward(n, D, F, "silu", t)
+
+
 @pytest.mark.parametrize("n,D,F", CASES)
 @pytest.mark.parametrize("act,t,f32", [("silu", "bf16", False), ("gelu", "f16", True), ("relu", "bf16", True),
                                        ("sigmoid", "f16", False), ("none", "bf16", False)])
