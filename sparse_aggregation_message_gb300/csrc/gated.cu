@@ -156,6 +156,10 @@ __device__ __forceinline__ uint4* staged(uint8_t* tile, int r, int k) {
   return reinterpret_cast<uint4*>(tile + r * 128 + ((k ^ (r & 7)) << 4));
 }
 
+__device__ __forceinline__ float2 pair_at(const uint32_t* v, int i) {
+  return make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+}
+
 template <Mode M, class T>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) gated_kernel(const __grid_constant__ Args g) {
   extern __shared__ uint8_t smem_raw[];
@@ -279,8 +283,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) gated_ke
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
                 const int i = 8 * k + 2 * j;
-                o[j] = Pack2<T>::to(act_f(__uint_as_float(gate[i]), A) * __uint_as_float(up[i]),
-                                    act_f(__uint_as_float(gate[i + 1]), A) * __uint_as_float(up[i + 1]));
+                const float2 v = mul2_rn(act2(pair_at(gate, i), A), pair_at(up, i));
+                o[j] = Pack2<T>::to(v.x, v.y);
               }
               *staged(stage, lane, (c >> 3) + k) = make_uint4(o[0], o[1], o[2], o[3]);
             }
@@ -333,17 +337,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) gated_ke
               uint32_t og[4], ou[4];
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
-                float x[2], y[2];
-#pragma unroll
-                for (int z = 0; z < 2; ++z) {
-                  const int i = 8 * k + 2 * j + z;
-                  float a, d;
-                  act_grad_f(__uint_as_float(gate[i]), A, a, d);
-                  x[z] = dh[c][i] * __uint_as_float(up[i]) * d;
-                  y[z] = dh[c][i] * a;
-                }
-                og[j] = Pack2<T>::to(x[0], x[1]);
-                ou[j] = Pack2<T>::to(y[0], y[1]);
+                const int i = 8 * k + 2 * j;
+                const float2 d2 = make_float2(dh[c][i], dh[c][i + 1]);
+                float2 a, d;
+                act_grad2(pair_at(gate, i), A, a, d);
+                const float2 x = mul2_rn(mul2_rn(d2, pair_at(up, i)), d), y = mul2_rn(d2, a);
+                og[j] = Pack2<T>::to(x.x, x.y);
+                ou[j] = Pack2<T>::to(y.x, y.y);
               }
               *staged(stage, lane, c * 4 + k) = make_uint4(og[0], og[1], og[2], og[3]);
               *staged(stage + SUB, lane, c * 4 + k) = make_uint4(ou[0], ou[1], ou[2], ou[3]);

@@ -9,6 +9,7 @@
 
 #include <type_traits>
 
+#include "device.cuh"
 #include "gnnagg.h"
 
 namespace gnn {
@@ -111,66 +112,77 @@ __device__ __forceinline__ float rcp_f(float x) {
 
 constexpr float kLog2e = 1.4426950408889634f;
 
-// 1 / (1 + exp(-z)): exp(-z) may reach infinity, whose reciprocal is zero.
-__device__ __forceinline__ float sigmoid_f(float z) { return rcp_f(1.f + ex2_f(-kLog2e * z)); }
+__device__ __forceinline__ float2 neg2(float2 a) { return make_float2(-a.x, -a.y); }
+__device__ __forceinline__ float2 ex2_2(float2 x) { return make_float2(ex2_f(x.x), ex2_f(x.y)); }
+__device__ __forceinline__ float2 rcp_2(float2 x) { return make_float2(rcp_f(x.x), rcp_f(x.y)); }
 
-// The normal distribution's Phi(z) and exp(-z^2/2).  With x = |z|/sqrt 2,
+// The activations work on pairs, two operations to an instruction: the kernels
+// that use them run short of instructions before bandwidth.
+
+// 1 / (1 + exp(-z)): exp(-z) may reach infinity, whose reciprocal is zero.
+__device__ __forceinline__ float2 sigmoid2(float2 z) {
+  return rcp_2(add2_rn(ex2_2(mul2_rn(z, dup2(-kLog2e))), dup2(1.f)));
+}
+
+// The normal distribution's Phi(z) and e = exp(-z^2/2).  With x = |z|/sqrt 2,
 // erfc(x) = t P(t) exp(-x^2), t = 1/(1 + 0.3275911 x): Abramowitz and Stegun
-// 7.1.26, absolute error at most 1.5e-7, so at most 7.5e-8 in Phi.  It shares
-// its exponential with the derivative of gelu.
-__device__ __forceinline__ float phi_f(float z, float& e) {
-  const float x = fabsf(z);
-  e = ex2_f((-0.5f * kLog2e) * z * z);
-  const float t = rcp_f(fmaf(0.3275911f * 0.70710678118654752f, x, 1.f));
-  float q = fmaf(1.061405429f, t, -1.453152027f);
-  q = fmaf(q, t, 1.421413741f);
-  q = fmaf(q, t, -0.284496736f);
-  q = fmaf(q, t, 0.254829592f);
-  q = 0.5f * t * q * e;
-  return z >= 0.f ? 1.f - q : q;
+// 7.1.26, absolute error at most 1.5e-7, so at most 7.5e-8 in q = erfc(x)/2;
+// Phi = 1/2 + sign(z) (1/2 - q).  It shares its exponential with the derivative
+// of gelu.
+__device__ __forceinline__ float2 phi2(float2 z, float2& e) {
+  e = ex2_2(mul2_rn(mul2_rn(z, dup2(-0.5f * kLog2e)), z));
+  const float2 x = make_float2(fabsf(z.x), fabsf(z.y));
+  const float2 t = rcp_2(fma2_rn(dup2(0.3275911f * 0.70710678118654752f), x, dup2(1.f)));
+  float2 q = fma2_rn(dup2(0.5f * 1.061405429f), t, dup2(0.5f * -1.453152027f));
+  q = fma2_rn(q, t, dup2(0.5f * 1.421413741f));
+  q = fma2_rn(q, t, dup2(0.5f * -0.284496736f));
+  q = fma2_rn(q, t, dup2(0.5f * 0.254829592f));
+  const float2 r = fma2_rn(neg2(mul2_rn(t, q)), e, dup2(0.5f));
+  return add2_rn(make_float2(copysignf(r.x, z.x), copysignf(r.y, z.y)), dup2(0.5f));
 }
 
 // act(z); `act` is the same for a whole launch, so the branch is uniform.
-__device__ __forceinline__ float act_f(float z, int act) {
+__device__ __forceinline__ float2 act2(float2 z, int act) {
   switch (act) {
-    case GNN_ACT_RELU: return z > 0.f ? z : (z != z ? z : 0.f);
-    case GNN_ACT_SILU: return z * sigmoid_f(z);
+    case GNN_ACT_RELU: return make_float2(z.x < 0.f ? 0.f : z.x, z.y < 0.f ? 0.f : z.y);  // keeps a NaN
+    case GNN_ACT_SILU: return mul2_rn(z, sigmoid2(z));
     case GNN_ACT_GELU: {
-      float e;
-      return z * phi_f(z, e);
+      float2 e;
+      return mul2_rn(z, phi2(z, e));
     }
-    case GNN_ACT_SIGMOID: return sigmoid_f(z);
+    case GNN_ACT_SIGMOID: return sigmoid2(z);
     default: return z;
   }
 }
+__device__ __forceinline__ float act_f(float z, int act) { return act2(make_float2(z, z), act).x; }
 
 // act(z) and act'(z).
-__device__ __forceinline__ void act_grad_f(float z, int act, float& a, float& d) {
+__device__ __forceinline__ void act_grad2(float2 z, int act, float2& a, float2& d) {
   switch (act) {
     case GNN_ACT_RELU:
-      d = z > 0.f ? 1.f : 0.f;
-      a = z > 0.f ? z : (z != z ? z : 0.f);
+      d = make_float2(z.x > 0.f ? 1.f : 0.f, z.y > 0.f ? 1.f : 0.f);
+      a = act2(z, GNN_ACT_RELU);
       break;
     case GNN_ACT_SILU: {
-      const float s = sigmoid_f(z);
-      a = z * s;
-      d = fmaf(a, 1.f - s, s);
+      const float2 s = sigmoid2(z);
+      a = mul2_rn(z, s);
+      d = fma2_rn(a, fma2_rn(s, dup2(-1.f), dup2(1.f)), s);
       break;
     }
     case GNN_ACT_GELU: {
-      float e;
-      const float c = phi_f(z, e);
-      a = z * c;
-      d = fmaf(z * 0.39894228040143268f, e, c);
+      float2 e;
+      const float2 c = phi2(z, e);
+      a = mul2_rn(z, c);
+      d = fma2_rn(mul2_rn(z, dup2(0.39894228040143268f)), e, c);
       break;
     }
     case GNN_ACT_SIGMOID:
-      a = sigmoid_f(z);
-      d = a * (1.f - a);
+      a = sigmoid2(z);
+      d = fma2_rn(neg2(a), a, a);
       break;
     default:
       a = z;
-      d = 1.f;
+      d = dup2(1.f);
   }
 }
 

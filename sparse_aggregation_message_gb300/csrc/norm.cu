@@ -17,11 +17,10 @@ namespace gnn {
 
 namespace {
 
-// A block holds as many rows of CH chunks side by side as fit 192 threads, at
-// least one (at most 256 threads then).  Small blocks: segments of a batch
-// are small, a block takes one at a time, and more blocks have more of them
-// in flight.
-constexpr int MAX_THREADS = 256, AIM_THREADS = 192;
+// A block holds as many rows of CH chunks side by side as fit its threads, at
+// least one: few threads are idle whatever a row's width (256 threads left 41% of
+// them idle at 602 fp32 channels).
+constexpr int block_threads(int V) { return V == 4 ? 384 : 192; }
 constexpr int FIN_THREADS = 512;
 
 struct NormArgs {
@@ -29,11 +28,12 @@ struct NormArgs {
   const void* dY;
   void* out;  // Y or dX
   int64_t ldx, ldy, ldo;
-  int64_t n;
+  int n;
   int C, groups, cg, n_seg, act;
   int CH;  // chunks of V channels a row has, padding columns of the output included
   int RP;  // rows a block holds side by side: RP * CH threads take part
-  int64_t R;
+  int R;
+  int longest;  // rows of a short segment
   int tiles;
   const int64_t* seg;  // may be NULL: one segment
   const float* gamma;
@@ -43,25 +43,32 @@ struct NormArgs {
   float* rstd;
   float2* part;  // forward: (mean, M2) of a piece's group; backward: the two sums
   float2* joined;  // backward: the two sums over a long segment's group, / m
-  float* dpart;    // backward: [tiles][2][C] sums of dz and dz xh
+  float* dpart;    // backward: [blocks][2][C] sums of dz and dz xh
+  int blocks;        // of the launch that walks the tiles
+  int apply_blocks;  // of the last launch
+  int* has_long;   // [tiles]: whether pieces of long segments are left for the last launch
   float* dgamma;
   float* dbeta;
   unsigned* flags;
 };
 
-__device__ __forceinline__ int64_t seg_at(const NormArgs& a, int s) {
-  return a.seg ? a.seg[s] : (s ? a.n : 0);
+// A border, brought into [0, n] whatever seg_start holds.
+__device__ __forceinline__ int seg_at(const NormArgs& a, int s) {
+  if (!a.seg) return s ? a.n : 0;
+  return (int)min(max(a.seg[s], (int64_t)0), (int64_t)a.n);
 }
-// The segment that holds row r: the last one that starts at or before it.
-__device__ __forceinline__ int seg_of(const NormArgs& a, int64_t r) {
+// The segment that holds row r: the last one that starts at or before it.  A
+// whole warp searches, 32 borders to a step: a step is a trip to L2, and a
+// bisection's dozen of them took longer than a small batch's rows.
+__device__ __forceinline__ int seg_of(const NormArgs& a, int r) {
   if (!a.seg) return 0;
   int lo = 0, hi = a.n_seg;  // seg[lo] <= r < seg[hi]
   while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (a.seg[mid] <= r)
-      lo = mid;
-    else
-      hi = mid;
+    const int step = (hi - lo - 1 + 31) / 32, probe = lo + 1 + (int)(threadIdx.x & 31) * step;
+    const int below = __popc(__ballot_sync(0xffffffffu, probe < hi && a.seg[probe < hi ? probe : lo] <= r));
+    const int first = lo + 1 + below * step;  // the first probe past r
+    hi = min(hi, first);
+    if (below) lo = first - step;
   }
   return lo;
 }
@@ -80,17 +87,17 @@ __device__ __forceinline__ float warp_sum(float v) {
 // `whole` true for a short segment taken from its first row to its last.
 template <class Fn>
 __device__ __forceinline__ void for_pieces(const NormArgs& a, int t, Fn f) {
-  const int64_t r0 = (int64_t)t * a.R, r1 = min(a.n, r0 + a.R);
+  const int r0 = t * a.R, r1 = min((int64_t)a.n, (int64_t)r0 + a.R);
   int s = seg_of(a, r0);
-  int64_t row = r0;
+  int row = r0;
   while (row < r1 && s < a.n_seg) {
-    const int64_t sb = seg_at(a, s), se = min(seg_at(a, s + 1), a.n);
+    const int sb = seg_at(a, s), se = seg_at(a, s + 1);
     if (se <= row) {  // empty (or not ascending, which the join launch flags)
       ++s;
       continue;
     }
-    if (sb < 0 || sb > row) break;
-    if (se - sb <= 2 * a.R) {
+    if (sb > row) break;
+    if (se - sb <= a.longest) {
       if (sb >= r0) f(s, sb, se, true);
     } else {
       f(s, row, min(se, r1), false);
@@ -115,8 +122,8 @@ struct Place {
     for (int k = 0; k < V; ++k) g[k] = min(c0 + k, a.C - 1) / a.cg;
   }
   // how many rows of [ra, rb) are this thread's
-  __device__ __forceinline__ int rows(const NormArgs& a, int64_t ra, int64_t rb) const {
-    return on ? (int)((rb - ra - ro + a.RP - 1) / a.RP) : 0;
+  __device__ __forceinline__ int rows(const NormArgs& a, int ra, int rb) const {
+    return on ? (unsigned)(rb - ra - ro + a.RP - 1) / (unsigned)a.RP : 0;
   }
 };
 
@@ -137,13 +144,16 @@ template <int V, class T>
 __device__ __forceinline__ void load_shared(uint32_t at, float (&v)[V]) {
   constexpr int W = V * sizeof(T) / 4;
   uint32_t w[W];
-  if constexpr (W == 4)
-    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                 : "r"(at)
-                 : "memory");
-  else
+  if constexpr (W == 2) {
     asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(at) : "memory");
+  } else {
+#pragma unroll
+    for (int i = 0; i < W; i += 4)
+      asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3])
+                   : "r"(at + 4 * i)
+                   : "memory");
+  }
 #pragma unroll
   for (int i = 0; i < W; ++i) {
     if constexpr (sizeof(T) == 4) {
@@ -153,6 +163,14 @@ __device__ __forceinline__ void load_shared(uint32_t at, float (&v)[V]) {
       v[2 * i] = f.x, v[2 * i + 1] = f.y;
     }
   }
+}
+template <int V>
+__device__ __forceinline__ void store_shared(uint32_t at, const float (&v)[V]) {
+#pragma unroll
+  for (int i = 0; i < V; i += 4)
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + 4 * i), "f"(v[i]), "f"(v[i + 1]), "f"(v[i + 2]),
+                 "f"(v[i + 3])
+                 : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -206,7 +224,17 @@ __device__ __forceinline__ void stream_rows(char* ring, int rows, const TA* pa, 
   }
   copy_wait<0>();
 }
-constexpr int FWD_DEPTH = 4, BWD_DEPTH = 3;
+constexpr int FWD_DEPTH = 4, BWD_DEPTH = 2;
+
+// Zero in the columns of the thread that are past C.
+template <int V>
+__device__ __forceinline__ void clear_padding(const Place<V>& p, int C, float (&v)[V]) {
+  if (p.c0 + V > C) {
+#pragma unroll
+    for (int k = 0; k < V; ++k)
+      if (p.c0 + k >= C) v[k] = 0.f;
+  }
+}
 
 // One fp32 value per channel of the thread (the fill where src is NULL).
 template <int V>
@@ -260,7 +288,7 @@ __device__ __forceinline__ void block_sums(const NormArgs& a, int width, const f
 // Y of the rows [ra, rb) from per-group (mean, rstd), last rows first: those
 // are the ones the statistics pass read last and the caches still hold.
 template <class TX, class TY, int V>
-__device__ __forceinline__ void fwd_rows(const NormArgs& a, const Place<V>& p, int64_t ra, int64_t rb,
+__device__ __forceinline__ void fwd_rows(const NormArgs& a, const Place<V>& p, int ra, int rb,
                                          const float* gmean, const float* grstd, char* ring) {
   const int rows = p.rows(a, ra, rb);
   float mu[V], sc[V], bt[V];
@@ -271,7 +299,7 @@ __device__ __forceinline__ void fwd_rows(const NormArgs& a, const Place<V>& p, i
     mu[k] = gmean[p.g[k]];
     sc[k] *= grstd[p.g[k]];
   }
-  const int64_t last = ra + p.ro + (int64_t)(rows - 1) * a.RP;
+  const int64_t last = ra + p.ro + (rows - 1) * a.RP;
   const TX* X = static_cast<const TX*>(a.X) + last * a.ldx + p.c0;
   TY* Y = static_cast<TY*>(a.out) + last * a.ldo + p.c0;
   const int64_t dx = (int64_t)a.RP * a.ldx, dy = (int64_t)a.RP * a.ldo;
@@ -284,7 +312,12 @@ __device__ __forceinline__ void fwd_rows(const NormArgs& a, const Place<V>& p, i
     stream_rows<V, FWD_DEPTH, false>(ring, rows, X, -dx, X, 0, [&](float (&x)[V], float (&)[V]) {
       float y[V];
 #pragma unroll
-      for (int k = 0; k < V; ++k) y[k] = p.c0 + k < a.C ? act_f((x[k] - mu[k]) * sc[k] + bt[k], act) : 0.f;
+      for (int k = 0; k < V; k += 2) {
+        const float2 d = add2_rn(make_float2(x[k], x[k + 1]), make_float2(-mu[k], -mu[k + 1]));
+        const float2 v = act2(fma2_rn(d, make_float2(sc[k], sc[k + 1]), make_float2(bt[k], bt[k + 1])), act);
+        y[k] = v.x, y[k + 1] = v.y;
+      }
+      clear_padding<V>(p, a.C, y);
       store_vec<V>(Y, y);
       Y -= dy;
     });
@@ -295,7 +328,7 @@ __device__ __forceinline__ void fwd_rows(const NormArgs& a, const Place<V>& p, i
 // output.  A group's sums are formed about its value in the piece's first row,
 // so a mean far from zero does not cancel in E[x^2] - mean^2.
 template <class TX, class TY, int V>
-__global__ void __launch_bounds__(MAX_THREADS, 3) norm_fwd_stats_kernel(NormArgs a, int L) {
+__global__ void __launch_bounds__(block_threads(V), V == 4 ? 2 : 4) norm_fwd_stats_kernel(NormArgs a, int L) {
   extern __shared__ float sm[];
   cudaTriggerProgrammaticLaunchCompletion();
   const Place<V> p(a);
@@ -308,8 +341,10 @@ __global__ void __launch_bounds__(MAX_THREADS, 3) norm_fwd_stats_kernel(NormArgs
   float* gr = gm + a.groups;
   char* ring = reinterpret_cast<char*>(align16(gr + a.groups));
   const TX* X = static_cast<const TX*>(a.X);
-  const int t = blockIdx.x;
-  for_pieces(a, t, [&](int s, int64_t ra, int64_t rb, bool whole) {
+  for (int t = blockIdx.x; t < a.tiles; t += gridDim.x) {
+  int left = 0;  // pieces of long segments
+  for_pieces(a, t, [&](int s, int ra, int rb, bool whole) {
+    left |= !whole;
     if (p.on) {
       constexpr int U = 32 / V;
       float piv[V], S[V], Q[V];
@@ -344,13 +379,13 @@ __global__ void __launch_bounds__(MAX_THREADS, 3) norm_fwd_stats_kernel(NormArgs
       store_vec<V>(red1 + p.ro * width + p.c0, S);
       store_vec<V>(red2 + p.ro * width + p.c0, Q);
     }
-    const float m = (float)(rb - ra) * (float)a.cg;
+    const float inv = rcp_f((float)(rb - ra) * (float)a.cg);  // 1 / values of a group
     block_sums(a, width, red1, red2, ch1, ch2, nullptr, L, [&](int g, float S, float Q) {
-      const float d = S / m;
+      const float d = S * inv;
       const float mean = to_f32(X[ra * a.ldx + (int64_t)g * a.cg]) + d;
       const float m2 = fmaxf(Q - S * d, 0.f) + 0.f * Q;  // the product keeps a NaN
       if (whole) {
-        const float rstd = rsqrtf(m2 / m + a.eps);
+        const float rstd = rsqrtf(m2 * inv + a.eps);
         gm[g] = mean;
         gr[g] = rstd;
         a.mean[(int64_t)s * a.groups + g] = mean;
@@ -364,13 +399,15 @@ __global__ void __launch_bounds__(MAX_THREADS, 3) norm_fwd_stats_kernel(NormArgs
       __syncthreads();  // gm, gr and the partials are written again
     }
   });
+  if (threadIdx.x == 0) a.has_long[t] = left;
+  }
 }
 
 // Segments without rows, and what seg_start has to be.
 __device__ __forceinline__ void check_segments(const NormArgs& a, int blocks, bool fill) {
   const int64_t stride = (int64_t)blocks * blockDim.x;
   for (int64_t s = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; s < a.n_seg; s += stride) {
-    const int64_t sb = seg_at(a, (int)s), se = seg_at(a, (int)s + 1);
+    const int64_t sb = a.seg ? a.seg[s] : 0, se = a.seg ? a.seg[s + 1] : a.n;
     if (sb > se || (s == 0 && sb != 0) || (s == a.n_seg - 1 && se != a.n)) atomicOr(a.flags, 1u);
     if (fill && se <= sb) {
       for (int g = 0; g < a.groups; ++g) {
@@ -386,8 +423,8 @@ __device__ __forceinline__ void check_segments(const NormArgs& a, int blocks, bo
 template <class Fn>
 __device__ __forceinline__ void for_long(const NormArgs& a, int blocks, Fn f) {
   for (int s = blockIdx.x; s < a.n_seg; s += blocks) {
-    const int64_t sb = seg_at(a, s), se = min(seg_at(a, s + 1), a.n);
-    if (sb >= 0 && se - sb > 2 * a.R) f(s, sb, se, (int)(sb / a.R), (int)((se - 1) / a.R));
+    const int sb = seg_at(a, s), se = seg_at(a, s + 1);
+    if (se - sb > a.longest) f(s, sb, se, sb / a.R, (se - 1) / a.R);
   }
 }
 
@@ -398,7 +435,7 @@ __global__ void __launch_bounds__(FIN_THREADS) norm_fwd_join_kernel(NormArgs a) 
   cudaGridDependencySynchronize();
   check_segments(a, gridDim.x, true);
   const int lane = threadIdx.x & 31;
-  for_long(a, gridDim.x, [&](int s, int64_t sb, int64_t se, int t0, int t1) {
+  for_long(a, gridDim.x, [&](int s, int sb, int se, int t0, int t1) {
     for (int g = threadIdx.x >> 5; g < a.groups; g += FIN_THREADS / 32) {
       const float2* part = a.part + (int64_t)s * a.groups + g;
       const float first = part[(int64_t)t0 * a.groups].x;
@@ -406,7 +443,7 @@ __global__ void __launch_bounds__(FIN_THREADS) norm_fwd_join_kernel(NormArgs a) 
 #pragma unroll 4
       for (int i = t0 + lane; i <= t1; i += 32) {
         const float2 v = part[(int64_t)i * a.groups];
-        const float m = (float)(min(se, (i + 1) * a.R) - max(sb, i * a.R)) * (float)a.cg;
+        const float m = (float)((int)min((int64_t)se, (i + 1) * (int64_t)a.R) - max(sb, i * a.R)) * (float)a.cg;
         const float d = v.x - first;
         M += m;
         S += m * d;
@@ -423,56 +460,88 @@ __global__ void __launch_bounds__(FIN_THREADS) norm_fwd_join_kernel(NormArgs a) 
 }
 
 template <class TX, class TY, int V>
-__global__ void __launch_bounds__(MAX_THREADS, 3) norm_fwd_apply_kernel(NormArgs a) {
+__global__ void __launch_bounds__(block_threads(V), V == 4 ? 2 : 4) norm_fwd_apply_kernel(NormArgs a) {
   extern __shared__ float sm[];
-  cudaGridDependencySynchronize();
   const Place<V> p(a);
+  cudaGridDependencySynchronize();
   // last tiles first, as within a tile
-  for_pieces(a, gridDim.x - 1 - blockIdx.x, [&](int s, int64_t ra, int64_t rb, bool whole) {
+  for (int t = a.tiles - 1 - (int)blockIdx.x; t >= 0; t -= gridDim.x) {
+  if (!a.has_long[t]) continue;
+  for_pieces(a, t, [&](int s, int ra, int rb, bool whole) {
     if (!whole)
       fwd_rows<TX, TY, V>(a, p, ra, rb, a.mean + (int64_t)s * a.groups, a.rstd + (int64_t)s * a.groups,
                              reinterpret_cast<char*>(sm));
   });
+  }
 }
 
 // ------------------------------------------------------------------ backward
-// The values a thread needs of its channels in one segment.
+// gamma and beta of a thread's channels, and one segment's statistics of them.
 template <int V>
 struct BwdChannels {
   float mu[V], rs[V], ga[V], be[V];
-  __device__ __forceinline__ BwdChannels(const NormArgs& a, const Place<V>& p, int s) {
+  __device__ __forceinline__ BwdChannels(const NormArgs& a, const Place<V>& p) {
     load_channels<V>(a.gamma, p, a.C, 1.f, ga);
     load_channels<V>(a.beta, p, a.C, 0.f, be);
+  }
+  __device__ __forceinline__ void segment(const NormArgs& a, const Place<V>& p, int s) {
 #pragma unroll
     for (int k = 0; k < V; ++k) {
       mu[k] = a.mean[(int64_t)s * a.groups + p.g[k]];
       rs[k] = a.rstd[(int64_t)s * a.groups + p.g[k]];
     }
   }
-  // dz of channel k, and its xh
+  // x becomes xh and dy becomes dz
   template <class Act>
-  __device__ __forceinline__ float dz(int k, float x, float dy, Act act, float& xh) const {
-    xh = (x - mu[k]) * rs[k];
-    float av, d;
-    act_grad_f(ga[k] * xh + be[k], act, av, d);
-    return dy * d;
+  __device__ __forceinline__ void derive(float (&x)[V], float (&dy)[V], Act act) const {
+#pragma unroll
+    for (int k = 0; k < V; k += 2) {
+      const float2 xh = mul2_rn(add2_rn(make_float2(x[k], x[k + 1]), make_float2(-mu[k], -mu[k + 1])),
+                                make_float2(rs[k], rs[k + 1]));
+      float2 av, d;
+      act_grad2(fma2_rn(make_float2(ga[k], ga[k + 1]), xh, make_float2(be[k], be[k + 1])), act, av, d);
+      d = mul2_rn(make_float2(dy[k], dy[k + 1]), d);
+      x[k] = xh.x, x[k + 1] = xh.y, dy[k] = d.x, dy[k + 1] = d.y;
+    }
+  }
+  // rs (gamma dz - A - xh B)
+  __device__ __forceinline__ void output(const float (&xh)[V], const float (&dz)[V], const float (&A)[V],
+                                         const float (&B)[V], float (&o)[V]) const {
+#pragma unroll
+    for (int k = 0; k < V; k += 2) {
+      float2 v = fma2_rn(make_float2(ga[k], ga[k + 1]), make_float2(dz[k], dz[k + 1]), make_float2(-A[k], -A[k + 1]));
+      v = fma2_rn(make_float2(-xh[k], -xh[k + 1]), make_float2(B[k], B[k + 1]), v);
+      v = mul2_rn(v, make_float2(rs[k], rs[k + 1]));
+      o[k] = v.x, o[k + 1] = v.y;
+    }
   }
 };
 
+// P1 += dz, P2 += dz xh
+template <int V>
+__device__ __forceinline__ void add_sums(const float (&xh)[V], const float (&dz)[V], float (&P1)[V], float (&P2)[V]) {
+#pragma unroll
+  for (int k = 0; k < V; k += 2) {
+    const float2 z = make_float2(dz[k], dz[k + 1]);
+    const float2 s = add2_rn(make_float2(P1[k], P1[k + 1]), z);
+    const float2 q = fma2_rn(z, make_float2(xh[k], xh[k + 1]), make_float2(P2[k], P2[k + 1]));
+    P1[k] = s.x, P1[k + 1] = s.y, P2[k] = q.x, P2[k + 1] = q.y;
+  }
+}
+
 // dX of the rows [ra, rb); gA, gB: the segment's two sums over each group, / m.
 template <class TX, class TY, int V>
-__device__ __forceinline__ void bwd_rows(const NormArgs& a, const Place<V>& p, int s, int64_t ra,
-                                         int64_t rb, const float* gA, const float* gB, int gstride,
+__device__ __forceinline__ void bwd_rows(const NormArgs& a, const Place<V>& p, const BwdChannels<V>& b,
+                                         int ra, int rb, const float* gA, const float* gB, int gstride,
                                          char* ring) {
   const int rows = p.rows(a, ra, rb);
-  const BwdChannels<V> b(a, p, s);
   float A[V], B[V];
 #pragma unroll
   for (int k = 0; k < V; ++k) {
     A[k] = gA[p.g[k] * gstride];
     B[k] = gB[p.g[k] * gstride];
   }
-  const int64_t last = ra + p.ro + (int64_t)(rows - 1) * a.RP;
+  const int64_t last = ra + p.ro + (rows - 1) * a.RP;
   const TX* X = static_cast<const TX*>(a.X) + last * a.ldx + p.c0;
   const TY* dY = static_cast<const TY*>(a.dY) + last * a.ldy + p.c0;
   TX* dX = static_cast<TX*>(a.out) + last * a.ldo + p.c0;
@@ -485,20 +554,25 @@ __device__ __forceinline__ void bwd_rows(const NormArgs& a, const Place<V>& p, i
   with_act(a.act, [&](auto act) {
     stream_rows<V, BWD_DEPTH, true>(ring, rows, X, -sx, dY, -sy, [&](float (&x)[V], float (&dy)[V]) {
       float o[V];
-#pragma unroll
-      for (int k = 0; k < V; ++k) {
-        float xh;
-        const float dz = b.dz(k, x[k], dy[k], act, xh);
-        o[k] = p.c0 + k < a.C ? b.rs[k] * (b.ga[k] * dz - A[k] - xh * B[k]) : 0.f;
-      }
+      b.derive(x, dy, act);
+      b.output(x, dy, A, B, o);
+      clear_padding<V>(p, a.C, o);
       store_vec<V>(dX, o);
       dX -= so;
     });
   });
 }
 
+// Rows of a thread that a short segment may have to stay in shared memory between
+// its sums and its output (as xh and dz in fp32): nothing is read or derived
+// twice then.
+template <int V>
+constexpr int kept_rows() {
+  return V == 4 ? 7 : 4;
+}
+
 template <class TX, class TY, int V>
-__global__ void __launch_bounds__(MAX_THREADS, 2) norm_bwd_sums_kernel(NormArgs a, int L) {
+__global__ void __launch_bounds__(block_threads(V), V == 4 ? 2 : 3) norm_bwd_sums_kernel(NormArgs a, int L) {
   extern __shared__ float sm[];
   cudaTriggerProgrammaticLaunchCompletion();
   const Place<V> p(a);
@@ -507,44 +581,67 @@ __global__ void __launch_bounds__(MAX_THREADS, 2) norm_bwd_sums_kernel(NormArgs 
   float* red2 = red1 + a.RP * width;
   float* ch1 = red2 + a.RP * width;
   float* ch2 = ch1 + a.C;
-  float* acc1 = ch2 + a.C;  // this tile's share of dbeta, dgamma
+  float* acc1 = ch2 + a.C;  // this block's share of dbeta, dgamma
   float* acc2 = acc1 + a.C;
   float* gA = acc2 + a.C;
   float* gB = gA + a.groups;
   char* ring = reinterpret_cast<char*>(align16(gB + a.groups));
   const TX* X = static_cast<const TX*>(a.X);
   const TY* dY = static_cast<const TY*>(a.dY);
-  const int t = blockIdx.x;
+  constexpr int KEEP = kept_rows<V>(), SLOT = V * 4;
+  // slot i of this thread: xh (first x) and, KEEP slots on, dz (first dY)
+  const uint32_t slots = static_cast<uint32_t>(__cvta_generic_to_shared(ring)) + threadIdx.x * SLOT;
+  const uint32_t next = blockDim.x * SLOT, dz_at = KEEP * next;
+  BwdChannels<V> b(a, p);
   for (int c = threadIdx.x; c < a.C; c += blockDim.x) acc1[c] = acc2[c] = 0.f;
-  for_pieces(a, t, [&](int s, int64_t ra, int64_t rb, bool whole) {
+  for (int t = blockIdx.x; t < a.tiles; t += gridDim.x) {
+  int left = 0;
+  for_pieces(a, t, [&](int s, int ra, int rb, bool whole) {
+    left |= !whole;
+    const bool keep = whole && rb - ra <= KEEP * a.RP;
+    const int rows = p.rows(a, ra, rb);
     if (p.on) {
-      const BwdChannels<V> b(a, p, s);
-      float P1[V], P2[V];
-#pragma unroll
-      for (int k = 0; k < V; ++k) P1[k] = P2[k] = 0.f;
       const TX* px = X + (ra + p.ro) * a.ldx + p.c0;
       const TY* py = dY + (ra + p.ro) * a.ldy + p.c0;
       const int64_t sx = (int64_t)a.RP * a.ldx, sy = (int64_t)a.RP * a.ldy;
-      with_act(a.act, [&](auto act) {
-        stream_rows<V, BWD_DEPTH, true>(ring, p.in ? p.rows(a, ra, rb) : 0, px, sx, py, sy,
-                                  [&](float (&x)[V], float (&dy)[V]) {
+      float P1[V], P2[V];
 #pragma unroll
-                                    for (int k = 0; k < V; ++k) {
-                                      float xh;
-                                      const float dz = b.dz(k, x[k], dy[k], act, xh);
-                                      P1[k] += dz;
-                                      P2[k] += dz * xh;
-                                    }
-                                  });
+      for (int k = 0; k < V; ++k) P1[k] = P2[k] = 0.f;
+      if (keep && p.in) {
+        for (int i = 0; i < rows; ++i, px += sx, py += sy) {
+          copy_async<V * sizeof(TX)>(slots + i * next, px);
+          copy_async<V * sizeof(TY)>(slots + dz_at + i * next, py);
+        }
+        copy_commit();
+      }
+      b.segment(a, p, s);
+      with_act(a.act, [&](auto act) {
+        if (keep) {
+          copy_wait<0>();
+          for (int i = 0; i < (p.in ? rows : 0); ++i) {
+            float x[V], dy[V];
+            load_shared<V, TX>(slots + i * next, x);
+            load_shared<V, TY>(slots + dz_at + i * next, dy);
+            b.derive(x, dy, act);
+            add_sums<V>(x, dy, P1, P2);
+            store_shared<V>(slots + i * next, x);
+            store_shared<V>(slots + dz_at + i * next, dy);
+          }
+        } else {
+          stream_rows<V, BWD_DEPTH, true>(ring, p.in ? rows : 0, px, sx, py, sy, [&](float (&x)[V], float (&dy)[V]) {
+            b.derive(x, dy, act);
+            add_sums<V>(x, dy, P1, P2);
+          });
+        }
       });
       store_vec<V>(red1 + p.ro * width + p.c0, P1);
       store_vec<V>(red2 + p.ro * width + p.c0, P2);
     }
-    const float m = (float)(rb - ra) * (float)a.cg;
+    const float inv = rcp_f((float)(rb - ra) * (float)a.cg);  // 1 / values of a group
     block_sums(a, width, red1, red2, ch1, ch2, a.gamma, L, [&](int g, float A, float B) {
       if (whole) {
-        gA[g] = A / m;
-        gB[g] = B / m;
+        gA[g] = A * inv;
+        gB[g] = B * inv;
       } else {
         a.part[((int64_t)t + s) * a.groups + g] = make_float2(A, B);
       }
@@ -553,11 +650,34 @@ __global__ void __launch_bounds__(MAX_THREADS, 2) norm_bwd_sums_kernel(NormArgs 
       acc1[c] += ch1[c];
       acc2[c] += ch2[c];
     }
-    if (whole) bwd_rows<TX, TY, V>(a, p, s, ra, rb, gA, gB, 1, ring);
+    if (keep) {
+      TX* dX = static_cast<TX*>(a.out) + (ra + p.ro) * a.ldo + p.c0;
+      const int64_t so = (int64_t)a.RP * a.ldo;
+      float A[V], B[V];
+#pragma unroll
+      for (int k = 0; k < V; ++k) {
+        A[k] = gA[p.g[k]];
+        B[k] = gB[p.g[k]];
+      }
+      for (int i = 0; i < rows; ++i, dX += so) {
+        float xh[V] = {}, dz[V] = {}, o[V];
+        if (p.in) {
+          load_shared<V, float>(slots + i * next, xh);
+          load_shared<V, float>(slots + dz_at + i * next, dz);
+        }
+        b.output(xh, dz, A, B, o);
+        clear_padding<V>(p, a.C, o);
+        store_vec<V>(dX, o);
+      }
+    } else if (whole) {
+      bwd_rows<TX, TY, V>(a, p, b, ra, rb, gA, gB, 1, ring);
+    }
     __syncthreads();
   });
+  if (threadIdx.x == 0) a.has_long[t] = left;
+  }
   if (a.dpart) {
-    float* d = a.dpart + (int64_t)t * 2 * a.C;
+    float* d = a.dpart + (int64_t)blockIdx.x * 2 * a.C;
     for (int c = threadIdx.x; c < a.C; c += blockDim.x) {
       d[c] = acc1[c];
       d[a.C + c] = acc2[c];
@@ -565,36 +685,42 @@ __global__ void __launch_bounds__(MAX_THREADS, 2) norm_bwd_sums_kernel(NormArgs 
   }
 }
 
-// The first `joiners` blocks join long segments; the others add the tiles'
-// shares of dbeta and dgamma, 32 columns each, in tile order.
+// The first `joiners` blocks join long segments; the others add the blocks'
+// shares of dbeta and dgamma, 8 columns each, in a fixed order.
 __global__ void __launch_bounds__(FIN_THREADS) norm_bwd_join_kernel(NormArgs a, int joiners) {
   cudaTriggerProgrammaticLaunchCompletion();
   cudaGridDependencySynchronize();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   constexpr int NW = FIN_THREADS / 32;
   if ((int)blockIdx.x >= joiners) {
-    __shared__ float red[NW][32];
-    const int col = ((int)blockIdx.x - joiners) * 32 + lane;
+    // 8 columns to a block: 64 threads share each
+    __shared__ float red[FIN_THREADS / 8][8];
+    const int c = threadIdx.x & 7, r = threadIdx.x >> 3;
+    const int col = ((int)blockIdx.x - joiners) * 8 + c;
     float sum = 0.f;
     if (col < 2 * a.C) {
 #pragma unroll 8
-      for (int i = warp; i < a.tiles; i += NW) sum += a.dpart[(int64_t)i * 2 * a.C + col];
+      for (int i = r; i < a.blocks; i += FIN_THREADS / 8) sum += a.dpart[(int64_t)i * 2 * a.C + col];
     }
-    red[warp][lane] = sum;
+    red[r][c] = sum;
     __syncthreads();
-    if (warp == 0 && col < 2 * a.C) {
-      float v = 0.f;
-      for (int w = 0; w < NW; ++w) v += red[w][lane];
-      if (col < a.C) {
-        if (a.dbeta) a.dbeta[col] = v;
-      } else if (a.dgamma) {
-        a.dgamma[col - a.C] = v;
+    if (r < 4) {
+      sum = 0.f;
+      for (int w = r; w < FIN_THREADS / 8; w += 4) sum += red[w][c];
+      sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+      if (r == 0 && col < 2 * a.C) {
+        if (col < a.C) {
+          if (a.dbeta) a.dbeta[col] = sum;
+        } else if (a.dgamma) {
+          a.dgamma[col - a.C] = sum;
+        }
       }
     }
     return;
   }
   check_segments(a, joiners, false);
-  for_long(a, joiners, [&](int s, int64_t sb, int64_t se, int t0, int t1) {
+  for_long(a, joiners, [&](int s, int sb, int se, int t0, int t1) {
     const float m = (float)(se - sb) * (float)a.cg;
     for (int g = warp; g < a.groups; g += NW) {
       const float2* part = a.part + (int64_t)s * a.groups + g;
@@ -612,22 +738,29 @@ __global__ void __launch_bounds__(FIN_THREADS) norm_bwd_join_kernel(NormArgs a, 
 }
 
 template <class TX, class TY, int V>
-__global__ void __launch_bounds__(MAX_THREADS, 2) norm_bwd_apply_kernel(NormArgs a) {
+__global__ void __launch_bounds__(block_threads(V), V == 4 ? 2 : 3) norm_bwd_apply_kernel(NormArgs a) {
   extern __shared__ float sm[];
-  cudaGridDependencySynchronize();
   const Place<V> p(a);
-  for_pieces(a, gridDim.x - 1 - blockIdx.x, [&](int s, int64_t ra, int64_t rb, bool whole) {
+  cudaGridDependencySynchronize();
+  // last tiles first, as within a tile
+  for (int t = a.tiles - 1 - (int)blockIdx.x; t >= 0; t -= gridDim.x) {
+  if (!a.has_long[t]) continue;
+  for_pieces(a, t, [&](int s, int ra, int rb, bool whole) {
     if (!whole) {
       const float* j = &a.joined[(int64_t)s * a.groups].x;
-      bwd_rows<TX, TY, V>(a, p, s, ra, rb, j, j + 1, 2, reinterpret_cast<char*>(sm));
+      BwdChannels<V> b(a, p);
+      b.segment(a, p, s);
+      bwd_rows<TX, TY, V>(a, p, b, ra, rb, j, j + 1, 2, reinterpret_cast<char*>(sm));
     }
   });
+  }
 }
 
 // ---------------------------------------------------------------- host side
 // About eight tiles per SM, so that the whole grid is resident in two or three
 // turns and a long segment has few pieces to join; at least 16 rows each.
 constexpr int64_t kTiles = 152 * 8, kTileRows = 16;
+constexpr int kShortRows = 256;
 
 int64_t tile_rows(int64_t n, int RP) {
   const int64_t r = (n + kTiles - 1) / kTiles, least = RP > kTileRows ? RP : kTileRows;
@@ -642,6 +775,7 @@ struct NormWs {
   float2* part;
   float2* joined;
   float* dpart;
+  int* has_long;
   size_t bytes;
 };
 NormWs norm_ws(void* base, size_t cap, int64_t n, int C, int groups, int n_seg, bool* ok) {
@@ -650,6 +784,7 @@ NormWs norm_ws(void* base, size_t cap, int64_t n, int C, int groups, int n_seg, 
   w.part = ar.take<float2>((size_t)(most_tiles(n) + n_seg) * groups);
   w.joined = ar.take<float2>((size_t)n_seg * groups);
   w.dpart = ar.take<float>((size_t)most_tiles(n) * 2 * C);
+  w.has_long = ar.take<int>((size_t)most_tiles(n));
   w.bytes = ar.used;
   *ok = ar.ok();
   return w;
@@ -696,11 +831,14 @@ int lanes_for(int cg) {
 }
 
 // Threads, rows and tiles of a launch; returns the block size.
-int plan(NormArgs& a, int pad, int V) {
+int plan(NormArgs& a, int pad, int V, int per_sm) {
   a.CH = (a.C + pad - 1) / pad * pad / V;
-  a.RP = a.CH < AIM_THREADS ? AIM_THREADS / a.CH : 1;
-  a.R = tile_rows(a.n, a.RP);
-  a.tiles = (int)((a.n + a.R - 1) / a.R);
+  a.RP = block_threads(V) / a.CH;
+  a.R = (int)tile_rows(a.n, a.RP);
+  a.longest = 2 * a.R > kShortRows ? 2 * a.R : kShortRows;
+  a.tiles = (int)(((int64_t)a.n + a.R - 1) / a.R);
+  a.blocks = a.tiles;
+  a.apply_blocks = a.tiles < per_sm * 152 ? a.tiles : per_sm * 152;
   return (a.RP * a.CH + 31) / 32 * 32;
 }
 int joiners(const NormArgs& a) { return a.n_seg < 4 * 152 ? a.n_seg : 4 * 152; }
@@ -716,34 +854,35 @@ gnn_status allow_smem(K* k, bool& ready) {
 template <class TX, class TY, int V>
 gnn_status norm_fwd(NormArgs a, cudaStream_t st) {
   static bool ready1 = false, ready2 = false;
-  const int threads = plan(a, sizeof(TY) == 4 ? 4 : 16, V);
+  const int threads = plan(a, sizeof(TY) == 4 ? 4 : 16, V, V == 4 ? 2 : 4);
   const size_t ring = (size_t)2 * (FWD_DEPTH + 1) * threads * V * sizeof(TX);
   const size_t smem = sizeof(float) * (size_t)(2 * a.RP * a.CH * V + 2 * a.C + 2 * a.groups) + 16 + ring;
   const Launch l{st};
   gnn_status s = allow_smem(norm_fwd_stats_kernel<TX, TY, V>, ready1);
   if (s == GNN_OK) s = allow_smem(norm_fwd_apply_kernel<TX, TY, V>, ready2);
   if (s == GNN_OK && a.tiles)
-    s = l.run(false, a.tiles, threads, smem, norm_fwd_stats_kernel<TX, TY, V>, a, lanes_for(a.cg));
+    s = l.run(false, a.blocks, threads, smem, norm_fwd_stats_kernel<TX, TY, V>, a, lanes_for(a.cg));
   if (s == GNN_OK) s = l.run(a.tiles > 0, joiners(a), FIN_THREADS, 0, norm_fwd_join_kernel, a);
-  if (s == GNN_OK && a.tiles) s = l.run(true, a.tiles, threads, ring, norm_fwd_apply_kernel<TX, TY, V>, a);
+  if (s == GNN_OK && a.tiles) s = l.run(true, a.apply_blocks, threads, ring, norm_fwd_apply_kernel<TX, TY, V>, a);
   return s;
 }
 
 template <class TX, class TY, int V>
 gnn_status norm_bwd(NormArgs a, cudaStream_t st) {
   static bool ready1 = false, ready2 = false;
-  const int threads = plan(a, sizeof(TX) == 4 ? 4 : 16, V);
-  const size_t ring = (size_t)2 * (BWD_DEPTH + 1) * threads * V * (sizeof(TX) + sizeof(TY));
+  const int threads = plan(a, sizeof(TX) == 4 ? 4 : 16, V, V == 4 ? 2 : 3);
+  const size_t stream = (size_t)2 * (BWD_DEPTH + 1) * threads * V * (sizeof(TX) + sizeof(TY));
+  const size_t kept = (size_t)2 * kept_rows<V>() * threads * V * 4, ring = stream > kept ? stream : kept;
   const size_t smem = sizeof(float) * (size_t)(2 * a.RP * a.CH * V + 4 * a.C + 2 * a.groups) + 16 + ring;
   const Launch l{st};
   gnn_status s = allow_smem(norm_bwd_sums_kernel<TX, TY, V>, ready1);
   if (s == GNN_OK) s = allow_smem(norm_bwd_apply_kernel<TX, TY, V>, ready2);
   if (s == GNN_OK && a.tiles)
-    s = l.run(false, a.tiles, threads, smem, norm_bwd_sums_kernel<TX, TY, V>, a, lanes_for(a.cg));
-  const int cols = a.dpart ? (2 * a.C + 31) / 32 : 0;
+    s = l.run(false, a.blocks, threads, smem, norm_bwd_sums_kernel<TX, TY, V>, a, lanes_for(a.cg));
+  const int cols = a.dpart ? (2 * a.C + 7) / 8 : 0;
   if (s == GNN_OK)
     s = l.run(a.tiles > 0, joiners(a) + cols, FIN_THREADS, 0, norm_bwd_join_kernel, a, joiners(a));
-  if (s == GNN_OK && a.tiles) s = l.run(true, a.tiles, threads, ring, norm_bwd_apply_kernel<TX, TY, V>, a);
+  if (s == GNN_OK && a.tiles) s = l.run(true, a.apply_blocks, threads, stream, norm_bwd_apply_kernel<TX, TY, V>, a);
   return s;
 }
 
@@ -795,9 +934,9 @@ extern "C" gnn_status gnn_group_norm_fwd(const void* X, int64_t ldx, int32_t x_t
   const NormWs w = norm_ws(ws, ws_bytes, n, C, groups, n_seg, &ok);
   GNN_REQUIRE(ws && ok, "gnn_group_norm_fwd: workspace too small (%zu < %zu)", ws_bytes, w.bytes);
   NormArgs a{};
-  a.X = X, a.ldx = ldx, a.out = Y, a.ldo = ldy, a.n = n, a.C = C, a.groups = groups, a.cg = C / groups;
+  a.X = X, a.ldx = ldx, a.out = Y, a.ldo = ldy, a.n = (int)n, a.C = C, a.groups = groups, a.cg = C / groups;
   a.n_seg = n_seg, a.act = act, a.seg = seg_start, a.gamma = gamma, a.beta = beta, a.eps = (float)eps;
-  a.mean = mean, a.rstd = rstd, a.part = w.part;
+  a.mean = mean, a.rstd = rstd, a.part = w.part, a.has_long = w.has_long;
   a.flags = device_flags();
   if (!a.flags) return fail(GNN_ERR_CUDA, "device flag word unavailable");
   cudaStream_t st = as_stream(stream);
@@ -830,10 +969,10 @@ extern "C" gnn_status gnn_group_norm_bwd(const void* dY, int64_t ldy, int32_t y_
   const NormWs w = norm_ws(ws, ws_bytes, n, C, groups, n_seg, &ok);
   GNN_REQUIRE(ws && ok, "gnn_group_norm_bwd: workspace too small (%zu < %zu)", ws_bytes, w.bytes);
   NormArgs a{};
-  a.X = X, a.ldx = ldx, a.dY = dY, a.ldy = ldy, a.out = dX, a.ldo = lddx, a.n = n, a.C = C, a.groups = groups;
+  a.X = X, a.ldx = ldx, a.dY = dY, a.ldy = ldy, a.out = dX, a.ldo = lddx, a.n = (int)n, a.C = C, a.groups = groups;
   a.cg = C / groups, a.n_seg = n_seg, a.act = act, a.seg = seg_start, a.gamma = gamma, a.beta = beta;
   a.mean = const_cast<float*>(mean), a.rstd = const_cast<float*>(rstd);
-  a.part = w.part, a.joined = w.joined, a.dpart = dgamma || dbeta ? w.dpart : nullptr;
+  a.part = w.part, a.has_long = w.has_long, a.joined = w.joined, a.dpart = dgamma || dbeta ? w.dpart : nullptr;
   a.dgamma = dgamma, a.dbeta = dbeta;
   a.flags = device_flags();
   if (!a.flags) return fail(GNN_ERR_CUDA, "device flag word unavailable");
