@@ -10,6 +10,8 @@
 // both only grow along the rows; so no plan has to be built from seg_start.
 #include <cuda_runtime.h>
 
+#include <algorithm>
+
 #include "internal.h"
 #include "nodewise.cuh"
 
@@ -19,8 +21,12 @@ namespace {
 
 // A block holds as many rows of CH chunks side by side as fit its threads, at
 // least one: few threads are idle whatever a row's width (256 threads left 41% of
-// them idle at 602 fp32 channels).
-constexpr int block_threads(int V) { return V == 4 ? 384 : 192; }
+// them idle at 602 fp32 channels).  Where segments are short a block is 128
+// threads: it takes them one at a time, and most of what a warp does for a
+// segment does not depend on its rows.
+constexpr int block_threads(int V, bool small = false) { return small ? 128 : V == 4 ? 384 : 192; }
+constexpr int fwd_blocks(int V, bool small) { return small ? 6 : V == 4 ? 2 : 4; }  // per SM at least
+constexpr int bwd_blocks(int V, bool small) { return small ? 5 : V == 4 ? 2 : 3; }
 constexpr int FIN_THREADS = 512;
 
 struct NormArgs {
@@ -34,6 +40,7 @@ struct NormArgs {
   int RP;  // rows a block holds side by side: RP * CH threads take part
   int R;
   int longest;  // rows of a short segment
+  int keep;     // rows of a thread that stay in shared memory
   int tiles;
   const int64_t* seg;  // may be NULL: one segment
   const float* gamma;
@@ -43,9 +50,7 @@ struct NormArgs {
   float* rstd;
   float2* part;  // forward: (mean, M2) of a piece's group; backward: the two sums
   float2* joined;  // backward: the two sums over a long segment's group, / m
-  float* dpart;    // backward: [blocks][2][C] sums of dz and dz xh
-  int blocks;        // of the launch that walks the tiles
-  int apply_blocks;  // of the last launch
+  float* dpart;    // backward: [tiles][2][C] sums of dz and dz xh
   int* has_long;   // [tiles]: whether pieces of long segments are left for the last launch
   float* dgamma;
   float* dbeta;
@@ -327,8 +332,8 @@ __device__ __forceinline__ void fwd_rows(const NormArgs& a, const Place<V>& p, i
 // Statistics of every piece of a tile; short segments end here with their
 // output.  A group's sums are formed about its value in the piece's first row,
 // so a mean far from zero does not cancel in E[x^2] - mean^2.
-template <class TX, class TY, int V>
-__global__ void __launch_bounds__(block_threads(V), V == 4 ? 2 : 4) norm_fwd_stats_kernel(NormArgs a, int L) {
+template <class TX, class TY, int V, bool SMALL>
+__global__ void __launch_bounds__(block_threads(V, SMALL), fwd_blocks(V, SMALL)) norm_fwd_stats_kernel(NormArgs a, int L) {
   extern __shared__ float sm[];
   cudaTriggerProgrammaticLaunchCompletion();
   const Place<V> p(a);
@@ -341,7 +346,7 @@ __global__ void __launch_bounds__(block_threads(V), V == 4 ? 2 : 4) norm_fwd_sta
   float* gr = gm + a.groups;
   char* ring = reinterpret_cast<char*>(align16(gr + a.groups));
   const TX* X = static_cast<const TX*>(a.X);
-  for (int t = blockIdx.x; t < a.tiles; t += gridDim.x) {
+  const int t = blockIdx.x;
   int left = 0;  // pieces of long segments
   for_pieces(a, t, [&](int s, int ra, int rb, bool whole) {
     left |= !whole;
@@ -400,7 +405,6 @@ __global__ void __launch_bounds__(block_threads(V), V == 4 ? 2 : 4) norm_fwd_sta
     }
   });
   if (threadIdx.x == 0) a.has_long[t] = left;
-  }
 }
 
 // Segments without rows, and what seg_start has to be.
@@ -436,11 +440,11 @@ __global__ void __launch_bounds__(FIN_THREADS) norm_fwd_join_kernel(NormArgs a) 
   check_segments(a, gridDim.x, true);
   const int lane = threadIdx.x & 31;
   for_long(a, gridDim.x, [&](int s, int sb, int se, int t0, int t1) {
-    for (int g = threadIdx.x >> 5; g < a.groups; g += FIN_THREADS / 32) {
+    for (int g = blockIdx.y * (FIN_THREADS / 32) + (threadIdx.x >> 5); g < a.groups; g += gridDim.y * (FIN_THREADS / 32)) {
       const float2* part = a.part + (int64_t)s * a.groups + g;
       const float first = part[(int64_t)t0 * a.groups].x;
       float M = 0.f, S = 0.f, Q = 0.f;
-#pragma unroll 4
+#pragma unroll 8
       for (int i = t0 + lane; i <= t1; i += 32) {
         const float2 v = part[(int64_t)i * a.groups];
         const float m = (float)((int)min((int64_t)se, (i + 1) * (int64_t)a.R) - max(sb, i * a.R)) * (float)a.cg;
@@ -460,19 +464,18 @@ __global__ void __launch_bounds__(FIN_THREADS) norm_fwd_join_kernel(NormArgs a) 
 }
 
 template <class TX, class TY, int V>
-__global__ void __launch_bounds__(block_threads(V), V == 4 ? 2 : 4) norm_fwd_apply_kernel(NormArgs a) {
+__global__ void __launch_bounds__(block_threads(V), fwd_blocks(V, false)) norm_fwd_apply_kernel(NormArgs a) {
   extern __shared__ float sm[];
-  const Place<V> p(a);
   cudaGridDependencySynchronize();
   // last tiles first, as within a tile
-  for (int t = a.tiles - 1 - (int)blockIdx.x; t >= 0; t -= gridDim.x) {
-  if (!a.has_long[t]) continue;
+  const int t = a.tiles - 1 - (int)blockIdx.x;
+  if (!a.has_long[t]) return;
+  const Place<V> p(a);
   for_pieces(a, t, [&](int s, int ra, int rb, bool whole) {
     if (!whole)
       fwd_rows<TX, TY, V>(a, p, ra, rb, a.mean + (int64_t)s * a.groups, a.rstd + (int64_t)s * a.groups,
                              reinterpret_cast<char*>(sm));
   });
-  }
 }
 
 // ------------------------------------------------------------------ backward
@@ -563,16 +566,11 @@ __device__ __forceinline__ void bwd_rows(const NormArgs& a, const Place<V>& p, c
   });
 }
 
-// Rows of a thread that a short segment may have to stay in shared memory between
-// its sums and its output (as xh and dz in fp32): nothing is read or derived
+// A short segment of at most a.keep rows a thread stays in shared memory between
+// its sums and its output, as xh and dz in fp32: nothing is read or derived
 // twice then.
-template <int V>
-constexpr int kept_rows() {
-  return V == 4 ? 7 : 4;
-}
-
-template <class TX, class TY, int V>
-__global__ void __launch_bounds__(block_threads(V), V == 4 ? 2 : 3) norm_bwd_sums_kernel(NormArgs a, int L) {
+template <class TX, class TY, int V, bool SMALL>
+__global__ void __launch_bounds__(block_threads(V, SMALL), bwd_blocks(V, SMALL)) norm_bwd_sums_kernel(NormArgs a, int L) {
   extern __shared__ float sm[];
   cudaTriggerProgrammaticLaunchCompletion();
   const Place<V> p(a);
@@ -588,17 +586,17 @@ __global__ void __launch_bounds__(block_threads(V), V == 4 ? 2 : 3) norm_bwd_sum
   char* ring = reinterpret_cast<char*>(align16(gB + a.groups));
   const TX* X = static_cast<const TX*>(a.X);
   const TY* dY = static_cast<const TY*>(a.dY);
-  constexpr int KEEP = kept_rows<V>(), SLOT = V * 4;
-  // slot i of this thread: xh (first x) and, KEEP slots on, dz (first dY)
+  constexpr int SLOT = V * 4;
+  // slot i of this thread: xh (first x) and, `keep` slots on, dz (first dY)
   const uint32_t slots = static_cast<uint32_t>(__cvta_generic_to_shared(ring)) + threadIdx.x * SLOT;
-  const uint32_t next = blockDim.x * SLOT, dz_at = KEEP * next;
+  const uint32_t next = blockDim.x * SLOT, dz_at = a.keep * next;
   BwdChannels<V> b(a, p);
   for (int c = threadIdx.x; c < a.C; c += blockDim.x) acc1[c] = acc2[c] = 0.f;
-  for (int t = blockIdx.x; t < a.tiles; t += gridDim.x) {
+  const int t = blockIdx.x;
   int left = 0;
   for_pieces(a, t, [&](int s, int ra, int rb, bool whole) {
     left |= !whole;
-    const bool keep = whole && rb - ra <= KEEP * a.RP;
+    const bool keep = whole && rb - ra <= a.keep * a.RP;
     const int rows = p.rows(a, ra, rb);
     if (p.on) {
       const TX* px = X + (ra + p.ro) * a.ldx + p.c0;
@@ -618,14 +616,25 @@ __global__ void __launch_bounds__(block_threads(V), V == 4 ? 2 : 3) norm_bwd_sum
       with_act(a.act, [&](auto act) {
         if (keep) {
           copy_wait<0>();
-          for (int i = 0; i < (p.in ? rows : 0); ++i) {
-            float x[V], dy[V];
-            load_shared<V, TX>(slots + i * next, x);
-            load_shared<V, TY>(slots + dz_at + i * next, dy);
+          // two rows at a time, for their independent chains
+          for (int i = 0; i < (p.in ? rows : 0); i += 2) {
+            const uint32_t at = slots + i * next;
+            const bool two = i + 1 < rows;
+            float x[V], dy[V], x1[V], dy1[V];
+            load_shared<V, TX>(at, x);
+            load_shared<V, TY>(at + dz_at, dy);
+            if (two) {
+              load_shared<V, TX>(at + next, x1);
+              load_shared<V, TY>(at + next + dz_at, dy1);
+              b.derive(x1, dy1, act);
+              add_sums<V>(x1, dy1, P1, P2);
+              store_shared<V>(at + next, x1);
+              store_shared<V>(at + next + dz_at, dy1);
+            }
             b.derive(x, dy, act);
             add_sums<V>(x, dy, P1, P2);
-            store_shared<V>(slots + i * next, x);
-            store_shared<V>(slots + dz_at + i * next, dy);
+            store_shared<V>(at, x);
+            store_shared<V>(at + dz_at, dy);
           }
         } else {
           stream_rows<V, BWD_DEPTH, true>(ring, p.in ? rows : 0, px, sx, py, sy, [&](float (&x)[V], float (&dy)[V]) {
@@ -675,9 +684,8 @@ __global__ void __launch_bounds__(block_threads(V), V == 4 ? 2 : 3) norm_bwd_sum
     __syncthreads();
   });
   if (threadIdx.x == 0) a.has_long[t] = left;
-  }
   if (a.dpart) {
-    float* d = a.dpart + (int64_t)blockIdx.x * 2 * a.C;
+    float* d = a.dpart + (int64_t)t * 2 * a.C;
     for (int c = threadIdx.x; c < a.C; c += blockDim.x) {
       d[c] = acc1[c];
       d[a.C + c] = acc2[c];
@@ -700,7 +708,7 @@ __global__ void __launch_bounds__(FIN_THREADS) norm_bwd_join_kernel(NormArgs a, 
     float sum = 0.f;
     if (col < 2 * a.C) {
 #pragma unroll 8
-      for (int i = r; i < a.blocks; i += FIN_THREADS / 8) sum += a.dpart[(int64_t)i * 2 * a.C + col];
+      for (int i = r; i < a.tiles; i += FIN_THREADS / 8) sum += a.dpart[(int64_t)i * 2 * a.C + col];
     }
     red[r][c] = sum;
     __syncthreads();
@@ -725,7 +733,7 @@ __global__ void __launch_bounds__(FIN_THREADS) norm_bwd_join_kernel(NormArgs a, 
     for (int g = warp; g < a.groups; g += NW) {
       const float2* part = a.part + (int64_t)s * a.groups + g;
       float A = 0.f, B = 0.f;
-#pragma unroll 4
+#pragma unroll 8
       for (int i = t0 + lane; i <= t1; i += 32) {
         const float2 v = part[(int64_t)i * a.groups];
         A += v.x;
@@ -738,13 +746,13 @@ __global__ void __launch_bounds__(FIN_THREADS) norm_bwd_join_kernel(NormArgs a, 
 }
 
 template <class TX, class TY, int V>
-__global__ void __launch_bounds__(block_threads(V), V == 4 ? 2 : 3) norm_bwd_apply_kernel(NormArgs a) {
+__global__ void __launch_bounds__(block_threads(V), bwd_blocks(V, false)) norm_bwd_apply_kernel(NormArgs a) {
   extern __shared__ float sm[];
-  const Place<V> p(a);
   cudaGridDependencySynchronize();
   // last tiles first, as within a tile
-  for (int t = a.tiles - 1 - (int)blockIdx.x; t >= 0; t -= gridDim.x) {
-  if (!a.has_long[t]) continue;
+  const int t = a.tiles - 1 - (int)blockIdx.x;
+  if (!a.has_long[t]) return;
+  const Place<V> p(a);
   for_pieces(a, t, [&](int s, int ra, int rb, bool whole) {
     if (!whole) {
       const float* j = &a.joined[(int64_t)s * a.groups].x;
@@ -753,21 +761,25 @@ __global__ void __launch_bounds__(block_threads(V), V == 4 ? 2 : 3) norm_bwd_app
       bwd_rows<TX, TY, V>(a, p, b, ra, rb, j, j + 1, 2, reinterpret_cast<char*>(sm));
     }
   });
-  }
 }
 
 // ---------------------------------------------------------------- host side
-// About eight tiles per SM, so that the whole grid is resident in two or three
-// turns and a long segment has few pieces to join; at least 16 rows each.
-constexpr int64_t kTiles = 152 * 8, kTileRows = 16;
-constexpr int kShortRows = 256;
+// Tiles per SM: a long segment's balance better when there are more of them, up
+// to what their partials cost (measured with 4, 8, 16: 716847 x 300 in 8 segments
+// forward 365, 342, 326 us; 232965 x 602 in 8 backward 365, 368, 387 us; 65537 x
+// 256 in 2800 backward, with 10 kept rows a thread, -, 78, 94 us).  A tile has at
+// least 16 rows.  Segments are taken for short where they have 256 rows or fewer
+// in the mean.
+constexpr int kShortRows = 256, kShortMean = 40;
 
-int64_t tile_rows(int64_t n, int RP) {
-  const int64_t r = (n + kTiles - 1) / kTiles, least = RP > kTileRows ? RP : kTileRows;
-  return r > least ? r : least;
+int tile_rows(int64_t n, int RP, bool backward, bool small) {
+  const auto per = [&](int64_t tiles) { return (int)((n + tiles - 1) / tiles); };
+  int R = per(small || backward ? 152 * 8 : 152 * 16);
+  if (!small) R = std::max(R, std::min(16 * RP, per(152 * 2)));
+  return std::max(R, std::max(RP, 16));
 }
 int64_t most_tiles(int64_t n) {
-  const int64_t R = tile_rows(n, 1);
+  const int64_t R = std::max<int64_t>((n + 152 * 16 - 1) / (152 * 16), 16);
   return (n + R - 1) / R;
 }
 
@@ -831,14 +843,14 @@ int lanes_for(int cg) {
 }
 
 // Threads, rows and tiles of a launch; returns the block size.
-int plan(NormArgs& a, int pad, int V, int per_sm) {
+int plan(NormArgs& a, int pad, int V, bool backward, bool* small) {
   a.CH = (a.C + pad - 1) / pad * pad / V;
-  a.RP = block_threads(V) / a.CH;
-  a.R = (int)tile_rows(a.n, a.RP);
+  *small = a.n / a.n_seg <= kShortMean && a.CH <= block_threads(V, true);
+  a.RP = block_threads(V, *small) / a.CH;
+  a.R = tile_rows(a.n, a.RP, backward, *small);
   a.longest = 2 * a.R > kShortRows ? 2 * a.R : kShortRows;
+  a.keep = *small ? 40 / V : 28 / V;
   a.tiles = (int)(((int64_t)a.n + a.R - 1) / a.R);
-  a.blocks = a.tiles;
-  a.apply_blocks = a.tiles < per_sm * 152 ? a.tiles : per_sm * 152;
   return (a.RP * a.CH + 31) / 32 * 32;
 }
 int joiners(const NormArgs& a) { return a.n_seg < 4 * 152 ? a.n_seg : 4 * 152; }
@@ -851,39 +863,49 @@ gnn_status allow_smem(K* k, bool& ready) {
   return GNN_OK;
 }
 
-template <class TX, class TY, int V>
-gnn_status norm_fwd(NormArgs a, cudaStream_t st) {
+template <class TX, class TY, int V, bool SMALL>
+gnn_status norm_fwd(NormArgs a, int threads, cudaStream_t st) {
   static bool ready1 = false, ready2 = false;
-  const int threads = plan(a, sizeof(TY) == 4 ? 4 : 16, V, V == 4 ? 2 : 4);
   const size_t ring = (size_t)2 * (FWD_DEPTH + 1) * threads * V * sizeof(TX);
   const size_t smem = sizeof(float) * (size_t)(2 * a.RP * a.CH * V + 2 * a.C + 2 * a.groups) + 16 + ring;
   const Launch l{st};
-  gnn_status s = allow_smem(norm_fwd_stats_kernel<TX, TY, V>, ready1);
+  gnn_status s = allow_smem(norm_fwd_stats_kernel<TX, TY, V, SMALL>, ready1);
   if (s == GNN_OK) s = allow_smem(norm_fwd_apply_kernel<TX, TY, V>, ready2);
   if (s == GNN_OK && a.tiles)
-    s = l.run(false, a.blocks, threads, smem, norm_fwd_stats_kernel<TX, TY, V>, a, lanes_for(a.cg));
+    s = l.run(false, a.tiles, threads, smem, norm_fwd_stats_kernel<TX, TY, V, SMALL>, a, lanes_for(a.cg));
   if (s == GNN_OK) s = l.run(a.tiles > 0, joiners(a), FIN_THREADS, 0, norm_fwd_join_kernel, a);
-  if (s == GNN_OK && a.tiles) s = l.run(true, a.apply_blocks, threads, ring, norm_fwd_apply_kernel<TX, TY, V>, a);
+  if (s == GNN_OK && a.tiles) s = l.run(true, a.tiles, threads, ring, norm_fwd_apply_kernel<TX, TY, V>, a);
   return s;
 }
-
 template <class TX, class TY, int V>
-gnn_status norm_bwd(NormArgs a, cudaStream_t st) {
+gnn_status norm_fwd(NormArgs a, cudaStream_t st) {
+  bool small;
+  const int threads = plan(a, sizeof(TY) == 4 ? 4 : 16, V, false, &small);
+  return small ? norm_fwd<TX, TY, V, true>(a, threads, st) : norm_fwd<TX, TY, V, false>(a, threads, st);
+}
+
+template <class TX, class TY, int V, bool SMALL>
+gnn_status norm_bwd(NormArgs a, int threads, cudaStream_t st) {
   static bool ready1 = false, ready2 = false;
-  const int threads = plan(a, sizeof(TX) == 4 ? 4 : 16, V, V == 4 ? 2 : 3);
   const size_t stream = (size_t)2 * (BWD_DEPTH + 1) * threads * V * (sizeof(TX) + sizeof(TY));
-  const size_t kept = (size_t)2 * kept_rows<V>() * threads * V * 4, ring = stream > kept ? stream : kept;
+  const size_t kept = (size_t)2 * a.keep * threads * V * 4, ring = stream > kept ? stream : kept;
   const size_t smem = sizeof(float) * (size_t)(2 * a.RP * a.CH * V + 4 * a.C + 2 * a.groups) + 16 + ring;
   const Launch l{st};
-  gnn_status s = allow_smem(norm_bwd_sums_kernel<TX, TY, V>, ready1);
+  gnn_status s = allow_smem(norm_bwd_sums_kernel<TX, TY, V, SMALL>, ready1);
   if (s == GNN_OK) s = allow_smem(norm_bwd_apply_kernel<TX, TY, V>, ready2);
   if (s == GNN_OK && a.tiles)
-    s = l.run(false, a.blocks, threads, smem, norm_bwd_sums_kernel<TX, TY, V>, a, lanes_for(a.cg));
+    s = l.run(false, a.tiles, threads, smem, norm_bwd_sums_kernel<TX, TY, V, SMALL>, a, lanes_for(a.cg));
   const int cols = a.dpart ? (2 * a.C + 7) / 8 : 0;
   if (s == GNN_OK)
     s = l.run(a.tiles > 0, joiners(a) + cols, FIN_THREADS, 0, norm_bwd_join_kernel, a, joiners(a));
-  if (s == GNN_OK && a.tiles) s = l.run(true, a.apply_blocks, threads, stream, norm_bwd_apply_kernel<TX, TY, V>, a);
+  if (s == GNN_OK && a.tiles) s = l.run(true, a.tiles, threads, stream, norm_bwd_apply_kernel<TX, TY, V>, a);
   return s;
+}
+template <class TX, class TY, int V>
+gnn_status norm_bwd(NormArgs a, cudaStream_t st) {
+  bool small;
+  const int threads = plan(a, sizeof(TX) == 4 ? 4 : 16, V, true, &small);
+  return small ? norm_bwd<TX, TY, V, true>(a, threads, st) : norm_bwd<TX, TY, V, false>(a, threads, st);
 }
 
 }  // namespace
