@@ -6,6 +6,8 @@ path: without the library or a CUDA device the calls raise."""
 from __future__ import annotations
 
 import ctypes
+import functools
+import threading
 from dataclasses import dataclass, field
 from typing import Optional, Sequence
 
@@ -154,14 +156,30 @@ def _workspace(nbytes: int, device):
     return torch.empty(max(int(nbytes), 1), dtype=torch.uint8, device=device)
 
 
-def _workspace_on(nbytes: int, device, stream):
-    """Scratch for a call on `stream`: allocated there, so that the allocator
-    hands it out again only behind the call's work."""
+_scratch_of = threading.local()
+_SCRATCH_MOST = 32 << 20
+
+
+def _scratch(nbytes: int, t, stream):
+    """Workspace of a call on t that brings none.  A thread keeps one small
+    buffer for each device and stream it calls on (what runs there is ordered;
+    an allocation a call cost as much time as three launches).  Large ones, calls
+    on a stream of their own and calls that are captured into a graph allocate:
+    on the call's stream, so that the allocator hands the memory out again only
+    behind the call's work, and in the graph's own pool."""
     import torch
-    if stream is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return torch.empty(nbytes, dtype=torch.uint8, device=t.device)
+    if nbytes > _SCRATCH_MOST or torch._C._cuda_isCurrentStreamCapturing():
+        return torch.empty(nbytes, dtype=torch.uint8, device=t.device)
+    kept = _scratch_of.__dict__
+    dev = t.get_device()
+    key = (dev, torch._C._cuda_getCurrentRawStream(dev))
+    buf = kept.get(key)
+    if buf is None or buf.numel() < nbytes:
+        buf = kept[key] = torch.empty(max(nbytes, 1 << 20), dtype=torch.uint8, device=t.device)
+    return buf
 
 
 def gnn_csr_build(n: int, src, dst, flags: int = CSR_GCN, stream=None) -> Csr:
@@ -794,6 +812,7 @@ def _seg(seg_start):
     return seg_start.data_ptr(), seg_start.numel() - 1
 
 
+@functools.lru_cache(maxsize=1024)
 def gnn_group_norm_workspace(n: int, C: int, groups: int, n_seg: int = 1) -> int:
     nb = ctypes.c_size_t()
     call("gnn_group_norm_workspace", n, C, groups, n_seg, ctypes.byref(nb))
@@ -808,7 +827,7 @@ def gnn_group_norm_fwd(X, n: int, C: int, groups: int, Y, mean, rstd, seg_start=
     seg, n_seg = _seg(seg_start)
     ldx, ldy = _rows(X, n, C, "X"), _rows(Y, n, C, "Y")
     if ws is None:
-        ws = _workspace_on(gnn_group_norm_workspace(n, C, groups, n_seg), X.device, stream)
+        ws = _scratch(gnn_group_norm_workspace(n, C, groups, n_seg), X, stream)
     call("gnn_group_norm_fwd", _ptr(X), ldx, _type(X), n, C, groups, seg, n_seg, _f32(gamma, C, "gamma"),
          _f32(beta, C, "beta"), float(eps), _act(act), _ptr(Y), ldy, _type(Y),
          _f32(mean, n_seg * groups, "mean"), _f32(rstd, n_seg * groups, "rstd"), _ptr(ws), ws.numel(),
@@ -825,13 +844,14 @@ def gnn_group_norm_bwd(dY, X, n: int, C: int, groups: int, mean, rstd, dX, dgamm
     if dX.dtype != X.dtype:
         raise ValueError("dX: needs X's type")
     if ws is None:
-        ws = _workspace_on(gnn_group_norm_workspace(n, C, groups, n_seg), X.device, stream)
+        ws = _scratch(gnn_group_norm_workspace(n, C, groups, n_seg), X, stream)
     call("gnn_group_norm_bwd", _ptr(dY), ldy, _type(dY), _ptr(X), ldx, _type(X), n, C, groups, seg, n_seg,
          _f32(gamma, C, "gamma"), _f32(beta, C, "beta"), _act(act), _f32(mean, n_seg * groups, "mean"),
          _f32(rstd, n_seg * groups, "rstd"), _ptr(dX), lddx, _f32(dgamma, C, "dgamma"),
          _f32(dbeta, C, "dbeta"), _ptr(ws), ws.numel(), _current(X, stream))
 
 
+@functools.lru_cache(maxsize=1024)
 def gnn_gated_workspace(n: int, F_in: int, F_mid: int):
     """Workspace bytes of gnn_gated_fwd and gnn_gated_bwd."""
     f, b = ctypes.c_size_t(), ctypes.c_size_t()
@@ -862,7 +882,7 @@ def gnn_gated_bwd(dH, X, n: int, F_in: int, Wg, Wu, F_mid: int, dX=None, dWg=Non
     recomputed).  dH has X's type or fp32."""
     t = _one_type(X, Wg=Wg, Wu=Wu, dX=dX, dWg=dWg, dWu=dWu)
     if ws is None:
-        ws = _workspace_on(gnn_gated_workspace(n, F_in, F_mid)[1], X.device, stream)
+        ws = _scratch(gnn_gated_workspace(n, F_in, F_mid)[1], X, stream)
     call("gnn_gated_bwd", _ptr(dH), _rows(dH, n, F_mid, "dH"), _type(dH), _ptr(X), _rows(X, n, F_in, "X"), t, n,
          F_in, _ptr(Wg), _rows(Wg, F_in, F_mid, "Wg"), _ptr(Wu), _rows(Wu, F_in, F_mid, "Wu"), F_mid, _act(act),
          _ptr(dX), _rows(dX, n, F_in, "dX") if dX is not None else 0,
@@ -916,6 +936,7 @@ def adamw_state(device="cuda"):
     return torch.tensor([0.0, 1.0, 1.0, 0.0], dtype=torch.float64, device=device)
 
 
+@functools.lru_cache(maxsize=1)
 def gnn_adamw_workspace() -> int:
     nb = ctypes.c_size_t()
     call("gnn_adamw_workspace", ctypes.byref(nb))
@@ -932,7 +953,7 @@ def gnn_adamw_step(tensors: AdamwTensors, state, lr: float, beta1: float = 0.9, 
     if state.dtype != torch.float64 or state.numel() != 4 or not state.is_contiguous() or state.device.type != "cuda":
         raise ValueError("state: needs the fp64 CUDA tensor that adamw_state makes")
     if ws is None:
-        ws = _workspace_on(gnn_adamw_workspace(), state.device, stream)
+        ws = _scratch(gnn_adamw_workspace(), state, stream)
     call("gnn_adamw_step", tensors.c, tensors.count, tensors.param_type, tensors.grad_type, tensors.state_bits,
          _ptr(state), float(lr), float(beta1), float(beta2), float(eps), float(weight_decay), float(grad_scale),
          float(max_norm), _f32(grad_norm, 1, "grad_norm"), _ptr(ws), ws.numel(), _current(state, stream))

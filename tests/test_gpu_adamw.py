@@ -257,6 +257,34 @@ def test_other_stream_and_graph_advance_the_step():
     check(dev, host, state, 3, HYPER, torch.tensor(1.0))
 
 
+def test_calls_on_many_streams_and_threads_keep_apart():
+    """Calls without a workspace of their own, in flight at once."""
+    import threading
+    jobs = []
+    for k in range(6):
+        host = make([3000 + k, 70000], "f32", "f32", 32, 20 + k)
+        jobs.append((host, on_gpu(host), G.adamw_state(), torch.zeros(1, device="cuda"), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+
+    def work(k):
+        _, dev, state, norm, stream = jobs[k]
+        T = G.AdamwTensors(**dev)
+        with torch.cuda.stream(stream if k % 2 else torch.cuda.default_stream()):
+            for _ in range(20):
+                G.gnn_adamw_step(T, state, max_norm=math.inf, grad_norm=norm, **HYPER)
+
+    threads = [threading.Thread(target=work, args=(k,)) for k in range(6)]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    G.gnn_sync_check()
+    for host, dev, state, norm, _ in jobs:
+        want = math.sqrt(sum(float(g.double().square().sum()) for g in host["grads"]))
+        assert abs(float(norm) - want) <= 2 ** -22 * want
+        check(dev, host, state, 20, HYPER, torch.tensor(1.0))
+
+
 def test_no_tensors():
     state, norm = G.adamw_state(), torch.full((1,), 5.0, device="cuda")
     G.gnn_adamw_step(G.AdamwTensors([], [], [], []), state, max_norm=1.0, grad_norm=norm, **HYPER)
