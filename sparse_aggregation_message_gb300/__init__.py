@@ -895,8 +895,8 @@ class AdamwTensors:
     """The tensors of an optimiser, checked once: lists of parameters (fp32 or
     bf16, updated in place), their gradients, m, v and, with 8-bit states
     (torch.float8_e4m3fn m and v), the scales m_scale and v_scale (fp32, one
-    per 256 elements of a tensor); copies (bf16, optional) receive the updated
-    parameters.  All are contiguous CUDA tensors and stay the caller's."""
+    per 256 elements of a tensor); copies (bf16, optional, None for a tensor
+    without one) receive the updated parameters.  All are contiguous CUDA tensors and stay the caller's."""
 
     def __init__(self, params, grads, m, v, m_scale=None, v_scale=None, copies=None):
         import torch
@@ -914,6 +914,8 @@ class AdamwTensors:
                     m=state, v=state, m_scale=torch.float32, v_scale=torch.float32, copies=torch.bfloat16)
         for name, ts in lists.items():
             for i, t in enumerate(ts or ()):
+                if t is None and name == "copies":
+                    continue
                 n = params[i].numel()
                 size = -(-n // 256) if name.endswith("scale") else n
                 if t.dtype != want[name] or t.numel() != size or not t.is_contiguous() or t.device.type != "cuda":
@@ -921,7 +923,7 @@ class AdamwTensors:
         self.param_type = _type(params[0]) if k else 0
         self.grad_type = _type(grads[0]) if k else 0
         self._keep = {name: list(ts) for name, ts in lists.items() if ts is not None}
-        at = lambda ts, i: None if ts is None else ts[i].data_ptr()  # noqa: E731
+        at = lambda ts, i: None if ts is None or ts[i] is None else ts[i].data_ptr()  # noqa: E731
         self.c = (GnnAdamwTensor * max(k, 1))(*[
             GnnAdamwTensor(at(params, i), at(grads, i), at(m, i), at(v, i),
                            at(m_scale, i) if self.state_bits == 8 else None,
