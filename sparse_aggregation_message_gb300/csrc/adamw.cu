@@ -21,7 +21,7 @@ namespace gnn {
 namespace {
 
 constexpr int BLOCK = 256;      // elements that share a scale, and of one warp step
-constexpr int MAX_UNITS = 16;   // blocks a warp takes in a row, at most
+constexpr int MAX_UNITS = 8;    // blocks a warp takes in a row, at most
 constexpr int NORM_UNITS = 4;
 constexpr int THREADS = 256;
 constexpr int MAX_TENSORS = 56;  // of one launch: the descriptors stay below 4 KB
@@ -118,7 +118,9 @@ struct Raw {
     } else {
 #pragma unroll
       for (int i = 0; i < W; i += 4)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(part + (threadIdx.x + i / 4 * THREADS) * 16),
+        // through L1: a lane's two halves of eight fp32 values share a sector (past
+        // L1 each half fetched it: 664 against 572 us at 242M elements)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(part + (threadIdx.x + i / 4 * THREADS) * 16),
                      "l"(reinterpret_cast<const char*>(p) + 4 * i)
                      : "memory");
     }
@@ -143,7 +145,12 @@ struct Raw {
 
 template <bool VEC, class T>
 __device__ __forceinline__ void store8(T* p, int live, const float (&v)[8]) {
-  if constexpr (VEC) {
+  if constexpr (VEC && sizeof(T) == 4) {
+    // a whole sector a lane
+    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]),
+                 "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+                 : "memory");
+  } else if constexpr (VEC) {
     store_vec<8>(p, v);
   } else {
 #pragma unroll
@@ -349,9 +356,10 @@ __device__ __forceinline__ void update(const Step<TP, TG, Q8, VEC>& now, const A
 
 // With 8-bit states a lane's next steps are copied into its own slots of shared
 // memory AHEAD steps before their use (no barrier: each lane reads what it
-// copied); registers alone could hold one step ahead.  With fp32 states 24 warps
-// of plain loads reach the bandwidth (6.6 TB/s at 184M elements), and holding a
-// step ahead in registers spilt and lost 7%.
+// copied); registers alone could hold one step ahead.  242M elements take 572 us,
+// 6.8 TB/s.  With fp32 states 24 warps of plain loads reach the bandwidth (184M
+// elements in 736 us, 7.0 TB/s), and holding a step ahead in registers spilt and
+// lost 7%.
 constexpr int AHEAD = 2;
 template <class TP, class TG, bool Q8>
 constexpr int ring_bytes() {
@@ -379,6 +387,7 @@ __global__ void __launch_bounds__(THREADS, 3)
       Step<TP, TG, Q8, true> now;
       if constexpr (Q8) {
         // lanes 0-15 hold the chunk's scales of m, 16-31 those of v
+        static_assert(MAX_UNITS <= 16, "a scale to a lane");
         float scale = 0.f;
         if ((lane & 15) < whole) scale = lane < 16 ? at.ms[lane] : at.vs[lane - 16];
         const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(slots));
@@ -652,8 +661,8 @@ extern "C" gnn_status gnn_adamw_step(const gnn_adamw_tensor* tensors, int32_t n_
         const int k = tab.count++;
         tab.t[k] = t;
         tab.first[k + 1] = tab.first[k] + (t.n + chunk - 1) / chunk;
-        if (aligned_to(t.param, 16) && aligned_to(t.grad, 16) && aligned_to(t.m, q8 ? 8 : 16) &&
-            aligned_to(t.v, q8 ? 8 : 16) && aligned_to(t.copy, 16))
+        if (aligned_to(t.param, 8 * ps) && aligned_to(t.grad, 16) && aligned_to(t.m, q8 ? 8 : 32) &&
+            aligned_to(t.v, q8 ? 8 : 32) && aligned_to(t.copy, 16))
           tab.aligned |= 1ull << k;
       }
       if (tab.count == 0) break;
@@ -688,7 +697,7 @@ extern "C" gnn_status gnn_adamw_step(const gnn_adamw_tensor* tensors, int32_t n_
   const int units = share < 1 ? 1 : share > MAX_UNITS ? MAX_UNITS : (int)share;
   bool first = true;
   return each(units, [&](const Table& tab) -> gnn_status {
-    const gnn_status r = update(st, first, grid_for(tab, 152 * 3 * 4), tab, h, ctl);
+    const gnn_status r = update(st, first, grid_for(tab, 152 * 3 * 16), tab, h, ctl);
     first = false;
     return r;
   });
