@@ -401,6 +401,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) gated_ke
   }
 done:
   if (warp >= 2 && lane == 0) tc::bulk_wait_all();  // stores finish before the block exits
+  __syncwarp();
+  if (*s.abort_flag) {
+    // a wait gave up: what is still in flight (loads, products) lands within
+    // microseconds; nothing may end before that
+    const long long t0 = clock64();
+    while (clock64() - t0 < 4000000) {
+    }
+  }
   tc::fence_before_sync();
   __syncthreads();
   tc::cluster_sync();  // nothing of the partner's arrives here any more

@@ -804,8 +804,8 @@ NormWs norm_ws(void* base, size_t cap, int64_t n, int C, int groups, int n_seg, 
 
 gnn_status check_norm(const char* who, int64_t n, int C, int groups, int n_seg) {
   if (n < 0 || n > (int64_t)0x7fffffff) return fail(GNN_ERR_INVALID_ARG, "%s: bad row count", who);
-  if (C < 1 || groups < 1 || C % groups || n_seg < 1)
-    return fail(GNN_ERR_INVALID_ARG, "%s: needs groups >= 1 that divide C >= 1, and n_seg >= 1", who);
+  if (C < 1 || groups < 1 || C % groups || n_seg < 1 || n_seg > 0x3fffffff)
+    return fail(GNN_ERR_INVALID_ARG, "%s: needs groups >= 1 that divide C >= 1, and 1 <= n_seg < 2^30", who);
   if (C > kMaxF) return fail(GNN_ERR_UNSUPPORTED, "%s: C=%d > %d", who, C, kMaxF);
   return GNN_OK;
 }
@@ -946,7 +946,7 @@ extern "C" gnn_status gnn_group_norm_fwd(const void* X, int64_t ldx, int32_t x_t
   gnn_status s = check_norm(who, n, C, groups, n_seg);
   if (s != GNN_OK) return s;
   if ((s = check_norm_args(who, x_type, y_type, act, seg_start, n_seg, gamma, beta)) != GNN_OK) return s;
-  GNN_REQUIRE(eps > 0 && eps < 1e30, "gnn_group_norm_fwd: eps must be positive");
+  GNN_REQUIRE(eps >= 1.2e-38 && eps < 1e30, "gnn_group_norm_fwd: eps must be positive (a normal fp32 value)");
   GNN_REQUIRE(mean && rstd, "gnn_group_norm_fwd: NULL mean or rstd");
   GNN_REQUIRE(n == 0 || !bad_rows(X, ldx, x_type, C, false), "gnn_group_norm_fwd: X needs 16-byte aligned rows "
               "and ldx >= C");

@@ -290,3 +290,51 @@ def test_no_tensors():
     G.gnn_adamw_step(G.AdamwTensors([], [], [], []), state, max_norm=1.0, grad_norm=norm, **HYPER)
     G.gnn_sync_check()
     assert float(norm) == 0.0 and state[0] == 1.0
+
+
+def test_more_than_2_31_elements():
+    """Offsets past 32 bits: the ends of one tensor of 2.2 G elements, 8-bit states."""
+    n = 2 ** 31 + 70_001
+    z = lambda dt, k=n: torch.zeros(k, dtype=dt, device="cuda")  # noqa: E731
+    dev = dict(params=[z(torch.bfloat16)], grads=[z(torch.bfloat16)], m=[z(F8)], v=[z(F8)],
+               m_scale=[z(torch.float32, -(-n // 256))], v_scale=[z(torch.float32, -(-n // 256))])
+    cut = 256 * ((n - 50_000) // 256)
+    host = make([n - cut], "bf16", "bf16", 8, 18)
+    for k in ("params", "grads", "m", "v"):
+        dev[k][0][cut:] = host[k][0].cuda()
+    for k in ("m_scale", "v_scale"):
+        dev[k][0][cut // 256:] = host[k][0].cuda()
+    state, norm = G.adamw_state(), torch.zeros(1, device="cuda")
+    G.gnn_adamw_step(G.AdamwTensors(**dev), state, max_norm=math.inf, grad_norm=norm, **HYPER)
+    G.gnn_sync_check()
+    want = math.sqrt(float(host["grads"][0].double().square().sum()))
+    assert abs(float(norm) - want) <= 2 ** -22 * want
+    assert not dev["params"][0][:cut].any() and not dev["m_scale"][0][:cut // 256].any()
+    host["copies"] = None
+    tail = {k: [v[0][cut // 256 if k.endswith("scale") else cut:]] for k, v in dev.items()}
+    host["copies"] = [torch.zeros(1)]
+    b1p, b2p = HYPER["beta1"], HYPER["beta2"]
+    r = step(host["params"][0], host["grads"][0], host["m"][0], host["v"][0], host["m_scale"][0], host["v_scale"][0], 1,
+             b1p, b2p, torch.tensor(1.0), HYPER)
+    for k, b in zip(("params", "m", "v", "m_scale", "v_scale"), r):
+        assert same(tail[k][0], b), k
+
+
+@pytest.mark.parametrize("part", range(4))
+def test_roots_and_quotients_of_every_mantissa(part):
+    """The paired square root over all 2^24 mantissas of two neighbouring powers
+    of two (others differ by exact powers of four), and quotients by them: with
+    beta1 = beta2 = 1/2, no gradient and the powers at zero, a step is
+    p = 0 - (m/2) / sqrt(v/2) to the bit."""
+    n = 1 << 22
+    bits = torch.arange(n, dtype=torch.int64) + part * n + (127 << 23)
+    v = 2 * bits.to(torch.int32).view(torch.float32)  # v/2 runs over [1, 4)
+    g = torch.Generator().manual_seed(part)
+    for m in (torch.full((n,), 2.0), torch.randn(n, generator=g), 2 * (1 + torch.rand(n, generator=g)) * 2.0 ** 40):
+        dev = on_gpu(dict(params=[torch.zeros(n)], grads=[torch.zeros(n)], m=[m.clone()], v=[v.clone()]))
+        state = torch.tensor([0.0, 0.0, 0.0, 0.0], dtype=torch.float64, device="cuda")
+        G.gnn_adamw_step(G.AdamwTensors(**dev), state, lr=1.0, beta1=0.5, beta2=0.5, eps=0.0, weight_decay=0.0)
+        G.gnn_sync_check()
+        want = 0 - (m / 2) / torch.sqrt(v / 2)
+        assert torch.equal(dev["params"][0].cpu(), want)
+        assert torch.equal(dev["v"][0].cpu(), v / 2)

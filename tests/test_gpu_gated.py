@@ -203,3 +203,28 @@ def test_repeats_bit_for_bit_on_a_stream_and_in_a_graph():
     G.gnn_sync_check()
     for u, v, w in zip(a, b, c):
         assert torch.equal(u, v) and torch.equal(u, w)
+
+
+def test_more_than_2_31_elements():
+    """Offsets past 32 bits: the last rows of 2.2 G inputs."""
+    n, D, F = 4_300_013, 512, 48
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.zeros(n, D, dtype=torch.bfloat16, device="cuda")
+    last = torch.randn(300, D, generator=g, device="cuda").to(torch.bfloat16)
+    x[-300:] = last
+    wg, wu = mat(D, F, torch.bfloat16, 2, D ** -0.5)[1], mat(D, F, torch.bfloat16, 3, D ** -0.5)[1]
+    h = mat(n, F, torch.bfloat16, 4, fill=float("nan"))[1]
+    G.gnn_gated_fwd(x, n, D, wg, wu, F, h)
+    dh = torch.zeros(n, F, dtype=torch.bfloat16, device="cuda")
+    dh[-300:] = torch.randn(300, F, generator=g, device="cuda").to(torch.bfloat16)
+    dx, dwg, dwu = torch.empty_like(x), torch.empty(D, F, dtype=torch.bfloat16, device="cuda"), torch.empty(D, F, dtype=torch.bfloat16, device="cuda")
+    G.gnn_gated_bwd(dh, x, n, D, wg, wu, F, dx, dwg, dwu)
+    few_h, few = torch.empty(300, F, dtype=torch.bfloat16, device="cuda"), [torch.empty_like(v) for v in (last, dwg, dwu)]
+    G.gnn_gated_fwd(last, 300, D, wg, wu, F, few_h)
+    G.gnn_gated_bwd(dh[-300:].clone(), last, 300, D, wg, wu, F, *few)
+    G.gnn_sync_check()
+    assert not h[:-300].any() and not dx[:-300].any()
+    assert torch.equal(h[-300:], few_h) and torch.equal(dx[-300:], few[0])
+    # the rows fall into other blocks of the sums: fp32 orders differ, then one rounding each
+    for a, b in ((dwg, few[1]), (dwu, few[2])):
+        assert torch.all((a.double() - b.double()).abs() <= 2 * torch.finfo(torch.bfloat16).eps * b.double().abs() + 1e-4 * b.double().abs().mean())

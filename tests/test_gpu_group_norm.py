@@ -296,3 +296,32 @@ def test_segments_that_are_not_ascending_are_flagged():
     with pytest.raises(G.GnnError):
         G.gnn_sync_check()
     G.gnn_sync_check()  # the flag is cleared
+
+
+def test_more_than_2_31_elements():
+    """Offsets past 32 bits: the first and the last segment of 2.2 G elements."""
+    n, C, groups = 2_150_000, 1024, 8
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.empty(n, C, dtype=torch.bfloat16, device="cuda")
+    for a in range(0, n, 100_000):
+        x[a:a + 100_000] = torch.randn(min(100_000, n - a), C, generator=g, device="cuda").to(torch.bfloat16)
+    seg = torch.tensor([0, 1000, n - 700, n], device="cuda")
+    y, mean, rstd = torch.empty_like(x), torch.empty(3, groups, device="cuda"), torch.empty(3, groups, device="cuda")
+    G.gnn_group_norm_fwd(x, n, C, groups, y, mean, rstd, seg_start=seg, act="silu")
+    dx, dg, db = torch.empty_like(x), torch.empty(C, device="cuda"), torch.empty(C, device="cuda")
+    G.gnn_group_norm_bwd(y, x, n, C, groups, mean, rstd, dx, dgamma=dg, dbeta=db, seg_start=seg, act="silu")
+    G.gnn_sync_check()
+    for a, b in ((0, 1000), (n - 700, n)):
+        o = torch.empty(b - a, C, dtype=torch.bfloat16, device="cuda")
+        m, r = torch.empty(1, groups, device="cuda"), torch.empty(1, groups, device="cuda")
+        part = x[a:b].clone()
+        G.gnn_group_norm_fwd(part, b - a, C, groups, o, m, r, act="silu")
+        *_, z = reference(part, None, groups, torch.ones(C, device="cuda"), torch.zeros(C, device="cuda"), 1e-5, "silu")
+        ref, _ = act64(z, "silu")
+        half = torch.finfo(torch.bfloat16).eps / 2
+        for got in (y[a:b], o):
+            assert torch.all((got.double() - ref).abs() <= half * ref.abs() + 1e-4 * (1 + z.abs()))
+        d = torch.empty_like(o)
+        G.gnn_group_norm_bwd(y[a:b].clone(), part, b - a, C, groups, m, r, d, act="silu")
+        scale = d.double().abs() + d.double().square().mean().sqrt()
+        assert torch.all((dx[a:b].double() - d.double()).abs() <= (2 * half + 1e-3) * scale)

@@ -26,7 +26,7 @@ def norm_fwd(lib, X=4096, ldx=64, xt=F32, n=10, C=64, groups=8, seg=None, n_seg=
     (dict(X=None), INVALID), (dict(X=4100), INVALID), (dict(ldx=63), INVALID), (dict(ldx=60), INVALID),
     (dict(n=-1), INVALID), (dict(C=0), INVALID), (dict(groups=0), INVALID), (dict(groups=7), INVALID),
     (dict(C=1032, groups=8, ldx=1032, ldy=1032), UNSUPPORTED), (dict(n_seg=0), INVALID), (dict(n_seg=2), INVALID),
-    (dict(eps=0.0), INVALID), (dict(eps=-1.0), INVALID), (dict(eps=float("nan")), INVALID), (dict(act=5), INVALID),
+    (dict(eps=0.0), INVALID), (dict(eps=-1.0), INVALID), (dict(eps=float("nan")), INVALID), (dict(eps=1e-60), INVALID), (dict(seg=64, n_seg=1 << 30), INVALID), (dict(act=5), INVALID),
     (dict(act=-1), INVALID), (dict(xt=3), INVALID), (dict(xt=BF16, yt=F32), UNSUPPORTED), (dict(xt=F16, yt=BF16), UNSUPPORTED),
     (dict(Y=None), INVALID), (dict(yt=BF16, ldy=68), INVALID), (dict(mean=None), INVALID), (dict(rstd=None), INVALID),
     (dict(ws=None), INVALID), (dict(ws_bytes=8), INVALID), (dict(seg=4), INVALID), (dict(gamma=2), INVALID),
