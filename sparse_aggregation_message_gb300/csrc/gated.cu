@@ -24,6 +24,8 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
+
 #include "gemm.h"
 #include "internal.h"
 #include "nodewise.cuh"
@@ -160,16 +162,14 @@ __device__ __forceinline__ float2 pair_at(const uint32_t* v, int i) {
   return make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1]));
 }
 
+// The tiles pair, pair + pairs, ... of one product, by one pair of CTAs.
 template <Mode M, class T>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) gated_kernel(const __grid_constant__ Args g) {
-  extern __shared__ uint8_t smem_raw[];
-  cudaTriggerProgrammaticLaunchCompletion();
+__device__ __forceinline__ void walk_tiles(const Args& g, uint8_t* smem_raw, int pair, int pairs) {
   const Smem s = carve<M>(smem_raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
   constexpr int ST = stages(M);
   const int rank = (int)tc::cluster_rank();
-  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   if (threadIdx.x == 0) {
     for (int i = 0; i < ST; ++i) {
       tc::mbar_init(&s.full[i], 1);
@@ -418,6 +418,28 @@ done:
   }
 }
 
+template <Mode M, class T>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) gated_kernel(const __grid_constant__ Args g) {
+  extern __shared__ uint8_t smem_raw[];
+  cudaTriggerProgrammaticLaunchCompletion();
+  walk_tiles<M, T>(g, smem_raw, blockIdx.x >> 1, gridDim.x >> 1);
+}
+
+// DX on the first dx_pairs pairs of CTAs and DW on the others: neither needs the
+// other, a small one alone leaves most SMs idle, and two uneven last rounds of
+// tiles become one.
+template <class T>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
+    gated_grads_kernel(const __grid_constant__ Args dx, const __grid_constant__ Args dw, int dx_pairs) {
+  extern __shared__ uint8_t smem_raw[];
+  cudaTriggerProgrammaticLaunchCompletion();
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  if (pair < dx_pairs)
+    walk_tiles<DX, T>(dx, smem_raw, pair, dx_pairs);
+  else
+    walk_tiles<DW, T>(dw, smem_raw, pair - dx_pairs, pairs - dx_pairs);
+}
+
 // dWg and dWu from the split partials, added in split order; padding columns
 // up to a multiple of 16 come out zero (their partials are).
 template <class T>
@@ -561,32 +583,54 @@ int sm_count() {
 
 int64_t up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 
-// The split of the weight gradients over the rows: the number of parts whose
-// rounds of tiles over the SMs take the fewest k blocks, each part at least
-// eight of them and its tile's drain counted as four.
-struct DwPlan {
-  int num_m, num_n, splits, kb_per_split;
+// How the gradients' products share the card: which pairs of CTAs take DX and
+// into how many parts DW's sum over the rows is split, by the rounds of tiles they
+// take, counted in k blocks (a tile's start and drain as four).
+constexpr int PAIRS = 76;
+struct GradPlan {
+  int dw_m, dw_n, splits, kb_per_split;  // DW's tiles and split
+  int dx_bn, dx_n;                       // DX's tile columns and column tiles
+  int dx_pairs;                          // 0: DX and DW by themselves
   size_t part_floats;
 };
-DwPlan dw_plan(int64_t n, int D, int F) {
-  DwPlan p;
-  p.num_m = (D + BM - 1) / BM;
-  p.num_n = (F + BN - 1) / BN;
-  const int64_t kb = (n + BK - 1) / BK, tiles = 2ll * p.num_m * p.num_n;
+
+int64_t dw_split(int64_t tiles, int64_t kb, int pairs, int* splits, int* per_split) {
   int64_t best = -1;
-  p.splits = 1;
-  p.kb_per_split = (int)(kb > 0 ? kb : 1);
-  for (int64_t s = 1; s <= 76 && s * 8 <= (kb > 8 ? kb : 8); ++s) {
-    if (s > 1 && s * tiles > 4 * 76) break;  // bounds the partials
-    const int64_t per = (kb + s - 1) / s, used = (kb + per - 1) / (per > 0 ? per : 1);
-    const int64_t rounds = (used * tiles + 75) / 76, cost = rounds * (per + 4);
-    if (used > 0 && (best < 0 || cost < best)) {
+  for (int64_t s = 1; s <= PAIRS && (s == 1 || (s * 8 <= kb && s * tiles <= 4 * PAIRS)); ++s) {
+    const int64_t per = std::max<int64_t>((kb + s - 1) / s, 1), used = std::max<int64_t>((kb + per - 1) / per, 1);
+    const int64_t cost = (used * tiles + pairs - 1) / pairs * (per + 4);
+    if (best < 0 || cost < best) {
       best = cost;
-      p.splits = (int)used;
-      p.kb_per_split = (int)per;
+      *splits = (int)used;
+      *per_split = (int)per;
     }
   }
-  p.part_floats = (size_t)p.splits * 2 * p.num_m * BM * p.num_n * BN;
+  return best;
+}
+
+GradPlan grad_plan(int64_t n, int D, int F, bool both) {
+  GradPlan p{};
+  p.dw_m = (D + BM - 1) / BM, p.dw_n = (F + BN - 1) / BN;
+  const int num_n = (D + BN - 1) / BN;
+  p.dx_bn = (int)up((D + num_n - 1) / num_n, 64), p.dx_n = (D + p.dx_bn - 1) / p.dx_bn;
+  const int64_t dw_tiles = 2ll * p.dw_m * p.dw_n, kb = (n + BK - 1) / BK;
+  const int64_t dx_tiles = (n + BM - 1) / BM * p.dx_n, dx_len = 2 * ((F + BK - 1) / BK) + 4;
+  int64_t best = dw_split(dw_tiles, kb, PAIRS, &p.splits, &p.kb_per_split);
+  if (both) {
+    best += (dx_tiles + PAIRS - 1) / PAIRS * dx_len + 10;  // one launch after the other
+    for (int at = 4; at < PAIRS; at += 4) {
+      const int pairs = (int)std::min<int64_t>(at, dx_tiles);
+      int s, per;
+      const int64_t cost = std::max((dx_tiles + pairs - 1) / pairs * dx_len,
+                                    dw_split(dw_tiles, kb, PAIRS - pairs, &s, &per));
+      if (cost < best) {
+        best = cost;
+        p.dx_pairs = pairs, p.splits = s, p.kb_per_split = per;
+      }
+      if (pairs < at) break;
+    }
+  }
+  p.part_floats = (size_t)p.splits * 2 * p.dw_m * BM * p.dw_n * BN;
   return p;
 }
 
@@ -603,7 +647,7 @@ GatedWs gated_ws(void* base, size_t cap, int64_t n, int D, int F, bool* ok) {
   w.ldf = up(F, 8);
   w.dg = ar.take<uint16_t>((size_t)n * w.ldf);
   w.du = ar.take<uint16_t>((size_t)n * w.ldf);
-  w.part = ar.take<float>(dw_plan(n, D, F).part_floats);
+  w.part = ar.take<float>(std::max(grad_plan(n, D, F, true).part_floats, grad_plan(n, D, F, false).part_floats));
   w.bytes = ar.used;
   *ok = ar.ok();
   return w;
@@ -710,36 +754,45 @@ gnn_status gated_bwd(int64_t n, int D, int F, int act, int dh_f32, Mat dH, Mat X
     GNN_TRY(map16<T>(&g.out[0], w.dg, n, F, w.ldf, 64, 32));
     GNN_TRY(map16<T>(&g.out[1], w.du, n, F, w.ldf, 64, 32));
     GNN_TRY((launch_gated<ACT, T>(false, g, st)));
-    if (dX.p) {
-      Args d{};
-      d.flags = g.flags;
-      const int num_n = (D + BN - 1) / BN;
-      d.bn = (int)up((D + num_n - 1) / num_n, 64);
-      d.num_m = g.num_m, d.num_n = (D + d.bn - 1) / d.bn, d.num_kb = (F + BK - 1) / BK;
-      GNN_TRY(map16<T>(&d.a[0], w.dg, n, F, w.ldf, BK, CM));
-      GNN_TRY(map16<T>(&d.a[1], w.du, n, F, w.ldf, BK, CM));
-      GNN_TRY(map16<T>(&d.b[0], Wg.p, D, F, Wg.ld, BK, d.bn / 2));
-      GNN_TRY(map16<T>(&d.b[1], Wu.p, D, F, Wu.ld, BK, d.bn / 2));
-      GNN_TRY(map16<T>(&d.out[0], dX.p, n, up(D, 16), dX.ld, 64, 32));
-      GNN_TRY((launch_gated<DX, T>(true, d, st)));
+  }
+  const GradPlan p = grad_plan(n, D, F, dX.p && dWg.p);
+  Args x{}, v{};
+  if (n > 0 && dX.p) {
+    x.flags = device_flags();
+    x.bn = p.dx_bn, x.num_m = (int)((n + BM - 1) / BM), x.num_n = p.dx_n, x.num_kb = (F + BK - 1) / BK;
+    GNN_TRY(map16<T>(&x.a[0], w.dg, n, F, w.ldf, BK, CM));
+    GNN_TRY(map16<T>(&x.a[1], w.du, n, F, w.ldf, BK, CM));
+    GNN_TRY(map16<T>(&x.b[0], Wg.p, D, F, Wg.ld, BK, x.bn / 2));
+    GNN_TRY(map16<T>(&x.b[1], Wu.p, D, F, Wu.ld, BK, x.bn / 2));
+    GNN_TRY(map16<T>(&x.out[0], dX.p, n, up(D, 16), dX.ld, 64, 32));
+  }
+  if (n > 0 && dWg.p) {
+    v.flags = device_flags();
+    v.num_m = p.dw_m, v.num_n = p.dw_n, v.num_kb = (int)((n + BK - 1) / BK);
+    v.splits = p.splits, v.kb_per_split = p.kb_per_split, v.part = w.part;
+    GNN_TRY(map16<T>(&v.a[0], X.p, n, D, X.ld, 64, BK));
+    GNN_TRY(map16<T>(&v.b[0], w.dg, n, F, w.ldf, 64, BK));
+    GNN_TRY(map16<T>(&v.b[1], w.du, n, F, w.ldf, 64, BK));
+  }
+  if (n > 0 && p.dx_pairs) {
+    static bool ready = false;
+    constexpr int smem = smem_bytes(DX) > smem_bytes(DW) ? smem_bytes(DX) : smem_bytes(DW);
+    if (!ready) {
+      GNN_CUDA(cudaFuncSetAttribute(gated_grads_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+      ready = true;
     }
+    const int64_t dw_tiles = 2ll * p.dw_m * p.dw_n * p.splits;
+    const int pairs = p.dx_pairs + (int)std::min<int64_t>(dw_tiles, sm_count() / 2 - p.dx_pairs);
+    GNN_TRY(launch(true, 2 * pairs, THREADS, smem, st, gated_grads_kernel<T>, x, v, p.dx_pairs));
+  } else if (n > 0) {
+    if (dX.p) GNN_TRY((launch_gated<DX, T>(true, x, st)));
+    if (dWg.p) GNN_TRY((launch_gated<DW, T>(true, v, st)));
   }
   if (dWg.p) {
-    const DwPlan p = dw_plan(n, D, F);
-    int splits = 0;
-    if (n > 0) {
-      Args d{};
-      d.flags = device_flags();
-      d.num_m = p.num_m, d.num_n = p.num_n, d.num_kb = (int)((n + BK - 1) / BK);
-      d.splits = splits = p.splits, d.kb_per_split = p.kb_per_split, d.part = w.part;
-      GNN_TRY(map16<T>(&d.a[0], X.p, n, D, X.ld, 64, BK));
-      GNN_TRY(map16<T>(&d.b[0], w.dg, n, F, w.ldf, 64, BK));
-      GNN_TRY(map16<T>(&d.b[1], w.du, n, F, w.ldf, 64, BK));
-      GNN_TRY((launch_gated<DW, T>(true, d, st)));
-    }
-    const int64_t work = 2ll * D * (up(F, 16) / 8), ldp = (int64_t)p.num_n * BN;
-    GNN_TRY(launch(n > 0, (int)((work + 255) / 256), 256, 0, st, gated_dw_kernel<T>, (const float*)w.part, splits, D, F,
-                   ldp, (int64_t)p.num_m * BM * ldp, static_cast<T*>(dWg.p), dWg.ld, static_cast<T*>(dWu.p), dWu.ld));
+    const int64_t work = 2ll * D * (up(F, 16) / 8), ldp = (int64_t)p.dw_n * BN;
+    GNN_TRY(launch(n > 0, (int)((work + 255) / 256), 256, 0, st, gated_dw_kernel<T>, (const float*)w.part,
+                   n > 0 ? p.splits : 0, D, F, ldp, (int64_t)p.dw_m * BM * ldp, static_cast<T*>(dWg.p), dWg.ld,
+                   static_cast<T*>(dWu.p), dWu.ld));
   }
   return GNN_OK;
 }
