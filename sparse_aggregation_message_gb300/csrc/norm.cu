@@ -1,13 +1,20 @@
 // Group norm with an activation, channels last, over contiguous row ranges
 // ("segments": graphs of a batch, or partitions), forward and backward.
 //
-// The rows are cut into tiles of R.  A segment of at most 2R rows is "short":
-// the block of the tile it starts in takes it whole, statistics and output in
-// one launch (the second read of its rows comes from L1/L2).  A longer segment
-// is cut at the tile borders: the first launch leaves per (piece, group)
-// partials, the second joins them in piece order, the third forms the output.
-// The piece of segment s in tile t has index t + s, which is unique because
-// both only grow along the rows; so no plan has to be built from seg_start.
+// The rows are cut into tiles of R.  A segment of at most max(2R, 256) rows is
+// "short": the block of the tile it starts in takes it whole, statistics and
+// output in one launch (the second read of its rows comes from shared memory, L1
+// or L2).  A longer segment is cut at the tile borders: the first launch leaves
+// per (piece, group) partials, the second joins them in piece order, the third
+// forms the output.  The piece of segment s in tile t has index t + s, which is
+// unique because both only grow along the rows; so no plan has to be built from
+// seg_start.
+//
+// Bound by memory where segments are long: X (backward: X and dY) is read twice,
+// since a segment of a partition does not stay on the chip.  716847 x 300 fp32 to
+// bf16 in 8 segments: 344 us, 6.3 TB/s with the second read; 232965 x 602
+// backward: 376 us, 6.0 TB/s.  Many short segments (65537 x 256 in 2800, backward
+// with gelu: 79 us for 0.2 GB) are bound by what a block does once per segment.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -768,8 +775,12 @@ __global__ void __launch_bounds__(block_threads(V), bwd_blocks(V, false)) norm_b
 // to what their partials cost (measured with 4, 8, 16: 716847 x 300 in 8 segments
 // forward 365, 342, 326 us; 232965 x 602 in 8 backward 365, 368, 387 us; 65537 x
 // 256 in 2800 backward, with 10 kept rows a thread, -, 78, 94 us).  A tile has at
-// least 16 rows.  Segments are taken for short where they have 256 rows or fewer
-// in the mean.
+// least 16 rows, and 16 a thread while that leaves two tiles an SM.
+//
+// Blocks are small where the segments have kShortMean rows or fewer in the mean
+// (65537 x 256, small against large blocks, forward and backward: 51, 78 against
+// 76, 81 us at 23 rows; 56, 98 against 61, 83 us at 55).  A segment of kShortRows
+// or fewer is one block's in any case.
 constexpr int kShortRows = 256, kShortMean = 40;
 
 int tile_rows(int64_t n, int RP, bool backward, bool small) {
