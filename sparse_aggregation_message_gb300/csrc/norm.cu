@@ -297,13 +297,10 @@ __device__ __forceinline__ void block_sums(const NormArgs& a, int width, const f
   __syncthreads();
 }
 
-// Y of the rows [ra, rb) from per-group (mean, rstd), last rows first: those
-// are the ones the statistics pass read last and the caches still hold.
-template <class TX, class TY, int V>
-__device__ __forceinline__ void fwd_rows(const NormArgs& a, const Place<V>& p, int ra, int rb,
-                                         const float* gmean, const float* grstd, char* ring) {
-  const int rows = p.rows(a, ra, rb);
-  float mu[V], sc[V], bt[V];
+// Mean, gamma rstd and beta of a thread's channels.
+template <int V>
+__device__ __forceinline__ void fwd_channels(const NormArgs& a, const Place<V>& p, const float* gmean,
+                                             const float* grstd, float (&mu)[V], float (&sc)[V], float (&bt)[V]) {
   load_channels<V>(a.gamma, p, a.C, 1.f, sc);
   load_channels<V>(a.beta, p, a.C, 0.f, bt);
 #pragma unroll
@@ -311,6 +308,27 @@ __device__ __forceinline__ void fwd_rows(const NormArgs& a, const Place<V>& p, i
     mu[k] = gmean[p.g[k]];
     sc[k] *= grstd[p.g[k]];
   }
+}
+// act((x - mean) gamma rstd + beta)
+template <int V, class Act>
+__device__ __forceinline__ void fwd_output(const float (&x)[V], const float (&mu)[V], const float (&sc)[V],
+                                           const float (&bt)[V], float (&y)[V], Act act) {
+#pragma unroll
+  for (int k = 0; k < V; k += 2) {
+    const float2 d = add2_rn(make_float2(x[k], x[k + 1]), make_float2(-mu[k], -mu[k + 1]));
+    const float2 v = act2(fma2_rn(d, make_float2(sc[k], sc[k + 1]), make_float2(bt[k], bt[k + 1])), act);
+    y[k] = v.x, y[k + 1] = v.y;
+  }
+}
+
+// Y of the rows [ra, rb) from per-group (mean, rstd), last rows first: those
+// are the ones the statistics pass read last and the caches still hold.
+template <class TX, class TY, int V>
+__device__ __forceinline__ void fwd_rows(const NormArgs& a, const Place<V>& p, int ra, int rb,
+                                         const float* gmean, const float* grstd, char* ring) {
+  const int rows = p.rows(a, ra, rb);
+  float mu[V], sc[V], bt[V];
+  fwd_channels<V>(a, p, gmean, grstd, mu, sc, bt);
   const int64_t last = ra + p.ro + (rows - 1) * a.RP;
   const TX* X = static_cast<const TX*>(a.X) + last * a.ldx + p.c0;
   TY* Y = static_cast<TY*>(a.out) + last * a.ldo + p.c0;
@@ -323,12 +341,7 @@ __device__ __forceinline__ void fwd_rows(const NormArgs& a, const Place<V>& p, i
   with_act(a.act, [&](auto act) {
     stream_rows<V, FWD_DEPTH, false>(ring, rows, X, -dx, X, 0, [&](float (&x)[V], float (&)[V]) {
       float y[V];
-#pragma unroll
-      for (int k = 0; k < V; k += 2) {
-        const float2 d = add2_rn(make_float2(x[k], x[k + 1]), make_float2(-mu[k], -mu[k + 1]));
-        const float2 v = act2(fma2_rn(d, make_float2(sc[k], sc[k + 1]), make_float2(bt[k], bt[k + 1])), act);
-        y[k] = v.x, y[k + 1] = v.y;
-      }
+      fwd_output<V>(x, mu, sc, bt, y, act);
       clear_padding<V>(p, a.C, y);
       store_vec<V>(Y, y);
       Y -= dy;
@@ -355,20 +368,54 @@ __global__ void __launch_bounds__(block_threads(V, SMALL), fwd_blocks(V, SMALL))
   const TX* X = static_cast<const TX*>(a.X);
   const int t = blockIdx.x;
   int left = 0;  // pieces of long segments
+  // slot i of this thread: its i-th row of a short segment, kept for the output
+  const uint32_t slots = static_cast<uint32_t>(__cvta_generic_to_shared(ring)) + threadIdx.x * 16;
+  const uint32_t next = blockDim.x * 16;
   for_pieces(a, t, [&](int s, int ra, int rb, bool whole) {
     left |= !whole;
+    const bool keep = whole && rb - ra <= a.keep * a.RP;
+    const int rows = p.rows(a, ra, rb);
     if (p.on) {
       constexpr int U = 32 / V;
       float piv[V], S[V], Q[V];
+      const TX* at = X + (ra + p.ro) * a.ldx + p.c0;
+      const int64_t dx = (int64_t)a.RP * a.ldx;
+      if (keep && p.in) {
+        for (int i = 0; i < rows; ++i, at += dx) copy_async<16>(slots + i * next, at);
+        copy_commit();
+      }
 #pragma unroll
       for (int k = 0; k < V; ++k) {
         piv[k] = to_f32(X[ra * a.ldx + (int64_t)p.g[k] * a.cg]);
         S[k] = 0.f;
         Q[k] = 0.f;
       }
-      const TX* at = X + (ra + p.ro) * a.ldx + p.c0;
-      const int64_t dx = (int64_t)a.RP * a.ldx;
-      for (int i = p.in ? p.rows(a, ra, rb) : 0; i > 0; i -= U) {
+      const auto add = [&](const float (&x)[V]) {
+#pragma unroll
+        for (int k = 0; k < V; k += 2) {
+          const float2 d = add2_rn(make_float2(x[k], x[k + 1]), make_float2(-piv[k], -piv[k + 1]));
+          const float2 s2 = add2_rn(make_float2(S[k], S[k + 1]), d);
+          const float2 q2 = fma2_rn(d, d, make_float2(Q[k], Q[k + 1]));
+          S[k] = s2.x, S[k + 1] = s2.y, Q[k] = q2.x, Q[k + 1] = q2.y;
+        }
+      };
+      if (keep) {
+        copy_wait<0>();
+        int i = 0;
+        for (; p.in && i + 4 <= rows; i += 4) {
+          float x[4][V];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) load_shared<V, TX>(slots + (i + u) * next, x[u]);
+#pragma unroll
+          for (int u = 0; u < 4; ++u) add(x[u]);
+        }
+        for (; p.in && i < rows; ++i) {
+          float x[V];
+          load_shared<V, TX>(slots + i * next, x);
+          add(x);
+        }
+      }
+      for (int i = p.in && !keep ? rows : 0; i > 0; i -= U) {
         float x[U][V];
 #pragma unroll
         for (int u = 0; u < U; ++u, at += dx) {
@@ -380,13 +427,7 @@ __global__ void __launch_bounds__(block_threads(V, SMALL), fwd_blocks(V, SMALL))
           }
         }
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-          for (int k = 0; k < V; ++k) {
-            const float d = x[u][k] - piv[k];
-            S[k] += d;
-            Q[k] += d * d;
-          }
+        for (int u = 0; u < U; ++u) add(x[u]);
       }
       store_vec<V>(red1 + p.ro * width + p.c0, S);
       store_vec<V>(red2 + p.ro * width + p.c0, Q);
@@ -406,10 +447,24 @@ __global__ void __launch_bounds__(block_threads(V, SMALL), fwd_blocks(V, SMALL))
         a.part[((int64_t)t + s) * a.groups + g] = make_float2(mean, m2);
       }
     });
-    if (whole) {
+    if (keep) {
+      float mu[V], sc[V], bt[V];
+      fwd_channels<V>(a, p, gm, gr, mu, sc, bt);
+      TY* Y = static_cast<TY*>(a.out) + (ra + p.ro) * a.ldo + p.c0;
+      const int64_t dy = (int64_t)a.RP * a.ldo;
+      with_act(a.act, [&](auto act) {
+        for (int i = 0; i < rows; ++i, Y += dy) {
+          float x[V] = {}, y[V];
+          if (p.in) load_shared<V, TX>(slots + i * next, x);
+          fwd_output<V>(x, mu, sc, bt, y, act);
+          clear_padding<V>(p, a.C, y);
+          store_vec<V>(Y, y);
+        }
+      });
+    } else if (whole) {
       fwd_rows<TX, TY, V>(a, p, ra, rb, gm, gr, ring);
-      __syncthreads();  // gm, gr and the partials are written again
     }
+    if (whole) __syncthreads();  // gm, gr, the partials and the slots are written again
   });
   if (threadIdx.x == 0) a.has_long[t] = left;
 }
@@ -786,7 +841,8 @@ constexpr int kShortRows = 256, kShortMean = 40;
 int tile_rows(int64_t n, int RP, bool backward, bool small) {
   const auto per = [&](int64_t tiles) { return (int)((n + tiles - 1) / tiles); };
   int R = per(small || backward ? 152 * 8 : 152 * 16);
-  if (!small) R = std::max(R, std::min(16 * RP, per(152 * 2)));
+  // whole turns of two blocks an SM, 16 rows a thread where they allow it
+  if (!small) R = std::max(R, per(152 * 2 * std::max<int64_t>(n / (16 * RP) / (152 * 2), 1)));
   return std::max(R, std::max(RP, 16));
 }
 int64_t most_tiles(int64_t n) {
@@ -860,7 +916,7 @@ int plan(NormArgs& a, int pad, int V, bool backward, bool* small) {
   a.RP = block_threads(V, *small) / a.CH;
   a.R = tile_rows(a.n, a.RP, backward, *small);
   a.longest = 2 * a.R > kShortRows ? 2 * a.R : kShortRows;
-  a.keep = *small ? 40 / V : 28 / V;
+  a.keep = backward ? (*small ? 40 / V : 28 / V) : (*small ? 12 : 10);
   a.tiles = (int)(((int64_t)a.n + a.R - 1) / a.R);
   return (a.RP * a.CH + 31) / 32 * 32;
 }
@@ -878,7 +934,8 @@ template <class TX, class TY, int V, bool SMALL>
 gnn_status norm_fwd(NormArgs a, int threads, cudaStream_t st) {
   static bool ready1 = false, ready2 = false;
   const size_t ring = (size_t)2 * (FWD_DEPTH + 1) * threads * V * sizeof(TX);
-  const size_t smem = sizeof(float) * (size_t)(2 * a.RP * a.CH * V + 2 * a.C + 2 * a.groups) + 16 + ring;
+  const size_t kept = (size_t)a.keep * threads * V * sizeof(TX);
+  const size_t smem = sizeof(float) * (size_t)(2 * a.RP * a.CH * V + 2 * a.C + 2 * a.groups) + 16 + std::max(ring, kept);
   const Launch l{st};
   gnn_status s = allow_smem(norm_fwd_stats_kernel<TX, TY, V, SMALL>, ready1);
   if (s == GNN_OK) s = allow_smem(norm_fwd_apply_kernel<TX, TY, V>, ready2);
