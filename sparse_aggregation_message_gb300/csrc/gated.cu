@@ -170,6 +170,10 @@ __device__ __forceinline__ void walk_tiles(const Args& g, uint8_t* smem_raw, int
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
   constexpr int ST = stages(M);
   const int rank = (int)tc::cluster_rank();
+  if (warp == 0 && lane < 2) {  // the maps arrive while the barriers are set up
+    tc::prefetch_tmap(&g.a[M == DX ? lane : 0]);
+    tc::prefetch_tmap(&g.b[lane]);
+  }
   if (threadIdx.x == 0) {
     for (int i = 0; i < ST; ++i) {
       tc::mbar_init(&s.full[i], 1);
