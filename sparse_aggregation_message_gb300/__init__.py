@@ -160,26 +160,52 @@ _scratch_of = threading.local()
 _SCRATCH_MOST = 32 << 20
 
 
+class _Torch:
+    """What the node-wise calls use of torch, looked up once: a small call takes
+    a few microseconds, of which an import statement was a noticeable part."""
+
+    def __init__(self):
+        import torch
+        self.types = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+        self.f32, self.f64, self.i64, self.u8 = torch.float32, torch.float64, torch.int64, torch.uint8
+        self.empty, self.on_stream = torch.empty, torch.cuda.stream
+        self.raw_stream, self.capturing = torch._C._cuda_getCurrentRawStream, torch._C._cuda_isCurrentStreamCapturing
+
+
+_bits = None
+
+
+def _torch_bits() -> _Torch:
+    global _bits
+    if _bits is None:
+        _bits = _Torch()
+    return _bits
+
+
 def _scratch(nbytes: int, t, stream):
-    """Workspace of a call on t that brings none.  A thread keeps one small
-    buffer for each device and stream it calls on (what runs there is ordered;
-    an allocation a call cost as much time as three launches).  Large ones, calls
-    on a stream of their own and calls that are captured into a graph allocate:
-    on the call's stream, so that the allocator hands the memory out again only
-    behind the call's work, and in the graph's own pool."""
-    import torch
+    """(pointer, bytes, owner) of a workspace for a call on t that brings none.
+    A thread keeps one small buffer for each device and stream it calls on (what
+    runs there is ordered; an allocation a call cost as much time as three
+    launches).  Large ones, calls on a stream of their own and calls that are
+    captured into a graph allocate: on the call's stream, so that the allocator
+    hands the memory out again only behind the call's work, and in the graph's own
+    pool."""
+    b = _bits or _torch_bits()
     if stream is not None:
-        with torch.cuda.stream(stream):
-            return torch.empty(nbytes, dtype=torch.uint8, device=t.device)
-    if nbytes > _SCRATCH_MOST or torch._C._cuda_isCurrentStreamCapturing():
-        return torch.empty(nbytes, dtype=torch.uint8, device=t.device)
-    kept = _scratch_of.__dict__
-    dev = t.get_device()
-    key = (dev, torch._C._cuda_getCurrentRawStream(dev))
-    buf = kept.get(key)
-    if buf is None or buf.numel() < nbytes:
-        buf = kept[key] = torch.empty(max(nbytes, 1 << 20), dtype=torch.uint8, device=t.device)
-    return buf
+        with b.on_stream(stream):
+            buf = b.empty(nbytes, dtype=b.u8, device=t.device)
+    elif nbytes > _SCRATCH_MOST or b.capturing():
+        buf = b.empty(nbytes, dtype=b.u8, device=t.device)
+    else:
+        kept = _scratch_of.__dict__
+        dev = t.get_device()
+        key = (dev, b.raw_stream(dev))
+        mine = kept.get(key)
+        if mine is None or mine[1] < nbytes:
+            buf = b.empty(max(nbytes, 1 << 20), dtype=b.u8, device=t.device)
+            mine = kept[key] = (buf.data_ptr(), buf.numel(), buf)
+        return mine
+    return buf.data_ptr(), buf.numel(), buf
 
 
 def gnn_csr_build(n: int, src, dst, flags: int = CSR_GCN, stream=None) -> Csr:
@@ -758,58 +784,60 @@ def gnn_gat_layer_bwd(csr: Csr, bnd: Optional[Boundary], tpos, spos, dH_out, H_o
 ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "sigmoid": 4}
 
 
-_TYPES = {}  # torch dtype -> GNN_F32, GNN_BF16, GNN_F16
-
-
 def _type(t) -> int:
     """The library's number of a tensor's type (-1, which it refuses, for one it does not have)."""
-    if not _TYPES:
-        import torch
-        _TYPES.update({torch.float32: 0, torch.bfloat16: 1, torch.float16: 2})
-    return _TYPES.get(t.dtype, -1)
+    return (_bits or _torch_bits()).types.get(t.dtype, -1)
 
 
 def _rows(t, n: int, F: int, what: str) -> int:
     """Row stride of a matrix that holds n rows of F columns, each contiguous."""
     shape = t.shape
-    if len(shape) != 2 or shape[0] < n or shape[1] < F or (shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"{what}: needs a [>={n}, >={F}] matrix with contiguous rows, got "
-                         f"{tuple(shape)} with strides {t.stride()}")
-    if not t.is_cuda:
-        raise ValueError(f"{what}: needs a CUDA tensor")
-    return t.stride(0)
+    if len(shape) == 2:
+        ld, step = t.stride()
+        if shape[0] >= n and shape[1] >= F and (step == 1 or shape[1] == 1):
+            if t.is_cuda:
+                return ld
+            raise ValueError(f"{what}: needs a CUDA tensor")
+    raise ValueError(f"{what}: needs a [>={n}, >={F}] matrix with contiguous rows, got "
+                     f"{tuple(shape)} with strides {t.stride()}")
 
 
 def _f32(t, count: int, what: str):
+    """Pointer of a contiguous fp32 vector (None for None)."""
     if t is None:
         return None
-    if _type(t) != 0 or t.numel() < count or not t.is_contiguous() or not t.is_cuda:
-        raise ValueError(f"{what}: needs a contiguous fp32 CUDA tensor of {count} elements")
-    return t.data_ptr()
+    if t.dtype is (_bits or _torch_bits()).f32 and t.is_cuda and t.numel() >= count and t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError(f"{what}: needs a contiguous fp32 CUDA tensor of {count} elements")
 
 
 def _current(t, stream) -> int:
     """The raw stream of a call on t: `stream`, or t's device's current one."""
     if stream is not None:
         return stream.cuda_stream
-    import torch
-    return torch._C._cuda_getCurrentRawStream(t.get_device())
+    return (_bits or _torch_bits()).raw_stream(t.get_device())
 
 
 def _act(act: str) -> int:
-    if act not in ACTS:
+    k = ACTS.get(act)
+    if k is None:
         raise ValueError(f"act: one of {sorted(ACTS)}, got {act!r}")
-    return ACTS[act]
+    return k
 
 
 def _seg(seg_start):
-    import torch
     if seg_start is None:
         return None, 1
-    if seg_start.dtype != torch.int64 or seg_start.dim() != 1 or seg_start.numel() < 2 or \
-            not seg_start.is_contiguous() or seg_start.device.type != "cuda":
-        raise ValueError("seg_start: needs a contiguous int64 CUDA tensor of n_seg + 1 elements")
-    return seg_start.data_ptr(), seg_start.numel() - 1
+    k = seg_start.numel()
+    if seg_start.dtype is (_bits or _torch_bits()).i64 and seg_start.is_cuda and seg_start.dim() == 1 and k >= 2 and \
+            seg_start.is_contiguous():
+        return seg_start.data_ptr(), k - 1
+    raise ValueError("seg_start: needs a contiguous int64 CUDA tensor of n_seg + 1 elements")
+
+
+def _ws(ws, nbytes: int, t, stream):
+    """(pointer, bytes, owner) of the caller's workspace, or of one of the binding's."""
+    return _scratch(nbytes, t, stream) if ws is None else (ws.data_ptr(), ws.numel(), ws)
 
 
 @functools.lru_cache(maxsize=1024)
@@ -826,12 +854,10 @@ def gnn_group_norm_fwd(X, n: int, C: int, groups: int, Y, mean, rstd, seg_start=
     mean and rstd [n_seg, groups] are kept for the backward."""
     seg, n_seg = _seg(seg_start)
     ldx, ldy = _rows(X, n, C, "X"), _rows(Y, n, C, "Y")
-    if ws is None:
-        ws = _scratch(gnn_group_norm_workspace(n, C, groups, n_seg), X, stream)
-    call("gnn_group_norm_fwd", _ptr(X), ldx, _type(X), n, C, groups, seg, n_seg, _f32(gamma, C, "gamma"),
-         _f32(beta, C, "beta"), float(eps), _act(act), _ptr(Y), ldy, _type(Y),
-         _f32(mean, n_seg * groups, "mean"), _f32(rstd, n_seg * groups, "rstd"), _ptr(ws), ws.numel(),
-         _current(X, stream))
+    at, size, ws = _ws(ws, gnn_group_norm_workspace(n, C, groups, n_seg), X, stream)
+    call("gnn_group_norm_fwd", X.data_ptr(), ldx, _type(X), n, C, groups, seg, n_seg, _f32(gamma, C, "gamma"),
+         _f32(beta, C, "beta"), eps, _act(act), Y.data_ptr(), ldy, _type(Y),
+         _f32(mean, n_seg * groups, "mean"), _f32(rstd, n_seg * groups, "rstd"), at, size, _current(X, stream))
 
 
 def gnn_group_norm_bwd(dY, X, n: int, C: int, groups: int, mean, rstd, dX, dgamma=None, dbeta=None,
@@ -841,14 +867,13 @@ def gnn_group_norm_bwd(dY, X, n: int, C: int, groups: int, mean, rstd, dX, dgamm
     mean and rstd (dY has Y's type, dX has X's)."""
     seg, n_seg = _seg(seg_start)
     ldx, ldy, lddx = _rows(X, n, C, "X"), _rows(dY, n, C, "dY"), _rows(dX, n, C, "dX")
-    if dX.dtype != X.dtype:
+    if dX.dtype is not X.dtype:
         raise ValueError("dX: needs X's type")
-    if ws is None:
-        ws = _scratch(gnn_group_norm_workspace(n, C, groups, n_seg), X, stream)
-    call("gnn_group_norm_bwd", _ptr(dY), ldy, _type(dY), _ptr(X), ldx, _type(X), n, C, groups, seg, n_seg,
+    at, size, ws = _ws(ws, gnn_group_norm_workspace(n, C, groups, n_seg), X, stream)
+    call("gnn_group_norm_bwd", dY.data_ptr(), ldy, _type(dY), X.data_ptr(), ldx, _type(X), n, C, groups, seg, n_seg,
          _f32(gamma, C, "gamma"), _f32(beta, C, "beta"), _act(act), _f32(mean, n_seg * groups, "mean"),
-         _f32(rstd, n_seg * groups, "rstd"), _ptr(dX), lddx, _f32(dgamma, C, "dgamma"),
-         _f32(dbeta, C, "dbeta"), _ptr(ws), ws.numel(), _current(X, stream))
+         _f32(rstd, n_seg * groups, "rstd"), dX.data_ptr(), lddx, _f32(dgamma, C, "dgamma"),
+         _f32(dbeta, C, "dbeta"), at, size, _current(X, stream))
 
 
 @functools.lru_cache(maxsize=1024)
@@ -859,10 +884,11 @@ def gnn_gated_workspace(n: int, F_in: int, F_mid: int):
     return f.value, b.value
 
 
-def _one_type(X, **others) -> int:
-    for name, t in others.items():
-        if t is not None and t.dtype != X.dtype:
-            raise ValueError(f"{name}: needs X's type {X.dtype}, got {t.dtype}")
+def _one_type(X, *others) -> int:
+    d = X.dtype
+    for t in others:
+        if t is not None and t.dtype is not d:
+            raise ValueError(f"operands of one type are needed: X has {d}, another {t.dtype}")
     return _type(X)
 
 
@@ -870,9 +896,9 @@ def gnn_gated_fwd(X, n: int, F_in: int, Wg, Wu, F_mid: int, H, act: str = "silu"
                   stream=None) -> None:
     """H = act(X Wg) * (X Wu) on tcgen05 (X, Wg, Wu, H of one type, bf16 or
     fp16; Wg, Wu [F_in, F_mid]).  It needs no workspace."""
-    t = _one_type(X, Wg=Wg, Wu=Wu, H=H)
-    call("gnn_gated_fwd", _ptr(X), _rows(X, n, F_in, "X"), t, n, F_in, _ptr(Wg), _rows(Wg, F_in, F_mid, "Wg"),
-         _ptr(Wu), _rows(Wu, F_in, F_mid, "Wu"), F_mid, _act(act), _ptr(H), _rows(H, n, F_mid, "H"),
+    t = _one_type(X, Wg, Wu, H)
+    call("gnn_gated_fwd", X.data_ptr(), _rows(X, n, F_in, "X"), t, n, F_in, Wg.data_ptr(), _rows(Wg, F_in, F_mid, "Wg"),
+         Wu.data_ptr(), _rows(Wu, F_in, F_mid, "Wu"), F_mid, _act(act), H.data_ptr(), _rows(H, n, F_mid, "H"),
          _ptr(ws), ws.numel() if ws is not None else 0, _current(X, stream))
 
 
@@ -880,15 +906,14 @@ def gnn_gated_bwd(dH, X, n: int, F_in: int, Wg, Wu, F_mid: int, dX=None, dWg=Non
                   act: str = "silu", ws=None, stream=None) -> None:
     """dX, dWg and dWu of gnn_gated_fwd (X's type; the projections are
     recomputed).  dH has X's type or fp32."""
-    t = _one_type(X, Wg=Wg, Wu=Wu, dX=dX, dWg=dWg, dWu=dWu)
-    if ws is None:
-        ws = _scratch(gnn_gated_workspace(n, F_in, F_mid)[1], X, stream)
+    t = _one_type(X, Wg, Wu, dX, dWg, dWu)
+    at, size, ws = _ws(ws, gnn_gated_workspace(n, F_in, F_mid)[1], X, stream)
     call("gnn_gated_bwd", _ptr(dH), _rows(dH, n, F_mid, "dH"), _type(dH), _ptr(X), _rows(X, n, F_in, "X"), t, n,
          F_in, _ptr(Wg), _rows(Wg, F_in, F_mid, "Wg"), _ptr(Wu), _rows(Wu, F_in, F_mid, "Wu"), F_mid, _act(act),
          _ptr(dX), _rows(dX, n, F_in, "dX") if dX is not None else 0,
          _ptr(dWg), _rows(dWg, F_in, F_mid, "dWg") if dWg is not None else 0,
          _ptr(dWu), _rows(dWu, F_in, F_mid, "dWu") if dWu is not None else 0,
-         _ptr(ws), ws.numel(), _current(X, stream))
+         at, size, _current(X, stream))
 
 
 class AdamwTensors:
@@ -951,14 +976,13 @@ def gnn_adamw_step(tensors: AdamwTensors, state, lr: float, beta1: float = 0.9, 
     """One AdamW step over every tensor; with max_norm > 0 the gradients are
     clipped by their global norm (written to grad_norm, fp32 [1]) and a step
     whose norm is not finite is skipped."""
-    import torch
-    if state.dtype != torch.float64 or state.numel() != 4 or not state.is_contiguous() or state.device.type != "cuda":
+    if state.dtype is not (_bits or _torch_bits()).f64 or state.numel() != 4 or not state.is_contiguous() or \
+            not state.is_cuda:
         raise ValueError("state: needs the fp64 CUDA tensor that adamw_state makes")
-    if ws is None:
-        ws = _scratch(gnn_adamw_workspace(), state, stream)
+    at, size, ws = _ws(ws, gnn_adamw_workspace(), state, stream)
     call("gnn_adamw_step", tensors.c, tensors.count, tensors.param_type, tensors.grad_type, tensors.state_bits,
-         _ptr(state), float(lr), float(beta1), float(beta2), float(eps), float(weight_decay), float(grad_scale),
-         float(max_norm), _f32(grad_norm, 1, "grad_norm"), _ptr(ws), ws.numel(), _current(state, stream))
+         state.data_ptr(), lr, beta1, beta2, eps, weight_decay, grad_scale, max_norm, _f32(grad_norm, 1, "grad_norm"), at,
+         size, _current(state, stream))
 
 
 # ---------------------------------------------------------------- epoch control (host only)
