@@ -474,6 +474,7 @@ __global__ void __launch_bounds__(THREADS) norm_kernel(const __grid_constant__ T
                                                        int add) {
   __shared__ double sm[THREADS / 32];
   cudaTriggerProgrammaticLaunchCompletion();
+  cudaGridDependencySynchronize();
   const int lane = threadIdx.x & 31;
   const int64_t chunks = tab.first[tab.count];
   const int64_t warps = (int64_t)gridDim.x * (THREADS / 32);
@@ -510,8 +511,8 @@ __global__ void __launch_bounds__(THREADS)
   __shared__ double sm[THREADS / 32];
   __shared__ float scalars[2];
   cudaTriggerProgrammaticLaunchCompletion();
-  // what the norm has no part in, one thread each, while its launch still runs
-  // (the state is nobody's but this kernel's)
+  cudaGridDependencySynchronize();
+  // what the norm has no part in, one thread each
   double power = 0;
   if (threadIdx.x == 32) {
     power = state->beta1_pow * beta1;
@@ -520,7 +521,6 @@ __global__ void __launch_bounds__(THREADS)
     power = state->beta2_pow * beta2;
     scalars[1] = (float)(1.0 / sqrt(1.0 - power));
   }
-  cudaGridDependencySynchronize();
   double sum = 0;
   for (int i = threadIdx.x; i < n_partial; i += THREADS) sum += partial[i];
   sum = block_sum(sum, sm);
@@ -550,8 +550,10 @@ __global__ void __launch_bounds__(THREADS)
 
 bool aligned_to(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 
+// Every launch may start while the kernel before it ends, and waits for that
+// before it touches memory.
 template <class... P, class... A>
-gnn_status launch(cudaStream_t st, bool after, int64_t grid, size_t smem, void (*k)(P...), A... args) {
+gnn_status launch(cudaStream_t st, int64_t grid, size_t smem, void (*k)(P...), A... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3(THREADS);
@@ -561,16 +563,16 @@ gnn_status launch(cudaStream_t st, bool after, int64_t grid, size_t smem, void (
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
-  cfg.numAttrs = after ? 1 : 0;
+  cfg.numAttrs = 1;
   count_launch();
   GNN_CUDA(cudaLaunchKernelEx(&cfg, k, args...));
   return GNN_OK;
 }
 
-using Update = gnn_status (*)(cudaStream_t, bool, int64_t, const Table&, const Hyper&, const Control*);
+using Update = gnn_status (*)(cudaStream_t, int64_t, const Table&, const Hyper&, const Control*);
 
 template <class TP, class TG, bool Q8>
-gnn_status launch_update(cudaStream_t st, bool after, int64_t grid, const Table& tab, const Hyper& h,
+gnn_status launch_update(cudaStream_t st, int64_t grid, const Table& tab, const Hyper& h,
                          const Control* ctl) {
   constexpr int smem = ring_bytes<TP, TG, Q8>();
   static bool ready = false;
@@ -578,7 +580,7 @@ gnn_status launch_update(cudaStream_t st, bool after, int64_t grid, const Table&
     GNN_CUDA(cudaFuncSetAttribute(adamw_kernel<TP, TG, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
     ready = true;
   }
-  return launch(st, after, grid, smem, adamw_kernel<TP, TG, Q8>, tab, h, ctl);
+  return launch(st, grid, smem, adamw_kernel<TP, TG, Q8>, tab, h, ctl);
 }
 template <class TP, class TG>
 Update update_for(bool q8) {
@@ -680,13 +682,13 @@ extern "C" gnn_status gnn_adamw_step(const gnn_adamw_tensor* tensors, int32_t n_
     const gnn_status s = each(NORM_UNITS, [&](const Table& tab) -> gnn_status {
       // every launch writes or adds to all partials of the first's grid
       const int64_t grid = n_partial ? n_partial : grid_for(tab, NORM_BLOCKS);
-      const gnn_status r = launch(st, false, grid, 0, norm, tab, partial, n_partial ? 1 : 0);
+      const gnn_status r = launch(st, grid, 0, norm, tab, partial, n_partial ? 1 : 0);
       n_partial = (int)grid;
       return r;
     });
     if (s != GNN_OK) return s;
   }
-  gnn_status s = launch(st, n_partial > 0, 1, 0, begin_kernel, (const double*)partial, n_partial, state, lr,
+  gnn_status s = launch(st, 1, 0, begin_kernel, (const double*)partial, n_partial, state, lr,
                         beta1, beta2, grad_scale, max_norm, grad_norm, ctl);
   if (s != GNN_OK) return s;
   // A chunk is what a warp takes in a row: long enough to fill its ring, short
@@ -695,10 +697,5 @@ extern "C" gnn_status gnn_adamw_step(const gnn_adamw_tensor* tensors, int32_t n_
   for (int i = 0; i < n_tensors; ++i) blocks += (tensors[i].n + BLOCK - 1) / BLOCK;
   const int64_t share = blocks / (152 * 3 * (THREADS / 32) * 4);
   const int units = share < 1 ? 1 : share > MAX_UNITS ? MAX_UNITS : (int)share;
-  bool first = true;
-  return each(units, [&](const Table& tab) -> gnn_status {
-    const gnn_status r = update(st, first, grid_for(tab, 152 * 3 * 16), tab, h, ctl);
-    first = false;
-    return r;
-  });
+  return each(units, [&](const Table& tab) { return update(st, grid_for(tab, 152 * 3 * 16), tab, h, ctl); });
 }

@@ -195,7 +195,7 @@ __device__ __forceinline__ void walk_tiles(const Args& g, uint8_t* smem_raw, int
   __syncthreads();
   tc::cluster_sync();  // the partner's barriers are there
   tc::fence_after_sync();
-  cudaGridDependencySynchronize();  // DX and DW read what ACT writes
+  cudaGridDependencySynchronize();
   const uint32_t tmem = *s.tmem;
   const int tiles = num_tiles<M>(g);
 
@@ -483,6 +483,8 @@ __global__ void __launch_bounds__(ROW_THREADS)
     gated_rows_kernel(const T* __restrict__ X, int64_t ldx, int n, int D, const T* __restrict__ Wg, int64_t ldg,
                       const T* __restrict__ Wu, int64_t ldu, int F, int act, T* __restrict__ H, int64_t ldh,
                       int cols) {
+  cudaTriggerProgrammaticLaunchCompletion();
+  cudaGridDependencySynchronize();
   constexpr int W = ROW_THREADS / 32, U = 4;
   __shared__ T xs[NR][ROW_CHUNK];
   __shared__ float red[W][NR][2][64];
@@ -657,9 +659,10 @@ GatedWs gated_ws(void* base, size_t cap, int64_t n, int D, int F, bool* ok) {
   return w;
 }
 
-// `after`: may start while the launch before it, one of this call's, ends.
+// A launch may start while the kernel before it ends; each waits for that before
+// it touches memory.
 template <class... P, class... A>
-gnn_status launch(bool after, int grid, int block, size_t smem, cudaStream_t st, void (*k)(P...), const A&... args) {
+gnn_status launch(int grid, int block, size_t smem, cudaStream_t st, void (*k)(P...), const A&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3((unsigned)block);
@@ -669,14 +672,14 @@ gnn_status launch(bool after, int grid, int block, size_t smem, cudaStream_t st,
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
-  cfg.numAttrs = after ? 1 : 0;
+  cfg.numAttrs = 1;
   count_launch();
   GNN_CUDA(cudaLaunchKernelEx(&cfg, k, args...));
   return GNN_OK;
 }
 
 template <Mode M, class T>
-gnn_status launch_gated(bool after, const Args& g, cudaStream_t st) {
+gnn_status launch_gated(const Args& g, cudaStream_t st) {
   static bool ready = false;
   if (!ready) {
     GNN_CUDA(cudaFuncSetAttribute(gated_kernel<M, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(M)));
@@ -684,7 +687,7 @@ gnn_status launch_gated(bool after, const Args& g, cudaStream_t st) {
   }
   const int64_t tiles = (int64_t)g.num_m * g.num_n * (M == DW ? 2 * g.splits : 1);
   const int pairs = (int)(tiles < sm_count() / 2 ? tiles : sm_count() / 2);
-  return launch(after, 2 * pairs, THREADS, smem_bytes(M), st, gated_kernel<M, T>, g);
+  return launch(2 * pairs, THREADS, smem_bytes(M), st, gated_kernel<M, T>, g);
 }
 
 // A map of a 2-byte matrix of `cols` used columns.
@@ -725,11 +728,9 @@ gnn_status launch_rows(int n, int D, int F, int act, Mat X, Mat Wg, Mat Wu, Mat 
   int cols = 64;
   while (cols > 16 && (F + cols - 1) / cols < 2 * 152) cols /= 2;
   const int grid = (int)((up(F, 16) + cols - 1) / cols);
-  gated_rows_kernel<T, NR><<<grid, ROW_THREADS, 0, st>>>(
-      static_cast<const T*>(X.p), X.ld, n, D, static_cast<const T*>(Wg.p), Wg.ld, static_cast<const T*>(Wu.p), Wu.ld, F,
-      act, static_cast<T*>(H.p), H.ld, cols);
-  GNN_CHECK_LAUNCH();
-  return GNN_OK;
+  return launch(grid, ROW_THREADS, 0, st, gated_rows_kernel<T, NR>, static_cast<const T*>(X.p), X.ld, n, D,
+                static_cast<const T*>(Wg.p), Wg.ld, static_cast<const T*>(Wu.p), Wu.ld, F, act, static_cast<T*>(H.p), H.ld,
+                cols);
 }
 
 template <class T>
@@ -741,7 +742,7 @@ gnn_status gated_fwd(int64_t n, int D, int F, int act, Mat X, Mat Wg, Mat Wu, Ma
   Args g{};
   GNN_TRY(product_args<T>(g, n, D, F, act, X, Wg, Wu));
   GNN_TRY(map16<T>(&g.out[0], H.p, n, up(F, 16), H.ld, 64, 32));
-  return launch_gated<FWD, T>(false, g, st);
+  return launch_gated<FWD, T>(g, st);
 }
 
 template <class T>
@@ -757,7 +758,7 @@ gnn_status gated_bwd(int64_t n, int D, int F, int act, int dh_f32, Mat dH, Mat X
       GNN_TRY(map16<T>(&g.dh, dH.p, n, F, dH.ld, 64, 32));
     GNN_TRY(map16<T>(&g.out[0], w.dg, n, F, w.ldf, 64, 32));
     GNN_TRY(map16<T>(&g.out[1], w.du, n, F, w.ldf, 64, 32));
-    GNN_TRY((launch_gated<ACT, T>(false, g, st)));
+    GNN_TRY((launch_gated<ACT, T>(g, st)));
   }
   const GradPlan p = grad_plan(n, D, F, dX.p && dWg.p);
   Args x{}, v{};
@@ -787,14 +788,14 @@ gnn_status gated_bwd(int64_t n, int D, int F, int act, int dh_f32, Mat dH, Mat X
     }
     const int64_t dw_tiles = 2ll * p.dw_m * p.dw_n * p.splits;
     const int pairs = p.dx_pairs + (int)std::min<int64_t>(dw_tiles, sm_count() / 2 - p.dx_pairs);
-    GNN_TRY(launch(true, 2 * pairs, THREADS, smem, st, gated_grads_kernel<T>, x, v, p.dx_pairs));
+    GNN_TRY(launch(2 * pairs, THREADS, smem, st, gated_grads_kernel<T>, x, v, p.dx_pairs));
   } else if (n > 0) {
-    if (dX.p) GNN_TRY((launch_gated<DX, T>(true, x, st)));
-    if (dWg.p) GNN_TRY((launch_gated<DW, T>(true, v, st)));
+    if (dX.p) GNN_TRY((launch_gated<DX, T>(x, st)));
+    if (dWg.p) GNN_TRY((launch_gated<DW, T>(v, st)));
   }
   if (dWg.p) {
     const int64_t work = 2ll * D * (up(F, 16) / 8), ldp = (int64_t)p.dw_n * BN;
-    GNN_TRY(launch(n > 0, (int)((work + 255) / 256), 256, 0, st, gated_dw_kernel<T>, (const float*)w.part,
+    GNN_TRY(launch((int)((work + 255) / 256), 256, 0, st, gated_dw_kernel<T>, (const float*)w.part,
                    n > 0 ? p.splits : 0, D, F, ldp, (int64_t)p.dw_m * BM * ldp, static_cast<T*>(dWg.p), dWg.ld,
                    static_cast<T*>(dWu.p), dWu.ld));
   }

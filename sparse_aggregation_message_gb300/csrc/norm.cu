@@ -393,6 +393,7 @@ template <class TX, class TY, int V, bool SMALL>
 __global__ void __launch_bounds__(block_threads(V, SMALL), fwd_blocks(V, SMALL)) norm_fwd_stats_kernel(NormArgs a) {
   extern __shared__ float sm[];
   cudaTriggerProgrammaticLaunchCompletion();
+  cudaGridDependencySynchronize();
   const Place<V> p(a);
   const int width = a.CH * V;
   float* red1 = sm;
@@ -685,6 +686,7 @@ template <class TX, class TY, int V, bool SMALL>
 __global__ void __launch_bounds__(block_threads(V, SMALL), bwd_blocks(V, SMALL)) norm_bwd_sums_kernel(NormArgs a) {
   extern __shared__ float sm[];
   cudaTriggerProgrammaticLaunchCompletion();
+  cudaGridDependencySynchronize();
   const Place<V> p(a);
   const int width = a.CH * V;
   float* red1 = sm;
@@ -973,7 +975,7 @@ bool bad_rows(const void* p, int64_t ld, int type, int C, bool output) {
 struct Launch {
   cudaStream_t st;
   template <class... P, class... A>
-  gnn_status run(bool after, int64_t grid, int block, size_t smem, void (*k)(P...), A... args) const {
+  gnn_status run(int64_t grid, int block, size_t smem, void (*k)(P...), A... args) const {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);
     cfg.blockDim = dim3(block);
@@ -983,7 +985,7 @@ struct Launch {
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
-    cfg.numAttrs = after ? 1 : 0;  // may start while the launch before it ends
+    cfg.numAttrs = 1;  // may start while the kernel before it ends: each waits for that first
     count_launch();
     GNN_CUDA(cudaLaunchKernelEx(&cfg, k, args...));
     return GNN_OK;
@@ -1029,9 +1031,9 @@ gnn_status norm_fwd(NormArgs a, int threads, cudaStream_t st) {
   gnn_status s = allow_smem(norm_fwd_stats_kernel<TX, TY, V, SMALL>, ready1);
   if (s == GNN_OK) s = allow_smem(norm_fwd_apply_kernel<TX, TY, V>, ready2);
   if (s == GNN_OK && a.tiles)
-    s = l.run(false, a.tiles, threads, smem, norm_fwd_stats_kernel<TX, TY, V, SMALL>, a);
-  if (s == GNN_OK) s = l.run(a.tiles > 0, joiners(a), FIN_THREADS, 0, norm_fwd_join_kernel, a);
-  if (s == GNN_OK && a.tiles) s = l.run(true, a.tiles, threads, ring, norm_fwd_apply_kernel<TX, TY, V>, a);
+    s = l.run(a.tiles, threads, smem, norm_fwd_stats_kernel<TX, TY, V, SMALL>, a);
+  if (s == GNN_OK) s = l.run(joiners(a), FIN_THREADS, 0, norm_fwd_join_kernel, a);
+  if (s == GNN_OK && a.tiles) s = l.run(a.tiles, threads, ring, norm_fwd_apply_kernel<TX, TY, V>, a);
   return s;
 }
 template <class TX, class TY, int V>
@@ -1051,11 +1053,11 @@ gnn_status norm_bwd(NormArgs a, int threads, cudaStream_t st) {
   gnn_status s = allow_smem(norm_bwd_sums_kernel<TX, TY, V, SMALL>, ready1);
   if (s == GNN_OK) s = allow_smem(norm_bwd_apply_kernel<TX, TY, V>, ready2);
   if (s == GNN_OK && a.tiles)
-    s = l.run(false, a.tiles, threads, smem, norm_bwd_sums_kernel<TX, TY, V, SMALL>, a);
+    s = l.run(a.tiles, threads, smem, norm_bwd_sums_kernel<TX, TY, V, SMALL>, a);
   const int cols = a.dpart ? (2 * a.C + 7) / 8 : 0;
   if (s == GNN_OK)
-    s = l.run(a.tiles > 0, joiners(a) + cols, FIN_THREADS, 0, norm_bwd_join_kernel, a, joiners(a));
-  if (s == GNN_OK && a.tiles) s = l.run(true, a.tiles, threads, stream, norm_bwd_apply_kernel<TX, TY, V>, a);
+    s = l.run(joiners(a) + cols, FIN_THREADS, 0, norm_bwd_join_kernel, a, joiners(a));
+  if (s == GNN_OK && a.tiles) s = l.run(a.tiles, threads, stream, norm_bwd_apply_kernel<TX, TY, V>, a);
   return s;
 }
 template <class TX, class TY, int V>
