@@ -642,7 +642,8 @@ gnn_status gnn_spmm_bwd_blocked(const gnn_csr* csr, const gnn_boundary* bnd,
  * F..round_up(F,4)-1 are written as zero; a 2-byte type has a row stride that
  * is a multiple of 8 and, as an output, at least round_up(F,16), with columns
  * F..round_up(F,16)-1 written as zero (the operand layout of
- * gnn_dense_fwd).  Padding columns of inputs are not used. */
+ * gnn_dense_fwd).  Padding columns of inputs are not used, but a row's whole
+ * stride lies in the caller's allocation. */
 
 /* Group norm with an activation, channels last.  Segment s holds the rows
  * [seg_start[s], seg_start[s+1]) -- a graph of a batch, or a partition:

@@ -106,8 +106,8 @@ __device__ __forceinline__ void for_pieces(const NormArgs& a, int t, Fn f) {
   int row = r0;
   while (row < r1 && s < a.n_seg) {
     const int sb = seg_at(a, s), se = seg_at(a, s + 1);
-    if (se <= row) {  // empty (or not ascending, which the join launch flags)
-      ++s;
+    if (se <= row) {  // empty, perhaps one of many (or not ascending, which the join launch flags)
+      s = max(s + 1, seg_of(a, row));
       continue;
     }
     if (sb > row) break;

@@ -325,3 +325,23 @@ def test_more_than_2_31_elements():
         G.gnn_group_norm_bwd(y[a:b].clone(), part, b - a, C, groups, m, r, d, act="silu")
         scale = d.double().abs() + d.double().square().mean().sqrt()
         assert torch.all((dx[a:b].double() - d.double()).abs() <= (2 * half + 1e-3) * scale)
+
+
+def test_many_empty_segments():
+    """Runs of empty segments at the start, inside and at the end."""
+    n, C, groups, k = 1000, 16, 4, 200_000
+    _, x = rows(n, C, torch.float32, 11)
+    cut = [0] * k + [0, 300] + [300] * k + [640, 641] + [n] * k
+    seg = torch.tensor(cut, device="cuda")
+    S = len(cut) - 1
+    y, mean, rstd = torch.empty(n, C, device="cuda"), torch.full((S, groups), 7.0, device="cuda"), torch.full((S, groups), 7.0, device="cuda")
+    G.gnn_group_norm_fwd(x, n, C, groups, y, mean, rstd, seg_start=seg, eps=0.25, act="silu")
+    G.gnn_sync_check()
+    o, m, r = torch.empty(n, C, device="cuda"), torch.empty(4, groups, device="cuda"), torch.empty(4, groups, device="cuda")
+    G.gnn_group_norm_fwd(x, n, C, groups, o, m, r, seg_start=torch.tensor([0, 300, 640, 641, n], device="cuda"), eps=0.25,
+                         act="silu")
+    full = torch.tensor([i for i, (a, b) in enumerate(zip(cut, cut[1:])) if a < b], device="cuda")
+    assert torch.allclose(mean[full], m, rtol=0, atol=2 * K) and torch.allclose(y, o, rtol=1e-4, atol=1e-4)
+    empty = torch.ones(S, dtype=torch.bool, device="cuda")
+    empty[full] = False
+    assert torch.all(mean[empty] == 0) and torch.all(rstd[empty] == 2)
