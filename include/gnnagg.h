@@ -655,7 +655,10 @@ gnn_status gnn_spmm_bwd_blocked(const gnn_csr* csr, const gnn_boundary* bnd,
  *   xh = (x - mean) rstd,  rstd = 1/sqrt(var + eps),
  *   Y = act(gamma xh + beta)           (gamma, beta fp32 [C]; NULL: 1, 0).
  * mean, rstd: fp32 [n_seg][groups], kept for the backward.  Statistics are
- * held in fp32 about a value of the group, so a large mean does not cancel.
+ * held in fp32 about a value of the group, and formed again about the mean where
+ * that value lies more than four standard deviations from it, so that neither a
+ * large mean nor a value far from the others cancels: the variance is as exact
+ * as a sum of squares about the mean, up to a factor of 17 in the rounding.
  * Types (x_type -> y_type): GNN_F32 -> any, GNN_BF16 -> GNN_BF16,
  * GNN_F16 -> GNN_F16.  C <= 1024, a multiple of groups.  Rows of a seg_start
  * that is not ascending raise the device-check flag. */

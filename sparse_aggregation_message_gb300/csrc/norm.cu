@@ -388,8 +388,15 @@ __device__ __forceinline__ void fwd_rows(const NormArgs& a, const Place<V>& p, i
 }
 
 // Statistics of every piece of a tile; short segments end here with their
-// output.  A group's sums are formed about its value in the piece's first row,
-// so a mean far from zero does not cancel in E[x^2] - mean^2.
+// output.  A group's sums S, Q of d = x - pivot and d^2 are formed about its value
+// in the piece's first row, so a mean far from zero does not cancel in
+// M2 = Q - S^2/m.  The pivot has to be a typical value for that: the difference
+// loses 1 + (mean - pivot)^2/var of the sums' precision.  Where that is more than
+// 1 + kFar in any group, the sums are formed once more about the mean that the
+// first ones gave, which is off by a few 2^-24 of |mean - pivot| and so by less
+// than the deviation (that is at least |mean - pivot|/sqrt(m)).  Of normally
+// distributed pieces one group in 16,000 takes the second turn.
+constexpr float kFar = 16.f;
 template <class TX, class TY, int V, bool SMALL>
 __global__ void __launch_bounds__(block_threads(V, SMALL), fwd_blocks(V, SMALL)) norm_fwd_stats_kernel(NormArgs a) {
   extern __shared__ float sm[];
@@ -410,6 +417,11 @@ __global__ void __launch_bounds__(block_threads(V, SMALL), fwd_blocks(V, SMALL))
   const TX* X = static_cast<const TX*>(a.X);
   const int t = blockIdx.x;
   int left = 0;  // pieces of long segments
+  // the last turn whose pivot was far off in some group: turns are counted, so the
+  // word is never reset between those who read it and those who write it
+  __shared__ int far_turn;
+  if (threadIdx.x == 0) far_turn = 0;
+  int turn = 0;
   // slot i of this thread: its i-th row of a short segment, kept for the output
   const uint32_t slots = static_cast<uint32_t>(__cvta_generic_to_shared(ring)) + threadIdx.x * 16;
   const uint32_t next = blockDim.x * 16;
@@ -417,88 +429,98 @@ __global__ void __launch_bounds__(block_threads(V, SMALL), fwd_blocks(V, SMALL))
     left |= !whole;
     const bool keep = whole && rb - ra <= a.keep * a.RP;
     const int rows = p.rows(a, ra, rb);
-    float s1 = 0.f, s2 = 0.f;  // over this thread's channels
-    if (p.on) {
-      constexpr int U = 32 / V;
-      float piv[V], S[V], Q[V];
-      const TX* at = X + (ra + p.ro) * a.ldx + p.c0;
-      const int64_t dx = (int64_t)a.RP * a.ldx;
-      if (keep && p.in) {
-        for (int i = 0; i < rows; ++i, at += dx) copy_async<16>(slots + i * next, at);
-        copy_commit();
-      }
-#pragma unroll
-      for (int k = 0; k < V; ++k) {
-        piv[k] = to_f32(X[ra * a.ldx + (int64_t)p.g[k] * a.cg]);
-        S[k] = 0.f;
-        Q[k] = 0.f;
-      }
-      const auto add = [&](const float (&x)[V]) {
-#pragma unroll
-        for (int k = 0; k < V; k += 2) {
-          const float2 d = add2_rn(make_float2(x[k], x[k + 1]), make_float2(-piv[k], -piv[k + 1]));
-          const float2 s2 = add2_rn(make_float2(S[k], S[k + 1]), d);
-          const float2 q2 = fma2_rn(d, d, make_float2(Q[k], Q[k + 1]));
-          S[k] = s2.x, S[k + 1] = s2.y, Q[k] = q2.x, Q[k + 1] = q2.y;
+    const float inv = rcp_f((float)(rb - ra) * (float)a.cg);  // 1 / values of a group
+    bool again = false;  // the turn about the mean
+    while (true) {
+      ++turn;
+      float s1 = 0.f, s2 = 0.f;  // over this thread's channels
+      if (p.on) {
+        constexpr int U = 32 / V;
+        float piv[V], S[V], Q[V];
+        const TX* at = X + (ra + p.ro) * a.ldx + p.c0;
+        const int64_t dx = (int64_t)a.RP * a.ldx;
+        if (keep && p.in && !again) {
+          for (int i = 0; i < rows; ++i, at += dx) copy_async<16>(slots + i * next, at);
+          copy_commit();
         }
-      };
-      if (keep) {
-        copy_wait<0>();
-        int i = 0;
-        for (; p.in && i + 4 <= rows; i += 4) {
-          float x[4][V];
 #pragma unroll
-          for (int u = 0; u < 4; ++u) load_shared<V, TX>(slots + (i + u) * next, x[u]);
-#pragma unroll
-          for (int u = 0; u < 4; ++u) add(x[u]);
+        for (int k = 0; k < V; ++k) {
+          piv[k] = again ? gm[p.g[k]] : to_f32(X[ra * a.ldx + (int64_t)p.g[k] * a.cg]);
+          S[k] = 0.f;
+          Q[k] = 0.f;
         }
-        for (; p.in && i < rows; ++i) {
-          float x[V];
-          load_shared<V, TX>(slots + i * next, x);
-          add(x);
-        }
-      }
-      for (int i = p.in && !keep ? rows : 0; i > 0; i -= U) {
-        float x[U][V];
+        const auto add = [&](const float (&x)[V]) {
 #pragma unroll
-        for (int u = 0; u < U; ++u, at += dx) {
-          if (u < i) {
-            load_vec<V>(at, x[u]);
-          } else {
+          for (int k = 0; k < V; k += 2) {
+            const float2 d = add2_rn(make_float2(x[k], x[k + 1]), make_float2(-piv[k], -piv[k + 1]));
+            const float2 s2 = add2_rn(make_float2(S[k], S[k + 1]), d);
+            const float2 q2 = fma2_rn(d, d, make_float2(Q[k], Q[k + 1]));
+            S[k] = s2.x, S[k + 1] = s2.y, Q[k] = q2.x, Q[k + 1] = q2.y;
+          }
+        };
+        if (keep) {
+          copy_wait<0>();
+          int i = 0;
+          for (; p.in && i + 4 <= rows; i += 4) {
+            float x[4][V];
 #pragma unroll
-            for (int k = 0; k < V; ++k) x[u][k] = piv[k];
+            for (int u = 0; u < 4; ++u) load_shared<V, TX>(slots + (i + u) * next, x[u]);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) add(x[u]);
+          }
+          for (; p.in && i < rows; ++i) {
+            float x[V];
+            load_shared<V, TX>(slots + i * next, x);
+            add(x);
           }
         }
+        for (int i = p.in && !keep ? rows : 0; i > 0; i -= U) {
+          float x[U][V];
 #pragma unroll
-        for (int u = 0; u < U; ++u) add(x[u]);
-      }
-      if (chunks) {
+          for (int u = 0; u < U; ++u, at += dx) {
+            if (u < i) {
+              load_vec<V>(at, x[u]);
+            } else {
 #pragma unroll
-        for (int k = 0; k < V; ++k) s1 += S[k], s2 += Q[k];
-      } else {
-        store_vec<V>(red1 + p.ro * width + p.c0, S);
-        store_vec<V>(red2 + p.ro * width + p.c0, Q);
+              for (int k = 0; k < V; ++k) x[u][k] = piv[k];
+            }
+          }
+#pragma unroll
+          for (int u = 0; u < U; ++u) add(x[u]);
+        }
+        if (chunks) {
+#pragma unroll
+          for (int k = 0; k < V; ++k) s1 += S[k], s2 += Q[k];
+        } else {
+          store_vec<V>(red1 + p.ro * width + p.c0, S);
+          store_vec<V>(red2 + p.ro * width + p.c0, Q);
+        }
       }
-    }
-    const float inv = rcp_f((float)(rb - ra) * (float)a.cg);  // 1 / values of a group
-    const auto finish = [&](int g, float S, float Q) {
-      const float d = S * inv;
-      const float mean = to_f32(X[ra * a.ldx + (int64_t)g * a.cg]) + d;
-      const float m2 = fmaxf(Q - S * d, 0.f) + 0.f * Q;  // the product keeps a NaN
-      if (whole) {
-        const float rstd = rsqrtf(m2 * inv + a.eps);
+      const auto finish = [&](int g, float S, float Q) {
+        const float d = S * inv;
+        const float mean = (again ? gm[g] : to_f32(X[ra * a.ldx + (int64_t)g * a.cg])) + d;
+        const float m2 = fmaxf(Q - S * d, 0.f) + 0.f * Q;  // the product keeps a NaN
         gm[g] = mean;
-        gr[g] = rstd;
-        a.mean[(int64_t)s * a.groups + g] = mean;
-        a.rstd[(int64_t)s * a.groups + g] = rstd;
-      } else {
-        a.part[((int64_t)t + s) * a.groups + g] = make_float2(mean, m2);
-      }
-    };
-    if (chunks)
-      chunk_sums(a, part, at_part, p.in, s1, s2, finish);
-    else
-      block_sums(a, width, red1, red2, ch1, ch2, nullptr, finish);
+        // also where Q has left fp32's range, but not where the rows hold what is not finite
+        if (!(d * d <= kFar * (m2 * inv)) && fabsf(mean) < __int_as_float(0x7f800000)) far_turn = turn;
+        if (whole) {
+          const float rstd = rsqrtf(m2 * inv + a.eps);
+          gr[g] = rstd;
+          a.mean[(int64_t)s * a.groups + g] = mean;
+          a.rstd[(int64_t)s * a.groups + g] = rstd;
+        } else {
+          a.part[((int64_t)t + s) * a.groups + g] = make_float2(mean, m2);
+        }
+      };
+      if (chunks)
+        chunk_sums(a, part, at_part, p.in, s1, s2, finish);
+      else
+        block_sums(a, width, red1, red2, ch1, ch2, nullptr, finish);
+      // read behind the barrier that ends the sums, and written again only behind the
+      // next turn's first one
+      if (again || far_turn != turn) break;
+      again = true;
+    }
     if (keep) {
       float mu[V], sc[V], bt[V];
       fwd_channels<V>(a, p, gm, gr, mu, sc, bt);
@@ -559,8 +581,10 @@ __device__ __forceinline__ void for_long(const NormArgs& a, int blocks, Fn f) {
   }
 }
 
-// Joins the pieces of long segments: with d_i = mean_i - mean_0 and
-// D = sum m_i d_i / M, mean = mean_0 + D, M2 = sum (M2_i + m_i d_i^2) - M D^2.
+// Joins the pieces of long segments.  First mean = mean_0 + sum m_i (mean_i -
+// mean_0) / M, which is off by a few 2^-24 of mean_0's distance; then about it, so
+// that no piece's place matters: with d_i = mean_i - mean and D = sum m_i d_i / M,
+// mean += D, M2 = sum (M2_i + m_i d_i^2) - M D^2.
 __global__ void __launch_bounds__(FIN_THREADS) norm_fwd_join_kernel(NormArgs a) {
   cudaTriggerProgrammaticLaunchCompletion();
   cudaGridDependencySynchronize();
@@ -569,20 +593,31 @@ __global__ void __launch_bounds__(FIN_THREADS) norm_fwd_join_kernel(NormArgs a) 
   for_long(a, gridDim.x, [&](int s, int sb, int se, int t0, int t1, int g) {
     const float2* part = a.part + (int64_t)s * a.groups + g;
     const float first = part[(int64_t)t0 * a.groups].x;
+    // values of piece i's group
+    const auto count = [&](int i) {
+      return (float)((int)min((int64_t)se, (i + 1) * (int64_t)a.R) - max(sb, i * a.R)) * (float)a.cg;
+    };
     float M = 0.f, S = 0.f, Q = 0.f;
 #pragma unroll 8
     for (int i = t0 + lane; i <= t1; i += 32) {
-      const float2 v = part[(int64_t)i * a.groups];
-      const float m = (float)((int)min((int64_t)se, (i + 1) * (int64_t)a.R) - max(sb, i * a.R)) * (float)a.cg;
-      const float d = v.x - first;
+      const float m = count(i);
       M += m;
+      S += m * (part[(int64_t)i * a.groups].x - first);
+    }
+    M = warp_sum(M);
+    const float mean = first + warp_sum(S) / M;
+    S = 0.f;
+#pragma unroll 8
+    for (int i = t0 + lane; i <= t1; i += 32) {
+      const float2 v = part[(int64_t)i * a.groups];
+      const float m = count(i), d = v.x - mean;
       S += m * d;
       Q += v.y + m * d * d;
     }
-    M = warp_sum(M), S = warp_sum(S), Q = warp_sum(Q);
+    S = warp_sum(S), Q = warp_sum(Q);
     if (lane == 0) {
       const float D = S / M;
-      a.mean[(int64_t)s * a.groups + g] = first + D;
+      a.mean[(int64_t)s * a.groups + g] = mean + D;
       a.rstd[(int64_t)s * a.groups + g] = rsqrtf(fmaxf(Q - S * D, 0.f) / M + 0.f * Q + a.eps);
     }
   });

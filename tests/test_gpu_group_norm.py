@@ -345,3 +345,56 @@ def test_many_empty_segments():
     empty = torch.ones(S, dtype=torch.bool, device="cuda")
     empty[full] = False
     assert torch.all(mean[empty] == 0) and torch.all(rstd[empty] == 2)
+
+
+# rows and channels that take each way through the statistics: a short segment
+# kept on the chip, short ones read again, many small ones (sums over chunks and
+# over channels), and long ones cut into tiles
+FAR_CASES = [(200, 32, 1, "one", "f32"), (256, 256, 1, "one", "f32"), (256, 1024, 1, "one", "f32"),
+             (256, 1024, 1, "one", "bf16"), (4000, 32, 1, "small", "f32"), (4000, 35, 7, "small", "f32"),
+             (2000, 64, 2, "small", "f16"), (3000, 32, 1, "one", "f32"), (40000, 256, 1, "parts", "f32"),
+             (40000, 1024, 2, "parts", "bf16")]
+
+
+@pytest.mark.parametrize("n,C,groups,cut,t", FAR_CASES)
+@pytest.mark.parametrize("outlier", [30.0, 1000.0, 10000.0])
+@pytest.mark.parametrize("where", ["value", "row", "rows"])
+def test_statistics_do_not_rest_on_one_value(n, C, groups, cut, t, outlier, where):
+    """The first value of a group, its first row or its first rows lie far from
+    all others: the same tolerances as elsewhere."""
+    _, x = rows(n, C, TYPES[t], 21)
+    seg = cuts(n, cut)
+    for a, b in bounds(seg, n):
+        if a < b and where == "value":
+            x[a, ::C // groups] = outlier
+        elif a < b:
+            x[a:a + (1 if where == "row" else (b - a + 19) // 20)] += outlier
+    S = len(bounds(seg, n))
+    yt = "bf16" if t == "f32" else t
+    _, y = rows(n, C, TYPES[yt], 3, fill=0.0)
+    mean, rstd = torch.empty(S, groups, device="cuda"), torch.empty(S, groups, device="cuda")
+    G.gnn_group_norm_fwd(x, n, C, groups, y, mean, rstd, seg_start=seg)
+    G.gnn_sync_check()
+    one, zero = torch.ones(C, device="cuda"), torch.zeros(C, device="cuda")
+    rm, rr, mu, rs, xh, z = reference(x, seg, groups, one, zero, 1e-5, "none")
+    # a mean that lies far from zero for its deviation is rounded to fp32: half a step
+    assert torch.all((mean.double() - rm).abs() <= K * (1 / rr + rm.abs() * 2 ** -20) * 2 + 2 ** -24 * rm.abs())
+    assert torch.all((rstd.double() - rr).abs() <= 2 * K * rr)
+    tol = torch.finfo(TYPES[yt]).eps / 2 * z.abs() + 2 * K * (1 + xh.abs()) + \
+        2 ** -22 * (x.double().abs() + mu.abs()) * rs + (2 ** -24 if yt == "f16" else 0)
+    assert torch.all((y.double() - z).abs() <= tol)
+
+
+def test_pieces_far_from_the_first():
+    """The first tile of a long segment lies far from the two thousand others."""
+    n, C, groups = 3_900_000, 16, 2
+    _, x = rows(n, C, torch.float32, 22)
+    x[:1600] += 20000.0
+    y, mean, rstd = torch.empty(n, C, device="cuda"), torch.empty(1, groups, device="cuda"), torch.empty(1, groups, device="cuda")
+    G.gnn_group_norm_fwd(x, n, C, groups, y, mean, rstd)
+    G.gnn_sync_check()
+    v = x.double().reshape(n, groups, -1)
+    rm = v.mean((0, 2))
+    rr = 1 / torch.sqrt(((v - rm[:, None]) ** 2).mean((0, 2)) + 1e-5)
+    assert torch.all((mean[0].double() - rm).abs() <= K * (1 / rr + rm.abs() * 2 ** -20) * 2)
+    assert torch.all((rstd[0].double() - rr).abs() <= 2 * K * rr)
