@@ -228,3 +228,24 @@ def test_more_than_2_31_elements():
     # the rows fall into other blocks of the sums: fp32 orders differ, then one rounding each
     for a, b in ((dwg, few[1]), (dwu, few[2])):
         assert torch.all((a.double() - b.double()).abs() <= 2 * torch.finfo(torch.bfloat16).eps * b.double().abs() + 1e-4 * b.double().abs().mean())
+
+
+@pytest.mark.parametrize("D,F", [(40, 72), (300, 801), (65, 129), (16, 1)])
+@pytest.mark.parametrize("n", [1, 2, 3, 300])
+@pytest.mark.parametrize("t", ["bf16", "f16"])
+def test_padding_is_zero_whatever_the_rows_hold(n, D, F, t):
+    """Columns past the last one are zero also beside values that are not finite."""
+    x, wg, wu = operands(n, D, F, TYPES[t])
+    dh = mat(n, F, TYPES[t], 5, extra=8)[1]
+    x[0, 0], x[n - 1, D - 1], dh[n // 2, 0] = float("nan"), float("inf"), float("nan")
+    bh, h = mat(n, F, TYPES[t], 4, extra=24, fill=float("nan"))
+    bx, dx = mat(n, D, TYPES[t], 6, extra=24, fill=float("nan"))
+    bg, dwg = mat(D, F, TYPES[t], 7, extra=24, fill=float("nan"))
+    bu, dwu = mat(D, F, TYPES[t], 8, extra=8, fill=float("nan"))
+    G.gnn_gated_fwd(x, n, D, wg, wu, F, h)
+    G.gnn_gated_bwd(dh, x, n, D, wg, wu, F, dX=dx, dWg=dwg, dWu=dwu)
+    G.gnn_sync_check()
+    assert torch.isnan(h[0]).all() and torch.isnan(dx[n // 2]).all() and torch.isnan(dwg[0]).all()
+    for buf, c in ((bh, F), (bx, D), (bg, F), (bu, F)):
+        pad = -(-c // 16) * 16
+        assert torch.all(buf[:, c:pad] == 0) and torch.all(torch.isnan(buf[:, pad:]))
