@@ -263,7 +263,7 @@ __device__ __forceinline__ void load_channels(const float* src, const Place<V>& 
 // [RP][CH * V] partials; ch1/ch2 [C] get the channel sums and f(g, s1, s2) runs
 // in one lane per group with the group's sums, each channel times w[c] (NULL:
 // 1).  L lanes (a power of two) share a group, so narrow groups do not leave
-// most of a warp idle.  Ends with a barrier.
+// most of a warp idle.  A barrier of the caller's ends it.
 template <class Fn>
 __device__ __forceinline__ void block_sums(const NormArgs& a, int width, const float* red1,
                                            const float* red2, float* ch1, float* ch2, const float* w,
@@ -298,7 +298,6 @@ __device__ __forceinline__ void block_sums(const NormArgs& a, int width, const f
     }
     if (g < a.groups && l == 0) f(g, s1, s2);
   }
-  __syncthreads();
 }
 
 // The same where a group is whole chunks, for small blocks (65537 x 256 in 2800
@@ -327,7 +326,6 @@ __device__ __forceinline__ void chunk_sums(const NormArgs& a, float2* part, int 
     }
     if (g < a.groups && l == 0) f(g, s1, s2);
   }
-  __syncthreads();
 }
 // A thread's place in them.
 template <int V>
@@ -395,8 +393,13 @@ __device__ __forceinline__ void fwd_rows(const NormArgs& a, const Place<V>& p, i
 // 1 + kFar in any group, the sums are formed once more about the mean that the
 // first ones gave, which is off by a few 2^-24 of |mean - pivot| and so by less
 // than the deviation (that is at least |mean - pivot|/sqrt(m)).  Of normally
-// distributed pieces one group in 16,000 takes the second turn.
+// distributed pieces one group in 16,000 takes the second turn; where every piece
+// of 716847 x 300 takes it, the forward takes 410 us instead of 333.
 constexpr float kFar = 16.f;
+// Also where Q has left fp32's range, but not where the rows hold what is not finite.
+__device__ __forceinline__ bool is_far(float d, float var, float mean) {
+  return !(d * d <= kFar * var) && fabsf(mean) < __int_as_float(0x7f800000);
+}
 template <class TX, class TY, int V, bool SMALL>
 __global__ void __launch_bounds__(block_threads(V, SMALL), fwd_blocks(V, SMALL)) norm_fwd_stats_kernel(NormArgs a) {
   extern __shared__ float sm[];
@@ -417,11 +420,6 @@ __global__ void __launch_bounds__(block_threads(V, SMALL), fwd_blocks(V, SMALL))
   const TX* X = static_cast<const TX*>(a.X);
   const int t = blockIdx.x;
   int left = 0;  // pieces of long segments
-  // the last turn whose pivot was far off in some group: turns are counted, so the
-  // word is never reset between those who read it and those who write it
-  __shared__ int far_turn;
-  if (threadIdx.x == 0) far_turn = 0;
-  int turn = 0;
   // slot i of this thread: its i-th row of a short segment, kept for the output
   const uint32_t slots = static_cast<uint32_t>(__cvta_generic_to_shared(ring)) + threadIdx.x * 16;
   const uint32_t next = blockDim.x * 16;
@@ -430,9 +428,11 @@ __global__ void __launch_bounds__(block_threads(V, SMALL), fwd_blocks(V, SMALL))
     const bool keep = whole && rb - ra <= a.keep * a.RP;
     const int rows = p.rows(a, ra, rb);
     const float inv = rcp_f((float)(rb - ra) * (float)a.cg);  // 1 / values of a group
-    bool again = false;  // the turn about the mean
-    while (true) {
-      ++turn;
+    // AGAIN: the turn about the mean, in code of its own (one loop for both turns spilt:
+    // 716847 x 256 bf16 215 us against 201); true where another one is due
+    const auto sums = [&](auto AGAIN) -> bool {
+      constexpr bool again = decltype(AGAIN)::value;
+      bool far = false;  // in a group whose sums this thread finished
       float s1 = 0.f, s2 = 0.f;  // over this thread's channels
       if (p.on) {
         constexpr int U = 32 / V;
@@ -501,8 +501,7 @@ __global__ void __launch_bounds__(block_threads(V, SMALL), fwd_blocks(V, SMALL))
         const float mean = (again ? gm[g] : to_f32(X[ra * a.ldx + (int64_t)g * a.cg])) + d;
         const float m2 = fmaxf(Q - S * d, 0.f) + 0.f * Q;  // the product keeps a NaN
         gm[g] = mean;
-        // also where Q has left fp32's range, but not where the rows hold what is not finite
-        if (!(d * d <= kFar * (m2 * inv)) && fabsf(mean) < __int_as_float(0x7f800000)) far_turn = turn;
+        if (is_far(d, m2 * inv, mean)) far = true;
         if (whole) {
           const float rstd = rsqrtf(m2 * inv + a.eps);
           gr[g] = rstd;
@@ -516,11 +515,14 @@ __global__ void __launch_bounds__(block_threads(V, SMALL), fwd_blocks(V, SMALL))
         chunk_sums(a, part, at_part, p.in, s1, s2, finish);
       else
         block_sums(a, width, red1, red2, ch1, ch2, nullptr, finish);
-      // read behind the barrier that ends the sums, and written again only behind the
-      // next turn's first one
-      if (again || far_turn != turn) break;
-      again = true;
-    }
+      if constexpr (again) {
+        __syncthreads();
+        return false;
+      } else {
+        return __syncthreads_or(far);  // ends the sums, and decides for the whole block
+      }
+    };
+    if (sums(std::false_type())) sums(std::true_type());
     if (keep) {
       float mu[V], sc[V], bt[V];
       fwd_channels<V>(a, p, gm, gr, mu, sc, bt);
@@ -581,10 +583,11 @@ __device__ __forceinline__ void for_long(const NormArgs& a, int blocks, Fn f) {
   }
 }
 
-// Joins the pieces of long segments.  First mean = mean_0 + sum m_i (mean_i -
-// mean_0) / M, which is off by a few 2^-24 of mean_0's distance; then about it, so
-// that no piece's place matters: with d_i = mean_i - mean and D = sum m_i d_i / M,
-// mean += D, M2 = sum (M2_i + m_i d_i^2) - M D^2.
+// Joins the pieces of long segments about the first one's mean: with
+// d_i = mean_i - mean_0 and D = sum m_i d_i / M, mean = mean_0 + D and
+// M2 = sum (M2_i + m_i d_i^2) - M D^2.  Where the first piece lies far from the
+// others, once more about the mean, as above (always both: 47 -> 52 us at one
+// segment of 65537 x 256).
 __global__ void __launch_bounds__(FIN_THREADS) norm_fwd_join_kernel(NormArgs a) {
   cudaTriggerProgrammaticLaunchCompletion();
   cudaGridDependencySynchronize();
@@ -592,33 +595,26 @@ __global__ void __launch_bounds__(FIN_THREADS) norm_fwd_join_kernel(NormArgs a) 
   const int lane = threadIdx.x & 31;
   for_long(a, gridDim.x, [&](int s, int sb, int se, int t0, int t1, int g) {
     const float2* part = a.part + (int64_t)s * a.groups + g;
-    const float first = part[(int64_t)t0 * a.groups].x;
-    // values of piece i's group
-    const auto count = [&](int i) {
-      return (float)((int)min((int64_t)se, (i + 1) * (int64_t)a.R) - max(sb, i * a.R)) * (float)a.cg;
-    };
-    float M = 0.f, S = 0.f, Q = 0.f;
+    float about = part[(int64_t)t0 * a.groups].x;
+    for (int turn = 0; turn < 2; ++turn) {
+      float M = 0.f, S = 0.f, Q = 0.f;
 #pragma unroll 8
-    for (int i = t0 + lane; i <= t1; i += 32) {
-      const float m = count(i);
-      M += m;
-      S += m * (part[(int64_t)i * a.groups].x - first);
-    }
-    M = warp_sum(M);
-    const float mean = first + warp_sum(S) / M;
-    S = 0.f;
-#pragma unroll 8
-    for (int i = t0 + lane; i <= t1; i += 32) {
-      const float2 v = part[(int64_t)i * a.groups];
-      const float m = count(i), d = v.x - mean;
-      S += m * d;
-      Q += v.y + m * d * d;
-    }
-    S = warp_sum(S), Q = warp_sum(Q);
-    if (lane == 0) {
-      const float D = S / M;
-      a.mean[(int64_t)s * a.groups + g] = mean + D;
-      a.rstd[(int64_t)s * a.groups + g] = rsqrtf(fmaxf(Q - S * D, 0.f) / M + 0.f * Q + a.eps);
+      for (int i = t0 + lane; i <= t1; i += 32) {
+        const float2 v = part[(int64_t)i * a.groups];
+        const float m = (float)((int)min((int64_t)se, (i + 1) * (int64_t)a.R) - max(sb, i * a.R)) * (float)a.cg;
+        const float d = v.x - about;
+        M += m;
+        S += m * d;
+        Q += v.y + m * d * d;
+      }
+      M = warp_sum(M), S = warp_sum(S), Q = warp_sum(Q);
+      const float D = S / M, var = fmaxf(Q - S * D, 0.f) / M + 0.f * Q;
+      about += D;
+      if (lane == 0) {
+        a.mean[(int64_t)s * a.groups + g] = about;
+        a.rstd[(int64_t)s * a.groups + g] = rsqrtf(var + a.eps);
+      }
+      if (!is_far(D, var, about)) break;  // the same in every lane
     }
   });
 }
@@ -844,8 +840,10 @@ __global__ void __launch_bounds__(block_threads(V, SMALL), bwd_blocks(V, SMALL))
     };
     if (chunks) {
       chunk_sums(a, part, at_part, p.in, s1, s2, finish);
+      __syncthreads();
     } else {
       block_sums(a, width, red1, red2, ch1, ch2, a.gamma, finish);
+      __syncthreads();
       for (int c = threadIdx.x; c < a.C; c += blockDim.x) {
         acc1[c] += ch1[c];
         acc2[c] += ch2[c];
