@@ -50,7 +50,8 @@ class NodeBlock:
         self._kept = None
 
     def forward(self, H, out=None, stream=None):
-        """H: fp32 [n, F]; returns H' (fp32 [n, F], `out` if given)."""
+        """H: fp32 [n, F]; returns H' (fp32 [n, F], `out` if given; with out = H in
+        place, which costs a copy: the backward needs H as it was)."""
         n, F, Fm, dev = H.shape[0], self.F, self.F_mid, H.device
         segs = 1 if self.seg is None else self.seg.numel() - 1
         with torch.cuda.stream(stream):
@@ -63,7 +64,8 @@ class NodeBlock:
                                beta=w["beta"], act=self.act_norm, stream=stream)
             gnn_gated_fwd(Y, n, F, self.bf16["Wg"], self.bf16["Wu"], Fm, M, act=self.act, stream=stream)
             gnn_dense_fwd(M, n, Fm, self.bf16["Wd"], F, False, Z, stream=stream)
-            self._kept = (H, Y, M, mean, rstd)
+            shared = out is not None and out.untyped_storage().data_ptr() == H.untyped_storage().data_ptr()
+            self._kept = (H.clone() if shared else H, Y, M, mean, rstd)
             return torch.add(H, Z, out=out)
 
     def backward(self, dH_out, stream=None):

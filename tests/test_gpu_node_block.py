@@ -120,3 +120,23 @@ def test_layers_and_blocks_train(bits):
     for got, ref in zip(losses, refs):
         assert abs(got - ref) <= TOL * ref + share * (refs[0] - ref)
     assert losses[-1] < losses[0]
+
+
+def test_residual_in_place():
+    """out = H: the backward still has what the forward read."""
+    from sparse_aggregation_message_gb300.block import NodeBlock
+    n, F = 700, 64
+    g = torch.Generator(device="cuda").manual_seed(1)
+    H, dO = torch.randn(n, F, generator=g, device="cuda"), torch.randn(n, F, generator=g, device="cuda")
+    wide = torch.zeros(n, 2 * F, device="cuda")
+    wide[:, :F] = H
+    got = []
+    for x, place in ((H.clone(), False), (H.clone(), True), (wide[:, :F], True)):
+        blk = NodeBlock(F, 176, 8, seed=3)
+        out = blk.forward(x, out=x if place else None)
+        assert not place or out is x
+        got.append([out.clone(), blk.backward(dO)] + [v.clone() for v in blk.grads.values()])
+    G.gnn_sync_check()
+    for other in got[1:]:
+        for a, b in zip(got[0], other):
+            assert torch.equal(a, b)
