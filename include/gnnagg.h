@@ -643,7 +643,12 @@ gnn_status gnn_spmm_bwd_blocked(const gnn_csr* csr, const gnn_boundary* bnd,
  * is a multiple of 8 and, as an output, at least round_up(F,16), with columns
  * F..round_up(F,16)-1 written as zero (the operand layout of
  * gnn_dense_fwd).  Padding columns of inputs are not used, but a row's whole
- * stride lies in the caller's allocation. */
+ * stride lies in the caller's allocation.  Padding is zero also in rows that
+ * hold values which are not finite.
+ *
+ * Outputs lie apart from each other and from every input, except where a
+ * function says that one may take an input's place; matrices that overlap
+ * otherwise are refused (columns of one buffer do not overlap). */
 
 /* Group norm with an activation, channels last.  Segment s holds the rows
  * [seg_start[s], seg_start[s+1]) -- a graph of a batch, or a partition:
@@ -661,7 +666,8 @@ gnn_status gnn_spmm_bwd_blocked(const gnn_csr* csr, const gnn_boundary* bnd,
  * as a sum of squares about the mean, up to a factor of 17 in the rounding.
  * Types (x_type -> y_type): GNN_F32 -> any, GNN_BF16 -> GNN_BF16,
  * GNN_F16 -> GNN_F16.  C <= 1024, a multiple of groups.  Rows of a seg_start
- * that is not ascending raise the device-check flag. */
+ * that is not ascending raise the device-check flag.  Y may be X (one type and
+ * stride), and dX of the backward X or dY. */
 gnn_status gnn_group_norm_workspace(int64_t n, int32_t C, int32_t groups, int32_t n_seg,
                                     size_t* ws_bytes);
 gnn_status gnn_group_norm_fwd(const void* X, int64_t ldx, int32_t x_type, int64_t n, int32_t C,
@@ -695,7 +701,9 @@ gnn_status gnn_gated_fwd(const void* X, int64_t ldx, int32_t type, int64_t n, in
  * forward): dG = dH U act'(G), dU = dH act(G), rounded to `type` as tensor-core
  * operands; dX = dG Wg^T + dU Wu^T, dWg = X^T dG, dWu = X^T dU, each
  * accumulated in fp32, in a fixed order, and rounded to `type`.  dH is `type`
- * or GNN_F32 (dh_type).  dX may be NULL; dWg and dWu may both be NULL. */
+ * or GNN_F32 (dh_type).  dX may be NULL; dWg and dWu may both be NULL.  dX may
+ * overlap dH, and X where no weights' gradients are wanted; dWg and dWu may
+ * overlap any input.  In fp16 a dG or dU past 65504 becomes infinite: scale dH. */
 gnn_status gnn_gated_bwd(const void* dH, int64_t lddh, int32_t dh_type, const void* X,
                          int64_t ldx, int32_t type, int64_t n, int32_t F_in, const void* Wg,
                          int64_t ldwg, const void* Wu, int64_t ldwu, int32_t F_mid, int32_t act,
@@ -718,7 +726,8 @@ gnn_status gnn_gated_bwd(const void* dH, int64_t lddh, int32_t dh_type, const vo
  * to nearest even from value (1/scale), except that a positive sqrt(v) never
  * becomes zero (its smallest code is 2^-9), which would leave eps alone in the
  * division.  The parameter update uses m and v before they are rounded to
- * codes.  copy (NULL or bf16 [n]) receives the updated parameters rounded. */
+ * codes.  copy (NULL or bf16 [n]) receives the updated parameters rounded.  No
+ * two arrays of a call overlap, nor is a tensor listed twice. */
 typedef struct gnn_adamw_tensor {
   void* param;      /* fp32 or bf16 [n], updated in place */
   const void* grad; /* fp32, bf16 or fp16 [n]             */

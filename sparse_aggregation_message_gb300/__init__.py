@@ -945,6 +945,9 @@ class AdamwTensors:
                 size = -(-n // 256) if name.endswith("scale") else n
                 if t.dtype != want[name] or t.numel() != size or not t.is_contiguous() or t.device.type != "cuda":
                     raise ValueError(f"{name}[{i}]: needs a contiguous {want[name]} CUDA tensor of {size} elements")
+        places = [p.data_ptr() for p in params if p.numel()]
+        if len(set(places)) < len(places):
+            raise ValueError("params: a tensor is listed twice")
         self.param_type = _type(params[0]) if k else 0
         self.grad_type = _type(grads[0]) if k else 0
         self._keep = {name: list(ts) for name, ts in lists.items() if ts is not None}

@@ -833,6 +833,9 @@ bool bad_mat(const void* p, int64_t ld, int64_t cols, int elem) {
   return !p || ((uintptr_t)p & 15) || (ld * elem) % 16 || ld < cols || ld > ((int64_t)1 << 36);
 }
 
+// A 2-byte matrix's memory.
+Span span(const void* p, int64_t rows, int64_t cols, int64_t ld) { return {p, rows, 2 * ld, 2 * cols}; }
+
 }  // namespace
 
 }  // namespace gnn
@@ -864,6 +867,9 @@ extern "C" gnn_status gnn_gated_fwd(const void* X, int64_t ldx, int32_t type, in
               "gnn_gated_fwd: Wg and Wu need 16-byte aligned rows and strides >= F_mid");
   GNN_REQUIRE(!bad_mat(H, ldh, up(F_mid, 16), 2),
               "gnn_gated_fwd: H needs 16-byte aligned rows and ldh >= round_up(F_mid, 16)");
+  const Span hs = span(H, n, up(F_mid, 16), ldh);
+  GNN_REQUIRE(!overlap(hs, span(X, n, F_in, ldx)) && !overlap(hs, span(Wg, F_in, F_mid, ldwg)) &&
+                  !overlap(hs, span(Wu, F_in, F_mid, ldwu)), "gnn_gated_fwd: H overlaps X, Wg or Wu");
   const Mat x{const_cast<void*>(X), ldx}, g{const_cast<void*>(Wg), ldwg}, u{const_cast<void*>(Wu), ldwu}, h{H, ldh};
   cudaStream_t st = as_stream(stream);
   return type == GNN_BF16 ? gated_fwd<__nv_bfloat16>(n, F_in, F_mid, act, x, g, u, h, st)
@@ -889,6 +895,13 @@ extern "C" gnn_status gnn_gated_bwd(const void* dH, int64_t lddh, int32_t dh_typ
               "gnn_gated_bwd: dX needs 16-byte aligned rows and lddx >= round_up(F_in, 16)");
   GNN_REQUIRE(!dWg || (!bad_mat(dWg, lddwg, up(F_mid, 16), 2) && !bad_mat(dWu, lddwu, up(F_mid, 16), 2)),
               "gnn_gated_bwd: dWg and dWu need 16-byte aligned rows and strides >= round_up(F_mid, 16)");
+  // dH is read before anything is written, X, Wg and Wu before dWg and dWu are
+  const Span dxs = span(dX, n, up(F_in, 16), lddx), dgs = span(dWg, F_in, up(F_mid, 16), lddwg),
+             dus = span(dWu, F_in, up(F_mid, 16), lddwu);
+  GNN_REQUIRE(!overlap(dxs, span(Wg, F_in, F_mid, ldwg)) && !overlap(dxs, span(Wu, F_in, F_mid, ldwu)),
+              "gnn_gated_bwd: dX overlaps Wg or Wu");
+  GNN_REQUIRE(!dWg || !overlap(dxs, span(X, n, F_in, ldx)), "gnn_gated_bwd: dX overlaps X, which dWg and dWu need");
+  GNN_REQUIRE(!overlap(dxs, dgs) && !overlap(dxs, dus) && !overlap(dgs, dus), "gnn_gated_bwd: outputs overlap");
   bool ok;
   const GatedWs w = gated_ws(ws, ws_bytes, n, F_in, F_mid, &ok);
   GNN_REQUIRE(ws && ok && ((uintptr_t)ws & 15) == 0, "gnn_gated_bwd: workspace too small (%zu < %zu) or misaligned",

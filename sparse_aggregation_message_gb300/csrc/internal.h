@@ -57,6 +57,28 @@ struct Arena {
   bool ok() const { return base == nullptr || used <= cap; }
 };
 
+// `rows` rows of `width` bytes, `stride` bytes apart, in device memory.
+struct Span {
+  const void* p;
+  int64_t rows, stride, width;
+};
+// Whether two of them may share a byte.  Rows that lie apart in a common period of
+// the strides (columns of one buffer) do not.
+inline bool overlap(const Span& a, const Span& b) {
+  if (!a.p || !b.p || a.rows < 1 || b.rows < 1 || a.width < 1 || b.width < 1) return false;
+  const __int128 pa = (uintptr_t)a.p, pb = (uintptr_t)b.p;  // strides may be anything
+  if (pa + (__int128)(a.rows - 1) * a.stride + a.width <= pb || pb + (__int128)(b.rows - 1) * b.stride + b.width <= pa)
+    return false;
+  int64_t period = a.rows > 1 ? a.stride : 0;
+  for (int64_t r = b.rows > 1 ? b.stride : 0; r;) {
+    const int64_t t = period % r;
+    period = r, r = t;
+  }
+  if (period == 0) return true;
+  const int64_t d = ((int64_t)(pb - pa) % period + period) % period;  // b's place in a's period
+  return d < a.width || d + b.width > period;
+}
+
 inline bool is_valid_bits(int b) { return b == 1 || b == 2 || b == 4 || b == 8 || b == 32; }
 
 constexpr int kMaxF = 1024;

@@ -1014,6 +1014,14 @@ bool bad_rows(const void* p, int64_t ld, int type, int C, bool output) {
   return !p || ((uintptr_t)p & 15) || ld % unit || ld < (C + pad - 1) / pad * pad;
 }
 
+// Whether an output may be written while an input is read: apart from it, or in its
+// place (each element is then read by the thread that writes it, before it does).
+bool clashes(const void* out, int64_t ldo, int otype, const void* in, int64_t ldi, int itype, int64_t n, int C) {
+  if (out == in && ldo == ldi && otype == itype) return false;
+  const int64_t so = type_size(otype), si = type_size(itype), pad = otype == GNN_F32 ? 4 : 16;
+  return overlap({out, n, ldo * so, (C + pad - 1) / pad * pad * so}, {in, n, ldi * si, C * si});
+}
+
 struct Launch {
   cudaStream_t st;
   template <class... P, class... A>
@@ -1159,6 +1167,7 @@ extern "C" gnn_status gnn_group_norm_fwd(const void* X, int64_t ldx, int32_t x_t
               "and ldx >= C");
   GNN_REQUIRE(n == 0 || !bad_rows(Y, ldy, y_type, C, true), "gnn_group_norm_fwd: Y needs 16-byte aligned rows and "
               "ldy >= C rounded up to 4 (fp32) or 16");
+  GNN_REQUIRE(!clashes(Y, ldy, y_type, X, ldx, x_type, n, C), "gnn_group_norm_fwd: Y overlaps X and is not in its place");
   bool ok;
   const NormWs w = norm_ws(ws, ws_bytes, n, C, groups, n_seg, &ok);
   GNN_REQUIRE(ws && ok, "gnn_group_norm_fwd: workspace too small (%zu < %zu)", ws_bytes, w.bytes);
@@ -1194,6 +1203,8 @@ extern "C" gnn_status gnn_group_norm_bwd(const void* dY, int64_t ldy, int32_t y_
               "and ldy >= C");
   GNN_REQUIRE(n == 0 || !bad_rows(dX, lddx, x_type, C, true), "gnn_group_norm_bwd: dX needs 16-byte aligned rows "
               "and lddx >= C rounded up to 4 (fp32) or 16");
+  GNN_REQUIRE(!clashes(dX, lddx, x_type, X, ldx, x_type, n, C) && !clashes(dX, lddx, x_type, dY, ldy, y_type, n, C),
+              "gnn_group_norm_bwd: dX overlaps X or dY and is not in its place");
   bool ok;
   const NormWs w = norm_ws(ws, ws_bytes, n, C, groups, n_seg, &ok);
   GNN_REQUIRE(ws && ok, "gnn_group_norm_bwd: workspace too small (%zu < %zu)", ws_bytes, w.bytes);

@@ -249,3 +249,18 @@ def test_padding_is_zero_whatever_the_rows_hold(n, D, F, t):
     for buf, c in ((bh, F), (bx, D), (bg, F), (bu, F)):
         pad = -(-c // 16) * 16
         assert torch.all(buf[:, c:pad] == 0) and torch.all(torch.isnan(buf[:, pad:]))
+
+
+def test_outputs_in_the_place_of_inputs():
+    """What the header allows: dX over dH, dX over X without weights' gradients, dWg and dWu over Wg and Wu."""
+    n, D, F = 1500, 208, 208
+    x, wg, wu = operands(n, D, F, torch.bfloat16)
+    dh = mat(n, F, torch.bfloat16, 5, extra=8)[1]
+    full = [mat(r, c, torch.bfloat16, 6)[1] for r, c in ((n, D), (D, F), (D, F))]
+    G.gnn_gated_bwd(dh, x, n, D, wg, wu, F, *full)
+    x2, dh2, wg2, wu2 = (v.clone() for v in (x, dh, wg, wu))
+    G.gnn_gated_bwd(dh, x2, n, D, wg, wu, F, dX=x2)
+    G.gnn_gated_bwd(dh2, x, n, D, wg2, wu2, F, dX=dh2, dWg=wg2, dWu=wu2)
+    G.gnn_sync_check()
+    for got, want in ((x2, full[0]), (dh2, full[0]), (wg2, full[1]), (wu2, full[2])):
+        assert torch.equal(got, want)

@@ -398,3 +398,25 @@ def test_pieces_far_from_the_first():
     rr = 1 / torch.sqrt(((v - rm[:, None]) ** 2).mean((0, 2)) + 1e-5)
     assert torch.all((mean[0].double() - rm).abs() <= K * (1 / rr + rm.abs() * 2 ** -20) * 2)
     assert torch.all((rstd[0].double() - rr).abs() <= 2 * K * rr)
+
+
+@pytest.mark.parametrize("n,C,groups,cut,t", [(5003, 64, 8, "small", "bf16"), (4000, 35, 7, "small", "f32"),
+                                              (70001, 40, 8, "parts", "f32"), (256, 1024, 1, "one", "f16")])
+def test_in_place(n, C, groups, cut, t):
+    """Y in X's place, dX in X's and in dY's: the bits of separate outputs."""
+    seg = cuts(n, cut)
+    S = len(bounds(seg, n))
+    stat = lambda: (torch.empty(S, groups, device="cuda"), torch.empty(S, groups, device="cuda"))  # noqa: E731
+    x, dy = rows(n, C, TYPES[t], 1, extra=16)[1], rows(n, C, TYPES[t], 4, extra=16)[1]
+    copy = lambda v: v._base.clone()[:, :C]  # noqa: E731
+    y, dx, (mean, rstd) = copy(x), copy(x), stat()
+    G.gnn_group_norm_fwd(x, n, C, groups, y, mean, rstd, seg_start=seg, act="silu")
+    G.gnn_group_norm_bwd(dy, x, n, C, groups, mean, rstd, dx, seg_start=seg, act="silu")
+    a, (m, r) = copy(x), stat()
+    G.gnn_group_norm_fwd(a, n, C, groups, a, m, r, seg_start=seg, act="silu")
+    b, c = copy(x), copy(dy)
+    G.gnn_group_norm_bwd(dy, b, n, C, groups, mean, rstd, b, seg_start=seg, act="silu")
+    G.gnn_group_norm_bwd(c, x, n, C, groups, mean, rstd, c, seg_start=seg, act="silu")
+    G.gnn_sync_check()
+    assert torch.equal(a, y) and torch.equal(m, mean) and torch.equal(r, rstd)
+    assert torch.equal(b, dx) and torch.equal(c, dx)

@@ -150,3 +150,79 @@ def test_binding_refuses_before_the_library():
         G.AdamwTensors([x], [], [x], [x])
     with pytest.raises(ValueError, match="act"):
         G._act("swish")
+
+
+MB = 1 << 20
+
+
+@pytest.mark.parametrize("bad", [
+    dict(Y=8192 + 16, X=8192), dict(X=8192, Y=8192, ldy=128), dict(X=8192, Y=8192, yt=BF16), dict(X=8192, Y=8192 + 4 * 64 * 9),
+    dict(X=8192, ldx=128, Y=8192 + 4 * 60, ldy=128), dict(X=8192 + 4 * 60, ldx=128, Y=8192, ldy=128)])
+def test_group_norm_forward_refuses_overlap(lib, bad):
+    """A part of X's memory, other strides, another type: none of it is launched."""
+    assert norm_fwd(lib, **bad) == INVALID
+    assert b"overlaps" in lib.gnn_last_error()
+
+
+@pytest.mark.parametrize("bad", [
+    dict(dX=8192 + 16, X=8192), dict(dX=4096 + 256, dY=4096), dict(X=MB, dY=8192, yt=BF16, dX=8192), dict(X=MB, dX=MB, lddx=128)])
+def test_group_norm_backward_refuses_overlap(lib, bad):
+    assert norm_bwd(lib, **bad) == INVALID
+    assert b"overlaps" in lib.gnn_last_error()
+
+
+@pytest.mark.parametrize("bad", [
+    dict(D=128, ldx=128, X=MB, H=MB), dict(D=128, ldx=128, X=MB, H=MB + 256), dict(Wg=MB, H=MB + 2 * 128 * 63),
+    dict(Wu=MB + 2 * 128 * 9, H=MB), dict(X=MB, ldx=512, H=MB + 96, ldh=512)])
+def test_gated_forward_refuses_overlap(lib, bad):
+    assert gated_fwd(lib, **bad) == INVALID
+    assert b"overlaps" in lib.gnn_last_error()
+
+
+APART = dict(dH=MB, X=2 * MB, Wg=3 * MB, Wu=4 * MB, dX=5 * MB, dWg=6 * MB, dWu=7 * MB)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(dX=2 * MB), dict(dX=2 * MB + 128 * 9), dict(dX=3 * MB), dict(dX=4 * MB + 64), dict(dX=6 * MB), dict(dX=7 * MB),
+    dict(dWg=7 * MB), dict(dWu=6 * MB + 256, ldg=128)])
+def test_gated_backward_refuses_overlap(lib, bad):
+    """dX over X would be written while dWg and dWu still read X."""
+    assert gated_bwd(lib, **{**APART, **bad}) == INVALID
+    assert b"overlap" in lib.gnn_last_error()
+
+
+def test_what_may_overlap_is_not_refused(lib):
+    """Up to the last check, a workspace that is too small: in place, columns of one
+    buffer, neighbours, and what is read before it is written."""
+    small = dict(ws_bytes=8)
+    for kw in (dict(X=8192, Y=8192), dict(X=8192, ldx=128, Y=8192 + 256, ldy=128), dict(X=8192 + 256, ldx=128, Y=8192, ldy=128),
+               dict(X=8192, Y=8192 + 4 * 64 * 10), dict(X=8192, xt=BF16, yt=BF16, Y=8192),
+               dict(X=8192, ldx=256, Y=8192 + 256, ldy=128)):
+        assert norm_fwd(lib, **kw, **small) == INVALID and b"workspace" in lib.gnn_last_error(), kw
+    for kw in (dict(dX=8192, X=8192), dict(dX=4096, dY=4096), dict(X=MB, ldx=192, dY=MB + 256, ldy=192, dX=MB + 512, lddx=192)):
+        assert norm_bwd(lib, **kw, **small) == INVALID and b"workspace" in lib.gnn_last_error(), kw
+    for kw in (dict(), dict(dX=MB, D=128, ldx=128, lddx=128), dict(dX=2 * MB, dWg=None, dWu=None), dict(dWg=3 * MB, dWu=4 * MB),
+               dict(dWg=2 * MB), dict(X=2 * MB, ldx=128, dX=2 * MB + 128, lddx=128)):
+        assert gated_bwd(lib, **{**APART, **kw}, **small) == INVALID and b"workspace" in lib.gnn_last_error(), kw
+
+
+def test_adamw_tensors_refuse_a_tensor_listed_twice(monkeypatch):
+    """Two warps would update the same elements."""
+    torch = pytest.importorskip("torch")
+    import sparse_aggregation_message_gb300 as G
+
+    class Fake:  # stands for a CUDA tensor
+        def __init__(self, at, n=8, dtype=torch.float32):
+            self.at, self.n, self.dtype, self.device = at, n, dtype, torch.device("cuda", 0)
+
+        numel = lambda self: self.n  # noqa: E731
+        data_ptr = lambda self: self.at  # noqa: E731
+        is_contiguous = lambda self: True  # noqa: E731
+
+    def tensors(p):
+        k = len(p)
+        return G.AdamwTensors([Fake(a, n) for a, n in p], *([Fake((10 * j + i) * 4096, p[i][1]) for i in range(k)] for j in (1, 2, 3)))
+
+    assert tensors([(64, 8), (128, 8), (0, 0), (0, 0)]).count == 4
+    with pytest.raises(ValueError, match="twice"):
+        tensors([(64, 8), (128, 8), (64, 8)])
