@@ -338,3 +338,34 @@ def test_roots_and_quotients_of_every_mantissa(part):
         want = 0 - (m / 2) / torch.sqrt(v / 2)
         assert torch.equal(dev["params"][0].cpu(), want)
         assert torch.equal(dev["v"][0].cpu(), v / 2)
+
+
+def test_small_tensors_before_a_large_one():
+    """A clipped step over sixty small tensors and a large one: the same result
+    and about the same time whichever comes first."""
+    small, large = [64] * 60, [30_000_000]
+    times, norms = [], []
+    for sizes in (large + small, small + large):
+        host = make([64] * 60, "f32", "bf16", 32, 30, exact_squares=True)
+        dev = on_gpu(host)
+        big = dict(params=torch.zeros(large[0], device="cuda"), m=torch.zeros(large[0], device="cuda"),
+                   v=torch.zeros(large[0], device="cuda"), copies=torch.zeros(large[0], dtype=torch.bfloat16, device="cuda"))
+        # squares that add exactly
+        big["grads"] = ((torch.arange(large[0], device="cuda") % 129 - 64) / 64).to(torch.bfloat16)
+        lists = {k: None if v is None else (v + [big[k]] if sizes[0] == 64 else [big[k]] + v) for k, v in dev.items()}
+        T, state, norm = G.AdamwTensors(**lists), G.adamw_state(), torch.zeros(1, device="cuda")
+        want = math.sqrt(sum(float(g.double().square().sum()) for g in lists["grads"]))
+        best = math.inf
+        for _ in range(6):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            G.gnn_adamw_step(T, state, max_norm=1.0, grad_norm=norm, **HYPER)
+            b.record()
+            torch.cuda.synchronize()
+            best = min(best, a.elapsed_time(b))
+        G.gnn_sync_check()
+        assert float(norm) == float(torch.tensor(want, dtype=torch.float64).float())
+        times.append(best)
+        norms.append(lists["params"][0 if sizes[0] != 64 else -1].clone())
+    assert torch.equal(*norms)
+    assert times[1] <= 2 * times[0], times
