@@ -646,6 +646,9 @@ gnn_status gnn_spmm_bwd_blocked(const gnn_csr* csr, const gnn_boundary* bnd,
  * stride lies in the caller's allocation.  Padding is zero also in rows that
  * hold values which are not finite.
  *
+ * seg_start, a step state and workspaces lie on 8-byte borders (gnn_gated_bwd's
+ * workspace on a 16-byte one), fp32 vectors on 4-byte ones.
+ *
  * Outputs lie apart from each other and from every input, except where a
  * function says that one may take an input's place; matrices that overlap
  * otherwise are refused (columns of one buffer do not overlap). */

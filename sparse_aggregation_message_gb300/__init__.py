@@ -837,7 +837,11 @@ def _seg(seg_start):
 
 def _ws(ws, nbytes: int, t, stream):
     """(pointer, bytes, owner) of the caller's workspace, or of one of the binding's."""
-    return _scratch(nbytes, t, stream) if ws is None else (ws.data_ptr(), ws.numel(), ws)
+    if ws is None:
+        return _scratch(nbytes, t, stream)
+    if not ws.is_cuda or not ws.is_contiguous():
+        raise ValueError("ws: needs a contiguous CUDA tensor")
+    return ws.data_ptr(), ws.numel(), ws
 
 
 @functools.lru_cache(maxsize=1024)

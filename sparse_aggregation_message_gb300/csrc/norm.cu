@@ -18,6 +18,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <initializer_list>
 
 #include "internal.h"
 #include "nodewise.cuh"
@@ -1139,15 +1140,18 @@ extern "C" gnn_status gnn_group_norm_workspace(int64_t n, int32_t C, int32_t gro
   return GNN_OK;
 }
 
-static gnn_status check_norm_args(const char* who, int x_type, int y_type, int act, const int64_t* seg,
-                                  int n_seg, const float* gamma, const float* beta) {
+static gnn_status check_norm_args(const char* who, int x_type, int y_type, int act, const int64_t* seg, int n_seg,
+                                  std::initializer_list<const void*> fp32, const void* ws) {
   if (!is_type(x_type) || !is_type(y_type) || !is_act(act))
     return fail(GNN_ERR_INVALID_ARG, "%s: unknown type or activation", who);
   if (x_type != GNN_F32 && x_type != y_type)
     return fail(GNN_ERR_UNSUPPORTED, "%s: a 2-byte x_type needs the same y_type", who);
   if (!seg && n_seg != 1) return fail(GNN_ERR_INVALID_ARG, "%s: seg_start NULL needs n_seg = 1", who);
-  if (((uintptr_t)seg & 7) || ((uintptr_t)gamma & 3) || ((uintptr_t)beta & 3))
-    return fail(GNN_ERR_INVALID_ARG, "%s: misaligned seg_start, gamma or beta", who);
+  uintptr_t low = 0;
+  for (const void* p : fp32) low |= (uintptr_t)p;
+  if (((uintptr_t)seg & 7) || (low & 3))
+    return fail(GNN_ERR_INVALID_ARG, "%s: misaligned seg_start or fp32 vector", who);
+  if ((uintptr_t)ws & 7) return fail(GNN_ERR_INVALID_ARG, "%s: misaligned workspace", who);
   return GNN_OK;
 }
 
@@ -1160,7 +1164,8 @@ extern "C" gnn_status gnn_group_norm_fwd(const void* X, int64_t ldx, int32_t x_t
   const char* who = "gnn_group_norm_fwd";
   gnn_status s = check_norm(who, n, C, groups, n_seg);
   if (s != GNN_OK) return s;
-  if ((s = check_norm_args(who, x_type, y_type, act, seg_start, n_seg, gamma, beta)) != GNN_OK) return s;
+  s = check_norm_args(who, x_type, y_type, act, seg_start, n_seg, {gamma, beta, mean, rstd}, ws);
+  if (s != GNN_OK) return s;
   GNN_REQUIRE(eps >= 1.2e-38 && eps < 1e30, "gnn_group_norm_fwd: eps must be positive (a normal fp32 value)");
   GNN_REQUIRE(mean && rstd, "gnn_group_norm_fwd: NULL mean or rstd");
   GNN_REQUIRE(n == 0 || !bad_rows(X, ldx, x_type, C, false), "gnn_group_norm_fwd: X needs 16-byte aligned rows "
@@ -1195,7 +1200,8 @@ extern "C" gnn_status gnn_group_norm_bwd(const void* dY, int64_t ldy, int32_t y_
   const char* who = "gnn_group_norm_bwd";
   gnn_status s = check_norm(who, n, C, groups, n_seg);
   if (s != GNN_OK) return s;
-  if ((s = check_norm_args(who, x_type, y_type, act, seg_start, n_seg, gamma, beta)) != GNN_OK) return s;
+  s = check_norm_args(who, x_type, y_type, act, seg_start, n_seg, {gamma, beta, mean, rstd, dgamma, dbeta}, ws);
+  if (s != GNN_OK) return s;
   GNN_REQUIRE(mean && rstd, "gnn_group_norm_bwd: NULL mean or rstd");
   GNN_REQUIRE(n == 0 || !bad_rows(X, ldx, x_type, C, false), "gnn_group_norm_bwd: X needs 16-byte aligned rows "
               "and ldx >= C");

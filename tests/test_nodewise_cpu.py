@@ -226,3 +226,27 @@ def test_adamw_tensors_refuse_a_tensor_listed_twice(monkeypatch):
     assert tensors([(64, 8), (128, 8), (0, 0), (0, 0)]).count == 4
     with pytest.raises(ValueError, match="twice"):
         tensors([(64, 8), (128, 8), (64, 8)])
+
+
+@pytest.mark.parametrize("bad", [dict(mean=66), dict(rstd=65), dict(gamma=66), dict(beta=67), dict(ws=260), dict(ws=258)])
+def test_group_norm_forward_refuses_misaligned(lib, bad):
+    """What a kernel would read or write off its type's border faults there."""
+    assert norm_fwd(lib, **bad) == INVALID
+    assert b"misaligned" in lib.gnn_last_error()
+
+
+@pytest.mark.parametrize("bad", [dict(mean=66), dict(rstd=65), dict(dgamma=1026), dict(dbeta=1025), dict(gamma=62), dict(beta=2), dict(ws=260)])
+def test_group_norm_backward_refuses_misaligned(lib, bad):
+    a = dict(gamma=None, beta=None, dgamma=None, dbeta=None, mean=64, rstd=64, ws=256)
+    a.update(bad)
+    got = lib.gnn_group_norm_bwd(P(4096), 64, F32, P(MB), 64, F32, 10, 64, 8, P(None), 1, P(a["gamma"]), P(a["beta"]), 0, P(a["mean"]),
+                                 P(a["rstd"]), P(2 * MB), 64, P(a["dgamma"]), P(a["dbeta"]), P(a["ws"]), 1 << 20, None)
+    assert got == INVALID
+    assert b"misaligned" in lib.gnn_last_error()
+
+
+def test_binding_refuses_a_workspace_that_is_not_on_a_gpu():
+    torch = pytest.importorskip("torch")
+    import sparse_aggregation_message_gb300 as G
+    with pytest.raises(ValueError, match="ws"):
+        G._ws(torch.zeros(64, dtype=torch.uint8), 8, None, None)
