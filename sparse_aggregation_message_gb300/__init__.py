@@ -169,6 +169,7 @@ class _Torch:
         self.types = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
         self.f32, self.f64, self.i64, self.u8 = torch.float32, torch.float64, torch.int64, torch.uint8
         self.empty, self.on_stream = torch.empty, torch.cuda.stream
+        self.device = torch._C._cuda_getDevice
         self.raw_stream, self.capturing = torch._C._cuda_getCurrentRawStream, torch._C._cuda_isCurrentStreamCapturing
 
 
@@ -812,10 +813,13 @@ def _f32(t, count: int, what: str):
 
 
 def _current(t, stream) -> int:
-    """The raw stream of a call on t: `stream`, or t's device's current one."""
-    if stream is not None:
-        return stream.cuda_stream
-    return (_bits or _torch_bits()).raw_stream(t.get_device())
+    """The raw stream of a call on t: `stream`, or the current one.  The launch
+    goes to the current device, so t has to be there."""
+    b = _bits or _torch_bits()
+    dev = t.get_device()
+    if dev != b.device():
+        raise ValueError(f"tensors on cuda:{dev}, but the current device is cuda:{b.device()}: set it with torch.cuda.device")
+    return b.raw_stream(dev) if stream is None else stream.cuda_stream
 
 
 def _act(act: str) -> int:
@@ -947,6 +951,8 @@ class AdamwTensors:
                     continue
                 n = params[i].numel()
                 size = -(-n // 256) if name.endswith("scale") else n
+                if t.device != params[0].device:
+                    raise ValueError(f"{name}[{i}]: on {t.device}, params[0] on {params[0].device}")
                 if t.dtype != want[name] or t.numel() != size or not t.is_contiguous() or t.device.type != "cuda":
                     raise ValueError(f"{name}[{i}]: needs a contiguous {want[name]} CUDA tensor of {size} elements")
         places = [p.data_ptr() for p in params if p.numel()]
@@ -954,6 +960,7 @@ class AdamwTensors:
             raise ValueError("params: a tensor is listed twice")
         self.param_type = _type(params[0]) if k else 0
         self.grad_type = _type(grads[0]) if k else 0
+        self.device = params[0].device if k else None
         self._keep = {name: list(ts) for name, ts in lists.items() if ts is not None}
         at = lambda ts, i: None if ts is None or ts[i] is None else ts[i].data_ptr()  # noqa: E731
         self.c = (GnnAdamwTensor * max(k, 1))(*[
@@ -986,6 +993,8 @@ def gnn_adamw_step(tensors: AdamwTensors, state, lr: float, beta1: float = 0.9, 
     if state.dtype is not (_bits or _torch_bits()).f64 or state.numel() != 4 or not state.is_contiguous() or \
             not state.is_cuda:
         raise ValueError("state: needs the fp64 CUDA tensor that adamw_state makes")
+    if tensors.device is not None and state.device != tensors.device:
+        raise ValueError(f"state: on {state.device}, the tensors on {tensors.device}")
     at, size, ws = _ws(ws, gnn_adamw_workspace(), state, stream)
     call("gnn_adamw_step", tensors.c, tensors.count, tensors.param_type, tensors.grad_type, tensors.state_bits,
          state.data_ptr(), lr, beta1, beta2, eps, weight_decay, grad_scale, max_norm, _f32(grad_norm, 1, "grad_norm"), at,

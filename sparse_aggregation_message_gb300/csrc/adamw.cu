@@ -576,11 +576,9 @@ template <class TP, class TG, bool Q8>
 gnn_status launch_update(cudaStream_t st, int64_t grid, const Table& tab, const Hyper& h,
                          const Control* ctl) {
   constexpr int smem = ring_bytes<TP, TG, Q8>();
-  static bool ready = false;
-  if (!ready) {
-    GNN_CUDA(cudaFuncSetAttribute(adamw_kernel<TP, TG, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
-    ready = true;
-  }
+  static PerDevice done;
+  const gnn_status s = allow_smem(adamw_kernel<TP, TG, Q8>, smem, done);
+  if (s != GNN_OK) return s;
   return launch(st, grid, smem, adamw_kernel<TP, TG, Q8>, tab, h, ctl);
 }
 template <class TP, class TG>

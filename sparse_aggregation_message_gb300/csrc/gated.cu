@@ -593,15 +593,15 @@ __global__ void __launch_bounds__(ROW_THREADS)
 }
 
 // ---------------------------------------------------------------- host side
-int sm_count() {
-  static int n = 0;
-  if (n == 0) {
-    int dev = 0;
-    cudaGetDevice(&dev);
-    cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-    if (n <= 0) n = 152;
-  }
-  return n;
+constexpr int PAIRS = 76;  // of CTAs, one an SM
+
+// Pairs that the current device holds at once.
+int pairs_there() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return PAIRS;
+  return std::max(n / 2, 1);
 }
 
 int64_t up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
@@ -609,7 +609,6 @@ int64_t up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 // How the gradients' products share the card: which pairs of CTAs take DX and
 // into how many parts DW's sum over the rows is split, by the rounds of tiles they
 // take, counted in k blocks (a tile's start and drain as four).
-constexpr int PAIRS = 76;
 struct GradPlan {
   int dw_m, dw_n, splits, kb_per_split;  // DW's tiles and split
   int dx_bn, dx_n;                       // DX's tile columns and column tiles
@@ -695,15 +694,18 @@ gnn_status launch(int grid, int block, size_t smem, cudaStream_t st, void (*k)(P
   return GNN_OK;
 }
 
+#define GNN_TRY(expr)                 \
+  do {                                \
+    const gnn_status s_ = (expr);     \
+    if (s_ != GNN_OK) return s_;      \
+  } while (0)
+
 template <Mode M, class T, bool PAD = true>
 gnn_status launch_gated(const Args& g, cudaStream_t st) {
-  static bool ready = false;
-  if (!ready) {
-    GNN_CUDA(cudaFuncSetAttribute(gated_kernel<M, T, PAD>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(M)));
-    ready = true;
-  }
+  static PerDevice done;
+  GNN_TRY(allow_smem(gated_kernel<M, T, PAD>, smem_bytes(M), done));
   const int64_t tiles = (int64_t)g.num_m * g.num_n * (M == DW ? 2 * g.splits : 1);
-  const int pairs = (int)(tiles < sm_count() / 2 ? tiles : sm_count() / 2);
+  const int pairs = (int)std::min<int64_t>(tiles, pairs_there());
   return launch(2 * pairs, THREADS, smem_bytes(M), st, gated_kernel<M, T, PAD>, g);
 }
 
@@ -714,12 +716,6 @@ gnn_status map16(CUtensorMap* m, const void* p, int64_t rows, int64_t cols, int6
                                                           : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
                         p, (uint64_t)cols, (uint64_t)rows, (uint64_t)ld * 2, (uint32_t)box_c, (uint32_t)box_r);
 }
-
-#define GNN_TRY(expr)                 \
-  do {                                \
-    const gnn_status s_ = (expr);     \
-    if (s_ != GNN_OK) return s_;      \
-  } while (0)
 
 struct Mat {
   void* p;
@@ -796,15 +792,13 @@ gnn_status gated_bwd(int64_t n, int D, int F, int act, int dh_f32, Mat dH, Mat X
     GNN_TRY(map16<T>(&v.b[0], w.dg, n, F, w.ldf, 64, BK));
     GNN_TRY(map16<T>(&v.b[1], w.du, n, F, w.ldf, 64, BK));
   }
-  if (n > 0 && p.dx_pairs) {
-    static bool ready = false;
+  // the plan shares PAIRS pairs; on a device with fewer the products run one by one
+  if (n > 0 && p.dx_pairs && pairs_there() >= PAIRS) {
+    static PerDevice done;
     constexpr int smem = smem_bytes(DX) > smem_bytes(DW) ? smem_bytes(DX) : smem_bytes(DW);
-    if (!ready) {
-      GNN_CUDA(cudaFuncSetAttribute(gated_grads_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
-      ready = true;
-    }
+    GNN_TRY(allow_smem(gated_grads_kernel<T>, smem, done));
     const int64_t dw_tiles = 2ll * p.dw_m * p.dw_n * p.splits;
-    const int pairs = p.dx_pairs + (int)std::min<int64_t>(dw_tiles, sm_count() / 2 - p.dx_pairs);
+    const int pairs = p.dx_pairs + (int)std::min<int64_t>(dw_tiles, PAIRS - p.dx_pairs);
     GNN_TRY(launch(2 * pairs, THREADS, smem, st, gated_grads_kernel<T>, x, v, p.dx_pairs));
   } else if (n > 0) {
     if (dX.p) GNN_TRY((launch_gated<DX, T>(x, st)));

@@ -5,6 +5,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "gnnagg.h"
 
 namespace gnn {
@@ -38,6 +40,21 @@ void count_launch();
   do {                                                                              \
     if (!(cond)) return ::gnn::fail(GNN_ERR_INVALID_ARG, __VA_ARGS__);              \
   } while (0)
+
+// Lets a kernel take `bytes` of shared memory on the current device: once for each
+// device, which `done` remembers (one for each kernel; devices past its end are
+// told at every call).
+using PerDevice = std::atomic<bool>[16];
+template <class K>
+gnn_status allow_smem(K* kernel, int bytes, PerDevice& done) {
+  int dev = 0;
+  GNN_CUDA(cudaGetDevice(&dev));
+  if (dev >= 16 || !done[dev].load(std::memory_order_acquire)) {
+    GNN_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
+    if (dev < 16) done[dev].store(true, std::memory_order_release);
+  }
+  return GNN_OK;
+}
 
 // Carves 256-byte aligned pieces out of a caller workspace.  With base NULL
 // it only measures.

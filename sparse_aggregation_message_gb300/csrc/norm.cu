@@ -1069,23 +1069,17 @@ int joiners(NormArgs& a) {
   return (int)(parts * std::min<int64_t>((a.n_seg + a.join_width - 1) / a.join_width, most));
 }
 
-// Kernels whose ring may pass 48 KB of shared memory.
-template <class K>
-gnn_status allow_smem(K* k, bool& ready) {
-  if (!ready) GNN_CUDA(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024));
-  ready = true;
-  return GNN_OK;
-}
+constexpr int kSmemMost = 160 * 1024;  // of a block, its ring included
 
 template <class TX, class TY, int V, bool SMALL>
 gnn_status norm_fwd(NormArgs a, int threads, cudaStream_t st) {
-  static bool ready1 = false, ready2 = false;
+  static PerDevice stats_done, apply_done;
   const size_t ring = (size_t)2 * (FWD_DEPTH + 1) * threads * V * sizeof(TX);
   const size_t kept = (size_t)a.keep * threads * V * sizeof(TX);
   const size_t smem = sizeof(float) * (size_t)(2 * a.RP * (a.CH * V + a.CH) + 2 * a.C + 2 * a.groups) + 48 + std::max(ring, kept);
   const Launch l{st};
-  gnn_status s = allow_smem(norm_fwd_stats_kernel<TX, TY, V, SMALL>, ready1);
-  if (s == GNN_OK) s = allow_smem(norm_fwd_apply_kernel<TX, TY, V>, ready2);
+  gnn_status s = allow_smem(norm_fwd_stats_kernel<TX, TY, V, SMALL>, kSmemMost, stats_done);
+  if (s == GNN_OK) s = allow_smem(norm_fwd_apply_kernel<TX, TY, V>, kSmemMost, apply_done);
   if (s == GNN_OK && a.tiles)
     s = l.run(a.tiles, threads, smem, norm_fwd_stats_kernel<TX, TY, V, SMALL>, a);
   const int blocks = joiners(a);
@@ -1102,13 +1096,13 @@ gnn_status norm_fwd(NormArgs a, cudaStream_t st) {
 
 template <class TX, class TY, int V, bool SMALL>
 gnn_status norm_bwd(NormArgs a, int threads, cudaStream_t st) {
-  static bool ready1 = false, ready2 = false;
+  static PerDevice stats_done, apply_done;
   const size_t stream = (size_t)2 * (BWD_DEPTH + 1) * threads * V * (sizeof(TX) + sizeof(TY));
   const size_t kept = (size_t)2 * a.keep * threads * V * 4, ring = stream > kept ? stream : kept;
   const size_t smem = sizeof(float) * (size_t)(2 * a.RP * (a.CH * V + a.CH) + 4 * a.C + 2 * a.groups) + 48 + ring;
   const Launch l{st};
-  gnn_status s = allow_smem(norm_bwd_sums_kernel<TX, TY, V, SMALL>, ready1);
-  if (s == GNN_OK) s = allow_smem(norm_bwd_apply_kernel<TX, TY, V>, ready2);
+  gnn_status s = allow_smem(norm_bwd_sums_kernel<TX, TY, V, SMALL>, kSmemMost, stats_done);
+  if (s == GNN_OK) s = allow_smem(norm_bwd_apply_kernel<TX, TY, V>, kSmemMost, apply_done);
   if (s == GNN_OK && a.tiles)
     s = l.run(a.tiles, threads, smem, norm_bwd_sums_kernel<TX, TY, V, SMALL>, a);
   const int cols = a.dpart ? (2 * a.C + 7) / 8 : 0;

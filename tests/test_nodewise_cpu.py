@@ -250,3 +250,37 @@ def test_binding_refuses_a_workspace_that_is_not_on_a_gpu():
     import sparse_aggregation_message_gb300 as G
     with pytest.raises(ValueError, match="ws"):
         G._ws(torch.zeros(64, dtype=torch.uint8), 8, None, None)
+
+
+def test_binding_refuses_another_device_than_the_current_one(monkeypatch):
+    """A launch goes to the current device, whichever device its stream is taken from."""
+    torch = pytest.importorskip("torch")
+    import sparse_aggregation_message_gb300 as G
+
+    class Bits:
+        device = staticmethod(lambda: 1)
+        raw_stream = staticmethod(lambda dev: 40 + dev)
+
+    class On:
+        def __init__(self, dev):
+            self.get_device = lambda: dev
+
+    monkeypatch.setattr(G, "_bits", Bits())
+    assert G._current(On(1), None) == 41
+    with pytest.raises(ValueError, match="current device"):
+        G._current(On(0), None)
+    with pytest.raises(ValueError, match="current device"):
+        G._current(On(0), object())
+
+    class Fake:
+        dtype = torch.float32
+
+        def __init__(self, dev):
+            self.device = torch.device("cuda", dev)
+
+        numel = lambda self: 8  # noqa: E731
+
+        is_contiguous = lambda self: True  # noqa: E731
+
+    with pytest.raises(ValueError, match=r"grads\[0\]: on cuda:1"):
+        G.AdamwTensors([Fake(0)], [Fake(1)], [Fake(0)], [Fake(0)])
