@@ -220,7 +220,8 @@ __device__ __forceinline__ float max8(const float (&v)[8]) {
 // Square roots and quotients of pairs, rounded to nearest, for operands whose
 // every step below stays normal (the caller checks).  The root is Goldschmidt's
 // iteration from an approximate reciprocal root, with h -> 1/(2 sqrt v), and a
-// final residual correction; the quotient is Markstein's method (IBM J. Res.
+// final residual correction (Markstein, "Software division and square root using
+// Goldschmidt's algorithms", RNC6, 2004); the quotient is Markstein's method (IBM J. Res.
 // Dev. 34(1), 1990): the reciprocal to the last bit by one Newton step, a
 // quotient made faithful by one fused residual and rounded correctly by the
 // next.  Two operations to an instruction: the update had 70 instructions an

@@ -98,7 +98,8 @@ template <>
 __device__ __forceinline__ __half from_f32<__half>(float x) { return __float2half_rn(x); }
 
 // 2^x and 1/x in one instruction each, subnormals taken as zero: all that is
-// formed from them below is compared with one.
+// formed from them below is compared with one.  In fp32 the backward is off by
+// 2e-7 to 7e-7 of a gradient's norm with them (7e-8 to 1e-7 with full-length ones).
 __device__ __forceinline__ float ex2_f(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

@@ -12,9 +12,11 @@
 //
 // Bound by memory where segments are long: X (backward: X and dY) is read twice,
 // since a segment of a partition does not stay on the chip.  716847 x 300 fp32 to
-// bf16 in 8 segments: 344 us, 6.3 TB/s with the second read; 232965 x 602
-// backward: 376 us, 6.0 TB/s.  Many short segments (65537 x 256 in 2800, backward
-// with gelu: 79 us for 0.2 GB) are bound by what a block does once per segment.
+// bf16 in 8 segments: 330 us on the GPU, 6.5 TB/s with the second read; 232965 x
+// 602 backward: 366 us, 6.1 TB/s.  Many short segments (65537 x 256 in 2800,
+// backward with gelu: 73 us for 0.2 GB) are bound by what a block does once per
+// segment.  The backward on 2-byte rows spills (eight channels a thread, about 1 KB
+// of reloads): 716847 x 256 bf16 in 8 segments takes 316 us, 5.8 TB/s.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -966,8 +968,9 @@ __global__ void __launch_bounds__(block_threads(V), bwd_blocks(V, false)) norm_b
 //
 // Blocks are small where the segments have kShortMean rows or fewer in the mean
 // (65537 x 256, small against large blocks, forward and backward: 51, 78 against
-// 76, 81 us at 23 rows; 56, 98 against 61, 83 us at 55).  A segment of kShortRows
-// or fewer is one block's in any case.
+// 76, 81 us at 23 rows; 56, 98 against 61, 83 us at 55; one long segment behind
+// 2,000 to 20,000 of one row each, whose mean is below kShortMean too: 139 to 144
+// against 282 to 339).  A segment of kShortRows or fewer is one block's in any case.
 constexpr int kShortRows = 256, kShortMean = 40;
 
 int tile_rows(int64_t n, int RP, bool backward, bool small) {
