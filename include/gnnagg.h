@@ -713,6 +713,58 @@ gnn_status gnn_gated_bwd(const void* dH, int64_t lddh, int32_t dh_type, const vo
                          void* dX, int64_t lddx, void* dWg, int64_t lddwg, void* dWu,
                          int64_t lddwu, void* ws, size_t ws_bytes, gnn_stream_t stream);
 
+/* The residual sum between two blocks, with the norms around it, by rows:
+ *   H = R + s act(G) z,   z = w_post norm_post(B) + b_post,
+ *   Y = w_pre norm_pre(H) + b_pre,
+ * B the block's output (the branch), R the stream it is added to, Y the next
+ * block's operand, formed from H before H is rounded.  norm of a row x:
+ * GNN_NORM_RMS x / sqrt(mean x^2 + eps), GNN_NORM_LAYER
+ * (x - mean x) / sqrt(mean (x - mean x)^2 + eps), GNN_NORM_NONE x itself
+ * (pre: there is no Y).  G: values of the gate before its activation, of B's
+ * type; gate_cols C: a matrix, 1: one a row (ldg apart; dgate lddg), 0: none
+ * (factor 1).  s: fp32, scale_cols values, C, 1 or 0 (factor 1).  w_*, b_*: fp32
+ * [C] or NULL (1, 0).  B may be NULL (no post norm, gate or scale then): H = R,
+ * and H may be NULL too.  stats (fp32 [n][4] on a 16-byte border: mean and
+ * 1/deviation of B's row, then of H's, 0 and 1 without a norm; NULL when no
+ * backward follows).  Sums are held in fp32, variances taken about the mean.
+ * Types (b_type, r_type, y_type): one 2-byte type or GNN_F32 throughout, a
+ * 2-byte type with an fp32 stream, or fp32 with Y in 2 bytes.  C <= 4096.  H
+ * may be R (one stride). */
+#define GNN_NORM_NONE 0
+#define GNN_NORM_RMS 1
+#define GNN_NORM_LAYER 2
+gnn_status gnn_residual_norm_fwd(const void* B, int64_t ldb, int32_t b_type, const void* R,
+                                 int64_t ldr, int32_t r_type, const void* gate, int64_t ldg,
+                                 int32_t gate_cols, int32_t gate_act, int64_t n, int32_t C,
+                                 int32_t post, const float* w_post, const float* b_post,
+                                 const float* scale, int32_t scale_cols, int32_t pre,
+                                 const float* w_pre, const float* b_pre, double eps, void* H,
+                                 int64_t ldh, void* Y, int64_t ldy, int32_t y_type, float* stats,
+                                 gnn_stream_t stream);
+/* Backward from dH (gradient of H from elsewhere, r_type) and dY (y_type); one
+ * of them may be NULL (zero).  B, H (read where there is a dY), gate, weights
+ * and stats as the forward left them.  With D the whole gradient at H, yh and bh
+ * the normalised rows, q = w_pre dY and means over a row:
+ *   D = dH + rstd_H (q - [layer] mean q - yh mean(q yh)),   dR = D,
+ *   v = D act(G) s w_post,
+ *   dB = rstd_B (v - [layer] mean v - bh mean(v bh))   (post none: v),
+ *   dgate = D s z act'(G) (summed over the row where gate_cols is 1),
+ * and summed over all rows: dw_pre = dY yh, db_pre = dY, dw_post = D act(G) s bh,
+ * db_post = D act(G) s, dscale = D act(G) z (over the row too where scale_cols
+ * is 1).  Any output may be NULL.  Sums over rows are added in a fixed order
+ * (deterministic).  dR may be dH (one stride). */
+gnn_status gnn_residual_norm_workspace(int64_t n, int32_t C, size_t* bwd_bytes);
+gnn_status gnn_residual_norm_bwd(const void* dH, int64_t lddh, const void* dY, int64_t lddy,
+                                 int32_t y_type, const void* B, int64_t ldb, int32_t b_type,
+                                 const void* H, int64_t ldh, int32_t r_type, const void* gate,
+                                 int64_t ldg, int32_t gate_cols, int32_t gate_act, int64_t n,
+                                 int32_t C, int32_t post, const float* w_post,
+                                 const float* b_post, const float* scale, int32_t scale_cols,
+                                 int32_t pre, const float* w_pre, const float* stats, void* dR,
+                                 int64_t lddr, void* dB, int64_t lddb, void* dgate, int64_t lddg,
+                                 float* dw_post, float* db_post, float* dscale, float* dw_pre,
+                                 float* db_pre, void* ws, size_t ws_bytes, gnn_stream_t stream);
+
 /* One AdamW step over many tensors.  The descriptors are a host array (they
  * go to the kernels as launch parameters, so they may change from call to
  * call and a call can be captured into a graph); what they point at is device

@@ -31,6 +31,7 @@ __all__ = [
     "gnn_spmm_bwd_masked", "gnn_spmm_bwd_local_masked", "gnn_dense_bwd_z", "ldz_for",
     "gnn_group_norm_workspace", "gnn_group_norm_fwd", "gnn_group_norm_bwd",
     "gnn_gated_workspace", "gnn_gated_fwd", "gnn_gated_bwd",
+    "gnn_residual_norm_workspace", "gnn_residual_norm_fwd", "gnn_residual_norm_bwd",
     "AdamwTensors", "adamw_state", "gnn_adamw_workspace", "gnn_adamw_step",
     "Blocked", "gnn_blocked_build", "gnn_spmm_fwd_blocked", "gnn_spmm_bwd_blocked",
 ]
@@ -922,6 +923,105 @@ def gnn_gated_bwd(dH, X, n: int, F_in: int, Wg, Wu, F_mid: int, dX=None, dWg=Non
          _ptr(dWg), _rows(dWg, F_in, F_mid, "dWg") if dWg is not None else 0,
          _ptr(dWu), _rows(dWu, F_in, F_mid, "dWu") if dWu is not None else 0,
          at, size, _current(X, stream))
+
+
+NORMS = {"none": 0, "rms": 1, "layer": 2}
+
+
+def _norm(kind: str, what: str) -> int:
+    k = NORMS.get(kind)
+    if k is None:
+        raise ValueError(f"{what}: one of {sorted(NORMS)}, got {kind!r}")
+    return k
+
+
+def _gate(gate, n: int, C: int, what: str):
+    """(pointer, stride, columns) of a gate: a matrix, or one value a row."""
+    if gate is None:
+        return None, 0, 0
+    if gate.dim() == 1:
+        if gate.numel() < n or not gate.is_cuda:
+            raise ValueError(f"{what}: needs a CUDA tensor of {n} values or a matrix")
+        return gate.data_ptr(), gate.stride(0), 1
+    return gate.data_ptr(), _rows(gate, n, C, what), C
+
+
+def _scale(scale, C: int):
+    if scale is None:
+        return None, 0
+    k = scale.numel()
+    if k != 1 and k != C:
+        raise ValueError(f"scale: needs 1 or {C} values, got {k}")
+    return _f32(scale, k, "scale"), k
+
+
+def _types(what, t, *others):
+    for name, o in others:
+        if o is not None and o.dtype is not t.dtype:
+            raise ValueError(f"{name}: needs {what}'s type {t.dtype}, got {o.dtype}")
+
+
+def _place(t, n: int, C: int, what: str):
+    return (None, 0) if t is None else (t.data_ptr(), _rows(t, n, C, what))
+
+
+@functools.lru_cache(maxsize=1024)
+def gnn_residual_norm_workspace(n: int, C: int) -> int:
+    """Workspace bytes of gnn_residual_norm_bwd."""
+    nb = ctypes.c_size_t()
+    call("gnn_residual_norm_workspace", n, C, ctypes.byref(nb))
+    return nb.value
+
+
+def gnn_residual_norm_fwd(B, R, n: int, C: int, H, Y=None, stats=None, gate=None, gate_act: str = "sigmoid",
+                          post: str = "rms", w_post=None, b_post=None, scale=None, pre: str = "rms", w_pre=None,
+                          b_pre=None, eps: float = 1e-6, stream=None) -> None:
+    """H = R + scale act(gate) (w_post norm(B) + b_post) and Y = w_pre norm(H) +
+    b_pre by rows (norms "none", "rms", "layer").  gate: [n, C] or one value a
+    row [n], of B's type; scale: fp32, C values or one; stats (fp32 [n, 4]) is
+    kept for the backward.  B None: H = R (H may be None), Y is R's norm."""
+    _types("B", R if B is None else B, ("gate", gate))
+    _types("R", R, ("H", H))
+    at_b, ldb = _place(B, n, C, "B")
+    at_g, ldg, gate_cols = _gate(gate, n, C, "gate")
+    at_s, scale_cols = _scale(scale, C)
+    at_h, ldh = _place(H, n, C, "H")
+    at_y, ldy = _place(Y, n, C, "Y")
+    bt = _type(B) if B is not None else _type(R) if Y is None or R.dtype is Y.dtype else 0
+    call("gnn_residual_norm_fwd", at_b, ldb, bt, R.data_ptr(), _rows(R, n, C, "R"), _type(R), at_g, ldg, gate_cols,
+         _act(gate_act), n, C, _norm(post, "post") if B is not None else 0, _f32(w_post, C, "w_post"),
+         _f32(b_post, C, "b_post"), at_s, scale_cols, _norm(pre, "pre"), _f32(w_pre, C, "w_pre"), _f32(b_pre, C, "b_pre"),
+         eps, at_h, ldh, at_y, ldy, bt if Y is None else _type(Y), _f32(stats, 4 * n, "stats"), _current(R, stream))
+
+
+def gnn_residual_norm_bwd(dH, dY, B, H, n: int, C: int, stats, dR=None, dB=None, gate=None, dgate=None,
+                          gate_act: str = "sigmoid", post: str = "rms", w_post=None, b_post=None, scale=None,
+                          pre: str = "rms", w_pre=None, dw_post=None, db_post=None, dscale=None, dw_pre=None,
+                          db_pre=None, ws=None, stream=None) -> None:
+    """Gradients of gnn_residual_norm_fwd from dH and dY (one may be None), with
+    B, H, gate, weights and stats as they were there; each output may be None."""
+    S = H if H is not None else dH
+    _types("B", S if B is None else B, ("gate", gate), ("dgate", dgate), ("dB", dB))
+    _types("H", S, ("dH", dH), ("dR", dR))
+    at_dh, lddh = _place(dH, n, C, "dH")
+    at_dy, lddy = _place(dY, n, C, "dY")
+    at_b, ldb = _place(B, n, C, "B")
+    at_h, ldh = _place(H, n, C, "H")
+    at_dr, lddr = _place(dR, n, C, "dR")
+    at_db, lddb = _place(dB, n, C, "dB")
+    at_g, ldg, gate_cols = _gate(gate, n, C, "gate")
+    at_dg, lddg, dgate_cols = _gate(dgate, n, C, "dgate")
+    if dgate is not None and dgate_cols != gate_cols:
+        raise ValueError("dgate: needs the gate's shape")
+    at_s, scale_cols = _scale(scale, C)
+    bt = _type(B) if B is not None else _type(S) if dY is None or S.dtype is dY.dtype else 0
+    at, size, ws = _ws(ws, gnn_residual_norm_workspace(n, C), S, stream)
+    call("gnn_residual_norm_bwd", at_dh, lddh, at_dy, lddy, bt if dY is None else _type(dY), at_b, ldb, bt, at_h, ldh,
+         _type(S), at_g, ldg, gate_cols, _act(gate_act), n, C, _norm(post, "post") if B is not None else 0,
+         _f32(w_post, C, "w_post"), _f32(b_post, C, "b_post"), at_s, scale_cols, _norm(pre, "pre"),
+         _f32(w_pre, C, "w_pre"), _f32(stats, 4 * n, "stats"), at_dr, lddr, at_db, lddb, at_dg, lddg,
+         _f32(dw_post, C, "dw_post"), _f32(db_post, C, "db_post"), _f32(dscale, scale_cols, "dscale"),
+         _f32(dw_pre, C, "dw_pre"), _f32(db_pre, C, "db_pre"), at, size, _current(S, stream))
 
 
 class AdamwTensors:

@@ -165,6 +165,14 @@ PROTOTYPES = {
     "gnn_gated_bwd": (ctypes.c_int, [c_vp, c_i64, c_i32, c_vp, c_i64, c_i32, c_i64, c_i32, c_vp, c_i64, c_vp,
                                      c_i64, c_i32, c_i32, c_vp, c_i64, c_vp, c_i64, c_vp, c_i64, c_vp,
                                      c_size, c_vp]),
+    "gnn_residual_norm_workspace": (ctypes.c_int, [c_i64, c_i32, P_size]),
+    "gnn_residual_norm_fwd": (ctypes.c_int, [c_vp, c_i64, c_i32, c_vp, c_i64, c_i32, c_vp, c_i64, c_i32, c_i32,
+                                             c_i64, c_i32, c_i32, c_vp, c_vp, c_vp, c_i32, c_i32, c_vp, c_vp,
+                                             ctypes.c_double, c_vp, c_i64, c_vp, c_i64, c_i32, c_vp, c_vp]),
+    "gnn_residual_norm_bwd": (ctypes.c_int, [c_vp, c_i64, c_vp, c_i64, c_i32, c_vp, c_i64, c_i32, c_vp, c_i64,
+                                             c_i32, c_vp, c_i64, c_i32, c_i32, c_i64, c_i32, c_i32, c_vp, c_vp,
+                                             c_vp, c_i32, c_i32, c_vp, c_vp, c_vp, c_i64, c_vp, c_i64, c_vp,
+                                             c_i64, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_size, c_vp]),
     "gnn_adamw_workspace": (ctypes.c_int, [P_size]),
     "gnn_adamw_step": (ctypes.c_int, [ctypes.POINTER(GnnAdamwTensor), c_i32, c_i32, c_i32, c_i32, c_vp,
                                       ctypes.c_double, ctypes.c_double, ctypes.c_double, ctypes.c_double,

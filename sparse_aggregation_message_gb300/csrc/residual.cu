@@ -1,0 +1,862 @@
+// The residual sum between two blocks, with the norms around it:
+//   H = R + s act(G) z,  z = w_post norm_post(B) + b_post
+//   Y = w_pre norm_pre(H) + b_pre
+// and its backward, row by row.  Every matrix is read once and written once; what
+// bounds both passes is DRAM.
+//
+// A row belongs to a group of L lanes with eight channels each in registers, so that
+// a row's statistics, its sum and the second norm need one read: 4 to 32 lanes
+// (several rows to a warp when rows are short), or several warps that add through
+// shared memory.  The rows ahead arrive in a ring in shared memory by asynchronous
+// copies; each lane copies and reads its own pieces, so the ring has no barriers.
+#include <cuda_runtime.h>
+#include <math.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "internal.h"
+#include "nodewise.cuh"
+
+namespace gnn {
+
+namespace {
+
+constexpr int THREADS = 256;  // of a block; rows of more than 256 lanes: one row's
+constexpr int MAX_LANES = 512;
+constexpr int MAX_C = 8 * MAX_LANES;
+
+struct Args {
+  const void *B, *R, *G;  // branch, stream, gate
+  const void *dH, *dY;
+  void *H, *Y;            // forward: outputs; backward: H is read
+  void *dR, *dB, *dG;
+  int64_t ldb, ldr, ldg, ldh, ldy, lddh, lddr, lddb, lddg;
+  int64_t n;
+  int C, lanes;
+  int gate;               // 0: none, 1: one value a row, 2: a matrix
+  int act, post, pre;
+  const float *w_post, *b_post, *scale, *w_pre, *b_pre;
+  int scale_cols;         // 0, 1 or C
+  float eps, inv_c;
+  float4* stats;
+  float* part;            // backward: [blocks][4][8 lanes]
+  int want_q, want_p;     // backward: which sums over all rows are kept
+  // the ring: stages, 16-byte pieces of a lane in one, and where each matrix's begin
+  int stages, pieces, at[5];
+};
+
+// ------------------------------------------------------- eight channels a lane
+using Eight = float2[4];
+
+__device__ __forceinline__ void mask(Eight& x, int cnt) {
+  if (cnt < 8) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = make_float2(2 * i < cnt ? x[i].x : 0.f, 2 * i + 1 < cnt ? x[i].y : 0.f);
+  }
+}
+
+__device__ __forceinline__ void copy16(uint4* dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src),
+               "r"(there ? 16 : 0)
+               : "memory");
+}
+
+// A lane's pieces of one stage of the ring, `threads` apart.
+template <class T>
+__device__ __forceinline__ void fetch(uint4* to, int threads, const void* base, int64_t at, int cnt) {
+  const T* p = static_cast<const T*>(base) + (cnt > 0 ? at : 0);
+  copy16(to, p, cnt > 0);
+  if constexpr (std::is_same<T, float>::value) copy16(to + threads, cnt > 4 ? p + 4 : p, cnt > 4);
+}
+// Channels past the row's last are zero.
+template <class T>
+__device__ __forceinline__ void take(const uint4* from, int threads, int cnt, Eight& x) {
+  const uint4 a = *from;
+  if constexpr (std::is_same<T, float>::value) {
+    const uint4 b = from[threads];
+    x[0] = make_float2(__uint_as_float(a.x), __uint_as_float(a.y)), x[1] = make_float2(__uint_as_float(a.z), __uint_as_float(a.w));
+    x[2] = make_float2(__uint_as_float(b.x), __uint_as_float(b.y)), x[3] = make_float2(__uint_as_float(b.z), __uint_as_float(b.w));
+  } else {
+    x[0] = Pack2<T>::from(a.x), x[1] = Pack2<T>::from(a.y), x[2] = Pack2<T>::from(a.z), x[3] = Pack2<T>::from(a.w);
+  }
+  mask(x, cnt);
+}
+
+// Writes the lane's channels and the zeros that pad a row (to a multiple of 16
+// channels in a 2-byte type, of 4 in fp32).  `cnt`: channels from here on; odd: the
+// second of two lanes that share 16 channels.
+template <class T>
+__device__ __forceinline__ void put(void* base, int64_t at, Eight& x, int cnt, bool odd) {
+  if (cnt <= (odd ? -8 : 0)) return;
+  T* p = static_cast<T*>(base) + at;
+  mask(x, cnt);
+  if constexpr (std::is_same<T, float>::value) {
+    if (cnt > 0) *reinterpret_cast<float4*>(p) = make_float4(x[0].x, x[0].y, x[1].x, x[1].y);
+    if (cnt > 4) *reinterpret_cast<float4*>(p + 4) = make_float4(x[2].x, x[2].y, x[3].x, x[3].y);
+  } else {
+    *reinterpret_cast<uint4*>(p) = make_uint4(Pack2<T>::to(x[0].x, x[0].y), Pack2<T>::to(x[1].x, x[1].y),
+                                              Pack2<T>::to(x[2].x, x[2].y), Pack2<T>::to(x[3].x, x[3].y));
+  }
+}
+
+// Eight of a vector of weights, `none` where there is no vector; zero past its end.
+__device__ __forceinline__ void weights(const float* p, int c, int cnt, float none, Eight& w) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    w[i].x = 2 * i < cnt ? (p ? __ldg(p + c + 2 * i) : none) : 0.f;
+    w[i].y = 2 * i + 1 < cnt ? (p ? __ldg(p + c + 2 * i + 1) : none) : 0.f;
+  }
+}
+
+// 1 / sqrt(x) by one Newton step on the approximate root.
+__device__ __forceinline__ float inv_root(float x) {
+  const float y = rsqrtf(x);
+  return x < 1e37f && x > 1e-37f ? fmaf(0.5f * y, fmaf(-x * y, y, 1.f), y) : y;
+}
+
+__device__ __forceinline__ float add_up(const Eight& x) {
+  const float2 s = add2_rn(add2_rn(x[0], x[1]), add2_rn(x[2], x[3]));
+  return s.x + s.y;
+}
+__device__ __forceinline__ float dot(const Eight& x, const Eight& y) {
+  float2 s = mul2_rn(x[0], y[0]);
+#pragma unroll
+  for (int i = 1; i < 4; ++i) s = fma2_rn(x[i], y[i], s);
+  return s.x + s.y;
+}
+
+// Sums over the lanes of a row, the same bits in each of them.
+template <bool MULTI>
+struct Row {
+  int lanes, lane, group;
+  float* buf;  // MULTI: two turns of 4 values for each warp of the block
+  int turn;
+  __device__ Row(int lanes_, float* sm) : lanes(lanes_), buf(sm), turn(0) {
+    group = threadIdx.x / lanes;
+    lane = threadIdx.x - group * lanes;
+  }
+  template <int N>
+  __device__ __forceinline__ void sum(float (&v)[N]) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+      if (MULTI || o < lanes) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+      }
+    }
+    if (MULTI) {
+      const int warps = lanes >> 5;
+      float* mine = buf + (turn * (MAX_LANES / 32) + group * warps) * 4;
+      if ((threadIdx.x & 31) == 0) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) mine[(lane >> 5) * 4 + i] = v[i];
+      }
+      // a row's warps only; a warp that writes a turn again has passed the other
+      // turn's barrier, which every reader of this turn has reached
+      asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(lanes) : "memory");
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = 0.f;
+      for (int w = 0; w < warps; ++w) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] += mine[w * 4 + i];
+      }
+      turn ^= 1;
+    }
+  }
+};
+
+// Mean and 1/deviation of a row; the variance about the mean.
+template <bool MULTI>
+__device__ __forceinline__ void statistics(const Eight& x, int cnt, int kind, float eps, float inv_c, Row<MULTI>& row,
+                                           float& mean, float& rstd) {
+  mean = 0.f, rstd = 1.f;
+  if (kind == GNN_NORM_NONE) return;
+  float s[1];
+  if (kind == GNN_NORM_LAYER) {
+    s[0] = add_up(x);
+    row.sum(s);
+    mean = s[0] * inv_c;
+    Eight d;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) d[i] = add2_rn(x[i], dup2(-mean));
+    mask(d, cnt);
+    s[0] = dot(d, d);
+  } else {
+    s[0] = dot(x, x);
+  }
+  row.sum(s);
+  rstd = inv_root(fmaf(s[0], inv_c, eps));
+}
+
+// (x - mean) rstd, zero past the row's end.
+__device__ __forceinline__ void normalise(Eight& x, int cnt, float mean, float rstd) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[i] = mul2_rn(add2_rn(x[i], dup2(-mean)), dup2(rstd));
+  mask(x, cnt);
+}
+
+template <int N>
+__device__ __forceinline__ void wait_copies() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+// All but the newest stages - 1 rows have arrived.
+__device__ __forceinline__ void wait_row(int stages) {
+  if (stages == 4)
+    wait_copies<3>();
+  else if (stages == 3)
+    wait_copies<2>();
+  else
+    wait_copies<1>();
+}
+
+template <class TB, class TR, class TY, bool MULTI>
+__global__ void __launch_bounds__(MULTI ? MAX_LANES : THREADS) residual_fwd_kernel(const __grid_constant__ Args g) {
+  extern __shared__ uint4 ring[];
+  __shared__ float sm[MULTI ? 2 * 4 * (MAX_LANES / 32) : 1];
+  cudaTriggerProgrammaticLaunchCompletion();
+  cudaGridDependencySynchronize();
+  Row<MULTI> row(g.lanes, sm);
+  const int threads = blockDim.x, groups = threads / g.lanes;
+  const int64_t step = (int64_t)gridDim.x * groups;
+  // the warp's first row: its groups leave the loop together
+  const int ahead = MULTI ? 0 : row.group & (32 / g.lanes - 1);
+  const int c = 8 * row.lane, cnt = g.C - c;
+  const bool odd = row.lane & 1;
+  Eight w1, b1, w2, b2;  // s w_post, s b_post, w_pre, b_pre
+  {
+    Eight s;
+    weights(g.w_post, c, cnt, 1.f, w1);
+    weights(g.b_post, c, cnt, 0.f, b1);
+    if (g.scale_cols == 1) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[i] = dup2(__ldg(g.scale));
+    } else {
+      weights(g.scale, c, cnt, 1.f, s);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w1[i] = mul2_rn(w1[i], s[i]), b1[i] = mul2_rn(b1[i], s[i]);
+    weights(g.w_pre, c, cnt, 1.f, w2);
+    weights(g.b_pre, c, cnt, 0.f, b2);
+  }
+  uint4* mine = ring + threadIdx.x;
+  const int stage_size = g.pieces * threads;
+  auto request = [&](int st, int64_t i) {
+    uint4* to = mine + st * stage_size;
+    const int m = i < g.n ? cnt : 0;
+    fetch<TR>(to + g.at[0] * threads, threads, g.R, i * g.ldr + c, m);
+    if (g.B) fetch<TB>(to + g.at[1] * threads, threads, g.B, i * g.ldb + c, m);
+    if (g.gate == 2) fetch<TB>(to + g.at[2] * threads, threads, g.G, i * g.ldg + c, m);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  auto row_gate = [&](int64_t i) { return g.gate == 1 && i < g.n ? to_f32(static_cast<const TB*>(g.G)[i * g.ldg]) : 0.f; };
+  int64_t i = (int64_t)blockIdx.x * groups + row.group;
+  for (int k = 0; k < g.stages - 1; ++k) request(k, i + k * step);
+  float t_next = row_gate(i);
+  int st = 0, into = g.stages - 1;
+  for (; i - ahead < g.n; i += step) {
+    request(into, i + (g.stages - 1) * step);
+    const float t_row = t_next;
+    t_next = row_gate(i + step);
+    wait_row(g.stages);
+    const bool live = i < g.n;
+    const uint4* from = mine + st * stage_size;
+    if (++st == g.stages) st = 0;
+    if (++into == g.stages) into = 0;
+    float4 stat = make_float4(0.f, 1.f, 0.f, 1.f);
+    Eight h;
+    take<TR>(from + g.at[0] * threads, threads, cnt, h);
+    if (g.B) {
+      Eight x, t;
+      take<TB>(from + g.at[1] * threads, threads, cnt, x);
+      statistics(x, cnt, g.post, g.eps, g.inv_c, row, stat.x, stat.y);
+      if (g.gate == 2) {
+        take<TB>(from + g.at[2] * threads, threads, cnt, t);
+        with_act(g.act, [&](auto A) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) t[j] = act2(t[j], A);
+        });
+      } else {
+        const float t1 = g.gate == 1 ? act_f(t_row, g.act) : 1.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) t[j] = dup2(t1);
+      }
+      normalise(x, cnt, stat.x, stat.y);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) h[j] = fma2_rn(t[j], fma2_rn(w1[j], x[j], b1[j]), h[j]);
+      mask(h, cnt);
+    }
+    if (g.H && live) put<TR>(g.H, i * g.ldh + c, h, cnt, odd);
+    if (g.pre != GNN_NORM_NONE) {
+      statistics(h, cnt, g.pre, g.eps, g.inv_c, row, stat.z, stat.w);
+      normalise(h, cnt, stat.z, stat.w);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) h[j] = fma2_rn(w2[j], h[j], b2[j]);
+      if (live) put<TY>(g.Y, i * g.ldy + c, h, cnt, odd);
+    }
+    if (g.stats && live && row.lane == 0) g.stats[i] = stat;
+  }
+}
+
+template <class TB, class TR, class TY, bool MULTI>
+__global__ void __launch_bounds__(MULTI ? MAX_LANES : THREADS, MULTI ? 1 : 2)
+    residual_bwd_kernel(const __grid_constant__ Args g) {
+  extern __shared__ uint4 ring[];
+  __shared__ float sm[MULTI ? 2 * 4 * (MAX_LANES / 32) : 1];
+  cudaTriggerProgrammaticLaunchCompletion();
+  cudaGridDependencySynchronize();
+  Row<MULTI> row(g.lanes, sm);
+  const int threads = blockDim.x, groups = threads / g.lanes;
+  const int64_t step = (int64_t)gridDim.x * groups;
+  const int ahead = MULTI ? 0 : row.group & (32 / g.lanes - 1);
+  const int c = 8 * row.lane, cnt = g.C - c;
+  const bool odd = row.lane & 1;
+  Eight w1, b1, w2;  // s w_post, s b_post, w_pre
+  {
+    Eight s;
+    weights(g.w_post, c, cnt, 1.f, w1);
+    weights(g.b_post, c, cnt, 0.f, b1);
+    if (g.scale_cols == 1) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[i] = dup2(__ldg(g.scale));
+    } else {
+      weights(g.scale, c, cnt, 1.f, s);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w1[i] = mul2_rn(w1[i], s[i]), b1[i] = mul2_rn(b1[i], s[i]);
+    weights(g.w_pre, c, cnt, 1.f, w2);
+  }
+  Eight acc[4];  // sums of dY yh, dY, D t bh, D t
+#pragma unroll
+  for (int a = 0; a < 4; ++a)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[a][j] = dup2(0.f);
+  uint4* mine = ring + threadIdx.x;
+  const int stage_size = g.pieces * threads;
+  auto request = [&](int st, int64_t i) {
+    uint4* to = mine + st * stage_size;
+    const int m = i < g.n ? cnt : 0;
+    if (g.dY) {
+      fetch<TY>(to + g.at[0] * threads, threads, g.dY, i * g.ldy + c, m);
+      fetch<TR>(to + g.at[1] * threads, threads, g.H, i * g.ldh + c, m);
+    }
+    if (g.dH) fetch<TR>(to + g.at[2] * threads, threads, g.dH, i * g.lddh + c, m);
+    if (g.B) fetch<TB>(to + g.at[3] * threads, threads, g.B, i * g.ldb + c, m);
+    if (g.gate == 2) fetch<TB>(to + g.at[4] * threads, threads, g.G, i * g.ldg + c, m);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  auto row_gate = [&](int64_t i) { return g.gate == 1 && i < g.n ? to_f32(static_cast<const TB*>(g.G)[i * g.ldg]) : 0.f; };
+  auto row_stats = [&](int64_t i) { return i < g.n ? __ldg(g.stats + i) : make_float4(0.f, 0.f, 0.f, 0.f); };
+  int64_t i = (int64_t)blockIdx.x * groups + row.group;
+  for (int k = 0; k < g.stages - 1; ++k) request(k, i + k * step);
+  float t_next = row_gate(i);
+  float4 s_next = row_stats(i);
+  int st = 0, into = g.stages - 1;
+  for (; i - ahead < g.n; i += step) {
+    request(into, i + (g.stages - 1) * step);
+    const float t_row = t_next;
+    const float4 stat = s_next;
+    t_next = row_gate(i + step), s_next = row_stats(i + step);
+    wait_row(g.stages);
+    const bool live = i < g.n;
+    const uint4* from = mine + st * stage_size;
+    if (++st == g.stages) st = 0;
+    if (++into == g.stages) into = 0;
+    Eight d;
+    if (g.dH) {
+      take<TR>(from + g.at[2] * threads, threads, cnt, d);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) d[j] = dup2(0.f);
+    }
+    if (g.dY) {
+      // q = w dY; D = dH + rstd (q - mean q - yh mean(q yh))
+      Eight q, yh;
+      take<TY>(from + g.at[0] * threads, threads, cnt, q);
+      take<TR>(from + g.at[1] * threads, threads, cnt, yh);
+      normalise(yh, cnt, stat.z, stat.w);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        acc[0][j] = fma2_rn(q[j], yh[j], acc[0][j]);
+        acc[1][j] = add2_rn(q[j], acc[1][j]);
+        q[j] = mul2_rn(q[j], w2[j]);
+      }
+      float s[2] = {dot(q, yh), add_up(q)};
+      if (g.pre == GNN_NORM_LAYER) {
+        row.sum(s);
+      } else {
+        float one[1] = {s[0]};
+        row.sum(one);
+        s[0] = one[0], s[1] = 0.f;
+      }
+      const float2 along = dup2(-s[0] * g.inv_c), mean = dup2(-s[1] * g.inv_c), r = dup2(stat.w);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) d[j] = fma2_rn(r, fma2_rn(yh[j], along, add2_rn(q[j], mean)), d[j]);
+      mask(d, cnt);
+    }
+    if (g.dR && live) put<TR>(g.dR, i * g.lddr + c, d, cnt, odd);
+    if (g.B) {
+      Eight bh, v;
+      take<TB>(from + g.at[3] * threads, threads, cnt, bh);
+      normalise(bh, cnt, stat.x, stat.y);
+      float s[3];
+      float slope1 = 0.f;
+      if (g.gate == 2) {
+        Eight t, slope;
+        take<TB>(from + g.at[4] * threads, threads, cnt, t);
+        with_act(g.act, [&](auto A) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 z = t[j];
+            act_grad2(z, A, t[j], slope[j]);
+          }
+        });
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          slope[j] = mul2_rn(slope[j], mul2_rn(d[j], fma2_rn(w1[j], bh[j], b1[j])));
+          d[j] = mul2_rn(d[j], t[j]);
+        }
+        if (g.dG && live) put<TB>(g.dG, i * g.lddg + c, slope, cnt, odd);
+      } else if (g.gate == 1) {
+        float2 a, b;
+        act_grad2(dup2(t_row), g.act, a, b);
+        slope1 = b.x;
+        float2 z = dup2(0.f);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          z = fma2_rn(d[j], fma2_rn(w1[j], bh[j], b1[j]), z);
+          d[j] = mul2_rn(d[j], a);
+        }
+        s[2] = z.x + z.y;
+      }
+      // d: D t from here on
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        acc[2][j] = fma2_rn(d[j], bh[j], acc[2][j]);
+        acc[3][j] = add2_rn(d[j], acc[3][j]);
+        v[j] = mul2_rn(d[j], w1[j]);
+      }
+      const bool norm = g.post != GNN_NORM_NONE;
+      s[0] = dot(v, bh), s[1] = add_up(v);
+      if (g.gate == 1) {
+        row.sum(s);
+        if (g.dG && live && row.lane == 0) static_cast<TB*>(g.dG)[i * g.lddg] = from_f32<TB>(s[2] * slope1);
+      } else if (norm) {
+        float two[2] = {s[0], s[1]};
+        row.sum(two);
+        s[0] = two[0], s[1] = two[1];
+      }
+      if (g.dB && live) {
+        if (norm) {
+          const float2 along = dup2(-s[0] * g.inv_c), mean = dup2(g.post == GNN_NORM_LAYER ? -s[1] * g.inv_c : 0.f),
+                       r = dup2(stat.y);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v[j] = mul2_rn(r, fma2_rn(bh[j], along, add2_rn(v[j], mean)));
+        }
+        put<TB>(g.dB, i * g.lddb + c, v, cnt, odd);
+      }
+    }
+  }
+  if (!g.want_q && !g.want_p) return;
+  // over the groups of a warp, then over the block's warps or groups in order, in
+  // the ring's memory (every copy has landed: the last rows' are waited for)
+  wait_copies<0>();
+  if (!MULTI) {
+    for (int o = g.lanes; o < 32; o <<= 1) {
+#pragma unroll
+      for (int a = 0; a < 4; ++a)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          acc[a][j] = add2_rn(acc[a][j], make_float2(__shfl_xor_sync(0xffffffffu, acc[a][j].x, o),
+                                                     __shfl_xor_sync(0xffffffffu, acc[a][j].y, o)));
+    }
+  }
+  __syncthreads();
+  // [turns][4][lanes][8]: every warp's (or group's) sums, then each column by one thread
+  const int turns = MULTI ? groups : threads / 32, turn = MULTI ? row.group : threadIdx.x >> 5;
+  const int width = 8 * g.lanes;
+  float* all = reinterpret_cast<float*>(ring);
+  if (MULTI || (threadIdx.x & 31) < g.lanes) {
+#pragma unroll
+    for (int a = 0; a < 4; ++a) {
+      float4* to = reinterpret_cast<float4*>(all + ((int64_t)turn * 4 + a) * width + c);
+      to[0] = make_float4(acc[a][0].x, acc[a][0].y, acc[a][1].x, acc[a][1].y);
+      to[1] = make_float4(acc[a][2].x, acc[a][2].y, acc[a][3].x, acc[a][3].y);
+    }
+  }
+  __syncthreads();
+  float* out = g.part + (int64_t)blockIdx.x * 4 * width;
+  for (int at = threadIdx.x; at < 4 * width; at += threads) {
+    float s = all[at];
+    for (int k = 1; k < turns; ++k) s += all[k * 4 * width + at];
+    out[at] = s;
+  }
+}
+
+// The blocks' sums, in order and in fp64, and the weights' gradients from them.
+// A block takes 32 channels; scalar[] (one learned scale): its share of dscale.
+constexpr int JOIN_ROWS = 32;
+struct Join {
+  const float* part;
+  int blocks, width, C, scale_cols;
+  const float *w_post, *b_post, *scale;
+  float *dw_post, *db_post, *dscale, *dw_pre, *db_pre;
+  double* scalar;
+  int want_q, want_p;
+};
+__global__ void __launch_bounds__(32 * JOIN_ROWS) residual_join_kernel(const Join g) {
+  __shared__ double sm[4][JOIN_ROWS][32];
+  cudaTriggerProgrammaticLaunchCompletion();
+  cudaGridDependencySynchronize();
+  const int lane = threadIdx.x & 31, r = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
+  double s[4] = {0, 0, 0, 0};
+  if (c < g.C) {
+#pragma unroll 4
+    for (int b = r; b < g.blocks; b += JOIN_ROWS) {
+      const float* p = g.part + (int64_t)b * 4 * g.width + c;
+      if (g.want_q) s[0] += p[0], s[1] += p[g.width];
+      if (g.want_p) s[2] += p[2 * g.width], s[3] += p[3 * g.width];
+    }
+  }
+#pragma unroll
+  for (int a = 0; a < 4; ++a) sm[a][r][lane] = s[a];
+  __syncthreads();
+  // one warp for each of the four sums, then the first has them all
+  if (r < 4) {
+    double t = 0;
+    for (int i = 0; i < JOIN_ROWS; ++i) t += sm[r][i][lane];
+    sm[r][0][lane] = t;
+  }
+  __syncthreads();
+  if (r) return;
+  double ds = 0;
+  if (c < g.C) {
+    const double P1 = sm[2][0][lane], P2 = sm[3][0][lane];
+    const double sc = g.scale_cols == 0 ? 1.0 : g.scale_cols == 1 ? g.scale[0] : g.scale[c];
+    if (g.dw_pre) g.dw_pre[c] = (float)sm[0][0][lane];
+    if (g.db_pre) g.db_pre[c] = (float)sm[1][0][lane];
+    if (g.dw_post) g.dw_post[c] = (float)(sc * P1);
+    if (g.db_post) g.db_post[c] = (float)(sc * P2);
+    ds = (g.w_post ? g.w_post[c] : 1.f) * P1 + (g.b_post ? g.b_post[c] : 0.f) * P2;
+    if (g.dscale && g.scale_cols > 1) g.dscale[c] = (float)ds;
+  }
+  if (g.dscale && g.scale_cols == 1) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) ds += __shfl_xor_sync(0xffffffffu, ds, o);
+    if (lane == 0) {
+      g.scalar[blockIdx.x] = ds;
+      if (gridDim.x == 1) g.dscale[0] = (float)ds;
+    }
+  }
+}
+__global__ void __launch_bounds__(32) residual_scalar_kernel(const double* scalar, int count, float* dscale) {
+  cudaTriggerProgrammaticLaunchCompletion();
+  cudaGridDependencySynchronize();
+  double s = 0;
+  for (int i = threadIdx.x; i < count; i += 32) s += scalar[i];
+#pragma unroll
+  for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if (threadIdx.x == 0) dscale[0] = (float)s;
+}
+
+// ---------------------------------------------------------------- host side
+// Lanes of a row of C channels, padding to 16 included.
+struct Shape {
+  int lanes, threads;
+  bool multi;
+};
+Shape shape_for(int C) {
+  const int v = (C + 15) / 16 * 2;
+  Shape s{4, THREADS, false};
+  while (s.lanes < v && s.lanes < 32) s.lanes *= 2;
+  if (s.lanes >= v) return s;
+  s.lanes = (v + 31) / 32 * 32;
+  s.multi = true;
+  s.threads = s.lanes > THREADS / 2 ? s.lanes : THREADS / s.lanes * s.lanes;
+  return s;
+}
+
+// Two blocks an SM, which their registers allow.
+constexpr int BLOCKS = 304;
+int64_t blocks_for(int64_t n, const Shape& s) {
+  const int64_t rows = s.threads / s.lanes;
+  return std::max<int64_t>(1, std::min<int64_t>((n + rows - 1) / rows, BLOCKS));
+}
+
+constexpr int RING_MOST = 108 << 10;  // of a block, so that two fit
+// Stages of a ring of g.pieces for s.threads: up to four, two at least.
+int ring_of(Args& g, const Shape& s) {
+  const int stage = g.pieces * s.threads * 16;
+  g.stages = std::max(2, std::min(4, RING_MOST / std::max(stage, 1)));
+  return g.stages * stage;
+}
+
+struct ResidualWs {
+  float* part;
+  double* scalar;
+  size_t bytes;
+};
+ResidualWs residual_ws(void* base, size_t cap, int64_t n, int C, bool* ok) {
+  Arena ar(base, cap);
+  ResidualWs w{};
+  const Shape s = shape_for(C);
+  w.part = ar.take<float>((size_t)blocks_for(n, s) * 4 * s.lanes * 8);
+  w.scalar = ar.take<double>((size_t)(C + 31) / 32);
+  w.bytes = ar.used;
+  *ok = ar.ok();
+  return w;
+}
+
+// A launch may start while the kernel before it ends; each waits for that before
+// it touches memory.
+template <class... P, class... A>
+gnn_status launch(int64_t grid, int block, size_t smem, cudaStream_t st, void (*k)(P...), const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3((unsigned)block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  count_launch();
+  GNN_CUDA(cudaLaunchKernelEx(&cfg, k, args...));
+  return GNN_OK;
+}
+
+constexpr int SMEM_MOST = 200 << 10;  // rows of 512 lanes, fp32 with a gate: 2 x 80 KB
+
+template <bool BWD, class TB, class TR, class TY, bool MULTI>
+gnn_status run_shape(Args& g, const Shape& s, cudaStream_t st) {
+  auto* k = BWD ? residual_bwd_kernel<TB, TR, TY, MULTI> : residual_fwd_kernel<TB, TR, TY, MULTI>;
+  static PerDevice done;
+  const gnn_status r = allow_smem(k, SMEM_MOST, done);
+  if (r != GNN_OK) return r;
+  int smem = ring_of(g, s);
+  // the backward's sums of every warp or group pass through the ring
+  if (BWD) smem = std::max(smem, (MULTI ? s.threads / s.lanes : s.threads / 32) * 4 * 8 * s.lanes * (int)sizeof(float));
+  return launch(blocks_for(g.n, s), s.threads, smem, st, k, g);
+}
+template <bool BWD, class TB, class TR, class TY>
+gnn_status run(Args& g, cudaStream_t st) {
+  const Shape s = shape_for(g.C);
+  g.lanes = s.lanes;
+  // pieces of 16 bytes of a lane's eight channels
+  auto add = [&](int k, const void* p, int elem) {
+    g.at[k] = g.pieces;
+    if (p) g.pieces += elem / 2;
+  };
+  g.pieces = 0;
+  if (BWD) {
+    add(0, g.dY, sizeof(TY)), add(1, g.dY, sizeof(TR)), add(2, g.dH, sizeof(TR)), add(3, g.B, sizeof(TB));
+    add(4, g.gate == 2 ? g.G : nullptr, sizeof(TB));
+  } else {
+    add(0, g.R, sizeof(TR)), add(1, g.B, sizeof(TB)), add(2, g.gate == 2 ? g.G : nullptr, sizeof(TB));
+  }
+  return s.multi ? run_shape<BWD, TB, TR, TY, true>(g, s, st) : run_shape<BWD, TB, TR, TY, false>(g, s, st);
+}
+
+// Types of branch, stream and next operand (one type, or an fp32 stream with a
+// 2-byte rest, or fp32 with a 2-byte operand).
+template <class Fn>
+gnn_status with_types(int bt, int rt, int yt, Fn f) {
+  using B16 = __nv_bfloat16;
+  if (bt == GNN_F32 && rt == GNN_F32 && yt == GNN_F32) return f(float(), float(), float());
+  if (bt == GNN_F32 && rt == GNN_F32 && yt == GNN_BF16) return f(float(), float(), B16());
+  if (bt == GNN_F32 && rt == GNN_F32 && yt == GNN_F16) return f(float(), float(), __half());
+  if (bt == GNN_BF16 && rt == GNN_BF16 && yt == GNN_BF16) return f(B16(), B16(), B16());
+  if (bt == GNN_F16 && rt == GNN_F16 && yt == GNN_F16) return f(__half(), __half(), __half());
+  if (bt == GNN_BF16 && rt == GNN_F32 && yt == GNN_BF16) return f(B16(), float(), B16());
+  if (bt == GNN_F16 && rt == GNN_F32 && yt == GNN_F16) return f(__half(), float(), __half());
+  return GNN_ERR_UNSUPPORTED;
+}
+bool good_types(int bt, int rt, int yt) {
+  return with_types(bt, rt, yt, [](auto, auto, auto) { return GNN_OK; }) == GNN_OK;
+}
+
+// What an output's row has to hold: the padding is written too.
+int64_t out_cols(int C, int t) { return t == GNN_F32 ? (C + 3) / 4 * 4 : (C + 15) / 16 * 16; }
+constexpr int64_t LD_MOST = (int64_t)1 << 36;
+bool bad_mat(const void* p, int64_t ld, int64_t cols, int t) {
+  const int64_t e = type_size(t);
+  return !p || ((uintptr_t)p & 15) || (ld * e) % 16 || ld < cols || ld > LD_MOST;
+}
+bool bad_vec(const void* p) { return ((uintptr_t)p & 3) != 0; }
+Span span(const void* p, int64_t rows, int64_t cols, int64_t ld, int t) {
+  return {p, rows, ld * type_size(t), cols * type_size(t)};
+}
+Span flat(const void* p, int64_t bytes) { return {p, 1, bytes, bytes}; }
+
+bool is_norm(int k) { return k == GNN_NORM_NONE || k == GNN_NORM_RMS || k == GNN_NORM_LAYER; }
+
+// What both directions ask of a call.
+gnn_status check(const char* who, const void* B, int64_t ldb, int bt, const void* G, int64_t ldg, int gate_cols, int act,
+                 int64_t n, int C, int rt, int yt, int post, const float* w_post, const float* b_post, const float* scale,
+                 int scale_cols, int pre, const float* w_pre) {
+  if (n < 0 || n > ((int64_t)1 << 40)) return fail(GNN_ERR_INVALID_ARG, "%s: bad row count", who);
+  if (C < 1) return fail(GNN_ERR_INVALID_ARG, "%s: C must be >= 1", who);
+  if (C > MAX_C) return fail(GNN_ERR_UNSUPPORTED, "%s: C > %d", who, MAX_C);
+  if (!is_type(bt) || !is_type(rt) || !is_type(yt)) return fail(GNN_ERR_INVALID_ARG, "%s: unknown type", who);
+  if (!good_types(bt, rt, yt))
+    return fail(GNN_ERR_UNSUPPORTED, "%s: types are (t, t, t), (t, fp32, t), (fp32, fp32, t) or fp32 for branch, stream and Y", who);
+  if (!is_norm(post) || !is_norm(pre)) return fail(GNN_ERR_INVALID_ARG, "%s: post and pre are GNN_NORM_*", who);
+  if (!is_act(act)) return fail(GNN_ERR_INVALID_ARG, "%s: gate_act is GNN_ACT_*", who);
+  if (gate_cols != 0 && gate_cols != 1 && gate_cols != C)
+    return fail(GNN_ERR_INVALID_ARG, "%s: gate_cols is 0, 1 or C", who);
+  if (scale_cols != 0 && scale_cols != 1 && scale_cols != C)
+    return fail(GNN_ERR_INVALID_ARG, "%s: scale_cols is 0, 1 or C", who);
+  if ((scale_cols != 0) != (scale != nullptr)) return fail(GNN_ERR_INVALID_ARG, "%s: scale and scale_cols disagree", who);
+  if (bad_vec(w_post) || bad_vec(b_post) || bad_vec(scale) || bad_vec(w_pre))
+    return fail(GNN_ERR_INVALID_ARG, "%s: misaligned weights", who);
+  if (n == 0) return GNN_OK;
+  if (!B && (gate_cols || scale || w_post || b_post || post != GNN_NORM_NONE))
+    return fail(GNN_ERR_INVALID_ARG, "%s: without a branch there is no post norm, gate or scale", who);
+  if (B && bad_mat(B, ldb, C, bt)) return fail(GNN_ERR_INVALID_ARG, "%s: B needs 16-byte aligned rows and ldb >= C", who);
+  if (gate_cols > 1 && bad_mat(G, ldg, C, bt))
+    return fail(GNN_ERR_INVALID_ARG, "%s: gate needs 16-byte aligned rows and ldg >= C", who);
+  if (gate_cols == 1 && (!G || ((uintptr_t)G & (type_size(bt) - 1)) || ldg < 1 || ldg > LD_MOST))
+    return fail(GNN_ERR_INVALID_ARG, "%s: gate of one value a row is NULL, misaligned or has no stride", who);
+  return GNN_OK;
+}
+
+}  // namespace
+
+}  // namespace gnn
+
+using namespace gnn;
+
+extern "C" gnn_status gnn_residual_norm_workspace(int64_t n, int32_t C, size_t* bwd_bytes) {
+  GNN_REQUIRE(n >= 0 && C >= 1, "gnn_residual_norm_workspace: bad sizes");
+  GNN_REQUIRE(bwd_bytes, "gnn_residual_norm_workspace: NULL result");
+  if (C > MAX_C) return fail(GNN_ERR_UNSUPPORTED, "gnn_residual_norm_workspace: C > %d", MAX_C);
+  bool ok;
+  *bwd_bytes = residual_ws(nullptr, 0, n, C, &ok).bytes;
+  return GNN_OK;
+}
+
+extern "C" gnn_status gnn_residual_norm_fwd(const void* B, int64_t ldb, int32_t b_type, const void* R, int64_t ldr,
+                                            int32_t r_type, const void* gate, int64_t ldg, int32_t gate_cols,
+                                            int32_t gate_act, int64_t n, int32_t C, int32_t post, const float* w_post,
+                                            const float* b_post, const float* scale, int32_t scale_cols, int32_t pre,
+                                            const float* w_pre, const float* b_pre, double eps, void* H, int64_t ldh,
+                                            void* Y, int64_t ldy, int32_t y_type, float* stats, gnn_stream_t stream) {
+  static const char* who = "gnn_residual_norm_fwd";
+  gnn_status s = check(who, B, ldb, b_type, gate, ldg, gate_cols, gate_act, n, C, r_type, y_type, post, w_post, b_post, scale,
+                       scale_cols, pre, w_pre);
+  if (s != GNN_OK) return s;
+  GNN_REQUIRE((float)eps > 0.f && std::isfinite((float)eps), "%s: eps must be positive in fp32", who);
+  GNN_REQUIRE(!bad_vec(b_pre), "%s: misaligned weights", who);
+  GNN_REQUIRE(pre != GNN_NORM_NONE || (!w_pre && !b_pre), "%s: w_pre and b_pre come with a pre norm", who);
+  if (n == 0) return GNN_OK;
+  GNN_REQUIRE((pre == GNN_NORM_NONE) == (Y == nullptr), "%s: Y comes with a pre norm, and only then", who);
+  GNN_REQUIRE(!bad_mat(R, ldr, C, r_type), "%s: R needs 16-byte aligned rows and ldr >= C", who);
+  GNN_REQUIRE(H || !B, "%s: H is NULL", who);
+  GNN_REQUIRE(H || Y, "%s: nothing to write", who);
+  GNN_REQUIRE(!H || !bad_mat(H, ldh, out_cols(C, r_type), r_type),
+              "%s: H needs 16-byte aligned rows and ldh >= C with its padding", who);
+  GNN_REQUIRE(!Y || !bad_mat(Y, ldy, out_cols(C, y_type), y_type),
+              "%s: Y needs 16-byte aligned rows and ldy >= C with its padding", who);
+  GNN_REQUIRE(((uintptr_t)stats & 15) == 0, "%s: misaligned stats", who);
+  const Span hs = span(H, n, out_cols(C, r_type), ldh, r_type), ys = span(Y, n, out_cols(C, y_type), ldy, y_type),
+             ss = flat(stats, n * 16);
+  const Span bs = span(B, n, C, ldb, b_type), rs = span(R, n, C, ldr, r_type),
+             gs = span(gate_cols ? gate : nullptr, n, gate_cols, ldg, b_type);
+  const Span vecs[5] = {flat(w_post, 4ll * C), flat(b_post, 4ll * C), flat(scale, 4ll * scale_cols), flat(w_pre, 4ll * C),
+                        flat(b_pre, 4ll * C)};
+  GNN_REQUIRE(!overlap(hs, bs) && !overlap(hs, gs) && ((H == R && ldh == ldr) || !overlap(hs, rs)),
+              "%s: H overlaps an input (it may be R)", who);
+  GNN_REQUIRE(!overlap(ys, bs) && !overlap(ys, gs) && !overlap(ys, rs) && !overlap(ys, hs), "%s: Y overlaps", who);
+  GNN_REQUIRE(!overlap(ss, bs) && !overlap(ss, gs) && !overlap(ss, rs) && !overlap(ss, hs) && !overlap(ss, ys),
+              "%s: stats overlaps", who);
+  for (const Span& v : vecs)
+    GNN_REQUIRE(!overlap(hs, v) && !overlap(ys, v) && !overlap(ss, v), "%s: an output overlaps a weight", who);
+  Args g{};
+  g.B = B, g.R = R, g.G = gate, g.H = H, g.Y = Y;
+  g.ldb = ldb, g.ldr = ldr, g.ldg = ldg, g.ldh = ldh, g.ldy = ldy;
+  g.n = n, g.C = C, g.gate = gate_cols == 1 ? 1 : gate_cols ? 2 : 0, g.act = gate_act, g.post = post, g.pre = pre;
+  g.w_post = w_post, g.b_post = b_post, g.scale = scale, g.w_pre = w_pre, g.b_pre = b_pre;
+  g.scale_cols = scale_cols, g.eps = (float)eps, g.inv_c = 1.f / (float)C, g.stats = reinterpret_cast<float4*>(stats);
+  return with_types(b_type, r_type, y_type, [&](auto b, auto r, auto y) {
+    return run<false, decltype(b), decltype(r), decltype(y)>(g, as_stream(stream));
+  });
+}
+
+extern "C" gnn_status gnn_residual_norm_bwd(const void* dH, int64_t lddh, const void* dY, int64_t lddy, int32_t y_type,
+                                            const void* B, int64_t ldb, int32_t b_type, const void* H, int64_t ldh,
+                                            int32_t r_type, const void* gate, int64_t ldg, int32_t gate_cols,
+                                            int32_t gate_act, int64_t n, int32_t C, int32_t post, const float* w_post,
+                                            const float* b_post, const float* scale, int32_t scale_cols, int32_t pre,
+                                            const float* w_pre, const float* stats, void* dR, int64_t lddr, void* dB,
+                                            int64_t lddb, void* dgate, int64_t lddg, float* dw_post, float* db_post,
+                                            float* dscale, float* dw_pre, float* db_pre, void* ws, size_t ws_bytes,
+                                            gnn_stream_t stream) {
+  static const char* who = "gnn_residual_norm_bwd";
+  gnn_status s = check(who, B, ldb, b_type, gate, ldg, gate_cols, gate_act, n, C, r_type, y_type, post, w_post, b_post, scale,
+                       scale_cols, pre, w_pre);
+  if (s != GNN_OK) return s;
+  GNN_REQUIRE(!bad_vec(dw_post) && !bad_vec(db_post) && !bad_vec(dscale) && !bad_vec(dw_pre) && !bad_vec(db_pre),
+              "%s: misaligned gradients", who);
+  GNN_REQUIRE(pre != GNN_NORM_NONE || (!w_pre && !dw_pre && !db_pre), "%s: w_pre and its gradients come with a pre norm", who);
+  GNN_REQUIRE(!dscale || scale, "%s: dscale without a scale", who);
+  if (n > 0) {
+    GNN_REQUIRE(B || (!dB && !dgate && !dw_post && !db_post && !dscale), "%s: gradients of a branch that is not there", who);
+    GNN_REQUIRE(gate_cols || !dgate, "%s: dgate without a gate", who);
+    GNN_REQUIRE(pre != GNN_NORM_NONE || !dY, "%s: dY comes with a pre norm", who);
+    GNN_REQUIRE(dH || dY, "%s: neither dH nor dY", who);
+    GNN_REQUIRE(!dH || !bad_mat(dH, lddh, C, r_type), "%s: dH needs 16-byte aligned rows and lddh >= C", who);
+    GNN_REQUIRE(!dY || !bad_mat(dY, lddy, C, y_type), "%s: dY needs 16-byte aligned rows and lddy >= C", who);
+    GNN_REQUIRE(!dY || !bad_mat(H, ldh, C, r_type), "%s: H needs 16-byte aligned rows and ldh >= C", who);
+    GNN_REQUIRE(stats && ((uintptr_t)stats & 15) == 0, "%s: stats is NULL or misaligned", who);
+    GNN_REQUIRE(!dR || !bad_mat(dR, lddr, out_cols(C, r_type), r_type),
+                "%s: dR needs 16-byte aligned rows and lddr >= C with its padding", who);
+    GNN_REQUIRE(!dB || !bad_mat(dB, lddb, out_cols(C, b_type), b_type),
+                "%s: dB needs 16-byte aligned rows and lddb >= C with its padding", who);
+    GNN_REQUIRE(gate_cols <= 1 || !dgate || !bad_mat(dgate, lddg, out_cols(C, b_type), b_type),
+                "%s: dgate needs 16-byte aligned rows and lddg >= C with its padding", who);
+    GNN_REQUIRE(gate_cols != 1 || !dgate || (((uintptr_t)dgate & (type_size(b_type) - 1)) == 0 && lddg >= 1 && lddg <= LD_MOST),
+                "%s: dgate of one value a row is misaligned or has no stride", who);
+  }
+  const int want_q = dw_pre || db_pre, want_p = dw_post || db_post || dscale;
+  bool ok;
+  const ResidualWs w = residual_ws(ws, ws_bytes, n, C, &ok);
+  GNN_REQUIRE((!want_q && !want_p) || (ws && ok && ((uintptr_t)ws & 7) == 0),
+              "%s: workspace too small (%zu < %zu) or misaligned", who, ws_bytes, w.bytes);
+  if (n > 0) {
+    const Span outs[9] = {span(dR, n, out_cols(C, r_type), lddr, r_type), span(dB, n, out_cols(C, b_type), lddb, b_type),
+                          span(dgate, n, gate_cols > 1 ? out_cols(C, b_type) : 1, lddg, b_type), flat(dw_post, 4ll * C),
+                          flat(db_post, 4ll * C), flat(dscale, 4ll * scale_cols), flat(dw_pre, 4ll * C), flat(db_pre, 4ll * C),
+                          flat(want_q || want_p ? ws : nullptr, (int64_t)w.bytes)};
+    const Span ins[10] = {span(dH, n, C, lddh, r_type), span(dY, n, C, lddy, y_type), span(B, n, C, ldb, b_type),
+                          span(dY ? H : nullptr, n, C, ldh, r_type), span(gate_cols ? gate : nullptr, n, gate_cols, ldg, b_type),
+                          flat(stats, n * 16), flat(w_post, 4ll * C), flat(b_post, 4ll * C), flat(scale, 4ll * scale_cols),
+                          flat(w_pre, 4ll * C)};
+    for (int o = 0; o < 9; ++o) {
+      for (int i = 0; i < 10; ++i)
+        GNN_REQUIRE((o == 0 && i == 0 && dR == dH && lddr == lddh) || !overlap(outs[o], ins[i]),
+                    "%s: an output overlaps an input (dR may be dH)", who);
+      for (int i = 0; i < o; ++i) GNN_REQUIRE(!overlap(outs[o], outs[i]), "%s: outputs overlap", who);
+    }
+    Args g{};
+    g.B = B, g.G = gate, g.dH = dH, g.dY = dY, g.H = const_cast<void*>(H), g.dR = dR, g.dB = dB, g.dG = dgate;
+    g.ldb = ldb, g.ldg = ldg, g.ldh = ldh, g.ldy = lddy, g.lddh = lddh, g.lddr = lddr, g.lddb = lddb, g.lddg = lddg;
+    g.n = n, g.C = C, g.gate = gate_cols == 1 ? 1 : gate_cols ? 2 : 0, g.act = gate_act, g.post = post, g.pre = pre;
+    g.w_post = w_post, g.b_post = b_post, g.scale = scale, g.w_pre = w_pre;
+    g.scale_cols = scale_cols, g.inv_c = 1.f / (float)C;
+    g.stats = reinterpret_cast<float4*>(const_cast<float*>(stats)), g.part = w.part;
+    g.want_q = want_q, g.want_p = want_p;
+    s = with_types(b_type, r_type, y_type, [&](auto b, auto r, auto y) {
+      return run<true, decltype(b), decltype(r), decltype(y)>(g, as_stream(stream));
+    });
+    if (s != GNN_OK) return s;
+  }
+  if (!want_q && !want_p) return GNN_OK;
+  const Shape sh = shape_for(C);
+  const int blocks = (C + 31) / 32;
+  const Join j{w.part, n > 0 ? (int)blocks_for(n, sh) : 0, sh.lanes * 8, C, scale_cols, w_post, b_post, scale, dw_post, db_post,
+               dscale, dw_pre, db_pre, w.scalar, want_q, want_p};
+  s = launch(blocks, 32 * JOIN_ROWS, 0, as_stream(stream), residual_join_kernel, j);
+  if (s != GNN_OK || !dscale || scale_cols != 1 || blocks == 1) return s;
+  return launch(1, 32, 0, as_stream(stream), residual_scalar_kernel, (const double*)w.scalar, blocks, dscale);
+}
