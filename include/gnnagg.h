@@ -816,6 +816,49 @@ gnn_status gnn_adamw_step(const gnn_adamw_tensor* tensors, int32_t n_tensors, in
                           double grad_scale, double max_norm, float* grad_norm, void* ws,
                           size_t ws_bytes, gnn_stream_t stream);
 
+/* Newton-Schulz orthogonalisation of `count` matrices [rows][cols] (row strides
+ * ldx, ldo; matrices stride_x, stride_o elements apart; any GNN_* types):
+ *   X0 = X / (|X|_F + eps), then `steps` times (0 to 16)
+ *   X <- a X + (b A + c A A) X,  A = X X'   (X' X where rows > cols)
+ * with {a, b, c} = coeffs[3 s], a host array (each within 32 of zero).  Operands
+ * are held to 22 bits, down to 2^-35 (of a matrix of norm one), products accumulate in fp32; the steps have to keep every
+ * singular value below 60.  norms (fp32 [count], may be NULL) receives |X|_F.  A
+ * matrix whose norm is not finite in fp32 gives NaN.  O may be X (one type size and
+ * strides).  rows, cols <= 65536, the smaller of them <= 16384. */
+gnn_status gnn_orthogonalise_workspace(int32_t count, int32_t rows, int32_t cols,
+                                       size_t* ws_bytes);
+gnn_status gnn_orthogonalise(const void* X, int64_t ldx, int64_t stride_x, int32_t x_type,
+                             int32_t count, int32_t rows, int32_t cols, const float* coeffs,
+                             int32_t steps, double eps, void* O, int64_t ldo, int64_t stride_o,
+                             int32_t o_type, float* norms, void* ws, size_t ws_bytes,
+                             gnn_stream_t stream);
+
+/* One Muon step over many matrices; per matrix, with g' = grad_scale grad,
+ *   m = momentum m + g',   u = nesterov ? momentum m + g' : m,
+ *   param = param (1 - lr weight_decay) - lr scale O,
+ * O the orthogonalised u as above (before m is rounded, where it is bf16).
+ * Descriptors are a host array, as gnn_adamw_step's.  copy (NULL or bf16)
+ * receives the updated parameters rounded.  A matrix whose |u|_F is not finite
+ * in fp32 keeps its parameters, copy and momentum; norms (fp32 [n_tensors], may
+ * be NULL) receives every |u|_F (matrices without elements have none written).
+ * No two arrays of a call overlap, nor is a matrix listed twice.  Workspaces of
+ * both functions lie on a 256-byte border. */
+typedef struct gnn_muon_tensor {
+  void* param;      /* fp32 or bf16 [rows][cols], updated in place */
+  const void* grad; /* fp32, bf16 or fp16                          */
+  void* m;          /* fp32 or bf16                                */
+  uint16_t* copy;
+  int64_t ldp, ldg, ldm, ldc; /* row strides, elements */
+  int32_t rows, cols;
+  float scale;      /* of the update */
+} gnn_muon_tensor;
+gnn_status gnn_muon_workspace(const gnn_muon_tensor* tensors, int32_t n_tensors, size_t* ws_bytes);
+gnn_status gnn_muon_step(const gnn_muon_tensor* tensors, int32_t n_tensors, int32_t param_type,
+                         int32_t grad_type, int32_t m_type, double lr, double momentum,
+                         int32_t nesterov, double weight_decay, double grad_scale,
+                         const float* coeffs, int32_t steps, double eps, float* norms, void* ws,
+                         size_t ws_bytes, gnn_stream_t stream);
+
 /* ------------------------------------------------------------------------ */
 /* Epoch control (SYLVIE guide, sections 8 and 11).  Host code.              */
 /* ------------------------------------------------------------------------ */

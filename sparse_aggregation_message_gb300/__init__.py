@@ -13,7 +13,7 @@ from typing import Optional, Sequence
 
 from . import _abi
 from ._abi import (CSR_DEDUP, CSR_GCN, CSR_MEAN, CSR_SELF_LOOPS, CSR_SYMMETRIZE,  # noqa: F401
-                   GnnAdamwTensor, GnnBitRule, GnnBlocked,
+                   GnnAdamwTensor, GnnBitRule, GnnBlocked, GnnMuonTensor,
                    GnnBoundary, GnnCsr, GnnError, GnnLdrState, call, load)
 
 LdrState = GnnLdrState
@@ -32,6 +32,7 @@ __all__ = [
     "gnn_group_norm_workspace", "gnn_group_norm_fwd", "gnn_group_norm_bwd",
     "gnn_gated_workspace", "gnn_gated_fwd", "gnn_gated_bwd",
     "gnn_residual_norm_workspace", "gnn_residual_norm_fwd", "gnn_residual_norm_bwd",
+    "NS_COEFFS", "gnn_orthogonalise_workspace", "gnn_orthogonalise", "MuonTensors", "gnn_muon_workspace", "gnn_muon_step",
     "AdamwTensors", "adamw_state", "gnn_adamw_workspace", "gnn_adamw_step",
     "Blocked", "gnn_blocked_build", "gnn_spmm_fwd_blocked", "gnn_spmm_bwd_blocked",
 ]
@@ -1099,6 +1100,121 @@ def gnn_adamw_step(tensors: AdamwTensors, state, lr: float, beta1: float = 0.9, 
     call("gnn_adamw_step", tensors.c, tensors.count, tensors.param_type, tensors.grad_type, tensors.state_bits,
          state.data_ptr(), lr, beta1, beta2, eps, weight_decay, grad_scale, max_norm, _f32(grad_norm, 1, "grad_norm"), at,
          size, _current(state, stream))
+
+
+# Muon's quintic: its singular values end between 0.7 and 1.2.
+NS_COEFFS = (3.4445, -4.7750, 2.0315)
+
+
+@functools.lru_cache(maxsize=64)
+def _coeffs(coeffs, steps: int):
+    """One triple for every step, or a triple each, as a C array."""
+    each = coeffs if coeffs and hasattr(coeffs[0], "__len__") else (coeffs,) * steps
+    flat = [float(c) for triple in each for c in triple]
+    if len(each) != steps or any(len(triple) != 3 for triple in each):
+        raise ValueError(f"coeffs: needs three numbers, or three for each of {steps} steps")
+    return (ctypes.c_float * max(len(flat), 1))(*flat)
+
+
+@functools.lru_cache(maxsize=1024)
+def gnn_orthogonalise_workspace(count: int, rows: int, cols: int) -> int:
+    nb = ctypes.c_size_t()
+    call("gnn_orthogonalise_workspace", count, rows, cols, ctypes.byref(nb))
+    return nb.value
+
+
+def _matrices(t, what: str):
+    """(row stride, stride between matrices) of [rows, cols] or [count, rows, cols]."""
+    if t.dim() not in (2, 3) or not t.is_cuda or (t.shape[-1] > 1 and t.stride(-1) != 1):
+        raise ValueError(f"{what}: needs a CUDA matrix, or a batch of them, with contiguous rows, got {tuple(t.shape)} "
+                         f"with strides {t.stride()}")
+    cols = t.shape[-1]
+    ld = t.stride(-2) if t.shape[-2] > 1 else cols
+    return ld, t.stride(0) if t.dim() == 3 else 0
+
+
+def gnn_orthogonalise(X, O, steps: int = 5, coeffs=NS_COEFFS, eps: float = 1e-7, norms=None, ws=None,  # noqa: E741
+                      stream=None) -> None:
+    """O = X / (|X| + eps) after `steps` of Newton-Schulz with coefficients
+    (a, b, c), or a triple for each step; X [rows, cols] or [count, rows, cols], O
+    of X's shape, any of fp32, bf16 and fp16 each; norms (fp32 [count]) receives
+    every |X|."""
+    ldx, sx = _matrices(X, "X")
+    ldo, so = _matrices(O, "O")
+    if O.shape != X.shape:
+        raise ValueError(f"O: needs X's shape {tuple(X.shape)}, got {tuple(O.shape)}")
+    rows, cols = X.shape[-2:]
+    count = X.shape[0] if X.dim() == 3 else 1
+    at, size, ws = _ws(ws, gnn_orthogonalise_workspace(count, rows, cols), X, stream)
+    call("gnn_orthogonalise", X.data_ptr(), ldx, sx, _type(X), count, rows, cols,
+         _coeffs(coeffs, steps), steps, eps, O.data_ptr(), ldo,
+         so, _type(O), _f32(norms, count, "norms"), at, size, _current(X, stream))
+
+
+class MuonTensors:
+    """The matrices of a Muon optimiser, checked once: lists of parameters (fp32
+    or bf16 [rows, cols], updated in place), their gradients (fp32, bf16 or fp16),
+    momenta (fp32 or bf16) and, optionally, copies (bf16, None for a matrix without
+    one), with contiguous rows, and the factors on the updates; scales None: 0.2
+    sqrt(max(rows, cols)), which makes an update's mean square that of AdamW's, so
+    that both take one learning rate.  All stay the caller's."""
+
+    def __init__(self, params, grads, momenta, copies=None, scales=None):
+        import torch
+        k = len(params)
+        self.count = k
+        lists = dict(params=params, grads=grads, momenta=momenta, copies=copies)
+        for name, ts in dict(lists, scales=scales).items():
+            if ts is not None and len(ts) != k:
+                raise ValueError(f"{name}: {len(ts)} for {k} parameters")
+        want = dict(params=params[0].dtype if k else torch.float32, grads=grads[0].dtype if k else torch.float32,
+                    momenta=momenta[0].dtype if k else torch.float32, copies=torch.bfloat16)
+        for name, ts in lists.items():
+            for i, t in enumerate(ts or ()):
+                if t is None and name == "copies":
+                    continue
+                if t.device != params[0].device:
+                    raise ValueError(f"{name}[{i}]: on {t.device}, params[0] on {params[0].device}")
+                if t.dim() != 2 or t.shape != params[i].shape or t.dtype != want[name] or t.device.type != "cuda" or \
+                        (t.shape[1] > 1 and t.stride(1) != 1):
+                    raise ValueError(f"{name}[{i}]: needs a {want[name]} CUDA matrix of {tuple(params[i].shape)} with "
+                                     "contiguous rows")
+        places = [p.data_ptr() for p in params if p.numel()]
+        if len(set(places)) < len(places):
+            raise ValueError("params: a matrix is listed twice")
+        self.param_type, self.grad_type, self.m_type = (_type(t[0]) if k else 0 for t in (params, grads, momenta))
+        self.device = params[0].device if k else None
+        self._keep = {name: list(ts) for name, ts in lists.items() if ts is not None}
+        at = lambda ts, i: None if ts is None or ts[i] is None else ts[i].data_ptr()  # noqa: E731
+        ld = lambda ts, i: 0 if ts is None or ts[i] is None else _matrices(ts[i], "matrix")[0]  # noqa: E731
+        four = (params, grads, momenta, copies)
+        self.c = (GnnMuonTensor * max(k, 1))(*[
+            GnnMuonTensor(*(at(ts, i) for ts in four), *(ld(ts, i) for ts in four), *params[i].shape,
+                          0.2 * max(params[i].shape) ** 0.5 if scales is None else float(scales[i])) for i in range(k)])
+        self.ws_bytes = gnn_muon_workspace(self)
+
+
+def gnn_muon_workspace(tensors: MuonTensors) -> int:
+    nb = ctypes.c_size_t()
+    call("gnn_muon_workspace", tensors.c, tensors.count, ctypes.byref(nb))
+    return nb.value
+
+
+def gnn_muon_step(tensors: MuonTensors, lr: float, momentum: float = 0.95, nesterov: bool = True,
+                  weight_decay: float = 0.0, grad_scale: float = 1.0, steps: int = 5, coeffs=NS_COEFFS,
+                  eps: float = 1e-7, norms=None, ws=None, stream=None) -> None:
+    """One Muon step over every matrix: m = momentum m + g, the update (with
+    nesterov g + momentum m, else m) orthogonalised, params (1 - lr weight_decay) -
+    lr scale update.  norms (fp32, one a matrix) receives the updates' norms; a
+    matrix whose norm is not finite is left as it is."""
+    if tensors.count == 0:
+        return
+    first = tensors._keep["params"][0]
+    at, size, ws = _ws(ws, tensors.ws_bytes, first, stream)
+    call("gnn_muon_step", tensors.c, tensors.count, tensors.param_type, tensors.grad_type, tensors.m_type, lr, momentum,
+         int(nesterov), weight_decay, grad_scale,
+         _coeffs(coeffs, steps), steps, eps,
+         _f32(norms, tensors.count, "norms"), at, size, _current(first, stream))
 
 
 # ---------------------------------------------------------------- epoch control (host only)

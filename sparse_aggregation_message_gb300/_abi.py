@@ -11,6 +11,7 @@ c_i32, c_i64, c_u8, c_u16, c_u32 = ctypes.c_int32, ctypes.c_int64, ctypes.c_uint
 c_size, c_vp, c_char_p = ctypes.c_size_t, ctypes.c_void_p, ctypes.c_char_p
 P_i64 = ctypes.POINTER(c_i64)
 P_size = ctypes.POINTER(c_size)
+P_f32 = ctypes.POINTER(ctypes.c_float)
 
 STATUS = {0: "GNN_OK", 1: "GNN_ERR_INVALID_ARG", 2: "GNN_ERR_UNSUPPORTED", 3: "GNN_ERR_CUDA",
           4: "GNN_ERR_DEVICE_CHECK", 5: "GNN_ERR_TIMEOUT", 6: "GNN_ERR_CAPACITY"}
@@ -54,6 +55,11 @@ class GnnLdrState(ctypes.Structure):
     _fields_ = [("lambda_", ctypes.c_double), ("delta", c_i32), ("b_min", c_i32), ("b_max", c_i32),
                 ("t", c_i32), ("base_bits", c_i32), ("async_next", c_i32), ("F", ctypes.c_double),
                 ("ldr", ctypes.c_double * (GNN_LDR_MAX_DELTA + 1))]
+
+
+class GnnMuonTensor(ctypes.Structure):
+    _fields_ = [("param", c_vp), ("grad", c_vp), ("m", c_vp), ("copy", c_vp), ("ldp", c_i64), ("ldg", c_i64),
+                ("ldm", c_i64), ("ldc", c_i64), ("rows", c_i32), ("cols", c_i32), ("scale", ctypes.c_float)]
 
 
 class GnnAdamwTensor(ctypes.Structure):
@@ -178,6 +184,13 @@ PROTOTYPES = {
                                       ctypes.c_double, ctypes.c_double, ctypes.c_double, ctypes.c_double,
                                       ctypes.c_double, ctypes.c_double, ctypes.c_double, c_vp, c_vp, c_size,
                                       c_vp]),
+    "gnn_orthogonalise_workspace": (ctypes.c_int, [c_i32, c_i32, c_i32, P_size]),
+    "gnn_orthogonalise": (ctypes.c_int, [c_vp, c_i64, c_i64, c_i32, c_i32, c_i32, c_i32, P_f32, c_i32,
+                                         ctypes.c_double, c_vp, c_i64, c_i64, c_i32, c_vp, c_vp, c_size, c_vp]),
+    "gnn_muon_workspace": (ctypes.c_int, [ctypes.POINTER(GnnMuonTensor), c_i32, P_size]),
+    "gnn_muon_step": (ctypes.c_int, [ctypes.POINTER(GnnMuonTensor), c_i32, c_i32, c_i32, c_i32, ctypes.c_double,
+                                     ctypes.c_double, c_i32, ctypes.c_double, ctypes.c_double, P_f32, c_i32,
+                                     ctypes.c_double, c_vp, c_vp, c_size, c_vp]),
     "gnn_sync_check": (ctypes.c_int, [c_vp]),
 }
 

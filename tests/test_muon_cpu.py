@@ -1,0 +1,148 @@
+"""The 64-bit Newton-Schulz steps against singular values, and the calls of the
+orthogonalisation and the Muon step that are refused on the host."""
+import ctypes
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from sparse_aggregation_message_gb300 import _abi  # noqa: E402
+from tests import muon_ref as ref  # noqa: E402
+
+P = ctypes.c_void_p
+F32, BF16, F16 = 0, 1, 2
+INVALID, UNSUPPORTED = 1, 2
+MB = 1 << 20
+
+
+@pytest.mark.parametrize("size", [(1, 1), (1, 9), (9, 1), (20, 33), (33, 20), (40, 40)])
+@pytest.mark.parametrize("steps,coeffs", [(5, ref.NS), (2, ((4.0, -6.0, 2.5), (2.0, -1.5, 0.5))), (0, ())])
+def test_steps_are_a_polynomial_of_the_singular_values(size, steps, coeffs):
+    """64-bit roundings, amplified by a^5 = 485 at most: 1e-15 * 40 * 485 < 1e-10."""
+    x = torch.randn(*size, generator=torch.Generator().manual_seed(1), dtype=torch.float64)
+    got = ref.steps64(x, coeffs, steps)
+    want = ref.by_singular_values(x, coeffs, steps) if steps else x / (torch.linalg.matrix_norm(x) + 1e-7)
+    assert float((got - want).abs().max()) < 1e-10
+
+
+def test_the_bound_tells_limbs_from_halves():
+    """One fp16 rounding of X a step is outside of the bound on two limbs."""
+    x = torch.randn(64, 100, generator=torch.Generator().manual_seed(2), dtype=torch.float64)
+    want, bound = ref.spread(x, ref.NS, 5)
+    half = ref.steps64(x, ref.NS, 5, noise=lambda v, mag, K: v if K else v.half().double())
+    assert float((half - want).abs().max()) > 4 * bound
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return _abi.load()
+
+
+def floats(*v):
+    return (ctypes.c_float * max(len(v), 1))(*v)
+
+
+NAN, INF = float("nan"), float("inf")
+
+
+def orth(lib, X=MB, ldx=64, sx=0, xt=F32, count=1, rows=32, cols=64, coeffs=(3.0, -4.0, 2.0) * 5, steps=5, eps=1e-7, O=2 * MB, ldo=64,  # noqa: E741
+         so=0, ot=F32, norms=None, ws=16 * MB, ws_bytes=1 << 40):
+    return lib.gnn_orthogonalise(P(X), ldx, sx, xt, count, rows, cols, floats(*coeffs) if coeffs is not None else None, steps, eps, P(O),
+                                 ldo, so, ot, P(norms), P(ws), ws_bytes, None)
+
+
+@pytest.mark.parametrize("bad,code", [
+    (dict(count=-1), INVALID), (dict(rows=-1), INVALID), (dict(cols=-2), INVALID), (dict(rows=65537, ldx=64), UNSUPPORTED),
+    (dict(rows=20000, cols=20000, ldx=20000, ldo=20000), UNSUPPORTED), (dict(xt=3), INVALID), (dict(ot=-1), INVALID), (dict(steps=-1), INVALID),
+    (dict(steps=17, coeffs=(1.0,) * 51), INVALID), (dict(coeffs=None), INVALID), (dict(coeffs=(NAN,) * 15), INVALID), (dict(coeffs=(33.0,) * 15), INVALID),
+    (dict(coeffs=(INF,) * 15), INVALID), (dict(eps=0.0), INVALID), (dict(eps=-1.0), INVALID), (dict(eps=NAN), INVALID), (dict(eps=INF), INVALID),
+    (dict(norms=2), INVALID), (dict(X=None), INVALID), (dict(O=None), INVALID), (dict(X=MB + 2), INVALID), (dict(O=2 * MB + 1, ot=BF16), INVALID),
+    (dict(ldx=63), INVALID), (dict(ldo=32), INVALID), (dict(count=2, sx=100, so=4096), INVALID), (dict(count=2, sx=4096, so=0), INVALID),
+    (dict(ws=None), INVALID), (dict(ws=16 * MB + 128), INVALID), (dict(ws_bytes=1000), INVALID), (dict(O=MB + 256), INVALID),
+    (dict(O=MB, ldo=65), INVALID), (dict(O=MB, ot=BF16), INVALID)])
+def test_orthogonalise_refuses(lib, bad, code):
+    assert orth(lib, **bad) == code
+    assert b"gnn_orthogonalise" in lib.gnn_last_error()
+
+
+def test_nothing_to_do_needs_nothing(lib):
+    for kw in (dict(count=0), dict(rows=0), dict(cols=0, ldx=0, ldo=0)):
+        assert orth(lib, **kw, X=None, O=None, ws=None, ws_bytes=0) == 0, kw
+
+
+def muon(lib, count=1, pt=F32, gt=F32, mt=F32, lr=0.01, mu=0.9, nesterov=1, wd=0.0, gs=1.0, coeffs=(3.0, -4.0, 2.0) * 5, steps=5, eps=1e-7,
+         norms=None, ws=16 * MB, ws_bytes=1 << 40, tensors=0, **t):
+    one = dict(param=MB, grad=2 * MB, m=3 * MB, copy=None, ldp=64, ldg=64, ldm=64, ldc=64, rows=32, cols=64, scale=1.0)
+    one.update(t)
+    arr = (_abi.GnnMuonTensor * 1)(_abi.GnnMuonTensor(*one.values()))
+    return lib.gnn_muon_step(arr if tensors == 0 else None, count, pt, gt, mt, lr, mu, nesterov, wd, gs,
+                             floats(*coeffs) if coeffs is not None else None, steps, eps, P(norms), P(ws), ws_bytes, None)
+
+
+@pytest.mark.parametrize("bad,code", [
+    (dict(count=-1), INVALID), (dict(tensors=None), INVALID), (dict(pt=F16), UNSUPPORTED), (dict(mt=F16), UNSUPPORTED), (dict(pt=7), UNSUPPORTED),
+    (dict(gt=5), INVALID), (dict(mu=1.0), INVALID), (dict(mu=-0.1), INVALID), (dict(mu=NAN), INVALID), (dict(lr=NAN), INVALID), (dict(lr=INF), INVALID),
+    (dict(wd=INF), INVALID), (dict(gs=NAN), INVALID), (dict(steps=20, coeffs=(1.0,) * 60), INVALID), (dict(coeffs=None), INVALID), (dict(eps=0.0), INVALID),
+    (dict(norms=1), INVALID), (dict(param=None), INVALID), (dict(grad=None), INVALID), (dict(m=None), INVALID), (dict(param=MB + 2), INVALID),
+    (dict(grad=2 * MB + 1, gt=BF16), INVALID), (dict(m=3 * MB + 3), INVALID), (dict(copy=4 * MB + 1), INVALID), (dict(ldp=63), INVALID),
+    (dict(ldg=0), INVALID), (dict(ldm=-64), INVALID), (dict(copy=4 * MB, ldc=60), INVALID), (dict(rows=-1), INVALID), (dict(rows=70000), UNSUPPORTED),
+    (dict(scale=NAN), INVALID), (dict(grad=MB), INVALID), (dict(m=MB + 128), INVALID), (dict(copy=MB), INVALID), (dict(copy=3 * MB + 64), INVALID),
+    (dict(ws=None), INVALID), (dict(ws=16 * MB + 64), INVALID), (dict(ws_bytes=4096), INVALID)])
+def test_muon_refuses(lib, bad, code):
+    assert muon(lib, **bad) == code
+    assert b"gnn_muon" in lib.gnn_last_error()
+
+
+def test_workspaces(lib):
+    nb = ctypes.c_size_t()
+    assert lib.gnn_orthogonalise_workspace(1, 64, 64, None) == INVALID
+    assert lib.gnn_orthogonalise_workspace(-1, 64, 64, ctypes.byref(nb)) == INVALID
+    assert lib.gnn_muon_workspace(None, 1, ctypes.byref(nb)) == INVALID
+    assert lib.gnn_muon_workspace(None, 0, None) == INVALID
+    assert lib.gnn_muon_workspace(None, 0, ctypes.byref(nb)) == 0 and nb.value == 0
+    sizes = []
+    for count in (0, 1, 64, 1000):  # 64 matrices a pass
+        assert lib.gnn_orthogonalise_workspace(count, 64, 256, ctypes.byref(nb)) == 0
+        sizes.append(nb.value)
+    assert sizes[0] == 0 < sizes[1] < sizes[2] == sizes[3]
+
+
+def test_descriptor_layout():
+    assert ctypes.sizeof(_abi.GnnMuonTensor) == 80
+
+
+def test_binding_refuses_before_the_library():
+    import sparse_aggregation_message_gb300 as G
+    x = torch.zeros(4, 16)
+    with pytest.raises(ValueError, match="CUDA"):
+        G.gnn_orthogonalise(x, x)
+    with pytest.raises(ValueError, match="coeffs"):
+        G._coeffs((1.0, 2.0), 5)
+    with pytest.raises(ValueError, match="coeffs"):
+        G._coeffs(((1.0, 2.0, 3.0),) * 2, 5)
+    with pytest.raises(ValueError, match="params"):
+        G.MuonTensors([x], [x], [x])
+    with pytest.raises(ValueError, match="grads"):
+        G.MuonTensors([x], [], [x])
+
+
+def test_muon_tensors_refuse_a_matrix_listed_twice(monkeypatch):
+    import sparse_aggregation_message_gb300 as G
+
+    class Fake:  # stands for a CUDA matrix
+        is_cuda = True
+
+        def __init__(self, at, rows=4, cols=8):
+            self.at, self.shape, self.dtype, self.device = at, (rows, cols), torch.float32, torch.device("cuda", 0)
+
+        numel = lambda self: self.shape[0] * self.shape[1]  # noqa: E731
+        data_ptr = lambda self: self.at  # noqa: E731
+        dim = lambda self: 2  # noqa: E731
+        stride = lambda self, k: (self.shape[1], 1)[k]  # noqa: E731
+
+    def tensors(at):
+        return G.MuonTensors([Fake(a) for a in at], [Fake(4096 + a) for a in at], [Fake(8192 + a) for a in at])
+
+    assert tensors([256, 512]).count == 2
+    with pytest.raises(ValueError, match="twice"):
+        tensors([256, 512, 256])
