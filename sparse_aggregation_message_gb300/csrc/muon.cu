@@ -9,9 +9,9 @@
 // value (22 bits; no entry exceeds the largest singular value, so 64 times the usual
 // range is left), and a product is hi hi + hi lo + lo hi with fp32 sums.
 //
-// Operands lie in the workspace as the tensor cores want them in shared memory:
-// blocks of 128 rows x 64 columns, a row's 128 bytes swizzled, the hi limb's 16 KB
-// before the lo limb's.
+// Operands lie in the workspace in blocks of 128 rows x 64 columns, the hi limb's
+// 16 KB before the lo limb's: rows of 128 bytes, so that one tensor map over the
+// whole workspace loads any of them, swizzled, into shared memory.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -57,6 +57,7 @@ struct Table {
   Mat mat[MAX_MATS];
   int first[MAX_MATS + 1];  // blocks (or parts) before each matrix
   int count;
+  int bn;  // the products' tiles: columns of a CTA's, or 0 for pairs of CTAs
 };
 
 struct Hyper {
@@ -159,7 +160,7 @@ __device__ __forceinline__ void limbs(float a, float b, uint32_t& hi, uint32_t& 
   lo = *reinterpret_cast<const uint32_t*>(&l);
 }
 // Byte of 8 columns (chunk k of 8) of row r in a block's limb.
-__device__ __forceinline__ int chunk_at(int r, int k) { return r * 128 + ((k ^ (r & 7)) << 4); }
+__device__ __forceinline__ int chunk_at(int r, int k) { return r * 128 + k * 16; }
 
 // u scaled into X's limbs, and the new momentum; a block of X a thread block.
 __global__ void __launch_bounds__(THREADS) begin_kernel(const __grid_constant__ Table tab, const Hyper h,
@@ -250,52 +251,316 @@ __global__ void __launch_bounds__(THREADS) apply_kernel(const __grid_constant__ 
 // ------------------------------------------------------------------ products
 enum Phase { GRAM, POLY, NEXT };  // A = X X', P = a I + b A + c A A, X <- P X
 
-__device__ __forceinline__ float value_at(const char* s, int nb, int r, int c) {
-  const char* b = s + ((int64_t)(r >> 7) * nb + (c >> 6)) * BLOCK + chunk_at(r & 127, (c & 63) >> 3) + (c & 7) * 2;
-  return __half2float(*reinterpret_cast<const __half*>(b)) + __half2float(*reinterpret_cast<const __half*>(b + LIMB));
+// One product of every matrix of a pass, by persistent, warp-specialised blocks: warp
+// 0 loads a ring of tiles by TMA, warp 1 issues the MMAs from one thread, warps 2-9
+// drain one of two accumulators in TMEM while the next tile is multiplied.  A tile
+// is 128 x bn on one CTA, or 256 x 256 on a pair of CTAs (cta_group::2), which reads
+// a third less from L2 for its flops.
+//
+// A and P are symmetric: only their blocks on and above the diagonal (of the tile's
+// size) are formed, and a block below is read as the transpose of its mirror image,
+// by loading that and setting the operand's major bit in the instruction.
+constexpr int BOX = 64 * 128;  // 64 rows of 128 bytes: what one TMA load brings
+constexpr int BLOCK_ROWS = BLOCK / 128;
+constexpr int EPI_WARPS = 8;
+constexpr int PRODUCT_THREADS = 64 + 32 * EPI_WARPS;
+constexpr int RING = 192 << 10;
+constexpr int MAX_STAGES = 4;
+constexpr int PRODUCT_SMEM = RING + 1024 /*barriers*/ + 1024 /*align*/;
+
+// A matrix's operands by their first row of the workspace, which has 128-byte rows.
+struct Rows {
+  int x, y, a, p;  // X now and next
+  int mb, nb;
+  int kx, km;      // blocks of 64 with values: of X's columns, of its rows
+};
+struct Product {
+  CUtensorMap map;
+  char* base;
+  unsigned* flags;
+  Phase phase;
+  int bn;      // columns of a CTA's share of B
+  int stages;
+  int count;
+  float ca, cb, cc;
+  int first[MAX_MATS + 1];  // tiles before each matrix
+  Rows mat[MAX_MATS];
+};
+
+struct Ring {
+  uint8_t* tiles;
+  uint64_t *full, *empty, *tfull, *tempty;
+  uint32_t* tmem;
+  volatile int* abort_flag;
+};
+__device__ __forceinline__ Ring carve(uint8_t* raw) {
+  Ring s;
+  s.tiles = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(s.tiles + RING);
+  s.full = bars;
+  s.empty = bars + MAX_STAGES;
+  s.tfull = bars + 2 * MAX_STAGES;
+  s.tempty = s.tfull + 2;
+  s.tmem = reinterpret_cast<uint32_t*>(s.tempty + 2);
+  s.abort_flag = reinterpret_cast<volatile int*>(s.tmem + 1);
+  return s;
 }
 
-// The plain form of a product: a thread block a block of the output, 64 of k at a time.
-__global__ void __launch_bounds__(THREADS) product_kernel(const __grid_constant__ Table tab, Phase phase, int which, float ca,
-                                                          float cb, float cc) {
-  __shared__ float left[128][17], right[16][65];
-  cudaTriggerProgrammaticLaunchCompletion();
+// A tile: its matrix, the first 128-row block and the first 64-column block of the
+// pair's (or the CTA's), and the length of its sum in blocks of 64.
+struct Tile {
+  Rows m;
+  int rb, cb, kb;
+};
+template <bool PAIR>
+__device__ __forceinline__ Tile tile_at(const Product& g, int t) {
+  int i = 0;
+  while (i + 1 < g.count && t >= g.first[i + 1]) ++i;
+  t -= g.first[i];
+  Tile r;
+  r.m = g.mat[i];
+  const int side = PAIR ? r.m.mb >> 1 : r.m.mb, wide = (PAIR ? 256 : g.bn) >> 6;  // tile rows; blocks of 64 across
+  if (g.phase == NEXT) {
+    // the tiles that share columns of X side by side
+    r.rb = t % side;
+    r.cb = t / side * wide;
+  } else {
+    const int each = (PAIR ? 4 : 2) / wide;  // tiles of a square of the diagonal's size
+    int row = 0;
+    while (t >= each * (side - row)) t -= each * (side - row), ++row;
+    r.rb = row;
+    r.cb = row * each * wide + t * wide;
+  }
+  if (PAIR) r.rb *= 2;
+  r.kb = g.phase == GRAM ? r.m.kx : r.m.km;
+  return r;
+}
+template <bool PAIR>
+__device__ __forceinline__ int tiles_of(const Product& g) {
+  return g.first[g.count];
+}
+
+// Whether rows of 128-row block b, columns of 64-block kb lie on or above the
+// diagonal of a symmetric operand (in squares of the tile's size).
+template <bool PAIR>
+__device__ __forceinline__ bool above(int b, int kb) {
+  return PAIR ? (b >> 1) <= (kb >> 2) : b <= (kb >> 1);
+}
+
+template <bool PAIR>
+__device__ __forceinline__ void load_box(const Product& g, uint8_t* to, uint32_t bar, uint64_t* local, int row) {
+  if (PAIR)
+    tc::tma_load_2d_pair(to, &g.map, bar, 0, row);
+  else
+    tc::tma_load_2d(to, &g.map, local, 0, row);
+}
+
+// 64 * boxes rows (from 64-row block r64) of an operand with `nb` column blocks from
+// row `s`, at k block kb: as they lie (K-major), or, below the diagonal, the mirror image's
+// columns (MN-major).
+template <bool PAIR>
+__device__ __forceinline__ void load_rows(const Product& g, uint8_t* to, uint32_t bar, uint64_t* local, int s, int nb, int r64,
+                                          int kb, int boxes, bool direct) {
+  for (int l = 0; l < 2; ++l) {
+    for (int h = 0; h < boxes; ++h, to += BOX) {
+      const int at = direct ? (((r64 + h) >> 1) * nb + kb) * BLOCK_ROWS + ((r64 + h) & 1) * 64
+                            : ((kb >> 1) * nb + r64 + h) * BLOCK_ROWS + (kb & 1) * 64;
+      load_box<PAIR>(g, to, bar, local, s + at + l * 128);
+    }
+  }
+}
+
+template <bool PAIR>
+__device__ __forceinline__ void multiply(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  if (PAIR)
+    tc::mma_16_pair(d, a, b, idesc, acc);
+  else
+    tc::mma_bf16(d, a, b, idesc, acc);
+}
+
+template <bool PAIR>
+__device__ __forceinline__ void products(const Product& g, uint8_t* smem_raw) {
+  const Ring s = carve(smem_raw);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = PAIR ? (int)tc::cluster_rank() : 0;
+  const int unit = PAIR ? blockIdx.x >> 1 : blockIdx.x, units = PAIR ? gridDim.x >> 1 : gridDim.x;
+  const int a_stage = BLOCK, stage = BLOCK + g.bn * 256, cols = PAIR ? 256 : g.bn;
+  if (warp == 0 && lane == 0) tc::prefetch_tmap(&g.map);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < g.stages; ++i) {
+      tc::mbar_init(&s.full[i], 1);
+      tc::mbar_init(&s.empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(&s.tfull[i], 1);
+      tc::mbar_init(&s.tempty[i], (PAIR ? 2 : 1) * EPI_WARPS);  // a lane of each warp
+    }
+    *s.abort_flag = 0;
+    tc::fence_barrier_init();
+  }
+  if (warp == 1) {
+    if (PAIR) {
+      tc::tmem_alloc_pair(s.tmem, 512);
+      tc::tmem_relinquish_pair();
+    } else {
+      tc::tmem_alloc(s.tmem, 256);
+      tc::tmem_relinquish();
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  if (PAIR) tc::cluster_sync();  // the partner's barriers are there
+  tc::fence_after_sync();
   cudaGridDependencySynchronize();
-  const int i = mat_of(tab, blockIdx.x);
-  const Mat& t = tab.mat[i];
-  const int out_nb = phase == NEXT ? t.nb : 2 * t.mb, block = blockIdx.x - tab.first[i];
-  const int r0 = block / out_nb * 128, c0 = block % out_nb * 64, sq = 2 * t.mb;
-  const char* x = t.x[which];
-  const int K = phase == GRAM ? t.nb * 64 : t.mb * 128;
-  float acc[32] = {};
-  const int tc = threadIdx.x & 63, tr = threadIdx.x >> 6;
-  for (int k0 = 0; k0 < K; k0 += 16) {
-    for (int e = threadIdx.x; e < 128 * 16; e += THREADS) {
-      const int r = e >> 4, k = e & 15;
-      left[r][k] = phase == GRAM ? value_at(x, t.nb, r0 + r, k0 + k) : value_at(phase == POLY ? t.a : t.p, sq, r0 + r, k0 + k);
+  const uint32_t tmem = *s.tmem;
+  const int tiles = tiles_of<PAIR>(g);
+
+  if (warp == 0 && lane == 0) {
+    // what ordinary stores of the kernels before wrote is read by TMA
+    asm volatile("fence.proxy.async;" ::: "memory");
+    int st = 0;
+    uint32_t ph = 0;
+    for (int t = unit; t < tiles; t += units) {
+      const Tile w = tile_at<PAIR>(g, t);
+      const int sq = 2 * w.m.mb;
+      const int left = g.phase == GRAM ? w.m.x : g.phase == POLY ? w.m.a : w.m.p, left_nb = g.phase == GRAM ? w.m.nb : sq;
+      const int rb = w.rb + rank, cb = w.cb + rank * (g.bn >> 6);
+      for (int kb = 0; kb < w.kb; ++kb) {
+        if (!tc::mbar_wait(&s.empty[st], ph ^ 1, g.flags, s.abort_flag)) goto done;
+        if (rank == 0) tc::mbar_expect_tx(&s.full[st], (PAIR ? 2 : 1) * stage);
+        uint8_t* a = s.tiles + st * stage;
+        const uint32_t bar = PAIR ? tc::map_to_rank(&s.full[st], 0) : 0;
+        load_rows<PAIR>(g, a, bar, &s.full[st], left, left_nb, 2 * rb, kb, 2, g.phase == GRAM || above<PAIR>(rb, kb));
+        if (g.phase == NEXT)
+          load_rows<PAIR>(g, a + a_stage, bar, &s.full[st], w.m.x, w.m.nb, cb, kb, g.bn >> 6, false);
+        else
+          load_rows<PAIR>(g, a + a_stage, bar, &s.full[st], left, left_nb, cb, kb, g.bn >> 6,
+                          g.phase == GRAM || above<PAIR>(cb >> 1, kb));
+        if (++st == g.stages) { st = 0; ph ^= 1; }
+      }
     }
-    for (int e = threadIdx.x; e < 64 * 16; e += THREADS) {
-      const int c = e >> 4, k = e & 15;
-      right[k][c] = phase == GRAM ? value_at(x, t.nb, c0 + c, k0 + k) : phase == POLY ? value_at(t.a, sq, c0 + c, k0 + k)
-                                                                                       : value_at(x, t.nb, k0 + k, c0 + c);
+    // every stage's release has arrived before this CTA may end
+    for (int i = 0; i < g.stages; ++i) {
+      if (!tc::mbar_wait(&s.empty[st], ph ^ 1, g.flags, s.abort_flag)) goto done;
+      if (++st == g.stages) { st = 0; ph ^= 1; }
     }
-    __syncthreads();
-    for (int k = 0; k < 16; ++k)
+  } else if (warp == 1 && lane == 0 && rank == 0) {
+    int st = 0, it = 0;
+    uint32_t ph = 0;
+    for (int t = unit; t < tiles; t += units, ++it) {
+      const Tile w = tile_at<PAIR>(g, t);
+      const int acc = it & 1;
+      if (!tc::mbar_wait<true>(&s.tempty[acc], ((it >> 1) & 1) ^ 1, g.flags, s.abort_flag)) goto done;
+      tc::fence_after_sync();
+      const uint32_t d = tmem + acc * cols;
+      for (int kb = 0; kb < w.kb; ++kb) {
+        const bool a_mn = g.phase != GRAM && !above<PAIR>(w.rb, kb);
+        const bool b_mn = g.phase == NEXT || (g.phase == POLY && !above<PAIR>(w.cb >> 1, kb));
+        const uint32_t idesc = tc::idesc_16(false, PAIR ? 256 : 128, cols, a_mn, b_mn);
+        if (!tc::mbar_wait(&s.full[st], ph, g.flags, s.abort_flag)) goto done;
+        tc::fence_after_sync();
+        const uint32_t a0 = tc::smem_u32(s.tiles + st * stage), b0 = a0 + a_stage;
+        const uint32_t a_lo = LIMB, b_lo = g.bn * 128;
 #pragma unroll
-      for (int j = 0; j < 32; ++j) acc[j] = fmaf(left[tr + 4 * j][k], right[k][tc], acc[j]);
-    __syncthreads();
-  }
-  char* out = phase == GRAM ? t.a : phase == POLY ? t.p : t.x[which ^ 1];
+        for (int k = 0; k < 4; ++k) {  // 16 of k: 32 bytes K-major, 16 rows of 128 bytes MN-major
+          const uint32_t ak = a0 + k * (a_mn ? 2048 : 32), bk = b0 + k * (b_mn ? 2048 : 32);
+          const uint64_t ah = tc::sw128_desc(ak, a_mn ? BOX : 16), al = tc::sw128_desc(ak + a_lo, a_mn ? BOX : 16);
+          const uint64_t bh = tc::sw128_desc(bk, b_mn ? BOX : 16), bl = tc::sw128_desc(bk + b_lo, b_mn ? BOX : 16);
+          multiply<PAIR>(d, ah, bh, idesc, kb || k ? 1u : 0u);
+          multiply<PAIR>(d, ah, bl, idesc, 1u);
+          multiply<PAIR>(d, al, bh, idesc, 1u);
+        }
+        if (PAIR)
+          tc::mma_commit_pair(&s.empty[st]);
+        else
+          tc::mma_commit(&s.empty[st]);
+        if (++st == g.stages) { st = 0; ph ^= 1; }
+      }
+      if (PAIR)
+        tc::mma_commit_pair(&s.tfull[acc]);
+      else
+        tc::mma_commit(&s.tfull[acc]);
+    }
+  } else if (warp >= 2) {
+    const int e = warp - 2, q = warp & 3, half = e >> 2;  // TMEM lane quarter, column half
+    const uint32_t lane0 = tmem + ((uint32_t)(q * 32) << 16);
+    const int r = q * 32 + lane;  // of the 128-row block
+    int it = 0;
+    for (int t = unit; t < tiles; t += units, ++it) {
+      const Tile w = tile_at<PAIR>(g, t);
+      const int acc = it & 1, rb = w.rb + rank;
+      const int out = g.phase == GRAM ? w.m.a : g.phase == POLY ? w.m.p : w.m.y, out_nb = g.phase == NEXT ? w.m.nb : 2 * w.m.mb;
+      if (!tc::mbar_wait(&s.tfull[acc], (it >> 1) & 1, g.flags, s.abort_flag)) goto done;
+      tc::fence_after_sync();
+#pragma unroll 1
+      for (int c = half * (cols >> 1); c < (half + 1) * (cols >> 1); c += 32) {
+        uint32_t v[32];
+        tc::tmem_ld32(lane0 + acc * cols + c, v);
+        const int cb = w.cb + (c >> 6);
+        const int64_t at = ((int64_t)rb * out_nb + cb) * BLOCK + chunk_at(r, (c & 63) >> 3);
+        char* to = g.base + (int64_t)out * 128 + at;
+        const char* from = g.base + (int64_t)w.m.a * 128 + at;
+        tc::tmem_wait_ld();
 #pragma unroll
-  for (int j = 0; j < 32; ++j) {
-    const int r = r0 + tr + 4 * j, c = c0 + tc;
-    float v = acc[j] * (1.f / UNIT);
-    if (phase == POLY) v = cc * v + cb * value_at(t.a, sq, r, c) + (r == c ? ca * UNIT : 0.f);
-    char* b = out + (int64_t)block * BLOCK + chunk_at(r & 127, (c & 63) >> 3) + (c & 7) * 2;
-    const __half hi = __float2half_rn(v);
-    *reinterpret_cast<__half*>(b) = hi;
-    *reinterpret_cast<__half*>(b + LIMB) = __float2half_rn(v - __half2float(hi));
+        for (int k = 0; k < 4; ++k) {
+          float f[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) f[j] = __uint_as_float(v[8 * k + j]) * (1.f / UNIT);
+          if (g.phase == POLY) {
+            const uint4 hi = *reinterpret_cast<const uint4*>(from + k * 16), lo = *reinterpret_cast<const uint4*>(from + LIMB + k * 16);
+            const uint32_t hw[4] = {hi.x, hi.y, hi.z, hi.w}, lw[4] = {lo.x, lo.y, lo.z, lo.w};
+            const int diag = rb * 128 + r - (cb * 64 + (c & 63) + 8 * k);  // the diagonal's place among the eight
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float2 x = Pack2<__half>::from(hw[j]), y = Pack2<__half>::from(lw[j]);
+              f[2 * j] = fmaf(g.cc, f[2 * j], g.cb * (x.x + y.x)) + (diag == 2 * j ? g.ca * UNIT : 0.f);
+              f[2 * j + 1] = fmaf(g.cc, f[2 * j + 1], g.cb * (x.y + y.y)) + (diag == 2 * j + 1 ? g.ca * UNIT : 0.f);
+            }
+          }
+          uint4 hi, lo;
+          limbs(f[0], f[1], hi.x, lo.x), limbs(f[2], f[3], hi.y, lo.y), limbs(f[4], f[5], hi.z, lo.z), limbs(f[6], f[7], hi.w, lo.w);
+          *reinterpret_cast<uint4*>(to + k * 16) = hi;
+          *reinterpret_cast<uint4*>(to + LIMB + k * 16) = lo;
+        }
+      }
+      // hands the accumulator back to the MMA warp
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive_cluster(tc::map_to_rank(&s.tempty[acc], 0));
+    }
+    asm volatile("fence.proxy.async;" ::: "memory");  // the next kernel reads them by TMA
   }
+done:
+  __syncwarp();
+  if (*s.abort_flag) {
+    // a wait gave up: what is still in flight (loads, products) lands within
+    // microseconds; nothing may end before that
+    const long long t0 = clock64();
+    while (clock64() - t0 < 4000000) {
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  if (PAIR) tc::cluster_sync();  // nothing of the partner's arrives here any more
+  if (warp == 1) {
+    tc::fence_after_sync();
+    if (PAIR)
+      tc::tmem_dealloc_pair(tmem, 512);
+    else
+      tc::tmem_dealloc(tmem, 256);
+  }
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PRODUCT_THREADS, 1)
+    product_pair_kernel(const __grid_constant__ Product g) {
+  extern __shared__ uint8_t smem_raw[];
+  cudaTriggerProgrammaticLaunchCompletion();
+  products<true>(g, smem_raw);
+}
+__global__ void __launch_bounds__(PRODUCT_THREADS, 1) product_kernel(const __grid_constant__ Product g) {
+  extern __shared__ uint8_t smem_raw[];
+  cudaTriggerProgrammaticLaunchCompletion();
+  products<false>(g, smem_raw);
 }
 
 // ---------------------------------------------------------------- host side
@@ -334,15 +599,65 @@ int64_t size_of(const Shape& s) {
   return m * m * n;
 }
 
-// Places of X's two copies, A and P in a pass's workspace.
-void place(Mat& t, Arena& ar) {
+// X's sides, padded to whole tiles.
+void sides(Mat& t, int bn) {
   t.flip = t.rows > t.cols;
   t.m = std::min(t.rows, t.cols), t.n = std::max(t.rows, t.cols);
-  t.mb = (t.m + 127) / 128, t.nb = (int)up((t.n + 63) / 64, 2);
+  t.mb = (int)up((t.m + 127) / 128, bn ? 1 : 2), t.nb = (int)up((t.n + 63) / 64, bn ? 2 : 4);
+}
+// Places of X's two copies, A and P in a pass's workspace.
+void place(Mat& t, Arena& ar, int bn) {
+  sides(t, bn);
   for (int k = 0; k < 2; ++k) t.x[k] = ar.take<char>((size_t)t.mb * t.nb * BLOCK);
   t.a = ar.take<char>((size_t)t.mb * 2 * t.mb * BLOCK);
   t.p = ar.take<char>((size_t)t.mb * 2 * t.mb * BLOCK);
   t.parts = (int)std::min<int64_t>(PARTS, ((int64_t)t.rows * t.cols + 16 * THREADS - 1) / (16 * THREADS));
+}
+
+// X's and P's tiles, sums in blocks of 64, of one phase.
+int64_t tiles_in(const Mat& t, Phase ph, int bn) {
+  const int64_t side = bn ? t.mb : t.mb / 2, each = bn ? 128 / bn : 1;
+  return ph == NEXT ? side * (t.nb / (bn ? bn / 64 : 4)) : each * side * (side + 1) / 2;
+}
+
+constexpr int SMS = 152;
+int sms_there() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return SMS;
+  return std::max(n, 2);
+}
+
+// A step's clocks on tiles of bn columns (0: pairs): rounds of tiles, each as long
+// as its products take, or its share of what L2 delivers (50 bytes a clock and SM).
+double clocks(const Table& tab, int bn) {
+  double sum = 0;
+  for (Phase ph : {GRAM, POLY, NEXT}) {
+    const int units = bn ? SMS : SMS / 2;
+    double total = 0, longest = 0;
+    int64_t tiles = 0;
+    for (int i = 0; i < tab.count; ++i) {
+      Mat t = tab.mat[i];
+      sides(t, bn);
+      const double len = (ph == GRAM ? t.n : t.m) / 64 + 1;
+      const int64_t k = tiles_in(t, ph, bn);
+      tiles += k, total += k * len, longest = std::max(longest, len);
+    }
+    const double active = (double)std::min<int64_t>(tiles, units) * (bn ? 1 : 2);
+    const double each = std::max(bn ? 6.0 * bn : 1536.0, active * (BLOCK + (bn ? bn : 128) * 256) / (50.0 * SMS));
+    const double rounds = (double)((tiles + units - 1) / units);
+    sum += std::max(rounds * total / tiles, longest) * each + 3000;
+  }
+  return sum;
+}
+
+// The tile of a pass, and every matrix's place in its workspace.
+void place_pass(Table& tab, Arena& ar) {
+  tab.bn = 64;
+  for (int bn : {128, 0})
+    if (clocks(tab, bn) < clocks(tab, tab.bn)) tab.bn = bn;
+  for (int i = 0; i < tab.count; ++i) place(tab.mat[i], ar, tab.bn);
 }
 
 // Matrices in the order of their work, the largest first, MAX_MATS to a pass; every
@@ -372,8 +687,24 @@ gnn_status each_pass(const std::vector<int>& order, void* ws, size_t cap, size_t
   return GNN_OK;
 }
 
-gnn_status run_pass(Table& tab, const Hyper& h, const float* coeffs, int steps, double* partial, float* norms,
-                    cudaStream_t st) {
+gnn_status launch_product(Product& g, const Table& tab, Phase phase, cudaStream_t st) {
+  g.phase = phase;
+  g.first[0] = 0;
+  for (int i = 0; i < tab.count; ++i) g.first[i + 1] = g.first[i] + (int)tiles_in(tab.mat[i], phase, tab.bn);
+  const int tiles = g.first[tab.count];
+  if (tab.bn == 0) {
+    static PerDevice done;
+    GNN_TRY(allow_smem(product_pair_kernel, PRODUCT_SMEM, done));
+    return launch(2 * std::min(tiles, sms_there() / 2), PRODUCT_THREADS, PRODUCT_SMEM, st, product_pair_kernel, g);
+  }
+  static PerDevice done;
+  GNN_TRY(allow_smem(product_kernel, PRODUCT_SMEM, done));
+  return launch(std::min(tiles, sms_there()), PRODUCT_THREADS, PRODUCT_SMEM, st, product_kernel, g);
+}
+
+gnn_status run_pass(void* ws, size_t used, Table& tab, const Hyper& h, const float* coeffs, int steps, double* partial,
+                    float* norms, cudaStream_t st) {
+  if (used / 128 > 0x7fffffff) return fail(GNN_ERR_UNSUPPORTED, "matrices too large together");
   auto blocks = [&](auto&& of) {
     tab.first[0] = 0;
     for (int i = 0; i < tab.count; ++i) tab.first[i + 1] = tab.first[i] + of(tab.mat[i]);
@@ -383,13 +714,24 @@ gnn_status run_pass(Table& tab, const Hyper& h, const float* coeffs, int steps, 
   GNN_TRY(launch(grid, THREADS, 0, st, square_kernel, tab, h, partial));
   grid = blocks([](const Mat& t) { return t.mb * t.nb; });
   GNN_TRY(launch(grid, THREADS, 0, st, begin_kernel, tab, h, (const double*)partial, norms));
-  for (int s = 0; s < steps; ++s) {
-    const float* c = coeffs + 3 * s;
-    grid = blocks([](const Mat& t) { return t.mb * 2 * t.mb; });
-    GNN_TRY(launch(grid, THREADS, 0, st, product_kernel, tab, GRAM, s & 1, c[0], c[1], c[2]));
-    GNN_TRY(launch(grid, THREADS, 0, st, product_kernel, tab, POLY, s & 1, c[0], c[1], c[2]));
-    grid = blocks([](const Mat& t) { return t.mb * t.nb; });
-    GNN_TRY(launch(grid, THREADS, 0, st, product_kernel, tab, NEXT, s & 1, c[0], c[1], c[2]));
+  if (steps) {
+    Product g;
+    g.base = static_cast<char*>(ws);
+    g.flags = device_flags();
+    if (!g.flags) return fail(GNN_ERR_CUDA, "device flag word unavailable");
+    GNN_TRY(encode_tmap_2d(&g.map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, ws, 64, used / 128, 128, 64, 64));
+    g.bn = tab.bn ? tab.bn : 128;
+    g.stages = std::min(MAX_STAGES, RING / (BLOCK + g.bn * 256));
+    g.count = tab.count;
+    auto row = [&](const char* p) { return (int)((p - g.base) / 128); };
+    for (int s = 0; s < steps; ++s) {
+      g.ca = coeffs[3 * s], g.cb = coeffs[3 * s + 1], g.cc = coeffs[3 * s + 2];
+      for (int i = 0; i < tab.count; ++i) {
+        const Mat& t = tab.mat[i];
+        g.mat[i] = {row(t.x[s & 1]), row(t.x[~s & 1]), row(t.a), row(t.p), t.mb, t.nb, (t.n + 63) / 64, (t.m + 63) / 64};
+      }
+      for (Phase ph : {GRAM, POLY, NEXT}) GNN_TRY(launch_product(g, tab, ph, st));
+    }
   }
   grid = blocks([](const Mat& t) { return t.mb * t.nb; });
   return launch(grid, THREADS, 0, st, apply_kernel, tab, h, (const double*)partial, steps & 1);
@@ -441,10 +783,10 @@ extern "C" gnn_status gnn_muon_workspace(const gnn_muon_tensor* tensors, int32_t
     const auto order = order_of(n_tensors, [&](int i) { return Shape{tensors[i].rows, tensors[i].cols}; });
     return each_pass(order, nullptr, 0, ws_bytes, [&](Table& tab, Arena& ar, double*, int k) {
       for (int i = 0; i < tab.count; ++i) {
-        Mat t{};
-        t.rows = tensors[order[k + i]].rows, t.cols = tensors[order[k + i]].cols;
-        place(t, ar);
+        tab.mat[i] = Mat{};
+        tab.mat[i].rows = tensors[order[k + i]].rows, tab.mat[i].cols = tensors[order[k + i]].cols;
       }
+      place_pass(tab, ar);
       return GNN_OK;
     });
   });
@@ -495,9 +837,9 @@ extern "C" gnn_status gnn_muon_step(const gnn_muon_tensor* tensors, int32_t n_te
         Mat& t = tab.mat[i];
         t = Mat{d.param, d.grad, d.m, d.copy, d.ldp, d.ldg, d.ldm, d.ldc, d.scale, d.rows, d.cols};
         t.slot = order[k + i];
-        place(t, ar);
       }
-      return run_pass(tab, h, coeffs, steps, partial, norms, as_stream(stream));
+      place_pass(tab, ar);
+      return run_pass(ws, ar.used, tab, h, coeffs, steps, partial, norms, as_stream(stream));
     });
   });
 }
@@ -508,14 +850,19 @@ extern "C" gnn_status gnn_orthogonalise_workspace(int32_t count, int32_t rows, i
   GNN_TRY(check_shape("gnn_orthogonalise_workspace", 0, rows, cols));
   *ws_bytes = 0;
   if (!rows || !cols || !count) return GNN_OK;
-  Arena ar(nullptr, 0);
-  ar.take<double>((size_t)MAX_MATS * PARTS);
-  for (int i = 0; i < std::min(count, MAX_MATS); ++i) {
-    Mat t{};
-    t.rows = rows, t.cols = cols;
-    place(t, ar);
+  // the last pass may have fewer matrices than the others, and other tiles
+  for (int left : {std::min(count, MAX_MATS), count % MAX_MATS}) {
+    Arena ar(nullptr, 0);
+    ar.take<double>((size_t)MAX_MATS * PARTS);
+    Table tab;
+    tab.count = left;
+    for (int i = 0; i < left; ++i) {
+      tab.mat[i] = Mat{};
+      tab.mat[i].rows = rows, tab.mat[i].cols = cols;
+    }
+    if (left) place_pass(tab, ar);
+    *ws_bytes = std::max(*ws_bytes, ar.used);
   }
-  *ws_bytes = ar.used;
   return GNN_OK;
 }
 
@@ -553,9 +900,9 @@ extern "C" gnn_status gnn_orthogonalise(const void* X, int64_t ldx, int64_t stri
         t = Mat{static_cast<char*>(O) + (k + i) * stride_o * os, static_cast<const char*>(X) + (k + i) * stride_x * xs, nullptr,
                 nullptr, ldo, ldx, 0, 0, 1.f, rows, cols};
         t.slot = k + i;
-        place(t, ar);
       }
-      return run_pass(tab, h, coeffs, steps, partial, norms, as_stream(stream));
+      place_pass(tab, ar);
+      return run_pass(ws, ar.used, tab, h, coeffs, steps, partial, norms, as_stream(stream));
     });
   });
 }
