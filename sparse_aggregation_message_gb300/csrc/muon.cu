@@ -96,11 +96,20 @@ __device__ __forceinline__ int mat_of(const Table& tab, int k) {
   return i;
 }
 
-// Sums of u^2 over a share of a matrix's rows.
-__global__ void __launch_bounds__(THREADS) square_kernel(const __grid_constant__ Table tab, const Hyper h, double* partial) {
+// Warps that have finished their share of a tile, by matrix and product.
+struct Done {
+  int of[4];
+};
+constexpr int DONE_WORDS = MAX_MATS * 4;
+
+// Sums of u^2 over a share of a matrix's rows; the counts of the steps start at zero.
+__global__ void __launch_bounds__(THREADS) square_kernel(const __grid_constant__ Table tab, const Hyper h, double* partial,
+                                                         int* done) {
   __shared__ double sm[THREADS / 32];
   cudaTriggerProgrammaticLaunchCompletion();
   cudaGridDependencySynchronize();
+  if (blockIdx.x == 0)
+    for (int k = threadIdx.x; k < DONE_WORDS; k += THREADS) done[k] = 0;
   const int i = mat_of(tab, blockIdx.x);
   const Mat& t = tab.mat[i];
   const int part = blockIdx.x - tab.first[i];
@@ -251,15 +260,28 @@ __global__ void __launch_bounds__(THREADS) apply_kernel(const __grid_constant__ 
 // ------------------------------------------------------------------ products
 enum Phase { GRAM, POLY, NEXT };  // A = X X', P = a I + b A + c A A, X <- P X
 
-// One product of every matrix of a pass, by persistent, warp-specialised blocks: warp
-// 0 loads a ring of tiles by TMA, warp 1 issues the MMAs from one thread, warps 2-9
-// drain one of two accumulators in TMEM while the next tile is multiplied.  A tile
-// is 128 x bn on one CTA, or 256 x 256 on a pair of CTAs (cta_group::2), which reads
-// a third less from L2 for its flops.
+// Every product of every step in one launch of persistent, warp-specialised blocks:
+// warp 0 loads a ring of tiles by TMA, warp 1 issues the MMAs from one thread, warps
+// 2-9 drain one of two accumulators in TMEM while the next tile is multiplied.  A
+// tile is 128 x 64 or 128 x 128 on one CTA, or 256 x 256 on a pair of CTAs
+// (cta_group::2), which reads a third less from L2 for its flops.  Tiles are dealt in
+// the order step, product, matrix; before a tile's first load its matrix's counts of
+// the product before are waited for, so a matrix goes on when its own tiles are
+// there, and no launch or barrier of the whole card comes between products.
 //
 // A and P are symmetric: only their blocks on and above the diagonal (of the tile's
 // size) are formed, and a block below is read as the transpose of its mirror image,
 // by loading that and setting the operand's major bit in the instruction.
+//
+// The tensor cores truncate at every 16 of k: a product's bits below 2^-25 of the
+// largest term, and the sum's below its last place (measured on sums of powers of
+// two).  Over a whole row of k that loss, of one sign with the sum, is what the result
+// would be off by (4.7e-6 of its norm for 64 x 256, 1.7e-5 for 1000 x 1000, where fp32
+// FMAs leave 1.3e-6 and 2.6e-6).  So an accumulator holds 64 of k only, the cross
+// products first, while it is small; warps 2-9 add it, rounded, to the tile's sums in
+// their registers, and put back what is lost on average, one unit in 2^23 where three
+// or four sums of 16 are in it: 1.7e-6 and 1.0e-6 (without that 2.6e-6 and 1.5e-6;
+// 128 of k: 2.4e-6 and 2.3e-6).
 constexpr int BOX = 64 * 128;  // 64 rows of 128 bytes: what one TMA load brings
 constexpr int BLOCK_ROWS = BLOCK / 128;
 constexpr int EPI_WARPS = 8;
@@ -270,20 +292,18 @@ constexpr int PRODUCT_SMEM = RING + 1024 /*barriers*/ + 1024 /*align*/;
 
 // A matrix's operands by their first row of the workspace, which has 128-byte rows.
 struct Rows {
-  int x, y, a, p;  // X now and next
+  int x0, x1, a, p;
   int mb, nb;
-  int kx, km;      // blocks of 64 with values: of X's columns, of its rows
+  int kx, km;  // 16s of k with values: of X's columns, of its rows
 };
-struct Product {
+struct Steps {
   CUtensorMap map;
   char* base;
+  Done* done;
   unsigned* flags;
-  Phase phase;
-  int bn;      // columns of a CTA's share of B
-  int stages;
-  int count;
-  float ca, cb, cc;
-  int first[MAX_MATS + 1];  // tiles before each matrix
+  int count, steps;
+  float coeff[MAX_STEPS][3];
+  int first[3][MAX_MATS + 1];  // a step's tiles before each matrix of each product
   Rows mat[MAX_MATS];
 };
 
@@ -306,38 +326,86 @@ __device__ __forceinline__ Ring carve(uint8_t* raw) {
   return s;
 }
 
-// A tile: its matrix, the first 128-row block and the first 64-column block of the
-// pair's (or the CTA's), and the length of its sum in blocks of 64.
+// A tile: its step, product and matrix, the first 128-row block and the first
+// 64-column block of the pair's (or the CTA's), and the length of its sum in 16s and
+// in blocks of 64.
 struct Tile {
   Rows m;
-  int rb, cb, kb;
+  int step, phase, mat;
+  int rb, cb, k16, kb;
 };
-template <bool PAIR>
-__device__ __forceinline__ Tile tile_at(const Product& g, int t) {
-  int i = 0;
-  while (i + 1 < g.count && t >= g.first[i + 1]) ++i;
-  t -= g.first[i];
+template <int COLS>
+__device__ __forceinline__ Tile tile_at(const Steps& g, int t) {
+  constexpr bool PAIR = COLS == 256;
+  const int n0 = g.first[0][g.count], n1 = g.first[1][g.count], each_step = n0 + n1 + g.first[2][g.count];
   Tile r;
-  r.m = g.mat[i];
-  const int side = PAIR ? r.m.mb >> 1 : r.m.mb, wide = (PAIR ? 256 : g.bn) >> 6;  // tile rows; blocks of 64 across
-  if (g.phase == NEXT) {
+  r.step = t / each_step;
+  t -= r.step * each_step;
+  r.phase = t < n0 ? GRAM : t < n0 + n1 ? POLY : NEXT;
+  t -= r.phase == GRAM ? 0 : r.phase == POLY ? n0 : n0 + n1;
+  const int* first = g.first[r.phase];
+  int lo = 0, hi = g.count - 1;  // the last matrix that begins at t or before
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (first[mid] <= t)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  t -= first[lo];
+  r.mat = lo;
+  r.m = g.mat[lo];
+  constexpr int wide = COLS >> 6;  // blocks of 64 across
+  const int side = PAIR ? r.m.mb >> 1 : r.m.mb;
+  if (r.phase == NEXT) {
     // the tiles that share columns of X side by side
     r.rb = t % side;
     r.cb = t / side * wide;
-  } else {
-    const int each = (PAIR ? 4 : 2) / wide;  // tiles of a square of the diagonal's size
+  } else if (COLS == 64) {
+    // columns to the last with values
+    const int cols = (r.m.km + 3) >> 2;
     int row = 0;
-    while (t >= each * (side - row)) t -= each * (side - row), ++row;
+    while (t >= cols - 2 * row) t -= cols - 2 * row, ++row;
     r.rb = row;
-    r.cb = row * each * wide + t * wide;
+    r.cb = 2 * row + t;
+  } else {
+    int row = 0;
+    while (t >= side - row) t -= side - row, ++row;
+    r.rb = row;
+    r.cb = (row + t) * wide;
   }
   if (PAIR) r.rb *= 2;
-  r.kb = g.phase == GRAM ? r.m.kx : r.m.km;
+  r.k16 = r.phase == GRAM ? r.m.kx : r.m.km;
+  r.kb = (r.k16 + 3) >> 2;
   return r;
 }
-template <bool PAIR>
-__device__ __forceinline__ int tiles_of(const Product& g) {
-  return g.first[g.count];
+template <int COLS>
+__device__ __forceinline__ int tiles_of(const Steps& g) {
+  return g.steps * (g.first[0][g.count] + g.first[1][g.count] + g.first[2][g.count]);
+}
+
+// Waits until what a tile reads has been written: the product before, of its matrix.
+// False after the time limit or once another role has given up.
+template <int COLS>
+__device__ __forceinline__ bool wait_for(const Steps& g, const Tile& w, volatile int* abort_flag) {
+  const int before = w.phase == GRAM ? NEXT : w.phase - 1;
+  const int times = w.phase == GRAM ? w.step : w.step + 1;
+  const int need = times * (g.first[before][w.mat + 1] - g.first[before][w.mat]) * (COLS == 256 ? 16 : 8);
+  const int* at = &g.done[w.mat].of[before];
+  int have;
+  asm volatile("ld.acquire.gpu.global.b32 %0, [%1];" : "=r"(have) : "l"(at) : "memory");
+  if (have >= need) return true;
+  const long long t0 = clock64();
+  while (true) {
+    asm volatile("ld.acquire.gpu.global.b32 %0, [%1];" : "=r"(have) : "l"(at) : "memory");
+    if (have >= need) return true;
+    if (*abort_flag) return false;
+    if (clock64() - t0 > tc::kWaitCycles) {
+      atomicOr(g.flags, 2u);
+      *abort_flag = 1;
+      return false;
+    }
+  }
 }
 
 // Whether rows of 128-row block b, columns of 64-block kb lie on or above the
@@ -348,7 +416,7 @@ __device__ __forceinline__ bool above(int b, int kb) {
 }
 
 template <bool PAIR>
-__device__ __forceinline__ void load_box(const Product& g, uint8_t* to, uint32_t bar, uint64_t* local, int row) {
+__device__ __forceinline__ void load_box(const Steps& g, uint8_t* to, uint32_t bar, uint64_t* local, int row) {
   if (PAIR)
     tc::tma_load_2d_pair(to, &g.map, bar, 0, row);
   else
@@ -359,7 +427,7 @@ __device__ __forceinline__ void load_box(const Product& g, uint8_t* to, uint32_t
 // row `s`, at k block kb: as they lie (K-major), or, below the diagonal, the mirror image's
 // columns (MN-major).
 template <bool PAIR>
-__device__ __forceinline__ void load_rows(const Product& g, uint8_t* to, uint32_t bar, uint64_t* local, int s, int nb, int r64,
+__device__ __forceinline__ void load_rows(const Steps& g, uint8_t* to, uint32_t bar, uint64_t* local, int s, int nb, int r64,
                                           int kb, int boxes, bool direct) {
   for (int l = 0; l < 2; ++l) {
     for (int h = 0; h < boxes; ++h, to += BOX) {
@@ -378,16 +446,19 @@ __device__ __forceinline__ void multiply(uint32_t d, uint64_t a, uint64_t b, uin
     tc::mma_bf16(d, a, b, idesc, acc);
 }
 
-template <bool PAIR>
-__device__ __forceinline__ void products(const Product& g, uint8_t* smem_raw) {
+// COLS: of a tile; 256: a pair's.
+template <int COLS>
+__device__ __forceinline__ void walk(const Steps& g, uint8_t* smem_raw) {
+  constexpr bool PAIR = COLS == 256;
   const Ring s = carve(smem_raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = PAIR ? (int)tc::cluster_rank() : 0;
   const int unit = PAIR ? blockIdx.x >> 1 : blockIdx.x, units = PAIR ? gridDim.x >> 1 : gridDim.x;
-  const int a_stage = BLOCK, stage = BLOCK + g.bn * 256, cols = PAIR ? 256 : g.bn;
+  constexpr int bn = PAIR ? 128 : COLS;  // columns of a CTA's share of B
+  constexpr int a_stage = BLOCK, stage = BLOCK + bn * 256, stages = RING / stage < MAX_STAGES ? RING / stage : MAX_STAGES;
   if (warp == 0 && lane == 0) tc::prefetch_tmap(&g.map);
   if (threadIdx.x == 0) {
-    for (int i = 0; i < g.stages; ++i) {
+    for (int i = 0; i < stages; ++i) {
       tc::mbar_init(&s.full[i], 1);
       tc::mbar_init(&s.empty[i], 1);
     }
@@ -411,124 +482,160 @@ __device__ __forceinline__ void products(const Product& g, uint8_t* smem_raw) {
   __syncthreads();
   if (PAIR) tc::cluster_sync();  // the partner's barriers are there
   tc::fence_after_sync();
-  cudaGridDependencySynchronize();
   const uint32_t tmem = *s.tmem;
-  const int tiles = tiles_of<PAIR>(g);
+  const int tiles = tiles_of<COLS>(g);
 
   if (warp == 0 && lane == 0) {
-    // what ordinary stores of the kernels before wrote is read by TMA
-    asm volatile("fence.proxy.async;" ::: "memory");
     int st = 0;
     uint32_t ph = 0;
     for (int t = unit; t < tiles; t += units) {
-      const Tile w = tile_at<PAIR>(g, t);
-      const int sq = 2 * w.m.mb;
-      const int left = g.phase == GRAM ? w.m.x : g.phase == POLY ? w.m.a : w.m.p, left_nb = g.phase == GRAM ? w.m.nb : sq;
-      const int rb = w.rb + rank, cb = w.cb + rank * (g.bn >> 6);
+      const Tile w = tile_at<COLS>(g, t);
+      const int x = w.step & 1 ? w.m.x1 : w.m.x0, sq = 2 * w.m.mb;
+      const int left = w.phase == GRAM ? x : w.phase == POLY ? w.m.a : w.m.p, left_nb = w.phase == GRAM ? w.m.nb : sq;
+      const int rb = w.rb + rank, cb = w.cb + rank * (bn >> 6);
+      if (!wait_for<COLS>(g, w, s.abort_flag)) goto done;
+      // what ordinary stores wrote is read by TMA
+      asm volatile("fence.proxy.async;" ::: "memory");
       for (int kb = 0; kb < w.kb; ++kb) {
         if (!tc::mbar_wait(&s.empty[st], ph ^ 1, g.flags, s.abort_flag)) goto done;
         if (rank == 0) tc::mbar_expect_tx(&s.full[st], (PAIR ? 2 : 1) * stage);
         uint8_t* a = s.tiles + st * stage;
         const uint32_t bar = PAIR ? tc::map_to_rank(&s.full[st], 0) : 0;
-        load_rows<PAIR>(g, a, bar, &s.full[st], left, left_nb, 2 * rb, kb, 2, g.phase == GRAM || above<PAIR>(rb, kb));
-        if (g.phase == NEXT)
-          load_rows<PAIR>(g, a + a_stage, bar, &s.full[st], w.m.x, w.m.nb, cb, kb, g.bn >> 6, false);
+        load_rows<PAIR>(g, a, bar, &s.full[st], left, left_nb, 2 * rb, kb, 2, w.phase == GRAM || above<PAIR>(rb, kb));
+        if (w.phase == NEXT)
+          load_rows<PAIR>(g, a + a_stage, bar, &s.full[st], x, w.m.nb, cb, kb, bn >> 6, false);
         else
-          load_rows<PAIR>(g, a + a_stage, bar, &s.full[st], left, left_nb, cb, kb, g.bn >> 6,
-                          g.phase == GRAM || above<PAIR>(cb >> 1, kb));
-        if (++st == g.stages) { st = 0; ph ^= 1; }
+          load_rows<PAIR>(g, a + a_stage, bar, &s.full[st], left, left_nb, cb, kb, bn >> 6,
+                          w.phase == GRAM || above<PAIR>(cb >> 1, kb));
+        if (++st == stages) { st = 0; ph ^= 1; }
       }
     }
     // every stage's release has arrived before this CTA may end
-    for (int i = 0; i < g.stages; ++i) {
+    for (int i = 0; i < stages; ++i) {
       if (!tc::mbar_wait(&s.empty[st], ph ^ 1, g.flags, s.abort_flag)) goto done;
-      if (++st == g.stages) { st = 0; ph ^= 1; }
+      if (++st == stages) { st = 0; ph ^= 1; }
     }
   } else if (warp == 1 && lane == 0 && rank == 0) {
     int st = 0, it = 0;
     uint32_t ph = 0;
-    for (int t = unit; t < tiles; t += units, ++it) {
-      const Tile w = tile_at<PAIR>(g, t);
-      const int acc = it & 1;
-      if (!tc::mbar_wait<true>(&s.tempty[acc], ((it >> 1) & 1) ^ 1, g.flags, s.abort_flag)) goto done;
-      tc::fence_after_sync();
-      const uint32_t d = tmem + acc * cols;
-      for (int kb = 0; kb < w.kb; ++kb) {
-        const bool a_mn = g.phase != GRAM && !above<PAIR>(w.rb, kb);
-        const bool b_mn = g.phase == NEXT || (g.phase == POLY && !above<PAIR>(w.cb >> 1, kb));
-        const uint32_t idesc = tc::idesc_16(false, PAIR ? 256 : 128, cols, a_mn, b_mn);
+    for (int t = unit; t < tiles; t += units) {
+      const Tile w = tile_at<COLS>(g, t);
+      for (int kb = 0; kb < w.kb; ++kb, ++it) {
+        const int acc = it & 1, some = min(w.k16 - 4 * kb, 4);
+        const uint32_t d = tmem + acc * COLS;
+        const bool a_mn = w.phase != GRAM && !above<PAIR>(w.rb, kb);
+        const bool b_mn = w.phase == NEXT || (w.phase == POLY && !above<PAIR>(w.cb >> 1, kb));
+        const uint32_t idesc = tc::idesc_16(false, PAIR ? 256 : 128, COLS, a_mn, b_mn);
+        if (!tc::mbar_wait<true>(&s.tempty[acc], ((it >> 1) & 1) ^ 1, g.flags, s.abort_flag)) goto done;
         if (!tc::mbar_wait(&s.full[st], ph, g.flags, s.abort_flag)) goto done;
         tc::fence_after_sync();
         const uint32_t a0 = tc::smem_u32(s.tiles + st * stage), b0 = a0 + a_stage;
-        const uint32_t a_lo = LIMB, b_lo = g.bn * 128;
+        // 16 of k: 32 bytes K-major, 16 rows of 128 bytes MN-major
+        auto left = [&](int k, int limb) {
+          return tc::sw128_desc(a0 + limb * LIMB + k * (a_mn ? 2048 : 32), a_mn ? BOX : 16);
+        };
+        auto right = [&](int k, int limb) {
+          return tc::sw128_desc(b0 + limb * bn * 128 + k * (b_mn ? 2048 : 32), b_mn ? BOX : 16);
+        };
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {  // 16 of k: 32 bytes K-major, 16 rows of 128 bytes MN-major
-          const uint32_t ak = a0 + k * (a_mn ? 2048 : 32), bk = b0 + k * (b_mn ? 2048 : 32);
-          const uint64_t ah = tc::sw128_desc(ak, a_mn ? BOX : 16), al = tc::sw128_desc(ak + a_lo, a_mn ? BOX : 16);
-          const uint64_t bh = tc::sw128_desc(bk, b_mn ? BOX : 16), bl = tc::sw128_desc(bk + b_lo, b_mn ? BOX : 16);
-          multiply<PAIR>(d, ah, bh, idesc, kb || k ? 1u : 0u);
-          multiply<PAIR>(d, ah, bl, idesc, 1u);
-          multiply<PAIR>(d, al, bh, idesc, 1u);
+        for (int k = 0; k < 4; ++k) {
+          if (k >= some) break;
+          multiply<PAIR>(d, left(k, 0), right(k, 1), idesc, k ? 1u : 0u);
+          multiply<PAIR>(d, left(k, 1), right(k, 0), idesc, 1u);
         }
-        if (PAIR)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (k >= some) break;
+          multiply<PAIR>(d, left(k, 0), right(k, 0), idesc, 1u);
+        }
+        if (PAIR) {
           tc::mma_commit_pair(&s.empty[st]);
-        else
+          tc::mma_commit_pair(&s.tfull[acc]);
+        } else {
           tc::mma_commit(&s.empty[st]);
-        if (++st == g.stages) { st = 0; ph ^= 1; }
+          tc::mma_commit(&s.tfull[acc]);
+        }
+        if (++st == stages) { st = 0; ph ^= 1; }
       }
-      if (PAIR)
-        tc::mma_commit_pair(&s.tfull[acc]);
-      else
-        tc::mma_commit(&s.tfull[acc]);
     }
   } else if (warp >= 2) {
     const int e = warp - 2, q = warp & 3, half = e >> 2;  // TMEM lane quarter, column half
     const uint32_t lane0 = tmem + ((uint32_t)(q * 32) << 16);
     const int r = q * 32 + lane;  // of the 128-row block
+    constexpr int MINE = COLS / 2;  // columns of this warp's half
+    const uint32_t freed0 = tc::map_to_rank(&s.tempty[0], 0), freed1 = tc::map_to_rank(&s.tempty[1], 0);
     int it = 0;
-    for (int t = unit; t < tiles; t += units, ++it) {
-      const Tile w = tile_at<PAIR>(g, t);
-      const int acc = it & 1, rb = w.rb + rank;
-      const int out = g.phase == GRAM ? w.m.a : g.phase == POLY ? w.m.p : w.m.y, out_nb = g.phase == NEXT ? w.m.nb : 2 * w.m.mb;
-      if (!tc::mbar_wait(&s.tfull[acc], (it >> 1) & 1, g.flags, s.abort_flag)) goto done;
-      tc::fence_after_sync();
-#pragma unroll 1
-      for (int c = half * (cols >> 1); c < (half + 1) * (cols >> 1); c += 32) {
-        uint32_t v[32];
-        tc::tmem_ld32(lane0 + acc * cols + c, v);
-        const int cb = w.cb + (c >> 6);
-        const int64_t at = ((int64_t)rb * out_nb + cb) * BLOCK + chunk_at(r, (c & 63) >> 3);
+    for (int t = unit; t < tiles; t += units) {
+      const Tile w = tile_at<COLS>(g, t);
+      const int rb = w.rb + rank, row = rb * 128 + r;
+      const int out = w.phase == GRAM ? w.m.a : w.phase == POLY ? w.m.p : w.step & 1 ? w.m.x0 : w.m.x1;
+      const int out_nb = w.phase == NEXT ? w.m.nb : 2 * w.m.mb;
+      const float ca = g.coeff[w.step][0], cb_ = g.coeff[w.step][1], cc = g.coeff[w.step][2];
+      // this thread's place on P's diagonal, from the first column of its half
+      const int on_diag = row - (w.cb * 64 + half * MINE);
+      if (w.phase == POLY) {  // A, by ordinary loads
+        if (lane == 0 && !wait_for<COLS>(g, w, s.abort_flag)) goto done;
+        __syncwarp();
+      }
+      float2 sum[MINE / 2];
+#pragma unroll
+      for (int j = 0; j < MINE / 2; ++j) sum[j] = dup2(0.f);
+      for (int kb = 0; kb < w.kb; ++kb, ++it) {
+        const int acc = it & 1;
+        const float2 back = dup2(w.k16 - 4 * kb > 2 ? 1.f + 0x1p-23f : 1.f);
+        if (!tc::mbar_wait(&s.tfull[acc], (it >> 1) & 1, g.flags, s.abort_flag)) goto done;
+        tc::fence_after_sync();
+#pragma unroll
+        for (int c = 0; c < MINE; c += 32) {
+          uint32_t v[32];
+          tc::tmem_ld32(lane0 + acc * COLS + half * MINE + c, v);
+          tc::tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            sum[c / 2 + j] = fma2_rn(back, make_float2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1])), sum[c / 2 + j]);
+        }
+        // hands the accumulator back to the MMA warp
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive_cluster(acc ? freed1 : freed0);
+      }
+#pragma unroll
+      for (int c = 0; c < MINE; c += 32) {
+        const int col = half * MINE + c, cb = w.cb + (col >> 6);
+        const int64_t at = ((int64_t)rb * out_nb + cb) * BLOCK + chunk_at(r, (col & 63) >> 3);
         char* to = g.base + (int64_t)out * 128 + at;
         const char* from = g.base + (int64_t)w.m.a * 128 + at;
-        tc::tmem_wait_ld();
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          float f[8];
+          float2 f[4];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) f[j] = __uint_as_float(v[8 * k + j]) * (1.f / UNIT);
-          if (g.phase == POLY) {
-            const uint4 hi = *reinterpret_cast<const uint4*>(from + k * 16), lo = *reinterpret_cast<const uint4*>(from + LIMB + k * 16);
+          for (int j = 0; j < 4; ++j) f[j] = mul2_rn(sum[c / 2 + 4 * k + j], dup2(1.f / UNIT));
+          if (w.phase == POLY) {
+            const int diag = on_diag - (c + 8 * k);  // the diagonal's place among the eight
+            const uint4 hi = __ldcg(reinterpret_cast<const uint4*>(from + k * 16)),
+                        lo = __ldcg(reinterpret_cast<const uint4*>(from + LIMB + k * 16));
             const uint32_t hw[4] = {hi.x, hi.y, hi.z, hi.w}, lw[4] = {lo.x, lo.y, lo.z, lo.w};
-            const int diag = rb * 128 + r - (cb * 64 + (c & 63) + 8 * k);  // the diagonal's place among the eight
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              const float2 x = Pack2<__half>::from(hw[j]), y = Pack2<__half>::from(lw[j]);
-              f[2 * j] = fmaf(g.cc, f[2 * j], g.cb * (x.x + y.x)) + (diag == 2 * j ? g.ca * UNIT : 0.f);
-              f[2 * j + 1] = fmaf(g.cc, f[2 * j + 1], g.cb * (x.y + y.y)) + (diag == 2 * j + 1 ? g.ca * UNIT : 0.f);
+              const float2 a = add2_rn(Pack2<__half>::from(hw[j]), Pack2<__half>::from(lw[j]));
+              f[j] = fma2_rn(dup2(cc), f[j], mul2_rn(dup2(cb_), a));
+              if (diag == 2 * j) f[j].x += ca * UNIT;
+              if (diag == 2 * j + 1) f[j].y += ca * UNIT;
             }
           }
           uint4 hi, lo;
-          limbs(f[0], f[1], hi.x, lo.x), limbs(f[2], f[3], hi.y, lo.y), limbs(f[4], f[5], hi.z, lo.z), limbs(f[6], f[7], hi.w, lo.w);
+          limbs(f[0].x, f[0].y, hi.x, lo.x), limbs(f[1].x, f[1].y, hi.y, lo.y);
+          limbs(f[2].x, f[2].y, hi.z, lo.z), limbs(f[3].x, f[3].y, hi.w, lo.w);
           *reinterpret_cast<uint4*>(to + k * 16) = hi;
           *reinterpret_cast<uint4*>(to + LIMB + k * 16) = lo;
         }
       }
-      // hands the accumulator back to the MMA warp
-      tc::fence_before_sync();
+      // the tile's readers, through TMA too, see what this warp wrote
+      asm volatile("fence.proxy.async;" ::: "memory");
       __syncwarp();
-      if (lane == 0) tc::mbar_arrive_cluster(tc::map_to_rank(&s.tempty[acc], 0));
+      if (lane == 0)
+        asm volatile("red.release.gpu.global.add.s32 [%0], 1;" ::"l"(&g.done[w.mat].of[w.phase]) : "memory");
     }
-    asm volatile("fence.proxy.async;" ::: "memory");  // the next kernel reads them by TMA
   }
 done:
   __syncwarp();
@@ -552,15 +659,14 @@ done:
 }
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PRODUCT_THREADS, 1)
-    product_pair_kernel(const __grid_constant__ Product g) {
+    steps_pair_kernel(const __grid_constant__ Steps g) {
   extern __shared__ uint8_t smem_raw[];
-  cudaTriggerProgrammaticLaunchCompletion();
-  products<true>(g, smem_raw);
+  walk<256>(g, smem_raw);
 }
-__global__ void __launch_bounds__(PRODUCT_THREADS, 1) product_kernel(const __grid_constant__ Product g) {
+template <int COLS>
+__global__ void __launch_bounds__(PRODUCT_THREADS, 1) steps_kernel(const __grid_constant__ Steps g) {
   extern __shared__ uint8_t smem_raw[];
-  cudaTriggerProgrammaticLaunchCompletion();
-  products<false>(g, smem_raw);
+  walk<COLS>(g, smem_raw);
 }
 
 // ---------------------------------------------------------------- host side
@@ -576,8 +682,14 @@ gnn_status launch(int64_t grid, int block, size_t smem, cudaStream_t st, void (*
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
+  if (smem == PRODUCT_SMEM) {
+    // its blocks wait on one another: all are there, or none starts
+    at[0].id = cudaLaunchAttributeCooperative;
+    at[0].val.cooperative = 1;
+  } else {
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+  }
   cfg.attrs = at;
   cfg.numAttrs = 1;
   count_launch();
@@ -614,10 +726,11 @@ void place(Mat& t, Arena& ar, int bn) {
   t.parts = (int)std::min<int64_t>(PARTS, ((int64_t)t.rows * t.cols + 16 * THREADS - 1) / (16 * THREADS));
 }
 
-// X's and P's tiles, sums in blocks of 64, of one phase.
+// A matrix's tiles of one product.
 int64_t tiles_in(const Mat& t, Phase ph, int bn) {
-  const int64_t side = bn ? t.mb : t.mb / 2, each = bn ? 128 / bn : 1;
-  return ph == NEXT ? side * (t.nb / (bn ? bn / 64 : 4)) : each * side * (side + 1) / 2;
+  const int64_t side = bn ? t.mb : t.mb / 2, km = (t.m + 63) / 64, kx = (t.n + 63) / 64;
+  if (ph == NEXT) return side * (bn == 64 ? kx : bn ? t.nb / 2 : t.nb / 4);
+  return bn == 64 ? side * km - side * (side - 1) : side * (side + 1) / 2;
 }
 
 constexpr int SMS = 152;
@@ -679,31 +792,31 @@ gnn_status each_pass(const std::vector<int>& order, void* ws, size_t cap, size_t
   for (size_t k = 0; k < order.size(); k += MAX_MATS) {
     Arena ar(ws, cap);
     double* partial = ar.take<double>((size_t)MAX_MATS * PARTS);
+    Done* done = ar.take<Done>(MAX_MATS);
     Table tab;
     tab.count = (int)std::min<size_t>(MAX_MATS, order.size() - k);
-    GNN_TRY(fill(tab, ar, partial, (int)k));
+    GNN_TRY(fill(tab, ar, partial, done, (int)k));
     *need = std::max(*need, ar.used);
   }
   return GNN_OK;
 }
 
-gnn_status launch_product(Product& g, const Table& tab, Phase phase, cudaStream_t st) {
-  g.phase = phase;
-  g.first[0] = 0;
-  for (int i = 0; i < tab.count; ++i) g.first[i + 1] = g.first[i] + (int)tiles_in(tab.mat[i], phase, tab.bn);
-  const int tiles = g.first[tab.count];
-  if (tab.bn == 0) {
-    static PerDevice done;
-    GNN_TRY(allow_smem(product_pair_kernel, PRODUCT_SMEM, done));
-    return launch(2 * std::min(tiles, sms_there() / 2), PRODUCT_THREADS, PRODUCT_SMEM, st, product_pair_kernel, g);
-  }
-  static PerDevice done;
-  GNN_TRY(allow_smem(product_kernel, PRODUCT_SMEM, done));
-  return launch(std::min(tiles, sms_there()), PRODUCT_THREADS, PRODUCT_SMEM, st, product_kernel, g);
+gnn_status launch_steps(const Steps& g, int bn, cudaStream_t st) {
+  const int64_t tiles = (int64_t)g.steps * (g.first[0][g.count] + g.first[1][g.count] + g.first[2][g.count]);
+  const int widest = std::max(std::max(g.first[0][g.count], g.first[1][g.count]), g.first[2][g.count]);
+  if (tiles > 0x3fffffff) return fail(GNN_ERR_UNSUPPORTED, "too many tiles in one call");
+  const int units = std::min(widest, bn ? sms_there() : sms_there() / 2);
+  auto run = [&](auto* k, PerDevice& done, int grid) -> gnn_status {
+    GNN_TRY(allow_smem(k, PRODUCT_SMEM, done));
+    return launch(grid, PRODUCT_THREADS, PRODUCT_SMEM, st, k, g);
+  };
+  static PerDevice done0, done64, done128;
+  if (bn == 0) return run(steps_pair_kernel, done0, 2 * units);
+  return bn == 64 ? run(steps_kernel<64>, done64, units) : run(steps_kernel<128>, done128, units);
 }
 
 gnn_status run_pass(void* ws, size_t used, Table& tab, const Hyper& h, const float* coeffs, int steps, double* partial,
-                    float* norms, cudaStream_t st) {
+                    Done* done, float* norms, cudaStream_t st) {
   if (used / 128 > 0x7fffffff) return fail(GNN_ERR_UNSUPPORTED, "matrices too large together");
   auto blocks = [&](auto&& of) {
     tab.first[0] = 0;
@@ -711,27 +824,33 @@ gnn_status run_pass(void* ws, size_t used, Table& tab, const Hyper& h, const flo
     return tab.first[tab.count];
   };
   int grid = blocks([](const Mat& t) { return t.parts; });
-  GNN_TRY(launch(grid, THREADS, 0, st, square_kernel, tab, h, partial));
+  GNN_TRY(launch(grid, THREADS, 0, st, square_kernel, tab, h, partial, &done->of[0]));
   grid = blocks([](const Mat& t) { return t.mb * t.nb; });
   GNN_TRY(launch(grid, THREADS, 0, st, begin_kernel, tab, h, (const double*)partial, norms));
   if (steps) {
-    Product g;
+    Steps g;
     g.base = static_cast<char*>(ws);
+    g.done = done;
     g.flags = device_flags();
     if (!g.flags) return fail(GNN_ERR_CUDA, "device flag word unavailable");
     GNN_TRY(encode_tmap_2d(&g.map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, ws, 64, used / 128, 128, 64, 64));
-    g.bn = tab.bn ? tab.bn : 128;
-    g.stages = std::min(MAX_STAGES, RING / (BLOCK + g.bn * 256));
-    g.count = tab.count;
-    auto row = [&](const char* p) { return (int)((p - g.base) / 128); };
-    for (int s = 0; s < steps; ++s) {
-      g.ca = coeffs[3 * s], g.cb = coeffs[3 * s + 1], g.cc = coeffs[3 * s + 2];
-      for (int i = 0; i < tab.count; ++i) {
-        const Mat& t = tab.mat[i];
-        g.mat[i] = {row(t.x[s & 1]), row(t.x[~s & 1]), row(t.a), row(t.p), t.mb, t.nb, (t.n + 63) / 64, (t.m + 63) / 64};
-      }
-      for (Phase ph : {GRAM, POLY, NEXT}) GNN_TRY(launch_product(g, tab, ph, st));
+    g.count = tab.count, g.steps = steps;
+    for (int s = 0; s < steps; ++s)
+      for (int k = 0; k < 3; ++k) g.coeff[s][k] = coeffs[3 * s + k];
+    auto row = [&](const void* p) { return (int)((static_cast<const char*>(p) - g.base) / 128); };
+    for (int i = 0; i < tab.count; ++i) {
+      const Mat& t = tab.mat[i];
+      g.mat[i] = {row(t.x[0]), row(t.x[1]), row(t.a), row(t.p), t.mb, t.nb, (t.n + 15) / 16, (t.m + 15) / 16};
     }
+    for (Phase ph : {GRAM, POLY, NEXT}) {
+      int64_t sum = 0;
+      for (int i = 0; i <= tab.count; ++i) {
+        if (sum > 0x3fffffff) return fail(GNN_ERR_UNSUPPORTED, "too many tiles in one call");
+        g.first[ph][i] = (int)sum;
+        if (i < tab.count) sum += tiles_in(tab.mat[i], ph, tab.bn);
+      }
+    }
+    GNN_TRY(launch_steps(g, tab.bn, st));
   }
   grid = blocks([](const Mat& t) { return t.mb * t.nb; });
   return launch(grid, THREADS, 0, st, apply_kernel, tab, h, (const double*)partial, steps & 1);
@@ -781,7 +900,7 @@ extern "C" gnn_status gnn_muon_workspace(const gnn_muon_tensor* tensors, int32_t
   for (int i = 0; i < n_tensors; ++i) GNN_TRY(check_shape("gnn_muon_workspace", i, tensors[i].rows, tensors[i].cols));
   return guarded("gnn_muon_workspace", [&] {
     const auto order = order_of(n_tensors, [&](int i) { return Shape{tensors[i].rows, tensors[i].cols}; });
-    return each_pass(order, nullptr, 0, ws_bytes, [&](Table& tab, Arena& ar, double*, int k) {
+    return each_pass(order, nullptr, 0, ws_bytes, [&](Table& tab, Arena& ar, double*, Done*, int k) {
       for (int i = 0; i < tab.count; ++i) {
         tab.mat[i] = Mat{};
         tab.mat[i].rows = tensors[order[k + i]].rows, tab.mat[i].cols = tensors[order[k + i]].cols;
@@ -831,7 +950,7 @@ extern "C" gnn_status gnn_muon_step(const gnn_muon_tensor* tensors, int32_t n_te
                 param_type, grad_type, m_type};
   return guarded(who, [&] {
     const auto order = order_of(n_tensors, [&](int i) { return Shape{tensors[i].rows, tensors[i].cols}; });
-    return each_pass(order, ws, ws_bytes, &need, [&](Table& tab, Arena& ar, double* partial, int k) {
+    return each_pass(order, ws, ws_bytes, &need, [&](Table& tab, Arena& ar, double* partial, Done* done, int k) {
       for (int i = 0; i < tab.count; ++i) {
         const gnn_muon_tensor& d = tensors[order[k + i]];
         Mat& t = tab.mat[i];
@@ -839,7 +958,7 @@ extern "C" gnn_status gnn_muon_step(const gnn_muon_tensor* tensors, int32_t n_te
         t.slot = order[k + i];
       }
       place_pass(tab, ar);
-      return run_pass(ws, ar.used, tab, h, coeffs, steps, partial, norms, as_stream(stream));
+      return run_pass(ws, ar.used, tab, h, coeffs, steps, partial, done, norms, as_stream(stream));
     });
   });
 }
@@ -854,6 +973,7 @@ extern "C" gnn_status gnn_orthogonalise_workspace(int32_t count, int32_t rows, i
   for (int left : {std::min(count, MAX_MATS), count % MAX_MATS}) {
     Arena ar(nullptr, 0);
     ar.take<double>((size_t)MAX_MATS * PARTS);
+    ar.take<Done>(MAX_MATS);
     Table tab;
     tab.count = left;
     for (int i = 0; i < left; ++i) {
@@ -894,7 +1014,7 @@ extern "C" gnn_status gnn_orthogonalise(const void* X, int64_t ldx, int64_t stri
   const Hyper h{0.f, 1.f, 1.f, 0.f, eps, 0, 1, o_type, x_type, 0};
   return guarded(who, [&] {
     const auto order = order_of(count, [&](int) { return Shape{rows, cols}; });
-    return each_pass(order, ws, ws_bytes, &need, [&](Table& tab, Arena& ar, double* partial, int k) {
+    return each_pass(order, ws, ws_bytes, &need, [&](Table& tab, Arena& ar, double* partial, Done* done, int k) {
       for (int i = 0; i < tab.count; ++i) {
         Mat& t = tab.mat[i];
         t = Mat{static_cast<char*>(O) + (k + i) * stride_o * os, static_cast<const char*>(X) + (k + i) * stride_x * xs, nullptr,
@@ -902,7 +1022,7 @@ extern "C" gnn_status gnn_orthogonalise(const void* X, int64_t ldx, int64_t stri
         t.slot = k + i;
       }
       place_pass(tab, ar);
-      return run_pass(ws, ar.used, tab, h, coeffs, steps, partial, norms, as_stream(stream));
+      return run_pass(ws, ar.used, tab, h, coeffs, steps, partial, done, norms, as_stream(stream));
     });
   });
 }
