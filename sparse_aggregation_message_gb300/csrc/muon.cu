@@ -57,7 +57,8 @@ struct Table {
   Mat mat[MAX_MATS];
   int first[MAX_MATS + 1];  // blocks (or parts) before each matrix
   int count;
-  int bn;  // the products' tiles: columns of a CTA's, or 0 for pairs of CTAs
+  int bn;  // the steps' tiles: columns of a CTA's, or 0 for pairs of CTAs
+  int half[3];  // pairs: tiles of 128 columns instead of 256, by product
 };
 
 struct Hyper {
@@ -288,7 +289,8 @@ constexpr int EPI_WARPS = 8;
 constexpr int PRODUCT_THREADS = 64 + 32 * EPI_WARPS;
 constexpr int RING = 192 << 10;
 constexpr int MAX_STAGES = 4;
-constexpr int PRODUCT_SMEM = RING + 1024 /*barriers*/ + 1024 /*align*/;
+constexpr int STAGED = 32 * 128;  // a warp's 32 rows of 128 bytes on their way out
+constexpr int PRODUCT_SMEM = RING + EPI_WARPS * STAGED + 1024 /*barriers*/ + 1024 /*align*/;
 
 // A matrix's operands by their first row of the workspace, which has 128-byte rows.
 struct Rows {
@@ -297,18 +299,19 @@ struct Rows {
   int kx, km;  // 16s of k with values: of X's columns, of its rows
 };
 struct Steps {
-  CUtensorMap map;
+  CUtensorMap map, out;  // boxes of 64 rows to load, of 32 to store
   char* base;
   Done* done;
   unsigned* flags;
   int count, steps;
+  int half[3];  // pairs: tiles of 128 columns instead of 256
   float coeff[MAX_STEPS][3];
   int first[3][MAX_MATS + 1];  // a step's tiles before each matrix of each product
   Rows mat[MAX_MATS];
 };
 
 struct Ring {
-  uint8_t* tiles;
+  uint8_t *tiles, *staged;
   uint64_t *full, *empty, *tfull, *tempty;
   uint32_t* tmem;
   volatile int* abort_flag;
@@ -316,7 +319,8 @@ struct Ring {
 __device__ __forceinline__ Ring carve(uint8_t* raw) {
   Ring s;
   s.tiles = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* bars = reinterpret_cast<uint64_t*>(s.tiles + RING);
+  s.staged = s.tiles + RING;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(s.staged + EPI_WARPS * STAGED);
   s.full = bars;
   s.empty = bars + MAX_STAGES;
   s.tfull = bars + 2 * MAX_STAGES;
@@ -333,6 +337,7 @@ struct Tile {
   Rows m;
   int step, phase, mat;
   int rb, cb, k16, kb;
+  int cols;  // of the tile
 };
 template <int COLS>
 __device__ __forceinline__ Tile tile_at(const Steps& g, int t) {
@@ -355,7 +360,8 @@ __device__ __forceinline__ Tile tile_at(const Steps& g, int t) {
   t -= first[lo];
   r.mat = lo;
   r.m = g.mat[lo];
-  constexpr int wide = COLS >> 6;  // blocks of 64 across
+  r.cols = PAIR && g.half[r.phase] ? COLS / 2 : COLS;
+  const int wide = r.cols >> 6;  // blocks of 64 across
   const int side = PAIR ? r.m.mb >> 1 : r.m.mb;
   if (r.phase == NEXT) {
     // the tiles that share columns of X side by side
@@ -369,10 +375,11 @@ __device__ __forceinline__ Tile tile_at(const Steps& g, int t) {
     r.rb = row;
     r.cb = 2 * row + t;
   } else {
+    const int each = COLS / r.cols;  // tiles of a square
     int row = 0;
-    while (t >= side - row) t -= side - row, ++row;
+    while (t >= each * (side - row)) t -= each * (side - row), ++row;
     r.rb = row;
-    r.cb = (row + t) * wide;
+    r.cb = row * each * wide + t * wide;
   }
   if (PAIR) r.rb *= 2;
   r.k16 = r.phase == GRAM ? r.m.kx : r.m.km;
@@ -454,9 +461,9 @@ __device__ __forceinline__ void walk(const Steps& g, uint8_t* smem_raw) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = PAIR ? (int)tc::cluster_rank() : 0;
   const int unit = PAIR ? blockIdx.x >> 1 : blockIdx.x, units = PAIR ? gridDim.x >> 1 : gridDim.x;
-  constexpr int bn = PAIR ? 128 : COLS;  // columns of a CTA's share of B
-  constexpr int a_stage = BLOCK, stage = BLOCK + bn * 256, stages = RING / stage < MAX_STAGES ? RING / stage : MAX_STAGES;
-  if (warp == 0 && lane == 0) tc::prefetch_tmap(&g.map);
+  constexpr int a_stage = BLOCK, stage = BLOCK + (PAIR ? COLS / 2 : COLS) * 256;
+  constexpr int stages = RING / stage < MAX_STAGES ? RING / stage : MAX_STAGES;
+  if (warp == 0 && lane < 2) tc::prefetch_tmap(lane ? &g.out : &g.map);
   if (threadIdx.x == 0) {
     for (int i = 0; i < stages; ++i) {
       tc::mbar_init(&s.full[i], 1);
@@ -490,6 +497,7 @@ __device__ __forceinline__ void walk(const Steps& g, uint8_t* smem_raw) {
     uint32_t ph = 0;
     for (int t = unit; t < tiles; t += units) {
       const Tile w = tile_at<COLS>(g, t);
+      const int bn = PAIR ? w.cols >> 1 : COLS;  // columns of a CTA's share of B
       const int x = w.step & 1 ? w.m.x1 : w.m.x0, sq = 2 * w.m.mb;
       const int left = w.phase == GRAM ? x : w.phase == POLY ? w.m.a : w.m.p, left_nb = w.phase == GRAM ? w.m.nb : sq;
       const int rb = w.rb + rank, cb = w.cb + rank * (bn >> 6);
@@ -498,7 +506,7 @@ __device__ __forceinline__ void walk(const Steps& g, uint8_t* smem_raw) {
       asm volatile("fence.proxy.async;" ::: "memory");
       for (int kb = 0; kb < w.kb; ++kb) {
         if (!tc::mbar_wait(&s.empty[st], ph ^ 1, g.flags, s.abort_flag)) goto done;
-        if (rank == 0) tc::mbar_expect_tx(&s.full[st], (PAIR ? 2 : 1) * stage);
+        if (rank == 0) tc::mbar_expect_tx(&s.full[st], (PAIR ? 2 : 1) * (BLOCK + bn * 256));
         uint8_t* a = s.tiles + st * stage;
         const uint32_t bar = PAIR ? tc::map_to_rank(&s.full[st], 0) : 0;
         load_rows<PAIR>(g, a, bar, &s.full[st], left, left_nb, 2 * rb, kb, 2, w.phase == GRAM || above<PAIR>(rb, kb));
@@ -520,12 +528,13 @@ __device__ __forceinline__ void walk(const Steps& g, uint8_t* smem_raw) {
     uint32_t ph = 0;
     for (int t = unit; t < tiles; t += units) {
       const Tile w = tile_at<COLS>(g, t);
+      const int bn = PAIR ? w.cols >> 1 : COLS;
       for (int kb = 0; kb < w.kb; ++kb, ++it) {
         const int acc = it & 1, some = min(w.k16 - 4 * kb, 4);
         const uint32_t d = tmem + acc * COLS;
         const bool a_mn = w.phase != GRAM && !above<PAIR>(w.rb, kb);
         const bool b_mn = w.phase == NEXT || (w.phase == POLY && !above<PAIR>(w.cb >> 1, kb));
-        const uint32_t idesc = tc::idesc_16(false, PAIR ? 256 : 128, COLS, a_mn, b_mn);
+        const uint32_t idesc = tc::idesc_16(false, PAIR ? 256 : 128, PAIR ? w.cols : COLS, a_mn, b_mn);
         if (!tc::mbar_wait<true>(&s.tempty[acc], ((it >> 1) & 1) ^ 1, g.flags, s.abort_flag)) goto done;
         if (!tc::mbar_wait(&s.full[st], ph, g.flags, s.abort_flag)) goto done;
         tc::fence_after_sync();
@@ -562,33 +571,53 @@ __device__ __forceinline__ void walk(const Steps& g, uint8_t* smem_raw) {
     const int e = warp - 2, q = warp & 3, half = e >> 2;  // TMEM lane quarter, column half
     const uint32_t lane0 = tmem + ((uint32_t)(q * 32) << 16);
     const int r = q * 32 + lane;  // of the 128-row block
-    constexpr int MINE = COLS / 2;  // columns of this warp's half
+    constexpr int MOST = COLS / 2;  // columns of this warp's half of a tile, at most
+    uint8_t* staged = s.staged + e * STAGED;
     const uint32_t freed0 = tc::map_to_rank(&s.tempty[0], 0), freed1 = tc::map_to_rank(&s.tempty[1], 0);
     int it = 0;
+    // The last tile's stores are waited for and counted when this warp would wait
+    // anyway, or when it has drained an accumulator.
+    int* pending = nullptr;
+    auto count_it = [&] {
+      if (!pending) return;
+      if (lane == 0) {
+        tc::bulk_wait_all();
+        // the tile's readers, through TMA or not, see what this warp wrote
+        asm volatile("fence.proxy.async;" ::: "memory");
+        asm volatile("red.release.gpu.global.add.s32 [%0], 1;" ::"l"(pending) : "memory");
+      }
+      pending = nullptr;
+    };
     for (int t = unit; t < tiles; t += units) {
       const Tile w = tile_at<COLS>(g, t);
-      const int rb = w.rb + rank, row = rb * 128 + r;
+      const int rb = w.rb + rank, row = rb * 128 + r, mine = PAIR ? w.cols >> 1 : MOST;
       const int out = w.phase == GRAM ? w.m.a : w.phase == POLY ? w.m.p : w.step & 1 ? w.m.x0 : w.m.x1;
       const int out_nb = w.phase == NEXT ? w.m.nb : 2 * w.m.mb;
       const float ca = g.coeff[w.step][0], cb_ = g.coeff[w.step][1], cc = g.coeff[w.step][2];
       // this thread's place on P's diagonal, from the first column of its half
-      const int on_diag = row - (w.cb * 64 + half * MINE);
+      const int on_diag = row - (w.cb * 64 + half * mine);
       if (w.phase == POLY) {  // A, by ordinary loads
+        count_it();
         if (lane == 0 && !wait_for<COLS>(g, w, s.abort_flag)) goto done;
         __syncwarp();
       }
-      float2 sum[MINE / 2];
+      float2 sum[MOST / 2];
 #pragma unroll
-      for (int j = 0; j < MINE / 2; ++j) sum[j] = dup2(0.f);
+      for (int j = 0; j < MOST / 2; ++j) sum[j] = dup2(0.f);
       for (int kb = 0; kb < w.kb; ++kb, ++it) {
         const int acc = it & 1;
         const float2 back = dup2(w.k16 - 4 * kb > 2 ? 1.f + 0x1p-23f : 1.f);
-        if (!tc::mbar_wait(&s.tfull[acc], (it >> 1) & 1, g.flags, s.abort_flag)) goto done;
+        if (!tc::mbar_test(&s.tfull[acc], (it >> 1) & 1)) {
+          count_it();
+          if (!tc::mbar_wait(&s.tfull[acc], (it >> 1) & 1, g.flags, s.abort_flag)) goto done;
+        }
+        __syncwarp();
         tc::fence_after_sync();
 #pragma unroll
-        for (int c = 0; c < MINE; c += 32) {
+        for (int c = 0; c < MOST; c += 32) {
+          if (c >= mine) break;
           uint32_t v[32];
-          tc::tmem_ld32(lane0 + acc * COLS + half * MINE + c, v);
+          tc::tmem_ld32(lane0 + acc * COLS + half * mine + c, v);
           tc::tmem_wait_ld();
 #pragma unroll
           for (int j = 0; j < 16; ++j)
@@ -598,23 +627,27 @@ __device__ __forceinline__ void walk(const Steps& g, uint8_t* smem_raw) {
         tc::fence_before_sync();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive_cluster(acc ? freed1 : freed0);
+        count_it();
       }
+      // 64 columns at a time: a row of one limb is then 128 bytes
 #pragma unroll
-      for (int c = 0; c < MINE; c += 32) {
-        const int col = half * MINE + c, cb = w.cb + (col >> 6);
-        const int64_t at = ((int64_t)rb * out_nb + cb) * BLOCK + chunk_at(r, (col & 63) >> 3);
-        char* to = g.base + (int64_t)out * 128 + at;
+      for (int c = 0; c < MOST; c += 64) {
+        if (c >= mine) break;
+        const int col = half * mine + c, cb = w.cb + (col >> 6);
+        constexpr int CHUNKS = MOST < 64 ? MOST / 8 : 8;  // of eight columns
+        const int64_t block = ((int64_t)rb * out_nb + cb) * BLOCK_ROWS, at = block * 128 + chunk_at(r, (col & 63) >> 3);
         const char* from = g.base + (int64_t)w.m.a * 128 + at;
+        uint4 hi[CHUNKS], lo[CHUNKS];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < CHUNKS; ++k) {
           float2 f[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) f[j] = mul2_rn(sum[c / 2 + 4 * k + j], dup2(1.f / UNIT));
           if (w.phase == POLY) {
             const int diag = on_diag - (c + 8 * k);  // the diagonal's place among the eight
-            const uint4 hi = __ldcg(reinterpret_cast<const uint4*>(from + k * 16)),
-                        lo = __ldcg(reinterpret_cast<const uint4*>(from + LIMB + k * 16));
-            const uint32_t hw[4] = {hi.x, hi.y, hi.z, hi.w}, lw[4] = {lo.x, lo.y, lo.z, lo.w};
+            const uint4 h = __ldcg(reinterpret_cast<const uint4*>(from + k * 16)),
+                        l = __ldcg(reinterpret_cast<const uint4*>(from + LIMB + k * 16));
+            const uint32_t hw[4] = {h.x, h.y, h.z, h.w}, lw[4] = {l.x, l.y, l.z, l.w};
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               const float2 a = add2_rn(Pack2<__half>::from(hw[j]), Pack2<__half>::from(lw[j]));
@@ -623,21 +656,44 @@ __device__ __forceinline__ void walk(const Steps& g, uint8_t* smem_raw) {
               if (diag == 2 * j + 1) f[j].y += ca * UNIT;
             }
           }
-          uint4 hi, lo;
-          limbs(f[0].x, f[0].y, hi.x, lo.x), limbs(f[1].x, f[1].y, hi.y, lo.y);
-          limbs(f[2].x, f[2].y, hi.z, lo.z), limbs(f[3].x, f[3].y, hi.w, lo.w);
-          *reinterpret_cast<uint4*>(to + k * 16) = hi;
-          *reinterpret_cast<uint4*>(to + LIMB + k * 16) = lo;
+          limbs(f[0].x, f[0].y, hi[k].x, lo[k].x), limbs(f[1].x, f[1].y, hi[k].y, lo[k].y);
+          limbs(f[2].x, f[2].y, hi[k].z, lo[k].z), limbs(f[3].x, f[3].y, hi[k].w, lo[k].w);
+        }
+        if (MOST < 64) {
+          char* to = g.base + (int64_t)out * 128 + at;
+#pragma unroll
+          for (int k = 0; k < CHUNKS; ++k) {
+            *reinterpret_cast<uint4*>(to + k * 16) = hi[k];
+            *reinterpret_cast<uint4*>(to + LIMB + k * 16) = lo[k];
+          }
+          asm volatile("fence.proxy.async;" ::: "memory");
+        } else {
+          // through shared memory: a warp's rows lie 128 bytes apart, and as ordinary
+          // stores each of their 16-byte pieces would be a transaction of its own
+#pragma unroll
+          for (int l = 0; l < 2; ++l) {
+            if (lane == 0) tc::bulk_wait_read<0>();
+            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < CHUNKS; ++k)
+              *reinterpret_cast<uint4*>(staged + lane * 128 + ((k ^ (lane & 7)) << 4)) = l ? lo[k] : hi[k];
+            tc::fence_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              tc::tma_store_2d(&g.out, staged, 0, (int)(out + block) + l * 128 + q * 32);
+              tc::bulk_commit();
+            }
+          }
         }
       }
-      // the tile's readers, through TMA too, see what this warp wrote
-      asm volatile("fence.proxy.async;" ::: "memory");
       __syncwarp();
-      if (lane == 0)
-        asm volatile("red.release.gpu.global.add.s32 [%0], 1;" ::"l"(&g.done[w.mat].of[w.phase]) : "memory");
+      pending = &g.done[w.mat].of[w.phase];
+      if (MOST < 64) count_it();
     }
+    count_it();
   }
 done:
+  if (warp >= 2 && lane == 0) tc::bulk_wait_all();  // stores finish before the block exits
   __syncwarp();
   if (*s.abort_flag) {
     // a wait gave up: what is still in flight (loads, products) lands within
@@ -726,11 +782,11 @@ void place(Mat& t, Arena& ar, int bn) {
   t.parts = (int)std::min<int64_t>(PARTS, ((int64_t)t.rows * t.cols + 16 * THREADS - 1) / (16 * THREADS));
 }
 
-// A matrix's tiles of one product.
-int64_t tiles_in(const Mat& t, Phase ph, int bn) {
+// A matrix's tiles of one product; half: of 128 columns on pairs.
+int64_t tiles_in(const Mat& t, Phase ph, int bn, int half) {
   const int64_t side = bn ? t.mb : t.mb / 2, km = (t.m + 63) / 64, kx = (t.n + 63) / 64;
-  if (ph == NEXT) return side * (bn == 64 ? kx : bn ? t.nb / 2 : t.nb / 4);
-  return bn == 64 ? side * km - side * (side - 1) : side * (side + 1) / 2;
+  if (ph == NEXT) return side * (bn == 64 ? kx : bn || half ? t.nb / 2 : t.nb / 4);
+  return bn == 64 ? side * km - side * (side - 1) : side * (side + 1) / 2 * (half ? 2 : 1);
 }
 
 constexpr int SMS = 152;
@@ -742,34 +798,37 @@ int sms_there() {
   return std::max(n, 2);
 }
 
-// A step's clocks on tiles of bn columns (0: pairs): rounds of tiles, each as long
-// as its products take, or its share of what L2 delivers (50 bytes a clock and SM).
-double clocks(const Table& tab, int bn) {
-  double sum = 0;
-  for (Phase ph : {GRAM, POLY, NEXT}) {
-    const int units = bn ? SMS : SMS / 2;
-    double total = 0, longest = 0;
-    int64_t tiles = 0;
-    for (int i = 0; i < tab.count; ++i) {
-      Mat t = tab.mat[i];
-      sides(t, bn);
-      const double len = (ph == GRAM ? t.n : t.m) / 64 + 1;
-      const int64_t k = tiles_in(t, ph, bn);
-      tiles += k, total += k * len, longest = std::max(longest, len);
-    }
-    const double active = (double)std::min<int64_t>(tiles, units) * (bn ? 1 : 2);
-    const double each = std::max(bn ? 6.0 * bn : 1536.0, active * (BLOCK + (bn ? bn : 128) * 256) / (50.0 * SMS));
-    const double rounds = (double)((tiles + units - 1) / units);
-    sum += std::max(rounds * total / tiles, longest) * each + 3000;
+// One product's clocks on tiles of bn columns (0: pairs, 256 or with half 128
+// columns): rounds of tiles, each as long as its MMAs take, or its share of what L2
+// delivers (50 bytes a clock and SM).
+double clocks(const Table& tab, Phase ph, int bn, int half) {
+  const int units = bn ? SMS : SMS / 2, cols = bn ? bn : half ? 64 : 128;  // of a CTA's share of B
+  double total = 0, longest = 0;
+  int64_t tiles = 0;
+  for (int i = 0; i < tab.count; ++i) {
+    Mat t = tab.mat[i];
+    sides(t, bn);
+    const double len = (ph == GRAM ? t.n : t.m) / 64 + 1;
+    const int64_t k = tiles_in(t, ph, bn, half);
+    tiles += k, total += k * len, longest = std::max(longest, len);
   }
-  return sum;
+  const double active = (double)std::min<int64_t>(tiles, units) * (bn ? 1 : 2);
+  const double each = std::max(bn ? 6.0 * bn : 12.0 * cols, active * (BLOCK + cols * 256) / (50.0 * SMS));
+  const double rounds = (double)((tiles + units - 1) / units);
+  return std::max(rounds * total / tiles, longest) * each + 3000;
+}
+double clocks(const Table& tab, int bn, const int (&half)[3]) {
+  return clocks(tab, GRAM, bn, half[GRAM]) + clocks(tab, POLY, bn, half[POLY]) + clocks(tab, NEXT, bn, half[NEXT]);
 }
 
-// The tile of a pass, and every matrix's place in its workspace.
+// The tiles of a pass, and every matrix's place in its workspace.
 void place_pass(Table& tab, Arena& ar) {
-  tab.bn = 64;
-  for (int bn : {128, 0})
-    if (clocks(tab, bn) < clocks(tab, tab.bn)) tab.bn = bn;
+  const int whole[3] = {0, 0, 0};
+  int half[3];
+  for (Phase ph : {GRAM, POLY, NEXT}) half[ph] = clocks(tab, ph, 0, 1) < clocks(tab, ph, 0, 0);
+  tab.bn = clocks(tab, 128, whole) < clocks(tab, 64, whole) ? 128 : 64;
+  if (clocks(tab, 0, half) < clocks(tab, tab.bn, whole)) tab.bn = 0;
+  for (int k = 0; k < 3; ++k) tab.half[k] = tab.bn ? 0 : half[k];
   for (int i = 0; i < tab.count; ++i) place(tab.mat[i], ar, tab.bn);
 }
 
@@ -834,6 +893,8 @@ gnn_status run_pass(void* ws, size_t used, Table& tab, const Hyper& h, const flo
     g.flags = device_flags();
     if (!g.flags) return fail(GNN_ERR_CUDA, "device flag word unavailable");
     GNN_TRY(encode_tmap_2d(&g.map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, ws, 64, used / 128, 128, 64, 64));
+    GNN_TRY(encode_tmap_2d(&g.out, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, ws, 64, used / 128, 128, 64, 32));
+    for (int k = 0; k < 3; ++k) g.half[k] = tab.half[k];
     g.count = tab.count, g.steps = steps;
     for (int s = 0; s < steps; ++s)
       for (int k = 0; k < 3; ++k) g.coeff[s][k] = coeffs[3 * s + k];
@@ -847,7 +908,7 @@ gnn_status run_pass(void* ws, size_t used, Table& tab, const Hyper& h, const flo
       for (int i = 0; i <= tab.count; ++i) {
         if (sum > 0x3fffffff) return fail(GNN_ERR_UNSUPPORTED, "too many tiles in one call");
         g.first[ph][i] = (int)sum;
-        if (i < tab.count) sum += tiles_in(tab.mat[i], ph, tab.bn);
+        if (i < tab.count) sum += tiles_in(tab.mat[i], ph, tab.bn, tab.half[ph]);
       }
     }
     GNN_TRY(launch_steps(g, tab.bn, st));
