@@ -41,6 +41,11 @@ gnn_status launch_relu_mask_f32(int64_t n, int F, const float* dH, int64_t ldg, 
 gnn_status encode_tmap_2d(CUtensorMap* map, CUtensorMapDataType type, const void* base, uint64_t inner,
                           uint64_t outer, uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer);
 
+// The same of `rank` dimensions, the innermost first; strides in bytes from the
+// second dimension on.
+gnn_status encode_tmap(CUtensorMap* map, CUtensorMapDataType type, int rank, const void* base, const uint64_t* dims,
+                       const uint64_t* strides, const uint32_t* box);
+
 gnn_status launch_transpose_w(const uint16_t* W, int F_in, int F_out, int K, uint16_t* Wt,
                               cudaStream_t st);
 

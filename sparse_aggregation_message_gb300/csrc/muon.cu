@@ -10,8 +10,8 @@
 // range is left), and a product is hi hi + hi lo + lo hi with fp32 sums.
 //
 // Operands lie in the workspace in blocks of 128 rows x 64 columns, the hi limb's
-// 16 KB before the lo limb's: rows of 128 bytes, so that one tensor map over the
-// whole workspace loads any of them, swizzled, into shared memory.
+// 16 KB before the lo limb's: rows of 128 bytes, so that a few tensor maps over the
+// whole workspace bring any of them, swizzled, to shared memory and back.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -59,6 +59,9 @@ struct Table {
   int count;
   int bn;  // the steps' tiles: columns of a CTA's, or 0 for pairs of CTAs
   int half[3];  // pairs: tiles of 128 columns instead of 256, by product
+  int64_t blocks;  // of the operands, from the workspace's start
+  double* partial;
+  int* done;
 };
 
 struct Hyper {
@@ -104,13 +107,12 @@ struct Done {
 constexpr int DONE_WORDS = MAX_MATS * 4;
 
 // Sums of u^2 over a share of a matrix's rows; the counts of the steps start at zero.
-__global__ void __launch_bounds__(THREADS) square_kernel(const __grid_constant__ Table tab, const Hyper h, double* partial,
-                                                         int* done) {
+__global__ void __launch_bounds__(THREADS) square_kernel(const __grid_constant__ Table tab, const Hyper h) {
   __shared__ double sm[THREADS / 32];
   cudaTriggerProgrammaticLaunchCompletion();
   cudaGridDependencySynchronize();
   if (blockIdx.x == 0)
-    for (int k = threadIdx.x; k < DONE_WORDS; k += THREADS) done[k] = 0;
+    for (int k = threadIdx.x; k < DONE_WORDS; k += THREADS) tab.done[k] = 0;
   const int i = mat_of(tab, blockIdx.x);
   const Mat& t = tab.mat[i];
   const int part = blockIdx.x - tab.first[i];
@@ -144,7 +146,7 @@ __global__ void __launch_bounds__(THREADS) square_kernel(const __grid_constant__
   if (threadIdx.x == 0) {
     double s = 0;
     for (int w = 0; w < THREADS / 32; ++w) s += sm[w];
-    partial[i * PARTS + part] = s;
+    tab.partial[i * PARTS + part] = s;
   }
 }
 
@@ -173,8 +175,7 @@ __device__ __forceinline__ void limbs(float a, float b, uint32_t& hi, uint32_t& 
 __device__ __forceinline__ int chunk_at(int r, int k) { return r * 128 + k * 16; }
 
 // u scaled into X's limbs, and the new momentum; a block of X a thread block.
-__global__ void __launch_bounds__(THREADS) begin_kernel(const __grid_constant__ Table tab, const Hyper h,
-                                                        const double* partial, float* norms) {
+__global__ void __launch_bounds__(THREADS) begin_kernel(const __grid_constant__ Table tab, const Hyper h, float* norms) {
   __shared__ float tile[128][65];
   __shared__ double sm;
   cudaTriggerProgrammaticLaunchCompletion();
@@ -182,7 +183,7 @@ __global__ void __launch_bounds__(THREADS) begin_kernel(const __grid_constant__ 
   const int i = mat_of(tab, blockIdx.x);
   const Mat& t = tab.mat[i];
   const int block = blockIdx.x - tab.first[i], r0 = block / t.nb * 128, c0 = block % t.nb * 64;
-  const double norm = norm_of(partial, i, t.parts, &sm);
+  const double norm = norm_of(tab.partial, i, t.parts, &sm);
   const bool good = isfinite((float)norm);
   const float inv = good ? (float)((double)UNIT / (norm + h.eps)) : 0.f;
   if (block == 0 && threadIdx.x == 0 && norms) norms[t.slot] = (float)norm;
@@ -215,8 +216,7 @@ __global__ void __launch_bounds__(THREADS) begin_kernel(const __grid_constant__ 
 }
 
 // Parameters (or the output) from the orthogonalised X.
-__global__ void __launch_bounds__(THREADS) apply_kernel(const __grid_constant__ Table tab, const Hyper h,
-                                                        const double* partial, int which) {
+__global__ void __launch_bounds__(THREADS) apply_kernel(const __grid_constant__ Table tab, const Hyper h, int which) {
   __shared__ float tile[128][65];
   __shared__ double sm;
   cudaTriggerProgrammaticLaunchCompletion();
@@ -224,7 +224,7 @@ __global__ void __launch_bounds__(THREADS) apply_kernel(const __grid_constant__ 
   const int i = mat_of(tab, blockIdx.x);
   const Mat& t = tab.mat[i];
   const int block = blockIdx.x - tab.first[i], r0 = block / t.nb * 128, c0 = block % t.nb * 64;
-  const double norm = norm_of(partial, i, t.parts, &sm);
+  const double norm = norm_of(tab.partial, i, t.parts, &sm);
   const bool good = isfinite((float)norm);
   if (!good && !h.orth) return;  // this matrix stays as it is
   const char* x = t.x[which] + (int64_t)block * BLOCK;
@@ -283,7 +283,6 @@ enum Phase { GRAM, POLY, NEXT };  // A = X X', P = a I + b A + c A A, X <- P X
 // their registers, and put back what is lost on average, one unit in 2^23 where three
 // or four sums of 16 are in it: 1.7e-6 and 1.0e-6 (without that 2.6e-6 and 1.5e-6;
 // 128 of k: 2.4e-6 and 2.3e-6).
-constexpr int BOX = 64 * 128;  // 64 rows of 128 bytes: what one TMA load brings
 constexpr int BLOCK_ROWS = BLOCK / 128;
 constexpr int EPI_WARPS = 8;
 constexpr int PRODUCT_THREADS = 64 + 32 * EPI_WARPS;
@@ -292,14 +291,20 @@ constexpr int MAX_STAGES = 4;
 constexpr int STAGED = 32 * 128;  // a warp's 32 rows of 128 bytes on their way out
 constexpr int PRODUCT_SMEM = RING + EPI_WARPS * STAGED + 1024 /*barriers*/ + 1024 /*align*/;
 
-// A matrix's operands by their first row of the workspace, which has 128-byte rows.
+// A matrix's operands by their first block of the workspace.
 struct Rows {
   int x0, x1, a, p;
   int mb, nb;
   int kx, km;  // 16s of k with values: of X's columns, of its rows
 };
 struct Steps {
-  CUtensorMap map, out;  // boxes of 64 rows to load, of 32 to store
+  // The workspace as rows of 64 columns: a block in one box, rows as they lie
+  // (K-major operands of 128 rows); and 32 rows of a limb, to store.
+  CUtensorMap block, out;
+  // As [half of a block][block][limb][64 rows][64 columns]: both limbs of 64 rows of
+  // one block, or of two neighbours (MN-major operands: columns of a mirror image or
+  // of X; K-major ones of 64 rows).
+  CUtensorMap one, two;
   char* base;
   Done* done;
   unsigned* flags;
@@ -313,6 +318,7 @@ struct Steps {
 struct Ring {
   uint8_t *tiles, *staged;
   uint64_t *full, *empty, *tfull, *tempty;
+  uint64_t *clear, *filled;  // tiles of 64 columns: the two warps of 32 rows meet
   uint32_t* tmem;
   volatile int* abort_flag;
 };
@@ -325,7 +331,9 @@ __device__ __forceinline__ Ring carve(uint8_t* raw) {
   s.empty = bars + MAX_STAGES;
   s.tfull = bars + 2 * MAX_STAGES;
   s.tempty = s.tfull + 2;
-  s.tmem = reinterpret_cast<uint32_t*>(s.tempty + 2);
+  s.clear = s.tempty + 2;
+  s.filled = s.clear + 4;
+  s.tmem = reinterpret_cast<uint32_t*>(s.filled + 4);
   s.abort_flag = reinterpret_cast<volatile int*>(s.tmem + 1);
   return s;
 }
@@ -422,27 +430,34 @@ __device__ __forceinline__ bool above(int b, int kb) {
   return PAIR ? (b >> 1) <= (kb >> 2) : b <= (kb >> 1);
 }
 
+// 64 or 128 rows (from 64-row block r64) of an operand with `nb` column blocks from
+// block `s`, at k block kb: as they lie (K-major), or, below the diagonal, the mirror
+// image's columns (MN-major).  128 rows as they lie come as [limb][128][64], all else
+// as [64 of them][limb][64][64].
 template <bool PAIR>
-__device__ __forceinline__ void load_box(const Steps& g, uint8_t* to, uint32_t bar, uint64_t* local, int row) {
-  if (PAIR)
-    tc::tma_load_2d_pair(to, &g.map, bar, 0, row);
-  else
-    tc::tma_load_2d(to, &g.map, local, 0, row);
+__device__ __forceinline__ void load_rows(const Steps& g, uint8_t* to, uint32_t bar, int s, int nb, int r64, int kb,
+                                          bool wide, bool direct) {
+  if (direct && wide) {
+    const int row = (s + (r64 >> 1) * nb + kb) * BLOCK_ROWS;
+    if (PAIR)
+      tc::tma_load_2d_pair(to, &g.block, bar, 0, row);
+    else
+      tc::tma_load_2d(to, &g.block, bar, 0, row);
+  } else if (direct) {
+    tc::tma_load_5d<PAIR>(to, &g.one, bar, s + (r64 >> 1) * nb + kb, r64 & 1);
+  } else {
+    tc::tma_load_5d<PAIR>(to, wide ? &g.two : &g.one, bar, s + (kb >> 1) * nb + r64, kb & 1);
+  }
 }
 
-// 64 * boxes rows (from 64-row block r64) of an operand with `nb` column blocks from
-// row `s`, at k block kb: as they lie (K-major), or, below the diagonal, the mirror image's
-// columns (MN-major).
-template <bool PAIR>
-__device__ __forceinline__ void load_rows(const Steps& g, uint8_t* to, uint32_t bar, uint64_t* local, int s, int nb, int r64,
-                                          int kb, int boxes, bool direct) {
-  for (int l = 0; l < 2; ++l) {
-    for (int h = 0; h < boxes; ++h, to += BOX) {
-      const int at = direct ? (((r64 + h) >> 1) * nb + kb) * BLOCK_ROWS + ((r64 + h) & 1) * 64
-                            : ((kb >> 1) * nb + r64 + h) * BLOCK_ROWS + (kb & 1) * 64;
-      load_box<PAIR>(g, to, bar, local, s + at + l * 128);
-    }
-  }
+// Where an operand's limbs and 16s of k lie in a stage, in units of 16 bytes of its
+// descriptor: K-major a row has its 128 bytes of k, MN-major 16 of k are 16 rows.
+struct Operand {
+  uint64_t desc;
+  uint32_t limb, step;
+};
+__device__ __forceinline__ Operand operand(uint32_t at, bool mn, bool wide) {
+  return {tc::sw128_desc(at, mn ? 2 * 8192 : 16), (uint32_t)(!mn && wide ? 16384 : 8192) >> 4, (uint32_t)(mn ? 2048 : 32) >> 4};
 }
 
 template <bool PAIR>
@@ -463,7 +478,7 @@ __device__ __forceinline__ void walk(const Steps& g, uint8_t* smem_raw) {
   const int unit = PAIR ? blockIdx.x >> 1 : blockIdx.x, units = PAIR ? gridDim.x >> 1 : gridDim.x;
   constexpr int a_stage = BLOCK, stage = BLOCK + (PAIR ? COLS / 2 : COLS) * 256;
   constexpr int stages = RING / stage < MAX_STAGES ? RING / stage : MAX_STAGES;
-  if (warp == 0 && lane < 2) tc::prefetch_tmap(lane ? &g.out : &g.map);
+  if (warp == 0 && lane < 4) tc::prefetch_tmap(lane == 0 ? &g.block : lane == 1 ? &g.one : lane == 2 ? &g.two : &g.out);
   if (threadIdx.x == 0) {
     for (int i = 0; i < stages; ++i) {
       tc::mbar_init(&s.full[i], 1);
@@ -472,6 +487,10 @@ __device__ __forceinline__ void walk(const Steps& g, uint8_t* smem_raw) {
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(&s.tfull[i], 1);
       tc::mbar_init(&s.tempty[i], (PAIR ? 2 : 1) * EPI_WARPS);  // a lane of each warp
+    }
+    for (int i = 0; i < 4; ++i) {
+      tc::mbar_init(&s.clear[i], 2);
+      tc::mbar_init(&s.filled[i], 2);
     }
     *s.abort_flag = 0;
     tc::fence_barrier_init();
@@ -502,19 +521,16 @@ __device__ __forceinline__ void walk(const Steps& g, uint8_t* smem_raw) {
       const int left = w.phase == GRAM ? x : w.phase == POLY ? w.m.a : w.m.p, left_nb = w.phase == GRAM ? w.m.nb : sq;
       const int rb = w.rb + rank, cb = w.cb + rank * (bn >> 6);
       if (!wait_for<COLS>(g, w, s.abort_flag)) goto done;
-      // what ordinary stores wrote is read by TMA
-      asm volatile("fence.proxy.async;" ::: "memory");
       for (int kb = 0; kb < w.kb; ++kb) {
         if (!tc::mbar_wait(&s.empty[st], ph ^ 1, g.flags, s.abort_flag)) goto done;
         if (rank == 0) tc::mbar_expect_tx(&s.full[st], (PAIR ? 2 : 1) * (BLOCK + bn * 256));
         uint8_t* a = s.tiles + st * stage;
-        const uint32_t bar = PAIR ? tc::map_to_rank(&s.full[st], 0) : 0;
-        load_rows<PAIR>(g, a, bar, &s.full[st], left, left_nb, 2 * rb, kb, 2, w.phase == GRAM || above<PAIR>(rb, kb));
+        const uint32_t bar = PAIR ? tc::map_to_rank(&s.full[st], 0) : tc::smem_u32(&s.full[st]);
+        load_rows<PAIR>(g, a, bar, left, left_nb, 2 * rb, kb, true, w.phase == GRAM || above<PAIR>(rb, kb));
         if (w.phase == NEXT)
-          load_rows<PAIR>(g, a + a_stage, bar, &s.full[st], x, w.m.nb, cb, kb, bn >> 6, false);
+          load_rows<PAIR>(g, a + a_stage, bar, x, w.m.nb, cb, kb, bn == 128, false);
         else
-          load_rows<PAIR>(g, a + a_stage, bar, &s.full[st], left, left_nb, cb, kb, bn >> 6,
-                          w.phase == GRAM || above<PAIR>(cb >> 1, kb));
+          load_rows<PAIR>(g, a + a_stage, bar, left, left_nb, cb, kb, bn == 128, w.phase == GRAM || above<PAIR>(cb >> 1, kb));
         if (++st == stages) { st = 0; ph ^= 1; }
       }
     }
@@ -538,24 +554,18 @@ __device__ __forceinline__ void walk(const Steps& g, uint8_t* smem_raw) {
         if (!tc::mbar_wait<true>(&s.tempty[acc], ((it >> 1) & 1) ^ 1, g.flags, s.abort_flag)) goto done;
         if (!tc::mbar_wait(&s.full[st], ph, g.flags, s.abort_flag)) goto done;
         tc::fence_after_sync();
-        const uint32_t a0 = tc::smem_u32(s.tiles + st * stage), b0 = a0 + a_stage;
-        // 16 of k: 32 bytes K-major, 16 rows of 128 bytes MN-major
-        auto left = [&](int k, int limb) {
-          return tc::sw128_desc(a0 + limb * LIMB + k * (a_mn ? 2048 : 32), a_mn ? BOX : 16);
-        };
-        auto right = [&](int k, int limb) {
-          return tc::sw128_desc(b0 + limb * bn * 128 + k * (b_mn ? 2048 : 32), b_mn ? BOX : 16);
-        };
+        const uint32_t at = tc::smem_u32(s.tiles + st * stage);
+        const Operand l = operand(at, a_mn, true), r = operand(at + a_stage, b_mn, bn == 128);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           if (k >= some) break;
-          multiply<PAIR>(d, left(k, 0), right(k, 1), idesc, k ? 1u : 0u);
-          multiply<PAIR>(d, left(k, 1), right(k, 0), idesc, 1u);
+          multiply<PAIR>(d, l.desc + k * l.step, r.desc + r.limb + k * r.step, idesc, k ? 1u : 0u);
+          multiply<PAIR>(d, l.desc + l.limb + k * l.step, r.desc + k * r.step, idesc, 1u);
         }
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           if (k >= some) break;
-          multiply<PAIR>(d, left(k, 0), right(k, 0), idesc, 1u);
+          multiply<PAIR>(d, l.desc + k * l.step, r.desc + k * r.step, idesc, 1u);
         }
         if (PAIR) {
           tc::mma_commit_pair(&s.empty[st]);
@@ -572,9 +582,11 @@ __device__ __forceinline__ void walk(const Steps& g, uint8_t* smem_raw) {
     const uint32_t lane0 = tmem + ((uint32_t)(q * 32) << 16);
     const int r = q * 32 + lane;  // of the 128-row block
     constexpr int MOST = COLS / 2;  // columns of this warp's half of a tile, at most
-    uint8_t* staged = s.staged + e * STAGED;
+    // tiles of 64 columns: the two warps of 32 rows share a tile for each limb
+    uint8_t* staged = s.staged + (MOST < 64 ? 2 * q : e) * STAGED;
     const uint32_t freed0 = tc::map_to_rank(&s.tempty[0], 0), freed1 = tc::map_to_rank(&s.tempty[1], 0);
     int it = 0;
+    uint32_t met = 0;  // parity of the two warps' next meeting
     // The last tile's stores are waited for and counted when this warp would wait
     // anyway, or when it has drained an accumulator.
     int* pending = nullptr;
@@ -582,8 +594,6 @@ __device__ __forceinline__ void walk(const Steps& g, uint8_t* smem_raw) {
       if (!pending) return;
       if (lane == 0) {
         tc::bulk_wait_all();
-        // the tile's readers, through TMA or not, see what this warp wrote
-        asm volatile("fence.proxy.async;" ::: "memory");
         asm volatile("red.release.gpu.global.add.s32 [%0], 1;" ::"l"(pending) : "memory");
       }
       pending = nullptr;
@@ -600,6 +610,15 @@ __device__ __forceinline__ void walk(const Steps& g, uint8_t* smem_raw) {
         count_it();
         if (lane == 0 && !wait_for<COLS>(g, w, s.abort_flag)) goto done;
         __syncwarp();
+      }
+      const int64_t a_at = (int64_t)w.m.a * BLOCK + ((int64_t)rb * out_nb + w.cb) * BLOCK + r * 128;
+      uint4 a_hi[MOST < 64 ? 4 : 1], a_lo[MOST < 64 ? 4 : 1];
+      if (MOST < 64 && w.phase == POLY) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          a_hi[k] = __ldcg(reinterpret_cast<const uint4*>(g.base + a_at + half * 64 + k * 16));
+          a_lo[k] = __ldcg(reinterpret_cast<const uint4*>(g.base + a_at + LIMB + half * 64 + k * 16));
+        }
       }
       float2 sum[MOST / 2];
 #pragma unroll
@@ -635,8 +654,8 @@ __device__ __forceinline__ void walk(const Steps& g, uint8_t* smem_raw) {
         if (c >= mine) break;
         const int col = half * mine + c, cb = w.cb + (col >> 6);
         constexpr int CHUNKS = MOST < 64 ? MOST / 8 : 8;  // of eight columns
-        const int64_t block = ((int64_t)rb * out_nb + cb) * BLOCK_ROWS, at = block * 128 + chunk_at(r, (col & 63) >> 3);
-        const char* from = g.base + (int64_t)w.m.a * 128 + at;
+        const int64_t block = out + (int64_t)rb * out_nb + cb;
+        const char* from = g.base + a_at + (int64_t)(col >> 6) * BLOCK;
         uint4 hi[CHUNKS], lo[CHUNKS];
 #pragma unroll
         for (int k = 0; k < CHUNKS; ++k) {
@@ -645,8 +664,13 @@ __device__ __forceinline__ void walk(const Steps& g, uint8_t* smem_raw) {
           for (int j = 0; j < 4; ++j) f[j] = mul2_rn(sum[c / 2 + 4 * k + j], dup2(1.f / UNIT));
           if (w.phase == POLY) {
             const int diag = on_diag - (c + 8 * k);  // the diagonal's place among the eight
-            const uint4 h = __ldcg(reinterpret_cast<const uint4*>(from + k * 16)),
-                        l = __ldcg(reinterpret_cast<const uint4*>(from + LIMB + k * 16));
+            uint4 h, l;
+            if (MOST < 64) {
+              h = a_hi[k], l = a_lo[k];
+            } else {
+              h = __ldcg(reinterpret_cast<const uint4*>(from + k * 16));
+              l = __ldcg(reinterpret_cast<const uint4*>(from + LIMB + k * 16));
+            }
             const uint32_t hw[4] = {h.x, h.y, h.z, h.w}, lw[4] = {l.x, l.y, l.z, l.w};
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -659,17 +683,33 @@ __device__ __forceinline__ void walk(const Steps& g, uint8_t* smem_raw) {
           limbs(f[0].x, f[0].y, hi[k].x, lo[k].x), limbs(f[1].x, f[1].y, hi[k].y, lo[k].y);
           limbs(f[2].x, f[2].y, hi[k].z, lo[k].z), limbs(f[3].x, f[3].y, hi[k].w, lo[k].w);
         }
+        // through shared memory: a warp's rows lie 128 bytes apart, and as ordinary
+        // stores each of their 16-byte pieces would be a transaction of its own
         if (MOST < 64) {
-          char* to = g.base + (int64_t)out * 128 + at;
+          // both warps' last tile has left (each sends one limb of it)
+          if (lane == 0) {
+            tc::bulk_wait_read<0>();
+            tc::mbar_arrive(&s.clear[q]);
+          }
+          if (!tc::mbar_wait(&s.clear[q], met, g.flags, s.abort_flag)) goto done;
+          __syncwarp();
 #pragma unroll
           for (int k = 0; k < CHUNKS; ++k) {
-            *reinterpret_cast<uint4*>(to + k * 16) = hi[k];
-            *reinterpret_cast<uint4*>(to + LIMB + k * 16) = lo[k];
+            uint4* to = reinterpret_cast<uint4*>(staged + lane * 128 + (((half * 4 + k) ^ (lane & 7)) << 4));
+            to[0] = hi[k];
+            to[STAGED / 16] = lo[k];
           }
-          asm volatile("fence.proxy.async;" ::: "memory");
+          tc::fence_async_smem();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&s.filled[q]);
+          if (!tc::mbar_wait(&s.filled[q], met, g.flags, s.abort_flag)) goto done;
+          __syncwarp();
+          met ^= 1;
+          if (lane == 0) {
+            tc::tma_store_2d(&g.out, staged + half * STAGED, 0, (int)(block * BLOCK_ROWS) + half * 128 + q * 32);
+            tc::bulk_commit();
+          }
         } else {
-          // through shared memory: a warp's rows lie 128 bytes apart, and as ordinary
-          // stores each of their 16-byte pieces would be a transaction of its own
 #pragma unroll
           for (int l = 0; l < 2; ++l) {
             if (lane == 0) tc::bulk_wait_read<0>();
@@ -680,7 +720,7 @@ __device__ __forceinline__ void walk(const Steps& g, uint8_t* smem_raw) {
             tc::fence_async_smem();
             __syncwarp();
             if (lane == 0) {
-              tc::tma_store_2d(&g.out, staged, 0, (int)(out + block) + l * 128 + q * 32);
+              tc::tma_store_2d(&g.out, staged, 0, (int)(block * BLOCK_ROWS) + l * 128 + q * 32);
               tc::bulk_commit();
             }
           }
@@ -688,7 +728,6 @@ __device__ __forceinline__ void walk(const Steps& g, uint8_t* smem_raw) {
       }
       __syncwarp();
       pending = &g.done[w.mat].of[w.phase];
-      if (MOST < 64) count_it();
     }
     count_it();
   }
@@ -830,6 +869,9 @@ void place_pass(Table& tab, Arena& ar) {
   if (clocks(tab, 0, half) < clocks(tab, tab.bn, whole)) tab.bn = 0;
   for (int k = 0; k < 3; ++k) tab.half[k] = tab.bn ? 0 : half[k];
   for (int i = 0; i < tab.count; ++i) place(tab.mat[i], ar, tab.bn);
+  tab.blocks = (int64_t)(ar.used / BLOCK);
+  tab.partial = ar.take<double>((size_t)MAX_MATS * PARTS);
+  tab.done = ar.take<int>(DONE_WORDS);
 }
 
 // Matrices in the order of their work, the largest first, MAX_MATS to a pass; every
@@ -850,11 +892,9 @@ gnn_status each_pass(const std::vector<int>& order, void* ws, size_t cap, size_t
   *need = 0;
   for (size_t k = 0; k < order.size(); k += MAX_MATS) {
     Arena ar(ws, cap);
-    double* partial = ar.take<double>((size_t)MAX_MATS * PARTS);
-    Done* done = ar.take<Done>(MAX_MATS);
     Table tab;
     tab.count = (int)std::min<size_t>(MAX_MATS, order.size() - k);
-    GNN_TRY(fill(tab, ar, partial, done, (int)k));
+    GNN_TRY(fill(tab, ar, (int)k));
     *need = std::max(*need, ar.used);
   }
   return GNN_OK;
@@ -874,34 +914,42 @@ gnn_status launch_steps(const Steps& g, int bn, cudaStream_t st) {
   return bn == 64 ? run(steps_kernel<64>, done64, units) : run(steps_kernel<128>, done128, units);
 }
 
-gnn_status run_pass(void* ws, size_t used, Table& tab, const Hyper& h, const float* coeffs, int steps, double* partial,
-                    Done* done, float* norms, cudaStream_t st) {
-  if (used / 128 > 0x7fffffff) return fail(GNN_ERR_UNSUPPORTED, "matrices too large together");
+gnn_status maps_of(Steps& g, const void* ws, uint64_t blocks) {
+  const CUtensorMapDataType t = CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  GNN_TRY(encode_tmap_2d(&g.block, t, ws, 64, blocks * BLOCK_ROWS, 128, 64, BLOCK_ROWS));
+  GNN_TRY(encode_tmap_2d(&g.out, t, ws, 64, blocks * BLOCK_ROWS, 128, 64, 32));
+  const uint64_t dims[5] = {64, 64, 2, blocks, 2}, strides[4] = {128, LIMB, BLOCK, LIMB / 2};
+  const uint32_t one[5] = {64, 64, 2, 1, 1}, two[5] = {64, 64, 2, 2, 1};
+  GNN_TRY(encode_tmap(&g.one, t, 5, ws, dims, strides, one));
+  return encode_tmap(&g.two, t, 5, ws, dims, strides, two);
+}
+
+gnn_status run_pass(void* ws, Table& tab, const Hyper& h, const float* coeffs, int steps, float* norms, cudaStream_t st) {
+  if (tab.blocks > 0x7fffff00 / BLOCK_ROWS) return fail(GNN_ERR_UNSUPPORTED, "matrices too large together");
   auto blocks = [&](auto&& of) {
     tab.first[0] = 0;
     for (int i = 0; i < tab.count; ++i) tab.first[i + 1] = tab.first[i] + of(tab.mat[i]);
     return tab.first[tab.count];
   };
   int grid = blocks([](const Mat& t) { return t.parts; });
-  GNN_TRY(launch(grid, THREADS, 0, st, square_kernel, tab, h, partial, &done->of[0]));
+  GNN_TRY(launch(grid, THREADS, 0, st, square_kernel, tab, h));
   grid = blocks([](const Mat& t) { return t.mb * t.nb; });
-  GNN_TRY(launch(grid, THREADS, 0, st, begin_kernel, tab, h, (const double*)partial, norms));
+  GNN_TRY(launch(grid, THREADS, 0, st, begin_kernel, tab, h, norms));
   if (steps) {
     Steps g;
     g.base = static_cast<char*>(ws);
-    g.done = done;
+    g.done = reinterpret_cast<Done*>(tab.done);
     g.flags = device_flags();
     if (!g.flags) return fail(GNN_ERR_CUDA, "device flag word unavailable");
-    GNN_TRY(encode_tmap_2d(&g.map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, ws, 64, used / 128, 128, 64, 64));
-    GNN_TRY(encode_tmap_2d(&g.out, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, ws, 64, used / 128, 128, 64, 32));
+    GNN_TRY(maps_of(g, ws, (uint64_t)tab.blocks));
     for (int k = 0; k < 3; ++k) g.half[k] = tab.half[k];
     g.count = tab.count, g.steps = steps;
     for (int s = 0; s < steps; ++s)
       for (int k = 0; k < 3; ++k) g.coeff[s][k] = coeffs[3 * s + k];
-    auto row = [&](const void* p) { return (int)((static_cast<const char*>(p) - g.base) / 128); };
+    auto at = [&](const char* p) { return (int)((p - g.base) / BLOCK); };
     for (int i = 0; i < tab.count; ++i) {
       const Mat& t = tab.mat[i];
-      g.mat[i] = {row(t.x[0]), row(t.x[1]), row(t.a), row(t.p), t.mb, t.nb, (t.n + 15) / 16, (t.m + 15) / 16};
+      g.mat[i] = {at(t.x[0]), at(t.x[1]), at(t.a), at(t.p), t.mb, t.nb, (t.n + 15) / 16, (t.m + 15) / 16};
     }
     for (Phase ph : {GRAM, POLY, NEXT}) {
       int64_t sum = 0;
@@ -914,7 +962,7 @@ gnn_status run_pass(void* ws, size_t used, Table& tab, const Hyper& h, const flo
     GNN_TRY(launch_steps(g, tab.bn, st));
   }
   grid = blocks([](const Mat& t) { return t.mb * t.nb; });
-  return launch(grid, THREADS, 0, st, apply_kernel, tab, h, (const double*)partial, steps & 1);
+  return launch(grid, THREADS, 0, st, apply_kernel, tab, h, steps & 1);
 }
 
 constexpr int MOST = 65536;  // rows or columns of a matrix
@@ -961,7 +1009,7 @@ extern "C" gnn_status gnn_muon_workspace(const gnn_muon_tensor* tensors, int32_t
   for (int i = 0; i < n_tensors; ++i) GNN_TRY(check_shape("gnn_muon_workspace", i, tensors[i].rows, tensors[i].cols));
   return guarded("gnn_muon_workspace", [&] {
     const auto order = order_of(n_tensors, [&](int i) { return Shape{tensors[i].rows, tensors[i].cols}; });
-    return each_pass(order, nullptr, 0, ws_bytes, [&](Table& tab, Arena& ar, double*, Done*, int k) {
+    return each_pass(order, nullptr, 0, ws_bytes, [&](Table& tab, Arena& ar, int k) {
       for (int i = 0; i < tab.count; ++i) {
         tab.mat[i] = Mat{};
         tab.mat[i].rows = tensors[order[k + i]].rows, tab.mat[i].cols = tensors[order[k + i]].cols;
@@ -1011,7 +1059,7 @@ extern "C" gnn_status gnn_muon_step(const gnn_muon_tensor* tensors, int32_t n_te
                 param_type, grad_type, m_type};
   return guarded(who, [&] {
     const auto order = order_of(n_tensors, [&](int i) { return Shape{tensors[i].rows, tensors[i].cols}; });
-    return each_pass(order, ws, ws_bytes, &need, [&](Table& tab, Arena& ar, double* partial, Done* done, int k) {
+    return each_pass(order, ws, ws_bytes, &need, [&](Table& tab, Arena& ar, int k) {
       for (int i = 0; i < tab.count; ++i) {
         const gnn_muon_tensor& d = tensors[order[k + i]];
         Mat& t = tab.mat[i];
@@ -1019,7 +1067,7 @@ extern "C" gnn_status gnn_muon_step(const gnn_muon_tensor* tensors, int32_t n_te
         t.slot = order[k + i];
       }
       place_pass(tab, ar);
-      return run_pass(ws, ar.used, tab, h, coeffs, steps, partial, done, norms, as_stream(stream));
+      return run_pass(ws, tab, h, coeffs, steps, norms, as_stream(stream));
     });
   });
 }
@@ -1033,8 +1081,6 @@ extern "C" gnn_status gnn_orthogonalise_workspace(int32_t count, int32_t rows, i
   // the last pass may have fewer matrices than the others, and other tiles
   for (int left : {std::min(count, MAX_MATS), count % MAX_MATS}) {
     Arena ar(nullptr, 0);
-    ar.take<double>((size_t)MAX_MATS * PARTS);
-    ar.take<Done>(MAX_MATS);
     Table tab;
     tab.count = left;
     for (int i = 0; i < left; ++i) {
@@ -1075,7 +1121,7 @@ extern "C" gnn_status gnn_orthogonalise(const void* X, int64_t ldx, int64_t stri
   const Hyper h{0.f, 1.f, 1.f, 0.f, eps, 0, 1, o_type, x_type, 0};
   return guarded(who, [&] {
     const auto order = order_of(count, [&](int) { return Shape{rows, cols}; });
-    return each_pass(order, ws, ws_bytes, &need, [&](Table& tab, Arena& ar, double* partial, Done* done, int k) {
+    return each_pass(order, ws, ws_bytes, &need, [&](Table& tab, Arena& ar, int k) {
       for (int i = 0; i < tab.count; ++i) {
         Mat& t = tab.mat[i];
         t = Mat{static_cast<char*>(O) + (k + i) * stride_o * os, static_cast<const char*>(X) + (k + i) * stride_x * xs, nullptr,
@@ -1083,7 +1129,7 @@ extern "C" gnn_status gnn_orthogonalise(const void* X, int64_t ldx, int64_t stri
         t.slot = k + i;
       }
       place_pass(tab, ar);
-      return run_pass(ws, ar.used, tab, h, coeffs, steps, partial, done, norms, as_stream(stream));
+      return run_pass(ws, tab, h, coeffs, steps, norms, as_stream(stream));
     });
   });
 }
