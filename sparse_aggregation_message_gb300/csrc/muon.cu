@@ -468,12 +468,15 @@ __device__ __forceinline__ void multiply(uint32_t d, uint64_t a, uint64_t b, uin
     tc::mma_bf16(d, a, b, idesc, acc);
 }
 
+// Of a warp: its lanes go on, or give up, together.
+__device__ __forceinline__ bool all(bool x) { return __all_sync(0xffffffffu, x); }
+
 // COLS: of a tile; 256: a pair's.
 template <int COLS>
 __device__ __forceinline__ void walk(const Steps& g, uint8_t* smem_raw) {
   constexpr bool PAIR = COLS == 256;
   const Ring s = carve(smem_raw);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int rank = PAIR ? (int)tc::cluster_rank() : 0;
   const int unit = PAIR ? blockIdx.x >> 1 : blockIdx.x, units = PAIR ? gridDim.x >> 1 : gridDim.x;
   constexpr int a_stage = BLOCK, stage = BLOCK + (PAIR ? COLS / 2 : COLS) * 256;
@@ -520,10 +523,10 @@ __device__ __forceinline__ void walk(const Steps& g, uint8_t* smem_raw) {
       const int x = w.step & 1 ? w.m.x1 : w.m.x0, sq = 2 * w.m.mb;
       const int left = w.phase == GRAM ? x : w.phase == POLY ? w.m.a : w.m.p, left_nb = w.phase == GRAM ? w.m.nb : sq;
       const int rb = w.rb + rank, cb = w.cb + rank * (bn >> 6);
-      if (!wait_for<COLS>(g, w, s.abort_flag)) goto done;
       for (int kb = 0; kb < w.kb; ++kb) {
         if (!tc::mbar_wait(&s.empty[st], ph ^ 1, g.flags, s.abort_flag)) goto done;
         if (rank == 0) tc::mbar_expect_tx(&s.full[st], (PAIR ? 2 : 1) * (BLOCK + bn * 256));
+        if (kb == 0 && !wait_for<COLS>(g, w, s.abort_flag)) goto done;
         uint8_t* a = s.tiles + st * stage;
         const uint32_t bar = PAIR ? tc::map_to_rank(&s.full[st], 0) : tc::smem_u32(&s.full[st]);
         load_rows<PAIR>(g, a, bar, left, left_nb, 2 * rb, kb, true, w.phase == GRAM || above<PAIR>(rb, kb));
@@ -539,7 +542,8 @@ __device__ __forceinline__ void walk(const Steps& g, uint8_t* smem_raw) {
       if (!tc::mbar_wait(&s.empty[st], ph ^ 1, g.flags, s.abort_flag)) goto done;
       if (++st == stages) { st = 0; ph ^= 1; }
     }
-  } else if (warp == 1 && lane == 0 && rank == 0) {
+  } else if (warp == 1 && rank == 0) {
+    // the whole warp walks, one lane issues
     int st = 0, it = 0;
     uint32_t ph = 0;
     for (int t = unit; t < tiles; t += units) {
@@ -551,29 +555,32 @@ __device__ __forceinline__ void walk(const Steps& g, uint8_t* smem_raw) {
         const bool a_mn = w.phase != GRAM && !above<PAIR>(w.rb, kb);
         const bool b_mn = w.phase == NEXT || (w.phase == POLY && !above<PAIR>(w.cb >> 1, kb));
         const uint32_t idesc = tc::idesc_16(false, PAIR ? 256 : 128, PAIR ? w.cols : COLS, a_mn, b_mn);
-        if (!tc::mbar_wait<true>(&s.tempty[acc], ((it >> 1) & 1) ^ 1, g.flags, s.abort_flag)) goto done;
-        if (!tc::mbar_wait(&s.full[st], ph, g.flags, s.abort_flag)) goto done;
+        if (!all(tc::mbar_wait<true>(&s.tempty[acc], ((it >> 1) & 1) ^ 1, g.flags, s.abort_flag))) goto done;
+        if (!all(tc::mbar_wait(&s.full[st], ph, g.flags, s.abort_flag))) goto done;
         tc::fence_after_sync();
         const uint32_t at = tc::smem_u32(s.tiles + st * stage);
         const Operand l = operand(at, a_mn, true), r = operand(at + a_stage, b_mn, bn == 128);
+        if (tc::elect_one()) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          if (k >= some) break;
-          multiply<PAIR>(d, l.desc + k * l.step, r.desc + r.limb + k * r.step, idesc, k ? 1u : 0u);
-          multiply<PAIR>(d, l.desc + l.limb + k * l.step, r.desc + k * r.step, idesc, 1u);
-        }
+          for (int k = 0; k < 4; ++k) {
+            if (k >= some) break;
+            multiply<PAIR>(d, l.desc + k * l.step, r.desc + r.limb + k * r.step, idesc, k ? 1u : 0u);
+            multiply<PAIR>(d, l.desc + l.limb + k * l.step, r.desc + k * r.step, idesc, 1u);
+          }
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          if (k >= some) break;
-          multiply<PAIR>(d, l.desc + k * l.step, r.desc + k * r.step, idesc, 1u);
+          for (int k = 0; k < 4; ++k) {
+            if (k >= some) break;
+            multiply<PAIR>(d, l.desc + k * l.step, r.desc + k * r.step, idesc, 1u);
+          }
+          if (PAIR) {
+            tc::mma_commit_pair(&s.empty[st]);
+            tc::mma_commit_pair(&s.tfull[acc]);
+          } else {
+            tc::mma_commit(&s.empty[st]);
+            tc::mma_commit(&s.tfull[acc]);
+          }
         }
-        if (PAIR) {
-          tc::mma_commit_pair(&s.empty[st]);
-          tc::mma_commit_pair(&s.tfull[acc]);
-        } else {
-          tc::mma_commit(&s.empty[st]);
-          tc::mma_commit(&s.tfull[acc]);
-        }
+        __syncwarp();
         if (++st == stages) { st = 0; ph ^= 1; }
       }
     }
@@ -594,6 +601,7 @@ __device__ __forceinline__ void walk(const Steps& g, uint8_t* smem_raw) {
       if (!pending) return;
       if (lane == 0) {
         tc::bulk_wait_all();
+        if (MOST < 64) tc::mbar_arrive(&s.clear[q]);
         asm volatile("red.release.gpu.global.add.s32 [%0], 1;" ::"l"(pending) : "memory");
       }
       pending = nullptr;
@@ -608,8 +616,7 @@ __device__ __forceinline__ void walk(const Steps& g, uint8_t* smem_raw) {
       const int on_diag = row - (w.cb * 64 + half * mine);
       if (w.phase == POLY) {  // A, by ordinary loads
         count_it();
-        if (lane == 0 && !wait_for<COLS>(g, w, s.abort_flag)) goto done;
-        __syncwarp();
+        if (!all(lane || wait_for<COLS>(g, w, s.abort_flag))) goto done;
       }
       const int64_t a_at = (int64_t)w.m.a * BLOCK + ((int64_t)rb * out_nb + w.cb) * BLOCK + r * 128;
       uint4 a_hi[MOST < 64 ? 4 : 1], a_lo[MOST < 64 ? 4 : 1];
@@ -626,9 +633,9 @@ __device__ __forceinline__ void walk(const Steps& g, uint8_t* smem_raw) {
       for (int kb = 0; kb < w.kb; ++kb, ++it) {
         const int acc = it & 1;
         const float2 back = dup2(w.k16 - 4 * kb > 2 ? 1.f + 0x1p-23f : 1.f);
-        if (!tc::mbar_test(&s.tfull[acc], (it >> 1) & 1)) {
+        if (!all(tc::mbar_test(&s.tfull[acc], (it >> 1) & 1))) {
           count_it();
-          if (!tc::mbar_wait(&s.tfull[acc], (it >> 1) & 1, g.flags, s.abort_flag)) goto done;
+          if (!all(tc::mbar_wait(&s.tfull[acc], (it >> 1) & 1, g.flags, s.abort_flag))) goto done;
         }
         __syncwarp();
         tc::fence_after_sync();
@@ -687,12 +694,8 @@ __device__ __forceinline__ void walk(const Steps& g, uint8_t* smem_raw) {
         // stores each of their 16-byte pieces would be a transaction of its own
         if (MOST < 64) {
           // both warps' last tile has left (each sends one limb of it)
-          if (lane == 0) {
-            tc::bulk_wait_read<0>();
-            tc::mbar_arrive(&s.clear[q]);
-          }
-          if (!tc::mbar_wait(&s.clear[q], met, g.flags, s.abort_flag)) goto done;
-          __syncwarp();
+          count_it();
+          if (!all(tc::mbar_wait(&s.clear[q], met ^ 1, g.flags, s.abort_flag))) goto done;
 #pragma unroll
           for (int k = 0; k < CHUNKS; ++k) {
             uint4* to = reinterpret_cast<uint4*>(staged + lane * 128 + (((half * 4 + k) ^ (lane & 7)) << 4));
@@ -702,8 +705,7 @@ __device__ __forceinline__ void walk(const Steps& g, uint8_t* smem_raw) {
           tc::fence_async_smem();
           __syncwarp();
           if (lane == 0) tc::mbar_arrive(&s.filled[q]);
-          if (!tc::mbar_wait(&s.filled[q], met, g.flags, s.abort_flag)) goto done;
-          __syncwarp();
+          if (!all(tc::mbar_wait(&s.filled[q], met, g.flags, s.abort_flag))) goto done;
           met ^= 1;
           if (lane == 0) {
             tc::tma_store_2d(&g.out, staged + half * STAGED, 0, (int)(block * BLOCK_ROWS) + half * 128 + q * 32);

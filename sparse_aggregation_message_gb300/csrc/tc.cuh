@@ -11,6 +11,20 @@
 namespace gnn {
 namespace tc {
 
+// True in one lane of a converged warp.  What that lane issues under it takes its
+// operands from uniform registers, which a test of the lane number does not give.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n"
+      " .reg .pred p;\n"
+      " elect.sync _|p, 0xffffffff;\n"
+      " selp.u32 %0, 1, 0, p;\n"
+      "}\n"
+      : "=r"(p));
+  return p != 0;
+}
+
 // ~2 s at 2 GHz: no legitimate wait in these kernels comes close.
 constexpr long long kWaitCycles = 4000000000LL;
 
