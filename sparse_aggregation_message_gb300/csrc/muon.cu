@@ -51,6 +51,7 @@ struct Mat {
   int m, n;           // X's rows and columns
   int mb, nb;         // blocks of X: 128 rows, 64 columns
   int parts, slot;    // partial sums of squares; the matrix's number in the call
+  int quads;          // bits: rows of param, grad, mom, copy lie on borders of four elements
   char *x[2], *a, *p;
 };
 struct Table {
@@ -71,28 +72,74 @@ struct Hyper {
   int pt, gt, mt;  // types of param (output), grad (input), momentum
 };
 
-__device__ __forceinline__ float load_any(const void* p, int64_t i, int type) {
-  if (type == GNN_F32) return static_cast<const float*>(p)[i];
-  if (type == GNN_BF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
-  return __half2float(static_cast<const __half*>(p)[i]);
+// Four elements of a row from column c, zero past `cols`; in one access where the
+// rows allow it.
+__device__ __forceinline__ float4 load4(const void* p, int64_t row, int64_t c, int64_t cols, int type, bool quad) {
+  float v[4] = {0.f, 0.f, 0.f, 0.f};
+  if (quad && c + 4 <= cols) {
+    if (type == GNN_F32) return *reinterpret_cast<const float4*>(static_cast<const float*>(p) + row + c);
+    const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + row + c);
+    const float2 a = type == GNN_BF16 ? Pack2<__nv_bfloat16>::from(w.x) : Pack2<__half>::from(w.x);
+    const float2 b = type == GNN_BF16 ? Pack2<__nv_bfloat16>::from(w.y) : Pack2<__half>::from(w.y);
+    return make_float4(a.x, a.y, b.x, b.y);
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (c + j < cols) {
+      const int64_t i = row + c + j;
+      v[j] = type == GNN_F32    ? static_cast<const float*>(p)[i]
+             : type == GNN_BF16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i])
+                                : __half2float(static_cast<const __half*>(p)[i]);
+    }
+  }
+  return make_float4(v[0], v[1], v[2], v[3]);
 }
-__device__ __forceinline__ void store_any(void* p, int64_t i, int type, float v) {
-  if (type == GNN_F32)
-    static_cast<float*>(p)[i] = v;
-  else if (type == GNN_BF16)
-    static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
-  else
-    static_cast<__half*>(p)[i] = __float2half_rn(v);
+__device__ __forceinline__ void store4(void* p, int64_t row, int64_t c, int64_t cols, int type, bool quad, float4 f) {
+  if (quad && c + 4 <= cols) {
+    if (type == GNN_F32) {
+      *reinterpret_cast<float4*>(static_cast<float*>(p) + row + c) = f;
+    } else {
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p) + row + c) =
+          type == GNN_BF16 ? make_uint2(Pack2<__nv_bfloat16>::to(f.x, f.y), Pack2<__nv_bfloat16>::to(f.z, f.w))
+                           : make_uint2(Pack2<__half>::to(f.x, f.y), Pack2<__half>::to(f.z, f.w));
+    }
+    return;
+  }
+  const float v[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (c + j < cols) {
+      const int64_t i = row + c + j;
+      if (type == GNN_F32)
+        static_cast<float*>(p)[i] = v[j];
+      else if (type == GNN_BF16)
+        static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v[j]);
+      else
+        static_cast<__half*>(p)[i] = __float2half_rn(v[j]);
+    }
+  }
+}
+enum { PARAM = 1, GRAD = 2, MOM = 4, COPY = 8 };  // of Mat::quads
+
+__device__ __forceinline__ float4 axpy4(float4 x, float a, float4 y) {
+  return make_float4(fmaf(x.x, a, y.x), fmaf(x.y, a, y.y), fmaf(x.z, a, y.z), fmaf(x.w, a, y.w));
 }
 
-// The momentum and the update that is orthogonalised, of one element.
-__device__ __forceinline__ float update_of(const Mat& t, const Hyper& h, int64_t r, int64_t c, float* mom) {
-  const float g = load_any(t.grad, r * t.ldg + c, h.gt) * h.grad_scale;
-  if (h.orth) return g;
-  const float m = fmaf(load_any(t.mom, r * t.ldm + c, h.mt), h.momentum, g);
-  *mom = m;
-  return h.nesterov ? fmaf(m, h.momentum, g) : m;
-}
+// A gradient and a momentum as they were, and the update that is orthogonalised.
+struct Quad {
+  float4 g, m;
+  __device__ __forceinline__ void load(const Mat& t, const Hyper& h, int64_t row, int64_t c, int64_t cols) {
+    g = load4(t.grad, row * t.ldg, c, cols, h.gt, t.quads & GRAD);
+    if (!h.orth) m = load4(t.mom, row * t.ldm, c, cols, h.mt, t.quads & MOM);
+  }
+  // m becomes the new momentum
+  __device__ __forceinline__ float4 update(const Hyper& h) {
+    g = make_float4(g.x * h.grad_scale, g.y * h.grad_scale, g.z * h.grad_scale, g.w * h.grad_scale);
+    if (h.orth) return g;
+    m = axpy4(m, h.momentum, g);
+    return h.nesterov ? axpy4(m, h.momentum, g) : m;
+  }
+};
 
 __device__ __forceinline__ int mat_of(const Table& tab, int k) {
   int i = 0;
@@ -117,25 +164,31 @@ __global__ void __launch_bounds__(THREADS) square_kernel(const __grid_constant__
   const Mat& t = tab.mat[i];
   const int part = blockIdx.x - tab.first[i];
   double sum = 0;
-  float mom;
-  // rows that lie end to end are one long row
+  // rows that lie end to end are one long row, and each part has a piece of it
   const bool flat = t.ldg == t.cols && (h.orth || t.ldm == t.cols);
   const int64_t cols = flat ? (int64_t)t.rows * t.cols : t.cols, rows = flat ? 1 : t.rows;
-  const int64_t share = flat ? (cols + t.parts - 1) / t.parts : (rows + t.parts - 1) / t.parts;
+  const int64_t share = flat ? ((cols + t.parts - 1) / t.parts + 3) / 4 * 4 : (rows + t.parts - 1) / t.parts;
   const int64_t lo = part * share, hi = min(lo + share, flat ? cols : rows);
   const int64_t r0 = flat ? 0 : lo, r1 = flat ? 1 : hi, c0 = flat ? lo : 0, c1 = flat ? hi : cols;
+  constexpr int AHEAD = 4;
   for (int64_t r = r0; r < r1; ++r) {
-    for (int64_t c = c0 + threadIdx.x; c < c1; c += 8 * THREADS) {
-      float u[8], s = 0.f;
+    for (int64_t c = c0 + 4 * threadIdx.x; c < c1; c += 4 * AHEAD * THREADS) {
+      Quad q[AHEAD];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) u[k] = c + k * THREADS < c1 ? update_of(t, h, r, c + k * THREADS, &mom) : 0.f;
+      for (int k = 0; k < AHEAD; ++k) q[k].load(t, h, r, c + 4 * k * THREADS, c1);
+      float s = 0.f;
+      float4 u[AHEAD];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) s = fmaf(u[k], u[k], s);
+      for (int k = 0; k < AHEAD; ++k) {
+        u[k] = q[k].update(h);
+        s = fmaf(u[k].x, u[k].x, fmaf(u[k].y, u[k].y, fmaf(u[k].z, u[k].z, fmaf(u[k].w, u[k].w, s))));
+      }
       if (s > 1e-28f && s < 1e38f) {
         sum += (double)s;
       } else {  // outside of what fp32 holds well
 #pragma unroll
-        for (int k = 0; k < 8; ++k) sum += (double)u[k] * (double)u[k];
+        for (int k = 0; k < AHEAD; ++k)
+          sum += (double)u[k].x * u[k].x + (double)u[k].y * u[k].y + (double)u[k].z * u[k].z + (double)u[k].w * u[k].w;
       }
     }
   }
@@ -183,23 +236,42 @@ __global__ void __launch_bounds__(THREADS) begin_kernel(const __grid_constant__ 
   const int i = mat_of(tab, blockIdx.x);
   const Mat& t = tab.mat[i];
   const int block = blockIdx.x - tab.first[i], r0 = block / t.nb * 128, c0 = block % t.nb * 64;
+  // in the order of the caller's rows, 64 or (transposed) 128 columns of them
+  const int across = t.flip ? 32 : 16, row0 = t.flip ? c0 : r0, col0 = t.flip ? r0 : c0;
+  constexpr int QUADS = 128 * 64 / 4 / THREADS, AHEAD = 4;
+  Quad q[AHEAD];
+  auto place = [&](int k, int& row, int& col) {
+    const int e = threadIdx.x + k * THREADS;
+    row = e / across, col = e % across * 4;
+  };
+  auto load = [&](int k, Quad& to) {
+    int row, col;
+    place(k, row, col);
+    to.load(t, h, min(row0 + row, t.rows - 1), col0 + col, row0 + row < t.rows ? t.cols : 0);
+  };
+#pragma unroll
+  for (int k = 0; k < AHEAD; ++k) load(k, q[k]);
   const double norm = norm_of(tab.partial, i, t.parts, &sm);
   const bool good = isfinite((float)norm);
-  const float inv = good ? (float)((double)UNIT / (norm + h.eps)) : 0.f;
+  const float inv = (float)((double)UNIT / (norm + h.eps));
   if (block == 0 && threadIdx.x == 0 && norms) norms[t.slot] = (float)norm;
-  // in the order of the caller's rows
-  const int across = t.flip ? 128 : 64;
-  for (int e = threadIdx.x; e < 128 * 64; e += THREADS) {
-    const int b = e % across, a = e / across;
-    const int r = t.flip ? b : a, c = t.flip ? a : b;
-    float u = 0.f;
-    if (r0 + r < t.m && c0 + c < t.n && good) {
-      const int64_t row = t.flip ? c0 + c : r0 + r, col = t.flip ? r0 + r : c0 + c;
-      float mom;
-      u = update_of(t, h, row, col, &mom) * inv;
-      if (!h.orth) store_any(t.mom, row * t.ldm + col, h.mt, mom);
+#pragma unroll
+  for (int k0 = 0; k0 < QUADS; k0 += AHEAD) {
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) {
+      int row, col;
+      place(k0 + k, row, col);
+      float4 u = q[k].update(h);
+      if (!h.orth && good && row0 + row < t.rows && col0 + col < t.cols)
+        store4(t.mom, (int64_t)(row0 + row) * t.ldm, col0 + col, t.cols, h.mt, t.quads & MOM, q[k].m);
+      u = good ? make_float4(u.x * inv, u.y * inv, u.z * inv, u.w * inv) : make_float4(0.f, 0.f, 0.f, 0.f);
+      if (t.flip) {
+        tile[col][row] = u.x, tile[col + 1][row] = u.y, tile[col + 2][row] = u.z, tile[col + 3][row] = u.w;
+      } else {
+        tile[row][col] = u.x, tile[row][col + 1] = u.y, tile[row][col + 2] = u.z, tile[row][col + 3] = u.w;
+      }
+      if (k0 + AHEAD < QUADS) load(k0 + AHEAD + k, q[k]);
     }
-    tile[r][c] = u;
   }
   __syncthreads();
   char* x = t.x[0] + (int64_t)block * BLOCK;
@@ -241,19 +313,23 @@ __global__ void __launch_bounds__(THREADS) apply_kernel(const __grid_constant__ 
     }
   }
   __syncthreads();
-  const int across = t.flip ? 128 : 64;
-  for (int e = threadIdx.x; e < 128 * 64; e += THREADS) {
-    const int b = e % across, a = e / across;
-    const int r = t.flip ? b : a, c = t.flip ? a : b;
-    if (r0 + r >= t.m || c0 + c >= t.n) continue;
-    const int64_t row = t.flip ? c0 + c : r0 + r, col = t.flip ? r0 + r : c0 + c;
-    const float o = good ? tile[r][c] : __int_as_float(0x7fc00000);
+  const int across = t.flip ? 32 : 16, row0 = t.flip ? c0 : r0, col0 = t.flip ? r0 : c0;
+#pragma unroll 4
+  for (int e = threadIdx.x; e < 128 * 64 / 4; e += THREADS) {
+    const int row = e / across, col = e % across * 4;
+    if (row0 + row >= t.rows || col0 + col >= t.cols) continue;
+    float4 o = t.flip ? make_float4(tile[col][row], tile[col + 1][row], tile[col + 2][row], tile[col + 3][row])
+                      : make_float4(tile[row][col], tile[row][col + 1], tile[row][col + 2], tile[row][col + 3]);
+    const int64_t at = (int64_t)(row0 + row) * t.ldp;
     if (h.orth) {
-      store_any(t.param, row * t.ldp + col, h.pt, o);
+      const float nan = __int_as_float(0x7fc00000);
+      if (!good) o = make_float4(nan, nan, nan, nan);
+      store4(t.param, at, col0 + col, t.cols, h.pt, t.quads & PARAM, o);
     } else {
-      const float p = fmaf(-h.lr * t.scale, o, load_any(t.param, row * t.ldp + col, h.pt) * h.decay);
-      store_any(t.param, row * t.ldp + col, h.pt, p);
-      if (t.copy) reinterpret_cast<__nv_bfloat16*>(t.copy)[row * t.ldc + col] = __float2bfloat16_rn(p);
+      const float4 p = load4(t.param, at, col0 + col, t.cols, h.pt, t.quads & PARAM);
+      const float4 n = axpy4(o, -h.lr * t.scale, make_float4(p.x * h.decay, p.y * h.decay, p.z * h.decay, p.w * h.decay));
+      store4(t.param, at, col0 + col, t.cols, h.pt, t.quads & PARAM, n);
+      if (t.copy) store4(t.copy, (int64_t)(row0 + row) * t.ldc, col0 + col, t.cols, GNN_BF16, t.quads & COPY, n);
     }
   }
 }
@@ -840,23 +916,25 @@ int sms_there() {
 }
 
 // One product's clocks on tiles of bn columns (0: pairs, 256 or with half 128
-// columns): rounds of tiles, each as long as its MMAs take, or its share of what L2
-// delivers (50 bytes a clock and SM).
+// columns): from a tile's last product to the first of what waits for it, and for
+// every 64 of k what the MMAs, or shared memory for smaller tiles, take.  Fitted to steps
+// of 1 to 12 matrices of 64 x 64 to 1024 x 4096 (within 15%).  Several matrices fill each
+// other's last rounds.
 double clocks(const Table& tab, Phase ph, int bn, int half) {
-  const int units = bn ? SMS : SMS / 2, cols = bn ? bn : half ? 64 : 128;  // of a CTA's share of B
+  const double between = bn == 64 ? 7000 : bn ? 11000 : half ? 12000 : 18000;
+  const double each = bn == 64 ? 1050 : bn ? 1130 : half ? 983 : 1490;
+  const int units = bn ? SMS : SMS / 2;
   double total = 0, longest = 0;
   int64_t tiles = 0;
   for (int i = 0; i < tab.count; ++i) {
     Mat t = tab.mat[i];
     sides(t, bn);
-    const double len = (ph == GRAM ? t.n : t.m) / 64 + 1;
+    const double len = ((ph == GRAM ? t.n : t.m) + 63) / 64;
     const int64_t k = tiles_in(t, ph, bn, half);
     tiles += k, total += k * len, longest = std::max(longest, len);
   }
-  const double active = (double)std::min<int64_t>(tiles, units) * (bn ? 1 : 2);
-  const double each = std::max(bn ? 6.0 * bn : 12.0 * cols, active * (BLOCK + cols * 256) / (50.0 * SMS));
-  const double rounds = (double)((tiles + units - 1) / units);
-  return std::max(rounds * total / tiles, longest) * each + 3000;
+  const double rounds = tab.count == 1 ? (double)((tiles + units - 1) / units) * longest : total / units;
+  return std::max(rounds, longest) * each + between;
 }
 double clocks(const Table& tab, int bn, const int (&half)[3]) {
   return clocks(tab, GRAM, bn, half[GRAM]) + clocks(tab, POLY, bn, half[POLY]) + clocks(tab, NEXT, bn, half[NEXT]);
@@ -997,6 +1075,9 @@ gnn_status guarded(const char* who, Fn f) {
   }
 }
 
+// Whether four elements from a column that is a multiple of four are one access.
+bool quad_rows(const void* p, int64_t ld, int elem) { return aligned_to(p, 4 * elem) && ld % 4 == 0; }
+
 Span span(const void* p, const gnn_muon_tensor& t, int64_t ld, int elem) { return {p, t.rows, ld * elem, (int64_t)t.cols * elem}; }
 
 }  // namespace
@@ -1067,6 +1148,8 @@ extern "C" gnn_status gnn_muon_step(const gnn_muon_tensor* tensors, int32_t n_te
         Mat& t = tab.mat[i];
         t = Mat{d.param, d.grad, d.m, d.copy, d.ldp, d.ldg, d.ldm, d.ldc, d.scale, d.rows, d.cols};
         t.slot = order[k + i];
+        t.quads = (quad_rows(d.param, d.ldp, ps) ? PARAM : 0) | (quad_rows(d.grad, d.ldg, gs) ? GRAD : 0) |
+                  (quad_rows(d.m, d.ldm, ms) ? MOM : 0) | (d.copy && quad_rows(d.copy, d.ldc, 2) ? COPY : 0);
       }
       place_pass(tab, ar);
       return run_pass(ws, tab, h, coeffs, steps, norms, as_stream(stream));
@@ -1129,6 +1212,7 @@ extern "C" gnn_status gnn_orthogonalise(const void* X, int64_t ldx, int64_t stri
         t = Mat{static_cast<char*>(O) + (k + i) * stride_o * os, static_cast<const char*>(X) + (k + i) * stride_x * xs, nullptr,
                 nullptr, ldo, ldx, 0, 0, 1.f, rows, cols};
         t.slot = k + i;
+        t.quads = (quad_rows(t.param, ldo, os) ? PARAM : 0) | (quad_rows(t.grad, ldx, xs) ? GRAD : 0);
       }
       place_pass(tab, ar);
       return run_pass(ws, tab, h, coeffs, steps, norms, as_stream(stream));
