@@ -4,11 +4,14 @@
 // and its backward, row by row.  Every matrix is read once and written once; what
 // bounds both passes is DRAM.
 //
-// A row belongs to a group of L lanes with eight channels each in registers, so that
-// a row's statistics, its sum and the second norm need one read: 4 to 32 lanes
-// (several rows to a warp when rows are short), or several warps that add through
-// shared memory.  The rows ahead arrive in a ring in shared memory by asynchronous
-// copies; each lane copies and reads its own pieces, so the ring has no barriers.
+// A row belongs to a group of L lanes with K times eight channels each in registers,
+// so that a row's statistics, its sum and the second norm need one read: 4 to 32
+// lanes of a warp (several rows to a warp when rows are short) and K of 1 to 4, or, past
+// 1024 channels, several warps that add through shared memory.  (Several warps from
+// 257 channels on: 232,965 x 602 backward in fp32 1,066 us, forward 913 for 200,000
+// rows; their barriers were what they waited for.)  The rows ahead arrive in a ring in
+// shared memory by asynchronous copies; each lane copies and reads its own pieces, so
+// the ring has no barriers.
 #include <cuda_runtime.h>
 #include <math.h>
 
@@ -23,6 +26,7 @@ namespace gnn {
 namespace {
 
 constexpr int THREADS = 256;  // of a block; rows of more than 256 lanes: one row's
+constexpr int FEW = 128;      // where a lane has more than one vector
 constexpr int MAX_LANES = 512;
 constexpr int MAX_C = 8 * MAX_LANES;
 
@@ -40,7 +44,7 @@ struct Args {
   int scale_cols;         // 0, 1 or C
   float eps, inv_c;
   float4* stats;
-  float* part;            // backward: [blocks][4][8 lanes]
+  float* part;            // backward: [blocks][4][8 lanes K]
   int want_q, want_p;     // backward: which sums over all rows are kept
   // the ring: stages, 16-byte pieces of a lane in one, and where each matrix's begin
   int stages, pieces, at[5];
@@ -97,15 +101,6 @@ __device__ __forceinline__ void put(void* base, int64_t at, Eight& x, int cnt, b
   } else {
     *reinterpret_cast<uint4*>(p) = make_uint4(Pack2<T>::to(x[0].x, x[0].y), Pack2<T>::to(x[1].x, x[1].y),
                                               Pack2<T>::to(x[2].x, x[2].y), Pack2<T>::to(x[3].x, x[3].y));
-  }
-}
-
-// Eight of a vector of weights, `none` where there is no vector; zero past its end.
-__device__ __forceinline__ void weights(const float* p, int c, int cnt, float none, Eight& w) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    w[i].x = 2 * i < cnt ? (p ? __ldg(p + c + 2 * i) : none) : 0.f;
-    w[i].y = 2 * i + 1 < cnt ? (p ? __ldg(p + c + 2 * i + 1) : none) : 0.f;
   }
 }
 
@@ -166,24 +161,31 @@ struct Row {
   }
 };
 
-// Mean and 1/deviation of a row; the variance about the mean.
-template <bool MULTI>
-__device__ __forceinline__ void statistics(const Eight& x, int cnt, int kind, float eps, float inv_c, Row<MULTI>& row,
-                                           float& mean, float& rstd) {
+// Mean and 1/deviation of a row; the variance about the mean.  `cnt`: channels from
+// this lane's first on, `span` from one of its vectors to the next.
+template <int K, bool MULTI>
+__device__ __forceinline__ void statistics(const Eight (&x)[K], int cnt, int span, int kind, float eps, float inv_c,
+                                           Row<MULTI>& row, float& mean, float& rstd) {
   mean = 0.f, rstd = 1.f;
   if (kind == GNN_NORM_NONE) return;
-  float s[1];
+  float s[1] = {0.f};
   if (kind == GNN_NORM_LAYER) {
-    s[0] = add_up(x);
+#pragma unroll
+    for (int k = 0; k < K; ++k) s[0] += add_up(x[k]);
     row.sum(s);
     mean = s[0] * inv_c;
-    Eight d;
+    s[0] = 0.f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) d[i] = add2_rn(x[i], dup2(-mean));
-    mask(d, cnt);
-    s[0] = dot(d, d);
+    for (int k = 0; k < K; ++k) {
+      Eight d;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) d[i] = add2_rn(x[k][i], dup2(-mean));
+      mask(d, cnt - k * span);
+      s[0] += dot(d, d);
+    }
   } else {
-    s[0] = dot(x, x);
+#pragma unroll
+    for (int k = 0; k < K; ++k) s[0] += dot(x[k], x[k]);
   }
   row.sum(s);
   rstd = inv_root(fmaf(s[0], inv_c, eps));
@@ -194,6 +196,27 @@ __device__ __forceinline__ void normalise(Eight& x, int cnt, float mean, float r
 #pragma unroll
   for (int i = 0; i < 4; ++i) x[i] = mul2_rn(add2_rn(x[i], dup2(-mean)), dup2(rstd));
   mask(x, cnt);
+}
+
+// Eight weights of this lane from the block's copy of a vector.
+__device__ __forceinline__ void from_shared(const float* p, Eight& w) {
+  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+  w[0] = make_float2(a.x, a.y), w[1] = make_float2(a.z, a.w), w[2] = make_float2(b.x, b.y), w[3] = make_float2(b.z, b.w);
+}
+
+// s w_post, s b_post, w_pre and (forward) b_pre of the block's `width` channels, zero
+// past the row's end.
+template <bool FWD>
+__device__ __forceinline__ void share_weights(const Args& g, float* to, int width) {
+  for (int c = threadIdx.x; c < width; c += blockDim.x) {
+    const bool there = c < g.C;
+    const float s = there ? (g.scale_cols == 0 ? 1.f : __ldg(g.scale + (g.scale_cols == 1 ? 0 : c))) : 0.f;
+    to[c] = s * (there && g.w_post ? __ldg(g.w_post + c) : 1.f);
+    to[width + c] = there && g.b_post ? s * __ldg(g.b_post + c) : 0.f;
+    to[2 * width + c] = there ? (g.w_pre ? __ldg(g.w_pre + c) : 1.f) : 0.f;
+    if (FWD) to[3 * width + c] = there && g.b_pre ? __ldg(g.b_pre + c) : 0.f;
+  }
+  __syncthreads();
 }
 
 template <int N>
@@ -210,49 +233,39 @@ __device__ __forceinline__ void wait_row(int stages) {
     wait_copies<1>();
 }
 
-template <class TB, class TR, class TY, bool MULTI>
-__global__ void __launch_bounds__(MULTI ? MAX_LANES : THREADS) residual_fwd_kernel(const __grid_constant__ Args g) {
-  extern __shared__ uint4 ring[];
+template <class TB, class TR, class TY, bool MULTI, int K>
+__global__ void __launch_bounds__(MULTI ? MAX_LANES : K == 1 ? THREADS : FEW, MULTI ? 1 : K == 1 ? 2 : K == 2 ? 4 : 3)
+    residual_fwd_kernel(const __grid_constant__ Args g) {
+  extern __shared__ uint4 smem[];
   __shared__ float sm[MULTI ? 2 * 4 * (MAX_LANES / 32) : 1];
   cudaTriggerProgrammaticLaunchCompletion();
   cudaGridDependencySynchronize();
   Row<MULTI> row(g.lanes, sm);
-  const int threads = blockDim.x, groups = threads / g.lanes;
+  const int threads = blockDim.x, groups = threads / g.lanes, span = 8 * g.lanes, width = K * span;
   const int64_t step = (int64_t)gridDim.x * groups;
   // the warp's first row: its groups leave the loop together
   const int ahead = MULTI ? 0 : row.group & (32 / g.lanes - 1);
   const int c = 8 * row.lane, cnt = g.C - c;
   const bool odd = row.lane & 1;
-  Eight w1, b1, w2, b2;  // s w_post, s b_post, w_pre, b_pre
-  {
-    Eight s;
-    weights(g.w_post, c, cnt, 1.f, w1);
-    weights(g.b_post, c, cnt, 0.f, b1);
-    if (g.scale_cols == 1) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) s[i] = dup2(__ldg(g.scale));
-    } else {
-      weights(g.scale, c, cnt, 1.f, s);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w1[i] = mul2_rn(w1[i], s[i]), b1[i] = mul2_rn(b1[i], s[i]);
-    weights(g.w_pre, c, cnt, 1.f, w2);
-    weights(g.b_pre, c, cnt, 0.f, b2);
-  }
-  uint4* mine = ring + threadIdx.x;
-  const int stage_size = g.pieces * threads;
+  float* const w_at = reinterpret_cast<float*>(smem);
+  uint4* const mine = smem + width + threadIdx.x;
+  const int stage_size = K * g.pieces * threads;
   auto request = [&](int st, int64_t i) {
-    uint4* to = mine + st * stage_size;
-    const int m = i < g.n ? cnt : 0;
-    fetch<TR>(to + g.at[0] * threads, threads, g.R, i * g.ldr + c, m);
-    if (g.B) fetch<TB>(to + g.at[1] * threads, threads, g.B, i * g.ldb + c, m);
-    if (g.gate == 2) fetch<TB>(to + g.at[2] * threads, threads, g.G, i * g.ldg + c, m);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      uint4* to = mine + st * stage_size + k * g.pieces * threads;
+      const int m = i < g.n ? cnt - k * span : 0, ck = c + k * span;
+      fetch<TR>(to + g.at[0] * threads, threads, g.R, i * g.ldr + ck, m);
+      if (g.B) fetch<TB>(to + g.at[1] * threads, threads, g.B, i * g.ldb + ck, m);
+      if (g.gate == 2) fetch<TB>(to + g.at[2] * threads, threads, g.G, i * g.ldg + ck, m);
+    }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
   auto row_gate = [&](int64_t i) { return g.gate == 1 && i < g.n ? to_f32(static_cast<const TB*>(g.G)[i * g.ldg]) : 0.f; };
   int64_t i = (int64_t)blockIdx.x * groups + row.group;
   for (int k = 0; k < g.stages - 1; ++k) request(k, i + k * step);
   float t_next = row_gate(i);
+  share_weights<true>(g, w_at, width);
   int st = 0, into = g.stages - 1;
   for (; i - ahead < g.n; i += step) {
     request(into, i + (g.stages - 1) * step);
@@ -261,88 +274,94 @@ __global__ void __launch_bounds__(MULTI ? MAX_LANES : THREADS) residual_fwd_kern
     wait_row(g.stages);
     const bool live = i < g.n;
     const uint4* from = mine + st * stage_size;
+    auto piece = [&](int which, int k) { return from + (k * g.pieces + g.at[which]) * threads; };
     if (++st == g.stages) st = 0;
     if (++into == g.stages) into = 0;
     float4 stat = make_float4(0.f, 1.f, 0.f, 1.f);
-    Eight h;
-    take<TR>(from + g.at[0] * threads, threads, cnt, h);
+    Eight h[K];
     if (g.B) {
-      Eight x, t;
-      take<TB>(from + g.at[1] * threads, threads, cnt, x);
-      statistics(x, cnt, g.post, g.eps, g.inv_c, row, stat.x, stat.y);
-      if (g.gate == 2) {
-        take<TB>(from + g.at[2] * threads, threads, cnt, t);
-        with_act(g.act, [&](auto A) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) t[j] = act2(t[j], A);
-        });
-      } else {
-        const float t1 = g.gate == 1 ? act_f(t_row, g.act) : 1.f;
+      for (int k = 0; k < K; ++k) take<TB>(piece(1, k), threads, cnt - k * span, h[k]);
+      statistics<K>(h, cnt, span, g.post, g.eps, g.inv_c, row, stat.x, stat.y);
+      const float t1 = g.gate == 1 ? act_f(t_row, g.act) : 1.f;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) t[j] = dup2(t1);
+      for (int k = 0; k < K; ++k) {
+        const int m = cnt - k * span;
+        Eight t, w, b, r;
+        if (g.gate == 2) {
+          take<TB>(piece(2, k), threads, m, t);
+          with_act(g.act, [&](auto A) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) t[j] = act2(t[j], A);
+          });
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) t[j] = dup2(t1);
+        }
+        normalise(h[k], m, stat.x, stat.y);
+        from_shared(w_at + c + k * span, w);
+        from_shared(w_at + width + c + k * span, b);
+        take<TR>(piece(0, k), threads, m, r);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) h[k][j] = fma2_rn(t[j], fma2_rn(w[j], h[k][j], b[j]), r[j]);
+        mask(h[k], m);
       }
-      normalise(x, cnt, stat.x, stat.y);
+    } else {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) h[j] = fma2_rn(t[j], fma2_rn(w1[j], x[j], b1[j]), h[j]);
-      mask(h, cnt);
+      for (int k = 0; k < K; ++k) take<TR>(piece(0, k), threads, cnt - k * span, h[k]);
     }
-    if (g.H && live) put<TR>(g.H, i * g.ldh + c, h, cnt, odd);
-    if (g.pre != GNN_NORM_NONE) {
-      statistics(h, cnt, g.pre, g.eps, g.inv_c, row, stat.z, stat.w);
-      normalise(h, cnt, stat.z, stat.w);
+    if (g.H && live) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) h[j] = fma2_rn(w2[j], h[j], b2[j]);
-      if (live) put<TY>(g.Y, i * g.ldy + c, h, cnt, odd);
+      for (int k = 0; k < K; ++k) put<TR>(g.H, i * g.ldh + c + k * span, h[k], cnt - k * span, odd);
+    }
+    if (g.pre != GNN_NORM_NONE) {
+      statistics<K>(h, cnt, span, g.pre, g.eps, g.inv_c, row, stat.z, stat.w);
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        const int m = cnt - k * span;
+        Eight w, b;
+        normalise(h[k], m, stat.z, stat.w);
+        from_shared(w_at + 2 * width + c + k * span, w);
+        from_shared(w_at + 3 * width + c + k * span, b);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) h[k][j] = fma2_rn(w[j], h[k][j], b[j]);
+        if (live) put<TY>(g.Y, i * g.ldy + c + k * span, h[k], m, odd);
+      }
     }
     if (g.stats && live && row.lane == 0) g.stats[i] = stat;
   }
 }
 
-template <class TB, class TR, class TY, bool MULTI>
-__global__ void __launch_bounds__(MULTI ? MAX_LANES : THREADS, MULTI ? 1 : 2)
+template <class TB, class TR, class TY, bool MULTI, int K>
+__global__ void __launch_bounds__(MULTI ? MAX_LANES : K == 1 ? THREADS : FEW, MULTI ? 1 : K == 1 ? 2 : K == 2 ? 3 : 2)
     residual_bwd_kernel(const __grid_constant__ Args g) {
-  extern __shared__ uint4 ring[];
+  extern __shared__ uint4 smem[];
   __shared__ float sm[MULTI ? 2 * 4 * (MAX_LANES / 32) : 1];
   cudaTriggerProgrammaticLaunchCompletion();
   cudaGridDependencySynchronize();
   Row<MULTI> row(g.lanes, sm);
-  const int threads = blockDim.x, groups = threads / g.lanes;
+  const int threads = blockDim.x, groups = threads / g.lanes, span = 8 * g.lanes, width = K * span;
   const int64_t step = (int64_t)gridDim.x * groups;
   const int ahead = MULTI ? 0 : row.group & (32 / g.lanes - 1);
   const int c = 8 * row.lane, cnt = g.C - c;
   const bool odd = row.lane & 1;
-  Eight w1, b1, w2;  // s w_post, s b_post, w_pre
-  {
-    Eight s;
-    weights(g.w_post, c, cnt, 1.f, w1);
-    weights(g.b_post, c, cnt, 0.f, b1);
-    if (g.scale_cols == 1) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) s[i] = dup2(__ldg(g.scale));
-    } else {
-      weights(g.scale, c, cnt, 1.f, s);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w1[i] = mul2_rn(w1[i], s[i]), b1[i] = mul2_rn(b1[i], s[i]);
-    weights(g.w_pre, c, cnt, 1.f, w2);
-  }
-  Eight acc[4];  // sums of dY yh, dY, D t bh, D t
-#pragma unroll
-  for (int a = 0; a < 4; ++a)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) acc[a][j] = dup2(0.f);
-  uint4* mine = ring + threadIdx.x;
-  const int stage_size = g.pieces * threads;
+  float* const w_at = reinterpret_cast<float*>(smem);
+  uint4* const ring = smem + 3 * width / 4;
+  uint4* const mine = ring + threadIdx.x;
+  const int stage_size = K * g.pieces * threads;
   auto request = [&](int st, int64_t i) {
-    uint4* to = mine + st * stage_size;
-    const int m = i < g.n ? cnt : 0;
-    if (g.dY) {
-      fetch<TY>(to + g.at[0] * threads, threads, g.dY, i * g.ldy + c, m);
-      fetch<TR>(to + g.at[1] * threads, threads, g.H, i * g.ldh + c, m);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      uint4* to = mine + st * stage_size + k * g.pieces * threads;
+      const int m = i < g.n ? cnt - k * span : 0, ck = c + k * span;
+      if (g.dY) {
+        fetch<TY>(to + g.at[0] * threads, threads, g.dY, i * g.ldy + ck, m);
+        fetch<TR>(to + g.at[1] * threads, threads, g.H, i * g.ldh + ck, m);
+      }
+      if (g.dH) fetch<TR>(to + g.at[2] * threads, threads, g.dH, i * g.lddh + ck, m);
+      if (g.B) fetch<TB>(to + g.at[3] * threads, threads, g.B, i * g.ldb + ck, m);
+      if (g.gate == 2) fetch<TB>(to + g.at[4] * threads, threads, g.G, i * g.ldg + ck, m);
     }
-    if (g.dH) fetch<TR>(to + g.at[2] * threads, threads, g.dH, i * g.lddh + c, m);
-    if (g.B) fetch<TB>(to + g.at[3] * threads, threads, g.B, i * g.ldb + c, m);
-    if (g.gate == 2) fetch<TB>(to + g.at[4] * threads, threads, g.G, i * g.ldg + c, m);
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
   auto row_gate = [&](int64_t i) { return g.gate == 1 && i < g.n ? to_f32(static_cast<const TB*>(g.G)[i * g.ldg]) : 0.f; };
@@ -351,6 +370,14 @@ __global__ void __launch_bounds__(MULTI ? MAX_LANES : THREADS, MULTI ? 1 : 2)
   for (int k = 0; k < g.stages - 1; ++k) request(k, i + k * step);
   float t_next = row_gate(i);
   float4 s_next = row_stats(i);
+  share_weights<false>(g, w_at, width);
+  Eight acc[4][K];  // sums of dY yh, dY, D t bh, D t
+#pragma unroll
+  for (int a = 0; a < 4; ++a)
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[a][k][j] = dup2(0.f);
   int st = 0, into = g.stages - 1;
   for (; i - ahead < g.n; i += step) {
     request(into, i + (g.stages - 1) * step);
@@ -360,28 +387,32 @@ __global__ void __launch_bounds__(MULTI ? MAX_LANES : THREADS, MULTI ? 1 : 2)
     wait_row(g.stages);
     const bool live = i < g.n;
     const uint4* from = mine + st * stage_size;
+    auto piece = [&](int which, int k) { return from + (k * g.pieces + g.at[which]) * threads; };
     if (++st == g.stages) st = 0;
     if (++into == g.stages) into = 0;
-    Eight d;
-    if (g.dH) {
-      take<TR>(from + g.at[2] * threads, threads, cnt, d);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) d[j] = dup2(0.f);
-    }
+    Eight d[K];
     if (g.dY) {
-      // q = w dY; D = dH + rstd (q - mean q - yh mean(q yh))
-      Eight q, yh;
-      take<TY>(from + g.at[0] * threads, threads, cnt, q);
-      take<TR>(from + g.at[1] * threads, threads, cnt, yh);
-      normalise(yh, cnt, stat.z, stat.w);
+      // q = w dY; D = dH + rstd (q - mean q - yh mean(q yh)); K > 1 reads yh again after
+      // the sums instead of keeping it
+      float s[2] = {0.f, 0.f};
+      Eight kept;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        acc[0][j] = fma2_rn(q[j], yh[j], acc[0][j]);
-        acc[1][j] = add2_rn(q[j], acc[1][j]);
-        q[j] = mul2_rn(q[j], w2[j]);
+      for (int k = 0; k < K; ++k) {
+        const int m = cnt - k * span;
+        Eight yh, w;
+        take<TY>(piece(0, k), threads, m, d[k]);
+        take<TR>(piece(1, k), threads, m, yh);
+        normalise(yh, m, stat.z, stat.w);
+        from_shared(w_at + 2 * width + c + k * span, w);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          acc[0][k][j] = fma2_rn(d[k][j], yh[j], acc[0][k][j]);
+          acc[1][k][j] = add2_rn(d[k][j], acc[1][k][j]);
+          d[k][j] = mul2_rn(d[k][j], w[j]);
+          if (K == 1) kept[j] = yh[j];
+        }
+        s[0] += dot(d[k], yh), s[1] += add_up(d[k]);
       }
-      float s[2] = {dot(q, yh), add_up(q)};
       if (g.pre == GNN_NORM_LAYER) {
         row.sum(s);
       } else {
@@ -391,69 +422,108 @@ __global__ void __launch_bounds__(MULTI ? MAX_LANES : THREADS, MULTI ? 1 : 2)
       }
       const float2 along = dup2(-s[0] * g.inv_c), mean = dup2(-s[1] * g.inv_c), r = dup2(stat.w);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) d[j] = fma2_rn(r, fma2_rn(yh[j], along, add2_rn(q[j], mean)), d[j]);
-      mask(d, cnt);
+      for (int k = 0; k < K; ++k) {
+        const int m = cnt - k * span;
+        Eight dh;
+        if (K > 1) {
+          take<TR>(piece(1, k), threads, m, kept);
+          normalise(kept, m, stat.z, stat.w);
+        }
+        if (g.dH) {
+          take<TR>(piece(2, k), threads, m, dh);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) dh[j] = dup2(0.f);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) d[k][j] = fma2_rn(r, fma2_rn(kept[j], along, add2_rn(d[k][j], mean)), dh[j]);
+        mask(d[k], m);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < K; ++k) take<TR>(piece(2, k), threads, cnt - k * span, d[k]);
     }
-    if (g.dR && live) put<TR>(g.dR, i * g.lddr + c, d, cnt, odd);
+    if (g.dR && live) {
+#pragma unroll
+      for (int k = 0; k < K; ++k) put<TR>(g.dR, i * g.lddr + c + k * span, d[k], cnt - k * span, odd);
+    }
     if (g.B) {
-      Eight bh, v;
-      take<TB>(from + g.at[3] * threads, threads, cnt, bh);
-      normalise(bh, cnt, stat.x, stat.y);
-      float s[3];
-      float slope1 = 0.f;
-      if (g.gate == 2) {
-        Eight t, slope;
-        take<TB>(from + g.at[4] * threads, threads, cnt, t);
-        with_act(g.act, [&](auto A) {
+      float s[3] = {0.f, 0.f, 0.f};
+      float2 t1 = dup2(1.f), slope1 = dup2(0.f);
+      if (g.gate == 1) act_grad2(dup2(t_row), g.act, t1, slope1);
+      Eight kept;
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        const int m = cnt - k * span;
+        Eight bh, w, b;
+        take<TB>(piece(3, k), threads, m, bh);
+        normalise(bh, m, stat.x, stat.y);
+        from_shared(w_at + c + k * span, w);
+        from_shared(w_at + width + c + k * span, b);
+        if (g.gate == 2) {
+          Eight t, slope;
+          take<TB>(piece(4, k), threads, m, t);
+          with_act(g.act, [&](auto A) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float2 z = t[j];
+              act_grad2(z, A, t[j], slope[j]);
+            }
+          });
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const float2 z = t[j];
-            act_grad2(z, A, t[j], slope[j]);
+            slope[j] = mul2_rn(slope[j], mul2_rn(d[k][j], fma2_rn(w[j], bh[j], b[j])));
+            d[k][j] = mul2_rn(d[k][j], t[j]);
           }
-        });
+          if (g.dG && live) put<TB>(g.dG, i * g.lddg + c + k * span, slope, m, odd);
+        } else if (g.gate == 1) {
+          float2 z = dup2(0.f);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            z = fma2_rn(d[k][j], fma2_rn(w[j], bh[j], b[j]), z);
+            d[k][j] = mul2_rn(d[k][j], t1);
+          }
+          s[2] += z.x + z.y;
+        }
+        // d: D t here, and times s w_post from here on
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          slope[j] = mul2_rn(slope[j], mul2_rn(d[j], fma2_rn(w1[j], bh[j], b1[j])));
-          d[j] = mul2_rn(d[j], t[j]);
+          acc[2][k][j] = fma2_rn(d[k][j], bh[j], acc[2][k][j]);
+          acc[3][k][j] = add2_rn(d[k][j], acc[3][k][j]);
+          d[k][j] = mul2_rn(d[k][j], w[j]);
+          if (K == 1) kept[j] = bh[j];
         }
-        if (g.dG && live) put<TB>(g.dG, i * g.lddg + c, slope, cnt, odd);
-      } else if (g.gate == 1) {
-        float2 a, b;
-        act_grad2(dup2(t_row), g.act, a, b);
-        slope1 = b.x;
-        float2 z = dup2(0.f);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          z = fma2_rn(d[j], fma2_rn(w1[j], bh[j], b1[j]), z);
-          d[j] = mul2_rn(d[j], a);
-        }
-        s[2] = z.x + z.y;
-      }
-      // d: D t from here on
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        acc[2][j] = fma2_rn(d[j], bh[j], acc[2][j]);
-        acc[3][j] = add2_rn(d[j], acc[3][j]);
-        v[j] = mul2_rn(d[j], w1[j]);
+        s[0] += dot(d[k], bh), s[1] += add_up(d[k]);
       }
       const bool norm = g.post != GNN_NORM_NONE;
-      s[0] = dot(v, bh), s[1] = add_up(v);
       if (g.gate == 1) {
         row.sum(s);
-        if (g.dG && live && row.lane == 0) static_cast<TB*>(g.dG)[i * g.lddg] = from_f32<TB>(s[2] * slope1);
-      } else if (norm) {
+        if (g.dG && live && row.lane == 0) static_cast<TB*>(g.dG)[i * g.lddg] = from_f32<TB>(s[2] * slope1.x);
+      } else if (g.post == GNN_NORM_LAYER) {
         float two[2] = {s[0], s[1]};
         row.sum(two);
         s[0] = two[0], s[1] = two[1];
+      } else if (norm) {
+        float one[1] = {s[0]};
+        row.sum(one);
+        s[0] = one[0];
       }
       if (g.dB && live) {
-        if (norm) {
-          const float2 along = dup2(-s[0] * g.inv_c), mean = dup2(g.post == GNN_NORM_LAYER ? -s[1] * g.inv_c : 0.f),
-                       r = dup2(stat.y);
+        const float2 along = dup2(-s[0] * g.inv_c), mean = dup2(g.post == GNN_NORM_LAYER ? -s[1] * g.inv_c : 0.f),
+                     r = dup2(stat.y);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) v[j] = mul2_rn(r, fma2_rn(bh[j], along, add2_rn(v[j], mean)));
+        for (int k = 0; k < K; ++k) {
+          const int m = cnt - k * span;
+          if (norm) {
+            if (K > 1) {
+              take<TB>(piece(3, k), threads, m, kept);
+              normalise(kept, m, stat.x, stat.y);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) d[k][j] = mul2_rn(r, fma2_rn(kept[j], along, add2_rn(d[k][j], mean)));
+          }
+          put<TB>(g.dB, i * g.lddb + c + k * span, d[k], m, odd);
         }
-        put<TB>(g.dB, i * g.lddb + c, v, cnt, odd);
       }
     }
   }
@@ -466,23 +536,26 @@ __global__ void __launch_bounds__(MULTI ? MAX_LANES : THREADS, MULTI ? 1 : 2)
 #pragma unroll
       for (int a = 0; a < 4; ++a)
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          acc[a][j] = add2_rn(acc[a][j], make_float2(__shfl_xor_sync(0xffffffffu, acc[a][j].x, o),
-                                                     __shfl_xor_sync(0xffffffffu, acc[a][j].y, o)));
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            acc[a][k][j] = add2_rn(acc[a][k][j], make_float2(__shfl_xor_sync(0xffffffffu, acc[a][k][j].x, o),
+                                                             __shfl_xor_sync(0xffffffffu, acc[a][k][j].y, o)));
     }
   }
   __syncthreads();
-  // [turns][4][lanes][8]: every warp's (or group's) sums, then each column by one thread
+  // [turns][4][width]: every warp's (or group's) sums, then each column by one thread
   const int turns = MULTI ? groups : threads / 32, turn = MULTI ? row.group : threadIdx.x >> 5;
-  const int width = 8 * g.lanes;
   float* all = reinterpret_cast<float*>(ring);
   if (MULTI || (threadIdx.x & 31) < g.lanes) {
 #pragma unroll
-    for (int a = 0; a < 4; ++a) {
-      float4* to = reinterpret_cast<float4*>(all + ((int64_t)turn * 4 + a) * width + c);
-      to[0] = make_float4(acc[a][0].x, acc[a][0].y, acc[a][1].x, acc[a][1].y);
-      to[1] = make_float4(acc[a][2].x, acc[a][2].y, acc[a][3].x, acc[a][3].y);
-    }
+    for (int a = 0; a < 4; ++a)
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        float4* to = reinterpret_cast<float4*>(all + (turn * 4 + a) * width + c + k * span);
+        to[0] = make_float4(acc[a][k][0].x, acc[a][k][0].y, acc[a][k][1].x, acc[a][k][1].y);
+        to[1] = make_float4(acc[a][k][2].x, acc[a][k][2].y, acc[a][k][3].x, acc[a][k][3].y);
+      }
   }
   __syncthreads();
   float* out = g.part + (int64_t)blockIdx.x * 4 * width;
@@ -493,25 +566,26 @@ __global__ void __launch_bounds__(MULTI ? MAX_LANES : THREADS, MULTI ? 1 : 2)
   }
 }
 
-// The blocks' sums, in order and in fp64, and the weights' gradients from them.
-// A block takes 32 channels; scalar[] (one learned scale): its share of dscale.
+// The blocks' sums, in order, and the weights' gradients from them.  In fp32: an
+// SM adds two fp64 numbers a clock, and with those this kernel took 27 us of 39.  A
+// block takes 32 channels; scalar[] (one learned scale): its share of dscale.
 constexpr int JOIN_ROWS = 32;
 struct Join {
   const float* part;
   int blocks, width, C, scale_cols;
   const float *w_post, *b_post, *scale;
   float *dw_post, *db_post, *dscale, *dw_pre, *db_pre;
-  double* scalar;
+  float* scalar;
   int want_q, want_p;
 };
 __global__ void __launch_bounds__(32 * JOIN_ROWS) residual_join_kernel(const Join g) {
-  __shared__ double sm[4][JOIN_ROWS][32];
+  __shared__ float sm[4][JOIN_ROWS][33];
   cudaTriggerProgrammaticLaunchCompletion();
   cudaGridDependencySynchronize();
   const int lane = threadIdx.x & 31, r = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
-  double s[4] = {0, 0, 0, 0};
+  float s[4] = {0.f, 0.f, 0.f, 0.f};
   if (c < g.C) {
-#pragma unroll 4
+#pragma unroll 5
     for (int b = r; b < g.blocks; b += JOIN_ROWS) {
       const float* p = g.part + (int64_t)b * 4 * g.width + c;
       if (g.want_q) s[0] += p[0], s[1] += p[g.width];
@@ -521,87 +595,91 @@ __global__ void __launch_bounds__(32 * JOIN_ROWS) residual_join_kernel(const Joi
 #pragma unroll
   for (int a = 0; a < 4; ++a) sm[a][r][lane] = s[a];
   __syncthreads();
-  // one warp for each of the four sums, then the first has them all
-  if (r < 4) {
-    double t = 0;
-    for (int i = 0; i < JOIN_ROWS; ++i) t += sm[r][i][lane];
-    sm[r][0][lane] = t;
+  // a warp for each channel: its lanes are the rows
+#pragma unroll
+  for (int a = 0; a < 4; ++a) {
+    s[a] = sm[a][lane][r];
+#pragma unroll
+    for (int o = 16; o; o >>= 1) s[a] += __shfl_xor_sync(0xffffffffu, s[a], o);
   }
   __syncthreads();
+  if (lane < 4) sm[lane][0][r] = lane == 0 ? s[0] : lane == 1 ? s[1] : lane == 2 ? s[2] : s[3];
+  __syncthreads();
   if (r) return;
-  double ds = 0;
+  float ds = 0.f;
   if (c < g.C) {
-    const double P1 = sm[2][0][lane], P2 = sm[3][0][lane];
-    const double sc = g.scale_cols == 0 ? 1.0 : g.scale_cols == 1 ? g.scale[0] : g.scale[c];
-    if (g.dw_pre) g.dw_pre[c] = (float)sm[0][0][lane];
-    if (g.db_pre) g.db_pre[c] = (float)sm[1][0][lane];
-    if (g.dw_post) g.dw_post[c] = (float)(sc * P1);
-    if (g.db_post) g.db_post[c] = (float)(sc * P2);
-    ds = (g.w_post ? g.w_post[c] : 1.f) * P1 + (g.b_post ? g.b_post[c] : 0.f) * P2;
-    if (g.dscale && g.scale_cols > 1) g.dscale[c] = (float)ds;
+    const float P1 = sm[2][0][lane], P2 = sm[3][0][lane];
+    const float sc = g.scale_cols == 0 ? 1.f : g.scale_cols == 1 ? g.scale[0] : g.scale[c];
+    if (g.dw_pre) g.dw_pre[c] = sm[0][0][lane];
+    if (g.db_pre) g.db_pre[c] = sm[1][0][lane];
+    if (g.dw_post) g.dw_post[c] = sc * P1;
+    if (g.db_post) g.db_post[c] = sc * P2;
+    ds = fmaf(g.w_post ? g.w_post[c] : 1.f, P1, (g.b_post ? g.b_post[c] : 0.f) * P2);
+    if (g.dscale && g.scale_cols > 1) g.dscale[c] = ds;
   }
   if (g.dscale && g.scale_cols == 1) {
 #pragma unroll
     for (int o = 16; o; o >>= 1) ds += __shfl_xor_sync(0xffffffffu, ds, o);
     if (lane == 0) {
       g.scalar[blockIdx.x] = ds;
-      if (gridDim.x == 1) g.dscale[0] = (float)ds;
+      if (gridDim.x == 1) g.dscale[0] = ds;
     }
   }
 }
-__global__ void __launch_bounds__(32) residual_scalar_kernel(const double* scalar, int count, float* dscale) {
+__global__ void __launch_bounds__(32) residual_scalar_kernel(const float* scalar, int count, float* dscale) {
   cudaTriggerProgrammaticLaunchCompletion();
   cudaGridDependencySynchronize();
-  double s = 0;
+  float s = 0.f;
   for (int i = threadIdx.x; i < count; i += 32) s += scalar[i];
 #pragma unroll
   for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  if (threadIdx.x == 0) dscale[0] = (float)s;
+  if (threadIdx.x == 0) dscale[0] = s;
 }
 
 // ---------------------------------------------------------------- host side
-// Lanes of a row of C channels, padding to 16 included.
+// Lanes and vectors of a row of C channels, padding to 16 included.
 struct Shape {
-  int lanes, threads;
+  int lanes, vecs, threads;
   bool multi;
 };
 Shape shape_for(int C) {
   const int v = (C + 15) / 16 * 2;
-  Shape s{4, THREADS, false};
-  while (s.lanes < v && s.lanes < 32) s.lanes *= 2;
-  if (s.lanes >= v) return s;
-  s.lanes = (v + 31) / 32 * 32;
-  s.multi = true;
+  Shape s{0, 0, 0, false};
+  for (int k = 1; k <= 4; ++k)
+    for (int l = 4; l <= 32; l *= 2)
+      if (l * k >= v && (!s.lanes || l * k < s.lanes * s.vecs)) s = {l, k, k == 1 ? THREADS : FEW, false};
+  if (s.lanes) return s;
+  s.lanes = (v + 31) / 32 * 32, s.vecs = 1, s.multi = true;
   s.threads = s.lanes > THREADS / 2 ? s.lanes : THREADS / s.lanes * s.lanes;
   return s;
 }
 
-// Two blocks an SM, which their registers allow.
-constexpr int BLOCKS = 304;
-int64_t blocks_for(int64_t n, const Shape& s) {
+// As many blocks as the card holds at once; the backward's join reads a piece of each.
+int blocks_an_sm(const Shape& s, bool bwd) { return s.multi || s.vecs == 1 ? 2 : s.vecs == 2 ? (bwd ? 3 : 4) : bwd ? 2 : 3; }
+int64_t blocks_for(int64_t n, const Shape& s, bool bwd) {
   const int64_t rows = s.threads / s.lanes;
-  return std::max<int64_t>(1, std::min<int64_t>((n + rows - 1) / rows, BLOCKS));
+  return std::max<int64_t>(1, std::min<int64_t>((n + rows - 1) / rows, 152 * blocks_an_sm(s, bwd)));
 }
 
-constexpr int RING_MOST = 108 << 10;  // of a block, so that two fit
-// Stages of a ring of g.pieces for s.threads: up to four, two at least.
-int ring_of(Args& g, const Shape& s) {
-  const int stage = g.pieces * s.threads * 16;
-  g.stages = std::max(2, std::min(4, RING_MOST / std::max(stage, 1)));
+// Stages of a ring of g.pieces a vector: up to four, two at least, in a block's share
+// of 220 KB beside `other` bytes.
+int ring_of(Args& g, const Shape& s, bool bwd, int other) {
+  const int stage = s.vecs * g.pieces * s.threads * 16, most = (220 << 10) / blocks_an_sm(s, bwd) - other;
+  g.stages = std::max(2, std::min(4, most / std::max(stage, 1)));
   return g.stages * stage;
 }
 
 struct ResidualWs {
   float* part;
-  double* scalar;
+  float* scalar;
   size_t bytes;
 };
 ResidualWs residual_ws(void* base, size_t cap, int64_t n, int C, bool* ok) {
   Arena ar(base, cap);
   ResidualWs w{};
   const Shape s = shape_for(C);
-  w.part = ar.take<float>((size_t)blocks_for(n, s) * 4 * s.lanes * 8);
-  w.scalar = ar.take<double>((size_t)(C + 31) / 32);
+  w.part = ar.take<float>((size_t)blocks_for(n, s, true) * 4 * s.lanes * s.vecs * 8);
+  w.scalar = ar.take<float>((size_t)(C + 31) / 32);
   w.bytes = ar.used;
   *ok = ar.ok();
   return w;
@@ -626,18 +704,19 @@ gnn_status launch(int64_t grid, int block, size_t smem, cudaStream_t st, void (*
   return GNN_OK;
 }
 
-constexpr int SMEM_MOST = 200 << 10;  // rows of 512 lanes, fp32 with a gate: 2 x 80 KB
+constexpr int SMEM_MOST = 224 << 10;  // rows of 512 lanes, fp32 with a gate: 2 x 80 KB and 64 of weights
 
-template <bool BWD, class TB, class TR, class TY, bool MULTI>
+template <bool BWD, class TB, class TR, class TY, bool MULTI, int K>
 gnn_status run_shape(Args& g, const Shape& s, cudaStream_t st) {
-  auto* k = BWD ? residual_bwd_kernel<TB, TR, TY, MULTI> : residual_fwd_kernel<TB, TR, TY, MULTI>;
   static PerDevice done;
+  auto* k = BWD ? residual_bwd_kernel<TB, TR, TY, MULTI, K> : residual_fwd_kernel<TB, TR, TY, MULTI, K>;
   const gnn_status r = allow_smem(k, SMEM_MOST, done);
   if (r != GNN_OK) return r;
-  int smem = ring_of(g, s);
+  const int width = 8 * s.lanes * K * (int)sizeof(float), weights = (BWD ? 3 : 4) * width;
+  int ring = ring_of(g, s, BWD, weights);
   // the backward's sums of every warp or group pass through the ring
-  if (BWD) smem = std::max(smem, (MULTI ? s.threads / s.lanes : s.threads / 32) * 4 * 8 * s.lanes * (int)sizeof(float));
-  return launch(blocks_for(g.n, s), s.threads, smem, st, k, g);
+  if (BWD) ring = std::max(ring, (MULTI ? s.threads / s.lanes : s.threads / 32) * 4 * width);
+  return launch(blocks_for(g.n, s, BWD), s.threads, weights + ring, st, k, g);
 }
 template <bool BWD, class TB, class TR, class TY>
 gnn_status run(Args& g, cudaStream_t st) {
@@ -655,7 +734,11 @@ gnn_status run(Args& g, cudaStream_t st) {
   } else {
     add(0, g.R, sizeof(TR)), add(1, g.B, sizeof(TB)), add(2, g.gate == 2 ? g.G : nullptr, sizeof(TB));
   }
-  return s.multi ? run_shape<BWD, TB, TR, TY, true>(g, s, st) : run_shape<BWD, TB, TR, TY, false>(g, s, st);
+  if (s.multi) return run_shape<BWD, TB, TR, TY, true, 1>(g, s, st);
+  return s.vecs == 1   ? run_shape<BWD, TB, TR, TY, false, 1>(g, s, st)
+         : s.vecs == 2 ? run_shape<BWD, TB, TR, TY, false, 2>(g, s, st)
+         : s.vecs == 3 ? run_shape<BWD, TB, TR, TY, false, 3>(g, s, st)
+                       : run_shape<BWD, TB, TR, TY, false, 4>(g, s, st);
 }
 
 // Types of branch, stream and next operand (one type, or an fp32 stream with a
@@ -854,9 +937,9 @@ extern "C" gnn_status gnn_residual_norm_bwd(const void* dH, int64_t lddh, const 
   if (!want_q && !want_p) return GNN_OK;
   const Shape sh = shape_for(C);
   const int blocks = (C + 31) / 32;
-  const Join j{w.part, n > 0 ? (int)blocks_for(n, sh) : 0, sh.lanes * 8, C, scale_cols, w_post, b_post, scale, dw_post, db_post,
+  const Join j{w.part, n > 0 ? (int)blocks_for(n, sh, true) : 0, sh.lanes * sh.vecs * 8, C, scale_cols, w_post, b_post, scale, dw_post, db_post,
                dscale, dw_pre, db_pre, w.scalar, want_q, want_p};
   s = launch(blocks, 32 * JOIN_ROWS, 0, as_stream(stream), residual_join_kernel, j);
   if (s != GNN_OK || !dscale || scale_cols != 1 || blocks == 1) return s;
-  return launch(1, 32, 0, as_stream(stream), residual_scalar_kernel, (const double*)w.scalar, blocks, dscale);
+  return launch(1, 32, 0, as_stream(stream), residual_scalar_kernel, (const float*)w.scalar, blocks, dscale);
 }
