@@ -51,12 +51,23 @@ struct Args {
 };
 
 // ------------------------------------------------------- eight channels a lane
+// Two fours of channels: side by side where every matrix is of a 2-byte type (one
+// 16-byte access each), else 4 lanes apart (SPLIT), so that a warp's 16 bytes of fp32
+// a lane lie side by side as well (in pairs 32 bytes apart 200,000 x 602 forward in
+// fp32 took 763 us).
 using Eight = float2[4];
 
-__device__ __forceinline__ void mask(Eight& x, int cnt) {
-  if (cnt < 8) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = make_float2(2 * i < cnt ? x[i].x : 0.f, 2 * i + 1 < cnt ? x[i].y : 0.f);
+// Channels of the row from each of the two fours' first on.
+struct Left {
+  int a, b;
+};
+
+__device__ __forceinline__ void mask(Eight& x, Left m) {
+  if (m.a < 4 || m.b < 4) {
+    x[0] = make_float2(m.a > 0 ? x[0].x : 0.f, m.a > 1 ? x[0].y : 0.f);
+    x[1] = make_float2(m.a > 2 ? x[1].x : 0.f, m.a > 3 ? x[1].y : 0.f);
+    x[2] = make_float2(m.b > 0 ? x[2].x : 0.f, m.b > 1 ? x[2].y : 0.f);
+    x[3] = make_float2(m.b > 2 ? x[3].x : 0.f, m.b > 3 ? x[3].y : 0.f);
   }
 }
 
@@ -65,17 +76,30 @@ __device__ __forceinline__ void copy16(uint4* dst, const void* src, bool there) 
                "r"(there ? 16 : 0)
                : "memory");
 }
+__device__ __forceinline__ void copy8(void* dst, const void* src, bool there) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src),
+               "r"(there ? 8 : 0)
+               : "memory");
+}
 
-// A lane's pieces of one stage of the ring, `threads` apart.
-template <class T>
-__device__ __forceinline__ void fetch(uint4* to, int threads, const void* base, int64_t at, int cnt) {
-  const T* p = static_cast<const T*>(base) + (cnt > 0 ? at : 0);
-  copy16(to, p, cnt > 0);
-  if constexpr (std::is_same<T, float>::value) copy16(to + threads, cnt > 4 ? p + 4 : p, cnt > 4);
+// A lane's pieces of one stage of the ring, `threads` apart: row `at`, from channel c
+// and `apart` channels further on.  What is past the row comes as zero.
+template <class T, bool SPLIT>
+__device__ __forceinline__ void fetch(uint4* to, int threads, const void* base, int64_t at, int c, int apart, Left m) {
+  const T* row = static_cast<const T*>(base) + (m.a > 0 ? at + c : 0);
+  if constexpr (std::is_same<T, float>::value) {
+    copy16(to, row, m.a > 0);
+    copy16(to + threads, m.b > 0 ? row + apart : row, m.b > 0);
+  } else if constexpr (SPLIT) {
+    copy8(to, row, m.a > 0);
+    copy8(reinterpret_cast<char*>(to) + 8, m.b > 0 ? row + apart : row, m.b > 0);
+  } else {
+    copy16(to, row, m.a > 0);
+  }
 }
 // Channels past the row's last are zero.
 template <class T>
-__device__ __forceinline__ void take(const uint4* from, int threads, int cnt, Eight& x) {
+__device__ __forceinline__ void take(const uint4* from, int threads, Left m, Eight& x) {
   const uint4 a = *from;
   if constexpr (std::is_same<T, float>::value) {
     const uint4 b = from[threads];
@@ -84,23 +108,28 @@ __device__ __forceinline__ void take(const uint4* from, int threads, int cnt, Ei
   } else {
     x[0] = Pack2<T>::from(a.x), x[1] = Pack2<T>::from(a.y), x[2] = Pack2<T>::from(a.z), x[3] = Pack2<T>::from(a.w);
   }
-  mask(x, cnt);
+  mask(x, m);
 }
 
 // Writes the lane's channels and the zeros that pad a row (to a multiple of 16
-// channels in a 2-byte type, of 4 in fp32).  `cnt`: channels from here on; odd: the
-// second of two lanes that share 16 channels.
-template <class T>
-__device__ __forceinline__ void put(void* base, int64_t at, Eight& x, int cnt, bool odd) {
-  if (cnt <= (odd ? -8 : 0)) return;
-  T* p = static_cast<T*>(base) + at;
-  mask(x, cnt);
+// channels in a 2-byte type, of 4 in fp32).
+template <class T, bool SPLIT>
+__device__ __forceinline__ void put(void* base, int64_t at, int c, int apart, Eight& x, Left m) {
+  T* p = static_cast<T*>(base) + at + c;
+  mask(x, m);
   if constexpr (std::is_same<T, float>::value) {
-    if (cnt > 0) *reinterpret_cast<float4*>(p) = make_float4(x[0].x, x[0].y, x[1].x, x[1].y);
-    if (cnt > 4) *reinterpret_cast<float4*>(p + 4) = make_float4(x[2].x, x[2].y, x[3].x, x[3].y);
+    if (m.a > 0) *reinterpret_cast<float4*>(p) = make_float4(x[0].x, x[0].y, x[1].x, x[1].y);
+    if (m.b > 0) *reinterpret_cast<float4*>(p + apart) = make_float4(x[2].x, x[2].y, x[3].x, x[3].y);
   } else {
-    *reinterpret_cast<uint4*>(p) = make_uint4(Pack2<T>::to(x[0].x, x[0].y), Pack2<T>::to(x[1].x, x[1].y),
-                                              Pack2<T>::to(x[2].x, x[2].y), Pack2<T>::to(x[3].x, x[3].y));
+    const uint2 a = make_uint2(Pack2<T>::to(x[0].x, x[0].y), Pack2<T>::to(x[1].x, x[1].y)),
+                b = make_uint2(Pack2<T>::to(x[2].x, x[2].y), Pack2<T>::to(x[3].x, x[3].y));
+    // a four is written where its sixteen channels begin inside of the row
+    if constexpr (SPLIT) {
+      if (m.a > -(c & 15)) *reinterpret_cast<uint2*>(p) = a;
+      if (m.b > -((c + apart) & 15)) *reinterpret_cast<uint2*>(p + apart) = b;
+    } else {
+      if (m.a > -(c & 15)) *reinterpret_cast<uint4*>(p) = make_uint4(a.x, a.y, b.x, b.y);
+    }
   }
 }
 
@@ -161,10 +190,10 @@ struct Row {
   }
 };
 
-// Mean and 1/deviation of a row; the variance about the mean.  `cnt`: channels from
-// this lane's first on, `span` from one of its vectors to the next.
+// Mean and 1/deviation of a row; the variance about the mean.  `left`: of the lane's
+// first vector, `span`: channels from one of its vectors to the next.
 template <int K, bool MULTI>
-__device__ __forceinline__ void statistics(const Eight (&x)[K], int cnt, int span, int kind, float eps, float inv_c,
+__device__ __forceinline__ void statistics(const Eight (&x)[K], Left left, int span, int kind, float eps, float inv_c,
                                            Row<MULTI>& row, float& mean, float& rstd) {
   mean = 0.f, rstd = 1.f;
   if (kind == GNN_NORM_NONE) return;
@@ -180,7 +209,7 @@ __device__ __forceinline__ void statistics(const Eight (&x)[K], int cnt, int spa
       Eight d;
 #pragma unroll
       for (int i = 0; i < 4; ++i) d[i] = add2_rn(x[k][i], dup2(-mean));
-      mask(d, cnt - k * span);
+      mask(d, {left.a - k * span, left.b - k * span});
       s[0] += dot(d, d);
     }
   } else {
@@ -192,29 +221,38 @@ __device__ __forceinline__ void statistics(const Eight (&x)[K], int cnt, int spa
 }
 
 // (x - mean) rstd, zero past the row's end.
-__device__ __forceinline__ void normalise(Eight& x, int cnt, float mean, float rstd) {
+__device__ __forceinline__ void normalise(Eight& x, Left m, float mean, float rstd) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) x[i] = mul2_rn(add2_rn(x[i], dup2(-mean)), dup2(rstd));
-  mask(x, cnt);
+  mask(x, m);
 }
 
-// Eight weights of this lane from the block's copy of a vector.
-__device__ __forceinline__ void from_shared(const float* p, Eight& w) {
-  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+// Where channel c's weight lies in the block's copy of a vector: the first fours of
+// every lane, then the second ones, so that a warp's accesses lie side by side.
+template <bool SPLIT>
+__device__ __forceinline__ int weight_at(int c, int width) {
+  return SPLIT ? c : (c & 4 ? width / 2 : 0) + c / 8 * 4 + (c & 3);
+}
+// Eight weights of this lane, from channel c on.
+template <bool SPLIT>
+__device__ __forceinline__ void from_shared(const float* p, int c, int apart, int width, Eight& w) {
+  const float4 a = *reinterpret_cast<const float4*>(p + weight_at<SPLIT>(c, width)),
+               b = *reinterpret_cast<const float4*>(p + weight_at<SPLIT>(c + apart, width));
   w[0] = make_float2(a.x, a.y), w[1] = make_float2(a.z, a.w), w[2] = make_float2(b.x, b.y), w[3] = make_float2(b.z, b.w);
 }
 
 // s w_post, s b_post, w_pre and (forward) b_pre of the block's `width` channels, zero
 // past the row's end.
-template <bool FWD>
+template <bool FWD, bool SPLIT>
 __device__ __forceinline__ void share_weights(const Args& g, float* to, int width) {
   for (int c = threadIdx.x; c < width; c += blockDim.x) {
     const bool there = c < g.C;
+    const int at = weight_at<SPLIT>(c, width);
     const float s = there ? (g.scale_cols == 0 ? 1.f : __ldg(g.scale + (g.scale_cols == 1 ? 0 : c))) : 0.f;
-    to[c] = s * (there && g.w_post ? __ldg(g.w_post + c) : 1.f);
-    to[width + c] = there && g.b_post ? s * __ldg(g.b_post + c) : 0.f;
-    to[2 * width + c] = there ? (g.w_pre ? __ldg(g.w_pre + c) : 1.f) : 0.f;
-    if (FWD) to[3 * width + c] = there && g.b_pre ? __ldg(g.b_pre + c) : 0.f;
+    to[at] = s * (there && g.w_post ? __ldg(g.w_post + c) : 1.f);
+    to[width + at] = there && g.b_post ? s * __ldg(g.b_post + c) : 0.f;
+    to[2 * width + at] = there ? (g.w_pre ? __ldg(g.w_pre + c) : 1.f) : 0.f;
+    if (FWD) to[3 * width + at] = there && g.b_pre ? __ldg(g.b_pre + c) : 0.f;
   }
   __syncthreads();
 }
@@ -234,7 +272,7 @@ __device__ __forceinline__ void wait_row(int stages) {
 }
 
 template <class TB, class TR, class TY, bool MULTI, int K>
-__global__ void __launch_bounds__(MULTI ? MAX_LANES : K == 1 ? THREADS : FEW, MULTI ? 1 : K == 1 ? 2 : K == 2 ? 4 : 3)
+__global__ void __launch_bounds__(MULTI ? MAX_LANES : K == 1 ? THREADS : FEW)
     residual_fwd_kernel(const __grid_constant__ Args g) {
   extern __shared__ uint4 smem[];
   __shared__ float sm[MULTI ? 2 * 4 * (MAX_LANES / 32) : 1];
@@ -245,8 +283,9 @@ __global__ void __launch_bounds__(MULTI ? MAX_LANES : K == 1 ? THREADS : FEW, MU
   const int64_t step = (int64_t)gridDim.x * groups;
   // the warp's first row: its groups leave the loop together
   const int ahead = MULTI ? 0 : row.group & (32 / g.lanes - 1);
-  const int c = 8 * row.lane, cnt = g.C - c;
-  const bool odd = row.lane & 1;
+  constexpr bool SPLIT = std::is_same<TB, float>::value || std::is_same<TR, float>::value || std::is_same<TY, float>::value;
+  const int c = (SPLIT ? 4 : 8) * row.lane, apart = SPLIT ? 4 * g.lanes : 4;
+  const Left left{g.C - c, g.C - c - apart};
   float* const w_at = reinterpret_cast<float*>(smem);
   uint4* const mine = smem + width + threadIdx.x;
   const int stage_size = K * g.pieces * threads;
@@ -254,10 +293,11 @@ __global__ void __launch_bounds__(MULTI ? MAX_LANES : K == 1 ? THREADS : FEW, MU
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       uint4* to = mine + st * stage_size + k * g.pieces * threads;
-      const int m = i < g.n ? cnt - k * span : 0, ck = c + k * span;
-      fetch<TR>(to + g.at[0] * threads, threads, g.R, i * g.ldr + ck, m);
-      if (g.B) fetch<TB>(to + g.at[1] * threads, threads, g.B, i * g.ldb + ck, m);
-      if (g.gate == 2) fetch<TB>(to + g.at[2] * threads, threads, g.G, i * g.ldg + ck, m);
+      const int ck = c + k * span;
+      const Left m = i < g.n ? Left{left.a - k * span, left.b - k * span} : Left{0, 0};
+      fetch<TR, SPLIT>(to + g.at[0] * threads, threads, g.R, i * g.ldr, ck, apart, m);
+      if (g.B) fetch<TB, SPLIT>(to + g.at[1] * threads, threads, g.B, i * g.ldb, ck, apart, m);
+      if (g.gate == 2) fetch<TB, SPLIT>(to + g.at[2] * threads, threads, g.G, i * g.ldg, ck, apart, m);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
@@ -265,7 +305,7 @@ __global__ void __launch_bounds__(MULTI ? MAX_LANES : K == 1 ? THREADS : FEW, MU
   int64_t i = (int64_t)blockIdx.x * groups + row.group;
   for (int k = 0; k < g.stages - 1; ++k) request(k, i + k * step);
   float t_next = row_gate(i);
-  share_weights<true>(g, w_at, width);
+  share_weights<true, SPLIT>(g, w_at, width);
   int st = 0, into = g.stages - 1;
   for (; i - ahead < g.n; i += step) {
     request(into, i + (g.stages - 1) * step);
@@ -281,12 +321,12 @@ __global__ void __launch_bounds__(MULTI ? MAX_LANES : K == 1 ? THREADS : FEW, MU
     Eight h[K];
     if (g.B) {
 #pragma unroll
-      for (int k = 0; k < K; ++k) take<TB>(piece(1, k), threads, cnt - k * span, h[k]);
-      statistics<K>(h, cnt, span, g.post, g.eps, g.inv_c, row, stat.x, stat.y);
+      for (int k = 0; k < K; ++k) take<TB>(piece(1, k), threads, Left{left.a - k * span, left.b - k * span}, h[k]);
+      statistics<K>(h, left, span, g.post, g.eps, g.inv_c, row, stat.x, stat.y);
       const float t1 = g.gate == 1 ? act_f(t_row, g.act) : 1.f;
 #pragma unroll
       for (int k = 0; k < K; ++k) {
-        const int m = cnt - k * span;
+        const Left m{left.a - k * span, left.b - k * span};
         Eight t, w, b, r;
         if (g.gate == 2) {
           take<TB>(piece(2, k), threads, m, t);
@@ -299,8 +339,8 @@ __global__ void __launch_bounds__(MULTI ? MAX_LANES : K == 1 ? THREADS : FEW, MU
           for (int j = 0; j < 4; ++j) t[j] = dup2(t1);
         }
         normalise(h[k], m, stat.x, stat.y);
-        from_shared(w_at + c + k * span, w);
-        from_shared(w_at + width + c + k * span, b);
+        from_shared<SPLIT>(w_at, c + k * span, apart, width, w);
+        from_shared<SPLIT>(w_at + width, c + k * span, apart, width, b);
         take<TR>(piece(0, k), threads, m, r);
 #pragma unroll
         for (int j = 0; j < 4; ++j) h[k][j] = fma2_rn(t[j], fma2_rn(w[j], h[k][j], b[j]), r[j]);
@@ -308,24 +348,24 @@ __global__ void __launch_bounds__(MULTI ? MAX_LANES : K == 1 ? THREADS : FEW, MU
       }
     } else {
 #pragma unroll
-      for (int k = 0; k < K; ++k) take<TR>(piece(0, k), threads, cnt - k * span, h[k]);
+      for (int k = 0; k < K; ++k) take<TR>(piece(0, k), threads, Left{left.a - k * span, left.b - k * span}, h[k]);
     }
     if (g.H && live) {
 #pragma unroll
-      for (int k = 0; k < K; ++k) put<TR>(g.H, i * g.ldh + c + k * span, h[k], cnt - k * span, odd);
+      for (int k = 0; k < K; ++k) put<TR, SPLIT>(g.H, i * g.ldh, c + k * span, apart, h[k], Left{left.a - k * span, left.b - k * span});
     }
     if (g.pre != GNN_NORM_NONE) {
-      statistics<K>(h, cnt, span, g.pre, g.eps, g.inv_c, row, stat.z, stat.w);
+      statistics<K>(h, left, span, g.pre, g.eps, g.inv_c, row, stat.z, stat.w);
 #pragma unroll
       for (int k = 0; k < K; ++k) {
-        const int m = cnt - k * span;
+        const Left m{left.a - k * span, left.b - k * span};
         Eight w, b;
         normalise(h[k], m, stat.z, stat.w);
-        from_shared(w_at + 2 * width + c + k * span, w);
-        from_shared(w_at + 3 * width + c + k * span, b);
+        from_shared<SPLIT>(w_at + 2 * width, c + k * span, apart, width, w);
+        from_shared<SPLIT>(w_at + 3 * width, c + k * span, apart, width, b);
 #pragma unroll
         for (int j = 0; j < 4; ++j) h[k][j] = fma2_rn(w[j], h[k][j], b[j]);
-        if (live) put<TY>(g.Y, i * g.ldy + c + k * span, h[k], m, odd);
+        if (live) put<TY, SPLIT>(g.Y, i * g.ldy, c + k * span, apart, h[k], m);
       }
     }
     if (g.stats && live && row.lane == 0) g.stats[i] = stat;
@@ -333,7 +373,7 @@ __global__ void __launch_bounds__(MULTI ? MAX_LANES : K == 1 ? THREADS : FEW, MU
 }
 
 template <class TB, class TR, class TY, bool MULTI, int K>
-__global__ void __launch_bounds__(MULTI ? MAX_LANES : K == 1 ? THREADS : FEW, MULTI ? 1 : K == 1 ? 2 : K == 2 ? 3 : 2)
+__global__ void __launch_bounds__(MULTI ? MAX_LANES : K == 1 ? THREADS : FEW, MULTI ? 1 : 2)
     residual_bwd_kernel(const __grid_constant__ Args g) {
   extern __shared__ uint4 smem[];
   __shared__ float sm[MULTI ? 2 * 4 * (MAX_LANES / 32) : 1];
@@ -343,8 +383,9 @@ __global__ void __launch_bounds__(MULTI ? MAX_LANES : K == 1 ? THREADS : FEW, MU
   const int threads = blockDim.x, groups = threads / g.lanes, span = 8 * g.lanes, width = K * span;
   const int64_t step = (int64_t)gridDim.x * groups;
   const int ahead = MULTI ? 0 : row.group & (32 / g.lanes - 1);
-  const int c = 8 * row.lane, cnt = g.C - c;
-  const bool odd = row.lane & 1;
+  constexpr bool SPLIT = std::is_same<TB, float>::value || std::is_same<TR, float>::value || std::is_same<TY, float>::value;
+  const int c = (SPLIT ? 4 : 8) * row.lane, apart = SPLIT ? 4 * g.lanes : 4;
+  const Left left{g.C - c, g.C - c - apart};
   float* const w_at = reinterpret_cast<float*>(smem);
   uint4* const ring = smem + 3 * width / 4;
   uint4* const mine = ring + threadIdx.x;
@@ -353,14 +394,15 @@ __global__ void __launch_bounds__(MULTI ? MAX_LANES : K == 1 ? THREADS : FEW, MU
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       uint4* to = mine + st * stage_size + k * g.pieces * threads;
-      const int m = i < g.n ? cnt - k * span : 0, ck = c + k * span;
+      const int ck = c + k * span;
+      const Left m = i < g.n ? Left{left.a - k * span, left.b - k * span} : Left{0, 0};
       if (g.dY) {
-        fetch<TY>(to + g.at[0] * threads, threads, g.dY, i * g.ldy + ck, m);
-        fetch<TR>(to + g.at[1] * threads, threads, g.H, i * g.ldh + ck, m);
+        fetch<TY, SPLIT>(to + g.at[0] * threads, threads, g.dY, i * g.ldy, ck, apart, m);
+        fetch<TR, SPLIT>(to + g.at[1] * threads, threads, g.H, i * g.ldh, ck, apart, m);
       }
-      if (g.dH) fetch<TR>(to + g.at[2] * threads, threads, g.dH, i * g.lddh + ck, m);
-      if (g.B) fetch<TB>(to + g.at[3] * threads, threads, g.B, i * g.ldb + ck, m);
-      if (g.gate == 2) fetch<TB>(to + g.at[4] * threads, threads, g.G, i * g.ldg + ck, m);
+      if (g.dH) fetch<TR, SPLIT>(to + g.at[2] * threads, threads, g.dH, i * g.lddh, ck, apart, m);
+      if (g.B) fetch<TB, SPLIT>(to + g.at[3] * threads, threads, g.B, i * g.ldb, ck, apart, m);
+      if (g.gate == 2) fetch<TB, SPLIT>(to + g.at[4] * threads, threads, g.G, i * g.ldg, ck, apart, m);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
@@ -370,7 +412,7 @@ __global__ void __launch_bounds__(MULTI ? MAX_LANES : K == 1 ? THREADS : FEW, MU
   for (int k = 0; k < g.stages - 1; ++k) request(k, i + k * step);
   float t_next = row_gate(i);
   float4 s_next = row_stats(i);
-  share_weights<false>(g, w_at, width);
+  share_weights<false, SPLIT>(g, w_at, width);
   Eight acc[4][K];  // sums of dY yh, dY, D t bh, D t
 #pragma unroll
   for (int a = 0; a < 4; ++a)
@@ -398,12 +440,12 @@ __global__ void __launch_bounds__(MULTI ? MAX_LANES : K == 1 ? THREADS : FEW, MU
       Eight kept;
 #pragma unroll
       for (int k = 0; k < K; ++k) {
-        const int m = cnt - k * span;
+        const Left m{left.a - k * span, left.b - k * span};
         Eight yh, w;
         take<TY>(piece(0, k), threads, m, d[k]);
         take<TR>(piece(1, k), threads, m, yh);
         normalise(yh, m, stat.z, stat.w);
-        from_shared(w_at + 2 * width + c + k * span, w);
+        from_shared<SPLIT>(w_at + 2 * width, c + k * span, apart, width, w);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           acc[0][k][j] = fma2_rn(d[k][j], yh[j], acc[0][k][j]);
@@ -423,7 +465,7 @@ __global__ void __launch_bounds__(MULTI ? MAX_LANES : K == 1 ? THREADS : FEW, MU
       const float2 along = dup2(-s[0] * g.inv_c), mean = dup2(-s[1] * g.inv_c), r = dup2(stat.w);
 #pragma unroll
       for (int k = 0; k < K; ++k) {
-        const int m = cnt - k * span;
+        const Left m{left.a - k * span, left.b - k * span};
         Eight dh;
         if (K > 1) {
           take<TR>(piece(1, k), threads, m, kept);
@@ -441,11 +483,11 @@ __global__ void __launch_bounds__(MULTI ? MAX_LANES : K == 1 ? THREADS : FEW, MU
       }
     } else {
 #pragma unroll
-      for (int k = 0; k < K; ++k) take<TR>(piece(2, k), threads, cnt - k * span, d[k]);
+      for (int k = 0; k < K; ++k) take<TR>(piece(2, k), threads, Left{left.a - k * span, left.b - k * span}, d[k]);
     }
     if (g.dR && live) {
 #pragma unroll
-      for (int k = 0; k < K; ++k) put<TR>(g.dR, i * g.lddr + c + k * span, d[k], cnt - k * span, odd);
+      for (int k = 0; k < K; ++k) put<TR, SPLIT>(g.dR, i * g.lddr, c + k * span, apart, d[k], Left{left.a - k * span, left.b - k * span});
     }
     if (g.B) {
       float s[3] = {0.f, 0.f, 0.f};
@@ -454,12 +496,12 @@ __global__ void __launch_bounds__(MULTI ? MAX_LANES : K == 1 ? THREADS : FEW, MU
       Eight kept;
 #pragma unroll
       for (int k = 0; k < K; ++k) {
-        const int m = cnt - k * span;
+        const Left m{left.a - k * span, left.b - k * span};
         Eight bh, w, b;
         take<TB>(piece(3, k), threads, m, bh);
         normalise(bh, m, stat.x, stat.y);
-        from_shared(w_at + c + k * span, w);
-        from_shared(w_at + width + c + k * span, b);
+        from_shared<SPLIT>(w_at, c + k * span, apart, width, w);
+        from_shared<SPLIT>(w_at + width, c + k * span, apart, width, b);
         if (g.gate == 2) {
           Eight t, slope;
           take<TB>(piece(4, k), threads, m, t);
@@ -475,7 +517,7 @@ __global__ void __launch_bounds__(MULTI ? MAX_LANES : K == 1 ? THREADS : FEW, MU
             slope[j] = mul2_rn(slope[j], mul2_rn(d[k][j], fma2_rn(w[j], bh[j], b[j])));
             d[k][j] = mul2_rn(d[k][j], t[j]);
           }
-          if (g.dG && live) put<TB>(g.dG, i * g.lddg + c + k * span, slope, m, odd);
+          if (g.dG && live) put<TB, SPLIT>(g.dG, i * g.lddg, c + k * span, apart, slope, m);
         } else if (g.gate == 1) {
           float2 z = dup2(0.f);
 #pragma unroll
@@ -513,7 +555,7 @@ __global__ void __launch_bounds__(MULTI ? MAX_LANES : K == 1 ? THREADS : FEW, MU
                      r = dup2(stat.y);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-          const int m = cnt - k * span;
+          const Left m{left.a - k * span, left.b - k * span};
           if (norm) {
             if (K > 1) {
               take<TB>(piece(3, k), threads, m, kept);
@@ -522,7 +564,7 @@ __global__ void __launch_bounds__(MULTI ? MAX_LANES : K == 1 ? THREADS : FEW, MU
 #pragma unroll
             for (int j = 0; j < 4; ++j) d[k][j] = mul2_rn(r, fma2_rn(kept[j], along, add2_rn(d[k][j], mean)));
           }
-          put<TB>(g.dB, i * g.lddb + c + k * span, d[k], m, odd);
+          put<TB, SPLIT>(g.dB, i * g.lddb, c + k * span, apart, d[k], m);
         }
       }
     }
@@ -552,9 +594,9 @@ __global__ void __launch_bounds__(MULTI ? MAX_LANES : K == 1 ? THREADS : FEW, MU
     for (int a = 0; a < 4; ++a)
 #pragma unroll
       for (int k = 0; k < K; ++k) {
-        float4* to = reinterpret_cast<float4*>(all + (turn * 4 + a) * width + c + k * span);
-        to[0] = make_float4(acc[a][k][0].x, acc[a][k][0].y, acc[a][k][1].x, acc[a][k][1].y);
-        to[1] = make_float4(acc[a][k][2].x, acc[a][k][2].y, acc[a][k][3].x, acc[a][k][3].y);
+        float* to = all + (turn * 4 + a) * width + c + k * span;
+        *reinterpret_cast<float4*>(to) = make_float4(acc[a][k][0].x, acc[a][k][0].y, acc[a][k][1].x, acc[a][k][1].y);
+        *reinterpret_cast<float4*>(to + apart) = make_float4(acc[a][k][2].x, acc[a][k][2].y, acc[a][k][3].x, acc[a][k][3].y);
       }
   }
   __syncthreads();
@@ -637,36 +679,49 @@ __global__ void __launch_bounds__(32) residual_scalar_kernel(const float* scalar
 }
 
 // ---------------------------------------------------------------- host side
+#ifndef V_BK
+#define V_BK 3
+#endif
+#ifndef V_FK
+#define V_FK 4
+#endif
 // Lanes and vectors of a row of C channels, padding to 16 included.
 struct Shape {
   int lanes, vecs, threads;
   bool multi;
 };
-Shape shape_for(int C) {
+Shape shape_for(int C, bool bwd) {
   const int v = (C + 15) / 16 * 2;
   Shape s{0, 0, 0, false};
-  for (int k = 1; k <= 4; ++k)
+  for (int k = 1; k <= (bwd ? V_BK : V_FK); k += bwd || V_FK == 3 ? 2 : 1)
     for (int l = 4; l <= 32; l *= 2)
       if (l * k >= v && (!s.lanes || l * k < s.lanes * s.vecs)) s = {l, k, k == 1 ? THREADS : FEW, false};
-  if (s.lanes) return s;
-  s.lanes = (v + 31) / 32 * 32, s.vecs = 1, s.multi = true;
-  s.threads = s.lanes > THREADS / 2 ? s.lanes : THREADS / s.lanes * s.lanes;
-  return s;
+  const int lanes = (v + 31) / 32 * 32;
+  if (s.lanes && (s.vecs == 1 || s.lanes * s.vecs < lanes + (bwd ? 0 : 1))) return s;
+  // 64 lanes at least here, so at most eight rows and their barriers to a block; few
+  // blocks: each takes sixteen barriers, and an SM has them for four
+  return {lanes, 1, MAX_LANES / lanes * lanes, true};
 }
 
-// As many blocks as the card holds at once; the backward's join reads a piece of each.
-int blocks_an_sm(const Shape& s, bool bwd) { return s.multi || s.vecs == 1 ? 2 : s.vecs == 2 ? (bwd ? 3 : 4) : bwd ? 2 : 3; }
+// Blocks that an SM holds at once, by the kernels' registers and with two stages of the ring
+// at least; up to four stages in what that leaves of shared memory.
+struct Fit {
+  int blocks, stages;
+};
+Fit fit_of(const Shape& s, bool bwd, int pieces) {
+  const int regs = bwd ? (s.vecs == 1 ? 128 : 256) : s.vecs == 1 ? 104 : 128;
+  const int stage = s.vecs * pieces * s.threads * 16, weights = (bwd ? 12 : 16) * 8 * s.lanes * s.vecs + 2048;
+  const int most = 227 << 10;
+  Fit f{std::max(1, 65536 / (regs * s.threads)), 4};
+  while (f.blocks > 1 && f.blocks * (weights + 2 * stage) > most) --f.blocks;
+  f.stages = std::max(2, std::min(4, (most / f.blocks - weights) / std::max(stage, 1)));
+  return f;
+}
+// The backward's join reads a piece of each block's, so their number does not depend on
+// which matrices there are.
 int64_t blocks_for(int64_t n, const Shape& s, bool bwd) {
   const int64_t rows = s.threads / s.lanes;
-  return std::max<int64_t>(1, std::min<int64_t>((n + rows - 1) / rows, 152 * blocks_an_sm(s, bwd)));
-}
-
-// Stages of a ring of g.pieces a vector: up to four, two at least, in a block's share
-// of 220 KB beside `other` bytes.
-int ring_of(Args& g, const Shape& s, bool bwd, int other) {
-  const int stage = s.vecs * g.pieces * s.threads * 16, most = (220 << 10) / blocks_an_sm(s, bwd) - other;
-  g.stages = std::max(2, std::min(4, most / std::max(stage, 1)));
-  return g.stages * stage;
+  return std::max<int64_t>(1, std::min<int64_t>((n + rows - 1) / rows, 152 * fit_of(s, bwd, bwd ? 5 : 3).blocks));
 }
 
 struct ResidualWs {
@@ -677,7 +732,7 @@ struct ResidualWs {
 ResidualWs residual_ws(void* base, size_t cap, int64_t n, int C, bool* ok) {
   Arena ar(base, cap);
   ResidualWs w{};
-  const Shape s = shape_for(C);
+  const Shape s = shape_for(C, true);
   w.part = ar.take<float>((size_t)blocks_for(n, s, true) * 4 * s.lanes * s.vecs * 8);
   w.scalar = ar.take<float>((size_t)(C + 31) / 32);
   w.bytes = ar.used;
@@ -704,23 +759,29 @@ gnn_status launch(int64_t grid, int block, size_t smem, cudaStream_t st, void (*
   return GNN_OK;
 }
 
-constexpr int SMEM_MOST = 224 << 10;  // rows of 512 lanes, fp32 with a gate: 2 x 80 KB and 64 of weights
+constexpr int SMEM_MOST = 226 << 10;  // of the 227 KB, fit_of leaves 2 out
 
 template <bool BWD, class TB, class TR, class TY, bool MULTI, int K>
 gnn_status run_shape(Args& g, const Shape& s, cudaStream_t st) {
   static PerDevice done;
-  auto* k = BWD ? residual_bwd_kernel<TB, TR, TY, MULTI, K> : residual_fwd_kernel<TB, TR, TY, MULTI, K>;
+  auto* k = [] {
+    if constexpr (BWD)
+      return residual_bwd_kernel<TB, TR, TY, MULTI, K>;
+    else
+      return residual_fwd_kernel<TB, TR, TY, MULTI, K>;
+  }();
   const gnn_status r = allow_smem(k, SMEM_MOST, done);
   if (r != GNN_OK) return r;
   const int width = 8 * s.lanes * K * (int)sizeof(float), weights = (BWD ? 3 : 4) * width;
-  int ring = ring_of(g, s, BWD, weights);
+  g.stages = fit_of(s, BWD, g.pieces).stages;
+  int ring = g.stages * K * g.pieces * s.threads * 16;
   // the backward's sums of every warp or group pass through the ring
   if (BWD) ring = std::max(ring, (MULTI ? s.threads / s.lanes : s.threads / 32) * 4 * width);
   return launch(blocks_for(g.n, s, BWD), s.threads, weights + ring, st, k, g);
 }
 template <bool BWD, class TB, class TR, class TY>
 gnn_status run(Args& g, cudaStream_t st) {
-  const Shape s = shape_for(g.C);
+  const Shape s = shape_for(g.C, BWD);
   g.lanes = s.lanes;
   // pieces of 16 bytes of a lane's eight channels
   auto add = [&](int k, const void* p, int elem) {
@@ -735,10 +796,10 @@ gnn_status run(Args& g, cudaStream_t st) {
     add(0, g.R, sizeof(TR)), add(1, g.B, sizeof(TB)), add(2, g.gate == 2 ? g.G : nullptr, sizeof(TB));
   }
   if (s.multi) return run_shape<BWD, TB, TR, TY, true, 1>(g, s, st);
-  return s.vecs == 1   ? run_shape<BWD, TB, TR, TY, false, 1>(g, s, st)
-         : s.vecs == 2 ? run_shape<BWD, TB, TR, TY, false, 2>(g, s, st)
-         : s.vecs == 3 ? run_shape<BWD, TB, TR, TY, false, 3>(g, s, st)
-                       : run_shape<BWD, TB, TR, TY, false, 4>(g, s, st);
+  if (s.vecs == 1) return run_shape<BWD, TB, TR, TY, false, 1>(g, s, st);
+  if (s.vecs == 3) return run_shape<BWD, TB, TR, TY, false, 3>(g, s, st);
+  if constexpr (BWD) return GNN_ERR_UNSUPPORTED;  // shape_for has no such row
+  else return s.vecs == 2 ? run_shape<false, TB, TR, TY, false, 2>(g, s, st) : run_shape<false, TB, TR, TY, false, 4>(g, s, st);
 }
 
 // Types of branch, stream and next operand (one type, or an fp32 stream with a
@@ -935,7 +996,7 @@ extern "C" gnn_status gnn_residual_norm_bwd(const void* dH, int64_t lddh, const 
     if (s != GNN_OK) return s;
   }
   if (!want_q && !want_p) return GNN_OK;
-  const Shape sh = shape_for(C);
+  const Shape sh = shape_for(C, true);
   const int blocks = (C + 31) / 32;
   const Join j{w.part, n > 0 ? (int)blocks_for(n, sh, true) : 0, sh.lanes * sh.vecs * 8, C, scale_cols, w_post, b_post, scale, dw_post, db_post,
                dscale, dw_pre, db_pre, w.scalar, want_q, want_p};
