@@ -45,6 +45,7 @@ struct Args {
   float eps, inv_c;
   float4* stats;
   float* part;            // backward: [blocks][4][8 lanes K]
+  double* part_s;         // backward, one learned scale: every block's share of its gradient, or NULL
   int want_q, want_p;     // backward: which sums over all rows are kept
   // the ring: stages, 16-byte pieces of a lane in one, and where each matrix's begin
   int stages, pieces, at[5];
@@ -242,13 +243,14 @@ __device__ __forceinline__ void from_shared(const float* p, int c, int apart, in
 }
 
 // s w_post, s b_post, w_pre and (forward) b_pre of the block's `width` channels, zero
-// past the row's end.
+// past the row's end.  Where the gradient of one scale of all channels is wanted, that is
+// kept apart: the gradient is a sum of z without it.
 template <bool FWD, bool SPLIT>
 __device__ __forceinline__ void share_weights(const Args& g, float* to, int width) {
   for (int c = threadIdx.x; c < width; c += blockDim.x) {
     const bool there = c < g.C;
     const int at = weight_at<SPLIT>(c, width);
-    const float s = there ? (g.scale_cols == 0 ? 1.f : __ldg(g.scale + (g.scale_cols == 1 ? 0 : c))) : 0.f;
+    const float s = !there ? 0.f : g.scale_cols == 0 || (!FWD && g.part_s) ? 1.f : __ldg(g.scale + (g.scale_cols == 1 ? 0 : c));
     to[at] = s * (there && g.w_post ? __ldg(g.w_post + c) : 1.f);
     to[width + at] = there && g.b_post ? s * __ldg(g.b_post + c) : 0.f;
     to[2 * width + at] = there ? (g.w_pre ? __ldg(g.w_pre + c) : 1.f) : 0.f;
@@ -413,6 +415,14 @@ __global__ void __launch_bounds__(MULTI ? MAX_LANES : K == 1 ? THREADS : FEW, MU
   float t_next = row_gate(i);
   float4 s_next = row_stats(i);
   share_weights<false, SPLIT>(g, w_at, width);
+  const float2 one_scale = dup2(g.part_s ? __ldg(g.scale) : 1.f);
+  float ds_hi = 0.f, ds_lo = 0.f;  // D t z over this lane's channels and rows, and what the sum lost
+  // a sum of millions of terms of either sign: Knuth's two-term sum keeps its tail
+  auto add_ds = [&](float x) {
+    const float sum = ds_hi + x, part = sum - ds_hi;
+    ds_lo += (ds_hi - (sum - part)) + (x - part);
+    ds_hi = sum;
+  };
   Eight acc[4][K];  // sums of dY yh, dY, D t bh, D t
 #pragma unroll
   for (int a = 0; a < 4; ++a)
@@ -514,11 +524,18 @@ __global__ void __launch_bounds__(MULTI ? MAX_LANES : K == 1 ? THREADS : FEW, MU
           });
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            slope[j] = mul2_rn(slope[j], mul2_rn(d[k][j], fma2_rn(w[j], bh[j], b[j])));
+            const float2 z = fma2_rn(w[j], bh[j], b[j]);
+            slope[j] = mul2_rn(slope[j], mul2_rn(d[k][j], z));
             d[k][j] = mul2_rn(d[k][j], t[j]);
+            t[j] = z;
+          }
+          if (g.part_s) {
+            add_ds(dot(d[k], t));
+#pragma unroll
+            for (int j = 0; j < 4; ++j) slope[j] = mul2_rn(slope[j], one_scale);
           }
           if (g.dG && live) put<TB, SPLIT>(g.dG, i * g.lddg, c + k * span, apart, slope, m);
-        } else if (g.gate == 1) {
+        } else if (g.gate == 1 || g.part_s) {
           float2 z = dup2(0.f);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
@@ -526,6 +543,11 @@ __global__ void __launch_bounds__(MULTI ? MAX_LANES : K == 1 ? THREADS : FEW, MU
             d[k][j] = mul2_rn(d[k][j], t1);
           }
           s[2] += z.x + z.y;
+          if (g.part_s) add_ds(t1.x * (z.x + z.y));
+        }
+        if (g.part_s) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) w[j] = mul2_rn(w[j], one_scale);
         }
         // d: D t here, and times s w_post from here on
 #pragma unroll
@@ -540,7 +562,8 @@ __global__ void __launch_bounds__(MULTI ? MAX_LANES : K == 1 ? THREADS : FEW, MU
       const bool norm = g.post != GNN_NORM_NONE;
       if (g.gate == 1) {
         row.sum(s);
-        if (g.dG && live && row.lane == 0) static_cast<TB*>(g.dG)[i * g.lddg] = from_f32<TB>(s[2] * slope1.x);
+        if (g.dG && live && row.lane == 0)
+          static_cast<TB*>(g.dG)[i * g.lddg] = from_f32<TB>(s[2] * one_scale.x * slope1.x);
       } else if (g.post == GNN_NORM_LAYER) {
         float two[2] = {s[0], s[1]};
         row.sum(two);
@@ -567,6 +590,19 @@ __global__ void __launch_bounds__(MULTI ? MAX_LANES : K == 1 ? THREADS : FEW, MU
           put<TB, SPLIT>(g.dB, i * g.lddb, c + k * span, apart, d[k], m);
         }
       }
+    }
+  }
+  if (g.part_s) {
+    __shared__ double share[MAX_LANES / 32];
+    double t = (double)ds_hi + (double)ds_lo;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+    if ((threadIdx.x & 31) == 0) share[threadIdx.x >> 5] = t;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      t = 0;
+      for (int k = 0; k < threads / 32; ++k) t += share[k];
+      g.part_s[blockIdx.x] = t;
     }
   }
   if (!g.want_q && !g.want_p) return;
@@ -610,14 +646,14 @@ __global__ void __launch_bounds__(MULTI ? MAX_LANES : K == 1 ? THREADS : FEW, MU
 
 // The blocks' sums, in order, and the weights' gradients from them.  In fp32: an
 // SM adds two fp64 numbers a clock, and with those this kernel took 27 us of 39.  A
-// block takes 32 channels; scalar[] (one learned scale): its share of dscale.
+// block takes 32 channels; with one learned scale a block more adds its gradient.
 constexpr int JOIN_ROWS = 32;
 struct Join {
   const float* part;
+  const double* part_s;
   int blocks, width, C, scale_cols;
   const float *w_post, *b_post, *scale;
   float *dw_post, *db_post, *dscale, *dw_pre, *db_pre;
-  float* scalar;
   int want_q, want_p;
 };
 __global__ void __launch_bounds__(32 * JOIN_ROWS) residual_join_kernel(const Join g) {
@@ -625,6 +661,15 @@ __global__ void __launch_bounds__(32 * JOIN_ROWS) residual_join_kernel(const Joi
   cudaTriggerProgrammaticLaunchCompletion();
   cudaGridDependencySynchronize();
   const int lane = threadIdx.x & 31, r = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
+  if (blockIdx.x * 32 >= g.C) {
+    if (r) return;
+    double s = 0;
+    for (int b = lane; b < g.blocks; b += 32) s += g.part_s[b];
+#pragma unroll
+    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (lane == 0) g.dscale[0] = (float)s;
+    return;
+  }
   float s[4] = {0.f, 0.f, 0.f, 0.f};
   if (c < g.C) {
 #pragma unroll 5
@@ -647,35 +692,14 @@ __global__ void __launch_bounds__(32 * JOIN_ROWS) residual_join_kernel(const Joi
   __syncthreads();
   if (lane < 4) sm[lane][0][r] = lane == 0 ? s[0] : lane == 1 ? s[1] : lane == 2 ? s[2] : s[3];
   __syncthreads();
-  if (r) return;
-  float ds = 0.f;
-  if (c < g.C) {
-    const float P1 = sm[2][0][lane], P2 = sm[3][0][lane];
-    const float sc = g.scale_cols == 0 ? 1.f : g.scale_cols == 1 ? g.scale[0] : g.scale[c];
-    if (g.dw_pre) g.dw_pre[c] = sm[0][0][lane];
-    if (g.db_pre) g.db_pre[c] = sm[1][0][lane];
-    if (g.dw_post) g.dw_post[c] = sc * P1;
-    if (g.db_post) g.db_post[c] = sc * P2;
-    ds = fmaf(g.w_post ? g.w_post[c] : 1.f, P1, (g.b_post ? g.b_post[c] : 0.f) * P2);
-    if (g.dscale && g.scale_cols > 1) g.dscale[c] = ds;
-  }
-  if (g.dscale && g.scale_cols == 1) {
-#pragma unroll
-    for (int o = 16; o; o >>= 1) ds += __shfl_xor_sync(0xffffffffu, ds, o);
-    if (lane == 0) {
-      g.scalar[blockIdx.x] = ds;
-      if (gridDim.x == 1) g.dscale[0] = ds;
-    }
-  }
-}
-__global__ void __launch_bounds__(32) residual_scalar_kernel(const float* scalar, int count, float* dscale) {
-  cudaTriggerProgrammaticLaunchCompletion();
-  cudaGridDependencySynchronize();
-  float s = 0.f;
-  for (int i = threadIdx.x; i < count; i += 32) s += scalar[i];
-#pragma unroll
-  for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  if (threadIdx.x == 0) dscale[0] = s;
+  if (r || c >= g.C) return;
+  const float P1 = sm[2][0][lane], P2 = sm[3][0][lane];
+  const float sc = g.scale_cols == 0 ? 1.f : g.scale_cols == 1 ? g.scale[0] : g.scale[c];
+  if (g.dw_pre) g.dw_pre[c] = sm[0][0][lane];
+  if (g.db_pre) g.db_pre[c] = sm[1][0][lane];
+  if (g.dw_post) g.dw_post[c] = sc * P1;
+  if (g.db_post) g.db_post[c] = sc * P2;
+  if (g.dscale && g.scale_cols > 1) g.dscale[c] = fmaf(g.w_post ? g.w_post[c] : 1.f, P1, (g.b_post ? g.b_post[c] : 0.f) * P2);
 }
 
 // ---------------------------------------------------------------- host side
@@ -710,7 +734,7 @@ struct Fit {
 };
 Fit fit_of(const Shape& s, bool bwd, int pieces) {
   const int regs = bwd ? (s.vecs == 1 ? 128 : 256) : s.vecs == 1 ? 104 : 128;
-  const int stage = s.vecs * pieces * s.threads * 16, weights = (bwd ? 12 : 16) * 8 * s.lanes * s.vecs + 2048;
+  const int stage = s.vecs * pieces * s.threads * 16, weights = (bwd ? 12 : 16) * 8 * s.lanes * s.vecs + 4096;
   const int most = 227 << 10;
   Fit f{std::max(1, 65536 / (regs * s.threads)), 4};
   while (f.blocks > 1 && f.blocks * (weights + 2 * stage) > most) --f.blocks;
@@ -726,7 +750,7 @@ int64_t blocks_for(int64_t n, const Shape& s, bool bwd) {
 
 struct ResidualWs {
   float* part;
-  float* scalar;
+  double* part_s;
   size_t bytes;
 };
 ResidualWs residual_ws(void* base, size_t cap, int64_t n, int C, bool* ok) {
@@ -734,7 +758,7 @@ ResidualWs residual_ws(void* base, size_t cap, int64_t n, int C, bool* ok) {
   ResidualWs w{};
   const Shape s = shape_for(C, true);
   w.part = ar.take<float>((size_t)blocks_for(n, s, true) * 4 * s.lanes * s.vecs * 8);
-  w.scalar = ar.take<float>((size_t)(C + 31) / 32);
+  w.part_s = ar.take<double>((size_t)blocks_for(n, s, true));
   w.bytes = ar.used;
   *ok = ar.ok();
   return w;
@@ -759,7 +783,7 @@ gnn_status launch(int64_t grid, int block, size_t smem, cudaStream_t st, void (*
   return GNN_OK;
 }
 
-constexpr int SMEM_MOST = 226 << 10;  // of the 227 KB, fit_of leaves 2 out
+constexpr int SMEM_MOST = 224 << 10;  // of 227 KB; less than one is static, and fit_of leaves 4 out
 
 template <bool BWD, class TB, class TR, class TY, bool MULTI, int K>
 gnn_status run_shape(Args& g, const Shape& s, cudaStream_t st) {
@@ -777,7 +801,11 @@ gnn_status run_shape(Args& g, const Shape& s, cudaStream_t st) {
   int ring = g.stages * K * g.pieces * s.threads * 16;
   // the backward's sums of every warp or group pass through the ring
   if (BWD) ring = std::max(ring, (MULTI ? s.threads / s.lanes : s.threads / 32) * 4 * width);
-  return launch(blocks_for(g.n, s, BWD), s.threads, weights + ring, st, k, g);
+  // No more blocks to an SM than the grid counts on: a launch that starts while the
+  // last one ends would crowd SMs that are free first (716,847 x 256 forward, one
+  // call behind another: 541 us against 423 alone).
+  const int smem = std::max(weights + ring, (227 << 10) / (fit_of(s, BWD, BWD ? 5 : 3).blocks + 1));
+  return launch(blocks_for(g.n, s, BWD), s.threads, smem, st, k, g);
 }
 template <bool BWD, class TB, class TR, class TY>
 gnn_status run(Args& g, cudaStream_t st) {
@@ -962,16 +990,16 @@ extern "C" gnn_status gnn_residual_norm_bwd(const void* dH, int64_t lddh, const 
     GNN_REQUIRE(gate_cols != 1 || !dgate || (((uintptr_t)dgate & (type_size(b_type) - 1)) == 0 && lddg >= 1 && lddg <= LD_MOST),
                 "%s: dgate of one value a row is misaligned or has no stride", who);
   }
-  const int want_q = dw_pre || db_pre, want_p = dw_post || db_post || dscale;
+  const int want_q = dw_pre || db_pre, want_p = dw_post || db_post || (dscale && scale_cols > 1), want_s = dscale && scale_cols == 1;
   bool ok;
   const ResidualWs w = residual_ws(ws, ws_bytes, n, C, &ok);
-  GNN_REQUIRE((!want_q && !want_p) || (ws && ok && ((uintptr_t)ws & 7) == 0),
+  GNN_REQUIRE((!want_q && !want_p && !want_s) || (ws && ok && ((uintptr_t)ws & 7) == 0),
               "%s: workspace too small (%zu < %zu) or misaligned", who, ws_bytes, w.bytes);
   if (n > 0) {
     const Span outs[9] = {span(dR, n, out_cols(C, r_type), lddr, r_type), span(dB, n, out_cols(C, b_type), lddb, b_type),
                           span(dgate, n, gate_cols > 1 ? out_cols(C, b_type) : 1, lddg, b_type), flat(dw_post, 4ll * C),
                           flat(db_post, 4ll * C), flat(dscale, 4ll * scale_cols), flat(dw_pre, 4ll * C), flat(db_pre, 4ll * C),
-                          flat(want_q || want_p ? ws : nullptr, (int64_t)w.bytes)};
+                          flat(want_q || want_p || want_s ? ws : nullptr, (int64_t)w.bytes)};
     const Span ins[10] = {span(dH, n, C, lddh, r_type), span(dY, n, C, lddy, y_type), span(B, n, C, ldb, b_type),
                           span(dY ? H : nullptr, n, C, ldh, r_type), span(gate_cols ? gate : nullptr, n, gate_cols, ldg, b_type),
                           flat(stats, n * 16), flat(w_post, 4ll * C), flat(b_post, 4ll * C), flat(scale, 4ll * scale_cols),
@@ -989,18 +1017,16 @@ extern "C" gnn_status gnn_residual_norm_bwd(const void* dH, int64_t lddh, const 
     g.w_post = w_post, g.b_post = b_post, g.scale = scale, g.w_pre = w_pre;
     g.scale_cols = scale_cols, g.inv_c = 1.f / (float)C;
     g.stats = reinterpret_cast<float4*>(const_cast<float*>(stats)), g.part = w.part;
-    g.want_q = want_q, g.want_p = want_p;
+    g.want_q = want_q, g.want_p = want_p, g.part_s = want_s ? w.part_s : nullptr;
     s = with_types(b_type, r_type, y_type, [&](auto b, auto r, auto y) {
       return run<true, decltype(b), decltype(r), decltype(y)>(g, as_stream(stream));
     });
     if (s != GNN_OK) return s;
   }
-  if (!want_q && !want_p) return GNN_OK;
+  if (!want_q && !want_p && !want_s) return GNN_OK;
   const Shape sh = shape_for(C, true);
   const int blocks = (C + 31) / 32;
-  const Join j{w.part, n > 0 ? (int)blocks_for(n, sh, true) : 0, sh.lanes * sh.vecs * 8, C, scale_cols, w_post, b_post, scale, dw_post, db_post,
-               dscale, dw_pre, db_pre, w.scalar, want_q, want_p};
-  s = launch(blocks, 32 * JOIN_ROWS, 0, as_stream(stream), residual_join_kernel, j);
-  if (s != GNN_OK || !dscale || scale_cols != 1 || blocks == 1) return s;
-  return launch(1, 32, 0, as_stream(stream), residual_scalar_kernel, (const float*)w.scalar, blocks, dscale);
+  const Join j{w.part, w.part_s, n > 0 ? (int)blocks_for(n, sh, true) : 0, sh.lanes * sh.vecs * 8, C, scale_cols, w_post, b_post,
+               scale, dw_post, db_post, dscale, dw_pre, db_pre, want_q, want_p};
+  return launch(blocks + want_s, 32 * JOIN_ROWS, 0, as_stream(stream), residual_join_kernel, j);
 }
