@@ -58,6 +58,7 @@ struct Table {
   Mat mat[MAX_MATS];
   int first[MAX_MATS + 1];  // blocks (or parts) before each matrix
   int count;
+  int small;  // every matrix stays in one CTA's shared memory
   int bn;  // the steps' tiles: columns of a CTA's, or 0 for pairs of CTAs
   int half[3];  // pairs: tiles of 128 columns instead of 256, by product
   int64_t blocks;  // of the operands, from the workspace's start
@@ -842,6 +843,272 @@ __global__ void __launch_bounds__(PRODUCT_THREADS, 1) steps_kernel(const __grid_
   walk<COLS>(g, smem_raw);
 }
 
+// ------------------------------------------------------------- small matrices
+// A matrix of up to 64 x 512 stays in one CTA's shared memory from its gradient to its
+// update: no tile waits for another CTA's, which is what bounds small matrices above
+// (16 of 64 x 256: 94 us).  The same limbs, products and sums; every 64 of k has an
+// accumulator of its own in TMEM, so that a product is issued without a pause.
+// Operands have 64 rows; an MMA reads 128 of A, and what the other 64 give stays in
+// lanes of TMEM that nobody reads.
+constexpr int SMALL_M = 64, SMALL_N = 512;
+constexpr int SMALL_THREADS = 512;
+constexpr int HALF_LIMB = 64 * 128, HALF_BLOCK = 2 * HALF_LIMB;  // of 64 rows
+struct SmallSteps {
+  int steps;
+  float coeff[MAX_STEPS][3];
+  unsigned* flags;
+};
+constexpr int small_smem(int kb) { return (kb + 3) * HALF_BLOCK + 1024 /*barrier*/ + 1024 /*align*/; }
+
+// Byte of 8 columns (chunk k of 8) of row r of a limb in shared memory.
+__device__ __forceinline__ int small_at(int r, int k) { return r * 128 + ((k ^ (r & 7)) << 4); }
+
+__global__ void __launch_bounds__(SMALL_THREADS, 1)
+    small_kernel(const __grid_constant__ Table tab, const Hyper h, const __grid_constant__ SmallSteps g, float* norms) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ double part[SMALL_THREADS / 32];
+  __shared__ float shared_norm;
+  cudaTriggerProgrammaticLaunchCompletion();
+  const Mat& t = tab.mat[blockIdx.x];
+  uint8_t* const x = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int kbs = (t.n + 63) >> 6, kx = (t.n + 15) >> 4, km = (t.m + 15) >> 4;
+  uint8_t* const a = x + kbs * HALF_BLOCK;
+  uint8_t* const p = a + HALF_BLOCK;
+  uint64_t* const bar = reinterpret_cast<uint64_t*>(p + 2 * HALF_BLOCK);
+  uint32_t* const tmem_at = reinterpret_cast<uint32_t*>(bar + 1);
+  volatile int* const abort_flag = reinterpret_cast<volatile int*>(tmem_at + 1);
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const uint32_t tmem_cols = kbs <= 4 ? 256 : 512;
+  if (threadIdx.x == 0) {
+    tc::mbar_init(bar, 1);
+    *abort_flag = 0;
+    tc::fence_barrier_init();
+  }
+  if (warp == 0) {
+    tc::tmem_alloc(tmem_at, tmem_cols);
+    tc::tmem_relinquish();
+  }
+  for (int e = threadIdx.x; e < kbs * HALF_BLOCK / 16; e += SMALL_THREADS)
+    reinterpret_cast<uint4*>(x)[e] = make_uint4(0, 0, 0, 0);
+  tc::fence_before_sync();
+  cudaGridDependencySynchronize();
+  // |u|
+  const int across = (t.cols + 3) >> 2, quads = t.rows * across;
+  double sum = 0;
+  for (int e = threadIdx.x; e < quads; e += 4 * SMALL_THREADS) {
+    Quad q[4];
+    float s = 0.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int i = e + k * SMALL_THREADS, row = min(i / across, t.rows - 1);
+      q[k].load(t, h, row, i % across * 4, i < quads ? t.cols : 0);
+    }
+    float4 u[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      u[k] = q[k].update(h);
+      s = fmaf(u[k].x, u[k].x, fmaf(u[k].y, u[k].y, fmaf(u[k].z, u[k].z, fmaf(u[k].w, u[k].w, s))));
+    }
+    if (s > 1e-28f && s < 1e38f) {
+      sum += (double)s;
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        sum += (double)u[k].x * u[k].x + (double)u[k].y * u[k].y + (double)u[k].z * u[k].z + (double)u[k].w * u[k].w;
+    }
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (lane == 0) part[warp] = sum;
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = *tmem_at;
+  if (threadIdx.x == 0) {
+    double s = 0;
+    for (int w = 0; w < SMALL_THREADS / 32; ++w) s += part[w];
+    shared_norm = (float)sqrt(s);
+    if (norms) norms[t.slot] = shared_norm;
+  }
+  __syncthreads();
+  const float norm = shared_norm;
+  const bool good = isfinite(norm);
+  const float inv = (float)((double)UNIT / ((double)norm + h.eps));
+  for (int e = threadIdx.x; e < quads; e += SMALL_THREADS) {
+    const int row = e / across, col = e % across * 4;
+    Quad q;
+    q.load(t, h, row, col, t.cols);
+    const float4 u = q.update(h);
+    if (!good) continue;
+    if (!h.orth) store4(t.mom, (int64_t)row * t.ldm, col, t.cols, h.mt, t.quads & MOM, q.m);
+    uint32_t hi[2], lo[2];
+    limbs(u.x * inv, u.y * inv, hi[0], lo[0]);
+    limbs(u.z * inv, u.w * inv, hi[1], lo[1]);
+    if (t.flip) {  // four rows of X; those past its last stay zero
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int r = col + j;
+        if (r >= t.m) break;
+        uint8_t* to = x + (row >> 6) * HALF_BLOCK + small_at(r, (row & 63) >> 3) + (row & 7) * 2;
+        *reinterpret_cast<uint16_t*>(to) = (uint16_t)(hi[j >> 1] >> (16 * (j & 1)));
+        *reinterpret_cast<uint16_t*>(to + HALF_LIMB) = (uint16_t)(lo[j >> 1] >> (16 * (j & 1)));
+      }
+    } else {
+      uint8_t* to = x + (col >> 6) * HALF_BLOCK + small_at(row, (col & 63) >> 3) + (col & 7) * 2;
+      *reinterpret_cast<uint2*>(to) = make_uint2(hi[0], hi[1]);
+      *reinterpret_cast<uint2*>(to + HALF_LIMB) = make_uint2(lo[0], lo[1]);
+    }
+  }
+  tc::fence_async_smem();
+  __syncthreads();
+
+  // 64 of k (or `some` 16s of it) of a product, from one lane
+  auto multiply64 = [&](uint32_t d, uint32_t left, uint32_t right, bool right_mn, int cols, int some) {
+    const uint32_t idesc = tc::idesc_16(false, 128, cols, false, right_mn);
+    const uint64_t l = tc::sw128_desc(left, 16), r = tc::sw128_desc(right, right_mn ? HALF_BLOCK : 16);
+    const uint32_t limb = HALF_LIMB >> 4, ls = 32 >> 4, rs = (right_mn ? 2048 : 32) >> 4;
+    for (int k = 0; k < some; ++k) {
+      tc::mma_bf16(d, l + k * ls, r + limb + k * rs, idesc, k ? 1u : 0u);
+      tc::mma_bf16(d, l + limb + k * ls, r + k * rs, idesc, 1u);
+    }
+    for (int k = 0; k < some; ++k) tc::mma_bf16(d, l + k * ls, r + k * rs, idesc, 1u);
+  };
+  const uint32_t xs = tc::smem_u32(x), as = tc::smem_u32(a), ps = tc::smem_u32(p);
+  uint32_t ph = 0;
+  // every thread: the product is there, or all give up
+  auto arrived = [&] {
+    const bool ok = tc::mbar_wait(bar, ph, g.flags, abort_flag);
+    ph ^= 1;
+    const bool all_ok = !__syncthreads_or(!ok);
+    tc::fence_after_sync();
+    return all_ok;
+  };
+  // what was written is there for the next product
+  auto written = [&] {
+    tc::fence_before_sync();
+    tc::fence_async_smem();
+    __syncthreads();
+    tc::fence_after_sync();
+  };
+  const int q = warp & 3, piece = warp >> 2, r = q * 32 + lane;  // TMEM lanes; 16 columns of 64
+  const bool mine = q < 2;
+  const uint32_t lane0 = tmem + ((uint32_t)(q * 32) << 16);
+  auto put16 = [&](uint8_t* limb, int col, const float (&f)[16]) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      uint4 hi, lo;
+      limbs(f[8 * k], f[8 * k + 1], hi.x, lo.x), limbs(f[8 * k + 2], f[8 * k + 3], hi.y, lo.y);
+      limbs(f[8 * k + 4], f[8 * k + 5], hi.z, lo.z), limbs(f[8 * k + 6], f[8 * k + 7], hi.w, lo.w);
+      uint8_t* to = limb + small_at(r, (col >> 3) + k);
+      *reinterpret_cast<uint4*>(to) = hi;
+      *reinterpret_cast<uint4*>(to + HALF_LIMB) = lo;
+    }
+  };
+  // what truncated sums lose on average (see the steps' kernel)
+  auto back_of = [](int k16) { return k16 > 2 ? 1.f + 0x1p-23f : 1.f; };
+  for (int s = 0; s < g.steps; ++s) {
+    const float ca = g.coeff[s][0], cb = g.coeff[s][1], cc = g.coeff[s][2];
+    if (warp == 0 && tc::elect_one()) {
+      for (int kb = 0; kb < kbs; ++kb)
+        multiply64(tmem + 64 * kb, xs + kb * HALF_BLOCK, xs + kb * HALF_BLOCK, false, 64, min(kx - 4 * kb, 4));
+      tc::mma_commit(bar);
+    }
+    __syncwarp();
+    if (!arrived()) goto done;
+    float am[16];
+    if (mine) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) am[j] = 0.f;
+      for (int kb = 0; kb < kbs; ++kb) {
+        float v[16];
+        tc::tmem_ld16(lane0 + 64 * kb + 16 * piece, v);
+        const float back = back_of(kx - 4 * kb);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) am[j] = fmaf(back, v[j], am[j]);
+      }
+#pragma unroll
+      for (int j = 0; j < 16; ++j) am[j] *= 1.f / UNIT;
+      put16(a, 16 * piece, am);
+    }
+    written();
+    if (warp == 0 && tc::elect_one()) {
+      multiply64(tmem, as, as, false, 64, km);
+      tc::mma_commit(bar);
+    }
+    __syncwarp();
+    if (!arrived()) goto done;
+    if (mine) {
+      float v[16];
+      tc::tmem_ld16(lane0 + 16 * piece, v);
+      const float back = back_of(km) * (1.f / UNIT);
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        // A as its limbs hold it
+        const __half ah = __float2half_rn(am[j]);
+        const float held = __half2float(ah) + __half2float(__float2half_rn(am[j] - __half2float(ah)));
+        v[j] = fmaf(cc, v[j] * back, cb * held) + (r == 16 * piece + j ? ca * UNIT : 0.f);
+      }
+      put16(p, 16 * piece, v);
+    }
+    written();
+    if (warp == 0 && tc::elect_one()) {
+      for (int kb = 0; kb < kbs; kb += 4)
+        multiply64(tmem + 64 * kb, ps, xs + kb * HALF_BLOCK, true, 64 * min(kbs - kb, 4), km);
+      tc::mma_commit(bar);
+    }
+    __syncwarp();
+    if (!arrived()) goto done;
+    if (mine) {
+      const float back = back_of(km) * (1.f / UNIT);
+      for (int kb = 0; kb < kbs; ++kb) {
+        float v[16];
+        tc::tmem_ld16(lane0 + 64 * kb + 16 * piece, v);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) v[j] *= back;
+        put16(x + kb * HALF_BLOCK, 16 * piece, v);
+      }
+    }
+    written();
+  }
+  for (int e = threadIdx.x; e < quads; e += SMALL_THREADS) {
+    const int row = e / across, col = e % across * 4;
+    if (!good && !h.orth) break;  // this matrix stays as it is
+    float o[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int xr = t.flip ? col + j : row, xc = t.flip ? row : col + j;
+      const uint8_t* from = x + (xc >> 6) * HALF_BLOCK + small_at(xr, (xc & 63) >> 3) + (xc & 7) * 2;
+      const bool there = xr < t.m && xc < t.n;
+      o[j] = !good ? __int_as_float(0x7fc00000)
+             : there ? (__half2float(*reinterpret_cast<const __half*>(from)) +
+                        __half2float(*reinterpret_cast<const __half*>(from + HALF_LIMB))) * (1.f / UNIT)
+                     : 0.f;
+    }
+    const float4 f = make_float4(o[0], o[1], o[2], o[3]);
+    const int64_t at = (int64_t)row * t.ldp;
+    if (h.orth) {
+      store4(t.param, at, col, t.cols, h.pt, t.quads & PARAM, f);
+    } else {
+      const float4 w = load4(t.param, at, col, t.cols, h.pt, t.quads & PARAM);
+      const float4 n = axpy4(f, -h.lr * t.scale, make_float4(w.x * h.decay, w.y * h.decay, w.z * h.decay, w.w * h.decay));
+      store4(t.param, at, col, t.cols, h.pt, t.quads & PARAM, n);
+      if (t.copy) store4(t.copy, (int64_t)row * t.ldc, col, t.cols, GNN_BF16, t.quads & COPY, n);
+    }
+  }
+done:
+  if (*abort_flag) {
+    // a wait gave up: products in flight land within microseconds
+    const long long t0 = clock64();
+    while (clock64() - t0 < 4000000) {
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == 0) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, tmem_cols);
+  }
+}
+
 // ---------------------------------------------------------------- host side
 int64_t up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 
@@ -942,6 +1209,18 @@ double clocks(const Table& tab, int bn, const int (&half)[3]) {
 
 // The tiles of a pass, and every matrix's place in its workspace.
 void place_pass(Table& tab, Arena& ar) {
+  // a pass of small matrices alone needs none; among larger ones theirs are hidden
+  tab.small = 1;
+  for (int i = 0; i < tab.count; ++i) {
+    const int m = std::min(tab.mat[i].rows, tab.mat[i].cols), n = std::max(tab.mat[i].rows, tab.mat[i].cols);
+    tab.small &= m <= SMALL_M && n <= SMALL_N;
+  }
+  tab.blocks = 0;
+  if (tab.small) {
+    for (int i = 0; i < tab.count; ++i) sides(tab.mat[i], 64);
+    ar.take<int>(1);
+    return;
+  }
   const int whole[3] = {0, 0, 0};
   int half[3];
   for (Phase ph : {GRAM, POLY, NEXT}) half[ph] = clocks(tab, ph, 0, 1) < clocks(tab, ph, 0, 0);
@@ -1011,6 +1290,19 @@ gnn_status run_pass(void* ws, Table& tab, const Hyper& h, const float* coeffs, i
     for (int i = 0; i < tab.count; ++i) tab.first[i + 1] = tab.first[i] + of(tab.mat[i]);
     return tab.first[tab.count];
   };
+  if (tab.small) {
+    static PerDevice done;
+    GNN_TRY(allow_smem(small_kernel, small_smem(SMALL_N / 64), done));
+    SmallSteps g;
+    g.steps = steps;
+    for (int s = 0; s < steps; ++s)
+      for (int k = 0; k < 3; ++k) g.coeff[s][k] = coeffs[3 * s + k];
+    g.flags = device_flags();
+    if (!g.flags) return fail(GNN_ERR_CUDA, "device flag word unavailable");
+    int kb = 0;
+    for (int i = 0; i < tab.count; ++i) kb = std::max(kb, (tab.mat[i].n + 63) / 64);
+    return launch(tab.count, SMALL_THREADS, small_smem(kb), st, small_kernel, tab, h, g, norms);
+  }
   int grid = blocks([](const Mat& t) { return t.parts; });
   GNN_TRY(launch(grid, THREADS, 0, st, square_kernel, tab, h));
   grid = blocks([](const Mat& t) { return t.mb * t.nb; });

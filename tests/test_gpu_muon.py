@@ -44,7 +44,7 @@ def close(got, want, bound, t, what):
 
 SIZES = [(1, 1), (1, 2), (1, 300), (300, 1), (2, 2), (7, 5), (16, 64), (63, 64), (64, 64), (65, 64), (64, 129), (128, 128), (129, 127),
          (127, 500), (130, 300), (256, 256), (256, 512), (512, 256), (257, 511), (300, 800), (800, 300), (602, 256), (47, 1000),
-         (640, 640), (385, 1025)]
+         (640, 640), (385, 1025), (64, 256), (64, 512), (512, 64), (33, 511), (500, 17), (64, 513), (65, 512), (48, 320)]
 
 
 @pytest.mark.parametrize("i,size", list(enumerate(SIZES)))
@@ -63,9 +63,10 @@ def test_sizes(i, size):
 
 @pytest.mark.parametrize("steps,coeffs", [(0, ()), (1, ref.NS), (2, ((4.0, -6.0, 2.5), (2.0, -1.5, 0.5))), (7, (1.875, -1.25, 0.375)),
                                           (16, (1.5, -0.5, 0.0))])
-def test_steps_and_coefficients(steps, coeffs):
-    x = matrix(70, 150, 3)
-    O = torch.empty(70, 150, device="cuda")  # noqa: E741
+@pytest.mark.parametrize("rows", [70, 60])
+def test_steps_and_coefficients(steps, coeffs, rows):
+    x = matrix(rows, 150, 3)
+    O = torch.empty(rows, 150, device="cuda")  # noqa: E741
     G.gnn_orthogonalise(x.cuda(), O, steps=steps, coeffs=coeffs)
     close(O, *ref.spread(x.double(), coeffs, steps), F32, "O")
 
@@ -83,8 +84,9 @@ def test_batches(count, rows, cols):
     assert (buf[:, rows:] == GUARD).all() and (buf[:, :, cols:] == GUARD).all()
 
 
-def test_in_place_and_same_bits():
-    x = matrix(300, 200, 8).cuda()
+@pytest.mark.parametrize("rows,cols", [(300, 200), (40, 200)])
+def test_in_place_and_same_bits(rows, cols):
+    x = matrix(rows, cols, 8).cuda()
     a, b = torch.empty_like(x), torch.empty_like(x)
     G.gnn_orthogonalise(x, a)
     G.gnn_orthogonalise(x, b)
@@ -101,13 +103,14 @@ def test_magnitudes(size):
     close(O, *ref.spread(x.double(), ref.NS, 5), F32, "O")
 
 
-def test_zero_one_direction_and_not_finite():
-    x = torch.zeros(5, 60, 130)
-    x[1] = matrix(60, 1, 1) @ matrix(1, 130, 2)
-    x[2:] = matrix(60, 130, 3)
+@pytest.mark.parametrize("rows", [60, 90])
+def test_zero_one_direction_and_not_finite(rows):
+    x = torch.zeros(5, rows, 130)
+    x[1] = matrix(rows, 1, 1) @ matrix(1, 130, 2)
+    x[2:] = matrix(rows, 130, 3)
     x[3, 5, 7] = float("nan")
     x[4, 59, 129] = float("inf")
-    O, norms = torch.empty(5, 60, 130, device="cuda"), torch.empty(5, device="cuda")  # noqa: E741
+    O, norms = torch.empty(5, rows, 130, device="cuda"), torch.empty(5, device="cuda")  # noqa: E741
     G.gnn_orthogonalise(x.cuda(), O, norms=norms)
     assert (O[0] == 0).all() and norms[0] == 0
     for i in (1, 2):
@@ -123,7 +126,7 @@ def step64(p, g, m, lr, mu, nesterov, wd, scale, gs, coeffs, steps):
     return p.double() * (1 - lr * wd) - lr * scale * o, m, lr * scale * bound, torch.linalg.matrix_norm(u)
 
 
-CASES = [[(256, 512), (256, 512), (512, 256)], [(300, 80), (1, 40), (40, 1), (64, 64), (3, 700), (129, 131)], [(20, 30)] * 70, [(5, 7), (0, 3), (9, 0)]]
+CASES = [[(64, 300), (300, 64), (1, 1), (17, 512), (9, 5)], [(256, 512), (256, 512), (512, 256)], [(300, 80), (1, 40), (40, 1), (64, 64), (3, 700), (129, 131)], [(20, 30)] * 70, [(5, 7), (0, 3), (9, 0)]]
 
 
 @pytest.mark.parametrize("k,shapes", list(enumerate(CASES)))
@@ -136,7 +139,7 @@ def test_step(k, shapes, pt, gt, mt, nesterov):
     P, Gr, M = ([padded(t, 3) for t in ts] for ts in (p, g, m))
     C = [padded(torch.zeros(*t.shape, dtype=BF16), 5) if i % 3 != 1 else None for i, t in enumerate(p)]
     cut = lambda ts: [None if b is None else b[:, :c] for b, (_, c) in zip(ts, shapes)]  # noqa: E731
-    scales = [0.3 + 0.1 * (i % 4) for i in range(n)] if k == 1 else None
+    scales = [0.3 + 0.1 * (i % 4) for i in range(n)] if k == 2 else None
     handle = G.MuonTensors(cut(P), cut(Gr), cut(M), cut(C), scales)
     norms = torch.full((n,), -1.0, device="cuda")
     G.gnn_muon_step(handle, 0.02, momentum=0.9, nesterov=nesterov, weight_decay=0.1, grad_scale=0.5, norms=norms)
@@ -160,8 +163,9 @@ def test_step(k, shapes, pt, gt, mt, nesterov):
             assert (C[i][:, c:] == GUARD).all()
 
 
-def test_a_matrix_that_is_not_finite_is_left_as_it_is():
-    p, g, m = ([matrix(100, 60, 10 * s + i).cuda() for i in range(3)] for s in range(3))
+@pytest.mark.parametrize("rows", [100, 50])
+def test_a_matrix_that_is_not_finite_is_left_as_it_is(rows):
+    p, g, m = ([matrix(rows, 80, 10 * s + i).cuda() for i in range(3)] for s in range(3))
     g[1][3, 4] = float("inf")
     before = [t.clone() for t in p + m]
     norms = torch.zeros(3, device="cuda")
@@ -171,10 +175,11 @@ def test_a_matrix_that_is_not_finite_is_left_as_it_is():
         assert torch.equal(p[i], before[i]) == (i == 1) and torch.equal(m[i], before[3 + i]) == (i == 1)
 
 
-def test_streams_and_graphs():
+@pytest.mark.parametrize("shapes", [[(130, 70), (64, 300)], [(30, 70), (300, 64)]])
+def test_streams_and_graphs(shapes):
     """A captured step, replayed, does what steps one after the other do."""
     def new():
-        return [[matrix(r, c, 7 * i + j).cuda() for i, (r, c) in enumerate([(130, 70), (64, 300)])] for j in range(3)]
+        return [[matrix(r, c, 7 * i + j).cuda() for i, (r, c) in enumerate(shapes)] for j in range(3)]
 
     p, g, m = new()
     h = G.MuonTensors(p, g, m)

@@ -58,7 +58,7 @@ def orth(lib, X=MB, ldx=64, sx=0, xt=F32, count=1, rows=32, cols=64, coeffs=(3.0
     (dict(coeffs=(INF,) * 15), INVALID), (dict(eps=0.0), INVALID), (dict(eps=-1.0), INVALID), (dict(eps=NAN), INVALID), (dict(eps=INF), INVALID),
     (dict(norms=2), INVALID), (dict(X=None), INVALID), (dict(O=None), INVALID), (dict(X=MB + 2), INVALID), (dict(O=2 * MB + 1, ot=BF16), INVALID),
     (dict(ldx=63), INVALID), (dict(ldo=32), INVALID), (dict(count=2, sx=100, so=4096), INVALID), (dict(count=2, sx=4096, so=0), INVALID),
-    (dict(ws=None), INVALID), (dict(ws=16 * MB + 128), INVALID), (dict(ws_bytes=1000), INVALID), (dict(O=MB + 256), INVALID),
+    (dict(ws=None), INVALID), (dict(ws=16 * MB + 128), INVALID), (dict(ws_bytes=100), INVALID), (dict(rows=65, cols=70, ldx=70, ldo=70, ws_bytes=1000), INVALID), (dict(O=MB + 256), INVALID),
     (dict(O=MB, ldo=65), INVALID), (dict(O=MB, ot=BF16), INVALID)])
 def test_orthogonalise_refuses(lib, bad, code):
     assert orth(lib, **bad) == code
@@ -87,7 +87,7 @@ def muon(lib, count=1, pt=F32, gt=F32, mt=F32, lr=0.01, mu=0.9, nesterov=1, wd=0
     (dict(grad=2 * MB + 1, gt=BF16), INVALID), (dict(m=3 * MB + 3), INVALID), (dict(copy=4 * MB + 1), INVALID), (dict(ldp=63), INVALID),
     (dict(ldg=0), INVALID), (dict(ldm=-64), INVALID), (dict(copy=4 * MB, ldc=60), INVALID), (dict(rows=-1), INVALID), (dict(rows=70000), UNSUPPORTED),
     (dict(scale=NAN), INVALID), (dict(grad=MB), INVALID), (dict(m=MB + 128), INVALID), (dict(copy=MB), INVALID), (dict(copy=3 * MB + 64), INVALID),
-    (dict(ws=None), INVALID), (dict(ws=16 * MB + 64), INVALID), (dict(ws_bytes=4096), INVALID)])
+    (dict(ws=None), INVALID), (dict(ws=16 * MB + 64), INVALID), (dict(ws_bytes=100), INVALID), (dict(rows=65, cols=70, ldp=70, ldg=70, ldm=70, ws_bytes=4096), INVALID)])
 def test_muon_refuses(lib, bad, code):
     assert muon(lib, **bad) == code
     assert b"gnn_muon" in lib.gnn_last_error()
@@ -101,10 +101,11 @@ def test_workspaces(lib):
     assert lib.gnn_muon_workspace(None, 0, None) == INVALID
     assert lib.gnn_muon_workspace(None, 0, ctypes.byref(nb)) == 0 and nb.value == 0
     sizes = []
-    for count in (0, 1, 64, 1000):  # 64 matrices a pass
-        assert lib.gnn_orthogonalise_workspace(count, 64, 256, ctypes.byref(nb)) == 0
+    for count in (0, 1, 64, 1024):  # 64 matrices a pass
+        assert lib.gnn_orthogonalise_workspace(count, 65, 256, ctypes.byref(nb)) == 0
         sizes.append(nb.value)
     assert sizes[0] == 0 < sizes[1] < sizes[2] == sizes[3]
+    assert lib.gnn_orthogonalise_workspace(1000, 512, 64, ctypes.byref(nb)) == 0 and nb.value <= 256
 
 
 def test_descriptor_layout():
