@@ -820,11 +820,13 @@ gnn_status gnn_adamw_step(const gnn_adamw_tensor* tensors, int32_t n_tensors, in
  * ldx, ldo; matrices stride_x, stride_o elements apart; any GNN_* types):
  *   X0 = X / (|X|_F + eps), then `steps` times (0 to 16)
  *   X <- a X + (b A + c A A) X,  A = X X'   (X' X where rows > cols)
- * with {a, b, c} = coeffs[3 s], a host array (each within 32 of zero).  Operands
- * are held to 22 bits, down to 2^-35 (of a matrix of norm one), products accumulate in fp32; the steps have to keep every
- * singular value below 60.  norms (fp32 [count], may be NULL) receives |X|_F.  A
- * matrix whose norm is not finite in fp32 gives NaN.  O may be X (one type size and
- * strides).  rows, cols <= 65536, the smaller of them <= 16384. */
+ * with {a, b, c} = coeffs[3 s], a host array (each within 32 of zero), eps of at
+ * least 1e-30.  Operands are held to 22 bits, down to 2^-35 (of a matrix of norm
+ * one), products accumulate in fp32; the steps have to keep every singular value v
+ * below 7 and a + b v^2 + c v^4 within 60 of zero.  norms (fp32 [count], may be NULL)
+ * receives |X|_F.  A matrix whose norm is not finite in fp32 gives NaN.  O may be X
+ * (one type size and strides).  rows, cols <= 65536, the smaller of them <= 16384.
+ * Workspaces lie on a 256-byte border. */
 gnn_status gnn_orthogonalise_workspace(int32_t count, int32_t rows, int32_t cols,
                                        size_t* ws_bytes);
 gnn_status gnn_orthogonalise(const void* X, int64_t ldx, int64_t stride_x, int32_t x_type,
@@ -841,8 +843,7 @@ gnn_status gnn_orthogonalise(const void* X, int64_t ldx, int64_t stride_x, int32
  * receives the updated parameters rounded.  A matrix whose |u|_F is not finite
  * in fp32 keeps its parameters, copy and momentum; norms (fp32 [n_tensors], may
  * be NULL) receives every |u|_F (matrices without elements have none written).
- * No two arrays of a call overlap, nor is a matrix listed twice.  Workspaces of
- * both functions lie on a 256-byte border. */
+ * No two arrays of a call overlap, nor is a matrix listed twice. */
 typedef struct gnn_muon_tensor {
   void* param;      /* fp32 or bf16 [rows][cols], updated in place */
   const void* grad; /* fp32, bf16 or fp16                          */

@@ -204,14 +204,24 @@ __global__ void __launch_bounds__(THREADS) square_kernel(const __grid_constant__
   }
 }
 
-// |u|_F, in every thread of the block; `sm` is one double.
-__device__ __forceinline__ double norm_of(const double* partial, int i, int parts, double* sm) {
+// sqrt(s) in fp32 without fp64's root, which an SM forms slowly: s by an even power of
+// two, so that fp32 holds it.
+__device__ __forceinline__ float root_of(double s) {
+  if (!(s > 0) || !isfinite(s)) return (float)s;
+  const int e = ilogb(s) & ~1;
+  return ldexpf(sqrtf((float)scalbn(s, -e)), e / 2);
+}
+// UNIT / (norm + eps): what u is multiplied by.
+__device__ __forceinline__ float scale_of(float norm, double eps) { return UNIT / (norm + (float)eps); }
+
+// |u|_F, in every thread of the block; `sm` is one float.
+__device__ __forceinline__ float norm_of(const double* partial, int i, int parts, float* sm) {
   if (threadIdx.x < 32) {
     double s = 0;
     for (int k = threadIdx.x; k < parts; k += 32) s += partial[i * PARTS + k];
 #pragma unroll
     for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (threadIdx.x == 0) *sm = sqrt(s);
+    if (threadIdx.x == 0) *sm = root_of(s);
   }
   __syncthreads();
   return *sm;
@@ -231,7 +241,7 @@ __device__ __forceinline__ int chunk_at(int r, int k) { return r * 128 + k * 16;
 // u scaled into X's limbs, and the new momentum; a block of X a thread block.
 __global__ void __launch_bounds__(THREADS) begin_kernel(const __grid_constant__ Table tab, const Hyper h, float* norms) {
   __shared__ float tile[128][65];
-  __shared__ double sm;
+  __shared__ float sm;
   cudaTriggerProgrammaticLaunchCompletion();
   cudaGridDependencySynchronize();
   const int i = mat_of(tab, blockIdx.x);
@@ -252,10 +262,10 @@ __global__ void __launch_bounds__(THREADS) begin_kernel(const __grid_constant__ 
   };
 #pragma unroll
   for (int k = 0; k < AHEAD; ++k) load(k, q[k]);
-  const double norm = norm_of(tab.partial, i, t.parts, &sm);
-  const bool good = isfinite((float)norm);
-  const float inv = (float)((double)UNIT / (norm + h.eps));
-  if (block == 0 && threadIdx.x == 0 && norms) norms[t.slot] = (float)norm;
+  const float norm = norm_of(tab.partial, i, t.parts, &sm);
+  const bool good = isfinite(norm);
+  const float inv = scale_of(norm, h.eps);
+  if (block == 0 && threadIdx.x == 0 && norms) norms[t.slot] = norm;
 #pragma unroll
   for (int k0 = 0; k0 < QUADS; k0 += AHEAD) {
 #pragma unroll
@@ -291,14 +301,13 @@ __global__ void __launch_bounds__(THREADS) begin_kernel(const __grid_constant__ 
 // Parameters (or the output) from the orthogonalised X.
 __global__ void __launch_bounds__(THREADS) apply_kernel(const __grid_constant__ Table tab, const Hyper h, int which) {
   __shared__ float tile[128][65];
-  __shared__ double sm;
+  __shared__ float sm;
   cudaTriggerProgrammaticLaunchCompletion();
   cudaGridDependencySynchronize();
   const int i = mat_of(tab, blockIdx.x);
   const Mat& t = tab.mat[i];
   const int block = blockIdx.x - tab.first[i], r0 = block / t.nb * 128, c0 = block % t.nb * 64;
-  const double norm = norm_of(tab.partial, i, t.parts, &sm);
-  const bool good = isfinite((float)norm);
+  const bool good = isfinite(norm_of(tab.partial, i, t.parts, &sm));
   if (!good && !h.orth) return;  // this matrix stays as it is
   const char* x = t.x[which] + (int64_t)block * BLOCK;
   for (int e = threadIdx.x; e < 128 * 8; e += THREADS) {
@@ -926,13 +935,13 @@ __global__ void __launch_bounds__(SMALL_THREADS, 1)
   if (threadIdx.x == 0) {
     double s = 0;
     for (int w = 0; w < SMALL_THREADS / 32; ++w) s += part[w];
-    shared_norm = (float)sqrt(s);
+    shared_norm = root_of(s);
     if (norms) norms[t.slot] = shared_norm;
   }
   __syncthreads();
   const float norm = shared_norm;
   const bool good = isfinite(norm);
-  const float inv = (float)((double)UNIT / ((double)norm + h.eps));
+  const float inv = scale_of(norm, h.eps);
   for (int e = threadIdx.x; e < quads; e += SMALL_THREADS) {
     const int row = e / across, col = e % across * 4;
     Quad q;
@@ -1113,8 +1122,9 @@ done:
 int64_t up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 
 // A launch may start while the kernel before it ends; each waits for that before
-// it touches memory.
-template <class... P, class... A>
+// it touches memory.  TOGETHER: its blocks wait on one another, so all are there or none
+// starts.
+template <bool TOGETHER = false, class... P, class... A>
 gnn_status launch(int64_t grid, int block, size_t smem, cudaStream_t st, void (*k)(P...), const A&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
@@ -1122,8 +1132,7 @@ gnn_status launch(int64_t grid, int block, size_t smem, cudaStream_t st, void (*
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute at[1];
-  if (smem == PRODUCT_SMEM) {
-    // its blocks wait on one another: all are there, or none starts
+  if (TOGETHER) {
     at[0].id = cudaLaunchAttributeCooperative;
     at[0].val.cooperative = 1;
   } else {
@@ -1262,11 +1271,11 @@ gnn_status each_pass(const std::vector<int>& order, void* ws, size_t cap, size_t
 gnn_status launch_steps(const Steps& g, int bn, cudaStream_t st) {
   const int64_t tiles = (int64_t)g.steps * (g.first[0][g.count] + g.first[1][g.count] + g.first[2][g.count]);
   const int widest = std::max(std::max(g.first[0][g.count], g.first[1][g.count]), g.first[2][g.count]);
-  if (tiles > 0x3fffffff) return fail(GNN_ERR_UNSUPPORTED, "too many tiles in one call");
+  if (tiles > 0x3fffffff) return fail(GNN_ERR_UNSUPPORTED, "Newton-Schulz: too many tiles in one call");
   const int units = std::min(widest, bn ? sms_there() : sms_there() / 2);
   auto run = [&](auto* k, PerDevice& done, int grid) -> gnn_status {
     GNN_TRY(allow_smem(k, PRODUCT_SMEM, done));
-    return launch(grid, PRODUCT_THREADS, PRODUCT_SMEM, st, k, g);
+    return launch<true>(grid, PRODUCT_THREADS, PRODUCT_SMEM, st, k, g);
   };
   static PerDevice done0, done64, done128;
   if (bn == 0) return run(steps_pair_kernel, done0, 2 * units);
@@ -1284,7 +1293,7 @@ gnn_status maps_of(Steps& g, const void* ws, uint64_t blocks) {
 }
 
 gnn_status run_pass(void* ws, Table& tab, const Hyper& h, const float* coeffs, int steps, float* norms, cudaStream_t st) {
-  if (tab.blocks > 0x7fffff00 / BLOCK_ROWS) return fail(GNN_ERR_UNSUPPORTED, "matrices too large together");
+  if (tab.blocks > 0x7fffff00 / BLOCK_ROWS) return fail(GNN_ERR_UNSUPPORTED, "Newton-Schulz: matrices too large together");
   auto blocks = [&](auto&& of) {
     tab.first[0] = 0;
     for (int i = 0; i < tab.count; ++i) tab.first[i + 1] = tab.first[i] + of(tab.mat[i]);
@@ -1326,7 +1335,7 @@ gnn_status run_pass(void* ws, Table& tab, const Hyper& h, const float* coeffs, i
     for (Phase ph : {GRAM, POLY, NEXT}) {
       int64_t sum = 0;
       for (int i = 0; i <= tab.count; ++i) {
-        if (sum > 0x3fffffff) return fail(GNN_ERR_UNSUPPORTED, "too many tiles in one call");
+        if (sum > 0x3fffffff) return fail(GNN_ERR_UNSUPPORTED, "Newton-Schulz: too many tiles in one call");
         g.first[ph][i] = (int)sum;
         if (i < tab.count) sum += tiles_in(tab.mat[i], ph, tab.bn, tab.half[ph]);
       }
@@ -1350,7 +1359,7 @@ gnn_status check_steps(const char* who, const float* coeffs, int steps, double e
   if (steps && !coeffs) return fail(GNN_ERR_INVALID_ARG, "%s: NULL coeffs", who);
   for (int i = 0; i < 3 * steps; ++i)
     if (!(std::fabs(coeffs[i]) <= 32.f)) return fail(GNN_ERR_INVALID_ARG, "%s: coeffs lie in [-32, 32]", who);
-  if (!(eps > 0) || !std::isfinite(eps)) return fail(GNN_ERR_INVALID_ARG, "%s: eps must be positive", who);
+  if (!(eps >= 1e-30) || !(eps <= 1e30)) return fail(GNN_ERR_INVALID_ARG, "%s: eps lies in [1e-30, 1e30]", who);
   return GNN_OK;
 }
 bool aligned_to(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }

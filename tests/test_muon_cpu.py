@@ -55,7 +55,7 @@ def orth(lib, X=MB, ldx=64, sx=0, xt=F32, count=1, rows=32, cols=64, coeffs=(3.0
     (dict(count=-1), INVALID), (dict(rows=-1), INVALID), (dict(cols=-2), INVALID), (dict(rows=65537, ldx=64), UNSUPPORTED),
     (dict(rows=20000, cols=20000, ldx=20000, ldo=20000), UNSUPPORTED), (dict(xt=3), INVALID), (dict(ot=-1), INVALID), (dict(steps=-1), INVALID),
     (dict(steps=17, coeffs=(1.0,) * 51), INVALID), (dict(coeffs=None), INVALID), (dict(coeffs=(NAN,) * 15), INVALID), (dict(coeffs=(33.0,) * 15), INVALID),
-    (dict(coeffs=(INF,) * 15), INVALID), (dict(eps=0.0), INVALID), (dict(eps=-1.0), INVALID), (dict(eps=NAN), INVALID), (dict(eps=INF), INVALID),
+    (dict(coeffs=(INF,) * 15), INVALID), (dict(eps=0.0), INVALID), (dict(eps=-1.0), INVALID), (dict(eps=NAN), INVALID), (dict(eps=INF), INVALID), (dict(eps=1e-40), INVALID),
     (dict(norms=2), INVALID), (dict(X=None), INVALID), (dict(O=None), INVALID), (dict(X=MB + 2), INVALID), (dict(O=2 * MB + 1, ot=BF16), INVALID),
     (dict(ldx=63), INVALID), (dict(ldo=32), INVALID), (dict(count=2, sx=100, so=4096), INVALID), (dict(count=2, sx=4096, so=0), INVALID),
     (dict(ws=None), INVALID), (dict(ws=16 * MB + 128), INVALID), (dict(ws_bytes=100), INVALID), (dict(rows=65, cols=70, ldx=70, ldo=70, ws_bytes=1000), INVALID), (dict(O=MB + 256), INVALID),
