@@ -765,6 +765,37 @@ gnn_status gnn_residual_norm_bwd(const void* dH, int64_t lddh, const void* dY, i
                                  float* dw_post, float* db_post, float* dscale, float* dw_pre,
                                  float* db_pre, void* ws, size_t ws_bytes, gnn_stream_t stream);
 
+/* The same calls with their arguments in a struct, for callers to whom forty single
+ * ones cost more than the kernel of a few rows (every field has eight bytes). */
+typedef struct gnn_residual_norm_fwd_args {
+  const void* B; int64_t ldb, b_type;
+  const void* R; int64_t ldr, r_type;
+  const void* gate; int64_t ldg, gate_cols, gate_act;
+  int64_t n, C, post;
+  const float *w_post, *b_post, *scale; int64_t scale_cols, pre;
+  const float *w_pre, *b_pre; double eps;
+  void* H; int64_t ldh;
+  void* Y; int64_t ldy, y_type;
+  float* stats; gnn_stream_t stream;
+} gnn_residual_norm_fwd_args;
+typedef struct gnn_residual_norm_bwd_args {
+  const void* dH; int64_t lddh;
+  const void* dY; int64_t lddy, y_type;
+  const void* B; int64_t ldb, b_type;
+  const void* H; int64_t ldh, r_type;
+  const void* gate; int64_t ldg, gate_cols, gate_act;
+  int64_t n, C, post;
+  const float *w_post, *b_post, *scale; int64_t scale_cols, pre;
+  const float *w_pre, *stats;
+  void* dR; int64_t lddr;
+  void* dB; int64_t lddb;
+  void* dgate; int64_t lddg;
+  float *dw_post, *db_post, *dscale, *dw_pre, *db_pre;
+  void* ws; int64_t ws_bytes; gnn_stream_t stream;
+} gnn_residual_norm_bwd_args;
+gnn_status gnn_residual_norm_fwd_struct(const gnn_residual_norm_fwd_args* args);
+gnn_status gnn_residual_norm_bwd_struct(const gnn_residual_norm_bwd_args* args);
+
 /* One AdamW step over many tensors.  The descriptors are a host array (they
  * go to the kernels as launch parameters, so they may change from call to
  * call and a call can be captured into a graph); what they point at is device

@@ -927,6 +927,8 @@ def gnn_gated_bwd(dH, X, n: int, F_in: int, Wg, Wu, F_mid: int, dX=None, dWg=Non
 
 
 NORMS = {"none": 0, "rms": 1, "layer": 2}
+# the calls' arguments as a struct's bytes, in which None is a zero
+_RESIDUAL_FWD, _RESIDUAL_BWD = _abi.RESIDUAL_FWD.pack, _abi.RESIDUAL_BWD.pack
 
 
 def _norm(kind: str, what: str) -> int:
@@ -939,17 +941,17 @@ def _norm(kind: str, what: str) -> int:
 def _gate(gate, n: int, C: int, what: str):
     """(pointer, stride, columns) of a gate: a matrix, or one value a row."""
     if gate is None:
-        return None, 0, 0
+        return 0, 0, 0
     if gate.dim() == 1:
         if gate.numel() < n or not gate.is_cuda:
             raise ValueError(f"{what}: needs a CUDA tensor of {n} values or a matrix")
-        return gate.data_ptr(), gate.stride(0), 1
+        return gate.data_ptr(), gate.stride()[0], 1
     return gate.data_ptr(), _rows(gate, n, C, what), C
 
 
 def _scale(scale, C: int):
     if scale is None:
-        return None, 0
+        return 0, 0
     k = scale.numel()
     if k != 1 and k != C:
         raise ValueError(f"scale: needs 1 or {C} values, got {k}")
@@ -963,7 +965,7 @@ def _types(what, t, *others):
 
 
 def _place(t, n: int, C: int, what: str):
-    return (None, 0) if t is None else (t.data_ptr(), _rows(t, n, C, what))
+    return (0, 0) if t is None else (t.data_ptr(), _rows(t, n, C, what))
 
 
 @functools.lru_cache(maxsize=1024)
@@ -981,18 +983,29 @@ def gnn_residual_norm_fwd(B, R, n: int, C: int, H, Y=None, stats=None, gate=None
     b_pre by rows (norms "none", "rms", "layer").  gate: [n, C] or one value a
     row [n], of B's type; scale: fp32, C values or one; stats (fp32 [n, 4]) is
     kept for the backward.  B None: H = R (H may be None), Y is R's norm."""
-    _types("B", R if B is None else B, ("gate", gate))
-    _types("R", R, ("H", H))
+    b = _bits or _torch_bits()
+    rt = R.dtype
+    if H is not None and H.dtype is not rt:
+        raise ValueError(f"H: needs R's type {rt}, got {H.dtype}")
+    if gate is not None:
+        _types("B", R if B is None else B, ("gate", gate))
     at_b, ldb = _place(B, n, C, "B")
     at_g, ldg, gate_cols = _gate(gate, n, C, "gate")
     at_s, scale_cols = _scale(scale, C)
     at_h, ldh = _place(H, n, C, "H")
     at_y, ldy = _place(Y, n, C, "Y")
-    bt = _type(B) if B is not None else _type(R) if Y is None or R.dtype is Y.dtype else 0
-    call("gnn_residual_norm_fwd", at_b, ldb, bt, R.data_ptr(), _rows(R, n, C, "R"), _type(R), at_g, ldg, gate_cols,
-         _act(gate_act), n, C, _norm(post, "post") if B is not None else 0, _f32(w_post, C, "w_post"),
-         _f32(b_post, C, "b_post"), at_s, scale_cols, _norm(pre, "pre"), _f32(w_pre, C, "w_pre"), _f32(b_pre, C, "b_pre"),
-         eps, at_h, ldh, at_y, ldy, bt if Y is None else _type(Y), _f32(stats, 4 * n, "stats"), _current(R, stream))
+    types = b.types
+    rt = types.get(rt, -1)
+    yt = rt if Y is None else types.get(Y.dtype, -1)
+    bt = types.get(B.dtype, -1) if B is not None else rt if rt == yt else 0
+    if Y is None:
+        yt = bt
+    call("gnn_residual_norm_fwd_struct", _RESIDUAL_FWD(
+        at_b, ldb, bt, R.data_ptr(), _rows(R, n, C, "R"), rt, at_g, ldg, gate_cols, _act(gate_act), n, C,
+        _norm(post, "post") if B is not None else 0, w_post is not None and _f32(w_post, C, "w_post"),
+        b_post is not None and _f32(b_post, C, "b_post"), at_s, scale_cols, _norm(pre, "pre"),
+        w_pre is not None and _f32(w_pre, C, "w_pre"), b_pre is not None and _f32(b_pre, C, "b_pre"), eps, at_h, ldh, at_y, ldy,
+        yt, stats is not None and _f32(stats, 4 * n, "stats"), _current(R, stream)))
 
 
 def gnn_residual_norm_bwd(dH, dY, B, H, n: int, C: int, stats, dR=None, dB=None, gate=None, dgate=None,
@@ -1017,12 +1030,13 @@ def gnn_residual_norm_bwd(dH, dY, B, H, n: int, C: int, stats, dR=None, dB=None,
     at_s, scale_cols = _scale(scale, C)
     bt = _type(B) if B is not None else _type(S) if dY is None or S.dtype is dY.dtype else 0
     at, size, ws = _ws(ws, gnn_residual_norm_workspace(n, C), S, stream)
-    call("gnn_residual_norm_bwd", at_dh, lddh, at_dy, lddy, bt if dY is None else _type(dY), at_b, ldb, bt, at_h, ldh,
-         _type(S), at_g, ldg, gate_cols, _act(gate_act), n, C, _norm(post, "post") if B is not None else 0,
-         _f32(w_post, C, "w_post"), _f32(b_post, C, "b_post"), at_s, scale_cols, _norm(pre, "pre"),
-         _f32(w_pre, C, "w_pre"), _f32(stats, 4 * n, "stats"), at_dr, lddr, at_db, lddb, at_dg, lddg,
-         _f32(dw_post, C, "dw_post"), _f32(db_post, C, "db_post"), _f32(dscale, scale_cols, "dscale"),
-         _f32(dw_pre, C, "dw_pre"), _f32(db_pre, C, "db_pre"), at, size, _current(S, stream))
+    vec = lambda t, k, what: t is not None and _f32(t, k, what)  # noqa: E731
+    call("gnn_residual_norm_bwd_struct", _RESIDUAL_BWD(
+        at_dh, lddh, at_dy, lddy, bt if dY is None else _type(dY), at_b, ldb, bt, at_h, ldh, _type(S), at_g, ldg, gate_cols,
+        _act(gate_act), n, C, _norm(post, "post") if B is not None else 0, vec(w_post, C, "w_post"), vec(b_post, C, "b_post"),
+        at_s, scale_cols, _norm(pre, "pre"), vec(w_pre, C, "w_pre"), vec(stats, 4 * n, "stats"), at_dr, lddr, at_db, lddb,
+        at_dg, lddg, vec(dw_post, C, "dw_post"), vec(db_post, C, "db_post"), vec(dscale, scale_cols, "dscale"),
+        vec(dw_pre, C, "dw_pre"), vec(db_pre, C, "db_pre"), at, size, _current(S, stream)))
 
 
 class AdamwTensors:

@@ -4,6 +4,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 from . import builder as _build
 
@@ -55,6 +56,12 @@ class GnnLdrState(ctypes.Structure):
     _fields_ = [("lambda_", ctypes.c_double), ("delta", c_i32), ("b_min", c_i32), ("b_max", c_i32),
                 ("t", c_i32), ("base_bits", c_i32), ("async_next", c_i32), ("F", ctypes.c_double),
                 ("ldr", ctypes.c_double * (GNN_LDR_MAX_DELTA + 1))]
+
+
+# gnn_residual_norm_fwd_args and gnn_residual_norm_bwd_args: eight bytes a field, the
+# forward's twenty-first the double eps
+RESIDUAL_FWD = struct.Struct("20qd7q")
+RESIDUAL_BWD = struct.Struct("39q")
 
 
 class GnnMuonTensor(ctypes.Structure):
@@ -179,6 +186,8 @@ PROTOTYPES = {
                                              c_i32, c_vp, c_i64, c_i32, c_i32, c_i64, c_i32, c_i32, c_vp, c_vp,
                                              c_vp, c_i32, c_i32, c_vp, c_vp, c_vp, c_i64, c_vp, c_i64, c_vp,
                                              c_i64, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_size, c_vp]),
+    "gnn_residual_norm_fwd_struct": (ctypes.c_int, [c_char_p]),
+    "gnn_residual_norm_bwd_struct": (ctypes.c_int, [c_char_p]),
     "gnn_adamw_workspace": (ctypes.c_int, [P_size]),
     "gnn_adamw_step": (ctypes.c_int, [ctypes.POINTER(GnnAdamwTensor), c_i32, c_i32, c_i32, c_i32, c_vp,
                                       ctypes.c_double, ctypes.c_double, ctypes.c_double, ctypes.c_double,

@@ -17,6 +17,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <initializer_list>
 
 #include "internal.h"
 #include "nodewise.cuh"
@@ -1026,4 +1027,32 @@ extern "C" gnn_status gnn_residual_norm_bwd(const void* dH, int64_t lddh, const 
   const Join j{w.part, w.part_s, n > 0 ? (int)blocks_for(n, sh, true) : 0, sh.lanes * sh.vecs * 8, C, scale_cols, w_post, b_post,
                scale, dw_post, db_post, dscale, dw_pre, db_pre, want_q, want_p};
   return launch(blocks + want_s, 32 * JOIN_ROWS, 0, as_stream(stream), residual_join_kernel, j);
+}
+
+// A struct's numbers that the calls take in 32 bits.
+static bool narrow(std::initializer_list<int64_t> v) {
+  for (int64_t x : v)
+    if (x != (int32_t)x) return false;
+  return true;
+}
+
+extern "C" gnn_status gnn_residual_norm_fwd_struct(const gnn_residual_norm_fwd_args* a) {
+  GNN_REQUIRE(a, "gnn_residual_norm_fwd: NULL arguments");
+  GNN_REQUIRE(narrow({a->b_type, a->r_type, a->gate_cols, a->gate_act, a->C, a->post, a->scale_cols, a->pre, a->y_type}),
+              "gnn_residual_norm_fwd: a number of more than 32 bits");
+  return gnn_residual_norm_fwd(a->B, a->ldb, (int32_t)a->b_type, a->R, a->ldr, (int32_t)a->r_type, a->gate, a->ldg,
+                               (int32_t)a->gate_cols, (int32_t)a->gate_act, a->n, (int32_t)a->C, (int32_t)a->post, a->w_post,
+                               a->b_post, a->scale, (int32_t)a->scale_cols, (int32_t)a->pre, a->w_pre, a->b_pre, a->eps, a->H,
+                               a->ldh, a->Y, a->ldy, (int32_t)a->y_type, a->stats, a->stream);
+}
+
+extern "C" gnn_status gnn_residual_norm_bwd_struct(const gnn_residual_norm_bwd_args* a) {
+  GNN_REQUIRE(a, "gnn_residual_norm_bwd: NULL arguments");
+  GNN_REQUIRE(narrow({a->y_type, a->b_type, a->r_type, a->gate_cols, a->gate_act, a->C, a->post, a->scale_cols, a->pre}) &&
+                  a->ws_bytes >= 0, "gnn_residual_norm_bwd: a number of more than 32 bits");
+  return gnn_residual_norm_bwd(a->dH, a->lddh, a->dY, a->lddy, (int32_t)a->y_type, a->B, a->ldb, (int32_t)a->b_type, a->H,
+                               a->ldh, (int32_t)a->r_type, a->gate, a->ldg, (int32_t)a->gate_cols, (int32_t)a->gate_act, a->n,
+                               (int32_t)a->C, (int32_t)a->post, a->w_post, a->b_post, a->scale, (int32_t)a->scale_cols,
+                               (int32_t)a->pre, a->w_pre, a->stats, a->dR, a->lddr, a->dB, a->lddb, a->dgate, a->lddg,
+                               a->dw_post, a->db_post, a->dscale, a->dw_pre, a->db_pre, a->ws, (size_t)a->ws_bytes, a->stream);
 }

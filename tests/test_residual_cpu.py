@@ -150,3 +150,26 @@ def test_binding_refuses_before_the_library():
         G._norm("batch", "post")
     with pytest.raises(ValueError, match="scale"):
         G._scale(torch.zeros(3), 16)
+
+
+def test_structs_are_the_same_calls(lib):
+    """Numbers reach the same checks; sizes as the header's structs have them."""
+    assert _abi.RESIDUAL_FWD.size == 28 * 8 and _abi.RESIDUAL_BWD.size == 39 * 8
+    assert lib.gnn_residual_norm_fwd_struct(None) == INVALID and lib.gnn_residual_norm_bwd_struct(None) == INVALID
+    good = [MB, 64, BF16, 2 * MB, 64, F32, 0, 0, 0, 0, 10, 64, 1, 0, 0, 0, 0, 1, 0, 0, 1e-6, 3 * MB, 64, 4 * MB, 64, BF16, 5 * MB, 0]
+    for at, value, text in ((0, MB + 8, b"B needs"), (3, 0, b"R needs"), (10, -1, b"row count"), (11, 0, b"C must"), (12, 3, b"post"),
+                            (13, 7 * MB + 1, b"misaligned"), (20, 0.0, b"eps"), (22, 60, b"H needs"), (23, 0, b"Y comes"),
+                            (25, 1 << 33, b"32 bits"), (26, 5 * MB + 8, b"stats")):
+        args = list(good)
+        args[at] = value
+        assert lib.gnn_residual_norm_fwd_struct(_abi.RESIDUAL_FWD.pack(*args)) == INVALID, at
+        assert text in lib.gnn_last_error(), (at, lib.gnn_last_error())
+    good = [MB, 64, 2 * MB, 64, BF16, 3 * MB, 64, BF16, 4 * MB, 64, F32, 0, 0, 0, 0, 10, 64, 1, 0, 0, 0, 0, 1, 0, 5 * MB, 6 * MB, 64,
+            7 * MB, 64, 0, 0, 9 * MB, 0, 0, 10 * MB, 0, 16 * MB, 1 << 30, 0]
+    for at, value, text in ((0, MB + 4, b"dH needs"), (6, 56, b"B needs"), (8, 0, b"H needs"), (16, 1 << 32, b"32 bits"), (24, 0, b"stats"),
+                            (25, 2 * MB, b"overlaps"), (29, 8 * MB, b"dgate"), (31, 9 * MB + 2, b"misaligned"), (37, 64, b"workspace"),
+                            (37, -1, b"32 bits")):
+        args = list(good)
+        args[at] = value
+        assert lib.gnn_residual_norm_bwd_struct(_abi.RESIDUAL_BWD.pack(*args)) == INVALID, at
+        assert text in lib.gnn_last_error(), (at, lib.gnn_last_error())
