@@ -647,7 +647,8 @@ __global__ void __launch_bounds__(MULTI ? MAX_LANES : K == 1 ? THREADS : FEW, MU
 
 // The blocks' sums, in order, and the weights' gradients from them.  In fp32: an
 // SM adds two fp64 numbers a clock, and with those this kernel took 27 us of 39.  A
-// block takes 32 channels; with one learned scale a block more adds its gradient.
+// block takes 32 channels of the pre norm's two sums or of the post norm's; with one
+// learned scale a block more adds its gradient.
 constexpr int JOIN_ROWS = 32;
 struct Join {
   const float* part;
@@ -658,11 +659,12 @@ struct Join {
   int want_q, want_p;
 };
 __global__ void __launch_bounds__(32 * JOIN_ROWS) residual_join_kernel(const Join g) {
-  __shared__ float sm[4][JOIN_ROWS][33];
+  __shared__ float sm[2][JOIN_ROWS][33];
   cudaTriggerProgrammaticLaunchCompletion();
   cudaGridDependencySynchronize();
-  const int lane = threadIdx.x & 31, r = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
-  if (blockIdx.x * 32 >= g.C) {
+  const int lane = threadIdx.x & 31, r = threadIdx.x >> 5;
+  const int pieces = (g.C + 31) / 32, of = (int)blockIdx.x / pieces, c = ((int)blockIdx.x - of * pieces) * 32 + lane;
+  if (of == 2) {
     if (r) return;
     double s = 0;
     for (int b = lane; b < g.blocks; b += 32) s += g.part_s[b];
@@ -671,36 +673,39 @@ __global__ void __launch_bounds__(32 * JOIN_ROWS) residual_join_kernel(const Joi
     if (lane == 0) g.dscale[0] = (float)s;
     return;
   }
-  float s[4] = {0.f, 0.f, 0.f, 0.f};
+  if (!(of ? g.want_p : g.want_q)) return;
+  float s[2] = {0.f, 0.f};
   if (c < g.C) {
-#pragma unroll 5
+    const float* p = g.part + 2 * of * g.width + c;
+#pragma unroll 10
     for (int b = r; b < g.blocks; b += JOIN_ROWS) {
-      const float* p = g.part + (int64_t)b * 4 * g.width + c;
-      if (g.want_q) s[0] += p[0], s[1] += p[g.width];
-      if (g.want_p) s[2] += p[2 * g.width], s[3] += p[3 * g.width];
+      const int64_t at = (int64_t)b * 4 * g.width;
+      s[0] += p[at], s[1] += p[at + g.width];
     }
   }
-#pragma unroll
-  for (int a = 0; a < 4; ++a) sm[a][r][lane] = s[a];
+  sm[0][r][lane] = s[0], sm[1][r][lane] = s[1];
   __syncthreads();
   // a warp for each channel: its lanes are the rows
 #pragma unroll
-  for (int a = 0; a < 4; ++a) {
+  for (int a = 0; a < 2; ++a) {
     s[a] = sm[a][lane][r];
 #pragma unroll
     for (int o = 16; o; o >>= 1) s[a] += __shfl_xor_sync(0xffffffffu, s[a], o);
   }
   __syncthreads();
-  if (lane < 4) sm[lane][0][r] = lane == 0 ? s[0] : lane == 1 ? s[1] : lane == 2 ? s[2] : s[3];
+  if (lane < 2) sm[lane][0][r] = lane ? s[1] : s[0];
   __syncthreads();
   if (r || c >= g.C) return;
-  const float P1 = sm[2][0][lane], P2 = sm[3][0][lane];
+  const float s1 = sm[0][0][lane], s2 = sm[1][0][lane];
+  if (of == 0) {
+    if (g.dw_pre) g.dw_pre[c] = s1;
+    if (g.db_pre) g.db_pre[c] = s2;
+    return;
+  }
   const float sc = g.scale_cols == 0 ? 1.f : g.scale_cols == 1 ? g.scale[0] : g.scale[c];
-  if (g.dw_pre) g.dw_pre[c] = sm[0][0][lane];
-  if (g.db_pre) g.db_pre[c] = sm[1][0][lane];
-  if (g.dw_post) g.dw_post[c] = sc * P1;
-  if (g.db_post) g.db_post[c] = sc * P2;
-  if (g.dscale && g.scale_cols > 1) g.dscale[c] = fmaf(g.w_post ? g.w_post[c] : 1.f, P1, (g.b_post ? g.b_post[c] : 0.f) * P2);
+  if (g.dw_post) g.dw_post[c] = sc * s1;
+  if (g.db_post) g.db_post[c] = sc * s2;
+  if (g.dscale && g.scale_cols > 1) g.dscale[c] = fmaf(g.w_post ? g.w_post[c] : 1.f, s1, (g.b_post ? g.b_post[c] : 0.f) * s2);
 }
 
 // ---------------------------------------------------------------- host side
@@ -1026,7 +1031,7 @@ extern "C" gnn_status gnn_residual_norm_bwd(const void* dH, int64_t lddh, const 
   const int blocks = (C + 31) / 32;
   const Join j{w.part, w.part_s, n > 0 ? (int)blocks_for(n, sh, true) : 0, sh.lanes * sh.vecs * 8, C, scale_cols, w_post, b_post,
                scale, dw_post, db_post, dscale, dw_pre, db_pre, want_q, want_p};
-  return launch(blocks + want_s, 32 * JOIN_ROWS, 0, as_stream(stream), residual_join_kernel, j);
+  return launch(2 * blocks + want_s, 32 * JOIN_ROWS, 0, as_stream(stream), residual_join_kernel, j);
 }
 
 // A struct's numbers that the calls take in 32 bits.
