@@ -877,7 +877,6 @@ __global__ void __launch_bounds__(SMALL_THREADS, 1)
   extern __shared__ uint8_t smem_raw[];
   __shared__ double part[SMALL_THREADS / 32];
   __shared__ float shared_norm;
-  cudaTriggerProgrammaticLaunchCompletion();
   const Mat& t = tab.mat[blockIdx.x];
   uint8_t* const x = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int kbs = (t.n + 63) >> 6, kx = (t.n + 15) >> 4, km = (t.m + 15) >> 4;
@@ -893,14 +892,19 @@ __global__ void __launch_bounds__(SMALL_THREADS, 1)
     *abort_flag = 0;
     tc::fence_barrier_init();
   }
+  for (int e = threadIdx.x; e < kbs * HALF_BLOCK / 16; e += SMALL_THREADS)
+    reinterpret_cast<uint4*>(x)[e] = make_uint4(0, 0, 0, 0);
+  cudaGridDependencySynchronize();
+  // Columns of TMEM are asked for when the kernel before has given its own back, and the
+  // kernel behind starts when they are there: on a shared SM neither can hold columns
+  // that the other, which it waits for, has yet to get.
   if (warp == 0) {
     tc::tmem_alloc(tmem_at, tmem_cols);
     tc::tmem_relinquish();
   }
-  for (int e = threadIdx.x; e < kbs * HALF_BLOCK / 16; e += SMALL_THREADS)
-    reinterpret_cast<uint4*>(x)[e] = make_uint4(0, 0, 0, 0);
+  __syncwarp();
+  cudaTriggerProgrammaticLaunchCompletion();
   tc::fence_before_sync();
-  cudaGridDependencySynchronize();
   // |u|
   const int across = (t.cols + 3) >> 2, quads = t.rows * across;
   double sum = 0;

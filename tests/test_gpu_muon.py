@@ -199,3 +199,22 @@ def test_streams_and_graphs(shapes):
     torch.cuda.synchronize()
     for a, b in zip(p + m, p2 + m2):
         assert torch.equal(a, b)
+
+
+def test_small_batches_behind_one_another():
+    """Calls that hold different numbers of tensor-memory columns, in a row on one
+    stream, give what each gives alone."""
+    sizes = [(64, 320), (64, 64), (16, 100), (30, 512), (64, 256), (20, 300)]
+    X = [torch.stack([matrix(r, c, 100 * k + i) for i in range(64)]).cuda() for k, (r, c) in enumerate(sizes)]
+    alone = []
+    for x in X:
+        alone.append(torch.empty_like(x))
+        G.gnn_orthogonalise(x, alone[-1])
+        torch.cuda.synchronize()
+    ws = torch.empty(256, dtype=torch.uint8, device="cuda")
+    together = [torch.empty_like(x) for _ in range(4) for x in X]
+    for i, O in enumerate(together):  # noqa: E741
+        G.gnn_orthogonalise(X[i % len(X)], O, ws=ws)
+    torch.cuda.synchronize()
+    for i, O in enumerate(together):  # noqa: E741
+        assert torch.equal(O, alone[i % len(X)])
