@@ -1015,6 +1015,8 @@ def gnn_residual_norm_bwd(dH, dY, B, H, n: int, C: int, stats, dR=None, dB=None,
     """Gradients of gnn_residual_norm_fwd from dH and dY (one may be None), with
     B, H, gate, weights and stats as they were there; each output may be None."""
     S = H if H is not None else dH
+    if S is None:
+        raise ValueError("H: needed where there is no dH")
     _types("B", S if B is None else B, ("gate", gate), ("dgate", dgate), ("dB", dB))
     _types("H", S, ("dH", dH), ("dR", dR))
     at_dh, lddh = _place(dH, n, C, "dH")
@@ -1120,9 +1122,15 @@ def gnn_adamw_step(tensors: AdamwTensors, state, lr: float, beta1: float = 0.9, 
 NS_COEFFS = (3.4445, -4.7750, 2.0315)
 
 
-@functools.lru_cache(maxsize=64)
 def _coeffs(coeffs, steps: int):
     """One triple for every step, or a triple each, as a C array."""
+    if not isinstance(coeffs, tuple) or any(isinstance(c, list) for c in coeffs):
+        coeffs = tuple(tuple(c) if hasattr(c, "__len__") else c for c in coeffs)
+    return _coeff_array(coeffs, steps)
+
+
+@functools.lru_cache(maxsize=64)
+def _coeff_array(coeffs, steps: int):
     each = coeffs if coeffs and hasattr(coeffs[0], "__len__") else (coeffs,) * steps
     flat = [float(c) for triple in each for c in triple]
     if len(each) != steps or any(len(triple) != 3 for triple in each):
@@ -1193,9 +1201,10 @@ class MuonTensors:
                         (t.shape[1] > 1 and t.stride(1) != 1):
                     raise ValueError(f"{name}[{i}]: needs a {want[name]} CUDA matrix of {tuple(params[i].shape)} with "
                                      "contiguous rows")
-        places = [p.data_ptr() for p in params if p.numel()]
-        if len(set(places)) < len(places):
-            raise ValueError("params: a matrix is listed twice")
+        for name in ("params", "momenta", "copies"):
+            places = [t.data_ptr() for t in lists[name] or () if t is not None and t.numel()]
+            if len(set(places)) < len(places):
+                raise ValueError(f"{name}: a matrix is listed twice")
         self.param_type, self.grad_type, self.m_type = (_type(t[0]) if k else 0 for t in (params, grads, momenta))
         self.device = params[0].device if k else None
         self._keep = {name: list(ts) for name, ts in lists.items() if ts is not None}

@@ -1383,6 +1383,7 @@ gnn_status guarded(const char* who, Fn f) {
 // Whether four elements from a column that is a multiple of four are one access.
 bool quad_rows(const void* p, int64_t ld, int elem) { return aligned_to(p, 4 * elem) && ld % 4 == 0; }
 
+Span flat(const void* p, int64_t bytes) { return {p, 1, bytes, bytes}; }
 Span span(const void* p, const gnn_muon_tensor& t, int64_t ld, int elem) { return {p, t.rows, ld * elem, (int64_t)t.cols * elem}; }
 
 }  // namespace
@@ -1418,8 +1419,8 @@ extern "C" gnn_status gnn_muon_step(const gnn_muon_tensor* tensors, int32_t n_te
   if ((param_type != GNN_F32 && param_type != GNN_BF16) || (m_type != GNN_F32 && m_type != GNN_BF16))
     return fail(GNN_ERR_UNSUPPORTED, "%s: parameters and momentum are fp32 or bf16", who);
   GNN_REQUIRE(momentum >= 0 && momentum < 1, "%s: momentum lies in [0, 1)", who);
-  GNN_REQUIRE(std::isfinite(lr) && std::isfinite(weight_decay) && std::isfinite(grad_scale),
-              "%s: lr, weight_decay or grad_scale is not finite", who);
+  GNN_REQUIRE(std::isfinite((float)lr) && std::isfinite((float)(1.0 - lr * weight_decay)) && std::isfinite((float)grad_scale),
+              "%s: lr, 1 - lr weight_decay or grad_scale is not finite in fp32", who);
   GNN_TRY(check_steps(who, coeffs, steps, eps));
   GNN_REQUIRE(aligned_to(norms, 4), "%s: misaligned norms", who);
   const int ps = type_size(param_type), gs = type_size(grad_type), ms = type_size(m_type);
@@ -1443,6 +1444,15 @@ extern "C" gnn_status gnn_muon_step(const gnn_muon_tensor* tensors, int32_t n_te
   if (need == 0) return GNN_OK;  // no elements
   GNN_REQUIRE(ws && ws_bytes >= need && aligned_to(ws, 256), "%s: workspace too small (%zu < %zu) or misaligned", who,
               ws_bytes, need);
+  const Span taken[2] = {flat(ws, (int64_t)need), flat(norms, 4ll * n_tensors)};
+  GNN_REQUIRE(!overlap(taken[0], taken[1]), "%s: norms overlaps the workspace", who);
+  for (int i = 0; i < n_tensors; ++i) {
+    const gnn_muon_tensor& t = tensors[i];
+    for (const Span& s : taken)
+      GNN_REQUIRE(!overlap(s, span(t.param, t, t.ldp, ps)) && !overlap(s, span(t.grad, t, t.ldg, gs)) &&
+                      !overlap(s, span(t.m, t, t.ldm, ms)) && !overlap(s, span(t.copy, t, t.ldc, 2)),
+                  "%s: matrix %d overlaps norms or the workspace", who, i);
+  }
   const Hyper h{(float)momentum, (float)grad_scale, (float)(1.0 - lr * weight_decay), (float)lr, eps, nesterov != 0, 0,
                 param_type, grad_type, m_type};
   return guarded(who, [&] {
@@ -1500,14 +1510,18 @@ extern "C" gnn_status gnn_orthogonalise(const void* X, int64_t ldx, int64_t stri
   const int64_t x_size = (rows - 1) * ldx + cols, o_size = (rows - 1) * ldo + cols;
   GNN_REQUIRE(count == 1 || (stride_x >= x_size && stride_o >= o_size && stride_x <= LD_MOST && stride_o <= LD_MOST),
               "%s: matrices of a batch overlap", who);
+  const Span x_all{X, count, stride_x * xs, x_size * xs}, o_all{O, count, stride_o * os, o_size * os};
   // in place each element is read before anything is written
   GNN_REQUIRE((X == O && ldx == ldo && xs == os && (count == 1 || stride_x == stride_o)) ||
-                  !overlap(Span{X, count, stride_x * xs, x_size * xs}, Span{O, count, stride_o * os, o_size * os}),
+                  !overlap(x_all, o_all),
               "%s: O overlaps X (it may be X)", who);
   size_t need = 0;
   gnn_orthogonalise_workspace(count, rows, cols, &need);
   GNN_REQUIRE(ws && ws_bytes >= need && aligned_to(ws, 256), "%s: workspace too small (%zu < %zu) or misaligned", who,
               ws_bytes, need);
+  const Span w_all = flat(ws, (int64_t)need), n_all = flat(norms, 4ll * count);
+  GNN_REQUIRE(!overlap(w_all, x_all) && !overlap(w_all, o_all) && !overlap(w_all, n_all) && !overlap(n_all, x_all) &&
+                  !overlap(n_all, o_all), "%s: norms or the workspace overlaps an array", who);
   const Hyper h{0.f, 1.f, 1.f, 0.f, eps, 0, 1, o_type, x_type, 0};
   return guarded(who, [&] {
     const auto order = order_of(count, [&](int) { return Shape{rows, cols}; });

@@ -147,3 +147,47 @@ def test_muon_tensors_refuse_a_matrix_listed_twice(monkeypatch):
     assert tensors([256, 512]).count == 2
     with pytest.raises(ValueError, match="twice"):
         tensors([256, 512, 256])
+
+
+def test_muon_tensors_refuse_momenta_or_copies_listed_twice():
+    import sparse_aggregation_message_gb300 as G
+
+    class Fake:
+        is_cuda, shape, device = True, (4, 8), torch.device("cuda", 0)
+
+        def __init__(self, at, dtype=torch.float32):
+            self.at, self.dtype = at, dtype
+
+        numel = lambda self: 32  # noqa: E731
+        data_ptr = lambda self: self.at  # noqa: E731
+        dim = lambda self: 2  # noqa: E731
+        stride = lambda self, k: (8, 1)[k]  # noqa: E731
+
+    p, g = [Fake(256), Fake(512)], [Fake(4096), Fake(8192)]
+    with pytest.raises(ValueError, match="momenta.*twice"):
+        G.MuonTensors(p, g, [Fake(1024), Fake(1024)])
+    with pytest.raises(ValueError, match="copies.*twice"):
+        G.MuonTensors(p, g, [Fake(1024), Fake(2048)], [Fake(65536, torch.bfloat16)] * 2)
+    assert G.MuonTensors(p, g, [Fake(1024), Fake(2048)], [Fake(65536, torch.bfloat16), None]).count == 2
+
+
+def test_coefficients_may_be_lists():
+    import sparse_aggregation_message_gb300 as G
+    want = [3.0, -4.0, 2.0, 1.5, -0.5, 0.0]
+    for c in ([[3.0, -4.0, 2.0], (1.5, -0.5, 0.0)], ([3.0, -4.0, 2.0], [1.5, -0.5, 0.0]), torch.tensor(want).view(2, 3).tolist()):
+        assert list(G._coeffs(c, 2)) == want
+    assert list(G._coeffs([3.0, -4.0, 2.0], 2)) == want[:3] * 2
+
+
+@pytest.mark.parametrize("bad", [dict(lr=1e39), dict(gs=-1e39), dict(lr=1e30, wd=1e30), dict(norms=MB + 64), dict(norms=3 * MB), dict(norms=16 * MB),
+                                 dict(ws=MB), dict(ws=2 * MB + 256), dict(copy=16 * MB)])
+def test_muon_refuses_what_overflows_or_overlaps(lib, bad):
+    assert muon(lib, **bad) == INVALID
+    assert b"gnn_muon" in lib.gnn_last_error()
+
+
+@pytest.mark.parametrize("bad", [dict(ws=MB), dict(ws=2 * MB), dict(norms=MB + 4), dict(norms=2 * MB + 8), dict(norms=16 * MB),
+                                 dict(O=MB, norms=MB)])
+def test_orthogonalise_refuses_overlaps_of_the_workspace_and_norms(lib, bad):
+    assert orth(lib, **bad) == INVALID
+    assert b"gnn_orthogonalise" in lib.gnn_last_error()

@@ -173,3 +173,10 @@ def test_structs_are_the_same_calls(lib):
         args[at] = value
         assert lib.gnn_residual_norm_bwd_struct(_abi.RESIDUAL_BWD.pack(*args)) == INVALID, at
         assert text in lib.gnn_last_error(), (at, lib.gnn_last_error())
+
+
+def test_backward_names_what_is_missing():
+    import sparse_aggregation_message_gb300 as G
+    x = torch.zeros(4, 16)
+    with pytest.raises(ValueError, match="H: needed"):
+        G.gnn_residual_norm_bwd(None, x, x, None, 4, 16, x, dR=x)
