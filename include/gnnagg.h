@@ -874,7 +874,8 @@ gnn_status gnn_orthogonalise(const void* X, int64_t ldx, int64_t stride_x, int32
  * receives the updated parameters rounded.  A matrix whose |u|_F is not finite
  * in fp32 keeps its parameters, copy and momentum; norms (fp32 [n_tensors], may
  * be NULL) receives every |u|_F (matrices without elements have none written).
- * No two arrays of a call overlap, nor is a matrix listed twice. */
+ * No two arrays of a call overlap (but bf16 parameters may be their own copy), nor
+ * is a matrix listed twice. */
 typedef struct gnn_muon_tensor {
   void* param;      /* fp32 or bf16 [rows][cols], updated in place */
   const void* grad; /* fp32, bf16 or fp16                          */

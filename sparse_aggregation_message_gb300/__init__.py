@@ -1177,7 +1177,7 @@ class MuonTensors:
     """The matrices of a Muon optimiser, checked once: lists of parameters (fp32
     or bf16 [rows, cols], updated in place), their gradients (fp32, bf16 or fp16),
     momenta (fp32 or bf16) and, optionally, copies (bf16, None for a matrix without
-    one), with contiguous rows, and the factors on the updates; scales None: 0.2
+    one; bf16 parameters may be their own), with contiguous rows, and the factors on the updates; scales None: 0.2
     sqrt(max(rows, cols)), which makes an update's mean square that of AdamW's, so
     that both take one learning rate.  All stay the caller's."""
 

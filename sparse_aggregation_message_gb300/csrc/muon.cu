@@ -1436,7 +1436,9 @@ extern "C" gnn_status gnn_muon_step(const gnn_muon_tensor* tensors, int32_t n_te
     GNN_REQUIRE(std::isfinite(t.scale), "%s: matrix %d has a scale that is not finite", who, i);
     const Span p = span(t.param, t, t.ldp, ps), g = span(t.grad, t, t.ldg, gs), m = span(t.m, t, t.ldm, ms),
                c = span(t.copy, t, t.ldc, 2);
-    GNN_REQUIRE(!overlap(p, g) && !overlap(p, m) && !overlap(g, m) && !overlap(c, p) && !overlap(c, g) && !overlap(c, m),
+    // bf16 parameters may be their own copy: a thread writes the same value twice
+    const bool own = param_type == GNN_BF16 && t.copy == t.param && t.ldc == t.ldp;
+    GNN_REQUIRE(!overlap(p, g) && !overlap(p, m) && !overlap(g, m) && (own || !overlap(c, p)) && !overlap(c, g) && !overlap(c, m),
                 "%s: matrix %d has arrays that overlap", who, i);
   }
   size_t need = 0;

@@ -218,3 +218,17 @@ def test_small_batches_behind_one_another():
     torch.cuda.synchronize()
     for i, O in enumerate(together):  # noqa: E741
         assert torch.equal(O, alone[i % len(X)])
+
+
+def test_parameters_may_be_their_own_copy():
+    shapes = [[(12, 6), (519, 2)], [(130, 70), (64, 300)]]
+    for some in shapes:
+        def new():
+            return [[matrix(r, c, 5 * i + j, BF16 if j == 0 else F32).cuda() for i, (r, c) in enumerate(some)] for j in range(3)]
+
+        p, g, m = new()
+        G.gnn_muon_step(G.MuonTensors(p, g, m), 0.02, weight_decay=0.1)
+        p2, g2, m2 = new()
+        G.gnn_muon_step(G.MuonTensors(p2, g2, m2, p2), 0.02, weight_decay=0.1)
+        for a, b in zip(p + m, p2 + m2):
+            assert torch.equal(a, b)

@@ -191,3 +191,10 @@ def test_muon_refuses_what_overflows_or_overlaps(lib, bad):
 def test_orthogonalise_refuses_overlaps_of_the_workspace_and_norms(lib, bad):
     assert orth(lib, **bad) == INVALID
     assert b"gnn_orthogonalise" in lib.gnn_last_error()
+
+
+@pytest.mark.parametrize("bad", [dict(copy=MB), dict(pt=BF16, copy=MB, ldc=128), dict(pt=BF16, copy=MB + 64)])
+def test_a_copy_that_overlaps_its_parameters_is_refused(lib, bad):
+    """All but bf16 parameters that are their own copy."""
+    assert muon(lib, **bad) == INVALID
+    assert b"overlap" in lib.gnn_last_error()
