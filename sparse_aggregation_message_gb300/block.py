@@ -135,7 +135,9 @@ class NodeStack:
         self._kept = None
 
     def forward(self, H, stream=None):
-        """H: fp32 [n, F]; returns the stream behind the last block (fp32 [n, F])."""
+        """H: fp32 [n, F], n >= 1; returns the stream behind the last block (fp32 [n, F])."""
+        if H.dim() != 2 or H.shape[0] < 1 or H.shape[1] != self.F or H.dtype is not torch.float32:
+            raise ValueError(f"H: needs fp32 [n, {self.F}] with n >= 1, got {H.dtype} {tuple(H.shape)}")
         n, F, Fm, dev, norm = H.shape[0], self.F, self.F_mid, H.device, self.norm
         with torch.cuda.stream(stream):
             operand = lambda c: torch.empty(n, ldb_for(c), dtype=torch.bfloat16, device=dev)  # noqa: E731

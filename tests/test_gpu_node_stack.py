@@ -130,3 +130,12 @@ def test_training_step_in_a_graph():
     for a, b in zip(eager.weights, caught.weights):
         for k in a:
             assert torch.equal(a[k], b[k]), k
+
+
+def test_refuses_other_streams():
+    from sparse_aggregation_message_gb300.block import NodeStack
+    stack = NodeStack(2, 32, 64, seed=1)
+    for H in (torch.empty(0, 32, device="cuda"), torch.zeros(4, 48, device="cuda"), torch.zeros(32, device="cuda"),
+              torch.zeros(4, 32, dtype=torch.bfloat16, device="cuda")):
+        with pytest.raises(ValueError, match="H: needs"):
+            stack.forward(H)
