@@ -44,8 +44,10 @@ struct Args {
   float eps, inv_c;
   float4* stats;
   float* part;            // backward: [blocks][4][8 lanes K]
+  float* part_lo;         // where a lane has more than CHAIN rows: what the sums over its chains lost, else NULL
   double* part_s;         // backward, one learned scale: every block's share of its gradient, or NULL
   int want_q, want_p;     // backward: which sums over all rows are kept
+  int64_t rounds, rest;   // backward: whole rounds of a row for every group of the grid, and rows left
   // the ring: stages, 16-byte pieces of a lane in one, and where each matrix's begin
   int stages, pieces, at[5];
 };
@@ -376,9 +378,17 @@ __global__ void __launch_bounds__(MULTI ? MAX_LANES : K == 1 ? THREADS : FEW)
   }
 }
 
-// The channels' sums stay in registers over all rows of a group, so its registers leave
-// 16 warps to an SM: 716,847 x 256 bf16 533 us, 5.5 TB/s, issue slots 60% taken beside
-// DRAM; 232,965 x 602 in fp32, three warps a row, 680 us, 5.0 TB/s.
+// The channels' sums stay in registers over CHAIN rows of a group, so its registers leave
+// 16 warps to an SM: 716,847 x 256 bf16 534 us, 5.5 TB/s, issue slots
+// 60% taken beside DRAM; 232,965 x 602 in fp32, three warps a row, 687 us, 4.9 TB/s.
+//
+// An addition to a lane's running sum errs by up to 2^-24 of the sum so far, equal terms
+// all to one side: a chain of 88 by 44.5 units at most, and with what follows (a warp's
+// groups, a block's warps, its share of 304 in the join, the join's lanes) by 64; a chain of
+// 1,028 equal terms measured 189.  So a block adds its lanes' sums up every CHAIN rows, in
+// two terms (716,847 x 256 bf16: 534 us, one chain 536).
+constexpr int CHAIN = 88;
+
 template <class TB, class TR, class TY, bool MULTI, int K>
 __global__ void __launch_bounds__(MULTI ? MAX_LANES : K == 1 ? THREADS : FEW, MULTI ? 1 : 2)
     residual_bwd_kernel(const __grid_constant__ Args g) {
@@ -389,7 +399,6 @@ __global__ void __launch_bounds__(MULTI ? MAX_LANES : K == 1 ? THREADS : FEW, MU
   Row<MULTI> row(g.lanes, sm);
   const int threads = blockDim.x, groups = threads / g.lanes, span = 8 * g.lanes, width = K * span;
   const int64_t step = (int64_t)gridDim.x * groups;
-  const int ahead = MULTI ? 0 : row.group & (32 / g.lanes - 1);
   constexpr bool SPLIT = std::is_same<TB, float>::value || std::is_same<TR, float>::value || std::is_same<TY, float>::value;
   const int c = (SPLIT ? 4 : 8) * row.lane, apart = SPLIT ? 4 * g.lanes : 4;
   const Left left{g.C - c, g.C - c - apart};
@@ -428,176 +437,8 @@ __global__ void __launch_bounds__(MULTI ? MAX_LANES : K == 1 ? THREADS : FEW, MU
     ds_lo += (ds_hi - (sum - part)) + (x - part);
     ds_hi = sum;
   };
-  Eight acc[4][K];  // sums of dY yh, dY, D t bh, D t
-#pragma unroll
-  for (int a = 0; a < 4; ++a)
-#pragma unroll
-    for (int k = 0; k < K; ++k)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) acc[a][k][j] = dup2(0.f);
-  int st = 0, into = g.stages - 1;
-  for (; i - ahead < g.n; i += step) {
-    request(into, i + (g.stages - 1) * step);
-    const float t_row = t_next;
-    const float4 stat = s_next;
-    t_next = row_gate(i + step), s_next = row_stats(i + step);
-    wait_row(g.stages);
-    const bool live = i < g.n;
-    const uint4* from = mine + st * stage_size;
-    auto piece = [&](int which, int k) { return from + (k * g.pieces + g.at[which]) * threads; };
-    if (++st == g.stages) st = 0;
-    if (++into == g.stages) into = 0;
-    Eight d[K];
-    if (g.dY) {
-      // q = w dY; D = dH + rstd (q - mean q - yh mean(q yh)); K > 1 reads yh again after
-      // the sums instead of keeping it
-      float s[2] = {0.f, 0.f};
-      Eight kept;
-#pragma unroll
-      for (int k = 0; k < K; ++k) {
-        const Left m{left.a - k * span, left.b - k * span};
-        Eight yh, w;
-        take<TY>(piece(0, k), threads, m, d[k]);
-        take<TR>(piece(1, k), threads, m, yh);
-        normalise(yh, m, stat.z, stat.w);
-        from_shared<SPLIT>(w_at + 2 * width, c + k * span, apart, width, w);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          acc[0][k][j] = fma2_rn(d[k][j], yh[j], acc[0][k][j]);
-          acc[1][k][j] = add2_rn(d[k][j], acc[1][k][j]);
-          d[k][j] = mul2_rn(d[k][j], w[j]);
-          if (K == 1) kept[j] = yh[j];
-        }
-        s[0] += dot(d[k], yh), s[1] += add_up(d[k]);
-      }
-      if (g.pre == GNN_NORM_LAYER) {
-        row.sum(s);
-      } else {
-        float one[1] = {s[0]};
-        row.sum(one);
-        s[0] = one[0], s[1] = 0.f;
-      }
-      const float2 along = dup2(-s[0] * g.inv_c), mean = dup2(-s[1] * g.inv_c), r = dup2(stat.w);
-#pragma unroll
-      for (int k = 0; k < K; ++k) {
-        const Left m{left.a - k * span, left.b - k * span};
-        Eight dh;
-        if (K > 1) {
-          take<TR>(piece(1, k), threads, m, kept);
-          normalise(kept, m, stat.z, stat.w);
-        }
-        if (g.dH) {
-          take<TR>(piece(2, k), threads, m, dh);
-        } else {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) dh[j] = dup2(0.f);
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) d[k][j] = fma2_rn(r, fma2_rn(kept[j], along, add2_rn(d[k][j], mean)), dh[j]);
-        mask(d[k], m);
-      }
-    } else {
-#pragma unroll
-      for (int k = 0; k < K; ++k) take<TR>(piece(2, k), threads, Left{left.a - k * span, left.b - k * span}, d[k]);
-    }
-    if (g.dR && live) {
-#pragma unroll
-      for (int k = 0; k < K; ++k) put<TR, SPLIT>(g.dR, i * g.lddr, c + k * span, apart, d[k], Left{left.a - k * span, left.b - k * span});
-    }
-    if (g.B) {
-      float s[3] = {0.f, 0.f, 0.f};
-      float2 t1 = dup2(1.f), slope1 = dup2(0.f);
-      if (g.gate == 1) act_grad2(dup2(t_row), g.act, t1, slope1);
-      Eight kept;
-#pragma unroll
-      for (int k = 0; k < K; ++k) {
-        const Left m{left.a - k * span, left.b - k * span};
-        Eight bh, w, b;
-        take<TB>(piece(3, k), threads, m, bh);
-        normalise(bh, m, stat.x, stat.y);
-        from_shared<SPLIT>(w_at, c + k * span, apart, width, w);
-        from_shared<SPLIT>(w_at + width, c + k * span, apart, width, b);
-        if (g.gate == 2) {
-          Eight t, slope;
-          take<TB>(piece(4, k), threads, m, t);
-          with_act(g.act, [&](auto A) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float2 z = t[j];
-              act_grad2(z, A, t[j], slope[j]);
-            }
-          });
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float2 z = fma2_rn(w[j], bh[j], b[j]);
-            slope[j] = mul2_rn(slope[j], mul2_rn(d[k][j], z));
-            d[k][j] = mul2_rn(d[k][j], t[j]);
-            t[j] = z;
-          }
-          if (g.part_s) {
-            add_ds(dot(d[k], t));
-#pragma unroll
-            for (int j = 0; j < 4; ++j) slope[j] = mul2_rn(slope[j], one_scale);
-          }
-          if (g.dG && live) put<TB, SPLIT>(g.dG, i * g.lddg, c + k * span, apart, slope, m);
-        } else if (g.gate == 1 || g.part_s) {
-          float2 z = dup2(0.f);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            z = fma2_rn(d[k][j], fma2_rn(w[j], bh[j], b[j]), z);
-            d[k][j] = mul2_rn(d[k][j], t1);
-          }
-          s[2] += z.x + z.y;
-          if (g.part_s) add_ds(t1.x * (z.x + z.y));
-        }
-        if (g.part_s) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) w[j] = mul2_rn(w[j], one_scale);
-        }
-        // d: D t here, and times s w_post from here on
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          acc[2][k][j] = fma2_rn(d[k][j], bh[j], acc[2][k][j]);
-          acc[3][k][j] = add2_rn(d[k][j], acc[3][k][j]);
-          d[k][j] = mul2_rn(d[k][j], w[j]);
-          if (K == 1) kept[j] = bh[j];
-        }
-        s[0] += dot(d[k], bh), s[1] += add_up(d[k]);
-      }
-      const bool norm = g.post != GNN_NORM_NONE;
-      if (g.gate == 1) {
-        row.sum(s);
-        if (g.dG && live && row.lane == 0)
-          static_cast<TB*>(g.dG)[i * g.lddg] = from_f32<TB>(s[2] * one_scale.x * slope1.x);
-      } else if (g.post == GNN_NORM_LAYER) {
-        float two[2] = {s[0], s[1]};
-        row.sum(two);
-        s[0] = two[0], s[1] = two[1];
-      } else if (norm) {
-        float one[1] = {s[0]};
-        row.sum(one);
-        s[0] = one[0];
-      }
-      if (g.dB && live) {
-        const float2 along = dup2(-s[0] * g.inv_c), mean = dup2(g.post == GNN_NORM_LAYER ? -s[1] * g.inv_c : 0.f),
-                     r = dup2(stat.y);
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-          const Left m{left.a - k * span, left.b - k * span};
-          if (norm) {
-            if (K > 1) {
-              take<TB>(piece(3, k), threads, m, kept);
-              normalise(kept, m, stat.x, stat.y);
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) d[k][j] = mul2_rn(r, fma2_rn(kept[j], along, add2_rn(d[k][j], mean)));
-          }
-          put<TB, SPLIT>(g.dB, i * g.lddb, c + k * span, apart, d[k], m);
-        }
-      }
-    }
-  }
-  if (g.part_s) {
+  auto one_scale_sum = [&] {
+    if (!g.part_s) return;
     __shared__ double share[MAX_LANES / 32];
     double t = (double)ds_hi + (double)ds_lo;
 #pragma unroll
@@ -609,44 +450,264 @@ __global__ void __launch_bounds__(MULTI ? MAX_LANES : K == 1 ? THREADS : FEW, MU
       for (int k = 0; k < threads / 32; ++k) t += share[k];
       g.part_s[blockIdx.x] = t;
     }
-  }
-  if (!g.want_q && !g.want_p) return;
-  // over the groups of a warp, then over the block's warps or groups in order, in
-  // the ring's memory (every copy has landed: the last rows' are waited for)
-  wait_copies<0>();
-  if (!MULTI) {
-    for (int o = g.lanes; o < 32; o <<= 1) {
-#pragma unroll
-      for (int a = 0; a < 4; ++a)
-#pragma unroll
-        for (int k = 0; k < K; ++k)
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            acc[a][k][j] = add2_rn(acc[a][k][j], make_float2(__shfl_xor_sync(0xffffffffu, acc[a][k][j].x, o),
-                                                             __shfl_xor_sync(0xffffffffu, acc[a][k][j].y, o)));
-    }
-  }
-  __syncthreads();
-  // [turns][4][width]: every warp's (or group's) sums, then each column by one thread
-  const int turns = MULTI ? groups : threads / 32, turn = MULTI ? row.group : threadIdx.x >> 5;
-  float* all = reinterpret_cast<float*>(ring);
-  if (MULTI || (threadIdx.x & 31) < g.lanes) {
+  };
+  int st = 0, into = g.stages - 1;
+  // the block's rounds of one row a group; with several chains the first ends sooner in some
+  // blocks, so that not all of the card adds up at the same time
+  int64_t rounds = g.rounds + ((int64_t)blockIdx.x * groups < g.rest);
+  int chain = !g.part_lo ? 0x7fffffff : CHAIN - (blockIdx.x + 2 * (blockIdx.x / 152)) % 4 * (CHAIN / 4);
+  bool first = true;
+  do {
+    Eight acc[4][K];  // sums of dY yh, dY, D t bh, D t
 #pragma unroll
     for (int a = 0; a < 4; ++a)
 #pragma unroll
-      for (int k = 0; k < K; ++k) {
-        float* to = all + (turn * 4 + a) * width + c + k * span;
-        *reinterpret_cast<float4*>(to) = make_float4(acc[a][k][0].x, acc[a][k][0].y, acc[a][k][1].x, acc[a][k][1].y);
-        *reinterpret_cast<float4*>(to + apart) = make_float4(acc[a][k][2].x, acc[a][k][2].y, acc[a][k][3].x, acc[a][k][3].y);
+      for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[a][k][j] = dup2(0.f);
+    int left_here = (int)min(rounds, (int64_t)chain);
+    rounds -= left_here;
+    chain = CHAIN;
+    for (; left_here > 0; --left_here, i += step) {
+      request(into, i + (g.stages - 1) * step);
+      const float t_row = t_next;
+      const float4 stat = s_next;
+      t_next = row_gate(i + step), s_next = row_stats(i + step);
+      wait_row(g.stages);
+      const bool live = i < g.n;
+      const uint4* from = mine + st * stage_size;
+      auto piece = [&](int which, int k) { return from + (k * g.pieces + g.at[which]) * threads; };
+      if (++st == g.stages) st = 0;
+      if (++into == g.stages) into = 0;
+      Eight d[K];
+      if (g.dY) {
+        // q = w dY; D = dH + rstd (q - mean q - yh mean(q yh)); K > 1 reads yh again after
+        // the sums instead of keeping it
+        float s[2] = {0.f, 0.f};
+        Eight kept;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+          const Left m{left.a - k * span, left.b - k * span};
+          Eight yh, w;
+          take<TY>(piece(0, k), threads, m, d[k]);
+          take<TR>(piece(1, k), threads, m, yh);
+          normalise(yh, m, stat.z, stat.w);
+          from_shared<SPLIT>(w_at + 2 * width, c + k * span, apart, width, w);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            acc[0][k][j] = fma2_rn(d[k][j], yh[j], acc[0][k][j]);
+            acc[1][k][j] = add2_rn(d[k][j], acc[1][k][j]);
+            d[k][j] = mul2_rn(d[k][j], w[j]);
+            if (K == 1) kept[j] = yh[j];
+          }
+          s[0] += dot(d[k], yh), s[1] += add_up(d[k]);
+        }
+        if (g.pre == GNN_NORM_LAYER) {
+          row.sum(s);
+        } else {
+          float one[1] = {s[0]};
+          row.sum(one);
+          s[0] = one[0], s[1] = 0.f;
+        }
+        const float2 along = dup2(-s[0] * g.inv_c), mean = dup2(-s[1] * g.inv_c), r = dup2(stat.w);
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+          const Left m{left.a - k * span, left.b - k * span};
+          Eight dh;
+          if (K > 1) {
+            take<TR>(piece(1, k), threads, m, kept);
+            normalise(kept, m, stat.z, stat.w);
+          }
+          if (g.dH) {
+            take<TR>(piece(2, k), threads, m, dh);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) dh[j] = dup2(0.f);
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) d[k][j] = fma2_rn(r, fma2_rn(kept[j], along, add2_rn(d[k][j], mean)), dh[j]);
+          mask(d[k], m);
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < K; ++k) take<TR>(piece(2, k), threads, Left{left.a - k * span, left.b - k * span}, d[k]);
       }
-  }
-  __syncthreads();
-  float* out = g.part + (int64_t)blockIdx.x * 4 * width;
-  for (int at = threadIdx.x; at < 4 * width; at += threads) {
-    float s = all[at];
-    for (int k = 1; k < turns; ++k) s += all[k * 4 * width + at];
-    out[at] = s;
-  }
+      if (g.dR && live) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) put<TR, SPLIT>(g.dR, i * g.lddr, c + k * span, apart, d[k], Left{left.a - k * span, left.b - k * span});
+      }
+      if (g.B) {
+        float s[3] = {0.f, 0.f, 0.f};
+        float2 t1 = dup2(1.f), slope1 = dup2(0.f);
+        if (g.gate == 1) act_grad2(dup2(t_row), g.act, t1, slope1);
+        Eight kept;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+          const Left m{left.a - k * span, left.b - k * span};
+          Eight bh, w, b;
+          take<TB>(piece(3, k), threads, m, bh);
+          normalise(bh, m, stat.x, stat.y);
+          from_shared<SPLIT>(w_at, c + k * span, apart, width, w);
+          from_shared<SPLIT>(w_at + width, c + k * span, apart, width, b);
+          if (g.gate == 2) {
+            Eight t, slope;
+            take<TB>(piece(4, k), threads, m, t);
+            with_act(g.act, [&](auto A) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const float2 z = t[j];
+                act_grad2(z, A, t[j], slope[j]);
+              }
+            });
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float2 z = fma2_rn(w[j], bh[j], b[j]);
+              slope[j] = mul2_rn(slope[j], mul2_rn(d[k][j], z));
+              d[k][j] = mul2_rn(d[k][j], t[j]);
+              t[j] = z;
+            }
+            if (g.part_s) {
+              add_ds(dot(d[k], t));
+#pragma unroll
+              for (int j = 0; j < 4; ++j) slope[j] = mul2_rn(slope[j], one_scale);
+            }
+            if (g.dG && live) put<TB, SPLIT>(g.dG, i * g.lddg, c + k * span, apart, slope, m);
+          } else if (g.gate == 1 || g.part_s) {
+            float2 z = dup2(0.f);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              z = fma2_rn(d[k][j], fma2_rn(w[j], bh[j], b[j]), z);
+              d[k][j] = mul2_rn(d[k][j], t1);
+            }
+            s[2] += z.x + z.y;
+            if (g.part_s) add_ds(t1.x * (z.x + z.y));
+          }
+          if (g.part_s) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w[j] = mul2_rn(w[j], one_scale);
+          }
+          // d: D t here, and times s w_post from here on
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            acc[2][k][j] = fma2_rn(d[k][j], bh[j], acc[2][k][j]);
+            acc[3][k][j] = add2_rn(d[k][j], acc[3][k][j]);
+            d[k][j] = mul2_rn(d[k][j], w[j]);
+            if (K == 1) kept[j] = bh[j];
+          }
+          s[0] += dot(d[k], bh), s[1] += add_up(d[k]);
+        }
+        const bool norm = g.post != GNN_NORM_NONE;
+        if (g.gate == 1) {
+          row.sum(s);
+          if (g.dG && live && row.lane == 0)
+            static_cast<TB*>(g.dG)[i * g.lddg] = from_f32<TB>(s[2] * one_scale.x * slope1.x);
+        } else if (g.post == GNN_NORM_LAYER) {
+          float two[2] = {s[0], s[1]};
+          row.sum(two);
+          s[0] = two[0], s[1] = two[1];
+        } else if (norm) {
+          float one[1] = {s[0]};
+          row.sum(one);
+          s[0] = one[0];
+        }
+        if (g.dB && live) {
+          const float2 along = dup2(-s[0] * g.inv_c), mean = dup2(g.post == GNN_NORM_LAYER ? -s[1] * g.inv_c : 0.f),
+                       r = dup2(stat.y);
+#pragma unroll
+          for (int k = 0; k < K; ++k) {
+            const Left m{left.a - k * span, left.b - k * span};
+            if (norm) {
+              if (K > 1) {
+                take<TB>(piece(3, k), threads, m, kept);
+                normalise(kept, m, stat.x, stat.y);
+              }
+#pragma unroll
+              for (int j = 0; j < 4; ++j) d[k][j] = mul2_rn(r, fma2_rn(kept[j], along, add2_rn(d[k][j], mean)));
+            }
+            put<TB, SPLIT>(g.dB, i * g.lddb, c + k * span, apart, d[k], m);
+          }
+        }
+      }
+    }
+    if (!g.want_q && !g.want_p) continue;
+    // over the groups of a warp, then over the block's warps or groups in order: one of the
+    // four sums at a time beside the ring, or, behind a block's only chain, all of them in
+    // the ring's memory (every copy has landed: the last rows' are waited for)
+    if (!MULTI) {
+      for (int o = g.lanes; o < 32; o <<= 1) {
+#pragma unroll
+        for (int a = 0; a < 4; ++a)
+#pragma unroll
+          for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              acc[a][k][j] = add2_rn(acc[a][k][j], make_float2(__shfl_xor_sync(0xffffffffu, acc[a][k][j].x, o),
+                                                               __shfl_xor_sync(0xffffffffu, acc[a][k][j].y, o)));
+      }
+    }
+    const int turns = MULTI ? groups : threads / 32, turn = MULTI ? row.group : threadIdx.x >> 5;
+    float* const out = g.part + (int64_t)blockIdx.x * 4 * width;
+    auto pass_on = [&](float* to, int a) {
+      if (MULTI || (threadIdx.x & 31) < g.lanes) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+          float* at = to + c + k * span;
+          *reinterpret_cast<float4*>(at) = make_float4(acc[a][k][0].x, acc[a][k][0].y, acc[a][k][1].x, acc[a][k][1].y);
+          *reinterpret_cast<float4*>(at + apart) = make_float4(acc[a][k][2].x, acc[a][k][2].y, acc[a][k][3].x, acc[a][k][3].y);
+        }
+      }
+    };
+    if (!g.part_lo) {  // [turns][4][width]
+      wait_copies<0>();
+      __syncthreads();
+      float* const all = reinterpret_cast<float*>(ring);
+#pragma unroll
+      for (int a = 0; a < 4; ++a) pass_on(all + (turn * 4 + a) * width, a);
+      __syncthreads();
+      for (int at = threadIdx.x; at < 4 * width; at += threads) {
+        float s = all[at];
+        for (int k = 1; k < turns; ++k) s += all[k * 4 * width + at];
+        out[at] = s;
+      }
+      return one_scale_sum();
+    }
+    // [turns][width]; every column of the running sums is one thread's, which asks for them
+    // early: where registers allow it for the next kind's while it adds this one's
+    constexpr int COLS = MULTI ? 8 : K == 1 ? 1 : 2 * K;  // of a thread, at most
+    constexpr int AHEAD = MULTI ? 0 : 1;
+    float* const all = reinterpret_cast<float*>(ring + g.stages * stage_size);
+    float hi[AHEAD + 1][COLS], lo[AHEAD + 1][COLS];
+    auto ask = [&](int a) {
+#pragma unroll
+      for (int j = 0; j < COLS; ++j) {
+        const int at = threadIdx.x + j * threads;
+        const bool there = !first && at < width;
+        hi[a & AHEAD][j] = there ? out[a * width + at] : 0.f;
+        lo[a & AHEAD][j] = there ? out[a * width + at + (g.part_lo - g.part)] : 0.f;
+      }
+    };
+    if (AHEAD) ask(0);
+#pragma unroll
+    for (int a = 0; a < 4; ++a) {
+      if (a + AHEAD < 4) ask(a + AHEAD);
+      pass_on(all + turn * width, a);
+      __syncthreads();
+#pragma unroll
+      for (int j = 0; j < COLS; ++j) {
+        const int at = threadIdx.x + j * threads;
+        if (at >= width) break;
+        float s = all[at];
+        for (int k = 1; k < turns; ++k) s += all[k * width + at];
+        const float before = hi[a & AHEAD][j], sum = before + s, part = sum - before;  // two terms (Knuth)
+        const float lost = lo[a & AHEAD][j] + ((before - (sum - part)) + (s - part));
+        out[a * width + at] = rounds > 0 ? sum : sum + lost;
+        if (rounds > 0) out[a * width + at + (g.part_lo - g.part)] = lost;
+      }
+      __syncthreads();
+    }
+    first = false;
+  } while (rounds > 0);
+  one_scale_sum();
 }
 
 // The blocks' sums, in order, and the weights' gradients from them.  In fp32: an
@@ -735,14 +796,20 @@ Shape shape_for(int C, bool bwd) {
   return {lanes, 1, MAX_LANES / lanes * lanes, true};
 }
 
+// What one of the four sums of every warp or group takes on its way through shared memory.
+int one_sum(const Shape& s) { return (s.multi ? s.threads / s.lanes : s.threads / 32) * 8 * s.lanes * s.vecs * (int)sizeof(float); }
+
 // Blocks that an SM holds at once, by the kernels' registers and with two stages of the ring
-// at least; up to four stages in what that leaves of shared memory.
+// at least; up to four stages in what that leaves of shared memory.  The 4 KB are for static
+// shared memory, what the system takes of it (2 KB together at most) and, where lanes have
+// several chains of sums, a sum of up to 2 KB on its way.
 struct Fit {
   int blocks, stages;
 };
-Fit fit_of(const Shape& s, bool bwd, int pieces) {
+Fit fit_of(const Shape& s, bool bwd, int pieces, bool chains = false) {
   const int regs = bwd ? (s.vecs == 1 ? 128 : 256) : s.vecs == 1 ? 104 : 128;
-  const int stage = s.vecs * pieces * s.threads * 16, weights = (bwd ? 12 : 16) * 8 * s.lanes * s.vecs + 4096;
+  const int stage = s.vecs * pieces * s.threads * 16;
+  const int weights = (bwd ? 12 : 16) * 8 * s.lanes * s.vecs + (chains ? std::max(0, one_sum(s) - 2048) : 0) + 4096;
   const int most = 227 << 10;
   Fit f{std::max(1, 65536 / (regs * s.threads)), 4};
   while (f.blocks > 1 && f.blocks * (weights + 2 * stage) > most) --f.blocks;
@@ -756,8 +823,11 @@ int64_t blocks_for(int64_t n, const Shape& s, bool bwd) {
   return std::max<int64_t>(1, std::min<int64_t>((n + rows - 1) / rows, 152 * fit_of(s, bwd, bwd ? 5 : 3).blocks));
 }
 
+// Whether some lane has more rows than one chain of sums takes.
+bool chained(int64_t n, const Shape& s) { return n > CHAIN * blocks_for(n, s, true) * (s.threads / s.lanes); }
+
 struct ResidualWs {
-  float* part;
+  float *part, *part_lo;
   double* part_s;
   size_t bytes;
 };
@@ -765,7 +835,9 @@ ResidualWs residual_ws(void* base, size_t cap, int64_t n, int C, bool* ok) {
   Arena ar(base, cap);
   ResidualWs w{};
   const Shape s = shape_for(C, true);
-  w.part = ar.take<float>((size_t)blocks_for(n, s, true) * 4 * s.lanes * s.vecs * 8);
+  const size_t sums = (size_t)blocks_for(n, s, true) * 4 * s.lanes * s.vecs * 8;
+  w.part = ar.take<float>(sums);
+  w.part_lo = chained(n, s) ? ar.take<float>(sums) : nullptr;
   w.part_s = ar.take<double>((size_t)blocks_for(n, s, true));
   w.bytes = ar.used;
   *ok = ar.ok();
@@ -805,15 +877,17 @@ gnn_status run_shape(Args& g, const Shape& s, cudaStream_t st) {
   const gnn_status r = allow_smem(k, SMEM_MOST, done);
   if (r != GNN_OK) return r;
   const int width = 8 * s.lanes * K * (int)sizeof(float), weights = (BWD ? 3 : 4) * width;
-  g.stages = fit_of(s, BWD, g.pieces).stages;
+  g.stages = fit_of(s, BWD, g.pieces, g.part_lo != nullptr).stages;
   int ring = g.stages * K * g.pieces * s.threads * 16;
-  // the backward's sums of every warp or group pass through the ring
-  if (BWD) ring = std::max(ring, (MULTI ? s.threads / s.lanes : s.threads / 32) * 4 * width);
+  // the backward's sums pass beside the ring, or all at once through it
+  if (BWD) ring = g.part_lo ? ring + one_sum(s) : std::max(ring, 4 * one_sum(s));
   // No more blocks to an SM than the grid counts on: a launch that starts while the
   // last one ends would crowd SMs that are free first (716,847 x 256 forward, one
   // call behind another: 541 us against 423 alone).
   const int smem = std::max(weights + ring, (227 << 10) / (fit_of(s, BWD, BWD ? 5 : 3).blocks + 1));
-  return launch(blocks_for(g.n, s, BWD), s.threads, smem, st, k, g);
+  const int64_t blocks = blocks_for(g.n, s, BWD), round = blocks * (s.threads / s.lanes);
+  g.rounds = g.n / round, g.rest = g.n % round;
+  return launch(blocks, s.threads, smem, st, k, g);
 }
 template <bool BWD, class TB, class TR, class TY>
 gnn_status run(Args& g, cudaStream_t st) {
@@ -999,6 +1073,7 @@ extern "C" gnn_status gnn_residual_norm_bwd(const void* dH, int64_t lddh, const 
                 "%s: dgate of one value a row is misaligned or has no stride", who);
   }
   const int want_q = dw_pre || db_pre, want_p = dw_post || db_post || (dscale && scale_cols > 1), want_s = dscale && scale_cols == 1;
+  const Shape sh = shape_for(C, true);
   bool ok;
   const ResidualWs w = residual_ws(ws, ws_bytes, n, C, &ok);
   GNN_REQUIRE((!want_q && !want_p && !want_s) || (ws && ok && ((uintptr_t)ws & 7) == 0),
@@ -1026,13 +1101,13 @@ extern "C" gnn_status gnn_residual_norm_bwd(const void* dH, int64_t lddh, const 
     g.scale_cols = scale_cols, g.inv_c = 1.f / (float)C;
     g.stats = reinterpret_cast<float4*>(const_cast<float*>(stats)), g.part = w.part;
     g.want_q = want_q, g.want_p = want_p, g.part_s = want_s ? w.part_s : nullptr;
+    g.part_lo = want_q || want_p ? w.part_lo : nullptr;
     s = with_types(b_type, r_type, y_type, [&](auto b, auto r, auto y) {
       return run<true, decltype(b), decltype(r), decltype(y)>(g, as_stream(stream));
     });
     if (s != GNN_OK) return s;
   }
   if (!want_q && !want_p && !want_s) return GNN_OK;
-  const Shape sh = shape_for(C, true);
   const int blocks = (C + 31) / 32;
   const Join j{w.part, w.part_s, n > 0 ? (int)blocks_for(n, sh, true) : 0, sh.lanes * sh.vecs * 8, C, scale_cols, w_post, b_post,
                scale, dw_post, db_post, dscale, dw_pre, db_pre, want_q, want_p};

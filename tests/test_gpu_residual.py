@@ -295,3 +295,48 @@ def test_offsets_past_32_bits():
     close(dB[-5:, :C], *want["dB"], BF16, "dB")
     close(dw, *want["dw_pre"], F32, "dw_pre")
     assert (dR[:-5] == 0).all() and (dB[:-5] == 0).all()
+
+
+def test_sums_over_many_equal_rows():
+    """Equal rows, as a mean over all of them gives: every addition of a running fp32
+    sum then errs the same way, by m/4 units after m terms (measured for 0.1 on the CPU:
+    160 u after 1,028), so no chain of additions may be that long.  Bounds as in
+    residual_ref, which hold for terms of one sign: 64 u, and 80 u where a term is a product."""
+    n, C = 20_000_003, 8
+    h = torch.linspace(0.3, 1.9, C)
+    r = float(1 / torch.sqrt(h.double().square().mean() + 1e-6))
+    H = h.cuda().repeat(n, 1)
+    dY = torch.full((n, C), 0.1, device="cuda")
+    st = torch.tensor([0.0, r, 0.0, r]).cuda().repeat(n, 1)
+    step, rstd = float(torch.tensor(0.1).double()), float(torch.tensor(r).float().double())
+    vec = lambda k=C: torch.full((k,), GUARD, device="cuda")  # noqa: E731
+
+    def near(got, want, units, what):
+        off = ((got.cpu().double() - want).abs() / want.abs()).max() / ref.U
+        assert off <= units, f"{what}: {float(off):.0f} units"
+
+    dw, db = vec(), vec()
+    G.gnn_residual_norm_bwd(None, dY, None, H, n, C, st, pre="rms", dw_pre=dw, db_pre=db)
+    near(dw, n * step * rstd * h.double(), 80, "dw_pre")
+    near(db, torch.full((C,), n * step, dtype=torch.float64), 64, "db_pre")
+    dw, db, ds, one = vec(), vec(), vec(), vec(1)
+    G.gnn_residual_norm_bwd(dY, None, H, H, n, C, st, pre="none", scale=torch.ones(C, device="cuda"), dw_post=dw, db_post=db, dscale=ds)
+    near(dw, n * step * rstd * h.double(), 80, "dw_post")
+    near(db, torch.full((C,), n * step, dtype=torch.float64), 64, "db_post")
+    near(ds, n * step * rstd * h.double(), 80, "dscale")
+    G.gnn_residual_norm_bwd(dY, None, H, H, n, C, st, pre="none", scale=torch.ones(1, device="cuda"), dscale=one)
+    near(one, (n * step * rstd * h.double()).sum()[None], 80, "one dscale")
+
+
+@pytest.mark.parametrize("n,C,t,scale", [(15_300, 2056, 3, "one"), (75_000, 520, 0, "all"), (60_000, 1024, 4, "all"), (240_003, 256, 5, "all"),
+                                         (235_000, 300, 3, "one"), (1_900_000, 8, 2, "all"), (940_000, 65, 1, "none")])
+def test_more_rows_than_one_chain_of_sums(n, C, t, scale):
+    """Rows of one warp, of parts of one and of several, one to 64 to a block, that take
+    several chains of sums."""
+    a = make(n, C, TYPES[t], "rms", "layer", "row", "sigmoid", scale, True, 61)
+    o, types = run_backward(a), dict(dR=a["types"][1], dB=a["types"][0], dgate=a["types"][0])
+    with torch.device("cuda"):
+        want = ref.backward({k: v.cuda() if isinstance(v, torch.Tensor) else v for k, v in a.items()})
+    for k, got in o.items():
+        value, bound = (x.cpu() for x in want.pop(k))
+        close(got[:, :C] if got.dim() == 2 else got, value, bound, types.get(k, F32), k)
