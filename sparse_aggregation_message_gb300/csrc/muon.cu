@@ -614,7 +614,10 @@ __device__ __forceinline__ void walk(const Steps& g, uint8_t* smem_raw) {
       for (int kb = 0; kb < w.kb; ++kb) {
         if (!tc::mbar_wait(&s.empty[st], ph ^ 1, g.flags, s.abort_flag)) goto done;
         if (rank == 0) tc::mbar_expect_tx(&s.full[st], (PAIR ? 2 : 1) * (BLOCK + bn * 256));
-        if (kb == 0 && !wait_for<COLS>(g, w, s.abort_flag)) goto done;
+        if (kb == 0) {
+          if (!wait_for<COLS>(g, w, s.abort_flag)) goto done;
+          tc::fence_async_global();  // what the count says is there, to TMA's reads too
+        }
         uint8_t* a = s.tiles + st * stage;
         const uint32_t bar = PAIR ? tc::map_to_rank(&s.full[st], 0) : tc::smem_u32(&s.full[st]);
         load_rows<PAIR>(g, a, bar, left, left_nb, 2 * rb, kb, true, w.phase == GRAM || above<PAIR>(rb, kb));
@@ -705,6 +708,7 @@ __device__ __forceinline__ void walk(const Steps& g, uint8_t* smem_raw) {
       if (w.phase == POLY) {  // A, by ordinary loads
         count_it();
         if (!all(lane || wait_for<COLS>(g, w, s.abort_flag))) goto done;
+        __syncwarp();  // orders the other lanes' reads behind the first one's wait, as a vote does not
       }
       const int64_t a_at = (int64_t)w.m.a * BLOCK + ((int64_t)rb * out_nb + w.cb) * BLOCK + r * 128;
       uint4 a_hi[MOST < 64 ? 4 : 1], a_lo[MOST < 64 ? 4 : 1];

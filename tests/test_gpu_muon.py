@@ -232,3 +232,20 @@ def test_parameters_may_be_their_own_copy():
         G.gnn_muon_step(G.MuonTensors(p2, g2, m2, p2), 0.02, weight_decay=0.1)
         for a, b in zip(p + m, p2 + m2):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("count,rows,cols", [(1, 65, 70), (3, 256, 512), (16, 65, 256), (8, 100, 2500), (1, 1000, 1000), (2, 640, 1700), (1, 2047, 2047),
+                                             (3, 1024, 4096)])
+def test_tiles_that_wait_for_one_another_give_the_same_bits(count, rows, cols):
+    """A tile that was read before all of it was there would show as other bits, on one
+    of the tile sizes, in one of many runs."""
+    x = torch.stack([matrix(rows, cols, 300 + i) for i in range(count)]).cuda()
+    first = torch.empty_like(x)
+    G.gnn_orthogonalise(x, first, steps=8)
+    again = [torch.full_like(x, GUARD) for _ in range(4)]
+    for _ in range(5):
+        for O in again:  # noqa: E741
+            G.gnn_orthogonalise(x, O, steps=8)
+        for O in again:  # noqa: E741
+            assert torch.equal(O, first)
+    G.gnn_sync_check()
