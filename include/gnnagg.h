@@ -855,7 +855,8 @@ gnn_status gnn_adamw_step(const gnn_adamw_tensor* tensors, int32_t n_tensors, in
  * least 1e-30.  Operands are held to 22 bits, down to 2^-35 (of a matrix of norm
  * one), products accumulate in fp32; the steps have to keep every singular value v
  * below 7 and a + b v^2 + c v^4 within 60 of zero.  norms (fp32 [count], may be NULL)
- * receives |X|_F.  A matrix whose norm is not finite in fp32 gives NaN.  O may be X
+ * receives |X|_F.  A matrix whose norm is not finite in fp32 gives NaN, and so does one
+ * whose steps a wait that ran out has ended (gnn_sync_check: GNN_ERR_TIMEOUT).  O may be X
  * (one type size and strides).  rows, cols <= 65536, the smaller of them <= 16384.
  * Workspaces lie on a 256-byte border. */
 gnn_status gnn_orthogonalise_workspace(int32_t count, int32_t rows, int32_t cols,
@@ -874,6 +875,8 @@ gnn_status gnn_orthogonalise(const void* X, int64_t ldx, int64_t stride_x, int32
  * receives the updated parameters rounded.  A matrix whose |u|_F is not finite
  * in fp32 keeps its parameters, copy and momentum; norms (fp32 [n_tensors], may
  * be NULL) receives every |u|_F (matrices without elements have none written).
+ * After a wait that ran out (gnn_sync_check: GNN_ERR_TIMEOUT) the matrices whose
+ * steps it ended keep parameters and copy; their momenta have taken the step.
  * No two arrays of a call overlap (but bf16 parameters may be their own copy), nor
  * is a matrix listed twice. */
 typedef struct gnn_muon_tensor {

@@ -57,18 +57,26 @@ def _compile(src: str, extra, build_dir: str = BUILD) -> str:
     return obj
 
 
-def build(force: bool = False, verbose: bool = False, extra=(), variant: str = "") -> str:
+def build(force: bool = False, verbose: bool = False, extra=(), variant: str = "", only=()) -> str:
     """Compile every csrc/*.cu and link libgnnagg.so; returns its path.
     `variant` names a build with extra compile flags kept apart from the
-    library (under _build/<variant>/; used by tests of kernel selections)."""
+    library (under _build/<variant>/; used by tests of kernel selections);
+    `only`: the sources that its flags are for, the others being the
+    library's."""
     build_dir = os.path.join(BUILD, variant) if variant else BUILD
     lib = os.path.join(build_dir, "libgnnagg.so") if variant else LIB
     if not force and not _stale(lib):
         return lib
     os.makedirs(build_dir, exist_ok=True)
-    srcs = _sources()
+    srcs = [s for s in _sources() if not only or os.path.basename(s) in only]
+    shared = []
+    if only:
+        names = [os.path.basename(s) for s in _sources() if s not in srcs]
+        shared = [os.path.join(BUILD, n + ".o") for n in names]
+        if _stale() or not all(map(os.path.exists, shared)):
+            build(force=True)
     with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 1))) as ex:
-        objs = list(ex.map(lambda s: _compile(s, list(extra), build_dir), srcs))
+        objs = list(ex.map(lambda s: _compile(s, list(extra), build_dir), srcs)) + shared
     tmp = lib + ".tmp"
     cmd = [nvcc(), *ARCH, "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)

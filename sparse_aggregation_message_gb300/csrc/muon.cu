@@ -54,6 +54,13 @@ struct Mat {
   int quads;          // bits: rows of param, grad, mom, copy lie on borders of four elements
   char *x[2], *a, *p;
 };
+// Warps that have finished their share of a tile, by matrix and product; and, of a pass's
+// first matrix, whether a wait of the steps has run out: what X holds is then unfinished.
+struct Done {
+  int of[3];
+  int gave_up;
+};
+constexpr int DONE_WORDS = MAX_MATS * sizeof(Done) / sizeof(int);
 struct Table {
   Mat mat[MAX_MATS];
   int first[MAX_MATS + 1];  // blocks (or parts) before each matrix
@@ -63,7 +70,7 @@ struct Table {
   int half[3];  // pairs: tiles of 128 columns instead of 256, by product
   int64_t blocks;  // of the operands, from the workspace's start
   double* partial;
-  int* done;
+  Done* done;
 };
 
 struct Hyper {
@@ -148,12 +155,6 @@ __device__ __forceinline__ int mat_of(const Table& tab, int k) {
   return i;
 }
 
-// Warps that have finished their share of a tile, by matrix and product.
-struct Done {
-  int of[4];
-};
-constexpr int DONE_WORDS = MAX_MATS * 4;
-
 // Sums of u^2 over a share of a matrix's rows; the counts of the steps start at zero.
 // It reads what begin_kernel reads again (a norm comes before the first limb): the three
 // kernels around the steps take 105 us of six matrices of 1024 x 4096 cold, DRAM at half.
@@ -162,7 +163,7 @@ __global__ void __launch_bounds__(THREADS) square_kernel(const __grid_constant__
   cudaTriggerProgrammaticLaunchCompletion();
   cudaGridDependencySynchronize();
   if (blockIdx.x == 0)
-    for (int k = threadIdx.x; k < DONE_WORDS; k += THREADS) tab.done[k] = 0;
+    for (int k = threadIdx.x; k < DONE_WORDS; k += THREADS) reinterpret_cast<int*>(tab.done)[k] = 0;
   const int i = mat_of(tab, blockIdx.x);
   const Mat& t = tab.mat[i];
   const int part = blockIdx.x - tab.first[i];
@@ -309,7 +310,7 @@ __global__ void __launch_bounds__(THREADS) apply_kernel(const __grid_constant__ 
   const int i = mat_of(tab, blockIdx.x);
   const Mat& t = tab.mat[i];
   const int block = blockIdx.x - tab.first[i], r0 = block / t.nb * 128, c0 = block % t.nb * 64;
-  const bool good = isfinite(norm_of(tab.partial, i, t.parts, &sm));
+  const bool good = isfinite(norm_of(tab.partial, i, t.parts, &sm)) && !tab.done->gave_up;
   if (!good && !h.orth) return;  // this matrix stays as it is
   const char* x = t.x[which] + (int64_t)block * BLOCK;
   for (int e = threadIdx.x; e < 128 * 8; e += THREADS) {
@@ -838,6 +839,7 @@ done:
   tc::fence_before_sync();
   __syncthreads();
   if (PAIR) tc::cluster_sync();  // nothing of the partner's arrives here any more
+  if (threadIdx.x == 0 && *s.abort_flag) atomicExch(&g.done->gave_up, 1);
   if (warp == 1) {
     tc::fence_after_sync();
     if (PAIR)
@@ -954,7 +956,7 @@ __global__ void __launch_bounds__(SMALL_THREADS, 1)
   }
   __syncthreads();
   const float norm = shared_norm;
-  const bool good = isfinite(norm);
+  bool good = isfinite(norm);
   const float inv = scale_of(norm, h.eps);
   for (int e = threadIdx.x; e < quads; e += SMALL_THREADS) {
     const int row = e / across, col = e % across * 4;
@@ -1028,6 +1030,7 @@ __global__ void __launch_bounds__(SMALL_THREADS, 1)
   };
   // what truncated sums lose on average (see the steps' kernel)
   auto back_of = [](int k16) { return k16 > 2 ? 1.f + 0x1p-23f : 1.f; };
+  bool done = true;  // false once a wait has run out: what X holds is unfinished
   for (int s = 0; s < g.steps; ++s) {
     const float ca = g.coeff[s][0], cb = g.coeff[s][1], cc = g.coeff[s][2];
     if (warp == 0 && tc::elect_one()) {
@@ -1036,7 +1039,7 @@ __global__ void __launch_bounds__(SMALL_THREADS, 1)
       tc::mma_commit(bar);
     }
     __syncwarp();
-    if (!arrived()) goto done;
+    if (!(done = arrived())) break;
     float am[16];
     if (mine) {
 #pragma unroll
@@ -1058,7 +1061,7 @@ __global__ void __launch_bounds__(SMALL_THREADS, 1)
       tc::mma_commit(bar);
     }
     __syncwarp();
-    if (!arrived()) goto done;
+    if (!(done = arrived())) break;
     if (mine) {
       float v[16];
       tc::tmem_ld16(lane0 + 16 * piece, v);
@@ -1079,7 +1082,7 @@ __global__ void __launch_bounds__(SMALL_THREADS, 1)
       tc::mma_commit(bar);
     }
     __syncwarp();
-    if (!arrived()) goto done;
+    if (!(done = arrived())) break;
     if (mine) {
       const float back = back_of(km) * (1.f / UNIT);
       for (int kb = 0; kb < kbs; ++kb) {
@@ -1092,6 +1095,7 @@ __global__ void __launch_bounds__(SMALL_THREADS, 1)
     }
     written();
   }
+  good &= done;
   for (int e = threadIdx.x; e < quads; e += SMALL_THREADS) {
     const int row = e / across, col = e % across * 4;
     if (!good && !h.orth) break;  // this matrix stays as it is
@@ -1117,7 +1121,6 @@ __global__ void __launch_bounds__(SMALL_THREADS, 1)
       if (t.copy) store4(t.copy, (int64_t)row * t.ldc, col, t.cols, GNN_BF16, t.quads & COPY, n);
     }
   }
-done:
   if (*abort_flag) {
     // a wait gave up: products in flight land within microseconds
     const long long t0 = clock64();
@@ -1253,7 +1256,7 @@ void place_pass(Table& tab, Arena& ar) {
   for (int i = 0; i < tab.count; ++i) place(tab.mat[i], ar, tab.bn);
   tab.blocks = (int64_t)(ar.used / BLOCK);
   tab.partial = ar.take<double>((size_t)MAX_MATS * PARTS);
-  tab.done = ar.take<int>(DONE_WORDS);
+  tab.done = ar.take<Done>(MAX_MATS);
 }
 
 // Matrices in the order of their work, the largest first, MAX_MATS to a pass; every
@@ -1333,7 +1336,7 @@ gnn_status run_pass(void* ws, Table& tab, const Hyper& h, const float* coeffs, i
   if (steps) {
     Steps g;
     g.base = static_cast<char*>(ws);
-    g.done = reinterpret_cast<Done*>(tab.done);
+    g.done = tab.done;
     g.flags = device_flags();
     if (!g.flags) return fail(GNN_ERR_CUDA, "device flag word unavailable");
     GNN_TRY(maps_of(g, ws, (uint64_t)tab.blocks));
