@@ -909,13 +909,14 @@ __global__ void __launch_bounds__(SMALL_THREADS, 1)
   cudaGridDependencySynchronize();
   // Columns of TMEM are asked for when the kernel before has given its own back, and the
   // kernel behind starts when they are there: on a shared SM neither can hold columns
-  // that the other, which it waits for, has yet to get.
+  // that the other, which it waits for, has yet to get.  A block's first thread to trigger
+  // counts for all of it, so only the warp that has them does.
   if (warp == 0) {
     tc::tmem_alloc(tmem_at, tmem_cols);
     tc::tmem_relinquish();
+    __syncwarp();
+    cudaTriggerProgrammaticLaunchCompletion();
   }
-  __syncwarp();
-  cudaTriggerProgrammaticLaunchCompletion();
   tc::fence_before_sync();
   // |u|
   const int across = (t.cols + 3) >> 2, quads = t.rows * across;

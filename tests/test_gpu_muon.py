@@ -249,3 +249,35 @@ def test_tiles_that_wait_for_one_another_give_the_same_bits(count, rows, cols):
         for O in again:  # noqa: E741
             assert torch.equal(O, first)
     G.gnn_sync_check()
+
+
+def test_small_matrices_before_and_behind_other_tensor_kernels():
+    """Kernels that hold tensor memory, behind one another on one stream and beside one
+    another on two, give what each gives alone."""
+    x = torch.stack([matrix(64, 200, i) for i in range(40)]).cuda()
+    X = matrix(3000, 256, 1, BF16, 1.0).cuda()
+    Wg, Wu = (matrix(256, 512, 2 + i, BF16, 0.05).cuda() for i in range(2))
+
+    def orth():
+        O = torch.empty_like(x)  # noqa: E741
+        G.gnn_orthogonalise(x, O)
+        return O
+
+    def gated():
+        H = torch.empty(3000, 512, dtype=BF16, device="cuda")
+        G.gnn_gated_fwd(X, 3000, 256, Wg, Wu, 512, H)
+        return H
+
+    a, b = orth(), gated()
+    torch.cuda.synchronize()
+    for got in [f() for _ in range(10) for f in (orth, orth, gated, orth, gated, gated)]:
+        assert torch.equal(got, a if got.dim() == 3 else b)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        there = [f() for _ in range(20) for f in (gated, orth)]
+    here = [f() for _ in range(20) for f in (orth, gated)]
+    torch.cuda.synchronize()
+    for got in there + here:
+        assert torch.equal(got, a if got.dim() == 3 else b)
+    G.gnn_sync_check()
