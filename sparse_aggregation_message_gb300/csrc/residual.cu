@@ -783,7 +783,7 @@ struct Shape {
   int lanes, vecs, threads;
   bool multi;
 };
-Shape shape_for(int C, bool bwd) {
+constexpr Shape shape_for(int C, bool bwd) {
   const int v = (C + 15) / 16 * 2;
   Shape s{0, 0, 0, false};
   for (int k = 1; k <= (bwd ? 3 : 4); k += bwd ? 2 : 1)
@@ -795,6 +795,22 @@ Shape shape_for(int C, bool bwd) {
   // blocks: each takes sixteen barriers, and an SM has them for four
   return {lanes, 1, MAX_LANES / lanes * lanes, true};
 }
+
+// What the kernels take for granted of a width's shape: the row fits, rows of one warp are a
+// power of two of lanes and have a kernel, and those of several are whole warps, each row
+// with a named barrier of its own (a block has fifteen beside its common one).
+constexpr bool fits(const Shape& s, int C, bool bwd) {
+  if (s.lanes < 1 || s.threads % s.lanes || s.threads > MAX_LANES || 8 * s.lanes * s.vecs < (C + 15) / 16 * 16) return false;
+  if (s.multi) return s.vecs == 1 && s.lanes % 32 == 0 && s.threads / s.lanes <= 15;
+  return 32 % s.lanes == 0 && s.threads == (s.vecs == 1 ? THREADS : FEW) && s.vecs >= 1 && s.vecs <= 4 &&
+         (!bwd || s.vecs == 1 || s.vecs == 3);
+}
+constexpr bool every_width_fits() {
+  for (int C = 1; C <= MAX_C; ++C)
+    if (!fits(shape_for(C, false), C, false) || !fits(shape_for(C, true), C, true)) return false;
+  return true;
+}
+static_assert(every_width_fits(), "a width whose rows have no kernel, or more than fifteen to a block of barriers");
 
 // What one of the four sums of every warp or group takes on its way through shared memory.
 int one_sum(const Shape& s) { return (s.multi ? s.threads / s.lanes : s.threads / 32) * 8 * s.lanes * s.vecs * (int)sizeof(float); }
