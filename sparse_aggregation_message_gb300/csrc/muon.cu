@@ -1400,6 +1400,28 @@ bool quad_rows(const void* p, int64_t ld, int elem) { return aligned_to(p, 4 * e
 Span flat(const void* p, int64_t bytes) { return {p, 1, bytes, bytes}; }
 Span span(const void* p, const gnn_muon_tensor& t, int64_t ld, int elem) { return {p, t.rows, ld * elem, (int64_t)t.cols * elem}; }
 
+// A batch of matrices, seen as whole matrices and as rows (of the distance that divides both
+// strides): it lies apart from something else where either does.
+struct Batch {
+  Span whole, rows;
+};
+Batch batch(const void* p, int count, int rows, int cols, int64_t ld, int64_t stride, int elem) {
+  if (count == 1) stride = 0;
+  int64_t step = rows > 1 ? ld : 0;
+  for (int64_t r = stride; r;) {
+    const int64_t t = step % r;
+    step = r, r = t;
+  }
+  const int64_t last = (count - 1) * stride + (rows > 1 ? (rows - 1) * ld : 0);  // the last row's place
+  return {{p, count, stride * elem, (last - (count - 1) * stride + cols) * elem},
+          {p, step ? last / step + 1 : 1, step * elem, (int64_t)cols * elem}};
+}
+bool overlap(const Batch& a, const Batch& b) {
+  return gnn::overlap(a.whole, b.whole) && gnn::overlap(a.whole, b.rows) && gnn::overlap(a.rows, b.whole) &&
+         gnn::overlap(a.rows, b.rows);
+}
+bool overlap(const Batch& a, const Span& b) { return gnn::overlap(a.whole, b) && gnn::overlap(a.rows, b); }
+
 }  // namespace
 
 }  // namespace gnn
@@ -1526,7 +1548,7 @@ extern "C" gnn_status gnn_orthogonalise(const void* X, int64_t ldx, int64_t stri
   const int64_t x_size = (rows - 1) * ldx + cols, o_size = (rows - 1) * ldo + cols;
   GNN_REQUIRE(count == 1 || (stride_x >= x_size && stride_o >= o_size && stride_x <= LD_MOST && stride_o <= LD_MOST),
               "%s: matrices of a batch overlap", who);
-  const Span x_all{X, count, stride_x * xs, x_size * xs}, o_all{O, count, stride_o * os, o_size * os};
+  const Batch x_all = batch(X, count, rows, cols, ldx, stride_x, xs), o_all = batch(O, count, rows, cols, ldo, stride_o, os);
   // in place each element is read before anything is written
   GNN_REQUIRE((X == O && ldx == ldo && xs == os && (count == 1 || stride_x == stride_o)) ||
                   !overlap(x_all, o_all),
@@ -1536,8 +1558,8 @@ extern "C" gnn_status gnn_orthogonalise(const void* X, int64_t ldx, int64_t stri
   GNN_REQUIRE(ws && ws_bytes >= need && aligned_to(ws, 256), "%s: workspace too small (%zu < %zu) or misaligned", who,
               ws_bytes, need);
   const Span w_all = flat(ws, (int64_t)need), n_all = flat(norms, 4ll * count);
-  GNN_REQUIRE(!overlap(w_all, x_all) && !overlap(w_all, o_all) && !overlap(w_all, n_all) && !overlap(n_all, x_all) &&
-                  !overlap(n_all, o_all), "%s: norms or the workspace overlaps an array", who);
+  GNN_REQUIRE(!overlap(x_all, w_all) && !overlap(o_all, w_all) && !overlap(w_all, n_all) && !overlap(x_all, n_all) &&
+                  !overlap(o_all, n_all), "%s: norms or the workspace overlaps an array", who);
   const Hyper h{0.f, 1.f, 1.f, 0.f, eps, 0, 1, o_type, x_type, 0};
   return guarded(who, [&] {
     const auto order = order_of(count, [&](int) { return Shape{rows, cols}; });

@@ -281,3 +281,38 @@ def test_small_matrices_before_and_behind_other_tensor_kernels():
     for got in there + here:
         assert torch.equal(got, a if got.dim() == 3 else b)
     G.gnn_sync_check()
+
+
+def columns(*parts, gap=0):
+    """Matrices side by side in one buffer."""
+    buf = torch.full((parts[0].shape[0], sum(p.shape[1] + gap for p in parts)), GUARD, device="cuda")
+    at, views = 0, []
+    for p in parts:
+        views.append(buf[:, at:at + p.shape[1]])
+        views[-1].copy_(p)
+        at += p.shape[1] + gap
+    return buf, views
+
+
+@pytest.mark.parametrize("rows,cols", [(40, 60), (150, 70)])
+def test_columns_of_one_buffer(rows, cols):
+    """X and O in other columns of the same rows share no element."""
+    x = matrix(rows, cols, 77)
+    want = torch.empty(rows, cols, device="cuda")
+    G.gnn_orthogonalise(x.cuda(), want)
+    buf, (X, O) = columns(x, torch.zeros(rows, cols), gap=3)  # noqa: E741
+    G.gnn_orthogonalise(X, O)
+    assert torch.equal(O, want) and torch.equal(X.cpu(), x)
+    assert (buf[:, cols:cols + 3] == GUARD).all() and (buf[:, 2 * cols + 3:] == GUARD).all()
+    # and a batch of them, matrices that alternate
+    batch = torch.stack([x, matrix(rows, cols, 78)])
+    want = torch.empty(2, rows, cols, device="cuda")
+    G.gnn_orthogonalise(batch.cuda(), want)
+    buf = torch.full((2, rows, 2 * cols), GUARD, device="cuda")
+    buf[:, :, :cols] = batch.cuda()
+    G.gnn_orthogonalise(buf[:, :, :cols], buf[:, :, cols:])
+    assert torch.equal(buf[:, :, cols:], want)
+    buf = torch.full((2, 2, rows, cols), GUARD, device="cuda")
+    buf[:, 0] = batch.cuda()
+    G.gnn_orthogonalise(buf[:, 0], buf[:, 1])
+    assert torch.equal(buf[:, 1], want)

@@ -198,3 +198,21 @@ def test_a_copy_that_overlaps_its_parameters_is_refused(lib, bad):
     """All but bf16 parameters that are their own copy."""
     assert muon(lib, **bad) == INVALID
     assert b"overlap" in lib.gnn_last_error()
+
+
+@pytest.mark.parametrize("kw", [
+    dict(O=MB + 256, ldx=128, ldo=128), dict(X=MB + 256, O=MB, ldx=128, ldo=128), dict(O=MB + 256, ldx=128, ldo=256),
+    dict(O=MB + 256, ldx=128, ldo=128, count=2, sx=32 * 128, so=32 * 128), dict(O=MB + 32 * 64 * 4, count=2, sx=2 * 32 * 64, so=2 * 32 * 64),
+    dict(O=MB + 256, xt=F32, ot=BF16, ldx=128, ldo=256)])
+def test_columns_of_one_buffer_are_taken(lib, kw):
+    """They come as far as the workspace's check."""
+    assert orth(lib, **kw, ws_bytes=8) == INVALID
+    assert b"workspace too small" in lib.gnn_last_error()
+
+
+@pytest.mark.parametrize("kw", [
+    dict(O=MB + 252, ldx=128, ldo=128), dict(O=MB + 256, ldx=128, ldo=96), dict(O=MB + 4, ldx=128, ldo=128),
+    dict(O=MB + 256, ldx=128, ldo=128, count=2, sx=32 * 128 + 1, so=32 * 128)])
+def test_columns_that_share_elements_are_refused(lib, kw):
+    assert orth(lib, **kw, ws_bytes=8) == INVALID
+    assert b"overlaps" in lib.gnn_last_error()
