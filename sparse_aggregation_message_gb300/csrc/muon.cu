@@ -1469,7 +1469,8 @@ extern "C" gnn_status gnn_muon_step(const gnn_muon_tensor* tensors, int32_t n_te
                 "%s: matrix %d has a misaligned array", who, i);
     GNN_REQUIRE(!bad_ld(t.ldp, t.rows, t.cols) && !bad_ld(t.ldg, t.rows, t.cols) && !bad_ld(t.ldm, t.rows, t.cols) &&
                     (!t.copy || !bad_ld(t.ldc, t.rows, t.cols)), "%s: matrix %d has a stride below its columns", who, i);
-    GNN_REQUIRE(std::isfinite(t.scale), "%s: matrix %d has a scale that is not finite", who, i);
+    GNN_REQUIRE(std::isfinite(t.scale) && std::isfinite((float)lr * t.scale),
+                "%s: matrix %d has a scale that is not finite, alone or times lr", who, i);
     const Span p = span(t.param, t, t.ldp, ps), g = span(t.grad, t, t.ldg, gs), m = span(t.m, t, t.ldm, ms),
                c = span(t.copy, t, t.ldc, 2);
     // bf16 parameters may be their own copy: a thread writes the same value twice

@@ -216,3 +216,10 @@ def test_columns_of_one_buffer_are_taken(lib, kw):
 def test_columns_that_share_elements_are_refused(lib, kw):
     assert orth(lib, **kw, ws_bytes=8) == INVALID
     assert b"overlaps" in lib.gnn_last_error()
+
+
+@pytest.mark.parametrize("bad", [dict(lr=1e20, scale=1e19), dict(lr=-1e30, scale=1e30), dict(lr=0.0, scale=INF), dict(lr=3e38, scale=2.0)])
+def test_muon_refuses_a_scale_that_overflows_with_lr(lib, bad):
+    """An update of zero would become 0 * inf."""
+    assert muon(lib, **bad, ws_bytes=8) == INVALID
+    assert b"scale" in lib.gnn_last_error()
