@@ -7,6 +7,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import math
 import threading
 from dataclasses import dataclass, field
 from typing import Optional, Sequence
@@ -1173,6 +1174,17 @@ def gnn_orthogonalise(X, O, steps: int = 5, coeffs=NS_COEFFS, eps: float = 1e-7,
          so, _type(O), _f32(norms, count, "norms"), at, size, _current(X, stream))
 
 
+def _share(a, b) -> bool:
+    """Whether (start, rows, stride, width) in bytes of two matrices may share one; rows
+    that lie apart in a common period of the strides (columns of one buffer) do not."""
+    (pa, ra, sa, wa), (pb, rb, sb, wb) = a, b
+    if pa + (ra - 1) * sa + wa <= pb or pb + (rb - 1) * sb + wb <= pa:
+        return False
+    period = math.gcd(sa if ra > 1 else 0, sb if rb > 1 else 0)
+    d = (pb - pa) % period if period else 0
+    return period == 0 or d < wa or d + wb > period
+
+
 class MuonTensors:
     """The matrices of a Muon optimiser, checked once: lists of parameters (fp32
     or bf16 [rows, cols], updated in place), their gradients (fp32, bf16 or fp16),
@@ -1205,6 +1217,16 @@ class MuonTensors:
             places = [t.data_ptr() for t in lists[name] or () if t is not None and t.numel()]
             if len(set(places)) < len(places):
                 raise ValueError(f"{name}: a matrix is listed twice")
+        spans = sorted(((t.data_ptr(), t.shape[0], _matrices(t, name)[0] * t.dtype.itemsize, t.shape[1] * t.dtype.itemsize), name, i)
+                       for name, ts in lists.items() for i, t in enumerate(ts or ()) if t is not None and t.numel())
+        open_ = []  # those whose end lies ahead
+        for span, name, i in spans:
+            open_ = [o for o in open_ if o[0][0] + (o[0][1] - 1) * o[0][2] + o[0][3] > span[0]]
+            for other, its, j in open_:
+                own = i == j and {name, its} == {"params", "copies"} and span == other
+                if not (name == its == "grads") and not own and _share(span, other):
+                    raise ValueError(f"{name}[{i}]: overlaps {its}[{j}]")
+            open_.append((span, name, i))
         self.param_type, self.grad_type, self.m_type = (_type(t[0]) if k else 0 for t in (params, grads, momenta))
         self.device = params[0].device if k else None
         self._keep = {name: list(ts) for name, ts in lists.items() if ts is not None}

@@ -223,3 +223,49 @@ def test_muon_refuses_a_scale_that_overflows_with_lr(lib, bad):
     """An update of zero would become 0 * inf."""
     assert muon(lib, **bad, ws_bytes=8) == INVALID
     assert b"scale" in lib.gnn_last_error()
+
+
+class Matrix:
+    """Stands for a CUDA matrix of 4 x 8 at an address."""
+    is_cuda, device = True, torch.device("cuda", 0)
+
+    def __init__(self, at, ld=8, dtype=torch.float32, rows=4, cols=8):
+        self.at, self.ld, self.dtype, self.shape = at, ld, dtype, (rows, cols)
+
+    numel = lambda self: self.shape[0] * self.shape[1]  # noqa: E731
+    data_ptr = lambda self: self.at  # noqa: E731
+    dim = lambda self: 2  # noqa: E731
+    stride = lambda self, k: (self.ld, 1)[k]  # noqa: E731
+
+
+def muon_tensors(params, grads, momenta, copies=None):
+    import sparse_aggregation_message_gb300 as G
+    return G.MuonTensors(params, grads, momenta, copies)
+
+
+
+@pytest.mark.parametrize("p,g,m,c,text", [
+    ((4096, 4160), (8192, 8448), (12288, 12544), None, r"params\[1\]: overlaps params\[0\]"),
+    ((4096, 4352), (8192, 8448), (12288, 12384), None, r"momenta\[1\]: overlaps momenta\[0\]"),
+    ((4096, 4352), (8192, 8448), (8192, 12544), None, "overlaps"),
+    ((4096, 4352), (8192, 8448), (4384, 12544), None, r"momenta\[0\]: overlaps params\[1\]"),
+    ((4096, 4352), (8192, 8448), (12288, 12544), (16384, 16400), r"copies\[1\]: overlaps copies\[0\]"),
+    ((4096, 4352), (8192, 8448), (12288, 12544), (16384, 8500), r"copies\[1\]: overlaps grads\[1\]")])
+def test_muon_tensors_refuse_matrices_that_share_elements(p, g, m, c, text):
+    make = lambda ats, t=torch.float32: [Matrix(a, dtype=t) for a in ats]  # noqa: E731
+    with pytest.raises(ValueError, match=text):
+        muon_tensors(make(p), make(g), make(m), c and make(c, torch.bfloat16))
+
+
+def test_muon_tensors_take_columns_of_one_buffer():
+    cols = lambda at, t=torch.float32: [Matrix(at, 24, t), Matrix(at + 8 * t.itemsize, 24, t), Matrix(at + 16 * t.itemsize, 24, t)]  # noqa: E731
+    assert muon_tensors(cols(4096), cols(8192), cols(12288), cols(16384, torch.bfloat16)).count == 3
+    same = [Matrix(8192)] * 2  # gradients are only read
+    assert muon_tensors([Matrix(4096), Matrix(4352)], same, [Matrix(12288), Matrix(12544)]).count == 2
+    with pytest.raises(ValueError, match="overlaps"):
+        muon_tensors([Matrix(4096, 24), Matrix(4096 + 28, 24)], same, [Matrix(12288), Matrix(12544)])
+    half = [Matrix(4096, dtype=torch.bfloat16), Matrix(4352, dtype=torch.bfloat16)]
+    momenta = [Matrix(12288), Matrix(12544)]
+    assert muon_tensors(half, same, momenta, half).count == 2  # their own copies
+    with pytest.raises(ValueError, match="overlaps"):
+        muon_tensors(half, same, momenta, half[::-1])
