@@ -51,3 +51,24 @@ def spread(x, coeffs, steps, eps=1e-7):
     rand = steps64(x, coeffs, steps, eps, lambda v, mag, K: v + mag * (torch.randint(0, 2, v.shape, generator=g) * 2 - 1))
     down = steps64(x, coeffs, steps, eps, lambda v, mag, K: v - mag if K else v + mag)
     return want, 2 * max(float((rand - want).abs().max()), float((down - want).abs().max())) + 2.0 ** -40
+
+
+def plain_steps(x, coeffs=NS, steps=5, eps=1e-7, stored=lambda v: v):
+    """The steps in x's own type; stored: what keeping an operand does to it."""
+    x = x / (x.double().norm() + eps).to(x.dtype)
+    flip = x.shape[0] > x.shape[1]
+    x = stored(x.mT if flip else x)
+    for a, b, c in triples(coeffs, steps):
+        g = stored(x @ x.mT)
+        p = stored(a * torch.eye(len(g), dtype=g.dtype, device=g.device) + b * g + c * (g @ g))
+        x = stored(p @ x)
+    return x.mT if flip else x
+
+
+def in_limbs(v, t, count):
+    """v as `count` limbs of type t hold 1024 times it."""
+    total, rest = torch.zeros_like(v), v * 1024
+    for _ in range(count):
+        limb = rest.to(t).to(v.dtype)
+        total, rest = total + limb, rest - limb
+    return total / 1024

@@ -316,3 +316,18 @@ def test_columns_of_one_buffer(rows, cols):
     buf[:, 0] = batch.cuda()
     G.gnn_orthogonalise(buf[:, 0], buf[:, 1])
     assert torch.equal(buf[:, 1], want)
+
+
+@pytest.mark.parametrize("count,rows,cols", [(16, 64, 256), (1, 256, 512), (3, 300, 800), (1, 1000, 1000), (6, 1024, 4096), (1, 2047, 2047)])
+def test_as_exact_as_fp32_steps(count, rows, cols):
+    """In the 2-norm, three times the error of plain fp32 steps at most.  An operand
+    is stored with half a step of 2^-23 of its value (two limbs of 11 bits and the
+    second's sign) where fp32's is 2^-24, twice as much; lo lo, left out, is at most
+    2^-24 of a term, one such rounding more."""
+    x = torch.stack([matrix(rows, cols, 900 + i) for i in range(count)]).cuda()
+    O = torch.empty_like(x)  # noqa: E741
+    G.gnn_orthogonalise(x, O)
+    for i in range(count):
+        exact, plain = ref.plain_steps(x[i].double()), ref.plain_steps(x[i])
+        off = lambda a: float((a.double() - exact).norm() / exact.norm())  # noqa: E731
+        assert off(O[i]) <= 3 * off(plain), (off(O[i]), off(plain))

@@ -340,3 +340,24 @@ def test_more_rows_than_one_chain_of_sums(n, C, t, scale):
     for k, got in o.items():
         value, bound = (x.cpu() for x in want.pop(k))
         close(got[:, :C] if got.dim() == 2 else got, value, bound, types.get(k, F32), k)
+
+
+def stats_means(a, st):
+    """The means that are kept: 64 u of the mean magnitude, H's with H's own error."""
+    want = ref.forward(a)
+    mean = lambda x: x.mean(1)  # noqa: E731
+    B, H = a["B"].double(), want["H"]
+    for col, x, e, kind in ((0, B, torch.zeros_like(B), a["post"]), (2, H, want["eH"], a["pre"])):
+        lim = 64 * ref.U * mean(x.abs()) + mean(e)
+        got = st[:, col].cpu().double()
+        if kind == "layer":
+            assert ((got - want["stats"][:, col]).abs() <= lim).all(), col
+        else:
+            assert (got == 0).all(), col
+
+
+@pytest.mark.parametrize("post,pre", [("layer", "layer"), ("layer", "rms"), ("rms", "layer"), ("none", "layer"), ("layer", "none"), ("rms", "none")])
+@pytest.mark.parametrize("C", [5, 200, 300, 1000, 4090])
+def test_kept_means(post, pre, C):
+    a = make(67, C, TYPES[(C + len(post)) % 7], post, pre, "row", "sigmoid", "all", True, C, shift=1.5)
+    stats_means(a, check_forward(a)[2])

@@ -269,3 +269,16 @@ def test_muon_tensors_take_columns_of_one_buffer():
     assert muon_tensors(half, same, momenta, half).count == 2  # their own copies
     with pytest.raises(ValueError, match="overlaps"):
         muon_tensors(half, same, momenta, half[::-1])
+
+
+@pytest.mark.parametrize("rows,cols", [(7, 5), (64, 256), (200, 300)])
+def test_three_times_fp32_steps_tells_fewer_bits(rows, cols):
+    """The 2-norm bound of the GPU tests: two fp16 limbs lie inside of it, two bf16
+    limbs and one fp16 limb far outside."""
+    x = torch.randn(rows, cols, generator=torch.Generator().manual_seed(rows)) * 0.01
+    exact = ref.plain_steps(x.double())
+    off = lambda a: float((a.double() - exact).norm() / exact.norm())  # noqa: E731
+    limbs = lambda t, k: off(ref.plain_steps(x.double(), stored=lambda v: ref.in_limbs(v, t, k)))  # noqa: E731
+    plain = off(ref.plain_steps(x))
+    assert limbs(torch.float16, 2) <= 3 * plain
+    assert limbs(torch.bfloat16, 2) > 6 * plain and limbs(torch.float16, 1) > 100 * plain
