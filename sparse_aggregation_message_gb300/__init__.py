@@ -1161,7 +1161,9 @@ def gnn_orthogonalise(X, O, steps: int = 5, coeffs=NS_COEFFS, eps: float = 1e-7,
     """O = X / (|X| + eps) after `steps` of Newton-Schulz with coefficients
     (a, b, c), or a triple for each step; X [rows, cols] or [count, rows, cols], O
     of X's shape, any of fp32, bf16 and fp16 each; norms (fp32 [count]) receives
-    every |X|."""
+    every |X|.  Operands are held to 22 bits in fp16's range, which the steps must not
+    leave: every singular value v stays below 7 and a + b v^2 + c v^4 within 60 of
+    zero (NS_COEFFS: 1.3 and 3.5).  A matrix whose norm is not finite gives NaN."""
     ldx, sx = _matrices(X, "X")
     ldo, so = _matrices(O, "O")
     if O.shape != X.shape:
@@ -1189,9 +1191,11 @@ class MuonTensors:
     """The matrices of a Muon optimiser, checked once: lists of parameters (fp32
     or bf16 [rows, cols], updated in place), their gradients (fp32, bf16 or fp16),
     momenta (fp32 or bf16) and, optionally, copies (bf16, None for a matrix without
-    one; bf16 parameters may be their own), with contiguous rows, and the factors on the updates; scales None: 0.2
-    sqrt(max(rows, cols)), which makes an update's mean square that of AdamW's, so
-    that both take one learning rate.  All stay the caller's."""
+    one; bf16 parameters may be their own), with contiguous rows, and the factors on
+    the updates; scales None: 0.2 sqrt(max(rows, cols)), which makes an update's mean
+    square that of AdamW's, so that both take one learning rate.  Matrices lie apart
+    from one another (columns of one buffer do; gradients may be shared).  All stay the
+    caller's."""
 
     def __init__(self, params, grads, momenta, copies=None, scales=None):
         import torch
@@ -1249,9 +1253,10 @@ def gnn_muon_step(tensors: MuonTensors, lr: float, momentum: float = 0.95, neste
                   weight_decay: float = 0.0, grad_scale: float = 1.0, steps: int = 5, coeffs=NS_COEFFS,
                   eps: float = 1e-7, norms=None, ws=None, stream=None) -> None:
     """One Muon step over every matrix: m = momentum m + g, the update (with
-    nesterov g + momentum m, else m) orthogonalised, params (1 - lr weight_decay) -
-    lr scale update.  norms (fp32, one a matrix) receives the updates' norms; a
-    matrix whose norm is not finite is left as it is."""
+    nesterov g + momentum m, else m) orthogonalised (coeffs within gnn_orthogonalise's
+    limits), params (1 - lr weight_decay) - lr scale update.  norms (fp32, one a
+    matrix) receives the updates' norms; a matrix whose norm is not finite is left as
+    it is."""
     if tensors.count == 0:
         return
     first = tensors._keep["params"][0]

@@ -14,8 +14,10 @@ NodeStack, several on one residual stream, with norms by rows before and after:
 
 where one call between two blocks takes the norm after the first, its scale, the
 sum and the norm before the second; Muon steps for the matrices, AdamW for the
-vectors.  Every step is a call of the library; torch holds the memory (and adds
-NodeBlock's residual)."""
+vectors.  Every step is a call of the library; torch holds the memory, adds
+NodeBlock's residual and widens the gated projections' gradients, which the
+library rounds to the weights' 2-byte type, to the optimisers' fp32 (so 8 of their
+bits count, with Muon as with AdamW)."""
 from __future__ import annotations
 
 import torch
@@ -105,7 +107,7 @@ class NodeBlock:
 class NodeStack:
     """depth blocks of width F (a multiple of 16, at most 256) and F_mid (a multiple
     of 16, at most 1024).  norm: "rms" or "layer"; scale: what every block's learned
-    scale s starts at."""
+    scale s starts at.  The passes of one step go to one stream."""
 
     def __init__(self, depth: int, F: int, F_mid: int, act: str = "silu", norm: str = "rms", scale: float = 1.0,
                  seed: int = 0, device="cuda"):
@@ -135,7 +137,8 @@ class NodeStack:
         self._kept = None
 
     def forward(self, H, stream=None):
-        """H: fp32 [n, F], n >= 1; returns the stream behind the last block (fp32 [n, F])."""
+        """H: fp32 [n, F], n >= 1; returns the stream behind the last block (fp32 [n, F]).
+        H is kept, not copied: it stays as it is until the backward has run."""
         if H.dim() != 2 or H.shape[0] < 1 or H.shape[1] != self.F or H.dtype is not torch.float32:
             raise ValueError(f"H: needs fp32 [n, {self.F}] with n >= 1, got {H.dtype} {tuple(H.shape)}")
         n, F, Fm, dev, norm = H.shape[0], self.F, self.F_mid, H.device, self.norm

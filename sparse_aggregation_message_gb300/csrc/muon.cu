@@ -849,8 +849,8 @@ done:
   }
 }
 
-// 4096 x 4096: 554 us a step, 1.36 PFLOP/s of fp16 products; 36 of 1024 x 4096 1.35-1.5,
-// at the card's power cap (a library's bf16 product sustains 1.72).
+// 4096 x 4096: 554 us a step, 1.49 PFLOP/s of fp16 products; 36 of 1024 x 4096 1.35-1.5,
+// at the card's power cap (a library's bf16 product sustains 1.70).
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PRODUCT_THREADS, 1)
     steps_pair_kernel(const __grid_constant__ Steps g) {
   extern __shared__ uint8_t smem_raw[];
@@ -1212,8 +1212,8 @@ int sms_there() {
 // One product's clocks on tiles of bn columns (0: pairs, 256 or with half 128
 // columns): from a tile's last product to the first of what waits for it, and for
 // every 64 of k what the MMAs, or shared memory for smaller tiles, take.  Fitted to steps
-// of 1 to 12 matrices of 64 x 64 to 1024 x 4096 (within 15%).  Several matrices fill each
-// other's last rounds.
+// of 1 to 12 matrices of 64 x 64 to 1024 x 4096 (within 15%; 36 of 1024 x 4096, at the power
+// cap, take half as long again, on any tiles).  Several matrices fill each other's last rounds.
 double clocks(const Table& tab, Phase ph, int bn, int half) {
   const double between = bn == 64 ? 7000 : bn ? 11000 : half ? 12000 : 18000;
   const double each = bn == 64 ? 1050 : bn ? 1130 : half ? 983 : 1490;
