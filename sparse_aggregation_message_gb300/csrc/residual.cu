@@ -275,8 +275,8 @@ __device__ __forceinline__ void wait_row(int stages) {
 }
 
 // Bound by DRAM: 716,847 x 256 with a bf16 branch and an fp32 stream 418 us, 6.2 TB/s of
-// 6.8 that a copy reaches; 200,000 x 1024 bf16 433 us (4.7).  Rows of several warps wait
-// for each other's sums: 30,000 x 4096 bf16 507 us (2.4).
+// 6.8 that a copy reaches; with layer norms 200,000 x 1024 bf16 433 us (4.7).  Rows of
+// several warps wait for each other's sums: 30,000 x 4096 bf16 506 us (2.4).
 template <class TB, class TR, class TY, bool MULTI, int K>
 __global__ void __launch_bounds__(MULTI ? MAX_LANES : K == 1 ? THREADS : FEW)
     residual_fwd_kernel(const __grid_constant__ Args g) {
@@ -712,9 +712,8 @@ __global__ void __launch_bounds__(MULTI ? MAX_LANES : K == 1 ? THREADS : FEW, MU
 
 // The blocks' sums, in order, and the weights' gradients from them.  In fp32: an
 // SM adds two fp64 numbers a clock, and with those this kernel took 27 us of 39 for
-// 2,500 x 300 (6 now).  A
-// block takes 32 channels of the pre norm's two sums or of the post norm's; with one
-// learned scale a block more adds its gradient.
+// 2,500 x 300 (6 now).  A block takes 32 channels of the pre norm's two sums or of the
+// post norm's; with one learned scale a block more adds its gradient.
 constexpr int JOIN_ROWS = 32;
 struct Join {
   const float* part;
