@@ -752,7 +752,8 @@ gnn_status gnn_residual_norm_fwd(const void* B, int64_t ldb, int32_t b_type, con
  * and summed over all rows: dw_pre = dY yh, db_pre = dY, dw_post = D act(G) s bh,
  * db_post = D act(G) s, dscale = D act(G) z (over the row too where scale_cols
  * is 1).  Any output may be NULL.  Sums over rows are added in a fixed order
- * (deterministic).  dR may be dH (one stride). */
+ * (deterministic), off by at most 64 units of 2^-24 of the terms' magnitudes for any
+ * number of rows.  dR may be dH (one stride). */
 gnn_status gnn_residual_norm_workspace(int64_t n, int32_t C, size_t* bwd_bytes);
 gnn_status gnn_residual_norm_bwd(const void* dH, int64_t lddh, const void* dY, int64_t lddy,
                                  int32_t y_type, const void* B, int64_t ldb, int32_t b_type,

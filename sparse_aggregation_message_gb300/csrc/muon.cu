@@ -868,9 +868,9 @@ __global__ void __launch_bounds__(PRODUCT_THREADS, 1) steps_kernel(const __grid_
 // A matrix of up to 64 x 512 stays in one CTA's shared memory from its gradient to its
 // update: no tile waits for another CTA's, which is what bounds small matrices above
 // (16 of 64 x 256: 94 us, here 39, fifteen products of 1.2 us and the passes around).  The
-// same limbs, products and sums; every 64 of k has an accumulator of its own in TMEM, so that a product is issued without a pause.
-// Operands have 64 rows; an MMA reads 128 of A, and what the other 64 give stays in
-// lanes of TMEM that nobody reads.
+// same limbs, products and sums; every 64 of k has an accumulator of its own in TMEM, so
+// that a product is issued without a pause.  Operands have 64 rows; an MMA reads 128 of A,
+// and what the other 64 give stays in lanes of TMEM that nobody reads.
 constexpr int SMALL_M = 64, SMALL_N = 512;
 constexpr int SMALL_THREADS = 512;
 constexpr int HALF_LIMB = 64 * 128, HALF_BLOCK = 2 * HALF_LIMB;  // of 64 rows

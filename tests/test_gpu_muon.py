@@ -331,3 +331,38 @@ def test_as_exact_as_fp32_steps(count, rows, cols):
         exact, plain = ref.plain_steps(x[i].double()), ref.plain_steps(x[i])
         off = lambda a: float((a.double() - exact).norm() / exact.norm())  # noqa: E731
         assert off(O[i]) <= 3 * off(plain), (off(O[i]), off(plain))
+
+
+def test_large_matrices_on_two_streams():
+    """Launches whose blocks wait on one another, of two streams at once, each with its own
+    memory: what each gives alone."""
+    X = [torch.stack([matrix(r, c, 40 + i) for i in range(k)]).cuda() for k, r, c in ((3, 256, 512), (1, 1000, 1000), (2, 1024, 2048), (12, 65, 300))]
+    alone = []
+    for x in X:
+        alone.append(torch.empty_like(x))
+        G.gnn_orthogonalise(x, alone[-1])
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in range(2)], []
+    for turn in range(6):
+        for s, stream in enumerate(streams):
+            i = (turn + 2 * s) % len(X)
+            with torch.cuda.stream(stream):
+                O = torch.empty_like(X[i])  # noqa: E741
+                G.gnn_orthogonalise(X[i], O)
+            got.append((i, O))
+    torch.cuda.synchronize()
+    for i, O in got:  # noqa: E741
+        assert torch.equal(O, alone[i])
+    G.gnn_sync_check()
+
+
+def test_columns_of_one_buffer_step():
+    """Three projections side by side in one buffer each: what matrices of their own get."""
+    parts = [matrix(96, c, 500 + c) for c in (64, 200, 33)]
+    grads, momenta = [matrix(96, p.shape[1], 600 + p.shape[1]) for p in parts], [matrix(96, p.shape[1], 700 + p.shape[1]) for p in parts]
+    own = [[t.cuda() for t in ts] for ts in (parts, grads, momenta)]
+    G.gnn_muon_step(G.MuonTensors(*own), 0.02, weight_decay=0.1)
+    (pb, pv), (_, gv), (mb, mv) = columns(*parts), columns(*grads), columns(*momenta)
+    G.gnn_muon_step(G.MuonTensors(pv, gv, mv), 0.02, weight_decay=0.1)
+    for a, b in zip(own[0] + own[2], pv + mv):
+        assert torch.equal(a, b)

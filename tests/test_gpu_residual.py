@@ -361,3 +361,67 @@ def stats_means(a, st):
 def test_kept_means(post, pre, C):
     a = make(67, C, TYPES[(C + len(post)) % 7], post, pre, "row", "sigmoid", "all", True, C, shift=1.5)
     stats_means(a, check_forward(a)[2])
+
+
+@pytest.mark.parametrize("n,C,t", [(300, 200, 5), (300, 300, 3), (70, 602, 0), (16_000, 2056, 3)])
+def test_any_outputs_alone(n, C, t):
+    """What is wanted beside an output does not change it, and what is not wanted may be None."""
+    a = make(n, C, TYPES[t], "layer", "rms", "full", "silu", "all", True, 71)
+    whole = run_backward(a)
+    for names in (["dR"], ["dB"], ["dgate"], ["dw_pre"], ["db_post"], ["dscale"], ["dB", "dw_pre"], ["dR", "dgate", "db_pre"], ["dw_post", "dB"]):
+        none = {k: None for k in whole if k not in names}
+        some = run_backward(a, **none)
+        for k in whole:
+            if k in names:
+                assert torch.equal(some[k], whole[k]), (names, k)
+            else:
+                assert (some[k] == GUARD).all() if some[k].dim() == 1 else (some[k][:, :C] == 0).all()
+
+
+@pytest.mark.parametrize("C", [8, 200, 1000])
+def test_fewer_rows_than_the_arrays_and_a_gate_with_gaps(C):
+    """Rows behind the last one stay as they are; one gate a row may lie in a column of a matrix."""
+    n, more = 150, 9
+    a = make(n, C, TYPES[5], "rms", "layer", "row", "sigmoid", "all", True, 81, pad=0)
+    want_f, want_b = check_forward(a), run_backward(a)
+    longer = lambda x, fill: torch.cat([x.cuda(), torch.full((more, *x.shape[1:]), fill, dtype=x.dtype, device="cuda")])  # noqa: E731
+    on = {k: longer(rows(a[k], a[k].dtype, 0), float("nan"))[:, :C] for k in ("B", "R", "H", "dH", "dY")}
+    gate = torch.full((n + more, 3), float("nan"), dtype=BF16, device="cuda")
+    gate[:n, 1] = a["gate"].cuda()
+    H, Y = longer(rows(torch.zeros(n, C), F32, 0), GUARD), longer(rows(torch.zeros(n, C), BF16, 0), GUARD)
+    st = torch.full((n + more, 4), GUARD, device="cuda")
+    G.gnn_residual_norm_fwd(on["B"], on["R"], n, C, H[:, :C], Y[:, :C], st, gate=gate[:, 1], b_pre=cuda(a["b_pre"]), **kinds(a))
+    for got, want in zip((H, Y, st), want_f):
+        assert torch.equal(got[:n], want) and (got[n:] == GUARD).all()
+    dR, dB = longer(rows(torch.zeros(n, C), F32, 0), GUARD), longer(rows(torch.zeros(n, C), BF16, 0), GUARD)
+    dg, dw = torch.full((n + more, 2), GUARD, dtype=BF16, device="cuda"), torch.zeros(C, device="cuda")
+    stats = longer(a["stats"], float("nan"))
+    G.gnn_residual_norm_bwd(on["dH"], on["dY"], on["B"], on["H"], n, C, stats, dR=dR[:, :C], dB=dB[:, :C], gate=gate[:, 1],
+                            dgate=dg[:, 0], dw_pre=dw, **kinds(a))
+    for got, want in ((dR, want_b["dR"]), (dB, want_b["dB"]), (dg[:, 0], want_b["dgate"])):
+        assert torch.equal(got[:n], want) and (got[n:] == GUARD).all()
+    assert torch.equal(dw, want_b["dw_pre"]) and (dg[:, 1] == GUARD).all()
+
+
+def test_two_threads_at_once():
+    """Each thread has its workspace; its results are what one thread gets."""
+    import threading
+    cases = [make(5000, 300, TYPES[3], "rms", "layer", "row", "sigmoid", "all", True, 91 + i) for i in range(2)]
+    want = [run_backward(a) for a in cases]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(i):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(10):
+                got = run_backward(cases[i])
+                torch.cuda.current_stream().synchronize()
+                if not all(torch.equal(got[k], want[i][k]) for k in got):
+                    wrong.append(i)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
